@@ -56,7 +56,8 @@ typedef struct CUstream_st* ddt_stream_t;
 #define DDT_ERR_ALIGN (-4)     /* a device pointer is not 16-byte aligned */
 #define DDT_ERR_LAUNCH (-5)    /* a kernel launch or CUDA runtime call failed */
 #define DDT_ERR_DEVICE (-6)    /* the current device is not an sm_103 GPU */
-#define DDT_ERR_ALIAS (-7)     /* ddtree_kv_compact_check: destinations overlap or cover a live row */
+#define DDT_ERR_ALIAS (-7)     /* ddtree_kv_compact_check: destinations overlap or cover a live row;
+                                  ddtree_kv_evict: an output overlaps an input or another output */
 
 /* Device status bits (ddtree_read_device_status). */
 #define DDT_STATUS_BAD_SLOT 1      /* a slot index outside [0, pool_slots): key left out */
@@ -64,6 +65,8 @@ typedef struct CUstream_st* ddt_stream_t;
 #define DDT_STATUS_BAD_PREFIX 4    /* prefix_len[b] outside [0, max_prefix_len]: clamped */
 #define DDT_STATUS_TIMEOUT 8       /* a bounded on-chip wait gave up; outputs are not valid */
 #define DDT_STATUS_BAD_TREE_LEN 16 /* tree_len[b] outside [0, num_nodes]: clamped */
+#define DDT_STATUS_BAD_NODE 32     /* a node_idx entry outside [0, num_nodes) other than -1: left out */
+#define DDT_STATUS_BAD_BLOCK 64    /* a block_idx entry that is no block of the prefix, other than -1: left out */
 
 /*
  * Sizes of one call.  Fixed by the library: D_qk = 576, D_v = 512.
@@ -301,6 +304,98 @@ DDT_API int ddtree_verify_attn_static_scratch(const void* q, const void* kv_pool
                                               const int32_t* prefix_len, const int32_t* tree_parent,
                                               const int32_t* tree_slot_idx, float sm_scale, float* out,
                                               float* lse, const ddt_dims* dims, ddt_stream_t stream);
+
+/*
+ * Keeping a long request's cache small: accumulated attention weights of the
+ * prefix keys, and eviction of the positions that weigh least.
+ *
+ * ddtree_kv_weight adds up what a verify call's softmax gave each prefix key:
+ *   weight_out[b][j] = decay * weight_in[b][j]
+ *                    + sum over the chosen nodes t and all heads h of
+ *                      exp(sm_scale * q[b][t][h].k_j - lse[b][t][h]),  j < prefix_len[b]
+ *   q, kv_pool, slot_idx, prefix_len as in ddtree_verify_attn
+ *   lse        fp32 [B, T, H]: the verify call's; rows with lse = -inf (inactive
+ *              nodes, rows without a key) and +inf add nothing, and their q is
+ *              not used
+ *   node_idx   int32 [B, num_sel] device, the nodes that count (the accepted
+ *              path, say): -1 = none, a node listed twice counts twice, values
+ *              outside [0, T) are left out and set DDT_STATUS_BAD_NODE.  NULL
+ *              with num_sel = 0: every node.  num_sel <= 65535.
+ *   weight_in  fp32 [B, slot_stride], not read when decay is 0 (it may then be
+ *              NULL); may be weight_out
+ *   weight_out fp32 [B, slot_stride]; entries from prefix_len[b] on are not written
+ * A key whose slot is outside the pool gains nothing and sets
+ * DDT_STATUS_BAD_SLOT.  Sums are in fp32 in a fixed order: the same bits on
+ * every run.  workspace >= ddtree_kv_weight_workspace_bytes(dims, num_sel).
+ * prefix_len_sum is not used.  B * T * H and B * ceil(max_prefix_len / 128) fit
+ * in 31 bits (else DDT_ERR_DIMS).
+ */
+DDT_API size_t ddtree_kv_weight_workspace_bytes(const ddt_dims* dims, int32_t num_sel);
+DDT_API int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_t* slot_idx, const int32_t* prefix_len,
+                             const float* lse, const int32_t* node_idx, int32_t num_sel, float sm_scale, float decay,
+                             const float* weight_in, float* weight_out, const ddt_dims* dims, void* workspace,
+                             size_t workspace_bytes, ddt_stream_t stream);
+
+/*
+ * Eviction: request b keeps n = clamp(keep_len[b], 0, L) of its L = prefix_len[b]
+ * positions.  The first `sink` and the last `recent` positions rank before all
+ * others, then the larger weight, then the lower position (NaN ranks with -inf;
+ * if the budget does not hold all the protected ones, the lowest of them stay).
+ *   weight, slot_idx        [B, slot_stride], as in ddtree_kv_weight
+ *   keep_len                int32 [B] device
+ *   slot_idx_out            int32 [B, slot_stride]: the kept positions' slots, in order
+ *   weight_out              fp32 [B, slot_stride]: their weights
+ *   prefix_len_out          int32 [B]: n
+ *   freed_slots             int32 [B, slot_stride]: the other L - n slots, in order
+ * Entries past those counts are not written; slot values are copied, not
+ * checked.  The cached rows stay where they are: the new table is a valid
+ * prefix for every other call, and ddtree_kv_compact can move it.  Outputs must
+ * not overlap inputs or one another (DDT_ERR_ALIAS).  dims gives batch,
+ * slot_stride and max_prefix_len.  workspace >= 256 bytes, 256-byte aligned.
+ */
+DDT_API int ddtree_kv_evict(const float* weight, const int32_t* slot_idx, const int32_t* prefix_len,
+                            const int32_t* keep_len, int32_t sink, int32_t recent, int32_t* slot_idx_out,
+                            float* weight_out, int32_t* prefix_len_out, int32_t* freed_slots, const ddt_dims* dims,
+                            void* workspace, ddt_stream_t stream);
+
+/*
+ * Reading a long cache sparsely: 8-bit means of blocks of the prefix, the best
+ * blocks of each tree node by a cheap score, and attention over them.  A block
+ * is `block` (16, 32, 64 or 128) consecutive positions, the last one cut at the
+ * prefix's end; N = ceil(max_prefix_len / block) is the block stride.
+ *
+ * ddtree_block_summary:
+ *   mean of the block's rows (the sum is exact, the mean rounded once to fp32),
+ *   scale = max |mean| / 127, summary = round to nearest even of mean / scale
+ *   from_len  int32 [B] device or NULL: only blocks that hold a position at or
+ *             after from_len[b] are computed (after a decode step: the old length)
+ *   summary   bf16 [B, N, 576]: integers in [-127, 127]
+ *   scale     fp32 [B, N]
+ * Rows whose slot is outside the pool are left out (DDT_STATUS_BAD_SLOT); a
+ * block with no row has scale 0, one whose sum is not finite in fp32 has scale
+ * NaN and zeros.  Other blocks' entries are not written.  workspace >= 256 bytes.
+ */
+DDT_API int ddtree_block_summary(const void* kv_pool, const int32_t* slot_idx, const int32_t* prefix_len,
+                                 const int32_t* from_len, int32_t block, void* summary, float* scale,
+                                 const ddt_dims* dims, void* workspace, ddt_stream_t stream);
+
+/*
+ * ddtree_block_select: for every node t, the topk best of request b's blocks:
+ *   qs_h = max |q[b][t][h]| / 127, q_int = round to nearest even of q / qs
+ *   score(t, j) = scale[b][j] * max over h of (qs_h * (q_int_h . summary[b][j]))
+ * with both products rounded to fp32 (the integer dot product is exact).  The
+ * first `first` and the last `last` blocks rank before all others, then the
+ * larger score, then the lower block (NaN ranks with -inf; a head whose q is not
+ * finite is left out).
+ *   block_idx  int32 [B, T, topk]: the chosen blocks in ascending order, then -1
+ * topk <= 2^20.  dims gives batch, num_nodes, num_heads, slot_stride and
+ * max_prefix_len; B * T * H and B * N fit in 31 bits.
+ * workspace >= ddtree_block_select_workspace_bytes(dims, block).
+ */
+DDT_API size_t ddtree_block_select_workspace_bytes(const ddt_dims* dims, int32_t block);
+DDT_API int ddtree_block_select(const void* q, const void* summary, const float* scale, const int32_t* prefix_len,
+                                int32_t block, int32_t topk, int32_t first, int32_t last, int32_t* block_idx,
+                                const ddt_dims* dims, void* workspace, size_t workspace_bytes, ddt_stream_t stream);
 
 /* Waits for `stream`, then copies the status word of the last call that used
  * `workspace` to *host_status.  Returns DDT_OK or DDT_ERR_*.  The kernels write

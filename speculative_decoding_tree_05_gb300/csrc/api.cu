@@ -8,6 +8,8 @@
 #include <utility>
 #include <vector>
 #include "../../include/ddtree.h"
+#include "cache_ops.cuh"
+#include "host.cuh"
 #include "kernels.cuh"
 #include "schedule.cuh"
 
@@ -15,7 +17,6 @@ namespace ddt {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr size_t kStatusBytes = 256;
 
 struct DeviceInfo {
   int sm_count = 0;
@@ -36,7 +37,8 @@ int device_info(DeviceInfo* out) {
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess &&
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) == cudaSuccess &&
         cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
-        major == 10 && minor == 3 && configure_prefix() == cudaSuccess && configure_tail_merge() == cudaSuccess)
+        major == 10 && minor == 3 && configure_prefix() == cudaSuccess && configure_tail_merge() == cudaSuccess &&
+        configure_scores() == cudaSuccess && configure_evict() == cudaSuccess && configure_topk() == cudaSuccess)
       d.ok = true;
     g_dev[dev] = d;
   });
@@ -44,13 +46,13 @@ int device_info(DeviceInfo* out) {
   return out->ok ? DDT_OK : DDT_ERR_DEVICE;
 }
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 struct Plan {
   int rows = 0, row_tiles = 0, chunk0 = kKeysPerTile, chunk = kKeysPerTile, splits = 0;
   int groups = 0;  // > 0: the two-launch path divides the batch into this many key-range groups
   size_t cnt_off = 0, cnt_bytes = 0, lse_off = 0, o_off = 0, bytes = 0;
 };
+
+}  // namespace
 
 int check_dims(const ddt_dims* d) {
   if (!d) return DDT_ERR_NULL;
@@ -61,6 +63,15 @@ int check_dims(const ddt_dims* d) {
     return DDT_ERR_DIMS;
   return DDT_OK;
 }
+
+int current_device(int* sm_count) {
+  DeviceInfo dev;
+  const int rc = device_info(&dev);
+  *sm_count = dev.sm_count;
+  return rc;
+}
+
+namespace {
 
 // Key-range split of the prefix.  Depends only on the sizes and the SM count, so
 // a repeated call (or a call on a compacted pool) splits identically.
@@ -149,8 +160,6 @@ int make_plan(const ddt_dims* d, int sm_count, Plan* plan) {
   return DDT_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 // cuTensorMapEncodeTiled, fetched from the driver once (no link-time libcuda dependency).
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -168,6 +177,8 @@ EncodeTiledFn encode_tiled() {
   return fn;
 }
 
+}  // namespace
+
 // The pool as a 2-D bf16 tensor [rows][576] (1152-byte rows), box of box_cols
 // columns x box_rows rows, 128-byte swizzle (64 columns) or 64-byte (32 columns).
 bool encode_pool_map(CUtensorMap* m, const void* pool, int64_t rows, uint32_t box_cols, uint32_t box_rows) {
@@ -183,7 +194,6 @@ bool encode_pool_map(CUtensorMap* m, const void* pool, int64_t rows, uint32_t bo
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
 }  // namespace ddt
 
 using namespace ddt;

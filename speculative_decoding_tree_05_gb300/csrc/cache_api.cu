@@ -1,0 +1,282 @@
+// cache_api.cu -- the extern "C" entry points of the cache-size and block-sparse
+// operators: argument checks, workspace layout, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+#include "../../include/ddtree.h"
+#include "cache_ops.cuh"
+#include "host.cuh"
+
+namespace ddt {
+namespace {
+
+constexpr int kScoreTileKeys = 128;
+constexpr int kScoreMaxRows = 256;  // query rows of one tile
+
+int round16(int x) { return (x + 15) / 16 * 16; }
+
+bool clear_status(void* workspace, cudaStream_t s) {
+  return cudaMemsetAsync(workspace, 0, 4 * sizeof(int32_t), s) == cudaSuccess;
+}
+
+// Tiles of query rows and keys; false if the sizes do not fit the kernels' 32-bit counters.
+bool score_tiles(ScoreParams* p, int64_t keys, int64_t q_rows) {
+  const int64_t key_tiles = (keys + kScoreTileKeys - 1) / kScoreTileKeys;
+  if (q_rows > INT32_MAX || key_tiles * p->batch > INT32_MAX) return false;
+  p->key_tiles = static_cast<int32_t>(key_tiles);
+  return true;
+}
+
+struct WeightLayout {
+  size_t q_off, lse_off, bytes;
+};
+int weight_layout(const ddt_dims* d, int32_t num_sel, WeightLayout* w) {
+  const int rc = check_dims(d);
+  if (rc != DDT_OK) return rc;
+  if (num_sel < 0 || num_sel > 65535) return DDT_ERR_DIMS;
+  const size_t rows = size_t(d->batch) * num_sel * d->num_heads;
+  w->q_off = kStatusBytes;
+  w->lse_off = align_up(w->q_off + rows * kRowBytes, 256);
+  w->bytes = align_up(w->lse_off + rows * sizeof(float), 256);
+  return DDT_OK;
+}
+
+bool block_ok(int32_t block) { return block == 16 || block == 32 || block == 64 || block == 128; }
+
+struct SelectLayout {
+  int64_t blocks;
+  size_t q_off, scale_off, score_off, bytes;
+};
+int select_layout(const ddt_dims* d, int32_t block, SelectLayout* w) {
+  const int rc = check_dims(d);
+  if (rc != DDT_OK) return rc;
+  if (!block_ok(block)) return DDT_ERR_DIMS;
+  const size_t nodes = size_t(d->batch) * d->num_nodes, rows = nodes * d->num_heads;
+  w->blocks = (int64_t(d->max_prefix_len) + block - 1) / block;
+  w->q_off = kStatusBytes;
+  w->scale_off = align_up(w->q_off + rows * kRowBytes, 256);
+  w->score_off = align_up(w->scale_off + rows * sizeof(float), 256);
+  w->bytes = align_up(w->score_off + nodes * w->blocks * sizeof(float), 256);
+  return DDT_OK;
+}
+
+}  // namespace
+}  // namespace ddt
+
+using namespace ddt;
+
+extern "C" size_t ddtree_kv_weight_workspace_bytes(const ddt_dims* dims, int32_t num_sel) {
+  WeightLayout w;
+  return weight_layout(dims, num_sel, &w) == DDT_OK ? w.bytes : 0;
+}
+
+extern "C" int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_t* slot_idx, const int32_t* prefix_len,
+                                const float* lse, const int32_t* node_idx, int32_t num_sel, float sm_scale,
+                                float decay, const float* weight_in, float* weight_out, const ddt_dims* dims,
+                                void* workspace, size_t workspace_bytes, ddt_stream_t stream) {
+  WeightLayout w;
+  int rc = weight_layout(dims, num_sel, &w);
+  if (rc != DDT_OK) return rc;
+  if (dims->batch == 0) return DDT_OK;
+  if (!q || !kv_pool || !prefix_len || !lse || !workspace || (num_sel > 0 && !node_idx) ||
+      ((!slot_idx || !weight_out) && dims->max_prefix_len > 0) || (!weight_in && decay != 0.f))
+    return DDT_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(workspace, 256) || !aligned(slot_idx, 4) ||
+      !aligned(prefix_len, 4) || !aligned(lse, 4) || !aligned(node_idx, 4) || !aligned(weight_in, 4) ||
+      !aligned(weight_out, 4))
+    return DDT_ERR_ALIGN;
+  if (workspace_bytes < w.bytes) return DDT_ERR_WORKSPACE;
+  int sms = 0;
+  if ((rc = current_device(&sms)) != DDT_OK) return rc;
+  const bool packed = num_sel > 0;
+  ScoreParams p = {};
+  p.batch = dims->batch;
+  p.rows = (packed ? num_sel : dims->num_nodes) * dims->num_heads;
+  const int64_t q_rows = int64_t(p.batch) * p.rows;
+  if (!score_tiles(&p, dims->max_prefix_len, q_rows)) return DDT_ERR_DIMS;
+  p.tiles = (p.rows + kScoreMaxRows - 1) / kScoreMaxRows;
+  p.tile_rows = p.tile_n = round16((p.rows + p.tiles - 1) / p.tiles);
+  p.tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
+  p.keys = static_cast<const uint16_t*>(kv_pool);
+  p.slot_idx = slot_idx;
+  p.prefix_len = prefix_len;
+  p.pool_slots = dims->pool_slots;
+  p.max_prefix_len = dims->max_prefix_len;
+  p.block = 1;
+  p.slot_stride = dims->slot_stride;
+  p.heads = dims->num_heads;
+  p.nodes = dims->num_nodes;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.decay = decay;
+  p.weight_in = decay != 0.f ? weight_in : nullptr;
+  p.weight_out = weight_out;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.status = reinterpret_cast<int32_t*>(ws);
+  const void* qs = packed ? static_cast<const void*>(ws + w.q_off) : q;
+  p.row_aux = packed ? reinterpret_cast<const float*>(ws + w.lse_off) : lse;
+  if (!encode_pool_map(&p.tmap_q, qs, q_rows, 64, p.tile_n)) return DDT_ERR_LAUNCH;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!clear_status(workspace, s)) return DDT_ERR_LAUNCH;
+  if (packed) {
+    PackParams k = {};
+    k.q = static_cast<const uint16_t*>(q);
+    k.lse = lse;
+    k.node_idx = node_idx;
+    k.q_out = reinterpret_cast<uint16_t*>(ws + w.q_off);
+    k.lse_out = reinterpret_cast<float*>(ws + w.lse_off);
+    k.nodes = dims->num_nodes;
+    k.heads = dims->num_heads;
+    k.sel = num_sel;
+    k.status = p.status;
+    if (launch_pack_nodes(k, dims->batch, s) != cudaSuccess) return DDT_ERR_LAUNCH;
+  }
+  return launch_scores(p, kScoreWeight, sms, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
+}
+
+extern "C" int ddtree_kv_evict(const float* weight, const int32_t* slot_idx, const int32_t* prefix_len,
+                               const int32_t* keep_len, int32_t sink, int32_t recent, int32_t* slot_idx_out,
+                               float* weight_out, int32_t* prefix_len_out, int32_t* freed_slots, const ddt_dims* dims,
+                               void* workspace, ddt_stream_t stream) {
+  int rc = check_dims(dims);
+  if (rc != DDT_OK) return rc;
+  if (sink < 0 || recent < 0) return DDT_ERR_DIMS;
+  if (dims->batch == 0) return DDT_OK;
+  if (!prefix_len || !keep_len || !prefix_len_out || !workspace ||
+      ((!weight || !slot_idx || !slot_idx_out || !weight_out || !freed_slots) && dims->max_prefix_len > 0))
+    return DDT_ERR_NULL;
+  if (!aligned(workspace, 256) || !aligned(weight, 4) || !aligned(slot_idx, 4) || !aligned(prefix_len, 4) ||
+      !aligned(keep_len, 4) || !aligned(slot_idx_out, 4) || !aligned(weight_out, 4) || !aligned(prefix_len_out, 4) ||
+      !aligned(freed_slots, 4))
+    return DDT_ERR_ALIGN;
+  // a request's entries are read while others' are written: no output may cover an input or another output
+  const size_t table = size_t(dims->batch) * dims->slot_stride * 4, lens = size_t(dims->batch) * 4;
+  const struct { const void* p; size_t n; } in[] = {{weight, table}, {slot_idx, table}, {prefix_len, lens}, {keep_len, lens}},
+      out[] = {{slot_idx_out, table}, {weight_out, table}, {freed_slots, table}, {prefix_len_out, lens}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return DDT_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return DDT_ERR_ALIAS;
+  }
+  int sms = 0;
+  if ((rc = current_device(&sms)) != DDT_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!clear_status(workspace, s)) return DDT_ERR_LAUNCH;
+  EvictParams p = {};
+  p.weight = weight;
+  p.slot_idx = slot_idx;
+  p.prefix_len = prefix_len;
+  p.keep_len = keep_len;
+  p.slot_out = slot_idx_out;
+  p.weight_out = weight_out;
+  p.len_out = prefix_len_out;
+  p.freed = freed_slots;
+  p.stride = dims->slot_stride;
+  p.max_prefix_len = dims->max_prefix_len;
+  p.sink = sink;
+  p.recent = recent;
+  p.status = static_cast<int32_t*>(workspace);
+  return launch_kv_evict(p, dims->batch, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
+}
+
+extern "C" int ddtree_block_summary(const void* kv_pool, const int32_t* slot_idx, const int32_t* prefix_len,
+                                    const int32_t* from_len, int32_t block, void* summary, float* scale,
+                                    const ddt_dims* dims, void* workspace, ddt_stream_t stream) {
+  int rc = check_dims(dims);
+  if (rc != DDT_OK) return rc;
+  if (!block_ok(block)) return DDT_ERR_DIMS;
+  if (dims->batch == 0) return DDT_OK;
+  if (!kv_pool || !prefix_len || !workspace || ((!slot_idx || !summary || !scale) && dims->max_prefix_len > 0))
+    return DDT_ERR_NULL;
+  if (!aligned(kv_pool, 16) || !aligned(summary, 16) || !aligned(workspace, 256) || !aligned(slot_idx, 4) ||
+      !aligned(prefix_len, 4) || !aligned(from_len, 4) || !aligned(scale, 4))
+    return DDT_ERR_ALIGN;
+  int sms = 0;
+  if ((rc = current_device(&sms)) != DDT_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!clear_status(workspace, s)) return DDT_ERR_LAUNCH;
+  SummaryParams p = {};
+  p.kv = static_cast<const uint16_t*>(kv_pool);
+  p.slot_idx = slot_idx;
+  p.prefix_len = prefix_len;
+  p.from_len = from_len;
+  p.summary = static_cast<uint16_t*>(summary);
+  p.scale = scale;
+  p.pool_slots = dims->pool_slots;
+  p.slot_stride = dims->slot_stride;
+  p.max_prefix_len = dims->max_prefix_len;
+  p.block = block;
+  p.blocks = static_cast<int32_t>((int64_t(dims->max_prefix_len) + block - 1) / block);
+  p.status = static_cast<int32_t*>(workspace);
+  return launch_block_summary(p, dims->batch, sms, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
+}
+
+extern "C" size_t ddtree_block_select_workspace_bytes(const ddt_dims* dims, int32_t block) {
+  SelectLayout w;
+  return select_layout(dims, block, &w) == DDT_OK ? w.bytes : 0;
+}
+
+extern "C" int ddtree_block_select(const void* q, const void* summary, const float* scale, const int32_t* prefix_len,
+                                   int32_t block, int32_t topk, int32_t first, int32_t last, int32_t* block_idx,
+                                   const ddt_dims* dims, void* workspace, size_t workspace_bytes,
+                                   ddt_stream_t stream) {
+  SelectLayout w;
+  int rc = select_layout(dims, block, &w);
+  if (rc != DDT_OK) return rc;
+  if (topk < 1 || topk > (1 << 20) || first < 0 || last < 0) return DDT_ERR_DIMS;
+  if (dims->batch == 0) return DDT_OK;
+  if (!q || !prefix_len || !block_idx || !workspace || ((!summary || !scale) && w.blocks > 0)) return DDT_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(summary, 16) || !aligned(workspace, 256) || !aligned(scale, 4) ||
+      !aligned(prefix_len, 4) || !aligned(block_idx, 4))
+    return DDT_ERR_ALIGN;
+  if (workspace_bytes < w.bytes) return DDT_ERR_WORKSPACE;
+  int sms = 0;
+  if ((rc = current_device(&sms)) != DDT_OK) return rc;
+  const int H = dims->num_heads;
+  ScoreParams p = {};
+  p.batch = dims->batch;
+  p.rows = dims->num_nodes * H;
+  const int64_t q_rows = int64_t(p.batch) * p.rows;
+  if (!score_tiles(&p, w.blocks, q_rows) || w.blocks * p.batch > INT32_MAX) return DDT_ERR_DIMS;
+  // a tile holds whole nodes (up to 256 heads), so each epilogue set owns its nodes
+  p.tile_rows = H <= kScoreMaxRows ? std::min(p.rows, kScoreMaxRows / H * H) : kScoreMaxRows;
+  p.tile_n = round16(p.tile_rows);
+  p.tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.keys = static_cast<const uint16_t*>(summary);
+  p.prefix_len = prefix_len;
+  p.key_stride = w.blocks;
+  p.max_prefix_len = dims->max_prefix_len;
+  p.block = block;
+  p.heads = H;
+  p.nodes = dims->num_nodes;
+  p.row_aux = reinterpret_cast<const float*>(ws + w.scale_off);
+  p.key_scale = scale;
+  p.score = reinterpret_cast<float*>(ws + w.score_off);
+  p.status = reinterpret_cast<int32_t*>(ws);
+  if (!encode_pool_map(&p.tmap_q, ws + w.q_off, q_rows, 64, p.tile_n)) return DDT_ERR_LAUNCH;
+  QuantParams k = {};
+  k.q = static_cast<const uint16_t*>(q);
+  k.q_int = reinterpret_cast<uint16_t*>(ws + w.q_off);
+  k.q_scale = reinterpret_cast<float*>(ws + w.scale_off);
+  k.rows = q_rows;
+  TopkParams t = {};
+  t.score = p.score;
+  t.prefix_len = prefix_len;
+  t.block_idx = block_idx;
+  t.nodes = dims->num_nodes;
+  t.blocks = static_cast<int32_t>(w.blocks);
+  t.block = block;
+  t.topk = topk;
+  t.first = first;
+  t.last = last;
+  t.max_prefix_len = dims->max_prefix_len;
+  t.status = p.status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!clear_status(workspace, s) || launch_quant_rows(k, s) != cudaSuccess ||
+      launch_scores(p, kScoreBlock, sms, s) != cudaSuccess || launch_block_topk(t, dims->batch, s) != cudaSuccess)
+    return DDT_ERR_LAUNCH;
+  return DDT_OK;
+}

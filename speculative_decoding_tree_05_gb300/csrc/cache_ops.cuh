@@ -1,0 +1,118 @@
+// cache_ops.cuh -- launch parameters of the cache-size and block-sparse operators:
+// key weights, eviction, block summaries, block selection, block attention.
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include "kernels.cuh"
+
+namespace ddt {
+
+constexpr int32_t kStatusBadNode = 32;
+constexpr int32_t kStatusBadBlock = 64;
+
+// ---------------------------------------------------------------- scores of rows against queries
+// Shared by key weights and block selection: 128 (or, on a CTA pair, 256) key
+// rows stay in shared memory while the query rows stream past them.
+enum ScoreMode : int { kScoreWeight = 0, kScoreBlock = 1 };
+
+struct ScoreParams {
+  CUtensorMap tmap_q;        // queries as [rows][576] bf16, box 64 cols x box_rows, 128-byte swizzle
+  const uint16_t* keys;      // bf16 [*, 576]
+  const int32_t* slot_idx;   // [B, slot_stride], or null: request b's row j is keys[b * key_stride + j]
+  const int32_t* prefix_len; // [B]
+  int64_t pool_slots;
+  int64_t key_stride;        // rows per request when slot_idx is null; row stride of the outputs
+  int32_t max_prefix_len;
+  int32_t block;             // kScoreBlock: positions per block (rows = ceil(len / block)); else 1
+  int32_t slot_stride;
+  int32_t batch;
+  int32_t rows;              // query rows per request
+  int32_t tile_rows;         // query rows per tile
+  int32_t tiles;             // ceil(rows / tile_rows)
+  int32_t tile_n;            // MMA N: tile_rows rounded up
+  int32_t heads;             // kScoreBlock: consecutive rows that make one node
+  int32_t nodes;             // kScoreBlock: T
+  int32_t key_tiles;         // key tiles of the longest request
+  float scale_log2;          // kScoreWeight: sm_scale * log2(e)
+  float decay;
+  const float* row_aux;      // [B, rows]: kScoreWeight natural-log lse, kScoreBlock query scales
+  const float* weight_in;    // kScoreWeight: [B, slot_stride] or null
+  float* weight_out;         // kScoreWeight: [B, slot_stride]
+  const float* key_scale;    // kScoreBlock: [B, key_stride]
+  float* score;              // kScoreBlock: [B, T, key_stride]
+  int32_t* status;
+};
+
+cudaError_t configure_scores();
+cudaError_t launch_scores(const ScoreParams& p, ScoreMode mode, int sm_count, cudaStream_t stream);
+
+// Selected nodes' query rows and lse, packed (node_idx[b][s], -1 = none).
+struct PackParams {
+  const uint16_t* q;
+  const float* lse;
+  const int32_t* node_idx;   // [B, sel]
+  uint16_t* q_out;           // [B, sel, H, 576]
+  float* lse_out;            // [B, sel, H]; +inf for rows of no node
+  int32_t nodes, heads, sel;
+  int32_t* status;
+};
+cudaError_t launch_pack_nodes(const PackParams& p, int batch, cudaStream_t stream);
+
+// ---------------------------------------------------------------- eviction
+struct EvictParams {
+  const float* weight;       // [B, stride]
+  const int32_t* slot_idx;   // [B, stride]
+  const int32_t* prefix_len; // [B]
+  const int32_t* keep_len;   // [B]
+  int32_t* slot_out;         // [B, stride]
+  float* weight_out;         // [B, stride]
+  int32_t* len_out;          // [B]
+  int32_t* freed;            // [B, stride]
+  int32_t stride, max_prefix_len, sink, recent;
+  int32_t* status;
+};
+cudaError_t configure_evict();
+cudaError_t launch_kv_evict(const EvictParams& p, int batch, cudaStream_t stream);
+
+// ---------------------------------------------------------------- block summaries and selection
+struct SummaryParams {
+  const uint16_t* kv;
+  const int32_t* slot_idx;
+  const int32_t* prefix_len;
+  const int32_t* from_len;   // [B] or null
+  uint16_t* summary;         // bf16 [B, blocks, 576]: integers in [-127, 127]
+  float* scale;              // [B, blocks]
+  int64_t pool_slots;
+  int32_t slot_stride, max_prefix_len, block, blocks;
+  int32_t* status;
+};
+cudaError_t launch_block_summary(const SummaryParams& p, int batch, int sm_count, cudaStream_t stream);
+
+struct QuantParams {
+  const uint16_t* q;         // bf16 [rows, 576]
+  uint16_t* q_int;           // bf16 [rows, 576]: integers in [-127, 127]
+  float* q_scale;            // [rows]
+  int64_t rows;
+};
+cudaError_t launch_quant_rows(const QuantParams& p, cudaStream_t stream);
+
+struct TopkParams {
+  const float* score;        // [B, T, blocks]
+  const int32_t* prefix_len;
+  int32_t* block_idx;        // [B, T, topk]
+  int32_t nodes, blocks, block, topk, first, last, max_prefix_len;
+  int32_t* status;
+};
+cudaError_t configure_topk();
+cudaError_t launch_block_topk(const TopkParams& p, int batch, cudaStream_t stream);
+
+// Map of a score to an unsigned key with the same order: NaN lowest (equal to
+// -inf), -0 equal to +0.
+__host__ __device__ inline uint32_t order_key_bits(uint32_t u) {
+  if ((u & 0x7fffffffu) > 0x7f800000u) u = 0xff800000u;  // NaN -> -inf
+  if (u == 0x80000000u) u = 0u;                          // -0 -> +0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+}  // namespace ddt

@@ -1,0 +1,373 @@
+// key_scores.cu -- a reduction of exp(q.k) or of q.k over query rows, per key.
+//
+// Two operators need, for every key row k_j of a request, a value summed or
+// maximised over that request's query rows q_r:
+//   key weights     w_j   = sum_r exp(sm_scale q_r.k_j - lse_r)
+//   block selection s_tj  = scale_j * max over the heads r of node t of (qs_r * q_r.m_j)
+// The keys are the M side of the product and the query rows the N side, the
+// reverse of attention: an accumulator lane then belongs to one key and every
+// reduction over the rows stays inside a thread (no shuffle, no atomic, one
+// fixed order, so the results are the same bits on every run), and each key row
+// is fetched from the pool once, whatever the number of query rows.
+//
+// Per CTA (512 threads), a loop over tiles of 128 keys:
+//   warp 0       TMEM, and lane 0 issues the MMAs (M = 128 keys, N = up to 256 rows)
+//   warp 1       lane 0 loads the query rows by TMA: stages of 64 dims x N rows
+//   warps 4-11   two epilogue sets: one key per thread, set s takes the query
+//                tiles of parity s (TMEM columns [256 s, +256))
+//   warps 12-15  gather the key rows by 16-byte cp.async, zero-filled where
+//                there is no key, into three 192-dim groups.  A group is
+//                refilled as soon as the last query tile has used it, so with one query tile
+//                (the memory-bound case) two of the three groups are always in flight.
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include "cache_ops.cuh"
+#include "ptx.cuh"
+
+namespace ddt {
+namespace {
+
+constexpr int kScThreads = 512;
+constexpr int kScKeys = 128;
+constexpr int kScChunk = kScKeys * 128;         // 64 dims of 128 keys: 16 KB
+constexpr int kScGroups = 3;
+constexpr int kScGroupBytes = 3 * kScChunk;     // 192 dims
+constexpr int kScMaxN = 256;
+constexpr int kScStages = 2;
+constexpr int kScStageBytes = kScMaxN * 128;    // 32 KB
+constexpr int kScOffQ = kScGroups * kScGroupBytes;
+constexpr int kScOffAux = kScOffQ + kScStages * kScStageBytes;   // [2 sets][256] row constants
+constexpr int kScOffComb = kScOffAux + 2 * kScMaxN * 4;          // [2][128] sums handed from set 1 to set 0
+constexpr int kScSmem = kScOffComb + 2 * kScKeys * 4 + 1024;
+constexpr float kScLog2e = 1.4426950408889634f;
+
+struct ScShared {
+  uint64_t k_full[kScGroups], k_empty[kScGroups];
+  uint64_t q_full[kScStages], q_empty[kScStages];
+  uint64_t s_full[2], s_free[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ int clamp_len(const int32_t* prefix_len, int b, int max_len) {
+  const int L = __ldg(prefix_len + b);
+  return L < 0 ? 0 : (L > max_len ? max_len : L);
+}
+
+// Keys of request b: positions, or blocks of positions.
+__device__ __forceinline__ int key_count(const ScoreParams& p, int b) {
+  const int L = clamp_len(p.prefix_len, b, p.max_prefix_len);
+  return (L + p.block - 1) / p.block;
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_constant__ ScoreParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ScShared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = &sh.abort;
+
+  if (tid == 0) {
+    for (int i = 0; i < kScGroups; ++i) {
+      mbar_init(&sh.k_full[i], 128);
+      mbar_init(&sh.k_empty[i], 1);
+    }
+    for (int i = 0; i < kScStages; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_free[i], 128);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&sh.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  const int units = p.batch * p.key_tiles;
+  bool ok = true;
+  // with more than 256 heads a node spans tiles, so one set takes them all
+  const bool two_sets = kMode == kScoreWeight || p.heads <= kScMaxN;
+
+  // every role walks the same units: those of its CTA that hold keys
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(kScKeys, p.tile_n, false, false);
+      const uint64_t d_k = smem_desc(base, 16, 1024, kSwizzle128B);
+      const uint64_t d_q = smem_desc(base + kScOffQ, 16, 1024, kSwizzle128B);
+      uint32_t n_unit = 0, n_stage = 0, n_tile = 0;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const int b = u / p.key_tiles, kt = u - b * p.key_tiles;
+        if (kt * kScKeys >= key_count(p, b)) continue;
+        for (int qt = 0; ok && qt < p.tiles; ++qt, ++n_tile) {
+          const uint32_t buf = n_tile & 1;
+          if (n_tile >= 2 && !mbar_wait_abortable(&sh.s_free[buf], ((n_tile >> 1) - 1) & 1, abort, false, __LINE__)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          for (int c = 0; c < 9; ++c, ++n_stage) {
+            if (qt == 0 && c % 3 == 0) {
+              if (!mbar_wait_abortable(&sh.k_full[c / 3], n_unit & 1, abort, false, __LINE__)) {
+                ok = false;
+                break;
+              }
+              fence_proxy_async_smem();  // the rows were written by cp.async
+            }
+            const uint32_t st = n_stage % kScStages;
+            if (!mbar_wait_abortable(&sh.q_full[st], (n_stage / kScStages) & 1, abort, false, __LINE__)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss(tmem + buf * kScMaxN, desc_advance(d_k, c * kScChunk + ks * 32),
+                     desc_advance(d_q, st * kScStageBytes + ks * 32), idesc, (c | ks) ? 1u : 0u);
+            mma_commit(&sh.q_empty[st]);
+            if (qt == p.tiles - 1 && c % 3 == 2) mma_commit(&sh.k_empty[c / 3]);
+          }
+          if (ok) mma_commit(&sh.s_full[buf]);
+        }
+        ++n_unit;
+      }
+      mma_commit(&sh.drain);
+      mbar_wait(&sh.drain, 0);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t n_stage = 0;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const int b = u / p.key_tiles, kt = u - b * p.key_tiles;
+        if (kt * kScKeys >= key_count(p, b)) continue;
+        for (int qt = 0; ok && qt < p.tiles; ++qt) {
+          for (int c = 0; c < 9; ++c, ++n_stage) {
+            const uint32_t st = n_stage % kScStages;
+            if (n_stage >= kScStages &&
+                !mbar_wait_abortable(&sh.q_empty[st], ((n_stage / kScStages) - 1) & 1, abort, false, __LINE__)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&sh.q_full[st], p.tile_n * 128);
+            tma_load_2d(base + kScOffQ + st * kScStageBytes, &p.tmap_q, c * 64, b * p.rows + qt * p.tile_rows,
+                        &sh.q_full[st]);
+          }
+        }
+      }
+      // after a give-up, the loads still in flight land before the CTA exits
+      if (!ok)
+        for (uint32_t i = n_stage > kScStages ? n_stage - kScStages : 0; i < n_stage; ++i)
+          mbar_wait(&sh.q_full[i % kScStages], (i / kScStages) & 1);
+    }
+  } else if (warp >= 12) {
+    const int pw = warp - 12;
+    uint32_t n_unit = 0;
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      const int b = u / p.key_tiles, kt = u - b * p.key_tiles;
+      const int n = key_count(p, b);
+      if (kt * kScKeys >= n) continue;
+      // this warp gathers keys 32 pw .. 32 pw + 31 of the tile, lane l holding the row of key l
+      const int j = kt * kScKeys + 32 * pw + lane;
+      int64_t row = -1;
+      if (j < n) {
+        if (p.slot_idx != nullptr) {
+          const int slot = __ldg(p.slot_idx + static_cast<int64_t>(b) * p.slot_stride + j);
+          if (slot >= 0 && slot < p.pool_slots) row = slot;
+          if (row < 0) atomicOr(p.status, kStatusBadSlot);
+        } else {
+          row = static_cast<int64_t>(b) * p.key_stride + j;
+        }
+      }
+      const int row32 = static_cast<int>(row);  // rows stay below 2^31
+      for (int g = 0; g < kScGroups; ++g) {
+        const bool w = n_unit == 0 || mbar_wait_abortable(&sh.k_empty[g], (n_unit - 1) & 1, abort, false, __LINE__);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
+        // 24 pieces of 16 bytes per row and group: consecutive lanes take consecutive pieces
+#pragma unroll 4
+        for (int i = 0; i < 24; ++i) {
+          const int e = i * 32 + lane;
+          const int r = e / 24, x = e - r * 24;
+          const int src_row = __shfl_sync(0xffffffffu, row32, r);
+          const int rr = 32 * pw + r;
+          const uint32_t dst = base + g * kScGroupBytes + (x >> 3) * kScChunk + rr * 128 + (((x & 7) ^ (rr & 7)) << 4);
+          const uint16_t* src = p.keys + (src_row < 0 ? 0 : static_cast<int64_t>(src_row) * kDqk + g * 192 + x * 8);
+          cp_async16(dst, src, src_row < 0 ? 0u : 16u);
+        }
+        cp_async_arrive_noinc(&sh.k_full[g]);
+      }
+      ++n_unit;
+    }
+    cp_async_wait<0>();
+  } else if (warp >= 4) {
+    const int set = (warp - 4) >> 2;
+    const int r = (warp & 3) * 32 + lane;  // key of the tile = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    float* aux = reinterpret_cast<float*>(smem + kScOffAux) + set * kScMaxN;
+    float* comb = reinterpret_cast<float*>(smem + kScOffComb);
+    uint32_t n_unit = 0, n_tile = 0;
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      const int b = u / p.key_tiles, kt = u - b * p.key_tiles;
+      const int n = key_count(p, b);
+      if (kt * kScKeys >= n) continue;
+      const int j = kt * kScKeys + r;
+      float acc = kMode == kScoreWeight ? 0.f : -CUDART_INF_F;
+      int node = 0, left = p.heads;  // kScoreBlock: the node that the next row belongs to, its rows left
+      for (int qt = 0; ok && qt < p.tiles; ++qt, ++n_tile) {
+        if ((two_sets ? static_cast<int>(n_tile & 1) : 0) != set) continue;
+        const uint32_t buf = n_tile & 1;
+        const int row0 = qt * p.tile_rows;
+        const int live = min(p.tile_rows, p.rows - row0);
+        // row constants of the tile: weights -lse in log2 units, -inf where a row counts for nothing
+        bar_sync(1 + set, 128);  // the last tile's are read
+        for (int i = r; i < kScMaxN; i += 128) {
+          float a;
+          if (kMode == kScoreWeight) {
+            const float l = i < live ? __ldg(p.row_aux + static_cast<int64_t>(b) * p.rows + row0 + i) : CUDART_INF_F;
+            a = fabsf(l) == CUDART_INF_F ? -CUDART_INF_F : -l * kScLog2e;
+          } else {
+            a = i < live ? __ldg(p.row_aux + static_cast<int64_t>(b) * p.rows + row0 + i) : CUDART_NAN_F;
+          }
+          aux[i] = a;
+        }
+        // the set leaves together if a wait of one of its warps ran out
+        const bool got = mbar_wait_abortable(&sh.s_full[buf], (n_tile >> 1) & 1, abort, false, __LINE__);
+        if (bar_red_or(1 + set, 128, !got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (kMode == kScoreBlock && two_sets) node = row0 / p.heads;
+        for (int c = 0; c < p.tile_n; c += 32) {
+          float s[32];
+          // (the columns past tile_n of the last 32 are stale: their constants are not used)
+          tmem_ld32(tmem + lane_off + buf * kScMaxN + c, s);
+          if (kMode == kScoreWeight) {
+            const bool all_live = __all_sync(0xffffffffu, aux[c + lane] != -CUDART_INF_F);
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            if (all_live) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(aux + c + k);
+                t[0] += fast_exp2(fmaf(s[k], p.scale_log2, a.x));
+                t[1] += fast_exp2(fmaf(s[k + 1], p.scale_log2, a.y));
+                t[2] += fast_exp2(fmaf(s[k + 2], p.scale_log2, a.z));
+                t[3] += fast_exp2(fmaf(s[k + 3], p.scale_log2, a.w));
+              }
+            } else {
+              // a row without weight may hold anything, NaN included: it is left out, not multiplied by zero
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const float a = aux[c + k];
+                t[k & 3] += a == -CUDART_INF_F ? 0.f : fast_exp2(fmaf(s[k], p.scale_log2, a));
+              }
+            }
+            acc += (t[0] + t[1]) + (t[2] + t[3]);
+          } else {
+            const int nc = min(32, live - c);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              if (k < nc) {
+                // both products rounded to 32 bits: part of the definition of the score; fmaxf drops a NaN scale
+                acc = fmaxf(acc, __fmul_rn(s[k], aux[c + k]));
+                if (--left == 0) {
+                  if (j < n)
+                    p.score[(static_cast<int64_t>(b) * p.nodes + node) * p.key_stride + j] =
+                        __fmul_rn(acc, __ldg(p.key_scale + static_cast<int64_t>(b) * p.key_stride + j));
+                  acc = -CUDART_INF_F;
+                  left = p.heads;
+                  ++node;
+                }
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&sh.s_free[buf]);
+      }
+      if (bar_red_or(3, 256, !ok)) {
+        ok = false;
+        break;
+      }
+      if (kMode == kScoreWeight) {
+        // set 1 hands its sum to set 0 (two slots: one barrier a unit is enough)
+        float* slot = comb + (n_unit & 1) * kScKeys;
+        if (set == 1) slot[r] = acc;
+        bar_sync(3, 256);
+        if (set == 0 && j < n) {
+          const int64_t at = static_cast<int64_t>(b) * p.slot_stride + j;
+          const int sl = __ldg(p.slot_idx + at);
+          const float sum = sl >= 0 && sl < p.pool_slots ? acc + slot[r] : 0.f;
+          p.weight_out[at] = p.weight_in != nullptr ? fmaf(p.decay, p.weight_in[at], sum) : sum;
+        }
+      }
+      ++n_unit;
+    }
+  }
+  if (!ok) {
+    *abort = 1;
+    atomicOr(p.status, kStatusTimeout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+  if (blockIdx.x == 0)
+    for (int b = tid; b < p.batch; b += kScThreads) {
+      const int L = __ldg(p.prefix_len + b);
+      if (L < 0 || L > p.max_prefix_len) atomicOr(p.status, kStatusBadPrefix);
+    }
+}
+
+// One CTA copies one selected node's rows (H x 72 pieces of 16 bytes) and lse.
+__global__ void __launch_bounds__(256) pack_nodes_kernel(PackParams p) {
+  const int s = blockIdx.x, b = blockIdx.y;
+  const int t = __ldg(p.node_idx + static_cast<int64_t>(b) * p.sel + s);
+  const bool in = t >= 0 && t < p.nodes;
+  if (!in && t != -1 && threadIdx.x == 0) atomicOr(p.status, kStatusBadNode);
+  const int64_t to = (static_cast<int64_t>(b) * p.sel + s) * p.heads;
+  const int64_t from = (static_cast<int64_t>(b) * p.nodes + (in ? t : 0)) * p.heads;
+  const uint4* src = reinterpret_cast<const uint4*>(p.q + from * kDqk);
+  uint4* dst = reinterpret_cast<uint4*>(p.q_out + to * kDqk);
+  for (int i = threadIdx.x; i < p.heads * kChunks; i += 256) dst[i] = in ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+  for (int h = threadIdx.x; h < p.heads; h += 256) p.lse_out[to + h] = in ? __ldg(p.lse + from + h) : CUDART_INF_F;
+}
+
+}  // namespace
+
+cudaError_t configure_scores() {
+  cudaError_t e = cudaFuncSetAttribute(score_kernel<kScoreWeight>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(score_kernel<kScoreBlock>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScSmem);
+}
+
+cudaError_t launch_scores(const ScoreParams& p, ScoreMode mode, int sm_count, cudaStream_t stream) {
+  const int64_t units = int64_t(p.batch) * p.key_tiles;
+  if (units == 0) return cudaSuccess;
+  const int grid = static_cast<int>(units < sm_count ? units : sm_count);
+  if (mode == kScoreWeight)
+    score_kernel<kScoreWeight><<<grid, kScThreads, kScSmem, stream>>>(p);
+  else
+    score_kernel<kScoreBlock><<<grid, kScThreads, kScSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pack_nodes(const PackParams& p, int batch, cudaStream_t stream) {
+  pack_nodes_kernel<<<dim3(p.sel, batch), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace ddt

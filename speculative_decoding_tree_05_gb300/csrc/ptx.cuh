@@ -159,6 +159,13 @@ __device__ __forceinline__ void st_shared_cluster_b32(uint32_t remote_addr, int 
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(remote_addr), "r"(v) : "memory");
 }
 
+// Plain 4-byte load from a peer CTA's shared memory (after a cluster barrier).
+__device__ __forceinline__ int ld_shared_cluster_b32(uint32_t remote_addr) {
+  int v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(remote_addr) : "memory");
+  return v;
+}
+
 // 4-byte variant of st_async_v4.
 __device__ __forceinline__ void st_async_b32(uint32_t remote_addr, uint32_t v, uint32_t remote_bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(remote_addr), "r"(v),

@@ -23,12 +23,16 @@ STATUS_BAD_PARENT = 2
 STATUS_BAD_PREFIX = 4
 STATUS_TIMEOUT = 8
 STATUS_BAD_TREE_LEN = 16
+STATUS_BAD_NODE = 32
+STATUS_BAD_BLOCK = 64
 
 EXPORTS = ("ddtree_verify_workspace_bytes", "ddtree_verify_attn", "ddtree_verify_attn_fused",
            "ddtree_verify_attn_ragged",
            "ddtree_verify_prefix_phase",
            "ddtree_verify_merge_phase", "ddtree_verify_attn_static_scratch", "ddtree_kv_compact",
            "ddtree_kv_compact_check", "ddtree_verify_sparse_workspace_bytes", "ddtree_verify_attn_sparse",
+           "ddtree_kv_weight_workspace_bytes", "ddtree_kv_weight", "ddtree_kv_evict", "ddtree_block_summary",
+           "ddtree_block_select_workspace_bytes", "ddtree_block_select",
            "ddtree_read_device_status", "ddtree_status_string")
 
 
@@ -84,6 +88,20 @@ def load(path: str):
         L.ddtree_verify_attn_sparse.restype = ctypes.c_int
         L.ddtree_verify_attn_sparse.argtypes = [vp, vp, i32p, ctypes.c_float, vp, vp, ctypes.POINTER(Dims), vp,
                                                 ctypes.c_size_t, vp]
+    if hasattr(L, "ddtree_kv_weight"):
+        i32, f32, size, dims = ctypes.c_int32, ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(Dims)
+        L.ddtree_kv_weight_workspace_bytes.restype = size
+        L.ddtree_kv_weight_workspace_bytes.argtypes = [dims, i32]
+        L.ddtree_kv_weight.restype = ctypes.c_int
+        L.ddtree_kv_weight.argtypes = [vp, vp, i32p, i32p, vp, i32p, i32, f32, f32, vp, vp, dims, vp, size, vp]
+        L.ddtree_kv_evict.restype = ctypes.c_int
+        L.ddtree_kv_evict.argtypes = [vp, i32p, i32p, i32p, i32, i32, i32p, vp, i32p, i32p, dims, vp, vp]
+        L.ddtree_block_summary.restype = ctypes.c_int
+        L.ddtree_block_summary.argtypes = [vp, i32p, i32p, i32p, i32, vp, vp, dims, vp, vp]
+        L.ddtree_block_select_workspace_bytes.restype = size
+        L.ddtree_block_select_workspace_bytes.argtypes = [dims, i32]
+        L.ddtree_block_select.restype = ctypes.c_int
+        L.ddtree_block_select.argtypes = [vp, vp, vp, i32p, i32, i32, i32, i32, i32p, dims, vp, size, vp]
     if hasattr(L, "ddtree_internal_plan"):
         L.ddtree_internal_plan.restype = ctypes.c_int
         L.ddtree_internal_plan.argtypes = [ctypes.POINTER(Dims), ctypes.c_int, ctypes.POINTER(ctypes.c_int32)]
@@ -236,6 +254,221 @@ class SparseVerifier:
                                                 self.workspace.numel(), _stream(stream))
         _check(rc, "ddtree_verify_attn_sparse")
         return out, lse
+
+    def status(self, stream=None) -> int:
+        return read_device_status(self.workspace, stream, library=self.lib)
+
+
+def _need(device, **tensors):
+    """Check tensors given as name=(tensor, dtype, shape): type, shape, contiguity and device."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}"
+                             + ("" if t.is_contiguous() else " (not contiguous)"))
+
+
+class _On:
+    """Makes `device` the current one for a call (the library works on the current device)."""
+
+    def __init__(self, device):
+        import torch
+        self.index = device.index
+        self.back = None if torch.cuda.current_device() == device.index else torch.cuda.current_device()
+
+    def __enter__(self):
+        if self.back is not None:
+            import torch
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            import torch
+            torch.cuda.set_device(self.back)
+
+
+def _cuda_device(device):
+    import torch
+    d = torch.device("cuda") if device is None else torch.device(device)
+    if d.type != "cuda":
+        raise ValueError(f"a CUDA device is needed, got {d}")
+    return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
+def _on_cuda(t, name):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    return t.device
+
+
+def _stream_of(device, stream):
+    import torch
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+class KeyWeights:
+    """Accumulated attention weight of every prefix key (ddtree_kv_weight), with a workspace for one set of sizes.
+
+    Call after a verify call with its q and lse: out[b, j] = decay * weight[b, j] + the softmax weights that the
+    chosen nodes' heads gave prefix position j.  node_idx [B, S] int32 (-1 = none) chooses nodes, for example the
+    accepted path; without it every node counts.  weight and out are fp32 [B, slot_stride]; out=weight updates in
+    place; entries from prefix_len[b] on are not written.  max_sel bounds S (default: the tree's nodes).
+    """
+
+    def __init__(self, batch, nodes, heads, pool_slots, slot_stride, max_prefix_len=None, max_sel=None, device=None,
+                 library=None):
+        import torch
+        self.lib = lib() if library is None else library
+        self.dims = make_dims(batch, nodes, heads, pool_slots, slot_stride,
+                              slot_stride if max_prefix_len is None else max_prefix_len)
+        self.max_sel = int(nodes if max_sel is None else max_sel)
+        self.device = _cuda_device(device)
+        n = int(self.lib.ddtree_kv_weight_workspace_bytes(ctypes.byref(self.dims), self.max_sel))
+        if n == 0:
+            raise DDTError(-2, "ddtree_kv_weight_workspace_bytes")
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def __call__(self, q, kv_pool, slot_idx, prefix_len, lse, sm_scale, weight=None, decay=1.0, node_idx=None,
+                 out=None, stream=None):
+        import torch
+        d = self.dims
+        table = (d.batch, d.slot_stride)
+        if weight is None:
+            decay = 0.0
+        if out is None:
+            out = torch.zeros(table, dtype=torch.float32, device=self.device)
+        checks = dict(q=(q, torch.bfloat16, (d.batch, d.num_nodes, d.num_heads, D_QK)),
+                      kv_pool=(kv_pool, torch.bfloat16, (d.pool_slots, D_QK)),
+                      slot_idx=(slot_idx, torch.int32, table), prefix_len=(prefix_len, torch.int32, (d.batch,)),
+                      lse=(lse, torch.float32, (d.batch, d.num_nodes, d.num_heads)), out=(out, torch.float32, table))
+        if weight is not None:
+            checks["weight"] = (weight, torch.float32, table)
+        sel = 0
+        if node_idx is not None:
+            if node_idx.dim() != 2 or not 1 <= node_idx.shape[1] <= self.max_sel:
+                raise ValueError(f"node_idx must be [batch, 1..{self.max_sel}], got {tuple(node_idx.shape)}")
+            sel = node_idx.shape[1]
+            checks["node_idx"] = (node_idx, torch.int32, (d.batch, sel))
+        _need(self.device, **checks)
+        with _On(self.device):
+            rc = self.lib.ddtree_kv_weight(_ptr(q), _ptr(kv_pool), _ptr(slot_idx), _ptr(prefix_len), _ptr(lse),
+                                           _ptr(node_idx), sel, float(sm_scale), float(decay), _ptr(weight),
+                                           _ptr(out), ctypes.byref(d), _ptr(self.workspace), self.workspace.numel(),
+                                           _stream_of(self.device, stream))
+        _check(rc, "ddtree_kv_weight")
+        return out
+
+    def status(self, stream=None) -> int:
+        return read_device_status(self.workspace, stream, library=self.lib)
+
+
+def kv_evict(weight, slot_idx, prefix_len, keep_len, sink=0, recent=0, slot_idx_out=None, weight_out=None,
+             prefix_len_out=None, freed=None, max_prefix_len=None, workspace=None, stream=None):
+    """Keep each request's heaviest keep_len[b] positions (ddtree_kv_evict).
+
+    The first `sink` and last `recent` positions stay first, then the larger weight, ties to the lower position.
+    Returns (slot_idx_out, weight_out, prefix_len_out, freed): the kept entries in order, and the slots that are
+    free now (prefix_len[b] - prefix_len_out[b] of them).  Outputs must be other buffers than the inputs.
+    """
+    import torch
+    device = _on_cuda(weight, "weight")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [batch, slot_stride]")
+    B, stride = weight.shape
+    slot_idx_out = torch.zeros_like(slot_idx) if slot_idx_out is None else slot_idx_out
+    weight_out = torch.zeros_like(weight) if weight_out is None else weight_out
+    prefix_len_out = torch.empty_like(prefix_len) if prefix_len_out is None else prefix_len_out
+    freed = torch.zeros_like(slot_idx) if freed is None else freed
+    workspace = torch.empty(256, dtype=torch.uint8, device=device) if workspace is None else workspace
+    _need(device, weight=(weight, torch.float32, (B, stride)), slot_idx=(slot_idx, torch.int32, (B, stride)),
+          prefix_len=(prefix_len, torch.int32, (B,)), keep_len=(keep_len, torch.int32, (B,)),
+          slot_idx_out=(slot_idx_out, torch.int32, (B, stride)), weight_out=(weight_out, torch.float32, (B, stride)),
+          prefix_len_out=(prefix_len_out, torch.int32, (B,)), freed=(freed, torch.int32, (B, stride)),
+          workspace=(workspace, torch.uint8, workspace.shape))
+    if workspace.numel() < 256:
+        raise ValueError("workspace must hold 256 bytes")
+    dims = make_dims(B, 1, 1, 1, stride, stride if max_prefix_len is None else max_prefix_len)
+    with _On(device):
+        rc = lib().ddtree_kv_evict(_ptr(weight), _ptr(slot_idx), _ptr(prefix_len), _ptr(keep_len), int(sink),
+                                   int(recent), _ptr(slot_idx_out), _ptr(weight_out), _ptr(prefix_len_out),
+                                   _ptr(freed), ctypes.byref(dims), _ptr(workspace), _stream_of(device, stream))
+    _check(rc, "ddtree_kv_evict")
+    return slot_idx_out, weight_out, prefix_len_out, freed
+
+
+def block_summary(kv_pool, slot_idx, prefix_len, block, from_len=None, summary=None, scale=None, max_prefix_len=None,
+                  workspace=None, stream=None):
+    """8-bit means of each request's blocks of `block` positions (ddtree_block_summary).
+
+    Returns (summary bf16 [B, N, 576] of integers in [-127, 127], scale fp32 [B, N]), N = ceil(max_prefix_len /
+    block).  With from_len (int32 [B]) only blocks that hold a position at or after it are computed; pass the
+    summary and scale of the step before.
+    """
+    import torch
+    device = _on_cuda(kv_pool, "kv_pool")
+    if slot_idx.dim() != 2 or kv_pool.dim() != 2:
+        raise ValueError("slot_idx must be [batch, slot_stride] and kv_pool [slots, 576]")
+    B, stride = slot_idx.shape
+    dims = make_dims(B, 1, 1, kv_pool.shape[0], stride, stride if max_prefix_len is None else max_prefix_len)
+    n = -(-dims.max_prefix_len // int(block)) if block > 0 else 0
+    if from_len is not None and (summary is None or scale is None):
+        raise ValueError("from_len updates the summary and scale of an earlier call: pass both")
+    summary = torch.zeros((B, n, D_QK), dtype=torch.bfloat16, device=device) if summary is None else summary
+    scale = torch.zeros((B, n), dtype=torch.float32, device=device) if scale is None else scale
+    workspace = torch.empty(256, dtype=torch.uint8, device=device) if workspace is None else workspace
+    checks = dict(kv_pool=(kv_pool, torch.bfloat16, (dims.pool_slots, D_QK)),
+                  slot_idx=(slot_idx, torch.int32, (B, stride)), prefix_len=(prefix_len, torch.int32, (B,)),
+                  summary=(summary, torch.bfloat16, (B, n, D_QK)), scale=(scale, torch.float32, (B, n)),
+                  workspace=(workspace, torch.uint8, workspace.shape))
+    if from_len is not None:
+        checks["from_len"] = (from_len, torch.int32, (B,))
+    _need(device, **checks)
+    if workspace.numel() < 256:
+        raise ValueError("workspace must hold 256 bytes")
+    with _On(device):
+        rc = lib().ddtree_block_summary(_ptr(kv_pool), _ptr(slot_idx), _ptr(prefix_len), _ptr(from_len), int(block),
+                                        _ptr(summary), _ptr(scale), ctypes.byref(dims), _ptr(workspace),
+                                        _stream_of(device, stream))
+    _check(rc, "ddtree_block_summary")
+    return summary, scale
+
+
+class BlockSelector:
+    """The best blocks of each tree node by a cheap score (ddtree_block_select), with a workspace for one set of sizes.
+
+    Call with q [B, T, H, 576] bf16 and block_summary's results; returns int32 [B, T, topk], the chosen blocks in
+    ascending order, then -1.  The first `first` and last `last` blocks of a prefix are always chosen.
+    """
+
+    def __init__(self, batch, nodes, heads, max_prefix_len, block, topk, first=0, last=1, device=None, library=None):
+        import torch
+        self.lib = lib() if library is None else library
+        self.dims = make_dims(batch, nodes, heads, 1, max_prefix_len, max_prefix_len)
+        self.block, self.topk, self.first, self.last = int(block), int(topk), int(first), int(last)
+        self.device = _cuda_device(device)
+        n = int(self.lib.ddtree_block_select_workspace_bytes(ctypes.byref(self.dims), self.block))
+        if n == 0:
+            raise DDTError(-2, "ddtree_block_select_workspace_bytes")
+        self.blocks = -(-int(max_prefix_len) // self.block)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def __call__(self, q, summary, scale, prefix_len, out=None, stream=None):
+        import torch
+        d = self.dims
+        if out is None:
+            out = torch.empty((d.batch, d.num_nodes, self.topk), dtype=torch.int32, device=self.device)
+        _need(self.device, q=(q, torch.bfloat16, (d.batch, d.num_nodes, d.num_heads, D_QK)),
+              summary=(summary, torch.bfloat16, (d.batch, self.blocks, D_QK)),
+              scale=(scale, torch.float32, (d.batch, self.blocks)), prefix_len=(prefix_len, torch.int32, (d.batch,)),
+              out=(out, torch.int32, (d.batch, d.num_nodes, self.topk)))
+        with _On(self.device):
+            rc = self.lib.ddtree_block_select(_ptr(q), _ptr(summary), _ptr(scale), _ptr(prefix_len), self.block,
+                                              self.topk, self.first, self.last, _ptr(out), ctypes.byref(d),
+                                              _ptr(self.workspace), self.workspace.numel(),
+                                              _stream_of(self.device, stream))
+        _check(rc, "ddtree_block_select")
+        return out
 
     def status(self, stream=None) -> int:
         return read_device_status(self.workspace, stream, library=self.lib)
