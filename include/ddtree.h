@@ -397,6 +397,30 @@ DDT_API int ddtree_block_select(const void* q, const void* summary, const float*
                                 int32_t block, int32_t topk, int32_t first, int32_t last, int32_t* block_idx,
                                 const ddt_dims* dims, void* workspace, size_t workspace_bytes, ddt_stream_t stream);
 
+/*
+ * ddtree_verify_attn_blocks: verify attention over each node's own blocks.  Node
+ * (b, t) attends, for all its H heads, to the prefix positions of the blocks in
+ * block_idx[b][t] (cut at prefix_len[b]), to its ancestors and to itself.
+ *   block_idx  int32 [B, T, topk] device, in any order; -1 = none, a block listed
+ *              twice counts once, other values that are no block of the prefix
+ *              are left out and set DDT_STATUS_BAD_BLOCK.  topk <= 2^20.
+ *   out        bf16 [B, T, H, 512] (the operand type of the product that follows)
+ *   lse        fp32 [B, T, H]
+ * The other arguments are ddtree_verify_attn's, and with every block listed it
+ * computes the same.  Nodes are processed in groups of up to 64 (node, head)
+ * rows over the union of their lists; the softmax weights are rounded to bf16,
+ * scores and sums are fp32.  A non-finite key row reaches only the nodes that
+ * list its block.  Results are the same bits on every run.
+ * workspace >= ddtree_verify_blocks_workspace_bytes(dims, block, topk), which
+ * needs a current CUDA device.
+ */
+DDT_API size_t ddtree_verify_blocks_workspace_bytes(const ddt_dims* dims, int32_t block, int32_t topk);
+DDT_API int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, const int32_t* slot_idx,
+                                      const int32_t* prefix_len, const int32_t* tree_parent,
+                                      const int32_t* tree_slot_idx, const int32_t* block_idx, int32_t block,
+                                      int32_t topk, float sm_scale, void* out, float* lse, const ddt_dims* dims,
+                                      void* workspace, size_t workspace_bytes, ddt_stream_t stream);
+
 /* Waits for `stream`, then copies the status word of the last call that used
  * `workspace` to *host_status.  Returns DDT_OK or DDT_ERR_*.  The kernels write
  * the word asynchronously on the stream the verify call was enqueued on, so

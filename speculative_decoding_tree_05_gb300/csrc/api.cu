@@ -38,7 +38,8 @@ int device_info(DeviceInfo* out) {
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) == cudaSuccess &&
         cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
         major == 10 && minor == 3 && configure_prefix() == cudaSuccess && configure_tail_merge() == cudaSuccess &&
-        configure_scores() == cudaSuccess && configure_evict() == cudaSuccess && configure_topk() == cudaSuccess)
+        configure_scores() == cudaSuccess && configure_evict() == cudaSuccess && configure_topk() == cudaSuccess &&
+        configure_block_attn() == cudaSuccess)
       d.ok = true;
     g_dev[dev] = d;
   });

@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kScoreTileKeys = 128;
 constexpr int kScoreMaxRows = 256;  // query rows of one tile
+constexpr int kBlockUnitTiles = 4;  // fixed cost of one block-attention unit, in 64-key tiles
 
 int round16(int x) { return (x + 15) / 16 * 16; }
 
@@ -59,6 +60,46 @@ int select_layout(const ddt_dims* d, int32_t block, SelectLayout* w) {
   w->scale_off = align_up(w->q_off + rows * kRowBytes, 256);
   w->score_off = align_up(w->scale_off + rows * sizeof(float), 256);
   w->bytes = align_up(w->score_off + nodes * w->blocks * sizeof(float), 256);
+  return DDT_OK;
+}
+
+struct BlocksLayout {
+  int groups, group_nodes, splits, row_tiles;
+  int64_t list_cap;
+  size_t len_off, list_off, lse_off, o_off, bytes;
+};
+
+// Groups of up to 64 (node, head) rows, and the key splits of each.  The splits
+// minimise waves * (64-key tiles of a unit + kBlockUnitTiles), the tiles being
+// those of lists that do not overlap (how far they do is known on the device only).
+int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, BlocksLayout* w) {
+  const int rc = check_dims(d);
+  if (rc != DDT_OK) return rc;
+  if (!block_ok(block) || topk < 1 || topk > (1 << 20)) return DDT_ERR_DIMS;
+  const int H = d->num_heads, T = d->num_nodes;
+  w->group_nodes = H <= kBlockRows ? std::min(T, kBlockRows / H) : 1;
+  w->groups = H <= kBlockRows ? (T + w->group_nodes - 1) / w->group_nodes : T * ((H + kBlockRows - 1) / kBlockRows);
+  const int64_t all = int64_t(d->batch) * w->groups;
+  if (all > (1 << 30)) return DDT_ERR_DIMS;
+  const int64_t blocks = (int64_t(d->max_prefix_len) + block - 1) / block;
+  w->list_cap = std::min<int64_t>(int64_t(w->group_nodes) * topk, blocks);
+  const int64_t tiles = std::max<int64_t>(1, (w->list_cap * block + 63) / 64);
+  int64_t best_cost = -1;
+  w->splits = 1;
+  for (int s = 1; s <= std::min<int64_t>(tiles, 32); ++s) {
+    const int64_t cost = (all * s + sm_count - 1) / sm_count * ((tiles + s - 1) / s + kBlockUnitTiles);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      w->splits = s;
+    }
+  }
+  w->row_tiles = (T * H + kTileRows - 1) / kTileRows;
+  const size_t part = size_t(d->batch) * w->splits * w->row_tiles * kTileRows;
+  w->len_off = kStatusBytes;
+  w->list_off = align_up(w->len_off + all * sizeof(int32_t), 256);
+  w->lse_off = align_up(w->list_off + size_t(all) * w->list_cap * sizeof(BlockEntry), 256);
+  w->o_off = align_up(w->lse_off + part * sizeof(float), 256);
+  w->bytes = align_up(w->o_off + part * kDv * sizeof(float), 256);
   return DDT_OK;
 }
 
@@ -277,6 +318,86 @@ extern "C" int ddtree_block_select(const void* q, const void* summary, const flo
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!clear_status(workspace, s) || launch_quant_rows(k, s) != cudaSuccess ||
       launch_scores(p, kScoreBlock, sms, s) != cudaSuccess || launch_block_topk(t, dims->batch, s) != cudaSuccess)
+    return DDT_ERR_LAUNCH;
+  return DDT_OK;
+}
+
+extern "C" size_t ddtree_verify_blocks_workspace_bytes(const ddt_dims* dims, int32_t block, int32_t topk) {
+  int sms = 0;
+  BlocksLayout w;
+  if (current_device(&sms) != DDT_OK || blocks_layout(dims, block, topk, sms, &w) != DDT_OK) return 0;
+  return w.bytes;
+}
+
+extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, const int32_t* slot_idx,
+                                         const int32_t* prefix_len, const int32_t* tree_parent,
+                                         const int32_t* tree_slot_idx, const int32_t* block_idx, int32_t block,
+                                         int32_t topk, float sm_scale, void* out, float* lse, const ddt_dims* dims,
+                                         void* workspace, size_t workspace_bytes, ddt_stream_t stream) {
+  BlocksLayout w;
+  int rc = blocks_layout(dims, block, topk, 1, &w);  // the sizes, before any device query
+  if (rc != DDT_OK) return rc;
+  if (dims->batch == 0) return DDT_OK;
+  if (!q || !kv_pool || !prefix_len || !tree_parent || !tree_slot_idx || !block_idx || !out || !lse || !workspace ||
+      (!slot_idx && dims->max_prefix_len > 0))
+    return DDT_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(out, 16) || !aligned(workspace, 256) ||
+      !aligned(slot_idx, 4) || !aligned(prefix_len, 4) || !aligned(tree_parent, 4) || !aligned(tree_slot_idx, 4) ||
+      !aligned(block_idx, 4) || !aligned(lse, 4))
+    return DDT_ERR_ALIGN;
+  int sms = 0;
+  if ((rc = current_device(&sms)) != DDT_OK) return rc;
+  if ((rc = blocks_layout(dims, block, topk, sms, &w)) != DDT_OK) return rc;
+  if (workspace_bytes < w.bytes) return DDT_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  BlockAttnParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.kv = static_cast<const uint16_t*>(kv_pool);
+  p.slot_idx = slot_idx;
+  p.prefix_len = prefix_len;
+  p.block_idx = block_idx;
+  p.list = reinterpret_cast<BlockEntry*>(ws + w.list_off);
+  p.list_len = reinterpret_cast<int32_t*>(ws + w.len_off);
+  p.pool_slots = dims->pool_slots;
+  p.list_cap = w.list_cap;
+  p.pstride = int64_t(w.row_tiles) * kTileRows;
+  p.batch = dims->batch;
+  p.nodes = dims->num_nodes;
+  p.heads = dims->num_heads;
+  p.slot_stride = dims->slot_stride;
+  p.max_prefix_len = dims->max_prefix_len;
+  p.block = block;
+  p.topk = topk;
+  p.groups = w.groups;
+  p.group_nodes = w.group_nodes;
+  p.splits = w.splits;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.o_part = reinterpret_cast<float*>(ws + w.o_off);
+  p.lse_part = reinterpret_cast<float*>(ws + w.lse_off);
+  p.status = reinterpret_cast<int32_t*>(ws);
+  TailParams tp = {};
+  tp.q = p.q;
+  tp.kv = p.kv;
+  tp.prefix_len = nullptr;  // every request has exactly `splits` partials: chunks of one
+  tp.max_prefix_len = tp.max_splits = w.splits;
+  tp.chunk0 = tp.chunk = 1;
+  tp.tree_parent = tree_parent;
+  tp.tree_slot_idx = tree_slot_idx;
+  tp.pool_slots = dims->pool_slots;
+  tp.nodes = p.nodes;
+  tp.heads = p.heads;
+  tp.heads_per_cta = p.heads < 8 ? p.heads : 8;
+  tp.row_tiles = w.row_tiles;
+  tp.batch = p.batch;
+  tp.scale_log2 = p.scale_log2;
+  tp.o_part = p.o_part;
+  tp.lse_part = p.lse_part;
+  tp.out_bf16 = static_cast<uint16_t*>(out);
+  tp.lse = lse;
+  tp.status = p.status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!clear_status(workspace, s) || launch_block_union(p, s) != cudaSuccess || launch_block_attn(p, s) != cudaSuccess ||
+      launch_tail_merge(tp, p.batch, s) != cudaSuccess)
     return DDT_ERR_LAUNCH;
   return DDT_OK;
 }

@@ -107,6 +107,39 @@ struct TopkParams {
 cudaError_t configure_topk();
 cudaError_t launch_block_topk(const TopkParams& p, int batch, cudaStream_t stream);
 
+// ---------------------------------------------------------------- block attention
+constexpr int kBlockRows = 64;  // (node, head) rows of one group
+
+struct alignas(16) BlockEntry {
+  unsigned long long mask;  // rows of the group that list the block
+  int32_t block;
+  int32_t pad;
+};
+
+struct BlockAttnParams {
+  const uint16_t* q;          // bf16 [B, T, H, 576]
+  const uint16_t* kv;         // bf16 [N, 576]
+  const int32_t* slot_idx;    // [B, slot_stride]
+  const int32_t* prefix_len;  // [B]
+  const int32_t* block_idx;   // [B, T, topk]
+  BlockEntry* list;           // [B * groups, list_cap]: union of the group's lists, in block order
+  int32_t* list_len;          // [B * groups]
+  int64_t pool_slots;
+  int64_t list_cap;
+  int64_t pstride;            // rows between consecutive splits of one request
+  int32_t batch, nodes, heads, slot_stride, max_prefix_len, block, topk;
+  int32_t groups;             // per request
+  int32_t group_nodes;        // nodes of a group (heads <= 64; else a group is 64 heads of one node)
+  int32_t splits;
+  float scale_log2;
+  float* o_part;              // fp32 [B, splits, pstride, 512], normalised
+  float* lse_part;            // fp32 [B, splits, pstride], natural log
+  int32_t* status;
+};
+cudaError_t configure_block_attn();
+cudaError_t launch_block_union(const BlockAttnParams& p, cudaStream_t stream);
+cudaError_t launch_block_attn(const BlockAttnParams& p, cudaStream_t stream);
+
 // Map of a score to an unsigned key with the same order: NaN lowest (equal to
 // -inf), -0 equal to +0.
 __host__ __device__ inline uint32_t order_key_bits(uint32_t u) {

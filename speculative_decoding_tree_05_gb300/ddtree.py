@@ -33,6 +33,7 @@ EXPORTS = ("ddtree_verify_workspace_bytes", "ddtree_verify_attn", "ddtree_verify
            "ddtree_kv_compact_check", "ddtree_verify_sparse_workspace_bytes", "ddtree_verify_attn_sparse",
            "ddtree_kv_weight_workspace_bytes", "ddtree_kv_weight", "ddtree_kv_evict", "ddtree_block_summary",
            "ddtree_block_select_workspace_bytes", "ddtree_block_select",
+           "ddtree_verify_blocks_workspace_bytes", "ddtree_verify_attn_blocks",
            "ddtree_read_device_status", "ddtree_status_string")
 
 
@@ -102,6 +103,11 @@ def load(path: str):
         L.ddtree_block_select_workspace_bytes.argtypes = [dims, i32]
         L.ddtree_block_select.restype = ctypes.c_int
         L.ddtree_block_select.argtypes = [vp, vp, vp, i32p, i32, i32, i32, i32, i32p, dims, vp, size, vp]
+        L.ddtree_verify_blocks_workspace_bytes.restype = size
+        L.ddtree_verify_blocks_workspace_bytes.argtypes = [dims, i32, i32]
+        L.ddtree_verify_attn_blocks.restype = ctypes.c_int
+        L.ddtree_verify_attn_blocks.argtypes = [vp, vp, i32p, i32p, i32p, i32p, i32p, i32, i32, f32, vp, vp, dims, vp,
+                                                size, vp]
     if hasattr(L, "ddtree_internal_plan"):
         L.ddtree_internal_plan.restype = ctypes.c_int
         L.ddtree_internal_plan.argtypes = [ctypes.POINTER(Dims), ctypes.c_int, ctypes.POINTER(ctypes.c_int32)]
@@ -469,6 +475,54 @@ class BlockSelector:
                                               _stream_of(self.device, stream))
         _check(rc, "ddtree_block_select")
         return out
+
+    def status(self, stream=None) -> int:
+        return read_device_status(self.workspace, stream, library=self.lib)
+
+
+class BlockVerifier:
+    """Verify attention over each node's own blocks (ddtree_verify_attn_blocks), with a workspace for one set of sizes.
+
+    Call with a verify call's tensors and block_idx [B, T, topk] int32 (BlockSelector's, or any list; -1 = none).
+    Returns (out bf16 [B, T, H, 512], lse fp32 [B, T, H]).
+    """
+
+    def __init__(self, batch, nodes, heads, pool_slots, slot_stride, block, topk, max_prefix_len=None, device=None,
+                 library=None):
+        import torch
+        self.lib = lib() if library is None else library
+        self.dims = make_dims(batch, nodes, heads, pool_slots, slot_stride,
+                              slot_stride if max_prefix_len is None else max_prefix_len)
+        self.block, self.topk = int(block), int(topk)
+        self.device = _cuda_device(device)
+        with _On(self.device):
+            n = int(self.lib.ddtree_verify_blocks_workspace_bytes(ctypes.byref(self.dims), self.block, self.topk))
+        if n == 0:
+            raise DDTError(-2, "ddtree_verify_blocks_workspace_bytes")
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def __call__(self, q, kv_pool, slot_idx, prefix_len, tree_parent, tree_slot_idx, block_idx, sm_scale, out=None,
+                 lse=None, stream=None):
+        import torch
+        d = self.dims
+        B, T, H = d.batch, d.num_nodes, d.num_heads
+        if out is None:
+            out = torch.empty((B, T, H, D_V), dtype=torch.bfloat16, device=self.device)
+        if lse is None:
+            lse = torch.empty((B, T, H), dtype=torch.float32, device=self.device)
+        _need(self.device, q=(q, torch.bfloat16, (B, T, H, D_QK)), kv_pool=(kv_pool, torch.bfloat16, (d.pool_slots, D_QK)),
+              slot_idx=(slot_idx, torch.int32, (B, d.slot_stride)), prefix_len=(prefix_len, torch.int32, (B,)),
+              tree_parent=(tree_parent, torch.int32, (B, T)), tree_slot_idx=(tree_slot_idx, torch.int32, (B, T)),
+              block_idx=(block_idx, torch.int32, (B, T, self.topk)), out=(out, torch.bfloat16, (B, T, H, D_V)),
+              lse=(lse, torch.float32, (B, T, H)))
+        with _On(self.device):
+            rc = self.lib.ddtree_verify_attn_blocks(_ptr(q), _ptr(kv_pool), _ptr(slot_idx), _ptr(prefix_len),
+                                                    _ptr(tree_parent), _ptr(tree_slot_idx), _ptr(block_idx),
+                                                    self.block, self.topk, float(sm_scale), _ptr(out), _ptr(lse),
+                                                    ctypes.byref(d), _ptr(self.workspace), self.workspace.numel(),
+                                                    _stream_of(self.device, stream))
+        _check(rc, "ddtree_verify_attn_blocks")
+        return out, lse
 
     def status(self, stream=None) -> int:
         return read_device_status(self.workspace, stream, library=self.lib)
