@@ -111,7 +111,9 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
   const Group u = group_of(p, g);
   int L = __ldg(p.prefix_len + u.b);
   L = L < 0 ? 0 : (L > p.max_prefix_len ? p.max_prefix_len : L);
-  const int count = __ldg(p.list_len + g);
+  grid_dep_launch();  // the tail/merge kernel
+  grid_dep_wait();    // the lists
+  const int count = __ldcg(p.list_len + g);
   const BlockEntry* list = p.list + static_cast<int64_t>(g) * p.list_cap;
   const int64_t keys = static_cast<int64_t>(count) * p.block;
   const int64_t all_tiles = (keys + kBaKeys - 1) / kBaKeys;
@@ -225,7 +227,10 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
       const int64_t i = (static_cast<int64_t>(t0 + t)) * kBaKeys + 16 * pw + lane;
       if (t < n && lane < 16 && i < keys) {
         const int e = static_cast<int>(i / p.block);
-        const BlockEntry be = list[e];
+        const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(list + e));
+        BlockEntry be;
+        be.mask = raw.x | (static_cast<unsigned long long>(raw.y) << 32);
+        be.block = static_cast<int>(raw.z);
         const int64_t x = static_cast<int64_t>(be.block) * p.block + (i - static_cast<int64_t>(e) * p.block);
         if (x < L) {
           *pos = static_cast<int>(x);
@@ -489,6 +494,7 @@ __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const BlockAttn
   __shared__ unsigned long long mask_sh[kUnBlocks];
   __shared__ int cnt[kUnThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_launch();
   const int g = blockIdx.x;
   const Group u = group_of(p, g);
   int L = __ldg(p.prefix_len + u.b);
@@ -555,8 +561,17 @@ cudaError_t launch_block_union(const BlockAttnParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_block_attn(const BlockAttnParams& p, cudaStream_t stream) {
-  block_attn_kernel<<<dim3(p.batch * p.groups, p.splits), kBaThreads, kBaSmem, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(p.batch * p.groups, p.splits);
+  cfg.blockDim = dim3(kBaThreads);
+  cfg.dynamicSmemBytes = kBaSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, block_attn_kernel, p);
 }
 
 }  // namespace ddt

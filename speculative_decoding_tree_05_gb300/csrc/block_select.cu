@@ -18,6 +18,7 @@ constexpr int kQuWarps = 8;
 
 // One warp per query row: 72 pieces of 16 bytes, lanes 0-7 take a third one.
 __global__ void __launch_bounds__(kQuWarps * 32) quant_rows_kernel(QuantParams p) {
+  grid_dep_launch();
   const int lane = threadIdx.x & 31;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kQuWarps + (threadIdx.x >> 5);
   if (r >= p.rows) return;
@@ -55,16 +56,18 @@ __global__ void __launch_bounds__(kQuWarps * 32) quant_rows_kernel(QuantParams p
   if (lane == 0) p.q_scale[r] = scale;
 }
 
-constexpr int kTkThreads = 256;
-constexpr int kTkCached = 16384;  // order keys kept in shared memory
+constexpr int kTkCached = 16384;  // scores kept in shared memory
+constexpr int kTkItems = 4;       // scores per thread and step of the ordered pass
 
 // One CTA per node: the digit select of rank_select.cuh over its scores, then
 // the chosen blocks in ascending order.
-__global__ void __launch_bounds__(kTkThreads) block_topk_kernel(TopkParams p, int cached) {
-  extern __shared__ uint32_t keys_sh[];
-  __shared__ int hist[kBins];
-  __shared__ int tmp[kTkThreads / 32 + 2];
-  __shared__ int cnt_gt[kTkThreads / 32], cnt_eq[kTkThreads / 32];
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int cached) {
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ uint32_t bits_sh[];
+  __shared__ int hist[kDigits][kBins];
+  __shared__ int tmp[2 * kWarps + 4];
+  __shared__ int cnt_gt[kTkItems * kWarps], cnt_eq[kTkItems * kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.x, b = blockIdx.y;
   int L = __ldg(p.prefix_len + b);
@@ -76,78 +79,108 @@ __global__ void __launch_bounds__(kTkThreads) block_topk_kernel(TopkParams p, in
   const float* score = p.score + (static_cast<int64_t>(b) * p.nodes + t) * p.blocks;
   int32_t* out = p.block_idx + (static_cast<int64_t>(b) * p.nodes + t) * p.topk;
   const int keep = min(p.topk, n);
-  for (int i = keep + tid; i < p.topk; i += kTkThreads) out[i] = -1;
+  for (int i = keep + tid; i < p.topk; i += kThreads) out[i] = -1;
   if (keep == n) {
-    for (int i = tid; i < n; i += kTkThreads) out[i] = i;
+    for (int i = tid; i < n; i += kThreads) out[i] = i;
+    grid_dep_wait();
     return;
   }
   const int lo = min(p.first, n), hi = max(lo, n - min(p.last, n));  // [lo, hi): chosen by score
   const int need = keep - (lo + (n - hi));
   if (need <= 0) {  // only forced blocks fit: the lowest ones
-    for (int i = tid; i < keep; i += kTkThreads) out[i] = i < lo ? i : hi + (i - lo);
+    for (int i = tid; i < keep; i += kThreads) out[i] = i < lo ? i : hi + (i - lo);
+    grid_dep_wait();
     return;
   }
+  for (int i = tid; i < kDigits * kBins; i += kThreads) (&hist[0][0])[i] = 0;
+  grid_dep_wait();  // the scores
   const bool in_sh = n <= cached;
-  if (in_sh)
-    for (int i = tid; i < n; i += kTkThreads) keys_sh[i] = order_key(__ldg(score + i));
-  auto key_of = [&](int i) { return in_sh ? keys_sh[i] : order_key(__ldg(score + i)); };
+  if (in_sh) {
+#pragma unroll 4
+    for (int i = tid; i < n; i += kThreads) bits_sh[i] = __float_as_uint(__ldcg(score + i));
+  }
+  __syncthreads();
+  auto key_of = [&](int i) { return order_key_bits(in_sh ? bits_sh[i] : __float_as_uint(__ldcg(score + i))); };
   uint32_t T = 0;
   int want = need;
   for (int pass = 0; pass < kDigits; ++pass) {
-    for (int i = tid; i < kBins; i += kTkThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i0 = 0; i0 < n; i0 += kTkThreads) {
+#pragma unroll 2
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
       const int i = i0 + tid;
       const bool live = i >= lo && i < hi;
-      count_key(hist, live ? key_of(i) : 0u, T, pass, live);
+      count_key(hist[pass], live ? key_of(i) : 0u, T, pass, live);
     }
     __syncthreads();
-    int bin, above;
-    find_bin<kTkThreads>(want, [&](int x) { return hist[x]; }, tmp, &bin, &above);
-    T |= static_cast<uint32_t>(bin) << digit_shift(pass);
-    want -= above;
+    const BinResult r = find_bin<kThreads>(want, [&](int x) { return hist[pass][x]; }, hist[pass], tmp);
+    T |= static_cast<uint32_t>(r.bin) << digit_shift(pass);
+    want -= r.above;
   }
   const int ties = want;
   int gt_base = 0, eq_base = 0;
-  for (int i0 = 0; i0 < n; i0 += kTkThreads) {
-    const int i = i0 + tid;
-    int c = 0;
-    if (i < n) {
-      if (i < lo || i >= hi) {
-        c = 2;
-      } else {
-        const uint32_t k = key_of(i);
-        c = k > T ? 2 : (k == T ? 1 : 0);
+  for (int i0 = 0; i0 < n; i0 += kThreads * kTkItems) {
+    int c[kTkItems];
+#pragma unroll
+    for (int k = 0; k < kTkItems; ++k) {
+      const int i = i0 + k * kThreads + tid;
+      c[k] = 0;
+      if (i < n) {
+        const uint32_t key = key_of(i);
+        c[k] = i < lo || i >= hi || key > T ? 2 : (key == T ? 1 : 0);
       }
-    }
-    const uint32_t mg = __ballot_sync(0xffffffffu, c == 2), me = __ballot_sync(0xffffffffu, c == 1);
-    if (lane == 0) {
-      cnt_gt[warp] = __popc(mg);
-      cnt_eq[warp] = __popc(me);
+      const uint32_t mg = __ballot_sync(0xffffffffu, c[k] == 2), me = __ballot_sync(0xffffffffu, c[k] == 1);
+      if (lane == 0) {
+        cnt_gt[k * kWarps + warp] = __popc(mg);
+        cnt_eq[k * kWarps + warp] = __popc(me);
+      }
     }
     __syncthreads();
-    int g = gt_base, e = eq_base;
+    if (warp < 2) {  // exclusive prefix of the (item, warp) counts
+      int* cnt = warp == 0 ? cnt_gt : cnt_eq;
+      constexpr int kEach = kTkItems * kWarps / 32;
+      int v[kEach], sum = 0;
 #pragma unroll
-    for (int w = 0; w < kTkThreads / 32; ++w) {
-      if (w < warp) {
-        g += cnt_gt[w];
-        e += cnt_eq[w];
+      for (int k = 0; k < kEach; ++k) {
+        v[k] = cnt[lane * kEach + k];
+        sum += v[k];
       }
-      gt_base += cnt_gt[w];
-      eq_base += cnt_eq[w];
+      int incl = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      int run = incl - sum;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        cnt[lane * kEach + k] = run;
+        run += v[k];
+      }
+      if (lane == 31) tmp[warp] = run;
     }
+    __syncthreads();
     const uint32_t lt = (1u << lane) - 1u;
-    g += __popc(mg & lt);
-    e += __popc(me & lt);
-    if (c == 2 || (c == 1 && e < ties)) out[g + min(e, ties)] = i;
+#pragma unroll
+    for (int k = 0; k < kTkItems; ++k) {
+      const uint32_t mg = __ballot_sync(0xffffffffu, c[k] == 2), me = __ballot_sync(0xffffffffu, c[k] == 1);
+      const int g = gt_base + cnt_gt[k * kWarps + warp] + __popc(mg & lt);
+      const int e = eq_base + cnt_eq[k * kWarps + warp] + __popc(me & lt);
+      if (c[k] == 2 || (c[k] == 1 && e < ties)) out[g + min(e, ties)] = i0 + k * kThreads + tid;
+    }
+    gt_base += tmp[0];
+    eq_base += tmp[1];
     __syncthreads();
   }
 }
 
+// Threads per node: 256 up to 1024 blocks (four scores a thread), 1024 beyond.
+constexpr int kTkSmall = 256, kTkLarge = 1024, kTkSmallBlocks = 1024;
+
 }  // namespace
 
 cudaError_t configure_topk() {
-  return cudaFuncSetAttribute(block_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTkCached * 4);
+  cudaError_t e = cudaFuncSetAttribute(block_topk_kernel<kTkSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTkCached * 4);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(block_topk_kernel<kTkLarge>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTkCached * 4);
 }
 
 cudaError_t launch_quant_rows(const QuantParams& p, cudaStream_t stream) {
@@ -160,8 +193,19 @@ cudaError_t launch_quant_rows(const QuantParams& p, cudaStream_t stream) {
 cudaError_t launch_block_topk(const TopkParams& p, int batch, cudaStream_t stream) {
   if (batch == 0) return cudaSuccess;
   const int cached = p.blocks <= kTkCached ? p.blocks : kTkCached;
-  block_topk_kernel<<<dim3(p.nodes, batch), kTkThreads, cached * 4, stream>>>(p, cached);
-  return cudaGetLastError();
+  // programmatic dependent of the scores: its set-up overlaps their end
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(p.nodes, batch);
+  cfg.dynamicSmemBytes = cached * 4;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(p.blocks <= kTkSmallBlocks ? kTkSmall : kTkLarge);
+  return p.blocks <= kTkSmallBlocks ? cudaLaunchKernelEx(&cfg, block_topk_kernel<kTkSmall>, p, cached)
+                                    : cudaLaunchKernelEx(&cfg, block_topk_kernel<kTkLarge>, p, cached);
 }
 
 }  // namespace ddt

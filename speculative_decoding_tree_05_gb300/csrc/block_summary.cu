@@ -14,26 +14,28 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include "cache_ops.cuh"
+#include "ptx.cuh"
 
 namespace ddt {
 namespace {
 
 constexpr int kSumGroups = 4;
 constexpr int kSumThreads = kSumGroups * kChunks;  // 288
-constexpr int kSumBatch = 4;                       // rows in flight per thread
+constexpr int kSumBatch = 8;                       // rows in flight per thread
 constexpr int kMaxBlock = 128;
 
-// (hi, lo) + x without losing the rounding error of hi + x
-__device__ __forceinline__ void two_sum(float& hi, float& lo, float x) {
-  const float s = __fadd_rn(hi, x);
-  const float v = __fsub_rn(s, hi);
-  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, v)), __fsub_rn(x, v)));
+// (hi, lo) + x without losing the rounding error of hi + x, two dims at a time
+// (the additions are half of the kernel's instructions: paired ones halve them)
+__device__ __forceinline__ void two_sum(uint64_t& hi, uint64_t& lo, uint64_t x) {
+  const uint64_t s = add_x2(hi, x);
+  const uint64_t v = sub_x2(s, hi);
+  lo = add_x2(lo, add_x2(sub_x2(hi, sub_x2(s, v)), sub_x2(x, v)));
   hi = s;
 }
 
 __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(SummaryParams p) {
   __shared__ int slot_sh[kMaxBlock];
-  __shared__ float part[kSumGroups - 1][2][kDqk];
+  __shared__ __align__(16) float part[kSumGroups - 1][2][kDqk];
   __shared__ float amax_sh[3];
   __shared__ int bad_sh[2];
   const int tid = threadIdx.x, g = tid / kChunks, c = tid - g * kChunks;
@@ -60,9 +62,9 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(SummaryParam
       slot_sh[tid] = s;
     }
     __syncthreads();
-    float hi[8], lo[8];
+    uint64_t hi2[4], lo2[4];
 #pragma unroll
-    for (int d = 0; d < 8; ++d) hi[d] = lo[d] = 0.f;
+    for (int d = 0; d < 4; ++d) hi2[d] = lo2[d] = 0;
     for (int r0 = g; r0 < n; r0 += kSumGroups * kSumBatch) {
       uint4 v[kSumBatch];
 #pragma unroll
@@ -76,17 +78,15 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(SummaryParam
       for (int u = 0; u < kSumBatch; ++u) {
         const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          two_sum(hi[2 * d], lo[2 * d], __uint_as_float(w[d] << 16));
-          two_sum(hi[2 * d + 1], lo[2 * d + 1], __uint_as_float(w[d] & 0xffff0000u));
-        }
+        for (int d = 0; d < 4; ++d)
+          two_sum(hi2[d], lo2[d], f32x2(__uint_as_float(w[d] << 16), __uint_as_float(w[d] & 0xffff0000u)));
       }
     }
     if (g > 0) {
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        part[g - 1][0][8 * c + d] = hi[d];
-        part[g - 1][1][8 * c + d] = lo[d];
+      for (int d = 0; d < 4; ++d) {
+        reinterpret_cast<uint64_t*>(part[g - 1][0])[4 * c + d] = hi2[d];
+        reinterpret_cast<uint64_t*>(part[g - 1][1])[4 * c + d] = lo2[d];
       }
     }
     __syncthreads();
@@ -95,13 +95,19 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(SummaryParam
     float mean[8], am = 0.f;
     bool finite = true;
     if (g == 0) {
+      float hi[8], lo[8];
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
+      for (int d = 0; d < 4; ++d) {
 #pragma unroll
         for (int o = 0; o < kSumGroups - 1; ++o) {
-          two_sum(hi[d], lo[d], part[o][0][8 * c + d]);
-          lo[d] += part[o][1][8 * c + d];
+          two_sum(hi2[d], lo2[d], reinterpret_cast<const uint64_t*>(part[o][0])[4 * c + d]);
+          lo2[d] = add_x2(lo2[d], reinterpret_cast<const uint64_t*>(part[o][1])[4 * c + d]);
         }
+        f32x2_split(hi2[d], hi[2 * d], hi[2 * d + 1]);
+        f32x2_split(lo2[d], lo[2 * d], lo[2 * d + 1]);
+      }
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
         mean[d] = count > 0 ? static_cast<float>((static_cast<double>(hi[d]) + lo[d]) / count) : 0.f;
         // an infinite row leaves a NaN in the carried error: any non-finite sum counts as such
         finite = finite && fabsf(mean[d]) < CUDART_INF_F;

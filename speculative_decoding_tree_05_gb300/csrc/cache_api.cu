@@ -173,7 +173,7 @@ extern "C" int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_
     k.status = p.status;
     if (launch_pack_nodes(k, dims->batch, s) != cudaSuccess) return DDT_ERR_LAUNCH;
   }
-  return launch_scores(p, kScoreWeight, sms, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
+  return launch_scores(p, kScoreWeight, sms, packed, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
 }
 
 extern "C" int ddtree_kv_evict(const float* weight, const int32_t* slot_idx, const int32_t* prefix_len,
@@ -317,7 +317,7 @@ extern "C" int ddtree_block_select(const void* q, const void* summary, const flo
   t.status = p.status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!clear_status(workspace, s) || launch_quant_rows(k, s) != cudaSuccess ||
-      launch_scores(p, kScoreBlock, sms, s) != cudaSuccess || launch_block_topk(t, dims->batch, s) != cudaSuccess)
+      launch_scores(p, kScoreBlock, sms, true, s) != cudaSuccess || launch_block_topk(t, dims->batch, s) != cudaSuccess)
     return DDT_ERR_LAUNCH;
   return DDT_OK;
 }

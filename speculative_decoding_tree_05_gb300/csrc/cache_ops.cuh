@@ -45,7 +45,9 @@ struct ScoreParams {
 };
 
 cudaError_t configure_scores();
-cudaError_t launch_scores(const ScoreParams& p, ScoreMode mode, int sm_count, cudaStream_t stream);
+// after_kernel: the query rows and row_aux are written by the kernel launched just
+// before, which this one follows as a programmatic dependent
+cudaError_t launch_scores(const ScoreParams& p, ScoreMode mode, int sm_count, bool after_kernel, cudaStream_t stream);
 
 // Selected nodes' query rows and lse, packed (node_idx[b][s], -1 = none).
 struct PackParams {

@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort = &sh.abort;
+  grid_dep_launch();
 
   if (tid == 0) {
     for (int i = 0; i < kScGroups; ++i) {
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      grid_dep_wait();  // the query rows may come from the kernel before (packed, 8-bit)
       uint32_t n_stage = 0;
       for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const int b = u / p.key_tiles, kt = u - b * p.key_tiles;
@@ -219,12 +221,14 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     float* aux = reinterpret_cast<float*>(smem + kScOffAux) + set * kScMaxN;
     float* comb = reinterpret_cast<float*>(smem + kScOffComb);
     uint32_t n_unit = 0, n_tile = 0;
+    grid_dep_wait();  // row_aux, as the query rows
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
       const int b = u / p.key_tiles, kt = u - b * p.key_tiles;
       const int n = key_count(p, b);
       if (kt * kScKeys >= n) continue;
       const int j = kt * kScKeys + r;
       float acc = kMode == kScoreWeight ? 0.f : -CUDART_INF_F;
+      const float key_scale = kMode == kScoreBlock && j < n ? __ldg(p.key_scale + static_cast<int64_t>(b) * p.key_stride + j) : 0.f;
       int node = 0, left = p.heads;  // kScoreBlock: the node that the next row belongs to, its rows left
       for (int qt = 0; ok && qt < p.tiles; ++qt, ++n_tile) {
         if ((two_sets ? static_cast<int>(n_tile & 1) : 0) != set) continue;
@@ -278,18 +282,33 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
             acc += (t[0] + t[1]) + (t[2] + t[3]);
           } else {
             const int nc = min(32, live - c);
+            // both products are rounded to 32 bits: part of the definition of the score; fmaxf drops a NaN scale
+            auto emit = [&] {
+              if (j < n)
+                p.score[(static_cast<int64_t>(b) * p.nodes + node) * p.key_stride + j] = __fmul_rn(acc, key_scale);
+              acc = -CUDART_INF_F;
+              left = p.heads;
+              ++node;
+            };
+            if (p.heads % 8 == 0) {  // nodes (and so the live rows) end on multiples of 8
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if (k < nc) {
-                // both products rounded to 32 bits: part of the definition of the score; fmaxf drops a NaN scale
-                acc = fmaxf(acc, __fmul_rn(s[k], aux[c + k]));
-                if (--left == 0) {
-                  if (j < n)
-                    p.score[(static_cast<int64_t>(b) * p.nodes + node) * p.key_stride + j] =
-                        __fmul_rn(acc, __ldg(p.key_scale + static_cast<int64_t>(b) * p.key_stride + j));
-                  acc = -CUDART_INF_F;
-                  left = p.heads;
-                  ++node;
+              for (int k = 0; k < 32; k += 8) {
+                if (k < nc) {
+                  const float4 a = *reinterpret_cast<const float4*>(aux + c + k);
+                  const float4 d = *reinterpret_cast<const float4*>(aux + c + k + 4);
+                  const float m0 = fmax3(__fmul_rn(s[k], a.x), __fmul_rn(s[k + 1], a.y), __fmul_rn(s[k + 2], a.z));
+                  const float m1 = fmax3(__fmul_rn(s[k + 3], a.w), __fmul_rn(s[k + 4], d.x), __fmul_rn(s[k + 5], d.y));
+                  const float m2 = fmax3(__fmul_rn(s[k + 6], d.z), __fmul_rn(s[k + 7], d.w), acc);
+                  acc = fmax3(m0, m1, m2);
+                  if ((left -= 8) == 0) emit();
+                }
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                if (k < nc) {
+                  acc = fmaxf(acc, __fmul_rn(s[k], aux[c + k]));
+                  if (--left == 0) emit();
                 }
               }
             }
@@ -334,6 +353,7 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
 
 // One CTA copies one selected node's rows (H x 72 pieces of 16 bytes) and lse.
 __global__ void __launch_bounds__(256) pack_nodes_kernel(PackParams p) {
+  grid_dep_launch();
   const int s = blockIdx.x, b = blockIdx.y;
   const int t = __ldg(p.node_idx + static_cast<int64_t>(b) * p.sel + s);
   const bool in = t >= 0 && t < p.nodes;
@@ -354,15 +374,22 @@ cudaError_t configure_scores() {
   return cudaFuncSetAttribute(score_kernel<kScoreBlock>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScSmem);
 }
 
-cudaError_t launch_scores(const ScoreParams& p, ScoreMode mode, int sm_count, cudaStream_t stream) {
+cudaError_t launch_scores(const ScoreParams& p, ScoreMode mode, int sm_count, bool after_kernel, cudaStream_t stream) {
   const int64_t units = int64_t(p.batch) * p.key_tiles;
   if (units == 0) return cudaSuccess;
   const int grid = static_cast<int>(units < sm_count ? units : sm_count);
-  if (mode == kScoreWeight)
-    score_kernel<kScoreWeight><<<grid, kScThreads, kScSmem, stream>>>(p);
-  else
-    score_kernel<kScoreBlock><<<grid, kScThreads, kScSmem, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kScThreads);
+  cfg.dynamicSmemBytes = kScSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = after_kernel ? 1 : 0;
+  return mode == kScoreWeight ? cudaLaunchKernelEx(&cfg, score_kernel<kScoreWeight>, p)
+                              : cudaLaunchKernelEx(&cfg, score_kernel<kScoreBlock>, p);
 }
 
 cudaError_t launch_pack_nodes(const PackParams& p, int batch, cudaStream_t stream) {

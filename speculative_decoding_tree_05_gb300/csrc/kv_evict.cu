@@ -7,12 +7,13 @@
 //   1. three digit histograms of the unprotected positions' weights, summed over
 //      the cluster through distributed shared memory, give the weight of the last
 //      position kept (T) and how many of the positions tied at T are kept;
-//   2. every CTA counts its positions above and at T; the cluster's prefix sums
-//      say where its kept and freed entries start;
+//   2. the histograms also say how many of a CTA's own positions lie above and at
+//      T; prefix sums over the cluster say where its kept and freed entries start;
 //   3. a pass in position order writes both lists (ballots and one scan a tile).
-// The weights are read from memory once: their order keys stay in shared memory
-// where they fit.  The work is a few bytes per position, so the time is the
-// latency of these dependent steps, not bandwidth, until the batch fills the GPU.
+// The weights are read from memory once and stay in shared memory where they
+// fit.  The work is a few bytes per position, so the time is the latency of
+// these dependent steps, not bandwidth, until the batch fills the GPU: small
+// batches take clusters of 16.
 #include <cuda_runtime.h>
 #include "cache_ops.cuh"
 #include "ptx.cuh"
@@ -22,20 +23,19 @@ namespace ddt {
 namespace {
 
 constexpr int kEvThreads = 1024;
-constexpr int kEvCluster = 8;
-constexpr int kEvItems = 4;                       // positions per thread and tile of the ordered pass
+constexpr int kEvMaxCluster = 16;
+constexpr int kEvItems = 8;                       // positions per thread and tile of the ordered pass
 constexpr int kEvTile = kEvThreads * kEvItems;
-constexpr int kEvMaxCached = 40960;               // order keys a CTA keeps in shared memory
+constexpr int kEvMaxCached = 40960;               // weights a CTA keeps in shared memory
 
-__global__ void __launch_bounds__(kEvThreads) __cluster_dims__(kEvCluster, 1, 1)
-    kv_evict_kernel(EvictParams p, int cached) {
-  extern __shared__ uint32_t keys_sh[];           // [cached] order keys of this CTA's share
+__global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int cached) {
+  extern __shared__ uint32_t bits_sh[];           // [cached] the weights of this CTA's share
   __shared__ int hist[kDigits][kBins];
-  __shared__ int tmp[kEvThreads / 32 + 2];
+  __shared__ int tmp[2 * kEvThreads / 32 + 4];
   __shared__ int tile_gt[kEvItems * 32], tile_eq[kEvItems * 32];
-  __shared__ int own[2];                          // this CTA's positions above T, at T
+  __shared__ int own[2];                          // this CTA's positions kept for sure, at T
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = static_cast<int>(cluster_ctarank());
+  const int rank = static_cast<int>(cluster_ctarank()), ctas = gridDim.x;  // one cluster spans x
   const int b = blockIdx.y;
   int L = __ldg(p.prefix_len + b);
   if (L < 0 || L > p.max_prefix_len) {
@@ -49,125 +49,128 @@ __global__ void __launch_bounds__(kEvThreads) __cluster_dims__(kEvCluster, 1, 1)
   const int64_t row = static_cast<int64_t>(b) * p.stride;
   const float* weight = p.weight + row;
   // this CTA's share of the positions, in order
-  const int share = (L + kEvCluster - 1) / kEvCluster;
+  const int share = (L + ctas - 1) / ctas;
   const int begin = min(L, rank * share), end = min(L, begin + share);
 
   for (int i = tid; i < kDigits * kBins; i += kEvThreads) (&hist[0][0])[i] = 0;
+  if (cached > 0) {
+#pragma unroll 8
+    for (int i = begin + tid; i < end; i += kEvThreads) bits_sh[i - begin] = __float_as_uint(__ldg(weight + i));
+  }
   __syncthreads();
-  auto key_of = [&](int i) { return cached > 0 ? keys_sh[i - begin] : order_key(__ldg(weight + i)); };
+  auto bits_of = [&](int i) { return cached > 0 ? bits_sh[i - begin] : __float_as_uint(__ldg(weight + i)); };
 
   uint32_t T = 0;   // order key of the last unprotected position kept
   int ties = 0;     // positions at T that are kept
+  int gt = 0, eq = 0;
   const bool select = need > 0 && keep < L;       // the same in every CTA of the cluster
-  if (cached > 0 && select) {
-    for (int i = begin + tid; i < end; i += kEvThreads) keys_sh[i - begin] = order_key(__ldg(weight + i));
-    __syncthreads();
-  }
   if (select) {
     int want = need;
     for (int pass = 0; pass < kDigits; ++pass) {
+#pragma unroll 4
       for (int i0 = begin; i0 < end; i0 += kEvThreads) {
         const int i = i0 + tid;
         const bool live = i < end && i >= lo && i < hi;
-        count_key(hist[pass], live ? key_of(i) : 0u, T, pass, live);
+        count_key(hist[pass], live ? order_key_bits(bits_of(i)) : 0u, T, pass, live);
       }
       cluster_sync();  // every CTA's histogram of this pass is complete
-      int bin, above;
-      find_bin<kEvThreads>(want, [&](int x) {
+      const BinResult r = find_bin<kEvThreads>(want, [&](int x) {
         int n = 0;
         const uint32_t a = smem_u32(&hist[pass][x]);
-#pragma unroll
-        for (int r = 0; r < kEvCluster; ++r) n += ld_shared_cluster_b32(mapa_shared(a, r));
+        for (int c = 0; c < ctas; ++c) n += ld_shared_cluster_b32(mapa_shared(a, c));
         return n;
-      }, tmp, &bin, &above);
-      T |= static_cast<uint32_t>(bin) << digit_shift(pass);
-      want -= above;
+      }, hist[pass], tmp);
+      T |= static_cast<uint32_t>(r.bin) << digit_shift(pass);
+      want -= r.above;
+      gt += r.own_above;
+      eq = r.own_in;
     }
     ties = want;
   }
-
-  // kept: protected positions (class 2), above T (class 1), at T (class 0)
-  auto klass = [&](int i) -> int {                // 2: kept, 1: tied at T, 0: freed
-    if (keep == L) return 2;
-    if (i < lo || i >= hi) {
-      if (need >= 0) return 2;
-      const int q = i < lo ? i : lo + (i - hi);   // rank among the protected positions
-      return q < keep ? 2 : 0;
-    }
-    if (!select) return 0;
-    const uint32_t k = key_of(i);
+  // protected positions that stay: all of them, or the lowest `keep`
+  const int held = min(prot, keep), held_lo = min(lo, held), held_hi = hi + (held - held_lo);
+  auto within = [&](int x0, int x1) { return max(0, min(end, x1) - max(begin, x0)); };
+  gt += within(0, held_lo) + within(hi, held_hi);
+  if (keep == L) gt = end - begin;
+  // 2: kept, 1: tied at T, 0: freed
+  auto klass = [&](int i, uint32_t bits) -> int {
+    if (keep == L || i < held_lo || (i >= hi && i < held_hi)) return 2;
+    if (!select || i < lo || i >= hi) return 0;
+    const uint32_t k = order_key_bits(bits);
     return k > T ? 2 : (k == T ? 1 : 0);
   };
 
-  int gt = 0, eq = 0;
-  for (int i = begin + tid; i < end; i += kEvThreads) {
-    const int c = klass(i);
-    gt += c == 2;
-    eq += c == 1;
-  }
-  gt = __reduce_add_sync(0xffffffffu, gt);
-  eq = __reduce_add_sync(0xffffffffu, eq);
-  if (tid == 0) own[0] = own[1] = 0;
-  __syncthreads();
-  if (lane == 0) {
-    atomicAdd(&own[0], gt);
-    atomicAdd(&own[1], eq);
+  if (tid == 0) {
+    own[0] = gt;
+    own[1] = eq;
   }
   cluster_sync();
   int gt_base = 0, eq_base = 0;
-  for (int r = 0; r < rank; ++r) {
-    gt_base += ld_shared_cluster_b32(mapa_shared(smem_u32(&own[0]), r));
-    eq_base += ld_shared_cluster_b32(mapa_shared(smem_u32(&own[1]), r));
+  {
+    const int g = lane < rank ? ld_shared_cluster_b32(mapa_shared(smem_u32(&own[0]), lane)) : 0;
+    const int e = lane < rank ? ld_shared_cluster_b32(mapa_shared(smem_u32(&own[1]), lane)) : 0;
+    gt_base = __reduce_add_sync(0xffffffffu, g);
+    eq_base = __reduce_add_sync(0xffffffffu, e);
   }
   cluster_arrive();  // this thread no longer reads a peer's shared memory
 
   for (int t0 = begin; t0 < end; t0 += kEvTile) {
-    int c[kEvItems];
-    uint32_t mgt[kEvItems], meq[kEvItems];
+    int c[kEvItems], slot[kEvItems];
+    uint32_t w[kEvItems];
 #pragma unroll
     for (int k = 0; k < kEvItems; ++k) {
       const int i = t0 + k * kEvThreads + tid;
-      c[k] = i < end ? klass(i) : -1;
-      mgt[k] = __ballot_sync(0xffffffffu, c[k] == 2);
-      meq[k] = __ballot_sync(0xffffffffu, c[k] == 1);
+      slot[k] = i < end ? __ldg(p.slot_idx + row + i) : 0;
+      w[k] = i < end ? bits_of(i) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kEvItems; ++k) {
+      const int i = t0 + k * kEvThreads + tid;
+      c[k] = i < end ? klass(i, w[k]) : -1;
+      const uint32_t mg = __ballot_sync(0xffffffffu, c[k] == 2), me = __ballot_sync(0xffffffffu, c[k] == 1);
       if (lane == 0) {
-        tile_gt[k * 32 + warp] = __popc(mgt[k]);
-        tile_eq[k * 32 + warp] = __popc(meq[k]);
+        tile_gt[k * 32 + warp] = __popc(mg);
+        tile_eq[k * 32 + warp] = __popc(me);
       }
     }
     __syncthreads();
     if (warp < 2) {  // exclusive prefix of the (item, warp) counts, in position order
       int* t = warp == 0 ? tile_gt : tile_eq;
-      int run = 0;
+      int v[kEvItems], sum = 0;  // lane l scans entries [8 l, 8 l + 8)
 #pragma unroll
       for (int k = 0; k < kEvItems; ++k) {
-        const int v = t[k * 32 + lane];
-        int incl = v;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int o = __shfl_up_sync(0xffffffffu, incl, off);
-          if (lane >= off) incl += o;
-        }
-        t[k * 32 + lane] = run + incl - v;
-        run += __shfl_sync(0xffffffffu, incl, 31);
+        v[k] = t[lane * kEvItems + k];
+        sum += v[k];
       }
-      if (lane == 0) tmp[warp] = run;
+      int incl = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      int run = incl - sum;
+#pragma unroll
+      for (int k = 0; k < kEvItems; ++k) {
+        t[lane * kEvItems + k] = run;
+        run += v[k];
+      }
+      if (lane == 31) tmp[warp] = run;
     }
     __syncthreads();
     const uint32_t lt = (1u << lane) - 1u;
 #pragma unroll
     for (int k = 0; k < kEvItems; ++k) {
       const int i = t0 + k * kEvThreads + tid;
+      const uint32_t mg = __ballot_sync(0xffffffffu, c[k] == 2), me = __ballot_sync(0xffffffffu, c[k] == 1);
       if (i < end) {
-        const int g = gt_base + tile_gt[k * 32 + warp] + __popc(mgt[k] & lt);
-        const int e = eq_base + tile_eq[k * 32 + warp] + __popc(meq[k] & lt);
+        const int g = gt_base + tile_gt[k * 32 + warp] + __popc(mg & lt);
+        const int e = eq_base + tile_eq[k * 32 + warp] + __popc(me & lt);
         const int kept_before = g + min(e, ties);
-        const int slot = __ldg(p.slot_idx + row + i);
         if (c[k] == 2 || (c[k] == 1 && e < ties)) {
-          p.slot_out[row + kept_before] = slot;
-          p.weight_out[row + kept_before] = __ldg(weight + i);
+          p.slot_out[row + kept_before] = slot[k];
+          p.weight_out[row + kept_before] = __uint_as_float(w[k]);
         } else {
-          p.freed[row + i - kept_before] = slot;
+          p.freed[row + i - kept_before] = slot[k];
         }
       }
     }
@@ -182,14 +185,29 @@ __global__ void __launch_bounds__(kEvThreads) __cluster_dims__(kEvCluster, 1, 1)
 }  // namespace
 
 cudaError_t configure_evict() {
-  return cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvMaxCached * 4);
+  cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvMaxCached * 4);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 cudaError_t launch_kv_evict(const EvictParams& p, int batch, cudaStream_t stream) {
-  const int64_t share = (int64_t(p.max_prefix_len) + kEvCluster - 1) / kEvCluster;
+  // 16 CTAs a request while the clusters of the batch fit the GPU side by side
+  // (at most 8 of 16 CTAs: clusters stay within a GPC), 8 beyond that
+  const int ctas = batch <= 8 ? kEvMaxCluster : 8;
+  const int64_t share = (int64_t(p.max_prefix_len) + ctas - 1) / ctas;
   const int cached = share <= kEvMaxCached ? static_cast<int>(share) : 0;
-  kv_evict_kernel<<<dim3(kEvCluster, batch), kEvThreads, cached * 4, stream>>>(p, cached);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(ctas, batch);
+  cfg.blockDim = dim3(kEvThreads);
+  cfg.dynamicSmemBytes = cached * 4;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_evict_kernel, p, cached);
 }
 
 }  // namespace ddt

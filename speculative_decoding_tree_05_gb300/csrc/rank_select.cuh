@@ -18,53 +18,82 @@ __host__ __device__ constexpr uint32_t above_mask(int pass) {
   return pass == 0 ? 0u : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
 }
 
-__device__ __forceinline__ uint32_t order_key(float w) { return order_key_bits(__float_as_uint(w)); }
-
-// Counts `key` in hist if it matches `prefix` above the pass's digit.  Lanes
-// that count the same bin are added up first: weights crowd into few bins.
+// Counts `key` in hist if it matches `prefix` above the pass's digit; a whole
+// warp calls it.  The lanes that share the first counted lane's bin are added in
+// one atomic: equal weights (zeros, ties) would otherwise serialise on one bin.
 __device__ __forceinline__ void count_key(int* hist, uint32_t key, uint32_t prefix, int pass, bool live) {
   const bool in = live && (key & above_mask(pass)) == prefix;
-  const uint32_t bin = in ? (key >> digit_shift(pass)) & digit_mask(pass) : 0xffffffffu;
-  const uint32_t same = __match_any_sync(0xffffffffu, bin);
-  if (in && (threadIdx.x & 31) == static_cast<unsigned>(__ffs(same) - 1)) atomicAdd(&hist[bin], __popc(same));
+  const uint32_t vote = __ballot_sync(0xffffffffu, in);
+  if (vote == 0) return;
+  const uint32_t bin = (key >> digit_shift(pass)) & digit_mask(pass);
+  const int lead = __ffs(vote) - 1;
+  const uint32_t lead_bin = __shfl_sync(0xffffffffu, bin, lead);
+  const uint32_t same = __ballot_sync(0xffffffffu, in && bin == lead_bin);
+  const int lane = threadIdx.x & 31;
+  if (lane == lead)
+    atomicAdd(&hist[bin], __popc(same));
+  else if (in && !((same >> lane) & 1u))
+    atomicAdd(&hist[bin], 1);
 }
 
-// The bin of the want-th largest key (want >= 1), bins counted from the top:
-// returns the bin and the keys in higher bins.  count(bin) gives a bin's
-// total; every thread of the block (kThreads of them, a multiple of 32 that
-// divides kBins) calls this.  tmp: kThreads / 32 + 2 ints of shared memory.
-template <int kThreads, class CountFn>
-__device__ __forceinline__ void find_bin(int want, CountFn count, int* tmp, int* bin, int* above) {
-  constexpr int kPer = kBins / kThreads;
+struct BinResult {
+  int bin;        // the bin of the want-th largest key, bins counted from the top
+  int above;      // keys in higher bins
+  int own_above;  // of this block's own histogram: keys in higher bins, and in the bin
+  int own_in;
+};
+
+// find_bin for a histogram spread over several blocks: total(bin) gives a bin's
+// sum over all of them, own[] is this block's share.  Every thread of the block
+// (kThreads, a multiple of 32 that divides kBins) calls it.  tmp: 2 *
+// kThreads / 32 + 4 ints of shared memory.
+template <int kThreads, class TotalFn>
+__device__ __forceinline__ BinResult find_bin(int want, TotalFn total, const int* own, int* tmp) {
+  constexpr int kPer = kBins / kThreads, kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int c[kPer], sum = 0;
+  const int top = kBins - 1 - kPer * tid;  // thread t holds bins top, top - 1, ...
+  int c[kPer], o[kPer], sum = 0, osum = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {  // thread t holds bins kBins - 1 - kPer t downwards
-    c[i] = count(kBins - 1 - kPer * tid - i);
+  for (int i = 0; i < kPer; ++i) {
+    c[i] = total(top - i);
+    o[i] = own[top - i];
     sum += c[i];
+    osum += o[i];
   }
-  int incl = sum;
+  int incl = sum, oincl = osum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += v;
+    const int v = __shfl_up_sync(0xffffffffu, incl, off), ov = __shfl_up_sync(0xffffffffu, oincl, off);
+    if (lane >= off) {
+      incl += v;
+      oincl += ov;
+    }
   }
-  if (lane == 31) tmp[warp] = incl;
+  if (lane == 31) {
+    tmp[warp] = incl;
+    tmp[kWarps + warp] = oincl;
+  }
   __syncthreads();
-  int before = incl - sum;
-  for (int w = 0; w < warp; ++w) before += tmp[w];
+  // every warp sums the warps before it
+  int w = lane < kWarps && lane < warp ? tmp[lane] : 0, ow = lane < kWarps && lane < warp ? tmp[kWarps + lane] : 0;
+  int before = incl - sum + __reduce_add_sync(0xffffffffu, w);
+  int obefore = oincl - osum + __reduce_add_sync(0xffffffffu, ow);
+  int* res = tmp + 2 * kWarps;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (before < want && want <= before + c[i]) {
-      tmp[kThreads / 32] = kBins - 1 - kPer * tid - i;
-      tmp[kThreads / 32 + 1] = before;
+      res[0] = top - i;
+      res[1] = before;
+      res[2] = obefore;
+      res[3] = o[i];
     }
     before += c[i];
+    obefore += o[i];
   }
   __syncthreads();
-  *bin = tmp[kThreads / 32];
-  *above = tmp[kThreads / 32 + 1];
+  BinResult r{res[0], res[1], res[2], res[3]};
   __syncthreads();
+  return r;
 }
 
 }  // namespace ddt
