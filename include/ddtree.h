@@ -326,9 +326,10 @@ DDT_API int ddtree_verify_attn_static_scratch(const void* q, const void* kv_pool
  *   weight_out fp32 [B, slot_stride]; entries from prefix_len[b] on are not written
  * A key whose slot is outside the pool gains nothing and sets
  * DDT_STATUS_BAD_SLOT.  Sums are in fp32 in a fixed order: the same bits on
- * every run.  workspace >= ddtree_kv_weight_workspace_bytes(dims, num_sel).
- * prefix_len_sum is not used.  B * T * H and B * ceil(max_prefix_len / 128) fit
- * in 31 bits (else DDT_ERR_DIMS).
+ * every run.  workspace >= ddtree_kv_weight_workspace_bytes(dims, num_sel),
+ * which needs a current CUDA device.  prefix_len_sum is not used.  The query
+ * rows of the batch fit in 31 bits, B * ceil(max_prefix_len / 256) in 25 (else
+ * DDT_ERR_DIMS).
  */
 DDT_API size_t ddtree_kv_weight_workspace_bytes(const ddt_dims* dims, int32_t num_sel);
 DDT_API int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_t* slot_idx, const int32_t* prefix_len,
@@ -389,7 +390,7 @@ DDT_API int ddtree_block_summary(const void* kv_pool, const int32_t* slot_idx, c
  * finite is left out).
  *   block_idx  int32 [B, T, topk]: the chosen blocks in ascending order, then -1
  * topk <= 2^20.  dims gives batch, num_nodes, num_heads, slot_stride and
- * max_prefix_len; B * T * H and B * N fit in 31 bits.
+ * max_prefix_len; B * T * H and B * N fit in 31 bits, B * ceil(N / 256) in 25.
  * workspace >= ddtree_block_select_workspace_bytes(dims, block).
  */
 DDT_API size_t ddtree_block_select_workspace_bytes(const ddt_dims* dims, int32_t block);

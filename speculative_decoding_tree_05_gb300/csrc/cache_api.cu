@@ -12,35 +12,65 @@
 namespace ddt {
 namespace {
 
-constexpr int kScoreTileKeys = 128;
-constexpr int kScoreMaxRows = 256;  // query rows of one tile
+constexpr int kScoreUnitTiles = 4;  // fixed cost of one score unit, in query tiles
 constexpr int kBlockUnitTiles = 4;  // fixed cost of one block-attention unit, in 64-key tiles
 
-int round16(int x) { return (x + 15) / 16 * 16; }
+int round32(int x) { return (x + 31) / 32 * 32; }
 
 bool clear_status(void* workspace, cudaStream_t s) {
   return cudaMemsetAsync(workspace, 0, 4 * sizeof(int32_t), s) == cudaSuccess;
 }
 
-// Tiles of query rows and keys; false if the sizes do not fit the kernels' 32-bit counters.
-bool score_tiles(ScoreParams* p, int64_t keys, int64_t q_rows) {
+// Key tiles, and the shares of the query tiles: with fewer key tiles than CTA
+// pairs the pairs left over take shares of the rows.  A unit costs its tiles plus
+// about kScoreUnitTiles (the gather of its keys and the pipeline's fill).
+struct ScoreGrid {
+  int key_tiles, splits, units;
+};
+bool score_grid(int64_t batch, int64_t keys, int tiles, int sm_count, ScoreGrid* g) {
   const int64_t key_tiles = (keys + kScoreTileKeys - 1) / kScoreTileKeys;
-  if (q_rows > INT32_MAX || key_tiles * p->batch > INT32_MAX) return false;
-  p->key_tiles = static_cast<int32_t>(key_tiles);
+  const int64_t all = batch * key_tiles, pairs = std::max(1, sm_count / 2);
+  if (all > INT32_MAX / 64) return false;
+  int64_t best = -1;
+  int splits = 1;
+  for (int s = 1; s <= std::min(tiles, 64); ++s) {
+    const int64_t cost = (all * s + pairs - 1) / pairs * ((tiles + s - 1) / s + kScoreUnitTiles);
+    if (best < 0 || cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
+  *g = {static_cast<int>(key_tiles), splits, static_cast<int>(all * splits)};
   return true;
 }
 
+// Query rows per tile of the weights: equal tiles of at most kScoreTileRows.
+int weight_tile_rows(int rows) {
+  const int tiles = (rows + kScoreTileRows - 1) / kScoreTileRows;
+  return round32((rows + tiles - 1) / tiles);
+}
+
 struct WeightLayout {
-  size_t q_off, lse_off, bytes;
+  int tile_rows, tiles;
+  ScoreGrid grid;
+  size_t q_off, lse_off, part_off, bytes;
 };
-int weight_layout(const ddt_dims* d, int32_t num_sel, WeightLayout* w) {
+// sm_count 0: the sizes only (no grid, no bytes)
+int weight_layout(const ddt_dims* d, int32_t num_sel, int sm_count, WeightLayout* w) {
   const int rc = check_dims(d);
   if (rc != DDT_OK) return rc;
   if (num_sel < 0 || num_sel > 65535) return DDT_ERR_DIMS;
-  const size_t rows = size_t(d->batch) * num_sel * d->num_heads;
+  const int64_t rows = int64_t(num_sel > 0 ? num_sel : d->num_nodes) * d->num_heads;
+  if (rows * d->batch > INT32_MAX) return DDT_ERR_DIMS;
+  w->tile_rows = weight_tile_rows(static_cast<int>(rows));
+  w->tiles = static_cast<int>((rows + w->tile_rows - 1) / w->tile_rows);
+  if (!score_grid(d->batch, d->max_prefix_len, w->tiles, std::max(sm_count, 2), &w->grid)) return DDT_ERR_DIMS;
+  const size_t packed = num_sel > 0 ? size_t(rows) * d->batch : 0;
   w->q_off = kStatusBytes;
-  w->lse_off = align_up(w->q_off + rows * kRowBytes, 256);
-  w->bytes = align_up(w->lse_off + rows * sizeof(float), 256);
+  w->lse_off = align_up(w->q_off + packed * kRowBytes, 256);
+  w->part_off = align_up(w->lse_off + packed * sizeof(float), 256);
+  const size_t parts = w->grid.splits > 1 ? size_t(w->grid.splits) * d->batch * d->slot_stride : 0;
+  w->bytes = align_up(w->part_off + parts * sizeof(float), 256);
   return DDT_OK;
 }
 
@@ -109,8 +139,10 @@ int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, 
 using namespace ddt;
 
 extern "C" size_t ddtree_kv_weight_workspace_bytes(const ddt_dims* dims, int32_t num_sel) {
+  int sms = 0;
   WeightLayout w;
-  return weight_layout(dims, num_sel, &w) == DDT_OK ? w.bytes : 0;
+  if (current_device(&sms) != DDT_OK || weight_layout(dims, num_sel, sms, &w) != DDT_OK) return 0;
+  return w.bytes;
 }
 
 extern "C" int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_t* slot_idx, const int32_t* prefix_len,
@@ -118,7 +150,7 @@ extern "C" int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_
                                 float decay, const float* weight_in, float* weight_out, const ddt_dims* dims,
                                 void* workspace, size_t workspace_bytes, ddt_stream_t stream) {
   WeightLayout w;
-  int rc = weight_layout(dims, num_sel, &w);
+  int rc = weight_layout(dims, num_sel, 0, &w);  // the sizes, before any device query
   if (rc != DDT_OK) return rc;
   if (dims->batch == 0) return DDT_OK;
   if (!q || !kv_pool || !prefix_len || !lse || !workspace || (num_sel > 0 && !node_idx) ||
@@ -128,18 +160,20 @@ extern "C" int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_
       !aligned(prefix_len, 4) || !aligned(lse, 4) || !aligned(node_idx, 4) || !aligned(weight_in, 4) ||
       !aligned(weight_out, 4))
     return DDT_ERR_ALIGN;
-  if (workspace_bytes < w.bytes) return DDT_ERR_WORKSPACE;
   int sms = 0;
   if ((rc = current_device(&sms)) != DDT_OK) return rc;
+  if ((rc = weight_layout(dims, num_sel, sms, &w)) != DDT_OK) return rc;
+  if (workspace_bytes < w.bytes) return DDT_ERR_WORKSPACE;
   const bool packed = num_sel > 0;
   ScoreParams p = {};
   p.batch = dims->batch;
   p.rows = (packed ? num_sel : dims->num_nodes) * dims->num_heads;
   const int64_t q_rows = int64_t(p.batch) * p.rows;
-  if (!score_tiles(&p, dims->max_prefix_len, q_rows)) return DDT_ERR_DIMS;
-  p.tiles = (p.rows + kScoreMaxRows - 1) / kScoreMaxRows;
-  p.tile_rows = p.tile_n = round16((p.rows + p.tiles - 1) / p.tiles);
-  p.tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
+  p.tile_rows = p.tile_n = w.tile_rows;
+  p.tiles = w.tiles;
+  p.key_tiles = w.grid.key_tiles;
+  p.splits = w.grid.splits;
+  p.units = w.grid.units;
   p.keys = static_cast<const uint16_t*>(kv_pool);
   p.slot_idx = slot_idx;
   p.prefix_len = prefix_len;
@@ -155,9 +189,11 @@ extern "C" int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_
   p.weight_out = weight_out;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.status = reinterpret_cast<int32_t*>(ws);
+  p.part = reinterpret_cast<float*>(ws + w.part_off);
+  p.part_stride = int64_t(dims->batch) * dims->slot_stride;
   const void* qs = packed ? static_cast<const void*>(ws + w.q_off) : q;
   p.row_aux = packed ? reinterpret_cast<const float*>(ws + w.lse_off) : lse;
-  if (!encode_pool_map(&p.tmap_q, qs, q_rows, 64, p.tile_n)) return DDT_ERR_LAUNCH;
+  if (!encode_pool_map(&p.tmap_q, qs, q_rows, 64, p.tile_n / 2)) return DDT_ERR_LAUNCH;  // one CTA's half of a tile
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!clear_status(workspace, s)) return DDT_ERR_LAUNCH;
   if (packed) {
@@ -280,11 +316,17 @@ extern "C" int ddtree_block_select(const void* q, const void* summary, const flo
   p.batch = dims->batch;
   p.rows = dims->num_nodes * H;
   const int64_t q_rows = int64_t(p.batch) * p.rows;
-  if (!score_tiles(&p, w.blocks, q_rows) || w.blocks * p.batch > INT32_MAX) return DDT_ERR_DIMS;
-  // a tile holds whole nodes (up to 256 heads), so each epilogue set owns its nodes
-  p.tile_rows = H <= kScoreMaxRows ? std::min(p.rows, kScoreMaxRows / H * H) : kScoreMaxRows;
-  p.tile_n = round16(p.tile_rows);
+  if (q_rows > INT32_MAX || w.blocks * p.batch > INT32_MAX) return DDT_ERR_DIMS;
+  // a tile holds whole nodes (up to 128 heads), so each epilogue set owns its nodes
+  p.tile_rows = H <= kScoreTileRows ? std::min(p.rows, kScoreTileRows / H * H) : kScoreTileRows;
+  p.tile_n = round32(p.tile_rows);
   p.tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
+  ScoreGrid grid;
+  // (a node of more heads spans tiles: its rows are not shared out)
+  if (!score_grid(p.batch, w.blocks, H <= kScoreTileRows ? p.tiles : 1, sms, &grid)) return DDT_ERR_DIMS;
+  p.key_tiles = grid.key_tiles;
+  p.splits = grid.splits;
+  p.units = grid.units;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.keys = static_cast<const uint16_t*>(summary);
   p.prefix_len = prefix_len;
@@ -297,7 +339,7 @@ extern "C" int ddtree_block_select(const void* q, const void* summary, const flo
   p.key_scale = scale;
   p.score = reinterpret_cast<float*>(ws + w.score_off);
   p.status = reinterpret_cast<int32_t*>(ws);
-  if (!encode_pool_map(&p.tmap_q, ws + w.q_off, q_rows, 64, p.tile_n)) return DDT_ERR_LAUNCH;
+  if (!encode_pool_map(&p.tmap_q, ws + w.q_off, q_rows, 64, p.tile_n / 2)) return DDT_ERR_LAUNCH;
   QuantParams k = {};
   k.q = static_cast<const uint16_t*>(q);
   k.q_int = reinterpret_cast<uint16_t*>(ws + w.q_off);

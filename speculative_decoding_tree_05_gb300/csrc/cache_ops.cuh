@@ -12,8 +12,10 @@ constexpr int32_t kStatusBadNode = 32;
 constexpr int32_t kStatusBadBlock = 64;
 
 // ---------------------------------------------------------------- scores of rows against queries
-// Shared by key weights and block selection: 128 (or, on a CTA pair, 256) key
-// rows stay in shared memory while the query rows stream past them.
+// Shared by key weights and block selection: 256 key rows stay in the shared
+// memory of a CTA pair while the query rows stream past them.
+constexpr int kScoreTileKeys = 256;
+constexpr int kScoreTileRows = 128;  // query rows of one tile
 enum ScoreMode : int { kScoreWeight = 0, kScoreBlock = 1 };
 
 struct ScoreParams {
@@ -34,6 +36,10 @@ struct ScoreParams {
   int32_t heads;             // kScoreBlock: consecutive rows that make one node
   int32_t nodes;             // kScoreBlock: T
   int32_t key_tiles;         // key tiles of the longest request
+  int32_t splits;            // shares of the query tiles (few key tiles, many rows)
+  int32_t units;             // batch * key_tiles * splits
+  float* part;               // kScoreWeight with splits > 1: [splits, B, slot_stride] partial sums
+  int64_t part_stride;       // batch * slot_stride
   float scale_log2;          // kScoreWeight: sm_scale * log2(e)
   float decay;
   const float* row_aux;      // [B, rows]: kScoreWeight natural-log lse, kScoreBlock query scales

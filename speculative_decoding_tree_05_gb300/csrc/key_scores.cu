@@ -10,15 +10,24 @@
 // fixed order, so the results are the same bits on every run), and each key row
 // is fetched from the pool once, whatever the number of query rows.
 //
-// Per CTA (512 threads), a loop over tiles of 128 keys:
-//   warp 0       TMEM, and lane 0 issues the MMAs (M = 128 keys, N = up to 256 rows)
-//   warp 1       lane 0 loads the query rows by TMA: stages of 64 dims x N rows
-//   warps 4-11   two epilogue sets: one key per thread, set s takes the query
-//                tiles of parity s (TMEM columns [256 s, +256))
-//   warps 12-15  gather the key rows by 16-byte cp.async, zero-filled where
-//                there is no key, into three 192-dim groups.  A group is
-//                refilled as soon as the last query tile has used it, so with one query tile
-//                (the memory-bound case) two of the three groups are always in flight.
+// A pair of CTAs (640 threads each) shares every MMA: M = 256 keys, 128 in each
+// CTA, N = up to 128 query rows, half of them loaded by each, which halves the
+// query traffic from L2 (each key tile streams all query rows past it).  A loop
+// over tiles of 256 keys:
+//   warp 0        TMEM; in CTA 0 lane 0 issues the MMAs of the pair
+//   warp 1        lane 0 loads its half of the query rows by TMA: 3 stages of 192 dims
+//                 (a wait costs the issuing thread as much as three MMAs: 12 MMAs a stage)
+//   warp 2        in CTA 1, lane 0 tells CTA 0 which key groups have landed
+//   warps 4-11    two epilogue sets: one key per thread, set s takes the query
+//                 tiles of parity s
+//   warps 12-19   gather the key rows by 16-byte cp.async, zero-filled where
+//                 there is no key, into three 192-dim groups.  A group is
+//                 refilled as soon as the last query tile has used it, so with
+//                 one query tile (the memory-bound case) two of the three
+//                 groups are always in flight.
+// The tensor core truncates each 16-dim step of an accumulation, a bias that
+// grows with the running sum: dims 0-287 and 288-575 go to two accumulators,
+// added in fp32, which halves it (TMEM: 2 tiles x 2 accumulators x 128 columns).
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include "cache_ops.cuh"
@@ -27,24 +36,28 @@
 namespace ddt {
 namespace {
 
-constexpr int kScThreads = 512;
-constexpr int kScKeys = 128;
+constexpr int kScThreads = 640;
+constexpr int kScKeys = 128;                    // per CTA
 constexpr int kScChunk = kScKeys * 128;         // 64 dims of 128 keys: 16 KB
 constexpr int kScGroups = 3;
 constexpr int kScGroupBytes = 3 * kScChunk;     // 192 dims
-constexpr int kScMaxN = 256;
-constexpr int kScStages = 2;
-constexpr int kScStageBytes = kScMaxN * 128;    // 32 KB
+constexpr int kScStages = 3;
+constexpr int kScQChunk = kScoreTileRows / 2 * 128;              // 8 KB: this CTA's half of the rows, 64 dims
+constexpr int kScStageBytes = 3 * kScQChunk;
 constexpr int kScOffQ = kScGroups * kScGroupBytes;
-constexpr int kScOffAux = kScOffQ + kScStages * kScStageBytes;   // [2 sets][256] row constants
-constexpr int kScOffComb = kScOffAux + 2 * kScMaxN * 4;          // [2][128] sums handed from set 1 to set 0
+constexpr int kScOffAux = kScOffQ + kScStages * kScStageBytes;   // [2 sets][128] row constants
+constexpr int kScOffComb = kScOffAux + 2 * kScoreTileRows * 4;   // [2][128] sums handed from set 1 to set 0
 constexpr int kScSmem = kScOffComb + 2 * kScKeys * 4 + 1024;
+constexpr int kScProducers = 256;
 constexpr float kScLog2e = 1.4426950408889634f;
 
 struct ScShared {
   uint64_t k_full[kScGroups], k_empty[kScGroups];
-  uint64_t q_full[kScStages], q_empty[kScStages];
-  uint64_t s_full[2], s_free[2];
+  uint64_t k_peer[kScGroups];   // CTA 0: CTA 1's group has landed
+  uint64_t q_full[kScStages];   // CTA 0: both halves of the stage have landed
+  uint64_t q_empty[kScStages];
+  uint64_t s_full[2];
+  uint64_t s_free[2];           // CTA 0: the 8 epilogue warps of the pair have read the scores
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -55,26 +68,53 @@ __device__ __forceinline__ int clamp_len(const int32_t* prefix_len, int b, int m
   return L < 0 ? 0 : (L > max_len ? max_len : L);
 }
 
+// 32 consecutive columns of two accumulators of this thread's TMEM lane, added.
+__device__ __forceinline__ void tmem_ld32_sum(uint32_t a, uint32_t b, float (&v)[32]) {
+  float w[32];
+  tmem_ld32(a, v);
+  tmem_ld32(b, w);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] += w[i];
+}
+
 // Keys of request b: positions, or blocks of positions.
 __device__ __forceinline__ int key_count(const ScoreParams& p, int b) {
   const int L = clamp_len(p.prefix_len, b, p.max_prefix_len);
   return (L + p.block - 1) / p.block;
 }
 
+// A unit: 256 consecutive keys of one request against one share of its query tiles.
+struct ScUnit {
+  int b, kt, t0, t1, n;  // request, key tile, query tiles [t0, t1), keys of the request
+};
+__device__ __forceinline__ bool unit_at(const ScoreParams& p, int u, ScUnit* x) {
+  const int s = u % p.splits, v = u / p.splits;
+  x->b = v / p.key_tiles;
+  x->kt = v - x->b * p.key_tiles;
+  x->t0 = static_cast<int>(static_cast<int64_t>(p.tiles) * s / p.splits);
+  x->t1 = static_cast<int>(static_cast<int64_t>(p.tiles) * (s + 1) / p.splits);
+  x->n = key_count(p, x->b);
+  return x->kt * (2 * kScKeys) < x->n;
+}
+
 template <int kMode>
-__global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_constant__ ScoreParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
+    score_kernel(const __grid_constant__ ScoreParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ ScShared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   volatile int* abort = &sh.abort;
   grid_dep_launch();
 
   if (tid == 0) {
     for (int i = 0; i < kScGroups; ++i) {
-      mbar_init(&sh.k_full[i], 128);
+      mbar_init(&sh.k_full[i], kScProducers);
       mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.k_peer[i], 1);
     }
     for (int i = 0; i < kScStages; ++i) {
       mbar_init(&sh.q_full[i], 1);
@@ -82,45 +122,48 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_free[i], 128);
+      mbar_init(&sh.s_free[i], 8);
     }
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc(&sh.tmem_base, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(&sh.tmem_base, 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
-  const int units = p.batch * p.key_tiles;
+  const int units = p.units;
   bool ok = true;
-  // with more than 256 heads a node spans tiles, so one set takes them all
-  const bool two_sets = kMode == kScoreWeight || p.heads <= kScMaxN;
+  // with more heads than tile rows a node spans tiles, so one set takes them all
+  const bool two_sets = kMode == kScoreWeight || p.heads <= kScoreTileRows;
 
-  // every role walks the same units: those of its CTA that hold keys
+  // every role walks the same units: those of its pair that hold keys
+  ScUnit u;
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(kScKeys, p.tile_n, false, false);
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = idesc_bf16_f32(2 * kScKeys, p.tile_n, false, false);
       const uint64_t d_k = smem_desc(base, 16, 1024, kSwizzle128B);
       const uint64_t d_q = smem_desc(base + kScOffQ, 16, 1024, kSwizzle128B);
       uint32_t n_unit = 0, n_stage = 0, n_tile = 0;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const int b = u / p.key_tiles, kt = u - b * p.key_tiles;
-        if (kt * kScKeys >= key_count(p, b)) continue;
-        for (int qt = 0; ok && qt < p.tiles; ++qt, ++n_tile) {
+      for (int i = pair; ok && i < units; i += pairs) {
+        if (!unit_at(p, i, &u)) continue;
+        for (int qt = u.t0; ok && qt < u.t1; ++qt, ++n_tile) {
           const uint32_t buf = n_tile & 1;
-          if (n_tile >= 2 && !mbar_wait_abortable(&sh.s_free[buf], ((n_tile >> 1) - 1) & 1, abort, false, __LINE__)) {
+          if (n_tile >= 2 &&
+              !mbar_wait_abortable(&sh.s_free[buf], ((n_tile >> 1) - 1) & 1, abort, true, __LINE__)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          for (int c = 0; c < 9; ++c, ++n_stage) {
-            if (qt == 0 && c % 3 == 0) {
-              if (!mbar_wait_abortable(&sh.k_full[c / 3], n_unit & 1, abort, false, __LINE__)) {
+          const uint32_t d = tmem + buf * 2 * kScoreTileRows;
+          for (int g = 0; g < kScGroups; ++g, ++n_stage) {
+            if (qt == u.t0) {
+              if (!mbar_wait_abortable(&sh.k_full[g], n_unit & 1, abort, false, __LINE__) ||
+                  !mbar_wait_abortable(&sh.k_peer[g], n_unit & 1, abort, true, __LINE__)) {
                 ok = false;
                 break;
               }
@@ -132,66 +175,88 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
               break;
             }
             tc_fence_after();
+            const uint64_t a = desc_advance(d_k, g * kScGroupBytes), q = desc_advance(d_q, st * kScStageBytes);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem + buf * kScMaxN, desc_advance(d_k, c * kScChunk + ks * 32),
-                     desc_advance(d_q, st * kScStageBytes + ks * 32), idesc, (c | ks) ? 1u : 0u);
-            mma_commit(&sh.q_empty[st]);
-            if (qt == p.tiles - 1 && c % 3 == 2) mma_commit(&sh.k_empty[c / 3]);
+            for (int k = 0; k < 12; ++k) {
+              // the accumulators change at step 18, the middle of the second group
+              const uint32_t upper = g == 2 || (g == 1 && k >= 6) ? kScoreTileRows : 0;
+              const uint32_t fresh = (g == 0 && k == 0) || (g == 1 && k == 6);
+              mma_ss_pair(d + upper, desc_advance(a, (k >> 2) * kScChunk + (k & 3) * 32),
+                          desc_advance(q, (k >> 2) * kScQChunk + (k & 3) * 32), idesc, fresh ? 0u : 1u);
+            }
+            mma_commit_pair(&sh.q_empty[st]);
+            if (qt == u.t1 - 1) mma_commit_pair(&sh.k_empty[g]);
           }
-          if (ok) mma_commit(&sh.s_full[buf]);
+          if (ok) mma_commit_pair(&sh.s_full[buf]);
         }
         ++n_unit;
       }
-      mma_commit(&sh.drain);
+      mma_commit_pair(&sh.drain);
       mbar_wait(&sh.drain, 0);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       grid_dep_wait();  // the query rows may come from the kernel before (packed, 8-bit)
       uint32_t n_stage = 0;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const int b = u / p.key_tiles, kt = u - b * p.key_tiles;
-        if (kt * kScKeys >= key_count(p, b)) continue;
-        for (int qt = 0; ok && qt < p.tiles; ++qt) {
-          for (int c = 0; c < 9; ++c, ++n_stage) {
+      const int half = p.tile_n / 2;
+      for (int i = pair; ok && i < units; i += pairs) {
+        if (!unit_at(p, i, &u)) continue;
+        for (int qt = u.t0; ok && qt < u.t1; ++qt) {
+          for (int g = 0; g < kScGroups; ++g, ++n_stage) {
             const uint32_t st = n_stage % kScStages;
             if (n_stage >= kScStages &&
                 !mbar_wait_abortable(&sh.q_empty[st], ((n_stage / kScStages) - 1) & 1, abort, false, __LINE__)) {
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(&sh.q_full[st], p.tile_n * 128);
-            tma_load_2d(base + kScOffQ + st * kScStageBytes, &p.tmap_q, c * 64, b * p.rows + qt * p.tile_rows,
-                        &sh.q_full[st]);
+            if (rank == 0) mbar_arrive_expect_tx(&sh.q_full[st], 3 * p.tile_n * 128);  // both halves
+            // rows past the tensor's end read as zero; a start past it is moved to the last row
+            const int row = min(u.b * p.rows + qt * p.tile_rows + rank * half, p.batch * p.rows - 1);
+            const uint32_t full = mapa_shared(smem_u32(&sh.q_full[st]), 0);
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+              tma_load_2d_pair(base + kScOffQ + st * kScStageBytes + c * kScQChunk, &p.tmap_q, (3 * g + c) * 64, row, full);
           }
         }
       }
-      // after a give-up, the loads still in flight land before the CTA exits
-      if (!ok)
-        for (uint32_t i = n_stage > kScStages ? n_stage - kScStages : 0; i < n_stage; ++i)
-          mbar_wait(&sh.q_full[i % kScStages], (i / kScStages) & 1);
+      // after a give-up, the loads still in flight land before the pair exits
+      if (!ok && rank == 0)
+        for (uint32_t j = n_stage > kScStages ? n_stage - kScStages : 0; j < n_stage; ++j)
+          mbar_wait(&sh.q_full[j % kScStages], (j / kScStages) & 1);
+    }
+  } else if (warp == 2) {
+    if (rank == 1 && lane == 0) {
+      uint32_t n_unit = 0;
+      for (int i = pair; ok && i < units; i += pairs) {
+        if (!unit_at(p, i, &u)) continue;
+        for (int g = 0; ok && g < kScGroups; ++g) {
+          if (!mbar_wait_abortable(&sh.k_full[g], n_unit & 1, abort, false, __LINE__)) {
+            ok = false;
+            break;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive_remote(mapa_shared(smem_u32(&sh.k_peer[g]), 0));
+        }
+        ++n_unit;
+      }
     }
   } else if (warp >= 12) {
     const int pw = warp - 12;
     uint32_t n_unit = 0;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const int b = u / p.key_tiles, kt = u - b * p.key_tiles;
-      const int n = key_count(p, b);
-      if (kt * kScKeys >= n) continue;
-      // this warp gathers keys 32 pw .. 32 pw + 31 of the tile, lane l holding the row of key l
-      const int j = kt * kScKeys + 32 * pw + lane;
-      int64_t row = -1;
-      if (j < n) {
+    for (int i = pair; ok && i < units; i += pairs) {
+      if (!unit_at(p, i, &u)) continue;
+      // this warp gathers keys 16 pw .. 16 pw + 15 of the CTA's 128, lane l < 16 holding the row of key l
+      const int j = (u.kt * 2 + rank) * kScKeys + 16 * pw + lane;
+      int row = -1;  // rows stay below 2^31
+      if (lane < 16 && j < u.n) {
         if (p.slot_idx != nullptr) {
-          const int slot = __ldg(p.slot_idx + static_cast<int64_t>(b) * p.slot_stride + j);
+          const int slot = __ldg(p.slot_idx + static_cast<int64_t>(u.b) * p.slot_stride + j);
           if (slot >= 0 && slot < p.pool_slots) row = slot;
           if (row < 0) atomicOr(p.status, kStatusBadSlot);
         } else {
-          row = static_cast<int64_t>(b) * p.key_stride + j;
+          row = static_cast<int>(u.b * p.key_stride + j);
         }
       }
-      const int row32 = static_cast<int>(row);  // rows stay below 2^31
       for (int g = 0; g < kScGroups; ++g) {
         const bool w = n_unit == 0 || mbar_wait_abortable(&sh.k_empty[g], (n_unit - 1) & 1, abort, false, __LINE__);
         if (!__all_sync(0xffffffffu, w)) {
@@ -199,12 +264,12 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
           break;
         }
         // 24 pieces of 16 bytes per row and group: consecutive lanes take consecutive pieces
-#pragma unroll 4
-        for (int i = 0; i < 24; ++i) {
-          const int e = i * 32 + lane;
+#pragma unroll 6
+        for (int k = 0; k < 12; ++k) {
+          const int e = k * 32 + lane;
           const int r = e / 24, x = e - r * 24;
-          const int src_row = __shfl_sync(0xffffffffu, row32, r);
-          const int rr = 32 * pw + r;
+          const int src_row = __shfl_sync(0xffffffffu, row, r);
+          const int rr = 16 * pw + r;
           const uint32_t dst = base + g * kScGroupBytes + (x >> 3) * kScChunk + rr * 128 + (((x & 7) ^ (rr & 7)) << 4);
           const uint16_t* src = p.keys + (src_row < 0 ? 0 : static_cast<int64_t>(src_row) * kDqk + g * 192 + x * 8);
           cp_async16(dst, src, src_row < 0 ? 0u : 16u);
@@ -216,36 +281,36 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     cp_async_wait<0>();
   } else if (warp >= 4) {
     const int set = (warp - 4) >> 2;
-    const int r = (warp & 3) * 32 + lane;  // key of the tile = TMEM lane
+    const int r = (warp & 3) * 32 + lane;  // key of the CTA's 128 = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    float* aux = reinterpret_cast<float*>(smem + kScOffAux) + set * kScMaxN;
+    float* aux = reinterpret_cast<float*>(smem + kScOffAux) + set * kScoreTileRows;
     float* comb = reinterpret_cast<float*>(smem + kScOffComb);
+    const uint32_t free0 = mapa_shared(smem_u32(&sh.s_free[0]), 0), free1 = mapa_shared(smem_u32(&sh.s_free[1]), 0);
     uint32_t n_unit = 0, n_tile = 0;
     grid_dep_wait();  // row_aux, as the query rows
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const int b = u / p.key_tiles, kt = u - b * p.key_tiles;
-      const int n = key_count(p, b);
-      if (kt * kScKeys >= n) continue;
-      const int j = kt * kScKeys + r;
+    for (int i = pair; ok && i < units; i += pairs) {
+      if (!unit_at(p, i, &u)) continue;
+      const int b = u.b, n = u.n;
+      const int j = (u.kt * 2 + rank) * kScKeys + r;
       float acc = kMode == kScoreWeight ? 0.f : -CUDART_INF_F;
-      const float key_scale = kMode == kScoreBlock && j < n ? __ldg(p.key_scale + static_cast<int64_t>(b) * p.key_stride + j) : 0.f;
+      const float key_scale = kMode == kScoreBlock && j < n ? __ldg(p.key_scale + b * p.key_stride + j) : 0.f;
       int node = 0, left = p.heads;  // kScoreBlock: the node that the next row belongs to, its rows left
-      for (int qt = 0; ok && qt < p.tiles; ++qt, ++n_tile) {
+      for (int qt = u.t0; ok && qt < u.t1; ++qt, ++n_tile) {
         if ((two_sets ? static_cast<int>(n_tile & 1) : 0) != set) continue;
         const uint32_t buf = n_tile & 1;
         const int row0 = qt * p.tile_rows;
         const int live = min(p.tile_rows, p.rows - row0);
         // row constants of the tile: weights -lse in log2 units, -inf where a row counts for nothing
         bar_sync(1 + set, 128);  // the last tile's are read
-        for (int i = r; i < kScMaxN; i += 128) {
+        {
           float a;
           if (kMode == kScoreWeight) {
-            const float l = i < live ? __ldg(p.row_aux + static_cast<int64_t>(b) * p.rows + row0 + i) : CUDART_INF_F;
+            const float l = r < live ? __ldcg(p.row_aux + static_cast<int64_t>(b) * p.rows + row0 + r) : CUDART_INF_F;
             a = fabsf(l) == CUDART_INF_F ? -CUDART_INF_F : -l * kScLog2e;
           } else {
-            a = i < live ? __ldg(p.row_aux + static_cast<int64_t>(b) * p.rows + row0 + i) : CUDART_NAN_F;
+            a = r < live ? __ldcg(p.row_aux + static_cast<int64_t>(b) * p.rows + row0 + r) : CUDART_NAN_F;
           }
-          aux[i] = a;
+          aux[r] = a;
         }
         // the set leaves together if a wait of one of its warps ran out
         const bool got = mbar_wait_abortable(&sh.s_full[buf], (n_tile >> 1) & 1, abort, false, __LINE__);
@@ -255,10 +320,10 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
         }
         tc_fence_after();
         if (kMode == kScoreBlock && two_sets) node = row0 / p.heads;
+        const uint32_t col = tmem + lane_off + buf * 2 * kScoreTileRows;
         for (int c = 0; c < p.tile_n; c += 32) {
           float s[32];
-          // (the columns past tile_n of the last 32 are stale: their constants are not used)
-          tmem_ld32(tmem + lane_off + buf * kScMaxN + c, s);
+          tmem_ld32_sum(col + c, col + kScoreTileRows + c, s);
           if (kMode == kScoreWeight) {
             const bool all_live = __all_sync(0xffffffffu, aux[c + lane] != -CUDART_INF_F);
             float t[4] = {0.f, 0.f, 0.f, 0.f};
@@ -315,7 +380,8 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
           }
         }
         tc_fence_before();
-        mbar_arrive(&sh.s_free[buf]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(buf ? free1 : free0);
       }
       if (bar_red_or(3, 256, !ok)) {
         ok = false;
@@ -330,7 +396,10 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
           const int64_t at = static_cast<int64_t>(b) * p.slot_stride + j;
           const int sl = __ldg(p.slot_idx + at);
           const float sum = sl >= 0 && sl < p.pool_slots ? acc + slot[r] : 0.f;
-          p.weight_out[at] = p.weight_in != nullptr ? fmaf(p.decay, p.weight_in[at], sum) : sum;
+          if (p.splits > 1)
+            p.part[(i % p.splits) * p.part_stride + at] = sum;
+          else
+            p.weight_out[at] = p.weight_in != nullptr ? fmaf(p.decay, p.weight_in[at], sum) : sum;
         }
       }
       ++n_unit;
@@ -340,15 +409,30 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     *abort = 1;
     atomicOr(p.status, kStatusTimeout);
   }
+  // the leader's commits arrive here too: the last one before this CTA may leave
+  if (warp == 0 && rank == 1 && lane == 0) mbar_wait(&sh.drain, 0);
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // nothing of the pair is in flight towards either CTA
   tc_fence_after();
-  if (warp == 0) tmem_dealloc(tmem, 512);
+  if (warp == 0) tmem_dealloc_pair(tmem, 512);
   if (blockIdx.x == 0)
     for (int b = tid; b < p.batch; b += kScThreads) {
       const int L = __ldg(p.prefix_len + b);
       if (L < 0 || L > p.max_prefix_len) atomicOr(p.status, kStatusBadPrefix);
     }
+}
+
+// Sums of the query shares of a key, in order, and the decayed old weight.
+__global__ void __launch_bounds__(256) weight_sum_kernel(const __grid_constant__ ScoreParams p) {
+  const int b = blockIdx.y;
+  const int L = clamp_len(p.prefix_len, b, p.max_prefix_len);
+  grid_dep_wait();
+  for (int j = blockIdx.x * 256 + threadIdx.x; j < L; j += gridDim.x * 256) {
+    const int64_t at = static_cast<int64_t>(b) * p.slot_stride + j;
+    float sum = 0.f;
+    for (int s = 0; s < p.splits; ++s) sum += __ldcg(p.part + s * p.part_stride + at);
+    p.weight_out[at] = p.weight_in != nullptr ? fmaf(p.decay, p.weight_in[at], sum) : sum;
+  }
 }
 
 // One CTA copies one selected node's rows (H x 72 pieces of 16 bytes) and lse.
@@ -375,21 +459,26 @@ cudaError_t configure_scores() {
 }
 
 cudaError_t launch_scores(const ScoreParams& p, ScoreMode mode, int sm_count, bool after_kernel, cudaStream_t stream) {
-  const int64_t units = int64_t(p.batch) * p.key_tiles;
-  if (units == 0) return cudaSuccess;
-  const int grid = static_cast<int>(units < sm_count ? units : sm_count);
+  if (p.units == 0) return cudaSuccess;
+  const int pairs = sm_count >= 4 ? sm_count / 2 : 1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(2 * (p.units < pairs ? p.units : pairs));
   cfg.blockDim = dim3(kScThreads);
   cfg.dynamicSmemBytes = kScSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = after_kernel ? 1 : 0;
-  return mode == kScoreWeight ? cudaLaunchKernelEx(&cfg, score_kernel<kScoreWeight>, p)
-                              : cudaLaunchKernelEx(&cfg, score_kernel<kScoreBlock>, p);
+  if (mode == kScoreBlock) return cudaLaunchKernelEx(&cfg, score_kernel<kScoreBlock>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, score_kernel<kScoreWeight>, p);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  cfg.gridDim = dim3((p.max_prefix_len + 1023) / 1024, p.batch);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weight_sum_kernel, p);
 }
 
 cudaError_t launch_pack_nodes(const PackParams& p, int batch, cudaStream_t stream) {

@@ -330,7 +330,9 @@ class KeyWeights:
                               slot_stride if max_prefix_len is None else max_prefix_len)
         self.max_sel = int(nodes if max_sel is None else max_sel)
         self.device = _cuda_device(device)
-        n = int(self.lib.ddtree_kv_weight_workspace_bytes(ctypes.byref(self.dims), self.max_sel))
+        with _On(self.device):
+            n = max(int(self.lib.ddtree_kv_weight_workspace_bytes(ctypes.byref(self.dims), k))
+                    for k in range(self.max_sel + 1))
         if n == 0:
             raise DDTError(-2, "ddtree_kv_weight_workspace_bytes")
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
