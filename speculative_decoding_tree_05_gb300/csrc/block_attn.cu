@@ -18,12 +18,14 @@
 // operand type, against row sums of the unrounded values: an error of half a
 // bf16 step per weight, averaged over the keys, below the bf16 rounding of out.
 //
-// Per CTA (288 threads), one unit = (group, split of its key tiles):
-//   warp 0      TMEM; lane 0 issues S(t) when stage t has landed and P.V(t) when P(t) is written
+// Per CTA (416 threads), one unit = (group, split of its key tiles):
+//   warp 0      TMEM; one lane issues S(t) dim group by dim group as stage t
+//               lands, and P.V(t) when P(t) is written, whichever is ready
 //   warps 1-4   softmax: TMEM rows 16 at a time in the 16x256b shape (row r in
 //               lanes 4 r .. 4 r + 3), the running max per row in shared memory,
 //               raised (and O^T rescaled) only when a score exceeds it by 2^8
-//   warps 5-8   gather 64 keys per stage by 16-byte cp.async, two stages
+//   warps 5-12  gather 64 keys per stage by 16-byte cp.async, two stages of four
+//               dim groups, each refilled as soon as its part of P.V is done
 // A unit writes the normalised O and the log-sum-exp of its share; the
 // tail/merge kernel adds the tree part and merges the splits.
 #include <cuda_runtime.h>
@@ -34,7 +36,9 @@
 namespace ddt {
 namespace {
 
-constexpr int kBaThreads = 288;
+constexpr int kBaThreads = 416;
+constexpr int kBaProducers = 256;
+constexpr int kBaGroups = 4;                    // dims {512-575, 0-127}, {128-255}, {256-383}, {384-511}
 constexpr int kBaKeys = 64;
 constexpr int kBaRows = kBlockRows;             // 64
 constexpr int kBaStages = 2;
@@ -54,12 +58,14 @@ constexpr float kBaThreshold = 8.f;             // log2 units
 constexpr float kBaLn2 = 0.69314718055994531f;
 
 struct BaShared {
-  uint64_t k_full[kBaStages], k_empty[kBaStages];  // k_empty: P.V of the stage's tile done
+  uint64_t k_full[kBaStages][kBaGroups];
+  uint64_t k_empty[kBaStages][kBaGroups];  // this group's part of the tile's P.V is done (and those before it)
   uint64_t s_full[2], s_free[2];
   uint64_t p_ready;
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+  int fail[2];  // softmax: a wait of tile t ran out, by parity of t
 };
 static_assert(sizeof(BaShared) <= 256, "barrier block");
 
@@ -129,10 +135,11 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
   }
 
   if (tid == 0) {
-    for (int i = 0; i < kBaStages; ++i) {
-      mbar_init(&sh.k_full[i], 128 + 4);
-      mbar_init(&sh.k_empty[i], 1);
-    }
+    for (int i = 0; i < kBaStages; ++i)
+      for (int x = 0; x < kBaGroups; ++x) {
+        mbar_init(&sh.k_full[i][x], kBaProducers + (x == 0 ? 8 : 0));  // group 0 carries the key masks
+        mbar_init(&sh.k_empty[i][x], 1);
+      }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_free[i], 128);
@@ -140,6 +147,7 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
     mbar_init(&sh.p_ready, 128);
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
+    sh.fail[0] = sh.fail[1] = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
   bool ok = true;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       const int ncol = (u.rows + 15) / 16 * 16;
       const uint32_t idesc_s = idesc_bf16_f32(64, ncol, false, false);
       const uint32_t idesc_o = idesc_bf16_f32(128, ncol, true, true);
@@ -174,37 +182,48 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
       const uint64_t d_q = smem_desc(base + kBaOffQ, 16, 1024, kSwizzle128B);
       const uint64_t d_v = smem_desc(base, kBaChunk, 1024, kSwizzle128B);            // MN-major
       const uint64_t d_p = smem_desc(base + kBaOffP, kBaChunk, 1024, kSwizzle128B);  // MN-major
-      int next_s = 0, next_pv = 0;
-      // whichever is ready: P.V(t) first, it frees the stage that the loads wait for
-      for (uint32_t spin = 0; next_pv < n;) {
-        if (next_pv < next_s && mbar_test_wait(&sh.p_ready, next_pv & 1)) {
+      int s_tile = 0, s_group = 0, pv = 0;
+      // P.V(t) first when it is ready: it frees the stage that the loads wait for
+      for (uint32_t spin = 0; pv < n;) {
+        if (pv < s_tile && mbar_test_wait(&sh.p_ready, pv & 1)) {
           fence_proxy_async_smem();
           tc_fence_after();
-          const uint32_t so = (next_pv & 1) * kBaStageBytes;
-#pragma unroll 1
-          for (int mt = 0; mt < 4; ++mt)
+          const uint64_t v = desc_advance(d_v, (pv & 1) * kBaStageBytes);
+          const uint32_t more = pv > 0 ? 1u : 0u;
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem + mt * kBaRows, desc_advance(d_v, so + mt * 2 * kBaChunk + ks * 2048),
-                     desc_advance(d_p, ks * 2048), idesc_o, (next_pv | ks) ? 1u : 0u);
-          mma_commit(&sh.k_empty[next_pv & 1]);
-          ++next_pv;
+              mma_ss(tmem + mt * kBaRows, desc_advance(v, mt * 2 * kBaChunk + ks * 2048), desc_advance(d_p, ks * 2048),
+                     idesc_o, ks > 0 ? 1u : more);
+            mma_commit(&sh.k_empty[pv & 1][mt]);
+          }
+          ++pv;
           spin = 0;
           continue;
         }
-        if (next_s < n && mbar_test_wait(&sh.k_full[next_s & 1], (next_s >> 1) & 1) &&
-            (next_s < 2 || mbar_test_wait(&sh.s_free[next_s & 1], ((next_s >> 1) - 1) & 1))) {
+        if (s_tile < n && mbar_test_wait(&sh.k_full[s_tile & 1][s_group], (s_tile >> 1) & 1) &&
+            (s_group > 0 || s_tile < 2 || mbar_test_wait(&sh.s_free[s_tile & 1], ((s_tile >> 1) - 1) & 1))) {
           fence_proxy_async_smem();  // the stage was written by cp.async
           tc_fence_after();
-          const uint32_t so = (next_s & 1) * kBaStageBytes;
-#pragma unroll 1
-          for (int c = 0; c < 9; ++c)
+          const uint64_t k = desc_advance(d_k, (s_tile & 1) * kBaStageBytes);
+          const uint32_t d = tmem + kBaColS + (s_tile & 1) * kBaRows;
+          if (s_group == 0) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem + kBaColS + (next_s & 1) * kBaRows, desc_advance(d_k, so + c * kBaChunk + ks * 32),
-                     desc_advance(d_q, c * kBaChunk + ks * 32), idesc_s, (c | ks) ? 1u : 0u);
-          mma_commit(&sh.s_full[next_s & 1]);
-          ++next_s;
+            for (int ks = 0; ks < 4; ++ks)  // the rope dims
+              mma_ss(d, desc_advance(k, 8 * kBaChunk + ks * 32), desc_advance(d_q, 8 * kBaChunk + ks * 32), idesc_s,
+                     ks > 0 ? 1u : 0u);
+          }
+          const uint64_t kg = desc_advance(k, s_group * 2 * kBaChunk), qg = desc_advance(d_q, s_group * 2 * kBaChunk);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ss(d, desc_advance(kg, (ks >> 2) * kBaChunk + (ks & 3) * 32),
+                   desc_advance(qg, (ks >> 2) * kBaChunk + (ks & 3) * 32), idesc_s, 1u);
+          if (++s_group == kBaGroups) {
+            mma_commit(&sh.s_full[s_tile & 1]);
+            s_group = 0;
+            ++s_tile;
+          }
           spin = 0;
           continue;
         }
@@ -217,15 +236,15 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
       mbar_wait(&sh.drain, 0);
     }
   } else if (warp >= 5) {
-    // ------------------------------------------------------------------ producers: 16 keys per warp
+    // ------------------------------------------------------------------ producers: 8 keys per warp
     const int pw = warp - 5;
     const int32_t* slots = p.slot_idx + static_cast<int64_t>(u.b) * p.slot_stride;
     // key of this lane in tile t: its block entry, then its slot
     auto entry_of = [&](int t, int* pos, uint64_t* mask) {
       *pos = -1;
       *mask = 0;
-      const int64_t i = (static_cast<int64_t>(t0 + t)) * kBaKeys + 16 * pw + lane;
-      if (t < n && lane < 16 && i < keys) {
+      const int64_t i = (static_cast<int64_t>(t0 + t)) * kBaKeys + 8 * pw + lane;
+      if (t < n && lane < 8 && i < keys) {
         const int e = static_cast<int>(i / p.block);
         const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(list + e));
         BlockEntry be;
@@ -256,26 +275,35 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
       uint64_t mask_f;
       entry_of(t + 2, &pos_f, &mask_f);
       const int st = t & 1;
-      const bool w = t < kBaStages || mbar_wait_abortable(&sh.k_empty[st], ((t >> 1) - 1) & 1, abort, false, __LINE__);
-      if (!__all_sync(0xffffffffu, w)) {
-        ok = false;
-        break;
-      }
-      if (lane < 16)
-        reinterpret_cast<uint64_t*>(smem + kBaOffMask)[st * kBaKeys + 16 * pw + lane] = slot_c >= 0 ? mask_c : 0;
       const uint32_t sbase = base + st * kBaStageBytes;
-#pragma unroll 4
-      for (int i = 0; i < 36; ++i) {
-        const int e = i * 32 + lane;
-        const int r = e / kChunks, x = e - r * kChunks;
-        const int row = __shfl_sync(0xffffffffu, slot_c, r);
-        const int rr = 16 * pw + r;
-        cp_async16(sbase + (x >> 3) * kBaChunk + rr * 128 + (((x & 7) ^ (rr & 7)) << 4),
-                   p.kv + (row < 0 ? 0 : static_cast<int64_t>(row) * kDqk + x * 8), row < 0 ? 0u : 16u);
+#pragma unroll
+      for (int x = 0; x < kBaGroups; ++x) {
+        const bool w = t < kBaStages || mbar_wait_abortable(&sh.k_empty[st][x], ((t >> 1) - 1) & 1, abort, false, __LINE__);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
+        if (x == 0) {
+          if (lane < 8)
+            reinterpret_cast<uint64_t*>(smem + kBaOffMask)[st * kBaKeys + 8 * pw + lane] = slot_c >= 0 ? mask_c : 0;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.k_full[st][0]);  // releases the masks
+        }
+        // pieces of 16 bytes per row: the group's two latent chunks, and with group 0 the rope chunk
+        const int per = x == 0 ? 24 : 16;
+#pragma unroll
+        for (int i = 0; i < per / 4; ++i) {
+          const int e = i * 32 + lane;
+          const int r = e / per, y = e - r * per;
+          const int c = y < 16 ? 2 * x + (y >> 3) : 8;  // 64-dim chunk
+          const int row = __shfl_sync(0xffffffffu, slot_c, r);
+          const int rr = 8 * pw + r;
+          cp_async16(sbase + c * kBaChunk + rr * 128 + (((y & 7) ^ (rr & 7)) << 4),
+                     p.kv + (row < 0 ? 0 : static_cast<int64_t>(row) * kDqk + c * 64 + (y & 7) * 8), row < 0 ? 0u : 16u);
+        }
+        cp_async_arrive_noinc(&sh.k_full[st][x]);
       }
-      cp_async_arrive_noinc(&sh.k_full[st]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.k_full[st]);  // releases the masks
+      if (!ok) break;
       slot_c = slot_n;
       mask_c = mask_n;
       pos_n = pos_f;
@@ -296,14 +324,17 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
     float l[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) l[i] = 0.f;
+    bool failed = false;  // a wait of this thread ran out: the warps leave together at the next barrier
+    auto wait_pv = [&](int t) {  // P.V(t) has read P, and O^T holds every tile up to t
+      if (!mbar_wait_abortable(&sh.k_empty[t & 1][kBaGroups - 1], (t >> 1) & 1, abort, false, __LINE__)) failed = true;
+      tc_fence_after();
+    };
     for (int t = 0; t < n; ++t) {
       const int st = t & 1;
-      const bool got = mbar_wait_abortable(&sh.s_full[st], (t >> 1) & 1, abort, false, __LINE__) &&
-                       mbar_wait_abortable(&sh.k_full[st], (t >> 1) & 1, abort, false, __LINE__);
-      if (bar_red_or(1, 128, !got)) {
-        ok = false;
-        break;
-      }
+      // (the masks were released with the stage's first group)
+      if (!mbar_wait_abortable(&sh.s_full[st], (t >> 1) & 1, abort, false, __LINE__) ||
+          !mbar_wait_abortable(&sh.k_full[st][0], (t >> 1) & 1, abort, false, __LINE__))
+        failed = true;
       tc_fence_after();
       float s[32];
       tmem_ld_16x64(tmem + lane_off + kBaColS + st * kBaRows, s);
@@ -346,17 +377,15 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
         over = fmax3(over, s[4 * i] - m.x, s[4 * i + 1] - m.y);
         over = fmax3(over, s[4 * i + 2] - m.x, s[4 * i + 3] - m.y);
       }
-      const bool raise = bar_red_or(1, 128, over > kBaThreshold);
-      if (t > 0) {
-        // P.V(t-1) has read P, and O^T holds every tile before this one
-        const bool w = mbar_wait_abortable(&sh.k_empty[st ^ 1], ((t - 1) >> 1) & 1, abort, false, __LINE__);
-        if (bar_red_or(1, 128, !w)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+      if (failed) sh.fail[st] = 1;
+      const bool raise = bar_red_or(1, 128, failed || over > kBaThreshold);
+      if (raise && *const_cast<volatile int*>(&sh.fail[st])) {
+        ok = false;
+        break;
       }
       if (raise) {
+        if (t > 0) wait_pv(t - 1);  // the scratch is the P buffer, and O^T is rescaled
+        bar_sync(1, 128);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -399,18 +428,26 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
       }
       // P^T, row (key) r of 64 columns, 128-byte swizzle
       uint8_t* pb = smem + kBaOffP;
+      uint32_t pk[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 m = *reinterpret_cast<const float2*>(mx + 8 * i + c0);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float x = fast_exp2(s[4 * i + 2 * h] - m.x), y = fast_exp2(s[4 * i + 2 * h + 1] - m.y);
-          const int key = r0 + 8 * h;
           l[2 * i] += x;
           l[2 * i + 1] += y;
-          *reinterpret_cast<uint32_t*>(pb + key * 128 + ((i ^ (key & 7)) << 4) + c0 * 2) = pack_bf16x2(x, y);
+          pk[2 * i + h] = pack_bf16x2(x, y);
         }
       }
+      if (t > 0) wait_pv(t - 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = r0 + 8 * h;
+          *reinterpret_cast<uint32_t*>(pb + key * 128 + ((i ^ (key & 7)) << 4) + c0 * 2) = pk[2 * i + h];
+        }
       if (part && __any_sync(0xffffffffu, bad0 || bad1)) {
         // A non-finite key row that not every row of the group reads: 0 * inf
         // would spoil the others' O, so its values become zero and the weights
@@ -438,9 +475,8 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
       mbar_arrive(&sh.p_ready);
     }
     if (ok) {
-      // the last P.V is done: O^T is complete and the P buffer free
-      const bool w = mbar_wait_abortable(&sh.k_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, false, __LINE__);
-      if (bar_red_or(1, 128, !w)) ok = false;
+      wait_pv(n - 1);  // O^T is complete and the P buffer free
+      if (bar_red_or(1, 128, failed)) ok = false;
     }
     if (ok) {
       tc_fence_after();
@@ -461,17 +497,25 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
         alpha_sh[c] = sum != 0.f ? 1.f / sum : 0.f;
         if (c < u.rows) p.lse_part[prow0 + c] = sum != 0.f ? (mx[c] + log2f(sum)) * kBaLn2 : -CUDART_INF_F;
       }
-      bar_sync(1, 128);
+    }
+  }
+  // every warp but the first writes O: quarter of the lanes by warp, three warps a quarter
+  if (warp > 0) {
+    if (!bar_red_or(2, kBaThreads - 32, !ok)) {
+      tc_fence_after();
+      const float* inv_l = reinterpret_cast<const float*>(smem + kBaOffAlpha);
+      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       // lane = value dim: each row's store is 128 contiguous bytes per warp
 #pragma unroll 1
-      for (int k0 = 0; k0 < 8; ++k0) {
+      for (int k0 = (warp - 1) >> 2; k0 < 8; k0 += 3) {
         const int mt = k0 >> 1, cc = (k0 & 1) * 32;
+        if (cc >= u.rows) continue;
         float o[32];
         tmem_ld32(tmem + lane_off + mt * kBaRows + cc, o);
-        float* dst = p.o_part + prow0 * kDv + mt * 128 + quarter * 32 + lane;
+        float* dst = p.o_part + prow0 * kDv + mt * 128 + (warp & 3) * 32 + lane;
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-          if (cc + k < u.rows) dst[static_cast<int64_t>(cc + k) * kDv] = o[k] * alpha_sh[cc + k];
+          if (cc + k < u.rows) dst[static_cast<int64_t>(cc + k) * kDv] = o[k] * inv_l[cc + k];
       }
     }
   }
