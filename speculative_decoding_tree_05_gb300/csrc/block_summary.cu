@@ -23,6 +23,7 @@ constexpr int kSumGroups = 4;
 constexpr int kSumThreads = kSumGroups * kChunks;  // 288
 constexpr int kSumBatch = 8;                       // rows in flight per thread
 constexpr int kMaxBlock = 128;
+constexpr int kSumCtasPerSm = 3;                   // resident at 72 registers
 
 // (hi, lo) + x without losing the rounding error of hi + x, two dims at a time
 // (the additions are half of the kernel's instructions: paired ones halve them)
@@ -33,7 +34,7 @@ __device__ __forceinline__ void two_sum(uint64_t& hi, uint64_t& lo, uint64_t x) 
   hi = s;
 }
 
-__global__ void __launch_bounds__(kSumThreads) block_summary_kernel(SummaryParams p) {
+__global__ void __launch_bounds__(kSumThreads, kSumCtasPerSm) block_summary_kernel(SummaryParams p) {
   __shared__ int slot_sh[kMaxBlock];
   __shared__ __align__(16) float part[kSumGroups - 1][2][kDqk];
   __shared__ float amax_sh[3];
@@ -48,20 +49,26 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(SummaryParam
   const int from = p.from_len != nullptr ? max(0, __ldg(p.from_len + b)) : 0;
   if (from >= L) return;
   const int n_blocks = (L + p.block - 1) / p.block;
-  for (int j = from / p.block + blockIdx.x; j < n_blocks; j += gridDim.x) {
+  auto slot_of = [&](int j) {  // of this thread's position in block j
+    const int64_t pos = static_cast<int64_t>(j) * p.block + tid;
+    return tid < p.block && pos < L ? __ldg(p.slot_idx + static_cast<int64_t>(b) * p.slot_stride + pos) : -1;
+  };
+  const int j0 = from / p.block + blockIdx.x;
+  int slot = slot_of(j0);
+  for (int j = j0; j < n_blocks; j += gridDim.x) {
     const int pos0 = j * p.block, n = min(p.block, L - pos0);
     if (tid == 0) bad_sh[0] = bad_sh[1] = 0;
     __syncthreads();
     if (tid < n) {
-      int s = __ldg(p.slot_idx + static_cast<int64_t>(b) * p.slot_stride + pos0 + tid);
-      if (s < 0 || s >= p.pool_slots) {
+      if (slot < 0 || slot >= p.pool_slots) {
         atomicOr(p.status, kStatusBadSlot);
         atomicAdd(&bad_sh[0], 1);
-        s = -1;
+        slot = -1;
       }
-      slot_sh[tid] = s;
+      slot_sh[tid] = slot;
     }
     __syncthreads();
+    slot = slot_of(j + gridDim.x);  // the next block's, while this one's rows travel
     uint64_t hi2[4], lo2[4];
 #pragma unroll
     for (int d = 0; d < 4; ++d) hi2[d] = lo2[d] = 0;
@@ -92,6 +99,8 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(SummaryParam
     __syncthreads();
     // group 0 (72 threads) adds the others' sums and finishes the block
     const int count = n - bad_sh[0];
+    const bool pow2 = (count & (count - 1)) == 0;
+    const float inv = 1.f / static_cast<float>(max(count, 1));
     float mean[8], am = 0.f;
     bool finite = true;
     if (g == 0) {
@@ -108,7 +117,11 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(SummaryParam
       }
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
-        mean[d] = count > 0 ? static_cast<float>((static_cast<double>(hi[d]) + lo[d]) / count) : 0.f;
+        // a power of two rows: hi + lo rounds once and the scaling is exact
+        // (64-bit division is slow here and would cost more than the sums)
+        float m = __fadd_rn(hi[d], lo[d]) * inv;
+        if (!pow2 || (fabsf(m) < 1e-30f && m != 0.f)) m = static_cast<float>((static_cast<double>(hi[d]) + lo[d]) / count);
+        mean[d] = count > 0 ? m : 0.f;
         // an infinite row leaves a NaN in the carried error: any non-finite sum counts as such
         finite = finite && fabsf(mean[d]) < CUDART_INF_F;
         am = fmaxf(am, fabsf(mean[d]));
@@ -154,7 +167,7 @@ cudaError_t launch_block_summary(const SummaryParams& p, int batch, int sm_count
   if (batch == 0 || p.blocks == 0) return cudaSuccess;
   // blocks of a request are dealt to at most enough CTAs to fill the GPU: how
   // many are touched (from_len) is known on the device only
-  const int64_t fill = (int64_t(sm_count) * 8 + batch - 1) / batch;
+  const int64_t fill = (int64_t(sm_count) * kSumCtasPerSm + batch - 1) / batch;
   const unsigned gx = static_cast<unsigned>(p.blocks < fill ? p.blocks : fill);
   block_summary_kernel<<<dim3(gx, batch), kSumThreads, 0, stream>>>(p);
   return cudaGetLastError();

@@ -5,7 +5,9 @@
 // lower position; what is kept stays in order.  One cluster of CTAs per request,
 // CTA r holding the r-th share of the positions:
 //   1. three digit histograms of the unprotected positions' weights, summed over
-//      the cluster through distributed shared memory, give the weight of the last
+//      the cluster through distributed shared memory (each CTA adds up its share
+//      of the bins and hands the totals to all: every CTA reading every
+//      histogram took 18,000 cycles a pass), give the weight of the last
 //      position kept (T) and how many of the positions tied at T are kept;
 //   2. the histograms also say how many of a CTA's own positions lie above and at
 //      T; prefix sums over the cluster say where its kept and freed entries start;
@@ -33,6 +35,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int
   __shared__ int hist[kDigits][kBins];
   __shared__ int tmp[2 * kEvThreads / 32 + 4];
   __shared__ int tile_gt[kEvItems * 32], tile_eq[kEvItems * 32];
+  __shared__ int total[kBins];                    // the cluster's histogram of a pass
   __shared__ int own[2];                          // this CTA's positions kept for sure, at T
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank()), ctas = gridDim.x;  // one cluster spans x
@@ -74,12 +77,16 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int
         count_key(hist[pass], live ? order_key_bits(bits_of(i)) : 0u, T, pass, live);
       }
       cluster_sync();  // every CTA's histogram of this pass is complete
-      const BinResult r = find_bin<kEvThreads>(want, [&](int x) {
-        int n = 0;
-        const uint32_t a = smem_u32(&hist[pass][x]);
-        for (int c = 0; c < ctas; ++c) n += ld_shared_cluster_b32(mapa_shared(a, c));
-        return n;
-      }, hist[pass], tmp);
+      // bins [rank seg, + seg) are added up here: `parts` threads a bin, which
+      // share the CTAs to read from and, the sum known, to write to
+      const int seg = kBins / ctas, parts = kEvThreads / seg;
+      const int bin = rank * seg + tid / parts, part = tid % parts;
+      int n = 0;
+      for (int c = part; c < ctas; c += parts) n += ld_shared_cluster_b32(mapa_shared(smem_u32(&hist[pass][bin]), c));
+      for (int off = 1; off < parts; off <<= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+      for (int c = part; c < ctas; c += parts) st_shared_cluster_b32(mapa_shared(smem_u32(&total[bin]), c), n);
+      cluster_sync();  // the totals have arrived
+      const BinResult r = find_bin<kEvThreads>(want, [&](int x) { return total[x]; }, hist[pass], tmp);
       T |= static_cast<uint32_t>(r.bin) << digit_shift(pass);
       want -= r.above;
       gt += r.own_above;

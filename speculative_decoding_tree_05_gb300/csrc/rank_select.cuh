@@ -19,21 +19,19 @@ __host__ __device__ constexpr uint32_t above_mask(int pass) {
 }
 
 // Counts `key` in hist if it matches `prefix` above the pass's digit; a whole
-// warp calls it.  The lanes that share the first counted lane's bin are added in
-// one atomic: equal weights (zeros, ties) would otherwise serialise on one bin.
+// warp calls it.  Equal weights (zeros, ties) would serialise on one bin: a
+// warp whose counted lanes all share one bin adds them in one atomic.
 __device__ __forceinline__ void count_key(int* hist, uint32_t key, uint32_t prefix, int pass, bool live) {
   const bool in = live && (key & above_mask(pass)) == prefix;
   const uint32_t vote = __ballot_sync(0xffffffffu, in);
   if (vote == 0) return;
   const uint32_t bin = (key >> digit_shift(pass)) & digit_mask(pass);
-  const int lead = __ffs(vote) - 1;
-  const uint32_t lead_bin = __shfl_sync(0xffffffffu, bin, lead);
-  const uint32_t same = __ballot_sync(0xffffffffu, in && bin == lead_bin);
-  const int lane = threadIdx.x & 31;
-  if (lane == lead)
-    atomicAdd(&hist[bin], __popc(same));
-  else if (in && !((same >> lane) & 1u))
+  const uint32_t lead_bin = __shfl_sync(0xffffffffu, bin, __ffs(vote) - 1);
+  if (__all_sync(0xffffffffu, !in || bin == lead_bin)) {
+    if ((threadIdx.x & 31) == static_cast<unsigned>(__ffs(vote) - 1)) atomicAdd(&hist[bin], __popc(vote));
+  } else if (in) {
     atomicAdd(&hist[bin], 1);
+  }
 }
 
 struct BinResult {
