@@ -57,17 +57,16 @@ __global__ void __launch_bounds__(kQuWarps * 32) quant_rows_kernel(QuantParams p
 }
 
 constexpr int kTkCached = 16384;  // scores kept in shared memory
-constexpr int kTkItems = 4;       // scores per thread and step of the ordered pass
 
 // One CTA per node: the digit select of rank_select.cuh over its scores, then
 // the chosen blocks in ascending order.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int cached) {
   constexpr int kWarps = kThreads / 32;
-  extern __shared__ uint32_t bits_sh[];
+  extern __shared__ uint32_t keys_sh[];
   __shared__ int hist[kDigits][kBins];
-  __shared__ int tmp[2 * kWarps + 4];
-  __shared__ int cnt_gt[kTkItems * kWarps], cnt_eq[kTkItems * kWarps];
+  __shared__ int tmp[kWarps + 2];
+  __shared__ int warp_gt[32], warp_eq[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.x, b = blockIdx.y;
   int L = __ldg(p.prefix_len + b);
@@ -97,79 +96,40 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
   const bool in_sh = n <= cached;
   if (in_sh) {
 #pragma unroll 4
-    for (int i = tid; i < n; i += kThreads) bits_sh[i] = __float_as_uint(__ldcg(score + i));
+    for (int i = tid; i < n; i += kThreads) keys_sh[i] = order_key_bits(__float_as_uint(__ldcg(score + i)));
   }
+  if (tid < 32) warp_gt[tid] = warp_eq[tid] = 0;
   __syncthreads();
-  auto key_of = [&](int i) { return order_key_bits(in_sh ? bits_sh[i] : __float_as_uint(__ldcg(score + i))); };
+  auto key_of = [&](int i) { return in_sh ? keys_sh[i] : order_key_bits(__float_as_uint(__ldcg(score + i))); };
   uint32_t T = 0;
   int want = need;
+#pragma unroll
   for (int pass = 0; pass < kDigits; ++pass) {
-#pragma unroll 2
-    for (int i0 = 0; i0 < n; i0 += kThreads) {
-      const int i = i0 + tid;
-      const bool live = i >= lo && i < hi;
-      count_key(hist[pass], live ? key_of(i) : 0u, T, pass, live);
-    }
+#pragma unroll 4
+    for (int i = lo + tid; i < hi; i += kThreads) count_key(hist[pass], key_of(i), T, pass);
     __syncthreads();
-    const BinResult r = find_bin<kThreads>(want, [&](int x) { return hist[pass][x]; }, hist[pass], tmp);
-    T |= static_cast<uint32_t>(r.bin) << digit_shift(pass);
-    want -= r.above;
+    const int2 r = find_bin<kThreads>(want, hist[pass], tmp);
+    T |= static_cast<uint32_t>(r.x) << digit_shift(pass);
+    want -= r.y;
   }
   const int ties = want;
-  int gt_base = 0, eq_base = 0;
-  for (int i0 = 0; i0 < n; i0 += kThreads * kTkItems) {
-    int c[kTkItems];
-#pragma unroll
-    for (int k = 0; k < kTkItems; ++k) {
-      const int i = i0 + k * kThreads + tid;
-      c[k] = 0;
-      if (i < n) {
-        const uint32_t key = key_of(i);
-        c[k] = i < lo || i >= hi || key > T ? 2 : (key == T ? 1 : 0);
-      }
-      const uint32_t mg = __ballot_sync(0xffffffffu, c[k] == 2), me = __ballot_sync(0xffffffffu, c[k] == 1);
-      if (lane == 0) {
-        cnt_gt[k * kWarps + warp] = __popc(mg);
-        cnt_eq[k * kWarps + warp] = __popc(me);
-      }
-    }
-    __syncthreads();
-    if (warp < 2) {  // exclusive prefix of the (item, warp) counts
-      int* cnt = warp == 0 ? cnt_gt : cnt_eq;
-      constexpr int kEach = kTkItems * kWarps / 32;
-      int v[kEach], sum = 0;
-#pragma unroll
-      for (int k = 0; k < kEach; ++k) {
-        v[k] = cnt[lane * kEach + k];
-        sum += v[k];
-      }
-      int incl = sum;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
-      }
-      int run = incl - sum;
-#pragma unroll
-      for (int k = 0; k < kEach; ++k) {
-        cnt[lane * kEach + k] = run;
-        run += v[k];
-      }
-      if (lane == 31) tmp[warp] = run;
-    }
-    __syncthreads();
-    const uint32_t lt = (1u << lane) - 1u;
-#pragma unroll
-    for (int k = 0; k < kTkItems; ++k) {
-      const uint32_t mg = __ballot_sync(0xffffffffu, c[k] == 2), me = __ballot_sync(0xffffffffu, c[k] == 1);
-      const int g = gt_base + cnt_gt[k * kWarps + warp] + __popc(mg & lt);
-      const int e = eq_base + cnt_eq[k * kWarps + warp] + __popc(me & lt);
-      if (c[k] == 2 || (c[k] == 1 && e < ties)) out[g + min(e, ties)] = i0 + k * kThreads + tid;
-    }
-    gt_base += tmp[0];
-    eq_base += tmp[1];
-    __syncthreads();
+  auto klass = [&](int i) -> int {
+    if (i < lo || i >= hi) return 2;
+    const uint32_t k = key_of(i);
+    return k > T ? 2 : (k == T ? 1 : 0);
+  };
+  const WarpRun run = warp_run(0, n, kWarps, warp);
+  const int2 mine = count_run(run, klass);
+  if (lane == 0) {
+    warp_gt[warp] = mine.x;
+    warp_eq[warp] = mine.y;
   }
+  __syncthreads();
+  const int g = __reduce_add_sync(0xffffffffu, lane < warp ? warp_gt[lane] : 0);
+  const int e = __reduce_add_sync(0xffffffffu, lane < warp ? warp_eq[lane] : 0);
+  emit_run(run, g, e, ties, klass, [&](int i, bool kept, int at) {
+    if (kept) out[at] = i;
+  });
 }
 
 // Threads per node: 256 up to 1024 blocks (four scores a thread), 1024 beyond.

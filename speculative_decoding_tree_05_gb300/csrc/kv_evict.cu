@@ -4,18 +4,18 @@
 // the last `recent` rank before all others, then the larger weight, then the
 // lower position; what is kept stays in order.  One cluster of CTAs per request,
 // CTA r holding the r-th share of the positions:
-//   1. three digit histograms of the unprotected positions' weights, summed over
-//      the cluster through distributed shared memory (each CTA adds up its share
-//      of the bins and hands the totals to all: every CTA reading every
-//      histogram took 18,000 cycles a pass), give the weight of the last
-//      position kept (T) and how many of the positions tied at T are kept;
-//   2. the histograms also say how many of a CTA's own positions lie above and at
-//      T; prefix sums over the cluster say where its kept and freed entries start;
-//   3. a pass in position order writes both lists (ballots and one scan a tile).
-// The weights are read from memory once and stay in shared memory where they
-// fit.  The work is a few bytes per position, so the time is the latency of
-// these dependent steps, not bandwidth, until the batch fills the GPU: small
-// batches take clusters of 16.
+//   1. three digit histograms of the unprotected positions' weights give the
+//      weight of the last position kept (T) and how many of the positions tied at
+//      T are kept.  Each CTA adds the bins that it filled to every CTA's total
+//      through distributed shared memory: one cluster barrier a digit (every CTA
+//      reading every histogram took 18,000 cycles a digit, this 3,000);
+//   2. every warp counts what it keeps of a run of consecutive positions, and
+//      prefix sums over the CTA and the cluster say where its entries start;
+//   3. the warps write both lists in position order, without further barriers.
+// The weights are read once for the ranking and stay in shared memory, as order
+// keys, where they fit.  The work is a few bytes per position, so the time is
+// the latency of these dependent steps, not bandwidth, until the batch fills the
+// GPU: small batches take clusters of 16.
 #include <cuda_runtime.h>
 #include "cache_ops.cuh"
 #include "ptx.cuh"
@@ -26,17 +26,20 @@ namespace {
 
 constexpr int kEvThreads = 1024;
 constexpr int kEvMaxCluster = 16;
-constexpr int kEvItems = 8;                       // positions per thread and tile of the ordered pass
-constexpr int kEvTile = kEvThreads * kEvItems;
-constexpr int kEvMaxCached = 40960;               // weights a CTA keeps in shared memory
+constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvMaxCached = 40960;               // order keys a CTA keeps in shared memory
+
+struct EvictShared {
+  int hist[kBins];            // this CTA's histogram of a digit
+  int total[kDigits][kBins];  // the cluster's
+  int tmp[kEvWarps + 2];
+  int warp_gt[kEvWarps], warp_eq[kEvWarps];
+  int own[2];                 // this CTA's positions kept for sure, at T
+};
 
 __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int cached) {
-  extern __shared__ uint32_t bits_sh[];           // [cached] the weights of this CTA's share
-  __shared__ int hist[kDigits][kBins];
-  __shared__ int tmp[2 * kEvThreads / 32 + 4];
-  __shared__ int tile_gt[kEvItems * 32], tile_eq[kEvItems * 32];
-  __shared__ int total[kBins];                    // the cluster's histogram of a pass
-  __shared__ int own[2];                          // this CTA's positions kept for sure, at T
+  extern __shared__ uint32_t keys_sh[];           // [cached] order keys of this CTA's share
+  __shared__ EvictShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank()), ctas = gridDim.x;  // one cluster spans x
   const int b = blockIdx.y;
@@ -55,136 +58,83 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int
   const int share = (L + ctas - 1) / ctas;
   const int begin = min(L, rank * share), end = min(L, begin + share);
 
-  for (int i = tid; i < kDigits * kBins; i += kEvThreads) (&hist[0][0])[i] = 0;
+  for (int i = tid; i < kDigits * kBins; i += kEvThreads) (&sh.total[0][0])[i] = 0;
+  cluster_arrive();  // this CTA's totals may be added to
   if (cached > 0) {
 #pragma unroll 8
-    for (int i = begin + tid; i < end; i += kEvThreads) bits_sh[i - begin] = __float_as_uint(__ldg(weight + i));
+    for (int i = begin + tid; i < end; i += kEvThreads) keys_sh[i - begin] = order_key_bits(__float_as_uint(__ldg(weight + i)));
   }
-  __syncthreads();
-  auto bits_of = [&](int i) { return cached > 0 ? bits_sh[i - begin] : __float_as_uint(__ldg(weight + i)); };
+  auto key_of = [&](int i) { return cached > 0 ? keys_sh[i - begin] : order_key_bits(__float_as_uint(__ldg(weight + i))); };
+  cluster_wait();
 
   uint32_t T = 0;   // order key of the last unprotected position kept
   int ties = 0;     // positions at T that are kept
-  int gt = 0, eq = 0;
   const bool select = need > 0 && keep < L;       // the same in every CTA of the cluster
   if (select) {
+    const int from = max(begin, lo), to = min(end, hi);
     int want = need;
+#pragma unroll
     for (int pass = 0; pass < kDigits; ++pass) {
+      for (int i = tid; i < kBins; i += kEvThreads) sh.hist[i] = 0;
+      __syncthreads();
 #pragma unroll 4
-      for (int i0 = begin; i0 < end; i0 += kEvThreads) {
-        const int i = i0 + tid;
-        const bool live = i < end && i >= lo && i < hi;
-        count_key(hist[pass], live ? order_key_bits(bits_of(i)) : 0u, T, pass, live);
+      for (int i = from + tid; i < to; i += kEvThreads) count_key(sh.hist, key_of(i), T, pass);
+      __syncthreads();
+      for (int i = tid; i < kBins; i += kEvThreads) {
+        const int n = sh.hist[i];
+        if (n != 0)
+          for (int c = 0; c < ctas; ++c) red_shared_cluster_add(mapa_shared(smem_u32(&sh.total[pass][i]), c), n);
       }
-      cluster_sync();  // every CTA's histogram of this pass is complete
-      // bins [rank seg, + seg) are added up here: `parts` threads a bin, which
-      // share the CTAs to read from and, the sum known, to write to
-      const int seg = kBins / ctas, parts = kEvThreads / seg;
-      const int bin = rank * seg + tid / parts, part = tid % parts;
-      int n = 0;
-      for (int c = part; c < ctas; c += parts) n += ld_shared_cluster_b32(mapa_shared(smem_u32(&hist[pass][bin]), c));
-      for (int off = 1; off < parts; off <<= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
-      for (int c = part; c < ctas; c += parts) st_shared_cluster_b32(mapa_shared(smem_u32(&total[bin]), c), n);
-      cluster_sync();  // the totals have arrived
-      const BinResult r = find_bin<kEvThreads>(want, [&](int x) { return total[x]; }, hist[pass], tmp);
-      T |= static_cast<uint32_t>(r.bin) << digit_shift(pass);
-      want -= r.above;
-      gt += r.own_above;
-      eq = r.own_in;
+      cluster_sync();  // every CTA's counts have arrived
+      const int2 r = find_bin<kEvThreads>(want, sh.total[pass], sh.tmp);
+      T |= static_cast<uint32_t>(r.x) << digit_shift(pass);
+      want -= r.y;
     }
     ties = want;
   }
   // protected positions that stay: all of them, or the lowest `keep`
   const int held = min(prot, keep), held_lo = min(lo, held), held_hi = hi + (held - held_lo);
-  auto within = [&](int x0, int x1) { return max(0, min(end, x1) - max(begin, x0)); };
-  gt += within(0, held_lo) + within(hi, held_hi);
-  if (keep == L) gt = end - begin;
-  // 2: kept, 1: tied at T, 0: freed
-  auto klass = [&](int i, uint32_t bits) -> int {
+  auto klass = [&](int i) -> int {
     if (keep == L || i < held_lo || (i >= hi && i < held_hi)) return 2;
     if (!select || i < lo || i >= hi) return 0;
-    const uint32_t k = order_key_bits(bits);
+    const uint32_t k = key_of(i);
     return k > T ? 2 : (k == T ? 1 : 0);
   };
 
-  if (tid == 0) {
-    own[0] = gt;
-    own[1] = eq;
+  __syncthreads();
+  const WarpRun run = warp_run(begin, end, kEvWarps, warp);
+  const int2 mine = count_run(run, klass);
+  if (lane == 0) {
+    sh.warp_gt[warp] = mine.x;
+    sh.warp_eq[warp] = mine.y;
+  }
+  __syncthreads();
+  const int wg = sh.warp_gt[lane], we = sh.warp_eq[lane];
+  int g = __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0), e = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0);
+  if (warp == 0) {
+    const int all_g = __reduce_add_sync(0xffffffffu, wg), all_e = __reduce_add_sync(0xffffffffu, we);
+    if (lane == 0) {
+      sh.own[0] = all_g;
+      sh.own[1] = all_e;
+    }
   }
   cluster_sync();
-  int gt_base = 0, eq_base = 0;
   {
-    const int g = lane < rank ? ld_shared_cluster_b32(mapa_shared(smem_u32(&own[0]), lane)) : 0;
-    const int e = lane < rank ? ld_shared_cluster_b32(mapa_shared(smem_u32(&own[1]), lane)) : 0;
-    gt_base = __reduce_add_sync(0xffffffffu, g);
-    eq_base = __reduce_add_sync(0xffffffffu, e);
+    const int pg = lane < rank ? ld_shared_cluster_b32(mapa_shared(smem_u32(&sh.own[0]), lane)) : 0;
+    const int pe = lane < rank ? ld_shared_cluster_b32(mapa_shared(smem_u32(&sh.own[1]), lane)) : 0;
+    g += __reduce_add_sync(0xffffffffu, pg);
+    e += __reduce_add_sync(0xffffffffu, pe);
   }
   cluster_arrive();  // this thread no longer reads a peer's shared memory
-
-  for (int t0 = begin; t0 < end; t0 += kEvTile) {
-    int c[kEvItems], slot[kEvItems];
-    uint32_t w[kEvItems];
-#pragma unroll
-    for (int k = 0; k < kEvItems; ++k) {
-      const int i = t0 + k * kEvThreads + tid;
-      slot[k] = i < end ? __ldg(p.slot_idx + row + i) : 0;
-      w[k] = i < end ? bits_of(i) : 0;
+  emit_run(run, g, e, ties, klass, [&](int i, bool kept, int at) {
+    const int slot = __ldg(p.slot_idx + row + i);
+    if (kept) {
+      p.slot_out[row + at] = slot;
+      p.weight_out[row + at] = __ldg(weight + i);
+    } else {
+      p.freed[row + i - at] = slot;
     }
-#pragma unroll
-    for (int k = 0; k < kEvItems; ++k) {
-      const int i = t0 + k * kEvThreads + tid;
-      c[k] = i < end ? klass(i, w[k]) : -1;
-      const uint32_t mg = __ballot_sync(0xffffffffu, c[k] == 2), me = __ballot_sync(0xffffffffu, c[k] == 1);
-      if (lane == 0) {
-        tile_gt[k * 32 + warp] = __popc(mg);
-        tile_eq[k * 32 + warp] = __popc(me);
-      }
-    }
-    __syncthreads();
-    if (warp < 2) {  // exclusive prefix of the (item, warp) counts, in position order
-      int* t = warp == 0 ? tile_gt : tile_eq;
-      int v[kEvItems], sum = 0;  // lane l scans entries [8 l, 8 l + 8)
-#pragma unroll
-      for (int k = 0; k < kEvItems; ++k) {
-        v[k] = t[lane * kEvItems + k];
-        sum += v[k];
-      }
-      int incl = sum;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
-      }
-      int run = incl - sum;
-#pragma unroll
-      for (int k = 0; k < kEvItems; ++k) {
-        t[lane * kEvItems + k] = run;
-        run += v[k];
-      }
-      if (lane == 31) tmp[warp] = run;
-    }
-    __syncthreads();
-    const uint32_t lt = (1u << lane) - 1u;
-#pragma unroll
-    for (int k = 0; k < kEvItems; ++k) {
-      const int i = t0 + k * kEvThreads + tid;
-      const uint32_t mg = __ballot_sync(0xffffffffu, c[k] == 2), me = __ballot_sync(0xffffffffu, c[k] == 1);
-      if (i < end) {
-        const int g = gt_base + tile_gt[k * 32 + warp] + __popc(mg & lt);
-        const int e = eq_base + tile_eq[k * 32 + warp] + __popc(me & lt);
-        const int kept_before = g + min(e, ties);
-        if (c[k] == 2 || (c[k] == 1 && e < ties)) {
-          p.slot_out[row + kept_before] = slot[k];
-          p.weight_out[row + kept_before] = __uint_as_float(w[k]);
-        } else {
-          p.freed[row + i - kept_before] = slot[k];
-        }
-      }
-    }
-    gt_base += tmp[0];
-    eq_base += tmp[1];
-    __syncthreads();
-  }
+  });
   if (rank == 0 && tid == 0) p.len_out[b] = keep;
   cluster_wait();  // no CTA leaves while a peer may still read its counts
 }

@@ -166,6 +166,11 @@ __device__ __forceinline__ int ld_shared_cluster_b32(uint32_t remote_addr) {
   return v;
 }
 
+// Add to a word of a peer CTA's shared memory (visible to the peer after a cluster barrier).
+__device__ __forceinline__ void red_shared_cluster_add(uint32_t remote_addr, int v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(remote_addr), "r"(v) : "memory");
+}
+
 // 4-byte variant of st_async_v4.
 __device__ __forceinline__ void st_async_b32(uint32_t remote_addr, uint32_t v, uint32_t remote_bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(remote_addr), "r"(v),
