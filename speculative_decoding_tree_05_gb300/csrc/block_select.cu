@@ -94,13 +94,14 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
   for (int i = tid; i < kDigits * kBins; i += kThreads) (&hist[0][0])[i] = 0;
   grid_dep_wait();  // the scores
   const bool in_sh = n <= cached;
+  auto load_key = [&](int i) { return i < lo || i >= hi ? 0xffffffffu : order_key_bits(__float_as_uint(__ldcg(score + i))); };
   if (in_sh) {
 #pragma unroll 4
-    for (int i = tid; i < n; i += kThreads) keys_sh[i] = order_key_bits(__float_as_uint(__ldcg(score + i)));
+    for (int i = tid; i < n; i += kThreads) keys_sh[i] = load_key(i);
   }
   if (tid < 32) warp_gt[tid] = warp_eq[tid] = 0;
   __syncthreads();
-  auto key_of = [&](int i) { return in_sh ? keys_sh[i] : order_key_bits(__float_as_uint(__ldcg(score + i))); };
+  auto key_of = [&](int i) { return in_sh ? keys_sh[i] : load_key(i); };
   uint32_t T = 0;
   int want = need;
 #pragma unroll
@@ -108,18 +109,13 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
 #pragma unroll 4
     for (int i = lo + tid; i < hi; i += kThreads) count_key(hist[pass], key_of(i), T, pass);
     __syncthreads();
-    const int2 r = find_bin<kThreads>(want, hist[pass], tmp);
+    const int2 r = find_bin<kThreads>(want, [&](int x) { return hist[pass][x]; }, tmp);
     T |= static_cast<uint32_t>(r.x) << digit_shift(pass);
     want -= r.y;
   }
   const int ties = want;
-  auto klass = [&](int i) -> int {
-    if (i < lo || i >= hi) return 2;
-    const uint32_t k = key_of(i);
-    return k > T ? 2 : (k == T ? 1 : 0);
-  };
   const WarpRun run = warp_run(0, n, kWarps, warp);
-  const int2 mine = count_run(run, klass);
+  const int2 mine = count_run(run, T, key_of);
   if (lane == 0) {
     warp_gt[warp] = mine.x;
     warp_eq[warp] = mine.y;
@@ -127,8 +123,8 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
   __syncthreads();
   const int g = __reduce_add_sync(0xffffffffu, lane < warp ? warp_gt[lane] : 0);
   const int e = __reduce_add_sync(0xffffffffu, lane < warp ? warp_eq[lane] : 0);
-  emit_run(run, g, e, ties, klass, [&](int i, bool kept, int at) {
-    if (kept) out[at] = i;
+  emit_run<int>(run, T, g, e, ties, key_of, [](int i) { return i; }, [&](int, int v, bool kept, int at) {
+    if (kept) out[at] = v;
   });
 }
 

@@ -6,9 +6,10 @@
 // CTA r holding the r-th share of the positions:
 //   1. three digit histograms of the unprotected positions' weights give the
 //      weight of the last position kept (T) and how many of the positions tied at
-//      T are kept.  Each CTA adds the bins that it filled to every CTA's total
-//      through distributed shared memory: one cluster barrier a digit (every CTA
-//      reading every histogram took 18,000 cycles a digit, this 3,000);
+//      T are kept.  Each CTA adds the bins that it filled to the totals of their
+//      owner (a share of the bins each) through distributed shared memory and
+//      reads the totals back from the owners: one cluster barrier a digit (every
+//      CTA reading every histogram took 18,000 cycles a digit, this 3,000);
 //   2. every warp counts what it keeps of a run of consecutive positions, and
 //      prefix sums over the CTA and the cluster say where its entries start;
 //   3. the warps write both lists in position order, without further barriers.
@@ -31,7 +32,7 @@ constexpr int kEvMaxCached = 40960;               // order keys a CTA keeps in s
 
 struct EvictShared {
   int hist[kBins];            // this CTA's histogram of a digit
-  int total[kDigits][kBins];  // the cluster's
+  int total[kDigits][kBins];  // the cluster's, in the bins that this CTA owns
   int tmp[kEvWarps + 2];
   int warp_gt[kEvWarps], warp_eq[kEvWarps];
   int own[2];                 // this CTA's positions kept for sure, at T
@@ -58,20 +59,30 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int
   const int share = (L + ctas - 1) / ctas;
   const int begin = min(L, rank * share), end = min(L, begin + share);
 
+  // protected positions that stay: all of them, or the lowest `keep`
+  const int held = min(prot, keep), held_lo = min(lo, held), held_hi = hi + (held - held_lo);
+  // order keys, protected positions above (they stay) or below (they do not) every weight's
+  auto load_key = [&](int i) -> uint32_t {
+    const uint32_t k = order_key_bits(__float_as_uint(__ldg(weight + i)));
+    if (i >= lo && i < hi) return k;
+    return i < held_lo || (i >= hi && i < held_hi) ? 0xffffffffu : 0u;
+  };
   for (int i = tid; i < kDigits * kBins; i += kEvThreads) (&sh.total[0][0])[i] = 0;
   cluster_arrive();  // this CTA's totals may be added to
   if (cached > 0) {
 #pragma unroll 8
-    for (int i = begin + tid; i < end; i += kEvThreads) keys_sh[i - begin] = order_key_bits(__float_as_uint(__ldg(weight + i)));
+    for (int i = begin + tid; i < end; i += kEvThreads) keys_sh[i - begin] = load_key(i);
   }
-  auto key_of = [&](int i) { return cached > 0 ? keys_sh[i - begin] : order_key_bits(__float_as_uint(__ldg(weight + i))); };
+  auto key_of = [&](int i) { return cached > 0 ? keys_sh[i - begin] : load_key(i); };
   cluster_wait();
 
-  uint32_t T = 0;   // order key of the last unprotected position kept
-  int ties = 0;     // positions at T that are kept
-  const bool select = need > 0 && keep < L;       // the same in every CTA of the cluster
+  // T: order key of the last unprotected position kept, `ties` of those at T stay
+  uint32_t T = need <= 0 && keep < L ? 0xfffffffeu : 0u;  // only the protected ones, or every position
+  int ties = 0;
+  const bool select = need > 0 && keep < L;  // the same in every CTA of the cluster
   if (select) {
     const int from = max(begin, lo), to = min(end, hi);
+    const int log_own = 31 - __clz(kBins / ctas);  // bins per owner
     int want = need;
 #pragma unroll
     for (int pass = 0; pass < kDigits; ++pass) {
@@ -82,28 +93,21 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int
       __syncthreads();
       for (int i = tid; i < kBins; i += kEvThreads) {
         const int n = sh.hist[i];
-        if (n != 0)
-          for (int c = 0; c < ctas; ++c) red_shared_cluster_add(mapa_shared(smem_u32(&sh.total[pass][i]), c), n);
+        if (n != 0) red_shared_cluster_add(mapa_shared(smem_u32(&sh.total[pass][i]), i >> log_own), n);
       }
       cluster_sync();  // every CTA's counts have arrived
-      const int2 r = find_bin<kEvThreads>(want, sh.total[pass], sh.tmp);
+      const int2 r = find_bin<kEvThreads>(want, [&](int x) {
+        return ld_shared_cluster_b32(mapa_shared(smem_u32(&sh.total[pass][x]), x >> log_own));
+      }, sh.tmp);
       T |= static_cast<uint32_t>(r.x) << digit_shift(pass);
       want -= r.y;
     }
     ties = want;
   }
-  // protected positions that stay: all of them, or the lowest `keep`
-  const int held = min(prot, keep), held_lo = min(lo, held), held_hi = hi + (held - held_lo);
-  auto klass = [&](int i) -> int {
-    if (keep == L || i < held_lo || (i >= hi && i < held_hi)) return 2;
-    if (!select || i < lo || i >= hi) return 0;
-    const uint32_t k = key_of(i);
-    return k > T ? 2 : (k == T ? 1 : 0);
-  };
 
   __syncthreads();
   const WarpRun run = warp_run(begin, end, kEvWarps, warp);
-  const int2 mine = count_run(run, klass);
+  const int2 mine = count_run(run, T, key_of);
   if (lane == 0) {
     sh.warp_gt[warp] = mine.x;
     sh.warp_eq[warp] = mine.y;
@@ -126,15 +130,16 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int
     e += __reduce_add_sync(0xffffffffu, pe);
   }
   cluster_arrive();  // this thread no longer reads a peer's shared memory
-  emit_run(run, g, e, ties, klass, [&](int i, bool kept, int at) {
-    const int slot = __ldg(p.slot_idx + row + i);
-    if (kept) {
-      p.slot_out[row + at] = slot;
-      p.weight_out[row + at] = __ldg(weight + i);
-    } else {
-      p.freed[row + i - at] = slot;
-    }
-  });
+  emit_run<int2>(run, T, g, e, ties, key_of,
+                 [&](int i) { return make_int2(__ldg(p.slot_idx + row + i), __float_as_int(__ldg(weight + i))); },
+                 [&](int i, int2 v, bool kept, int at) {
+                   if (kept) {
+                     p.slot_out[row + at] = v.x;
+                     p.weight_out[row + at] = __int_as_float(v.y);
+                   } else {
+                     p.freed[row + i - at] = v.x;
+                   }
+                 });
   if (rank == 0 && tid == 0) p.len_out[b] = keep;
   cluster_wait();  // no CTA leaves while a peer may still read its counts
 }

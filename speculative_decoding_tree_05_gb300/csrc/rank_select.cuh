@@ -25,17 +25,17 @@ __device__ __forceinline__ void count_key(int* hist, uint32_t key, uint32_t pref
 }
 
 // The bin of the want-th largest key (want >= 1), bins counted from the top, and
-// the keys in higher bins.  Every thread of the block (kThreads, a multiple of
+// the keys in higher bins; total(bin) is a bin's count.  Every thread of the block (kThreads, a multiple of
 // 32 that divides kBins) calls it.  tmp: kThreads / 32 + 2 ints of shared memory.
-template <int kThreads>
-__device__ __forceinline__ int2 find_bin(int want, const int* hist, int* tmp) {
+template <int kThreads, class TotalFn>
+__device__ __forceinline__ int2 find_bin(int want, TotalFn total, int* tmp) {
   constexpr int kPer = kBins / kThreads, kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int top = kBins - 1 - kPer * tid;  // thread t holds bins top, top - 1, ...
   int c[kPer], sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    c[i] = hist[top - i];
+    c[i] = total(top - i);
     sum += c[i];
   }
   int incl = sum;
@@ -60,8 +60,8 @@ __device__ __forceinline__ int2 find_bin(int want, const int* hist, int* tmp) {
   return make_int2(tmp[kWarps], tmp[kWarps + 1]);
 }
 
-// Ordered emission.  A warp owns a run of consecutive positions and classes each
-// (2: kept, 1: tied at the last weight kept, 0: not kept).
+// Ordered emission.  A warp owns a run of consecutive positions; a position is
+// kept if its key is above T, or at T among the first `ties` of those.
 struct WarpRun {
   int begin, end;  // positions
 };
@@ -72,34 +72,49 @@ __device__ __forceinline__ WarpRun warp_run(int begin, int end, int warps, int w
   r.end = min(end, r.begin + per);
   return r;
 }
-// Kept and tied positions of a run.
-template <class KlassFn>
-__device__ __forceinline__ int2 count_run(WarpRun r, KlassFn klass) {
+// Positions of a run above T and at T (keys of 0 lie below every T).
+template <class KeyFn>
+__device__ __forceinline__ int2 count_run(WarpRun r, uint32_t T, KeyFn key_of) {
   const int lane = threadIdx.x & 31;
   int g = 0, e = 0;
 #pragma unroll 4
-  for (int i0 = r.begin; i0 < r.end; i0 += 32) {
-    const int c = i0 + lane < r.end ? klass(i0 + lane) : 0;
-    g += __popc(__ballot_sync(0xffffffffu, c == 2));
-    e += __popc(__ballot_sync(0xffffffffu, c == 1));
+  for (int i = r.begin + lane; i < r.end; i += 32) {
+    const uint32_t k = key_of(i);
+    g += k > T;
+    e += k == T;
   }
-  return make_int2(g, e);
+  return make_int2(__reduce_add_sync(0xffffffffu, g), __reduce_add_sync(0xffffffffu, e));
 }
-// emit(position, kept, rank among the kept positions before it) for a run, with
-// g kept and e tied positions before the run, of which `ties` in all are kept.
-template <class KlassFn, class EmitFn>
-__device__ __forceinline__ void emit_run(WarpRun r, int g, int e, int ties, KlassFn klass, EmitFn emit) {
+// emit(position, value, kept, rank among the kept positions before it) for a run
+// with g positions above T and e at T before it; fetch(position) gives the value,
+// loaded for kEmitBatch positions at a time.
+constexpr int kEmitBatch = 6;
+template <class Value, class KeyFn, class FetchFn, class EmitFn>
+__device__ __forceinline__ void emit_run(WarpRun r, uint32_t T, int g, int e, int ties, KeyFn key_of, FetchFn fetch,
+                                         EmitFn emit) {
   const int lane = threadIdx.x & 31;
   const uint32_t lt = (1u << lane) - 1u;
-#pragma unroll 4
-  for (int i0 = r.begin; i0 < r.end; i0 += 32) {
-    const int i = i0 + lane;
-    const int c = i < r.end ? klass(i) : 0;
-    const uint32_t mg = __ballot_sync(0xffffffffu, c == 2), me = __ballot_sync(0xffffffffu, c == 1);
-    const int eb = e + __popc(me & lt);
-    if (i < r.end) emit(i, c == 2 || (c == 1 && eb < ties), g + __popc(mg & lt) + min(eb, ties));
-    g += __popc(mg);
-    e += __popc(me);
+  for (int i0 = r.begin; i0 < r.end; i0 += 32 * kEmitBatch) {
+    Value v[kEmitBatch];
+    uint32_t k[kEmitBatch];
+#pragma unroll
+    for (int u = 0; u < kEmitBatch; ++u) {
+      const int i = i0 + 32 * u + lane;
+      k[u] = 0;
+      if (i < r.end) {
+        v[u] = fetch(i);
+        k[u] = key_of(i);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kEmitBatch; ++u) {
+      const int i = i0 + 32 * u + lane;
+      const uint32_t mg = __ballot_sync(0xffffffffu, k[u] > T), me = __ballot_sync(0xffffffffu, k[u] == T && i < r.end);
+      const int eb = e + __popc(me & lt);
+      if (i < r.end) emit(i, v[u], k[u] > T || (k[u] == T && eb < ties), g + __popc(mg & lt) + min(eb, ties));
+      g += __popc(mg);
+      e += __popc(me);
+    }
   }
 }
 
