@@ -28,6 +28,7 @@ namespace {
 constexpr int kEvThreads = 1024;
 constexpr int kEvMaxCluster = 16;
 constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvBatch = 12;                      // weights in flight per thread
 constexpr int kEvMaxCached = 40960;               // order keys a CTA keeps in shared memory
 
 struct EvictShared {
@@ -62,18 +63,24 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int
   // protected positions that stay: all of them, or the lowest `keep`
   const int held = min(prot, keep), held_lo = min(lo, held), held_hi = hi + (held - held_lo);
   // order keys, protected positions above (they stay) or below (they do not) every weight's
-  auto load_key = [&](int i) -> uint32_t {
-    const uint32_t k = order_key_bits(__float_as_uint(__ldg(weight + i)));
-    if (i >= lo && i < hi) return k;
+  auto key_from = [&](int i, float w) -> uint32_t {
+    if (i >= lo && i < hi) return order_key_bits(__float_as_uint(w));
     return i < held_lo || (i >= hi && i < held_hi) ? 0xffffffffu : 0u;
   };
   for (int i = tid; i < kDigits * kBins; i += kEvThreads) (&sh.total[0][0])[i] = 0;
   cluster_arrive();  // this CTA's totals may be added to
   if (cached > 0) {
-#pragma unroll 8
-    for (int i = begin + tid; i < end; i += kEvThreads) keys_sh[i - begin] = load_key(i);
+    for (int i0 = begin + tid; i0 < end; i0 += kEvBatch * kEvThreads) {
+      float w[kEvBatch];
+#pragma unroll
+      for (int k = 0; k < kEvBatch; ++k)
+        if (i0 + k * kEvThreads < end) w[k] = __ldg(weight + i0 + k * kEvThreads);
+#pragma unroll
+      for (int k = 0; k < kEvBatch; ++k)
+        if (i0 + k * kEvThreads < end) keys_sh[i0 + k * kEvThreads - begin] = key_from(i0 + k * kEvThreads, w[k]);
+    }
   }
-  auto key_of = [&](int i) { return cached > 0 ? keys_sh[i - begin] : load_key(i); };
+  auto key_of = [&](int i) { return cached > 0 ? keys_sh[i - begin] : key_from(i, __ldg(weight + i)); };
   cluster_wait();
 
   // T: order key of the last unprotected position kept, `ties` of those at T stay
