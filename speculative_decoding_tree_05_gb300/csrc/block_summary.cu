@@ -99,8 +99,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtasPerSm) block_summary_kern
     __syncthreads();
     // group 0 (72 threads) adds the others' sums and finishes the block
     const int count = n - bad_sh[0];
-    const bool pow2 = (count & (count - 1)) == 0;
-    const float inv = 1.f / static_cast<float>(max(count, 1));
+    const float rows = static_cast<float>(max(count, 1));
     float mean[8], am = 0.f;
     bool finite = true;
     if (g == 0) {
@@ -117,10 +116,10 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtasPerSm) block_summary_kern
       }
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
-        // a power of two rows: hi + lo rounds once and the scaling is exact
-        // (64-bit division is slow here and would cost more than the sums)
-        float m = __fadd_rn(hi[d], lo[d]) * inv;
-        if (!pow2 || (fabsf(m) < 1e-30f && m != 0.f)) m = static_cast<float>((static_cast<double>(hi[d]) + lo[d]) / count);
+        // (hi + lo) / rows in fp32 pairs: the quotient of hi, and that of what is
+        // left of hi and lo (64-bit division is slow here and would cost more than the sums)
+        const float q = __fdiv_rn(hi[d], rows);
+        const float m = __fadd_rn(q, __fdiv_rn(__fadd_rn(__fmaf_rn(-q, rows, hi[d]), lo[d]), rows));
         mean[d] = count > 0 ? m : 0.f;
         // an infinite row leaves a NaN in the carried error: any non-finite sum counts as such
         finite = finite && fabsf(mean[d]) < CUDART_INF_F;

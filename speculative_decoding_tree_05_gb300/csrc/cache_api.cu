@@ -13,6 +13,7 @@ namespace ddt {
 namespace {
 
 constexpr int kScoreUnitTiles = 4;  // fixed cost of one score unit, in query tiles
+constexpr int kWeightSumTiles = 3;  // the launch that adds the shares' sums, in query tiles
 constexpr int kBlockUnitTiles = 4;  // fixed cost of one block-attention unit, in 64-key tiles
 
 int round32(int x) { return (x + 31) / 32 * 32; }
@@ -23,18 +24,20 @@ bool clear_status(void* workspace, cudaStream_t s) {
 
 // Key tiles, and the shares of the query tiles: with fewer key tiles than CTA
 // pairs the pairs left over take shares of the rows.  A unit costs its tiles plus
-// about kScoreUnitTiles (the gather of its keys and the pipeline's fill).
+// about kScoreUnitTiles (the gather of its keys and the pipeline's fill), sharing
+// itself split_tiles (the sum of the shares).
 struct ScoreGrid {
   int key_tiles, splits, units;
 };
-bool score_grid(int64_t batch, int64_t keys, int tiles, int sm_count, ScoreGrid* g) {
+bool score_grid(int64_t batch, int64_t keys, int tiles, int sm_count, int split_tiles, ScoreGrid* g) {
   const int64_t key_tiles = (keys + kScoreTileKeys - 1) / kScoreTileKeys;
   const int64_t all = batch * key_tiles, pairs = std::max(1, sm_count / 2);
   if (all > INT32_MAX / 64) return false;
   int64_t best = -1;
   int splits = 1;
   for (int s = 1; s <= std::min(tiles, 64); ++s) {
-    const int64_t cost = (all * s + pairs - 1) / pairs * ((tiles + s - 1) / s + kScoreUnitTiles);
+    const int64_t cost =
+        (all * s + pairs - 1) / pairs * ((tiles + s - 1) / s + kScoreUnitTiles) + (s > 1 ? split_tiles : 0);
     if (best < 0 || cost < best) {
       best = cost;
       splits = s;
@@ -64,7 +67,7 @@ int weight_layout(const ddt_dims* d, int32_t num_sel, int sm_count, WeightLayout
   if (rows * d->batch > INT32_MAX) return DDT_ERR_DIMS;
   w->tile_rows = weight_tile_rows(static_cast<int>(rows));
   w->tiles = static_cast<int>((rows + w->tile_rows - 1) / w->tile_rows);
-  if (!score_grid(d->batch, d->max_prefix_len, w->tiles, std::max(sm_count, 2), &w->grid)) return DDT_ERR_DIMS;
+  if (!score_grid(d->batch, d->max_prefix_len, w->tiles, std::max(sm_count, 2), kWeightSumTiles, &w->grid)) return DDT_ERR_DIMS;
   const size_t packed = num_sel > 0 ? size_t(rows) * d->batch : 0;
   w->q_off = kStatusBytes;
   w->lse_off = align_up(w->q_off + packed * kRowBytes, 256);
@@ -323,7 +326,7 @@ extern "C" int ddtree_block_select(const void* q, const void* summary, const flo
   p.tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
   ScoreGrid grid;
   // (a node of more heads spans tiles: its rows are not shared out)
-  if (!score_grid(p.batch, w.blocks, H <= kScoreTileRows ? p.tiles : 1, sms, &grid)) return DDT_ERR_DIMS;
+  if (!score_grid(p.batch, w.blocks, H <= kScoreTileRows ? p.tiles : 1, sms, 0, &grid)) return DDT_ERR_DIMS;
   p.key_tiles = grid.key_tiles;
   p.splits = grid.splits;
   p.units = grid.units;

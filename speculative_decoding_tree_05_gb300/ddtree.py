@@ -267,8 +267,9 @@ class SparseVerifier:
 
 def _need(device, **tensors):
     """Check tensors given as name=(tensor, dtype, shape): type, shape, contiguity and device."""
+    index = device.index
     for name, (t, dtype, shape) in tensors.items():
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                              f"{t.dtype} {tuple(t.shape)} on {t.device}"
                              + ("" if t.is_contiguous() else " (not contiguous)"))
@@ -279,8 +280,8 @@ class _On:
 
     def __init__(self, device):
         import torch
-        self.index = device.index
-        self.back = None if torch.cuda.current_device() == device.index else torch.cuda.current_device()
+        here = torch.cuda.current_device()
+        self.index, self.back = device.index, None if here == device.index else here
 
     def __enter__(self):
         if self.back is not None:
@@ -291,6 +292,11 @@ class _On:
         if self.back is not None:
             import torch
             torch.cuda.set_device(self.back)
+
+
+def _addr(t):
+    """A tensor's address as ctypes takes it (None: NULL); cheaper than a c_void_p a tensor."""
+    return None if t is None else t.data_ptr()
 
 
 def _cuda_device(device):
@@ -309,8 +315,8 @@ def _on_cuda(t, name):
 
 def _stream_of(device, stream):
     import torch
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle: building a Stream object costs as much as a launch
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 class KeyWeights:
@@ -360,9 +366,9 @@ class KeyWeights:
             checks["node_idx"] = (node_idx, torch.int32, (d.batch, sel))
         _need(self.device, **checks)
         with _On(self.device):
-            rc = self.lib.ddtree_kv_weight(_ptr(q), _ptr(kv_pool), _ptr(slot_idx), _ptr(prefix_len), _ptr(lse),
-                                           _ptr(node_idx), sel, float(sm_scale), float(decay), _ptr(weight),
-                                           _ptr(out), ctypes.byref(d), _ptr(self.workspace), self.workspace.numel(),
+            rc = self.lib.ddtree_kv_weight(_addr(q), _addr(kv_pool), _addr(slot_idx), _addr(prefix_len), _addr(lse),
+                                           _addr(node_idx), sel, float(sm_scale), float(decay), _addr(weight),
+                                           _addr(out), ctypes.byref(d), _addr(self.workspace), self.workspace.numel(),
                                            _stream_of(self.device, stream))
         _check(rc, "ddtree_kv_weight")
         return out
@@ -398,9 +404,9 @@ def kv_evict(weight, slot_idx, prefix_len, keep_len, sink=0, recent=0, slot_idx_
         raise ValueError("workspace must hold 256 bytes")
     dims = make_dims(B, 1, 1, 1, stride, stride if max_prefix_len is None else max_prefix_len)
     with _On(device):
-        rc = lib().ddtree_kv_evict(_ptr(weight), _ptr(slot_idx), _ptr(prefix_len), _ptr(keep_len), int(sink),
-                                   int(recent), _ptr(slot_idx_out), _ptr(weight_out), _ptr(prefix_len_out),
-                                   _ptr(freed), ctypes.byref(dims), _ptr(workspace), _stream_of(device, stream))
+        rc = lib().ddtree_kv_evict(_addr(weight), _addr(slot_idx), _addr(prefix_len), _addr(keep_len), int(sink),
+                                   int(recent), _addr(slot_idx_out), _addr(weight_out), _addr(prefix_len_out),
+                                   _addr(freed), ctypes.byref(dims), _addr(workspace), _stream_of(device, stream))
     _check(rc, "ddtree_kv_evict")
     return slot_idx_out, weight_out, prefix_len_out, freed
 
@@ -435,8 +441,8 @@ def block_summary(kv_pool, slot_idx, prefix_len, block, from_len=None, summary=N
     if workspace.numel() < 256:
         raise ValueError("workspace must hold 256 bytes")
     with _On(device):
-        rc = lib().ddtree_block_summary(_ptr(kv_pool), _ptr(slot_idx), _ptr(prefix_len), _ptr(from_len), int(block),
-                                        _ptr(summary), _ptr(scale), ctypes.byref(dims), _ptr(workspace),
+        rc = lib().ddtree_block_summary(_addr(kv_pool), _addr(slot_idx), _addr(prefix_len), _addr(from_len), int(block),
+                                        _addr(summary), _addr(scale), ctypes.byref(dims), _addr(workspace),
                                         _stream_of(device, stream))
     _check(rc, "ddtree_block_summary")
     return summary, scale
@@ -471,9 +477,9 @@ class BlockSelector:
               scale=(scale, torch.float32, (d.batch, self.blocks)), prefix_len=(prefix_len, torch.int32, (d.batch,)),
               out=(out, torch.int32, (d.batch, d.num_nodes, self.topk)))
         with _On(self.device):
-            rc = self.lib.ddtree_block_select(_ptr(q), _ptr(summary), _ptr(scale), _ptr(prefix_len), self.block,
-                                              self.topk, self.first, self.last, _ptr(out), ctypes.byref(d),
-                                              _ptr(self.workspace), self.workspace.numel(),
+            rc = self.lib.ddtree_block_select(_addr(q), _addr(summary), _addr(scale), _addr(prefix_len), self.block,
+                                              self.topk, self.first, self.last, _addr(out), ctypes.byref(d),
+                                              _addr(self.workspace), self.workspace.numel(),
                                               _stream_of(self.device, stream))
         _check(rc, "ddtree_block_select")
         return out
@@ -518,10 +524,10 @@ class BlockVerifier:
               block_idx=(block_idx, torch.int32, (B, T, self.topk)), out=(out, torch.bfloat16, (B, T, H, D_V)),
               lse=(lse, torch.float32, (B, T, H)))
         with _On(self.device):
-            rc = self.lib.ddtree_verify_attn_blocks(_ptr(q), _ptr(kv_pool), _ptr(slot_idx), _ptr(prefix_len),
-                                                    _ptr(tree_parent), _ptr(tree_slot_idx), _ptr(block_idx),
-                                                    self.block, self.topk, float(sm_scale), _ptr(out), _ptr(lse),
-                                                    ctypes.byref(d), _ptr(self.workspace), self.workspace.numel(),
+            rc = self.lib.ddtree_verify_attn_blocks(_addr(q), _addr(kv_pool), _addr(slot_idx), _addr(prefix_len),
+                                                    _addr(tree_parent), _addr(tree_slot_idx), _addr(block_idx),
+                                                    self.block, self.topk, float(sm_scale), _addr(out), _addr(lse),
+                                                    ctypes.byref(d), _addr(self.workspace), self.workspace.numel(),
                                                     _stream_of(self.device, stream))
         _check(rc, "ddtree_verify_attn_blocks")
         return out, lse
