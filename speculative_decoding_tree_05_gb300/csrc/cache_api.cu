@@ -258,7 +258,7 @@ extern "C" int ddtree_kv_evict(const float* weight, const int32_t* slot_idx, con
   p.sink = sink;
   p.recent = recent;
   p.status = static_cast<int32_t*>(workspace);
-  return launch_kv_evict(p, dims->batch, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
+  return launch_kv_evict(p, dims->batch, sms, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
 }
 
 extern "C" int ddtree_block_summary(const void* kv_pool, const int32_t* slot_idx, const int32_t* prefix_len,

@@ -81,7 +81,7 @@ struct EvictParams {
   int32_t* status;
 };
 cudaError_t configure_evict();
-cudaError_t launch_kv_evict(const EvictParams& p, int batch, cudaStream_t stream);
+cudaError_t launch_kv_evict(const EvictParams& p, int batch, int sm_count, cudaStream_t stream);
 
 // ---------------------------------------------------------------- block summaries and selection
 struct SummaryParams {

@@ -25,8 +25,8 @@
 namespace ddt {
 namespace {
 
-constexpr int kEvThreads = 1024;
 constexpr int kEvMaxCluster = 16;
+constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBatch = 12;                      // weights in flight per thread
 constexpr int kEvMaxCached = 40960;               // order keys a CTA keeps in shared memory
@@ -159,10 +159,13 @@ cudaError_t configure_evict() {
   return cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
-cudaError_t launch_kv_evict(const EvictParams& p, int batch, cudaStream_t stream) {
-  // 16 CTAs a request while the clusters of the batch fit the GPU side by side
-  // (at most 8 of 16 CTAs: clusters stay within a GPC), 8 beyond that
-  const int ctas = batch <= 8 ? kEvMaxCluster : 8;
+cudaError_t launch_kv_evict(const EvictParams& p, int batch, int sm_count, cudaStream_t stream) {
+  // One CTA (1024 threads, 64 registers) fills an SM.  The largest cluster, up to
+  // 16, with which the batch takes at most two rounds of the SMs: more CTAs a
+  // request shorten its steps, further rounds repeat their fixed costs (64
+  // requests of up to 131072: 81 us in clusters of 8, 60 us in clusters of 4).
+  int ctas = kEvMaxCluster;
+  while (ctas > 1 && int64_t(ctas) * batch > 2 * sm_count) ctas /= 2;
   const int64_t share = (int64_t(p.max_prefix_len) + ctas - 1) / ctas;
   const int cached = share <= kEvMaxCached ? static_cast<int>(share) : 0;
   cudaLaunchConfig_t cfg = {};

@@ -58,6 +58,14 @@ def test_sizes(n, sink, recent):
     assert run(w, [n, n // 2, max(1, n - 1)], [n // 2, n // 4 + 1, n], sink, recent) == 0
 
 
+def test_large_batches():
+    """More requests than the small-batch kernel takes, of very different lengths."""
+    rng = np.random.default_rng(7)
+    lens = [int(x) for x in rng.integers(0, 9000, 40)] + [9000, 1, 0]
+    w = rng.choice(rng.random(300, dtype=np.float32) ** 8, (len(lens), 9000))   # many ties
+    run(w, lens, [int(n * f) for n, f in zip(lens, rng.random(len(lens)) * 1.1)], 4, 64)
+
+
 def test_ties_and_special_values():
     rng = np.random.default_rng(1)
     n = 5000
