@@ -18,26 +18,35 @@
 // operand type, against row sums of the unrounded values: an error of half a
 // bf16 step per weight, averaged over the keys, below the bf16 rounding of out.
 //
-// Per CTA (416 threads), one unit = (group, split of its key tiles):
-//   warp 0      TMEM; one lane issues S(t) dim group by dim group as stage t
-//               lands, and P.V(t) when P(t) is written, whichever is ready
-//   warps 1-4   softmax: TMEM rows 16 at a time in the 16x256b shape (row r in
-//               lanes 4 r .. 4 r + 3), the running max per row in shared memory,
-//               raised (and O^T rescaled) only when a score exceeds it by 2^8
-//   warps 5-12  gather 64 keys per stage by 16-byte cp.async, two stages of four
-//               dim groups, each refilled as soon as its part of P.V is done
+// Per CTA (576 threads), one unit = (group, split of its key tiles):
+//   warp 0       TMEM; one lane issues S(t), dim group by dim group as stage t lands
+//   warps 1-8    softmax: 16 keys x 32 rows each, in the 16x256b shape (key r in
+//                lanes 4 r .. 4 r + 3), the running max per row in shared memory,
+//                raised (and O^T rescaled) only when a score exceeds it by 2^8
+//   warp 9       one lane issues P.V(t) when P(t) is written
+//   warps 10-17  gather 64 keys per stage, two stages of four dim groups, each
+//                refilled as soon as its part of P.V is done: warps 10-13 the first
+//                two groups (5 of 9 chunks) by 16-byte cp.async, warps 14-17 the
+//                others by TMA gather4 (85 cycles an instruction and warp), at the
+//                same time: an SM gathers about 24 B/clk either way and 34 both
+//                ways (L2-resident rows)
+// What bounds it: a stage lives from its load through S, the softmax and P.V, and
+// only two of them fit beside the query rows, so a tile takes half a stage's life.
 // A unit writes the normalised O and the log-sum-exp of its share; the
 // tail/merge kernel adds the tree part and merges the splits.
 #include <cuda_runtime.h>
 #include <math_constants.h>
+#include <type_traits>
 #include "cache_ops.cuh"
 #include "ptx.cuh"
 
 namespace ddt {
 namespace {
 
-constexpr int kBaThreads = 416;
-constexpr int kBaProducers = 256;
+constexpr int kBaThreads = 576;
+constexpr int kBaSoftmax = 256;
+constexpr int kBaCopiers = 128;                 // threads that gather the copied groups
+constexpr int kBaCopied = 2;                    // groups gathered by cp.async
 constexpr int kBaGroups = 4;                    // dims {512-575, 0-127}, {128-255}, {256-383}, {384-511}
 constexpr int kBaKeys = 64;
 constexpr int kBaRows = kBlockRows;             // 64
@@ -69,22 +78,31 @@ struct BaShared {
 };
 static_assert(sizeof(BaShared) <= 256, "barrier block");
 
-// 16 TMEM lanes x 64 columns over a warp: v[4 i + 2 h + e] = (lane L/4 + 8 h, column 8 i + 2 (L % 4) + e).
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
+// 16 TMEM lanes x 32 columns over a warp: v[4 i + 2 h + e] = (lane L/4 + 8 h, column 8 i + 2 (L % 4) + e).
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
-        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-        "=r"(r[30]), "=r"(r[31])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 8 consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 struct Group {
@@ -106,7 +124,7 @@ __device__ __forceinline__ Group group_of(const BlockAttnParams& p, int g) {
   return u;
 }
 
-__global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAttnParams p) {
+__global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_constant__ BlockAttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   BaShared& sh = *reinterpret_cast<BaShared*>(smem + kBaOffBar);
@@ -137,15 +155,16 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
   if (tid == 0) {
     for (int i = 0; i < kBaStages; ++i)
       for (int x = 0; x < kBaGroups; ++x) {
-        mbar_init(&sh.k_full[i][x], kBaProducers + (x == 0 ? 8 : 0));  // group 0 carries the key masks
+        // every thread's cp.async (group 0: and each warp's key masks), or two warps' arrivals with their bytes
+        mbar_init(&sh.k_full[i][x], x == 0 ? kBaCopiers + 4 : (x < kBaCopied ? kBaCopiers : 2));
         mbar_init(&sh.k_empty[i][x], 1);
       }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_free[i], 128);
+      mbar_init(&sh.s_free[i], kBaSoftmax / 32);
     }
-    mbar_init(&sh.p_ready, 128);
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.p_ready, kBaSoftmax / 32);
+    mbar_init(&sh.drain, 2);
     sh.abort = 0;
     sh.fail[0] = sh.fail[1] = 0;
     fence_mbar_init();
@@ -175,159 +194,212 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
 
   if (warp == 0) {
     if (elect_one()) {
-      const int ncol = (u.rows + 15) / 16 * 16;
-      const uint32_t idesc_s = idesc_bf16_f32(64, ncol, false, false);
-      const uint32_t idesc_o = idesc_bf16_f32(128, ncol, true, true);
+      // scores of all 64 columns (rows of zeros behind the group's): every column read out is defined
+      const uint32_t idesc = idesc_bf16_f32(64, kBaRows, false, false);
       const uint64_t d_k = smem_desc(base, 16, 1024, kSwizzle128B);
       const uint64_t d_q = smem_desc(base + kBaOffQ, 16, 1024, kSwizzle128B);
-      const uint64_t d_v = smem_desc(base, kBaChunk, 1024, kSwizzle128B);            // MN-major
-      const uint64_t d_p = smem_desc(base + kBaOffP, kBaChunk, 1024, kSwizzle128B);  // MN-major
-      int s_tile = 0, s_group = 0, pv = 0;
-      // P.V(t) first when it is ready: it frees the stage that the loads wait for
-      for (uint32_t spin = 0; pv < n;) {
-        if (pv < s_tile && mbar_test_wait(&sh.p_ready, pv & 1)) {
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const uint64_t v = desc_advance(d_v, (pv & 1) * kBaStageBytes);
-          const uint32_t more = pv > 0 ? 1u : 0u;
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem + mt * kBaRows, desc_advance(v, mt * 2 * kBaChunk + ks * 2048), desc_advance(d_p, ks * 2048),
-                     idesc_o, ks > 0 ? 1u : more);
-            mma_commit(&sh.k_empty[pv & 1][mt]);
-          }
-          ++pv;
-          spin = 0;
-          continue;
-        }
-        if (s_tile < n && mbar_test_wait(&sh.k_full[s_tile & 1][s_group], (s_tile >> 1) & 1) &&
-            (s_group > 0 || s_tile < 2 || mbar_test_wait(&sh.s_free[s_tile & 1], ((s_tile >> 1) - 1) & 1))) {
-          fence_proxy_async_smem();  // the stage was written by cp.async
-          tc_fence_after();
-          const uint64_t k = desc_advance(d_k, (s_tile & 1) * kBaStageBytes);
-          const uint32_t d = tmem + kBaColS + (s_tile & 1) * kBaRows;
-          if (s_group == 0) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)  // the rope dims
-              mma_ss(d, desc_advance(k, 8 * kBaChunk + ks * 32), desc_advance(d_q, 8 * kBaChunk + ks * 32), idesc_s,
-                     ks > 0 ? 1u : 0u);
-          }
-          const uint64_t kg = desc_advance(k, s_group * 2 * kBaChunk), qg = desc_advance(d_q, s_group * 2 * kBaChunk);
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ss(d, desc_advance(kg, (ks >> 2) * kBaChunk + (ks & 3) * 32),
-                   desc_advance(qg, (ks >> 2) * kBaChunk + (ks & 3) * 32), idesc_s, 1u);
-          if (++s_group == kBaGroups) {
-            mma_commit(&sh.s_full[s_tile & 1]);
-            s_group = 0;
-            ++s_tile;
-          }
-          spin = 0;
-          continue;
-        }
-        if (++spin > 16 * DDT_WAIT_LIMIT || ((spin & 255) == 255 && *abort)) {
+      for (int t = 0; ok && t < n; ++t) {
+        const int st = t & 1;
+        if (t >= 2 && !mbar_wait_abortable(&sh.s_free[st], ((t >> 1) - 1) & 1, abort, false, __LINE__)) {
           ok = false;
           break;
+        }
+        const uint64_t k = desc_advance(d_k, st * kBaStageBytes);
+        const uint32_t d = tmem + kBaColS + st * kBaRows;
+#pragma unroll
+        for (int x = 0; x < kBaGroups; ++x) {
+          if (!mbar_wait_abortable(&sh.k_full[st][x], (t >> 1) & 1, abort, false, __LINE__)) {
+            ok = false;
+            break;
+          }
+          if (x < kBaCopied) fence_proxy_async_smem();  // written by cp.async
+          tc_fence_after();
+          if (x == 0) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)  // the rope dims
+              mma_ss(d, desc_advance(k, 8 * kBaChunk + ks * 32), desc_advance(d_q, 8 * kBaChunk + ks * 32), idesc,
+                     ks > 0 ? 1u : 0u);
+          }
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ss(d, desc_advance(k, (2 * x + (ks >> 2)) * kBaChunk + (ks & 3) * 32),
+                   desc_advance(d_q, (2 * x + (ks >> 2)) * kBaChunk + (ks & 3) * 32), idesc, 1u);
+        }
+        if (ok) mma_commit(&sh.s_full[st]);
+      }
+      mma_commit(&sh.drain);
+      mbar_wait(&sh.drain, 0);
+    }
+  } else if (warp == 9) {
+    if (elect_one()) {
+      const uint32_t idesc = idesc_bf16_f32(128, (u.rows + 15) / 16 * 16, true, true);
+      const uint64_t d_v = smem_desc(base, kBaChunk, 1024, kSwizzle128B);            // MN-major
+      const uint64_t d_p = smem_desc(base + kBaOffP, kBaChunk, 1024, kSwizzle128B);  // MN-major
+      for (int t = 0; t < n; ++t) {
+        if (!mbar_wait_abortable(&sh.p_ready, t & 1, abort, false, __LINE__)) {
+          ok = false;
+          break;
+        }
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t v = desc_advance(d_v, (t & 1) * kBaStageBytes);
+        const uint32_t more = t > 0 ? 1u : 0u;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ss(tmem + mt * kBaRows, desc_advance(v, mt * 2 * kBaChunk + ks * 2048), desc_advance(d_p, ks * 2048),
+                   idesc, ks > 0 ? 1u : more);
+          mma_commit(&sh.k_empty[t & 1][mt]);
         }
       }
       mma_commit(&sh.drain);
       mbar_wait(&sh.drain, 0);
     }
-  } else if (warp >= 5) {
-    // ------------------------------------------------------------------ producers: 8 keys per warp
-    const int pw = warp - 5;
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------------ producers
     const int32_t* slots = p.slot_idx + static_cast<int64_t>(u.b) * p.slot_stride;
-    // key of this lane in tile t: its block entry, then its slot
-    auto entry_of = [&](int t, int* pos, uint64_t* mask) {
-      *pos = -1;
-      *mask = 0;
-      const int64_t i = (static_cast<int64_t>(t0 + t)) * kBaKeys + 8 * pw + lane;
-      if (t < n && lane < 8 && i < keys) {
-        const int e = static_cast<int>(i / p.block);
-        const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(list + e));
-        BlockEntry be;
-        be.mask = raw.x | (static_cast<unsigned long long>(raw.y) << 32);
-        be.block = static_cast<int>(raw.z);
-        const int64_t x = static_cast<int64_t>(be.block) * p.block + (i - static_cast<int64_t>(e) * p.block);
-        if (x < L) {
-          *pos = static_cast<int>(x);
-          *mask = be.mask;
-        }
+    // A key's row takes two dependent reads, its block entry and its slot, each a
+    // tile ahead of its use: nothing is computed from a value in the tile that
+    // reads it (an immediate use stalls the warp for the read: 2000 cycles a tile).
+    struct Key {
+      uint4 entry;    // of tile t + 1: mask, block
+      int slot;       // of tile t, as read; -1: no key
+      uint64_t mask;  // of tile t
+    };
+    // (a list names each block once, so its keys count in 32 bits; blocks are powers of two)
+    const int log_block = 31 - __clz(p.block);
+    const uint32_t first = static_cast<uint32_t>(t0) * kBaKeys, n_keys = static_cast<uint32_t>(keys);
+    auto read_entry = [&](int t, int k) -> uint4 {  // key k of tile t
+      const uint32_t i = first + t * kBaKeys + k;
+      if (t >= n || k >= kBaKeys || i >= n_keys) return make_uint4(0, 0, 0xffffffffu, 0);
+      return __ldcg(reinterpret_cast<const uint4*>(list + (i >> log_block)));
+    };
+    auto read_slot = [&](int t, int k, Key& key) {  // of tile t, whose entry has arrived
+      const uint32_t i = first + t * kBaKeys + k;
+      const int blk = static_cast<int>(key.entry.z);
+      const uint32_t pos = (static_cast<uint32_t>(blk) << log_block) + (i & (p.block - 1));
+      const bool in = blk >= 0 && pos < static_cast<uint32_t>(L);
+      key.mask = in ? key.entry.x | (static_cast<uint64_t>(key.entry.y) << 32) : 0;
+      key.slot = in ? __ldg(slots + pos) : -1;
+    };
+    auto row_of = [&](Key& key) -> int {
+      if (key.mask != 0 && (key.slot < 0 || key.slot >= p.pool_slots)) {
+        atomicOr(p.status, kStatusBadSlot);
+        key.mask = 0;
+      }
+      return key.mask != 0 ? key.slot : -1;
+    };
+    // 16-byte pieces of kRows rows from row0 on, kPer a row: chunks c0, c0 + 1 (and
+    // the rope chunk); zeros for rows without a slot
+    auto copy_rows = [&](uint32_t sbase, int row0, int c0, auto per_c, auto rows_c, int slot) {
+      constexpr int kPer = decltype(per_c)::value, kRows = decltype(rows_c)::value;
+#pragma unroll 4
+      for (int i = 0; i < kRows * kPer / 32; ++i) {
+        const int e = i * 32 + lane;
+        const int r = e / kPer, y = e - r * kPer;
+        const int row = __shfl_sync(0xffffffffu, slot, r);
+        const int c = y < 16 ? c0 + (y >> 3) : 8;
+        const int rr = row0 + r;
+        cp_async16(sbase + c * kBaChunk + rr * 128 + (((y & 7) ^ (rr & 7)) << 4),
+                   p.kv + (row < 0 ? 0 : static_cast<int64_t>(row) * kDqk + c * 64 + (y & 7) * 8), row < 0 ? 0u : 16u);
       }
     };
-    auto slot_at = [&](int pos) -> int {
-      if (pos < 0) return -1;
-      const int s = __ldg(slots + pos);
-      if (s >= 0 && s < p.pool_slots) return s;
-      atomicOr(p.status, kStatusBadSlot);
-      return -1;
+    const bool copier = warp < 14;
+    const int row0 = copier ? 16 * (warp - 10) : 32 * (warp & 1);  // the warp's first key: 16 or 32 of them
+    const int k = copier && lane >= 16 ? kBaKeys : row0 + lane;    // the lane's key
+    const int gx = copier ? 0 : kBaCopied + ((warp - 14) >> 1);    // a gather warp's dim group
+    Key key;
+    key.entry = read_entry(0, k);
+    read_slot(0, k, key);
+    key.entry = read_entry(1, k);
+    int done = 0;
+    auto wait_empty = [&](int t, int x) {
+      const bool w = t < kBaStages || mbar_wait_abortable(&sh.k_empty[t & 1][x], ((t >> 1) - 1) & 1, abort, false, __LINE__);
+      return __all_sync(0xffffffffu, w) != 0;
     };
-    int pos_n;
-    uint64_t mask_c, mask_n;
-    entry_of(0, &pos_n, &mask_c);
-    int slot_c = slot_at(pos_n);
-    entry_of(1, &pos_n, &mask_n);
-    for (int t = 0; t < n; ++t) {
-      const int slot_n = slot_at(pos_n);  // of tile t + 1
-      int pos_f;
-      uint64_t mask_f;
-      entry_of(t + 2, &pos_f, &mask_f);
+    for (int t = 0; ok && t < n; ++t) {
+      const int slot = row_of(key);
+      const uint64_t mask = key.mask;
+      read_slot(t + 1, k, key);
+      key.entry = read_entry(t + 2, k);
       const int st = t & 1;
       const uint32_t sbase = base + st * kBaStageBytes;
-#pragma unroll
-      for (int x = 0; x < kBaGroups; ++x) {
-        const bool w = t < kBaStages || mbar_wait_abortable(&sh.k_empty[st][x], ((t >> 1) - 1) & 1, abort, false, __LINE__);
-        if (!__all_sync(0xffffffffu, w)) {
+      if (copier) {
+        if (!wait_empty(t, 0)) {
           ok = false;
           break;
         }
-        if (x == 0) {
-          if (lane < 8)
-            reinterpret_cast<uint64_t*>(smem + kBaOffMask)[st * kBaKeys + 8 * pw + lane] = slot_c >= 0 ? mask_c : 0;
+        if (lane < 16) reinterpret_cast<uint64_t*>(smem + kBaOffMask)[st * kBaKeys + row0 + lane] = mask;
+        copy_rows(sbase, row0, 0, std::integral_constant<int, 24>(), std::integral_constant<int, 16>(), slot);
+        cp_async_arrive_noinc(&sh.k_full[st][0]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.k_full[st][0]);  // releases the masks
+        if (!wait_empty(t, 1)) {
+          ok = false;
+          break;
+        }
+        copy_rows(sbase, row0, 2, std::integral_constant<int, 16>(), std::integral_constant<int, 16>(), slot);
+        cp_async_arrive_noinc(&sh.k_full[st][1]);
+      } else {
+        if (!wait_empty(t, gx)) {
+          ok = false;
+          break;
+        }
+        if (__all_sync(0xffffffffu, slot >= 0)) {
+          // lanes 0-15: four of the warp's keys, one of the group's two chunks
+          if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[st][gx], 32 * 256);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.k_full[st][0]);  // releases the masks
+          const int q = 4 * (lane & 7), c = 2 * gx + ((lane >> 3) & 1);
+          const int ra = __shfl_sync(0xffffffffu, slot, q), rb = __shfl_sync(0xffffffffu, slot, q + 1);
+          const int rc = __shfl_sync(0xffffffffu, slot, q + 2), rd = __shfl_sync(0xffffffffu, slot, q + 3);
+          if (lane < 16)
+            tma_gather4(sbase + c * kBaChunk + (row0 + q) * 128, &p.tmap_kv, c * 64, ra, rb, rc, rd, &sh.k_full[st][gx]);
+        } else {
+          // a key is masked (the list's end, a bad slot): zero-filled copies
+          copy_rows(sbase, row0, 2 * gx, std::integral_constant<int, 16>(), std::integral_constant<int, 32>(), slot);
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.k_full[st][gx]);
         }
-        // pieces of 16 bytes per row: the group's two latent chunks, and with group 0 the rope chunk
-        const int per = x == 0 ? 24 : 16;
-#pragma unroll
-        for (int i = 0; i < per / 4; ++i) {
-          const int e = i * 32 + lane;
-          const int r = e / per, y = e - r * per;
-          const int c = y < 16 ? 2 * x + (y >> 3) : 8;  // 64-dim chunk
-          const int row = __shfl_sync(0xffffffffu, slot_c, r);
-          const int rr = 8 * pw + r;
-          cp_async16(sbase + c * kBaChunk + rr * 128 + (((y & 7) ^ (rr & 7)) << 4),
-                     p.kv + (row < 0 ? 0 : static_cast<int64_t>(row) * kDqk + c * 64 + (y & 7) * 8), row < 0 ? 0u : 16u);
-        }
-        cp_async_arrive_noinc(&sh.k_full[st][x]);
       }
-      if (!ok) break;
-      slot_c = slot_n;
-      mask_c = mask_n;
-      pos_n = pos_f;
-      mask_n = mask_f;
+      done = t + 1;
     }
     cp_async_wait<0>();
+    if (!ok && !copier)  // after a give-up the gathers still in flight land before the CTA exits
+      for (int v = max(0, done - 2); v < done; ++v) mbar_wait(&sh.k_full[v & 1][gx], (v >> 1) & 1, 1u << 16);
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, half = (warp - 1) >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const int r0 = quarter * 16 + (lane >> 2);  // keys r0 and r0 + 8 of the tile
-    const int c0 = 2 * (lane & 3);              // rows 8 i + c0 + {0, 1}
+    const int r0 = quarter * 16 + (lane >> 2);     // keys r0 and r0 + 8 of the tile
+    const int c0 = 32 * half + 2 * (lane & 3);     // rows c0 + 8 i + {0, 1}, i < 4
+    const int id = half * 128 + quarter * 32 + lane;
     float* mx = reinterpret_cast<float*>(smem + kBaOffMax);
     float* alpha_sh = reinterpret_cast<float*>(smem + kBaOffAlpha);
-    float* scratch = reinterpret_cast<float*>(smem + kBaOffP);  // [4 warps][64], while no P is in use
+    float* scratch = reinterpret_cast<float*>(smem + kBaOffP);  // [4 quarters][64], while no P is in use
     const uint64_t* masks = reinterpret_cast<const uint64_t*>(smem + kBaOffMask);
     const uint64_t full = u.rows == 64 ? ~0ull : ((1ull << u.rows) - 1);
-    float l[16];
+    float l[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) l[i] = 0.f;
+    for (int i = 0; i < 8; ++i) l[i] = 0.f;
     bool failed = false;  // a wait of this thread ran out: the warps leave together at the next barrier
     auto wait_pv = [&](int t) {  // P.V(t) has read P, and O^T holds every tile up to t
       if (!mbar_wait_abortable(&sh.k_empty[t & 1][kBaGroups - 1], (t >> 1) & 1, abort, false, __LINE__)) failed = true;
       tc_fence_after();
+    };
+    // column sums or maxima over the 16 keys of the warp, to scratch
+    auto to_scratch = [&](const float (&v)[8], auto op) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float x = v[i];
+        x = op(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = op(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = op(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        if (lane < 4) scratch[quarter * kBaRows + c0 + 8 * (i >> 1) + (i & 1)] = x;
+      }
     };
     for (int t = 0; t < n; ++t) {
       const int st = t & 1;
@@ -335,18 +407,20 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
       if (!mbar_wait_abortable(&sh.s_full[st], (t >> 1) & 1, abort, false, __LINE__) ||
           !mbar_wait_abortable(&sh.k_full[st][0], (t >> 1) & 1, abort, false, __LINE__))
         failed = true;
+      __syncwarp();
       tc_fence_after();
-      float s[32];
-      tmem_ld_16x64(tmem + lane_off + kBaColS + st * kBaRows, s);
+      float s[16];
+      tmem_ld_16x32(tmem + lane_off + kBaColS + st * kBaRows + 32 * half, s);
       tc_fence_before();
-      mbar_arrive(&sh.s_free[st]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_free[st]);
       const uint64_t m0 = masks[st * kBaKeys + r0], m1 = masks[st * kBaKeys + r0 + 8];
       const bool part = __any_sync(0xffffffffu, m0 != full || m1 != full);
       bool bad0 = false, bad1 = false;  // a row of non-finite scores that some rows do not read
       if (part) {
         float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           a0 += fabsf(s[4 * i]) + fabsf(s[4 * i + 1]);
           a1 += fabsf(s[4 * i + 2]) + fabsf(s[4 * i + 3]);
         }
@@ -356,82 +430,75 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
         a1 += __shfl_xor_sync(0xffffffffu, a1, 2);
         bad0 = !(a0 < CUDART_INF_F) && m0 != full && m0 != 0;
         bad1 = !(a1 < CUDART_INF_F) && m1 != full && m1 != 0;
-        const uint32_t w0[2] = {static_cast<uint32_t>(m0) >> c0, static_cast<uint32_t>(m0 >> 32) >> c0};
-        const uint32_t w1[2] = {static_cast<uint32_t>(m1) >> c0, static_cast<uint32_t>(m1 >> 32) >> c0};
+        const uint32_t w0 = static_cast<uint32_t>(m0 >> c0), w1 = static_cast<uint32_t>(m1 >> c0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            s[4 * i + e] = (w0[i >> 2] >> (8 * (i & 3) + e)) & 1u ? s[4 * i + e] * p.scale_log2 : -CUDART_INF_F;
-            s[4 * i + 2 + e] = (w1[i >> 2] >> (8 * (i & 3) + e)) & 1u ? s[4 * i + 2 + e] * p.scale_log2 : -CUDART_INF_F;
+            s[4 * i + e] = (w0 >> (8 * i + e)) & 1u ? s[4 * i + e] * p.scale_log2 : -CUDART_INF_F;
+            s[4 * i + 2 + e] = (w1 >> (8 * i + e)) & 1u ? s[4 * i + 2 + e] * p.scale_log2 : -CUDART_INF_F;
           }
       } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] *= p.scale_log2;
+        for (int i = 0; i < 16; ++i) s[i] *= p.scale_log2;
       }
       // s is now in log2 units; a score 2^8 above its row's running max raises the max first
       float over = -CUDART_INF_F;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 m = *reinterpret_cast<const float2*>(mx + 8 * i + c0);
+      for (int i = 0; i < 4; ++i) {
+        const float2 m = *reinterpret_cast<const float2*>(mx + c0 + 8 * i);
         over = fmax3(over, s[4 * i] - m.x, s[4 * i + 1] - m.y);
         over = fmax3(over, s[4 * i + 2] - m.x, s[4 * i + 3] - m.y);
       }
       if (failed) sh.fail[st] = 1;
-      const bool raise = bar_red_or(1, 128, failed || over > kBaThreshold);
+      const bool raise = bar_red_or(1, kBaSoftmax, failed || over > kBaThreshold);
       if (raise && *const_cast<volatile int*>(&sh.fail[st])) {
         ok = false;
         break;
       }
       if (raise) {
         if (t > 0) wait_pv(t - 1);  // the scratch is the P buffer, and O^T is rescaled
-        bar_sync(1, 128);
+        float top8[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v = fmaxf(s[4 * i + e], s[4 * i + 2 + e]);
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            if (lane < 4) scratch[quarter * kBaRows + 8 * i + c0 + e] = v;
-          }
-        bar_sync(1, 128);
-        const int st_id = quarter * 32 + lane;  // one thread per row decides
-        if (st_id < kBaRows) {
-          const float m = mx[st_id];
-          const float top = fmaxf(fmaxf(scratch[st_id], scratch[kBaRows + st_id]),
-                                  fmaxf(scratch[2 * kBaRows + st_id], scratch[3 * kBaRows + st_id]));
-          const bool up = top > m + kBaThreshold;
-          alpha_sh[st_id] = up ? fast_exp2(m - top) : 1.f;
-          mx[st_id] = up ? top : m;
+        for (int i = 0; i < 4; ++i) {
+          top8[2 * i] = fmaxf(s[4 * i], s[4 * i + 2]);
+          top8[2 * i + 1] = fmaxf(s[4 * i + 1], s[4 * i + 3]);
         }
-        bar_sync(1, 128);
+        to_scratch(top8, [](float a, float b) { return fmaxf(a, b); });
+        bar_sync(1, kBaSoftmax);
+        if (id < kBaRows) {  // one thread per row decides
+          const float m = mx[id];
+          const float top = fmaxf(fmaxf(scratch[id], scratch[kBaRows + id]),
+                                  fmaxf(scratch[2 * kBaRows + id], scratch[3 * kBaRows + id]));
+          const bool up = top > m + kBaThreshold;
+          alpha_sh[id] = up ? fast_exp2(m - top) : 1.f;
+          mx[id] = up ? top : m;
+        }
+        bar_sync(1, kBaSoftmax);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            l[2 * i + e] *= alpha_sh[8 * i + c0 + e];
-          }
+        for (int i = 0; i < 8; ++i) l[i] *= alpha_sh[c0 + 8 * (i >> 1) + (i & 1)];
         if (t > 0) {
 #pragma unroll 1
-          for (int c = 0; c < 4 * kBaRows; c += 32) {
-            float o[32];
-            tmem_ld32(tmem + lane_off + c, o);
-            uint32_t ob[32];
+          for (int k0 = 0; k0 < 16; ++k0) {  // this warp's half of the columns, 8 at a time
+            const int cc = 32 * half + (k0 & 3) * 8;
+            uint32_t o[8];
+            tmem_ld8(tmem + lane_off + (k0 >> 2) * kBaRows + cc, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) ob[k] = __float_as_uint(o[k] * alpha_sh[(c & 32) + k]);
-            tmem_st32(tmem + lane_off + c, ob);
+            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha_sh[cc + k]);
+            tmem_st8(tmem + lane_off + (k0 >> 2) * kBaRows + cc, o);
           }
         }
-        bar_sync(1, 128);  // scratch is read before P is written over it
+        bar_sync(1, kBaSoftmax);  // scratch is read before P is written over it
       }
       // P^T, row (key) r of 64 columns, 128-byte swizzle
       uint8_t* pb = smem + kBaOffP;
-      uint32_t pk[16];
+      auto p_at = [&](int key, int i) {
+        return reinterpret_cast<uint32_t*>(pb + key * 128 + (((4 * half + i) ^ (key & 7)) << 4) + (lane & 3) * 4);
+      };
+      uint32_t pk[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 m = *reinterpret_cast<const float2*>(mx + 8 * i + c0);
+      for (int i = 0; i < 4; ++i) {
+        const float2 m = *reinterpret_cast<const float2*>(mx + c0 + 8 * i);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float x = fast_exp2(s[4 * i + 2 * h] - m.x), y = fast_exp2(s[4 * i + 2 * h + 1] - m.y);
@@ -442,28 +509,26 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
       }
       if (t > 0) wait_pv(t - 1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int key = r0 + 8 * h;
-          *reinterpret_cast<uint32_t*>(pb + key * 128 + ((i ^ (key & 7)) << 4) + c0 * 2) = pk[2 * i + h];
-        }
+        for (int h = 0; h < 2; ++h) *p_at(r0 + 8 * h, i) = pk[2 * i + h];
       if (part && __any_sync(0xffffffffu, bad0 || bad1)) {
         // A non-finite key row that not every row of the group reads: 0 * inf
         // would spoil the others' O, so its values become zero and the weights
-        // of the rows that do read it NaN.
+        // of the rows that do read it NaN.  (Both halves' warps see such a row:
+        // it makes every score non-finite.)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint64_t m = h ? m1 : m0;
+          const uint32_t m = static_cast<uint32_t>((h ? m1 : m0) >> c0);
           const int key = r0 + 8 * h;
           if (h ? bad1 : bad0) {
             uint8_t* row = smem + st * kBaStageBytes + key * 128;
             for (int x = lane & 3; x < 64; x += 4)
               *reinterpret_cast<uint4*>(row + (x >> 3) * kBaChunk + ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t lo = (m >> (8 * i + c0)) & 1 ? 0x7fc0u : 0u, hi = (m >> (8 * i + c0 + 1)) & 1 ? 0x7fc0u : 0u;
-              *reinterpret_cast<uint32_t*>(pb + key * 128 + ((i ^ (key & 7)) << 4) + c0 * 2) = lo | (hi << 16);
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t lo = (m >> (8 * i)) & 1 ? 0x7fc0u : 0u, hi = (m >> (8 * i + 1)) & 1 ? 0x7fc0u : 0u;
+              *p_at(key, i) = lo | (hi << 16);
               if (lo) l[2 * i] = CUDART_NAN_F;
               if (hi) l[2 * i + 1] = CUDART_NAN_F;
             }
@@ -472,50 +537,40 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(&sh.p_ready);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_ready);
     }
     if (ok) {
       wait_pv(n - 1);  // O^T is complete and the P buffer free
-      if (bar_red_or(1, 128, failed)) ok = false;
+      if (bar_red_or(1, kBaSoftmax, failed)) ok = false;
     }
     if (ok) {
-      tc_fence_after();
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = l[2 * i + e];
-          v += __shfl_xor_sync(0xffffffffu, v, 4);
-          v += __shfl_xor_sync(0xffffffffu, v, 8);
-          v += __shfl_xor_sync(0xffffffffu, v, 16);
-          if (lane < 4) scratch[quarter * kBaRows + 8 * i + c0 + e] = v;
-        }
-      bar_sync(1, 128);
-      const int c = quarter * 32 + lane;
-      if (c < kBaRows) {
-        const float sum = (scratch[c] + scratch[kBaRows + c]) + (scratch[2 * kBaRows + c] + scratch[3 * kBaRows + c]);
-        alpha_sh[c] = sum != 0.f ? 1.f / sum : 0.f;
-        if (c < u.rows) p.lse_part[prow0 + c] = sum != 0.f ? (mx[c] + log2f(sum)) * kBaLn2 : -CUDART_INF_F;
+      to_scratch(l, [](float a, float b) { return a + b; });
+      bar_sync(1, kBaSoftmax);
+      if (id < kBaRows) {
+        const float sum = (scratch[id] + scratch[kBaRows + id]) + (scratch[2 * kBaRows + id] + scratch[3 * kBaRows + id]);
+        alpha_sh[id] = sum != 0.f ? 1.f / sum : 0.f;
+        if (id < u.rows) p.lse_part[prow0 + id] = sum != 0.f ? (mx[id] + log2f(sum)) * kBaLn2 : -CUDART_INF_F;
       }
     }
   }
-  // every warp but the first writes O: quarter of the lanes by warp, three warps a quarter
+  // the softmax and gather warps write O: quarter of the lanes by warp, four warps a quarter
   if (warp > 0) {
-    if (!bar_red_or(2, kBaThreads - 32, !ok)) {
+    if (!bar_red_or(2, kBaThreads - 32, !ok) && warp != 9) {
       tc_fence_after();
       const float* inv_l = reinterpret_cast<const float*>(smem + kBaOffAlpha);
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       // lane = value dim: each row's store is 128 contiguous bytes per warp
 #pragma unroll 1
-      for (int k0 = (warp - 1) >> 2; k0 < 8; k0 += 3) {
-        const int mt = k0 >> 1, cc = (k0 & 1) * 32;
+      for (int k0 = warp < 9 ? (warp - 1) >> 2 : (warp - 2) >> 2; k0 < 32; k0 += 4) {
+        const int mt = k0 >> 3, cc = (k0 & 7) * 8;
         if (cc >= u.rows) continue;
-        float o[32];
-        tmem_ld32(tmem + lane_off + mt * kBaRows + cc, o);
-        float* dst = p.o_part + prow0 * kDv + mt * 128 + (warp & 3) * 32 + lane;
+        uint32_t o[8];
+        tmem_ld8(tmem + lane_off + mt * kBaRows + cc, o);
+        float* dst = p.o_part + (prow0 + cc) * kDv + mt * 128 + (warp & 3) * 32 + lane;
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (cc + k < u.rows) dst[static_cast<int64_t>(cc + k) * kDv] = o[k] * inv_l[cc + k];
+        for (int k = 0; k < 8; ++k)
+          if (cc + k < u.rows) dst[k * kDv] = __uint_as_float(o[k]) * inv_l[cc + k];
       }
     }
   }
@@ -534,7 +589,7 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const BlockAt
 constexpr int kUnThreads = 256;
 constexpr int kUnBlocks = 2048;
 
-__global__ void __launch_bounds__(kUnThreads) block_union_kernel(const BlockAttnParams p) {
+__global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_constant__ BlockAttnParams p) {
   __shared__ unsigned long long mask_sh[kUnBlocks];
   __shared__ int cnt[kUnThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

@@ -420,6 +420,7 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
   p.o_part = reinterpret_cast<float*>(ws + w.o_off);
   p.lse_part = reinterpret_cast<float*>(ws + w.lse_off);
   p.status = reinterpret_cast<int32_t*>(ws);
+  if (!encode_pool_map(&p.tmap_kv, kv_pool, dims->pool_slots, 64, 1)) return DDT_ERR_LAUNCH;
   TailParams tp = {};
   tp.q = p.q;
   tp.kv = p.kv;

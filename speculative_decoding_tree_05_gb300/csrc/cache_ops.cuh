@@ -125,6 +125,7 @@ struct alignas(16) BlockEntry {
 };
 
 struct BlockAttnParams {
+  CUtensorMap tmap_kv;        // kv as [N][576], box 64 cols x 1 row, 128-byte swizzle
   const uint16_t* q;          // bf16 [B, T, H, 576]
   const uint16_t* kv;         // bf16 [N, 576]
   const int32_t* slot_idx;    // [B, slot_stride]
