@@ -290,21 +290,25 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       }
       return key.mask != 0 ? key.slot : -1;
     };
-    // 16-byte pieces of kRows rows from row0 on, kPer a row: chunks c0, c0 + 1 (and
-    // the rope chunk); zeros for rows without a slot
-    auto copy_rows = [&](uint32_t sbase, int row0, int c0, auto per_c, auto rows_c, int slot) {
-      constexpr int kPer = decltype(per_c)::value, kRows = decltype(rows_c)::value;
-#pragma unroll 4
-      for (int i = 0; i < kRows * kPer / 32; ++i) {
-        const int e = i * 32 + lane;
-        const int r = e / kPer, y = e - r * kPer;
-        const int row = __shfl_sync(0xffffffffu, slot, r);
-        const int c = y < 16 ? c0 + (y >> 3) : 8;
-        const int rr = row0 + r;
-        cp_async16(sbase + c * kBaChunk + rr * 128 + (((y & 7) ^ (rr & 7)) << 4),
-                   p.kv + (row < 0 ? 0 : static_cast<int64_t>(row) * kDqk + c * 64 + (y & 7) * 8), row < 0 ? 0u : 16u);
+    // 16-byte copies, 32 / kPieces rows at a time: kPieces consecutive pieces (8 a chunk) from chunk c0 on of kRows rows from row0 (a multiple of 8)
+    // on; zeros for rows without a slot.  A lane keeps its piece, so that a copy
+    // costs a shuffle and two address steps.
+    auto copy_rows = [&](uint32_t sbase, int row0, int c0, auto pieces, auto rows, int slot) {
+      constexpr int kPieces = decltype(pieces)::value, kStep = 32 / kPieces, kRows = decltype(rows)::value;
+      const int y = lane & (kPieces - 1), sub = lane / kPieces;  // piece, row within a step
+      const uint32_t dst = sbase + (c0 + (y >> 3)) * kBaChunk + (row0 + sub) * 128;
+      const uint16_t* src = p.kv + (c0 * 8 + y) * 8;
+#pragma unroll
+      for (int i = 0; i < kRows / kStep; ++i) {
+        const int row = __shfl_sync(0xffffffffu, slot, i * kStep + sub);
+        // the row's place in its swizzle atom: steps of kStep rows leave the low bits to sub
+        const uint32_t at = ((y & 7) ^ ((i * kStep + sub) & 7)) << 4;
+        cp_async16(dst + i * kStep * 128 + at, row < 0 ? p.kv : src + static_cast<int64_t>(row) * kDqk, row < 0 ? 0u : 16u);
       }
     };
+    using P16 = std::integral_constant<int, 16>;
+    using P8 = std::integral_constant<int, 8>;
+    using R32 = std::integral_constant<int, 32>;
     const bool copier = warp < 14;
     const int row0 = copier ? 16 * (warp - 10) : 32 * (warp & 1);  // the warp's first key: 16 or 32 of them
     const int k = copier && lane >= 16 ? kBaKeys : row0 + lane;    // the lane's key
@@ -331,7 +335,8 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
           break;
         }
         if (lane < 16) reinterpret_cast<uint64_t*>(smem + kBaOffMask)[st * kBaKeys + row0 + lane] = mask;
-        copy_rows(sbase, row0, 0, std::integral_constant<int, 24>(), std::integral_constant<int, 16>(), slot);
+        copy_rows(sbase, row0, 8, P8(), P16(), slot);
+        copy_rows(sbase, row0, 0, P16(), P16(), slot);
         cp_async_arrive_noinc(&sh.k_full[st][0]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_full[st][0]);  // releases the masks
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
           ok = false;
           break;
         }
-        copy_rows(sbase, row0, 2, std::integral_constant<int, 16>(), std::integral_constant<int, 16>(), slot);
+        copy_rows(sbase, row0, 2, P16(), P16(), slot);
         cp_async_arrive_noinc(&sh.k_full[st][1]);
       } else {
         if (!wait_empty(t, gx)) {
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
             tma_gather4(sbase + c * kBaChunk + (row0 + q) * 128, &p.tmap_kv, c * 64, ra, rb, rc, rd, &sh.k_full[st][gx]);
         } else {
           // a key is masked (the list's end, a bad slot): zero-filled copies
-          copy_rows(sbase, row0, 2 * gx, std::integral_constant<int, 16>(), std::integral_constant<int, 32>(), slot);
+          copy_rows(sbase, row0, 2 * gx, P16(), R32(), slot);
           cp_async_commit();
           cp_async_wait<0>();
           fence_proxy_async_smem();
