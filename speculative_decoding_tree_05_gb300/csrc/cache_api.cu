@@ -97,7 +97,7 @@ int select_layout(const ddt_dims* d, int32_t block, SelectLayout* w) {
 }
 
 struct BlocksLayout {
-  int groups, group_nodes, splits, row_tiles;
+  int groups, group_nodes, splits;
   int64_t list_cap;
   size_t len_off, list_off, lse_off, o_off, bytes;
 };
@@ -126,8 +126,7 @@ int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, 
       w->splits = s;
     }
   }
-  w->row_tiles = (T * H + kTileRows - 1) / kTileRows;
-  const size_t part = size_t(d->batch) * w->splits * w->row_tiles * kTileRows;
+  const size_t part = size_t(d->batch) * w->splits * T * H;
   w->len_off = kStatusBytes;
   w->list_off = align_up(w->len_off + all * sizeof(int32_t), 256);
   w->lse_off = align_up(w->list_off + size_t(all) * w->list_cap * sizeof(BlockEntry), 256);
@@ -405,10 +404,10 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
   p.list_len = reinterpret_cast<int32_t*>(ws + w.len_off);
   p.pool_slots = dims->pool_slots;
   p.list_cap = w.list_cap;
-  p.pstride = int64_t(w.row_tiles) * kTileRows;
   p.batch = dims->batch;
   p.nodes = dims->num_nodes;
   p.heads = dims->num_heads;
+  p.pstride = int64_t(p.nodes) * p.heads;
   p.slot_stride = dims->slot_stride;
   p.max_prefix_len = dims->max_prefix_len;
   p.block = block;
@@ -421,29 +420,27 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
   p.lse_part = reinterpret_cast<float*>(ws + w.lse_off);
   p.status = reinterpret_cast<int32_t*>(ws);
   if (!encode_pool_map(&p.tmap_kv, kv_pool, dims->pool_slots, 64, 1)) return DDT_ERR_LAUNCH;
-  TailParams tp = {};
-  tp.q = p.q;
-  tp.kv = p.kv;
-  tp.prefix_len = nullptr;  // every request has exactly `splits` partials: chunks of one
-  tp.max_prefix_len = tp.max_splits = w.splits;
-  tp.chunk0 = tp.chunk = 1;
-  tp.tree_parent = tree_parent;
-  tp.tree_slot_idx = tree_slot_idx;
-  tp.pool_slots = dims->pool_slots;
-  tp.nodes = p.nodes;
-  tp.heads = p.heads;
-  tp.heads_per_cta = p.heads < 8 ? p.heads : 8;
-  tp.row_tiles = w.row_tiles;
-  tp.batch = p.batch;
-  tp.scale_log2 = p.scale_log2;
-  tp.o_part = p.o_part;
-  tp.lse_part = p.lse_part;
-  tp.out_bf16 = static_cast<uint16_t*>(out);
-  tp.lse = lse;
-  tp.status = p.status;
+  BlockMergeParams m = {};
+  m.q = p.q;
+  m.kv = p.kv;
+  m.tree_parent = tree_parent;
+  m.tree_slot_idx = tree_slot_idx;
+  m.pool_slots = dims->pool_slots;
+  m.pstride = p.pstride;
+  m.nodes = p.nodes;
+  m.heads = p.heads;
+  // two rows a warp once the nodes fill the GPU with one
+  m.heads_per_cta = p.heads >= 16 && int64_t(p.batch) * p.nodes * p.heads > 8 * 4 * int64_t(sms) ? 16 : 8;
+  m.splits = w.splits;
+  m.scale_log2 = p.scale_log2;
+  m.o_part = p.o_part;
+  m.lse_part = p.lse_part;
+  m.out = static_cast<uint16_t*>(out);
+  m.lse = lse;
+  m.status = p.status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!clear_status(workspace, s) || launch_block_union(p, s) != cudaSuccess || launch_block_attn(p, s) != cudaSuccess ||
-      launch_tail_merge(tp, p.batch, s) != cudaSuccess)
+      launch_block_merge(m, p.batch, s) != cudaSuccess)
     return DDT_ERR_LAUNCH;
   return DDT_OK;
 }

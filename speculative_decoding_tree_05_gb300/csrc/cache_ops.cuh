@@ -149,6 +149,25 @@ cudaError_t configure_block_attn();
 cudaError_t launch_block_union(const BlockAttnParams& p, cudaStream_t stream);
 cudaError_t launch_block_attn(const BlockAttnParams& p, cudaStream_t stream);
 
+// The tree part of block attention and the merge of its splits.
+struct BlockMergeParams {
+  const uint16_t* q;
+  const uint16_t* kv;
+  const int32_t* tree_parent;    // [B, T]
+  const int32_t* tree_slot_idx;  // [B, T]
+  int64_t pool_slots;
+  int64_t pstride;
+  int32_t nodes, heads, heads_per_cta;
+  int32_t splits;                // at most 32
+  float scale_log2;
+  const float* o_part;
+  const float* lse_part;
+  uint16_t* out;                 // bf16 [B, T, H, 512]
+  float* lse;                    // fp32 [B, T, H]
+  int32_t* status;
+};
+cudaError_t launch_block_merge(const BlockMergeParams& p, int batch, cudaStream_t stream);
+
 // Map of a score to an unsigned key with the same order: NaN lowest (equal to
 // -inf), -0 equal to +0.
 __host__ __device__ inline uint32_t order_key_bits(uint32_t u) {

@@ -75,7 +75,6 @@ struct TailParams {
   const float* o_part;
   const float* lse_part;
   float* out;                   // fp32 [B, T, H, 512]
-  uint16_t* out_bf16 = nullptr; // bf16 [B, T, H, 512]: written instead of out
   float* lse;                   // fp32 [B, T, H]
   int32_t* status;
 };

@@ -62,7 +62,6 @@ struct MergeRowArgs {
   int64_t pstride;        // rows between consecutive splits of one request
   float* out;             // fp32 [rows, 512]
   float* lse;             // fp32 [rows], natural log
-  uint16_t* out_bf16 = nullptr;  // bf16 [rows, 512]: written instead of out
 };
 
 // One warp computes global row `grow`: its tail over the n_vis visible tree
@@ -183,16 +182,6 @@ __device__ __forceinline__ void merge_row(const MergeRowArgs& a, int64_t grow, i
     }
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-  if (a.out_bf16 != nullptr) {
-    uint2* dst16 = reinterpret_cast<uint2*>(a.out_bf16 + grow * kDv);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      dst16[lane + 32 * j] = make_uint2(pack_bf16x2(acc[4 * j] * inv, acc[4 * j + 1] * inv),
-                                        pack_bf16x2(acc[4 * j + 2] * inv, acc[4 * j + 3] * inv));
-    // a NaN weight (a non-finite key that the row reads) stays one
-    if (lane == 0) a.lse[grow] = wsum == 0.f ? -CUDART_INF_F : (mx + log2f(wsum)) * kMergeLn2;
-    return;
-  }
   float4* dst = reinterpret_cast<float4*>(a.out + grow * kDv);
 #pragma unroll
   for (int j = 0; j < 4; ++j)

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
   const int r = t * p.heads + h;                                   // row within the request
   const int64_t grow = static_cast<int64_t>(b) * T * p.heads + r;  // global row
   const int64_t pstride = static_cast<int64_t>(p.row_tiles) * kTileRows;
-  const MergeRowArgs a{p.q, p.scale_log2, p.o_part, p.lse_part, pstride, p.out, p.lse, p.out_bf16};
+  const MergeRowArgs a{p.q, p.scale_log2, p.o_part, p.lse_part, pstride, p.out, p.lse};
   // everything before the merge is independent of the prefix pass, which may
   // still be running (programmatic dependent launch)
   merge_row<true>(a, grow, static_cast<int64_t>(b) * p.max_splits * pstride + r, splits, n_vis,
