@@ -367,7 +367,8 @@ DDT_API int ddtree_kv_evict(const float* weight, const int32_t* slot_idx, const 
  *
  * ddtree_block_summary:
  *   mean of the block's rows (the sum is exact, the mean rounded once to fp32),
- *   scale = max |mean| / 127, summary = round to nearest even of mean / scale
+ *   scale = max |mean| * c, c the fp32 nearest to 1/127, summary = round to nearest
+ *   even of mean / scale, at most 127 in size
  *   from_len  int32 [B] device or NULL: only blocks that hold a position at or
  *             after from_len[b] are computed (after a decode step: the old length)
  *   summary   bf16 [B, N, 576]: integers in [-127, 127]
@@ -382,7 +383,8 @@ DDT_API int ddtree_block_summary(const void* kv_pool, const int32_t* slot_idx, c
 
 /*
  * ddtree_block_select: for every node t, the topk best of request b's blocks:
- *   qs_h = max |q[b][t][h]| / 127, q_int = round to nearest even of q / qs
+ *   qs_h = max |q[b][t][h]| * c, c the fp32 nearest to 1/127,
+ *   q_int = round to nearest even of q / qs, at most 127 in size
  *   score(t, j) = scale[b][j] * max over h of (qs_h * (q_int_h . summary[b][j]))
  * with both products rounded to fp32 (the integer dot product is exact).  The
  * first `first` and the last `last` blocks rank before all others, then the

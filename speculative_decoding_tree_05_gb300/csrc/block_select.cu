@@ -1,7 +1,7 @@
 // block_select.cu -- the blocks that each tree node reads: 8-bit query rows, and
 // the best blocks of a node's scores (the scores themselves: key_scores.cu).
 //
-//   query row r:  qs = max |q| / 127,  q_int = round(q / qs) in [-127, 127]
+//   query row r:  qs = max |q| * (1/127),  q_int = round(q / qs) in [-127, 127]
 //   score(t, j) = scale_j * max over the heads h of (qs_h * (q_int_h . summary_j))
 // The integer product is exact in fp32 and both roundings are fixed by this
 // order, so the ranking is the definition's on every run and tiling.
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kQuWarps * 32) quant_rows_kernel(QuantParams p
   }
   m = __reduce_max_sync(0xffffffffu, m);
   const bool finite = m < 0x7f80u;
-  const float scale = finite ? __fdiv_rn(__uint_as_float(m << 16), 127.f) : CUDART_NAN_F;
+  const float scale = finite ? __fmul_rn(__uint_as_float(m << 16), 1.f / 127.f) : CUDART_NAN_F;
   uint4* dst = reinterpret_cast<uint4*>(p.q_int + r * kDqk);
 #pragma unroll
   for (int i = 0; i < 3; ++i) {

@@ -2,7 +2,7 @@
 //
 // For block j of request b (positions [j n, j n + n), cut at the prefix's end):
 //   mean = (sum of its rows) / (rows)     576 dims
-//   scale = max |mean| / 127,  summary = round(mean / scale), integers in [-127, 127]
+//   scale = max |mean| * (1/127),  summary = round(mean / scale), integers in [-127, 127]
 // The integers are kept as bf16 (exact), the tensor cores' operand type: the
 // dot product of two such rows is an integer below 2^24, so block scores come
 // out exact in fp32 on any tiling.  The sums carry their rounding errors along
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtasPerSm) block_summary_kern
     if (g == 0) {
       am = fmaxf(fmaxf(amax_sh[0], amax_sh[1]), amax_sh[2]);
       const bool good = bad_sh[1] == 0;
-      const float scale = good ? __fdiv_rn(am, 127.f) : CUDART_NAN_F;
+      const float scale = good ? __fmul_rn(am, 1.f / 127.f) : CUDART_NAN_F;
       uint32_t w[4];
 #pragma unroll
       for (int d = 0; d < 4; ++d) {

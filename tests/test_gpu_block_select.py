@@ -37,7 +37,7 @@ def plain_summary(kv, slots):
     if not len(slots):
         return torch.zeros(576, dtype=torch.float32), 0.0
     mean = (kv[slots.long()].double().sum(0) / len(slots)).float().cpu()
-    scale = mean.abs().max() / 127
+    scale = mean.abs().max() * torch.tensor(np.float32(1) / np.float32(127))
     if not torch.isfinite(scale):
         return torch.zeros(576, dtype=torch.float32), float("nan")
     if scale == 0:
@@ -100,7 +100,7 @@ def plain_select(q, summary, scale, n, topk, first, last):
     qf = q.float().cpu().numpy()
     amax = np.abs(qf).max(1)
     with np.errstate(all="ignore"):
-        qs = (amax / np.float32(127)).astype(np.float32)
+        qs = (amax * (np.float32(1) / np.float32(127))).astype(np.float32)
         ok = np.isfinite(amax)
         qi = np.where((qs > 0)[:, None] & ok[:, None], np.clip(np.rint(qf / qs[:, None]), -127, 127), 0)
         dots = (qi.astype(np.float64) @ summary.float().cpu().numpy().astype(np.float64).T).astype(np.float32)
