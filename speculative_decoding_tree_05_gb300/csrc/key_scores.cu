@@ -149,11 +149,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
       const uint64_t d_k = smem_desc(base, 16, 1024, kSwizzle128B);
       const uint64_t d_q = smem_desc(base + kScOffQ, 16, 1024, kSwizzle128B);
       uint32_t n_unit = 0, n_stage = 0, n_tile = 0;
+      // A probe of a barrier takes as long as three MMAs, so each is probed a step
+      // before it is needed, while MMAs are being issued: the next stage of query
+      // rows, and at a tile's last stage the other score buffer.
+      bool q_ok = false, s_ok = false;
       for (int i = pair; ok && i < units; i += pairs) {
         if (!unit_at(p, i, &u)) continue;
         for (int qt = u.t0; ok && qt < u.t1; ++qt, ++n_tile) {
           const uint32_t buf = n_tile & 1;
-          if (n_tile >= 2 &&
+          if (n_tile >= 2 && !s_ok &&
               !mbar_wait_abortable(&sh.s_free[buf], ((n_tile >> 1) - 1) & 1, abort, true, __LINE__)) {
             ok = false;
             break;
@@ -170,11 +174,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
               fence_proxy_async_smem();  // the rows were written by cp.async
             }
             const uint32_t st = n_stage % kScStages;
-            if (!mbar_wait_abortable(&sh.q_full[st], (n_stage / kScStages) & 1, abort, false, __LINE__)) {
+            if (!q_ok && !mbar_wait_abortable(&sh.q_full[st], (n_stage / kScStages) & 1, abort, false, __LINE__)) {
               ok = false;
               break;
             }
             tc_fence_after();
+            const uint32_t next = n_stage + 1;
+            q_ok = mbar_test_wait(&sh.q_full[next % kScStages], (next / kScStages) & 1);
+            if (g == 2) s_ok = n_tile >= 1 && mbar_test_wait_cluster(&sh.s_free[buf ^ 1], (((n_tile + 1) >> 1) - 1) & 1);
             const uint64_t a = desc_advance(d_k, g * kScGroupBytes), q = desc_advance(d_q, st * kScStageBytes);
 #pragma unroll
             for (int k = 0; k < 12; ++k) {
@@ -381,7 +388,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(buf ? free1 : free0);
+        // relaxed: the scores are in registers, and no store has to be seen (a
+        // release at cluster scope took 1900 cycles here, most of a tile)
+        if (lane == 0) mbar_arrive_remote_relaxed(buf ? free1 : free0);
       }
       if (bar_red_or(3, 256, !ok)) {
         ok = false;
