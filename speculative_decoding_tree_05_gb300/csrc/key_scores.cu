@@ -18,8 +18,9 @@
 //   warp 1        lane 0 loads its half of the query rows by TMA: 3 stages of 192 dims
 //                 (a wait costs the issuing thread as much as three MMAs: 12 MMAs a stage)
 //   warp 2        in CTA 1, lane 0 tells CTA 0 which key groups have landed
-//   warps 4-11    two epilogue sets: one key per thread, set s takes the query
-//                 tiles of parity s
+//   warps 4-11    two epilogue sets: one key per thread, each set takes half of a
+//                 tile's query rows, so that a score buffer is free again well
+//                 before the tensor core has filled the other one
 //   warps 12-19   gather the key rows by 16-byte cp.async, zero-filled where
 //                 there is no key, into three 192-dim groups.  A group is
 //                 refilled as soon as the last query tile has used it, so with
@@ -57,7 +58,7 @@ struct ScShared {
   uint64_t q_full[kScStages];   // CTA 0: both halves of the stage have landed
   uint64_t q_empty[kScStages];
   uint64_t s_full[2];
-  uint64_t s_free[2];           // CTA 0: the 8 epilogue warps of the pair have read the scores
+  uint64_t s_free[2];           // CTA 0: the 16 epilogue warps of the pair have read the scores
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -68,13 +69,23 @@ __device__ __forceinline__ int clamp_len(const int32_t* prefix_len, int b, int m
   return L < 0 ? 0 : (L > max_len ? max_len : L);
 }
 
-// 32 consecutive columns of two accumulators of this thread's TMEM lane, added.
-__device__ __forceinline__ void tmem_ld32_sum(uint32_t a, uint32_t b, float (&v)[32]) {
-  float w[32];
-  tmem_ld32(a, v);
-  tmem_ld32(b, w);
+// 16 consecutive columns of two accumulators of this thread's TMEM lane, added.
+__device__ __forceinline__ void tmem_ld16_sum(uint32_t a, uint32_t b, float (&v)[16]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+      "[%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(a), "r"(b)
+      : "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] += w[i];
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]) + __uint_as_float(r[16 + i]);
 }
 
 // Keys of request b: positions, or blocks of positions.
@@ -122,7 +133,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_free[i], 8);
+      mbar_init(&sh.s_free[i], 16);
     }
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
@@ -138,8 +149,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
   const uint32_t tmem = sh.tmem_base;
   const int units = p.units;
   bool ok = true;
-  // with more heads than tile rows a node spans tiles, so one set takes them all
-  const bool two_sets = kMode == kScoreWeight || p.heads <= kScoreTileRows;
 
   // every role walks the same units: those of its pair that hold keys
   ScUnit u;
@@ -302,23 +311,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
       float acc = kMode == kScoreWeight ? 0.f : -CUDART_INF_F;
       const float key_scale = kMode == kScoreBlock && j < n ? __ldg(p.key_scale + b * p.key_stride + j) : 0.f;
       int node = 0, left = p.heads;  // kScoreBlock: the node that the next row belongs to, its rows left
+      // the set's columns [cb, ce) of a tile: half of its 16-column steps, or of its
+      // nodes; with more heads than tile rows a node spans tiles and set 0 takes them all
+      int cb, ce;
+      if (kMode == kScoreWeight) {
+        const int mid = (p.tile_n / 16 + 1) / 2 * 16;
+        cb = set ? mid : 0;
+        ce = set ? p.tile_n : mid;
+      } else {
+        const int mid = p.heads <= kScoreTileRows ? (p.tile_rows / p.heads + 1) / 2 * p.heads : p.tile_rows;
+        cb = set ? mid : 0;
+        ce = set ? p.tile_rows : mid;
+      }
+      // row constants of a tile: weights -lse in log2 units, -inf where a row counts for nothing
+      auto row_const = [&](int qt) -> float {
+        const int row = qt * p.tile_rows + r;
+        const bool in = r < p.tile_rows && row < p.rows && qt < u.t1;
+        if (kMode == kScoreBlock) return in ? __ldcg(p.row_aux + static_cast<int64_t>(b) * p.rows + row) : CUDART_NAN_F;
+        const float l = in ? __ldcg(p.row_aux + static_cast<int64_t>(b) * p.rows + row) : CUDART_INF_F;
+        return fabsf(l) == CUDART_INF_F ? -CUDART_INF_F : -l * kScLog2e;
+      };
+      float a_next = row_const(u.t0);
       for (int qt = u.t0; ok && qt < u.t1; ++qt, ++n_tile) {
-        if ((two_sets ? static_cast<int>(n_tile & 1) : 0) != set) continue;
         const uint32_t buf = n_tile & 1;
         const int row0 = qt * p.tile_rows;
         const int live = min(p.tile_rows, p.rows - row0);
-        // row constants of the tile: weights -lse in log2 units, -inf where a row counts for nothing
         bar_sync(1 + set, 128);  // the last tile's are read
-        {
-          float a;
-          if (kMode == kScoreWeight) {
-            const float l = r < live ? __ldcg(p.row_aux + static_cast<int64_t>(b) * p.rows + row0 + r) : CUDART_INF_F;
-            a = fabsf(l) == CUDART_INF_F ? -CUDART_INF_F : -l * kScLog2e;
-          } else {
-            a = r < live ? __ldcg(p.row_aux + static_cast<int64_t>(b) * p.rows + row0 + r) : CUDART_NAN_F;
-          }
-          aux[r] = a;
-        }
+        aux[r] = a_next;
+        a_next = row_const(qt + 1);
         // the set leaves together if a wait of one of its warps ran out
         const bool got = mbar_wait_abortable(&sh.s_full[buf], (n_tile >> 1) & 1, abort, false, __LINE__);
         if (bar_red_or(1 + set, 128, !got)) {
@@ -326,17 +346,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
           break;
         }
         tc_fence_after();
-        if (kMode == kScoreBlock && two_sets) node = row0 / p.heads;
+        if (kMode == kScoreBlock && p.heads <= kScoreTileRows) node = (row0 + cb) / p.heads;
         const uint32_t col = tmem + lane_off + buf * 2 * kScoreTileRows;
-        for (int c = 0; c < p.tile_n; c += 32) {
-          float s[32];
-          tmem_ld32_sum(col + c, col + kScoreTileRows + c, s);
+        // steps of 16 columns from a multiple of 16 on: none reaches past the accumulator
+        for (int c = cb & ~15; c < ce; c += 16) {
+          float s[16];
+          tmem_ld16_sum(col + c, col + kScoreTileRows + c, s);
           if (kMode == kScoreWeight) {
-            const bool all_live = __all_sync(0xffffffffu, aux[c + lane] != -CUDART_INF_F);
+            const bool all_live = __all_sync(0xffffffffu, aux[c + (lane & 15)] != -CUDART_INF_F);
             float t[4] = {0.f, 0.f, 0.f, 0.f};
             if (all_live) {
 #pragma unroll
-              for (int k = 0; k < 32; k += 4) {
+              for (int k = 0; k < 16; k += 4) {
                 const float4 a = *reinterpret_cast<const float4*>(aux + c + k);
                 t[0] += fast_exp2(fmaf(s[k], p.scale_log2, a.x));
                 t[1] += fast_exp2(fmaf(s[k + 1], p.scale_log2, a.y));
@@ -346,14 +367,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
             } else {
               // a row without weight may hold anything, NaN included: it is left out, not multiplied by zero
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
+              for (int k = 0; k < 16; ++k) {
                 const float a = aux[c + k];
                 t[k & 3] += a == -CUDART_INF_F ? 0.f : fast_exp2(fmaf(s[k], p.scale_log2, a));
               }
             }
             acc += (t[0] + t[1]) + (t[2] + t[3]);
           } else {
-            const int nc = min(32, live - c);
+            const int k0 = max(0, cb - c), nc = min(min(16, ce - c), live - c);
             // both products are rounded to 32 bits: part of the definition of the score; fmaxf drops a NaN scale
             auto emit = [&] {
               if (j < n)
@@ -364,8 +385,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
             };
             if (p.heads % 8 == 0) {  // nodes (and so the live rows) end on multiples of 8
 #pragma unroll
-              for (int k = 0; k < 32; k += 8) {
-                if (k < nc) {
+              for (int k = 0; k < 16; k += 8) {
+                if (k >= k0 && k < nc) {
                   const float4 a = *reinterpret_cast<const float4*>(aux + c + k);
                   const float4 d = *reinterpret_cast<const float4*>(aux + c + k + 4);
                   const float m0 = fmax3(__fmul_rn(s[k], a.x), __fmul_rn(s[k + 1], a.y), __fmul_rn(s[k + 2], a.z));
@@ -377,8 +398,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                if (k < nc) {
+              for (int k = 0; k < 16; ++k) {
+                if (k >= k0 && k < nc) {
                   acc = fmaxf(acc, __fmul_rn(s[k], aux[c + k]));
                   if (--left == 0) emit();
                 }

@@ -138,6 +138,7 @@ def select_case(batch, lens, nodes, heads, block, topk, first, last, seed=0, twe
     (1, [1], 1, 1, 16, 1, 0, 0), (1, [5000], 3, 16, 16, 8, 0, 1), (2, [2048, 100], 9, 16, 64, 4, 1, 2),
     (1, [9000], 2, 3, 16, 40, 0, 0), (1, [4097], 5, 24, 32, 17, 2, 2), (1, [4096], 2, 128, 32, 32, 1, 1),
     (1, [3000], 2, 300, 32, 9, 0, 0), (1, [3000], 2, 1024, 64, 9, 0, 0), (3, [1, 17, 40000], 4, 16, 16, 300, 0, 0),
+    (1, [2000], 9, 40, 32, 11, 0, 0), (1, [2000], 40, 7, 32, 11, 0, 0), (1, [900], 3, 72, 16, 7, 0, 0),
     (2, [640, 64], 65, 16, 64, 20, 0, 0), (1, [300], 4, 16, 16, 3, 5, 5), (1, [280000], 1, 2, 16, 64, 1, 4),
 ])
 def test_select(batch, lens, nodes, heads, block, topk, first, last):
