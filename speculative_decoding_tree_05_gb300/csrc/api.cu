@@ -39,7 +39,7 @@ int device_info(DeviceInfo* out) {
         cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
         major == 10 && minor == 3 && configure_prefix() == cudaSuccess && configure_tail_merge() == cudaSuccess &&
         configure_scores() == cudaSuccess && configure_evict() == cudaSuccess && configure_topk() == cudaSuccess &&
-        configure_block_attn() == cudaSuccess)
+        configure_block_attn() == cudaSuccess && configure_summary() == cudaSuccess)
       d.ok = true;
     g_dev[dev] = d;
   });

@@ -9,8 +9,13 @@
 // (two-sum), so the mean is the exact sum's, rounded once, and no integer depends
 // on the order of the rows.
 //
-// Bound by memory: each row is read once (1152 B).  One CTA of 288 threads per
-// block: thread (g, c) adds the 16-byte piece c of rows g, g + 4, ...
+// Bound by memory: each row is read once (1152 B).  One CTA per SM: four
+// warps keep up to five stages of 32 rows on their way into shared memory (one
+// bulk copy a row; a copy takes its warp about 85 cycles to issue, so one warp
+// stayed at 3.3 TB/s), 288 threads add them up, thread (g, c) the 16-byte piece c of
+// rows g, g + 4, ....  Loading through registers, 110 KB in flight per SM while
+// loading and none while reducing, stayed at 3.6-3.9 TB/s for scattered rows
+// (185000 rows: 55-61 us); the ring is never empty.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include "cache_ops.cuh"
@@ -20,10 +25,25 @@ namespace ddt {
 namespace {
 
 constexpr int kSumGroups = 4;
-constexpr int kSumThreads = kSumGroups * kChunks;  // 288
-constexpr int kSumBatch = 8;                       // rows in flight per thread
-constexpr int kMaxBlock = 128;
-constexpr int kSumCtasPerSm = 3;                   // resident at 72 registers
+constexpr int kSumThreads = kSumGroups * kChunks;  // 288 that add up a block
+constexpr int kSumTeams = 2;
+constexpr int kSumCopiers = 4;                     // and the warps that copy
+constexpr int kSumWarps = kSumThreads / 32;
+constexpr int kSumRows = 32;                       // rows of a stage
+constexpr int kSumStages = 5;
+constexpr int kSumStageBytes = kSumRows * kRowBytes;
+
+struct SumShared {
+  uint64_t full[kSumStages], empty[kSumStages];
+  alignas(4) uint8_t rows[kSumStages][kSumCopiers];           // the stage's rows that exist, 8 a copying warp
+  float amax[kSumTeams][kSumWarps];
+  int abort;
+};
+constexpr int kSumOffPart = kSumStages * kSumStageBytes;  // [4 groups][hi, lo][576]
+constexpr int kSumPart = kSumGroups * 2 * kDqk;           // floats of a team
+constexpr int kSumOffShared = kSumOffPart + kSumTeams * kSumPart * 4;
+constexpr int kSumBlockThreads = kSumTeams * kSumThreads + 32 * kSumCopiers;
+constexpr int kSumSmem = kSumOffShared + static_cast<int>(sizeof(SumShared)) + 16;
 
 // (hi, lo) + x without losing the rounding error of hi + x, two dims at a time
 // (the additions are half of the kernel's instructions: paired ones halve them)
@@ -34,12 +54,11 @@ __device__ __forceinline__ void two_sum(uint64_t& hi, uint64_t& lo, uint64_t x) 
   hi = s;
 }
 
-__global__ void __launch_bounds__(kSumThreads, kSumCtasPerSm) block_summary_kernel(SummaryParams p) {
-  __shared__ int slot_sh[kMaxBlock];
-  __shared__ __align__(16) float part[kSumGroups - 1][2][kDqk];
-  __shared__ float amax_sh[3];
-  __shared__ int bad_sh[2];
-  const int tid = threadIdx.x, g = tid / kChunks, c = tid - g * kChunks;
+__global__ void __launch_bounds__(kSumBlockThreads, 1) block_summary_kernel(SummaryParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  SumShared& sh = *reinterpret_cast<SumShared*>(smem + kSumOffShared);
+  volatile int* abort = &sh.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.y;
   int L = __ldg(p.prefix_len + b);
   if (L < 0 || L > p.max_prefix_len) {
@@ -47,128 +66,181 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtasPerSm) block_summary_kern
     L = L < 0 ? 0 : p.max_prefix_len;
   }
   const int from = p.from_len != nullptr ? max(0, __ldg(p.from_len + b)) : 0;
-  if (from >= L) return;
-  const int n_blocks = (L + p.block - 1) / p.block;
-  auto slot_of = [&](int j) {  // of this thread's position in block j
-    const int64_t pos = static_cast<int64_t>(j) * p.block + tid;
-    return tid < p.block && pos < L ? __ldg(p.slot_idx + static_cast<int64_t>(b) * p.slot_stride + pos) : -1;
-  };
-  const int j0 = from / p.block + blockIdx.x;
-  int slot = slot_of(j0);
-  for (int j = j0; j < n_blocks; j += gridDim.x) {
-    const int pos0 = j * p.block, n = min(p.block, L - pos0);
-    if (tid == 0) bad_sh[0] = bad_sh[1] = 0;
-    __syncthreads();
-    if (tid < n) {
-      if (slot < 0 || slot >= p.pool_slots) {
-        atomicOr(p.status, kStatusBadSlot);
-        atomicAdd(&bad_sh[0], 1);
-        slot = -1;
-      }
-      slot_sh[tid] = slot;
+  const int n_blocks = L > 0 ? (L - 1) / p.block + 1 : 0;
+  const int j0 = from / p.block + static_cast<int>(blockIdx.x), step = static_cast<int>(gridDim.x);
+  if (from >= L || j0 >= n_blocks) return;
+  if (tid == 0) {
+    for (int i = 0; i < kSumStages; ++i) {
+      mbar_init(&sh.full[i], kSumCopiers);
+      mbar_init(&sh.empty[i], kSumWarps);
     }
-    __syncthreads();
-    slot = slot_of(j + gridDim.x);  // the next block's, while this one's rows travel
-    uint64_t hi2[4], lo2[4];
-#pragma unroll
-    for (int d = 0; d < 4; ++d) hi2[d] = lo2[d] = 0;
-    for (int r0 = g; r0 < n; r0 += kSumGroups * kSumBatch) {
-      uint4 v[kSumBatch];
-#pragma unroll
-      for (int u = 0; u < kSumBatch; ++u) {
-        const int r = r0 + u * kSumGroups;
-        const int s = r < n ? slot_sh[r] : -1;
-        v[u] = s >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.kv + static_cast<int64_t>(s) * kDqk) + c)
-                      : make_uint4(0, 0, 0, 0);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int chunks = (p.block + kSumRows - 1) / kSumRows;  // stages of a block
+  bool ok = true;
+
+  if (warp >= kSumTeams * kSumWarps) {
+    // ------------------------------------------------------------------ copies: a warp takes 8 rows of the stage
+    const int k = warp - kSumTeams * kSumWarps, row8 = 8 * k + (lane & 7);
+    const int32_t* slots = p.slot_idx + static_cast<int64_t>(b) * p.slot_stride;
+    // the slots of a stage are read two stages before its copies
+    struct At {
+      int64_t j;  // block (past the last one once the walk is over)
+      int c;      // stage of the block
+    };
+    auto next_of = [&](At x) -> At { return x.c + 1 < chunks ? At{x.j, x.c + 1} : At{x.j + step, 0}; };
+    auto pos_of = [&](At x) -> int64_t {
+      const int row = x.c * kSumRows + row8;
+      const int64_t pos = x.j * p.block + row;
+      return lane < 8 && x.j < n_blocks && row < p.block && pos < L ? pos : -1;
+    };
+    auto slot_of = [&](At x) -> int {
+      const int64_t pos = pos_of(x);
+      return pos >= 0 ? __ldg(slots + pos) : -1;
+    };
+    At at{j0, 0}, at1 = next_of(at), at2 = next_of(at1);
+    int s0 = slot_of(at), s1 = slot_of(at1);
+    uint32_t n = 0;  // stages filled
+    while (at.j < n_blocks) {
+      const int s2 = slot_of(at2);
+      const uint32_t st = n % kSumStages;
+      const bool w = n < kSumStages || mbar_wait_abortable(&sh.empty[st], ((n / kSumStages) - 1) & 1, abort, false, __LINE__);
+      if (!__all_sync(0xffffffffu, w)) {
+        ok = false;
+        break;
       }
+      const bool here = pos_of(at) >= 0, good = here && s0 >= 0 && s0 < p.pool_slots;
+      if (here && !good) atomicOr(p.status, kStatusBadSlot);
+      const uint32_t rows = __ballot_sync(0xffffffffu, good);
+      if (lane == 0) {
+        sh.rows[st][k] = static_cast<uint8_t>(rows);
+        mbar_arrive_expect_tx(&sh.full[st], __popc(rows) * kRowBytes);
+      }
+      __syncwarp();
+      if (good) bulk_load(smem_u32(smem) + st * kSumStageBytes + row8 * kRowBytes, p.kv + static_cast<int64_t>(s0) * kDqk, kRowBytes, &sh.full[st]);
+      ++n;
+      s0 = s1;
+      s1 = s2;
+      at = at1;
+      at1 = at2;
+      at2 = next_of(at2);
+    }
+    // no copy is in flight when the CTA exits (after a give-up the adders leave stages unread)
+    for (uint32_t i = n > kSumStages ? n - kSumStages : 0; i < n; ++i) mbar_wait(&sh.full[i % kSumStages], (i / kSumStages) & 1);
+  } else {
+    // ------------------------------------------------------------------ sums
+    const int team = tid / kSumThreads, tt = tid - team * kSumThreads, tw = warp - team * kSumWarps;
+    const int g = tt / kChunks, c = tt - g * kChunks;
+    float* part = reinterpret_cast<float*>(smem + kSumOffPart) + team * kSumPart;
+    uint32_t n = team * chunks;  // stages before this block
+    bool failed = false;
+    for (int64_t j = j0 + static_cast<int64_t>(team) * step; j < n_blocks; j += kSumTeams * step, n += (kSumTeams - 1) * chunks) {
+      uint64_t hi[4], lo[4];
 #pragma unroll
-      for (int u = 0; u < kSumBatch; ++u) {
-        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      for (int d = 0; d < 4; ++d) hi[d] = lo[d] = 0;
+      int count = 0;
+      auto add = [&](const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          two_sum(hi2[d], lo2[d], f32x2(__uint_as_float(w[d] << 16), __uint_as_float(w[d] & 0xffff0000u)));
-      }
-    }
-    if (g > 0) {
+          two_sum(hi[d], lo[d], f32x2(__uint_as_float(w[d] << 16), __uint_as_float(w[d] & 0xffff0000u)));
+      };
+      for (int ch = 0; ch < chunks; ++ch, ++n) {
+        const uint32_t st = n % kSumStages;
+        if (!mbar_wait_abortable(&sh.full[st], (n / kSumStages) & 1, abort, false, __LINE__)) failed = true;
+        __syncwarp();
+        const uint32_t rows = *reinterpret_cast<const uint32_t*>(sh.rows[st]);
+        count += __popc(rows);
+        const uint4* src = reinterpret_cast<const uint4*>(smem + st * kSumStageBytes + g * kRowBytes) + c;
+        constexpr int kEach = kSumRows / kSumGroups;
+        if (rows == 0xffffffffu) {
+          uint4 v[kEach];
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        reinterpret_cast<uint64_t*>(part[g - 1][0])[4 * c + d] = hi2[d];
-        reinterpret_cast<uint64_t*>(part[g - 1][1])[4 * c + d] = lo2[d];
-      }
-    }
-    __syncthreads();
-    // group 0 (72 threads) adds the others' sums and finishes the block
-    const int count = n - bad_sh[0];
-    const float rows = static_cast<float>(max(count, 1));
-    float mean[8], am = 0.f;
-    bool finite = true;
-    if (g == 0) {
-      float hi[8], lo[8];
+          for (int u = 0; u < kEach; ++u) v[u] = src[u * kSumGroups * kChunks];
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-#pragma unroll
-        for (int o = 0; o < kSumGroups - 1; ++o) {
-          two_sum(hi2[d], lo2[d], reinterpret_cast<const uint64_t*>(part[o][0])[4 * c + d]);
-          lo2[d] = add_x2(lo2[d], reinterpret_cast<const uint64_t*>(part[o][1])[4 * c + d]);
+          for (int u = 0; u < kEach; ++u) add(v[u]);
+        } else {
+#pragma unroll 2
+          for (int u = 0; u < kEach; ++u)
+            if ((rows >> (u * kSumGroups + g)) & 1u) add(src[u * kSumGroups * kChunks]);
         }
-        f32x2_split(hi2[d], hi[2 * d], hi[2 * d + 1]);
-        f32x2_split(lo2[d], lo[2 * d], lo[2 * d + 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[st]);
       }
+      uint64_t* mine = reinterpret_cast<uint64_t*>(part + g * 2 * kDqk) + 4 * c;
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
+      for (int d = 0; d < 4; ++d) {
+        mine[d] = hi[d];
+        mine[kDqk / 2 + d] = lo[d];
+      }
+      if (bar_red_or(1 + team, kSumThreads, failed)) {
+        ok = false;
+        break;
+      }
+      // dims 2 tt and 2 tt + 1: the four groups' sums, the mean, the largest of all
+      const uint64_t* all = reinterpret_cast<const uint64_t*>(part) + tt;
+      uint64_t h2 = all[0], l2 = all[kDqk / 2];
+#pragma unroll
+      for (int o = 1; o < kSumGroups; ++o) {
+        two_sum(h2, l2, all[o * kDqk]);
+        l2 = add_x2(l2, all[o * kDqk + kDqk / 2]);
+      }
+      float hs[2], ls[2], mean[2];
+      f32x2_split(h2, hs[0], hs[1]);
+      f32x2_split(l2, ls[0], ls[1]);
+      const float n_rows = static_cast<float>(max(count, 1));
+      float am = 0.f;
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
         // (hi + lo) / rows in fp32 pairs: the quotient of hi, and that of what is
         // left of hi and lo (64-bit division is slow here and would cost more than the sums)
-        const float q = __fdiv_rn(hi[d], rows);
-        const float m = __fadd_rn(q, __fdiv_rn(__fadd_rn(__fmaf_rn(-q, rows, hi[d]), lo[d]), rows));
+        const float q = __fdiv_rn(hs[d], n_rows);
+        const float m = __fadd_rn(q, __fdiv_rn(__fadd_rn(__fmaf_rn(-q, n_rows, hs[d]), ls[d]), n_rows));
         mean[d] = count > 0 ? m : 0.f;
         // an infinite row leaves a NaN in the carried error: any non-finite sum counts as such
-        finite = finite && fabsf(mean[d]) < CUDART_INF_F;
-        am = fmaxf(am, fabsf(mean[d]));
+        am = fabsf(mean[d]) < CUDART_INF_F ? fmaxf(am, fabsf(mean[d])) : CUDART_INF_F;
       }
-    }
-    if (tid < 96) {  // three warps hold the 72 threads
-      const bool all = __all_sync(0xffffffffu, finite);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
-      if ((tid & 31) == 0) {
-        amax_sh[tid >> 5] = am;
-        if (!all) bad_sh[1] = 1;
-      }
-    }
-    __syncthreads();
-    if (g == 0) {
-      am = fmaxf(fmaxf(amax_sh[0], amax_sh[1]), amax_sh[2]);
-      const bool good = bad_sh[1] == 0;
+      if (lane == 0) sh.amax[team][tw] = am;
+      bar_sync(1 + team, kSumThreads);  // (and the partial sums are read)
+#pragma unroll
+      for (int i = 0; i < kSumWarps; ++i) am = fmaxf(am, sh.amax[team][i]);
+      const bool good = am < CUDART_INF_F;
       const float scale = good ? __fmul_rn(am, 1.f / 127.f) : CUDART_NAN_F;
-      uint32_t w[4];
+      uint32_t two = 0;
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        uint32_t two = 0;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float q = 0.f;
-          if (good && scale > 0.f) q = fminf(fmaxf(rintf(__fdiv_rn(mean[2 * d + e], scale)), -127.f), 127.f);
-          two |= (__float_as_uint(q) >> 16) << (16 * e);  // an integer of 7 bits and sign: exact in bf16
-        }
-        w[d] = two;
+      for (int d = 0; d < 2; ++d) {
+        float q = 0.f;
+        if (good && scale > 0.f) q = fminf(fmaxf(rintf(__fdiv_rn(mean[d], scale)), -127.f), 127.f);
+        two |= (__float_as_uint(q) >> 16) << (16 * d);  // an integer of 7 bits and sign: exact in bf16
       }
-      const int64_t at = static_cast<int64_t>(b) * p.blocks + j;
-      reinterpret_cast<uint4*>(p.summary + at * kDqk)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-      if (c == 0) p.scale[at] = scale;
+      const int64_t out = static_cast<int64_t>(b) * p.blocks + j;
+      reinterpret_cast<uint32_t*>(p.summary + out * kDqk)[tt] = two;
+      if (tt == 0) p.scale[out] = scale;
     }
-    __syncthreads();
+  }
+  if (!ok) {
+    *abort = 1;
+    atomicOr(p.status, kStatusTimeout);
   }
 }
 
 }  // namespace
 
+cudaError_t configure_summary() {
+  return cudaFuncSetAttribute(block_summary_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSumSmem);
+}
+
 cudaError_t launch_block_summary(const SummaryParams& p, int batch, int sm_count, cudaStream_t stream) {
   if (batch == 0 || p.blocks == 0) return cudaSuccess;
-  // blocks of a request are dealt to at most enough CTAs to fill the GPU: how
-  // many are touched (from_len) is known on the device only
-  const int64_t fill = (int64_t(sm_count) * kSumCtasPerSm + batch - 1) / batch;
-  const unsigned gx = static_cast<unsigned>(p.blocks < fill ? p.blocks : fill);
-  block_summary_kernel<<<dim3(gx, batch), kSumThreads, 0, stream>>>(p);
+  // blocks of a request are dealt to its share of the SMs: how many are touched
+  // (from_len) is known on the device only
+  const int share = (sm_count + batch - 1) / batch;
+  const unsigned gx = static_cast<unsigned>(p.blocks < share ? p.blocks : share);
+  block_summary_kernel<<<dim3(gx, batch), kSumBlockThreads, kSumSmem, stream>>>(p);
   return cudaGetLastError();
 }
 

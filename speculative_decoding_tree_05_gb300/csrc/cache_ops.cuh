@@ -95,6 +95,7 @@ struct SummaryParams {
   int32_t slot_stride, max_prefix_len, block, blocks;
   int32_t* status;
 };
+cudaError_t configure_summary();
 cudaError_t launch_block_summary(const SummaryParams& p, int batch, int sm_count, cudaStream_t stream);
 
 struct QuantParams {
