@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kSumBlockThreads, 1) block_summary_kernel(Summ
   if (tid == 0) {
     for (int i = 0; i < kSumStages; ++i) {
       mbar_init(&sh.full[i], kSumCopiers);
-      mbar_init(&sh.empty[i], kSumWarps);
+      mbar_init(&sh.empty[i], kSumTeams * kSumWarps);
     }
     sh.abort = 0;
     fence_mbar_init();
@@ -134,9 +134,28 @@ __global__ void __launch_bounds__(kSumBlockThreads, 1) block_summary_kernel(Summ
     const int team = tid / kSumThreads, tt = tid - team * kSumThreads, tw = warp - team * kSumWarps;
     const int g = tt / kChunks, c = tt - g * kChunks;
     float* part = reinterpret_cast<float*>(smem + kSumOffPart) + team * kSumPart;
-    uint32_t n = team * chunks;  // stages before this block
+    // A team passes the other's stages too: it waits for them to land and hands
+    // them back at once.  A barrier's parity tells a phase from the next one only,
+    // so no thread may fall a phase behind or get one ahead.
+    uint32_t n = 0;  // stages passed
     bool failed = false;
-    for (int64_t j = j0 + static_cast<int64_t>(team) * step; j < n_blocks; j += kSumTeams * step, n += (kSumTeams - 1) * chunks) {
+    auto land = [&](uint32_t i) {
+      if (!mbar_wait_abortable(&sh.full[i % kSumStages], (i / kSumStages) & 1, abort, false, __LINE__)) failed = true;
+      __syncwarp();
+    };
+    auto hand_back = [&](uint32_t i) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[i % kSumStages]);
+    };
+    int turn = 0;
+    for (int64_t j = j0; j < n_blocks; j += step, turn = turn + 1 == kSumTeams ? 0 : turn + 1) {
+      if (turn != team) {
+        for (int ch = 0; ch < chunks; ++ch, ++n) {
+          land(n);
+          hand_back(n);
+        }
+        continue;
+      }
       uint64_t hi[4], lo[4];
 #pragma unroll
       for (int d = 0; d < 4; ++d) hi[d] = lo[d] = 0;
@@ -149,8 +168,7 @@ __global__ void __launch_bounds__(kSumBlockThreads, 1) block_summary_kernel(Summ
       };
       for (int ch = 0; ch < chunks; ++ch, ++n) {
         const uint32_t st = n % kSumStages;
-        if (!mbar_wait_abortable(&sh.full[st], (n / kSumStages) & 1, abort, false, __LINE__)) failed = true;
-        __syncwarp();
+        land(n);
         const uint32_t rows = *reinterpret_cast<const uint32_t*>(sh.rows[st]);
         count += __popc(rows);
         const uint4* src = reinterpret_cast<const uint4*>(smem + st * kSumStageBytes + g * kRowBytes) + c;
@@ -166,8 +184,7 @@ __global__ void __launch_bounds__(kSumBlockThreads, 1) block_summary_kernel(Summ
           for (int u = 0; u < kEach; ++u)
             if ((rows >> (u * kSumGroups + g)) & 1u) add(src[u * kSumGroups * kChunks]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[st]);
+        hand_back(n);
       }
       uint64_t* mine = reinterpret_cast<uint64_t*>(part + g * 2 * kDqk) + 4 * c;
 #pragma unroll
