@@ -9,13 +9,13 @@
 // (two-sum), so the mean is the exact sum's, rounded once, and no integer depends
 // on the order of the rows.
 //
-// Bound by memory: each row is read once (1152 B).  One CTA per SM: four
-// warps keep up to five stages of 32 rows on their way into shared memory (one
-// bulk copy a row; a copy takes its warp about 85 cycles to issue, so one warp
-// stayed at 3.3 TB/s), 288 threads add them up, thread (g, c) the 16-byte piece c of
-// rows g, g + 4, ....  Loading through registers, 110 KB in flight per SM while
-// loading and none while reducing, stayed at 3.6-3.9 TB/s for scattered rows
-// (185000 rows: 55-61 us); the ring is never empty.
+// Bound by memory: each row is read once (1152 B).  One CTA per SM: four warps
+// keep up to four stages of 32 rows on their way into shared memory (one bulk
+// copy a row; a copy takes its warp about 85 cycles to issue, so one warp stayed
+// at 3.3 TB/s), and three teams of 288 threads add up every third block each,
+// thread (g, c) of a team the 16-byte piece c of rows g, g + 4, ....  185000
+// scattered rows: 51 us (two teams 53, one 70; loads through registers, which
+// leave the memory idle while a block is reduced, 55-61).
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include "cache_ops.cuh"
@@ -26,11 +26,11 @@ namespace {
 
 constexpr int kSumGroups = 4;
 constexpr int kSumThreads = kSumGroups * kChunks;  // 288 that add up a block
-constexpr int kSumTeams = 2;
+constexpr int kSumTeams = 3;
 constexpr int kSumCopiers = 4;                     // and the warps that copy
 constexpr int kSumWarps = kSumThreads / 32;
 constexpr int kSumRows = 32;                       // rows of a stage
-constexpr int kSumStages = 5;
+constexpr int kSumStages = 4;
 constexpr int kSumStageBytes = kSumRows * kRowBytes;
 
 struct SumShared {

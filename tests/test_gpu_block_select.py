@@ -64,6 +64,20 @@ def test_summary(block, heavy):
             assert torch.equal(summary[b, j].float().cpu(), want)
 
 
+@pytest.mark.parametrize("block", [16, 64, 128])
+def test_summary_of_many_blocks(block):
+    """Enough blocks that every stage buffer is used many times over."""
+    lens = [60000, 9000, 31]
+    kv, slot, n = pool_of(lens, seed=block)
+    summary, scale = ddtree.block_summary(kv, slot, n, block)
+    for b, L in enumerate(lens):
+        whole = L // block * block
+        mean = kv[slot[b, :whole].long()].double().reshape(-1, block, 576).mean(1).float()
+        want = mean.abs().amax(-1) * (torch.ones((), device="cuda") / torch.full((), 127.0, device="cuda"))
+        assert torch.equal(scale[b, :L // block], want)
+        assert torch.equal(summary[b, :L // block].float(), torch.round(mean / want[:, None]).clamp(-127, 127))
+
+
 def test_summary_update_after_a_step():
     lens = [200, 64, 65, 33]
     kv, slot, n = pool_of(lens, seed=9)
