@@ -25,9 +25,9 @@
 //                raised (and O^T rescaled) only when a score exceeds it by 2^8
 //   warp 9       one lane issues P.V(t) when P(t) is written
 //   warps 10-17  gather 64 keys per stage, two stages of four dim groups, each
-//                refilled as soon as its part of P.V is done: warps 10-13 the first
-//                two groups (5 of 9 chunks) by 16-byte cp.async, warps 14-17 the
-//                others by TMA gather4 (85 cycles an instruction and warp), at the
+//                refilled as soon as its part of P.V is done: warps 10-13 the latent
+//                chunks of the first two groups (4 of 9) by 16-byte cp.async, warps
+//                14-17 the others by TMA gather4 (85 cycles an instruction and warp), at the
 //                same time: an SM gathers about 24 B/clk either way and 34 both
 //                ways (L2-resident rows)
 // What bounds it: a stage lives from its load through S, the softmax and P.V, and
@@ -135,28 +135,15 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
   const Group u = group_of(p, g);
   int L = __ldg(p.prefix_len + u.b);
   L = L < 0 ? 0 : (L > p.max_prefix_len ? p.max_prefix_len : L);
-  grid_dep_launch();  // the tail/merge kernel
-  grid_dep_wait();    // the lists
-  const int count = __ldcg(p.list_len + g);
-  const BlockEntry* list = p.list + static_cast<int64_t>(g) * p.list_cap;
-  const int64_t keys = static_cast<int64_t>(count) * p.block;
-  const int64_t all_tiles = (keys + kBaKeys - 1) / kBaKeys;
-  const int t0 = static_cast<int>(all_tiles * split / p.splits);
-  const int n = static_cast<int>(all_tiles * (split + 1) / p.splits) - t0;  // tiles of this unit
+  grid_dep_launch();  // the merge kernel
   const int64_t prow0 = (static_cast<int64_t>(u.b) * p.splits + split) * p.pstride + u.row0;
-
-  if (n == 0) {  // no key: a partial of weight zero
-    float4* o = reinterpret_cast<float4*>(p.o_part + prow0 * kDv);
-    for (int i = tid; i < u.rows * (kDv / 4); i += kBaThreads) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = tid; i < u.rows; i += kBaThreads) p.lse_part[prow0 + i] = -CUDART_INF_F;
-    return;
-  }
 
   if (tid == 0) {
     for (int i = 0; i < kBaStages; ++i)
       for (int x = 0; x < kBaGroups; ++x) {
         // every thread's cp.async (group 0: and each warp's key masks), or two warps' arrivals with their bytes
-        mbar_init(&sh.k_full[i][x], x == 0 ? kBaCopiers + 4 : (x < kBaCopied ? kBaCopiers : 2));
+        // (group 0 also: the four gather warps' arrivals with the rope chunk)
+        mbar_init(&sh.k_full[i][x], x == 0 ? kBaCopiers + 4 + 4 : (x < kBaCopied ? kBaCopiers : 2));
         mbar_init(&sh.k_empty[i][x], 1);
       }
     for (int i = 0; i < 2; ++i) {
@@ -191,6 +178,25 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   bool ok = true;
+
+  grid_dep_wait();  // the lists: everything before this overlaps their making
+  const int count = __ldcg(p.list_len + g);
+  const BlockEntry* list = p.list + static_cast<int64_t>(g) * p.list_cap;
+  const int64_t keys = static_cast<int64_t>(count) * p.block;
+  const int64_t all_tiles = (keys + kBaKeys - 1) / kBaKeys;
+  const int t0 = static_cast<int>(all_tiles * split / p.splits);
+  const int n = static_cast<int>(all_tiles * (split + 1) / p.splits) - t0;  // tiles of this unit
+  if (split == 0 && tid == 0) {
+    const int32_t flags = __ldcg(p.list_flags + g);
+    if (flags) atomicOr(p.status, flags);
+  }
+  if (n == 0) {  // no key: a partial of weight zero
+    float4* o = reinterpret_cast<float4*>(p.o_part + prow0 * kDv);
+    for (int i = tid; i < u.rows * (kDv / 4); i += kBaThreads) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = tid; i < u.rows; i += kBaThreads) p.lse_part[prow0 + i] = -CUDART_INF_F;
+    if (warp == 0) tmem_dealloc(tmem, 512);
+    return;
+  }
 
   if (warp == 0) {
     if (elect_one()) {
@@ -335,7 +341,6 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
           break;
         }
         if (lane < 16) reinterpret_cast<uint64_t*>(smem + kBaOffMask)[st * kBaKeys + row0 + lane] = mask;
-        copy_rows(sbase, row0, 8, P8(), P16(), slot);
         copy_rows(sbase, row0, 0, P16(), P16(), slot);
         cp_async_arrive_noinc(&sh.k_full[st][0]);
         __syncwarp();
@@ -347,6 +352,28 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
         copy_rows(sbase, row0, 2, P16(), P16(), slot);
         cp_async_arrive_noinc(&sh.k_full[st][1]);
       } else {
+        // the rope chunk of 16 of the warp's keys, with group 0
+        const int rope0 = 16 * (gx - kBaCopied);
+        if (!wait_empty(t, 0)) {
+          ok = false;
+          break;
+        }
+        if (__all_sync(0xffffffffu, slot >= 0 || lane < rope0 || lane >= rope0 + 16)) {
+          if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[st][0], 16 * 128);
+          __syncwarp();
+          const int q = rope0 + 4 * (lane & 3);
+          const int ra = __shfl_sync(0xffffffffu, slot, q), rb = __shfl_sync(0xffffffffu, slot, q + 1);
+          const int rc = __shfl_sync(0xffffffffu, slot, q + 2), rd = __shfl_sync(0xffffffffu, slot, q + 3);
+          if (lane < 4)
+            tma_gather4(sbase + 8 * kBaChunk + (row0 + q) * 128, &p.tmap_kv, 512, ra, rb, rc, rd, &sh.k_full[st][0]);
+        } else {
+          copy_rows(sbase, row0 + rope0, 8, P8(), P16(), __shfl_sync(0xffffffffu, slot, (lane + rope0) & 31));
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.k_full[st][0]);
+        }
         if (!wait_empty(t, gx)) {
           ok = false;
           break;
@@ -374,7 +401,10 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
     }
     cp_async_wait<0>();
     if (!ok && !copier)  // after a give-up the gathers still in flight land before the CTA exits
-      for (int v = max(0, done - 2); v < done; ++v) mbar_wait(&sh.k_full[v & 1][gx], (v >> 1) & 1, 1u << 16);
+      for (int v = max(0, done - 2); v <= done && v < n; ++v) {
+        mbar_wait(&sh.k_full[v & 1][0], (v >> 1) & 1, 1u << 16);
+        mbar_wait(&sh.k_full[v & 1][gx], (v >> 1) & 1, 1u << 16);
+      }
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
     const int quarter = warp & 3, half = (warp - 1) >> 2;
@@ -598,12 +628,20 @@ __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_co
   __shared__ unsigned long long mask_sh[kUnBlocks];
   __shared__ int cnt[kUnThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_dep_launch();
   const int g = blockIdx.x;
+  // The call's first kernel clears the status word; its own findings go to it
+  // through the attention kernel, which runs after the clear.
+  __shared__ int flags_sh;
+  if (tid == 0) {
+    flags_sh = 0;
+    if (g == 0) *p.status = 0;
+  }
+  __syncthreads();
+  grid_dep_launch();
   const Group u = group_of(p, g);
   int L = __ldg(p.prefix_len + u.b);
   if (L < 0 || L > p.max_prefix_len) {
-    if (tid == 0) atomicOr(p.status, kStatusBadPrefix);
+    if (tid == 0) atomicOr(&flags_sh, kStatusBadPrefix);
     L = L < 0 ? 0 : p.max_prefix_len;
   }
   const int n_blocks = (L + p.block - 1) / p.block;
@@ -618,7 +656,7 @@ __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_co
     for (int i = tid; i < entries; i += kUnThreads) {
       const int x = __ldg(lists + i);
       if (x < 0 || x >= n_blocks) {
-        if (x != -1 && c0 == 0) atomicOr(p.status, kStatusBadBlock);
+        if (x != -1 && c0 == 0) atomicOr(&flags_sh, kStatusBadBlock);
         continue;
       }
       if (x < c0 || x - c0 >= kUnBlocks) continue;
@@ -650,7 +688,10 @@ __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_co
       __syncthreads();
     }
   }
-  if (tid == 0) p.list_len[g] = base;
+  if (tid == 0) {
+    p.list_len[g] = base;
+    p.list_flags[g] = flags_sh;
+  }
 }
 
 }  // namespace

@@ -36,11 +36,12 @@ __global__ void __launch_bounds__(kBmThreads, 4) block_merge_kernel(const __grid
     slot_sh[i] = __ldg(p.tree_slot_idx + static_cast<int64_t>(b) * T + i);
   }
   __syncthreads();
+  int32_t flags = 0;
   if (tid == 0) {
     int32_t st = 0;
     n_vis_sh = ancestor_slots(t, T, p.pool_slots, [&](int u) { return par_sh[u]; }, [&](int u) { return slot_sh[u]; },
                               vis_sh, &st);
-    if (st && blockIdx.y == 0) atomicOr(p.status, st);
+    flags = blockIdx.y == 0 ? st : 0;
   }
   __syncthreads();
   const int n_vis = n_vis_sh;
@@ -99,7 +100,8 @@ __global__ void __launch_bounds__(kBmThreads, 4) block_merge_kernel(const __grid
       }
     }
     // (m, l, o) starts the merge as one more partial, not normalised
-    grid_dep_wait();  // the splits' partials
+    grid_dep_wait();  // the splits' partials, and the status word cleared
+    if (flags) atomicOr(p.status, flags);
     if (!live) continue;
     const int64_t base = static_cast<int64_t>(b) * p.splits * p.pstride + r;
     // split s's log-sum-exp in log2 units, in lane s (at most 32 splits)

@@ -18,6 +18,7 @@ constexpr int kQuWarps = 8;
 
 // One warp per query row: 72 pieces of 16 bytes, lanes 0-7 take a third one.
 __global__ void __launch_bounds__(kQuWarps * 32) quant_rows_kernel(QuantParams p) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kQuWarps + (threadIdx.x >> 5);
@@ -70,10 +71,12 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.x, b = blockIdx.y;
   int L = __ldg(p.prefix_len + b);
-  if (L < 0 || L > p.max_prefix_len) {
-    if (t == 0 && tid == 0) atomicOr(p.status, kStatusBadPrefix);
-    L = L < 0 ? 0 : p.max_prefix_len;
-  }
+  const bool bad_len = L < 0 || L > p.max_prefix_len;
+  L = L < 0 ? 0 : (L > p.max_prefix_len ? p.max_prefix_len : L);
+  auto wait_scores = [&] {  // the scores, and the status word cleared
+    grid_dep_wait();
+    if (bad_len && t == 0 && tid == 0) atomicOr(p.status, kStatusBadPrefix);
+  };
   const int n = (L + p.block - 1) / p.block;
   const float* score = p.score + (static_cast<int64_t>(b) * p.nodes + t) * p.blocks;
   int32_t* out = p.block_idx + (static_cast<int64_t>(b) * p.nodes + t) * p.topk;
@@ -81,18 +84,18 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
   for (int i = keep + tid; i < p.topk; i += kThreads) out[i] = -1;
   if (keep == n) {
     for (int i = tid; i < n; i += kThreads) out[i] = i;
-    grid_dep_wait();
+    wait_scores();
     return;
   }
   const int lo = min(p.first, n), hi = max(lo, n - min(p.last, n));  // [lo, hi): chosen by score
   const int need = keep - (lo + (n - hi));
   if (need <= 0) {  // only forced blocks fit: the lowest ones
     for (int i = tid; i < keep; i += kThreads) out[i] = i < lo ? i : hi + (i - lo);
-    grid_dep_wait();
+    wait_scores();
     return;
   }
   for (int i = tid; i < kDigits * kBins; i += kThreads) (&hist[0][0])[i] = 0;
-  grid_dep_wait();  // the scores
+  wait_scores();
   const bool in_sh = n <= cached;
   auto load_key = [&](int i) { return i < lo || i >= hi ? 0xffffffffu : order_key_bits(__float_as_uint(__ldcg(score + i))); };
   if (in_sh) {

@@ -99,7 +99,7 @@ int select_layout(const ddt_dims* d, int32_t block, SelectLayout* w) {
 struct BlocksLayout {
   int groups, group_nodes, splits;
   int64_t list_cap;
-  size_t len_off, list_off, lse_off, o_off, bytes;
+  size_t len_off, flags_off, list_off, lse_off, o_off, bytes;
 };
 
 // Groups of up to 64 (node, head) rows, and the key splits of each.  The splits
@@ -128,7 +128,8 @@ int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, 
   }
   const size_t part = size_t(d->batch) * w->splits * T * H;
   w->len_off = kStatusBytes;
-  w->list_off = align_up(w->len_off + all * sizeof(int32_t), 256);
+  w->flags_off = align_up(w->len_off + all * sizeof(int32_t), 256);
+  w->list_off = align_up(w->flags_off + all * sizeof(int32_t), 256);
   w->lse_off = align_up(w->list_off + size_t(all) * w->list_cap * sizeof(BlockEntry), 256);
   w->o_off = align_up(w->lse_off + part * sizeof(float), 256);
   w->bytes = align_up(w->o_off + part * kDv * sizeof(float), 256);
@@ -360,7 +361,8 @@ extern "C" int ddtree_block_select(const void* q, const void* summary, const flo
   t.max_prefix_len = dims->max_prefix_len;
   t.status = p.status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!clear_status(workspace, s) || launch_quant_rows(k, s) != cudaSuccess ||
+  k.status = p.status;  // cleared there
+  if (launch_quant_rows(k, s) != cudaSuccess ||
       launch_scores(p, kScoreBlock, sms, true, s) != cudaSuccess || launch_block_topk(t, dims->batch, s) != cudaSuccess)
     return DDT_ERR_LAUNCH;
   return DDT_OK;
@@ -402,6 +404,7 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
   p.block_idx = block_idx;
   p.list = reinterpret_cast<BlockEntry*>(ws + w.list_off);
   p.list_len = reinterpret_cast<int32_t*>(ws + w.len_off);
+  p.list_flags = reinterpret_cast<int32_t*>(ws + w.flags_off);
   p.pool_slots = dims->pool_slots;
   p.list_cap = w.list_cap;
   p.batch = dims->batch;
@@ -439,7 +442,8 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
   m.lse = lse;
   m.status = p.status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!clear_status(workspace, s) || launch_block_union(p, s) != cudaSuccess || launch_block_attn(p, s) != cudaSuccess ||
+  // (the union kernel clears the status word)
+  if (launch_block_union(p, s) != cudaSuccess || launch_block_attn(p, s) != cudaSuccess ||
       launch_block_merge(m, p.batch, s) != cudaSuccess)
     return DDT_ERR_LAUNCH;
   return DDT_OK;

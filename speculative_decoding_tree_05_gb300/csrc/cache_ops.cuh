@@ -103,6 +103,7 @@ struct QuantParams {
   uint16_t* q_int;           // bf16 [rows, 576]: integers in [-127, 127]
   float* q_scale;            // [rows]
   int64_t rows;
+  int32_t* status;           // cleared: this is a selection's first kernel
 };
 cudaError_t launch_quant_rows(const QuantParams& p, cudaStream_t stream);
 
@@ -134,6 +135,7 @@ struct BlockAttnParams {
   const int32_t* block_idx;   // [B, T, topk]
   BlockEntry* list;           // [B * groups, list_cap]: union of the group's lists, in block order
   int32_t* list_len;          // [B * groups]
+  int32_t* list_flags;        // [B * groups] status bits found while making the lists
   int64_t pool_slots;
   int64_t list_cap;
   int64_t pstride;            // rows between consecutive splits of one request

@@ -437,6 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
   }
   if (!ok) {
     *abort = 1;
+    grid_dep_wait();  // (the kernel before may clear the word)
     atomicOr(p.status, kStatusTimeout);
   }
   // the leader's commits arrive here too: the last one before this CTA may leave
@@ -445,6 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
   cluster_sync();  // nothing of the pair is in flight towards either CTA
   tc_fence_after();
   if (warp == 0) tmem_dealloc_pair(tmem, 512);
+  grid_dep_wait();
   if (blockIdx.x == 0)
     for (int b = tid; b < p.batch; b += kScThreads) {
       const int L = __ldg(p.prefix_len + b);
