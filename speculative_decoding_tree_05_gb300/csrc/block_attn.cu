@@ -32,8 +32,10 @@
 //                ways (L2-resident rows)
 // What bounds it: a stage lives from its load through S, the softmax and P.V, and
 // only two of them fit beside the query rows, so a tile takes half a stage's life.
-// A unit writes the normalised O and the log-sum-exp of its share; the
-// tail/merge kernel adds the tree part and merges the splits.
+// The nodes' ancestors and themselves are keys like the others, behind the blocks'
+// keys, each with the rows that see it.  One split writes bf16 and the log-sum-exp
+// at once; with more, a unit writes the normalised O and the log-sum-exp of its
+// share, and the merge kernel joins them.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <type_traits>
@@ -182,7 +184,8 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
   grid_dep_wait();  // the lists: everything before this overlaps their making
   const int count = __ldcg(p.list_len + g);
   const BlockEntry* list = p.list + static_cast<int64_t>(g) * p.list_cap;
-  const int64_t keys = static_cast<int64_t>(count) * p.block;
+  const BlockEntry* tree = p.tree + static_cast<int64_t>(g) * p.nodes;
+  const int64_t list_keys = static_cast<int64_t>(count) * p.block, keys = list_keys + __ldcg(p.tree_len + g);
   const int64_t all_tiles = (keys + kBaKeys - 1) / kBaKeys;
   const int t0 = static_cast<int>(all_tiles * split / p.splits);
   const int n = static_cast<int>(all_tiles * (split + 1) / p.splits) - t0;  // tiles of this unit
@@ -191,9 +194,11 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
     if (flags) atomicOr(p.status, flags);
   }
   if (n == 0) {  // no key: a partial of weight zero
-    float4* o = reinterpret_cast<float4*>(p.o_part + prow0 * kDv);
-    for (int i = tid; i < u.rows * (kDv / 4); i += kBaThreads) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = tid; i < u.rows; i += kBaThreads) p.lse_part[prow0 + i] = -CUDART_INF_F;
+    uint4* o = p.splits == 1 ? reinterpret_cast<uint4*>(p.out + prow0 * kDv) : reinterpret_cast<uint4*>(p.o_part + prow0 * kDv);
+    const int each = p.splits == 1 ? kDv / 8 : kDv / 4;
+    for (int i = tid; i < u.rows * each; i += kBaThreads) o[i] = make_uint4(0, 0, 0, 0);
+    float* l = p.splits == 1 ? p.lse : p.lse_part;
+    for (int i = tid; i < u.rows; i += kBaThreads) l[prow0 + i] = -CUDART_INF_F;
     if (warp == 0) tmem_dealloc(tmem, 512);
     return;
   }
@@ -269,25 +274,26 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
     // tile ahead of its use: nothing is computed from a value in the tile that
     // reads it (an immediate use stalls the warp for the read: 2000 cycles a tile).
     struct Key {
-      uint4 entry;    // of tile t + 1: mask, block
+      uint4 entry;    // of tile t + 1: mask, block or tree slot, which of the two
       int slot;       // of tile t, as read; -1: no key
       uint64_t mask;  // of tile t
     };
     // (a list names each block once, so its keys count in 32 bits; blocks are powers of two)
     const int log_block = 31 - __clz(p.block);
-    const uint32_t first = static_cast<uint32_t>(t0) * kBaKeys, n_keys = static_cast<uint32_t>(keys);
+    const uint32_t first = static_cast<uint32_t>(t0) * kBaKeys, n_keys = static_cast<uint32_t>(keys),
+                   n_list = static_cast<uint32_t>(list_keys);
     auto read_entry = [&](int t, int k) -> uint4 {  // key k of tile t
       const uint32_t i = first + t * kBaKeys + k;
       if (t >= n || k >= kBaKeys || i >= n_keys) return make_uint4(0, 0, 0xffffffffu, 0);
-      return __ldcg(reinterpret_cast<const uint4*>(list + (i >> log_block)));
+      return __ldcg(reinterpret_cast<const uint4*>(i < n_list ? list + (i >> log_block) : tree + (i - n_list)));
     };
     auto read_slot = [&](int t, int k, Key& key) {  // of tile t, whose entry has arrived
       const uint32_t i = first + t * kBaKeys + k;
       const int blk = static_cast<int>(key.entry.z);
       const uint32_t pos = (static_cast<uint32_t>(blk) << log_block) + (i & (p.block - 1));
-      const bool in = blk >= 0 && pos < static_cast<uint32_t>(L);
+      const bool in = blk >= 0 && (key.entry.w != 0 || pos < static_cast<uint32_t>(L));
       key.mask = in ? key.entry.x | (static_cast<uint64_t>(key.entry.y) << 32) : 0;
-      key.slot = in ? __ldg(slots + pos) : -1;
+      key.slot = in ? (key.entry.w != 0 ? blk : __ldg(slots + pos)) : -1;
     };
     auto row_of = [&](Key& key) -> int {
       if (key.mask != 0 && (key.slot < 0 || key.slot >= p.pool_slots)) {
@@ -585,7 +591,8 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       if (id < kBaRows) {
         const float sum = (scratch[id] + scratch[kBaRows + id]) + (scratch[2 * kBaRows + id] + scratch[3 * kBaRows + id]);
         alpha_sh[id] = sum != 0.f ? 1.f / sum : 0.f;
-        if (id < u.rows) p.lse_part[prow0 + id] = sum != 0.f ? (mx[id] + log2f(sum)) * kBaLn2 : -CUDART_INF_F;
+        float* lse = p.splits == 1 ? p.lse : p.lse_part;
+        if (id < u.rows) lse[prow0 + id] = sum != 0.f ? (mx[id] + log2f(sum)) * kBaLn2 : -CUDART_INF_F;
       }
     }
   }
@@ -602,10 +609,23 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
         if (cc >= u.rows) continue;
         uint32_t o[8];
         tmem_ld8(tmem + lane_off + mt * kBaRows + cc, o);
-        float* dst = p.o_part + (prow0 + cc) * kDv + mt * 128 + (warp & 3) * 32 + lane;
+        const int dim = mt * 128 + (warp & 3) * 32;
+        if (p.splits == 1) {
+          // two rows a store: even lanes hold a pair of dims of the first, odd lanes of the second
+          uint16_t* dst = p.out + (prow0 + cc + (lane & 1)) * kDv + dim + (lane & ~1);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (cc + k < u.rows) dst[k * kDv] = __uint_as_float(o[k]) * inv_l[cc + k];
+          for (int k = 0; k < 8; k += 2) {
+            const float x = __uint_as_float(o[k]) * inv_l[cc + k], y = __uint_as_float(o[k + 1]) * inv_l[cc + k + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
+            if (cc + k + (lane & 1) < u.rows)
+              *reinterpret_cast<uint32_t*>(dst + k * kDv) = lane & 1 ? pack_bf16x2(got, y) : pack_bf16x2(x, got);
+          }
+        } else {
+          float* dst = p.o_part + (prow0 + cc) * kDv + dim + lane;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (cc + k < u.rows) dst[k * kDv] = __uint_as_float(o[k]) * inv_l[cc + k];
+        }
       }
     }
   }
@@ -620,50 +640,77 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
 }
 
 // The union of a group's lists, in block order, with the rows that list each
-// block.  One CTA per group: a mask per block in shared memory, 2048 blocks at a time.
-constexpr int kUnThreads = 256;
-constexpr int kUnBlocks = 2048;
+// block, and the tree rows that its nodes see.  One CTA per group: a mask per
+// block in shared memory, 4096 blocks at a time.
+constexpr int kUnThreads = 1024;
+constexpr int kUnWarps = kUnThreads / 32;
+constexpr int kUnBlocks = 4096;
 
 __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_constant__ BlockAttnParams p) {
   __shared__ unsigned long long mask_sh[kUnBlocks];
-  __shared__ int cnt[kUnThreads / 32];
+  __shared__ unsigned long long tree_sh[kMaxNodes];
+  __shared__ int par_sh[kMaxNodes], slot_sh[kMaxNodes];
+  __shared__ int cnt[kUnWarps];
+  __shared__ int flags_sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = blockIdx.x;
   // The call's first kernel clears the status word; its own findings go to it
   // through the attention kernel, which runs after the clear.
-  __shared__ int flags_sh;
   if (tid == 0) {
     flags_sh = 0;
     if (g == 0) *p.status = 0;
   }
+  const Group u = group_of(p, g);
+  if (tid < p.nodes) {
+    par_sh[tid] = __ldg(p.tree_parent + static_cast<int64_t>(u.b) * p.nodes + tid);
+    slot_sh[tid] = __ldg(p.tree_slot_idx + static_cast<int64_t>(u.b) * p.nodes + tid);
+    tree_sh[tid] = 0;
+  }
+  int L = __ldg(p.prefix_len + u.b);
+  const int bad_len = L < 0 || L > p.max_prefix_len ? kStatusBadPrefix : 0;
+  L = L < 0 ? 0 : (L > p.max_prefix_len ? p.max_prefix_len : L);
+  for (int i = tid; i < kUnBlocks; i += kUnThreads) mask_sh[i] = 0;
   __syncthreads();
   grid_dep_launch();
-  const Group u = group_of(p, g);
-  int L = __ldg(p.prefix_len + u.b);
-  if (L < 0 || L > p.max_prefix_len) {
-    if (tid == 0) atomicOr(&flags_sh, kStatusBadPrefix);
-    L = L < 0 ? 0 : p.max_prefix_len;
-  }
   const int n_blocks = (L + p.block - 1) / p.block;
   const int t_first = u.row0 / p.heads, t_last = (u.row0 + u.rows - 1) / p.heads;
+  auto rows_of = [&](int t) -> unsigned long long {  // of the group's t-th node: its rows [t H, t H + H)
+    const int lo = t * p.heads, hi = min(u.rows, lo + p.heads);
+    return (hi == 64 ? ~0ull : ((1ull << hi) - 1)) & ~((1ull << lo) - 1);
+  };
+  if (tid <= t_last - t_first) {
+    // a node's walk to the root: a link that is no earlier node ends it, a slot outside the pool is left out
+    int v = t_first + tid, flags = tid == 0 ? bad_len : 0;
+    for (int guard = 0; v >= 0 && guard < p.nodes; ++guard) {
+      const int slot = slot_sh[v], up = par_sh[v];
+      if (slot >= 0 && slot < p.pool_slots)
+        atomicOr(&tree_sh[v], rows_of(tid));
+      else
+        flags |= kStatusBadSlot;
+      if (v == 0 ? up != -1 : (up < 0 || up >= v)) {
+        flags |= kStatusBadParent;
+        break;
+      }
+      v = up;
+    }
+    if (flags) atomicOr(&flags_sh, flags);
+  }
   const int32_t* lists = p.block_idx + (static_cast<int64_t>(u.b) * p.nodes + t_first) * p.topk;
   const int entries = (t_last - t_first + 1) * p.topk;  // at most 64 lists of 2^20
   BlockEntry* out = p.list + static_cast<int64_t>(g) * p.list_cap;
   int base = 0;
   for (int c0 = 0; c0 < n_blocks || c0 == 0; c0 += kUnBlocks) {
-    for (int i = tid; i < kUnBlocks; i += kUnThreads) mask_sh[i] = 0;
-    __syncthreads();
+    if (c0 > 0) {
+      for (int i = tid; i < kUnBlocks; i += kUnThreads) mask_sh[i] = 0;
+      __syncthreads();
+    }
     for (int i = tid; i < entries; i += kUnThreads) {
       const int x = __ldg(lists + i);
       if (x < 0 || x >= n_blocks) {
         if (x != -1 && c0 == 0) atomicOr(&flags_sh, kStatusBadBlock);
         continue;
       }
-      if (x < c0 || x - c0 >= kUnBlocks) continue;
-      const int t = i / p.topk;  // node of the group: its rows [t H, t H + H)
-      const int lo = t * p.heads, hi = min(u.rows, lo + p.heads);
-      const unsigned long long below = hi == 64 ? ~0ull : ((1ull << hi) - 1);
-      atomicOr(&mask_sh[x - c0], below & ~((1ull << lo) - 1));
+      if (x >= c0 && x - c0 < kUnBlocks) atomicOr(&mask_sh[x - c0], rows_of(i / p.topk));
     }
     __syncthreads();
     const int here = min(kUnBlocks, n_blocks - c0);
@@ -672,27 +719,42 @@ __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_co
       const uint32_t vote = __ballot_sync(0xffffffffu, m != 0);
       if (lane == 0) cnt[warp] = __popc(vote);
       __syncthreads();
-      int at = base;
-#pragma unroll
-      for (int w = 0; w < kUnThreads / 32; ++w) {
-        if (w < warp) at += cnt[w];
-        base += cnt[w];
-      }
+      const int c = cnt[lane];
+      const int at = base + __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+      base += __reduce_add_sync(0xffffffffu, c);
       if (m != 0) {
         BlockEntry e;
         e.mask = m;
-        e.block = c0 + i0 + tid;
-        e.pad = 0;
+        e.index = c0 + i0 + tid;
+        e.tree = 0;
         out[at + __popc(vote & ((1u << lane) - 1u))] = e;
       }
       __syncthreads();
     }
   }
-  if (tid == 0) {
-    p.list_len[g] = base;
-    p.list_flags[g] = flags_sh;
+  if (warp == 0) {  // the tree rows, in node order
+    BlockEntry* tree = p.tree + static_cast<int64_t>(g) * p.nodes;
+    int n = 0;
+    for (int i0 = 0; i0 < p.nodes; i0 += 32) {
+      const unsigned long long m = i0 + lane < p.nodes ? tree_sh[i0 + lane] : 0;
+      const uint32_t vote = __ballot_sync(0xffffffffu, m != 0);
+      if (m != 0) {
+        BlockEntry e;
+        e.mask = m;
+        e.index = slot_sh[i0 + lane];
+        e.tree = 1;
+        tree[n + __popc(vote & ((1u << lane) - 1u))] = e;
+      }
+      n += __popc(vote);
+    }
+    if (lane == 0) {
+      p.list_len[g] = base;
+      p.tree_len[g] = n;
+      p.list_flags[g] = flags_sh;
+    }
   }
 }
+static_assert(kUnWarps == 32, "the prefix over warps takes one lane each");
 
 }  // namespace
 

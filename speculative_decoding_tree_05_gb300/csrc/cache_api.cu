@@ -99,7 +99,7 @@ int select_layout(const ddt_dims* d, int32_t block, SelectLayout* w) {
 struct BlocksLayout {
   int groups, group_nodes, splits;
   int64_t list_cap;
-  size_t len_off, flags_off, list_off, lse_off, o_off, bytes;
+  size_t len_off, tree_len_off, flags_off, list_off, tree_off, lse_off, o_off, bytes;
 };
 
 // Groups of up to 64 (node, head) rows, and the key splits of each.  The splits
@@ -116,7 +116,7 @@ int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, 
   if (all > (1 << 30)) return DDT_ERR_DIMS;
   const int64_t blocks = (int64_t(d->max_prefix_len) + block - 1) / block;
   w->list_cap = std::min<int64_t>(int64_t(w->group_nodes) * topk, blocks);
-  const int64_t tiles = std::max<int64_t>(1, (w->list_cap * block + 63) / 64);
+  const int64_t tiles = (w->list_cap * block + std::min(T, 16) + 63) / 64;  // with a path of tree rows
   int64_t best_cost = -1;
   w->splits = 1;
   for (int s = 1; s <= std::min<int64_t>(tiles, 32); ++s) {
@@ -126,11 +126,13 @@ int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, 
       w->splits = s;
     }
   }
-  const size_t part = size_t(d->batch) * w->splits * T * H;
+  const size_t part = w->splits > 1 ? size_t(d->batch) * w->splits * T * H : 0;
   w->len_off = kStatusBytes;
-  w->flags_off = align_up(w->len_off + all * sizeof(int32_t), 256);
+  w->tree_len_off = align_up(w->len_off + all * sizeof(int32_t), 256);
+  w->flags_off = align_up(w->tree_len_off + all * sizeof(int32_t), 256);
   w->list_off = align_up(w->flags_off + all * sizeof(int32_t), 256);
-  w->lse_off = align_up(w->list_off + size_t(all) * w->list_cap * sizeof(BlockEntry), 256);
+  w->tree_off = align_up(w->list_off + size_t(all) * w->list_cap * sizeof(BlockEntry), 256);
+  w->lse_off = align_up(w->tree_off + size_t(all) * T * sizeof(BlockEntry), 256);
   w->o_off = align_up(w->lse_off + part * sizeof(float), 256);
   w->bytes = align_up(w->o_off + part * kDv * sizeof(float), 256);
   return DDT_OK;
@@ -403,7 +405,11 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
   p.prefix_len = prefix_len;
   p.block_idx = block_idx;
   p.list = reinterpret_cast<BlockEntry*>(ws + w.list_off);
+  p.tree = reinterpret_cast<BlockEntry*>(ws + w.tree_off);
+  p.tree_parent = tree_parent;
+  p.tree_slot_idx = tree_slot_idx;
   p.list_len = reinterpret_cast<int32_t*>(ws + w.len_off);
+  p.tree_len = reinterpret_cast<int32_t*>(ws + w.tree_len_off);
   p.list_flags = reinterpret_cast<int32_t*>(ws + w.flags_off);
   p.pool_slots = dims->pool_slots;
   p.list_cap = w.list_cap;
@@ -423,28 +429,19 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
   p.lse_part = reinterpret_cast<float*>(ws + w.lse_off);
   p.status = reinterpret_cast<int32_t*>(ws);
   if (!encode_pool_map(&p.tmap_kv, kv_pool, dims->pool_slots, 64, 1)) return DDT_ERR_LAUNCH;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
   BlockMergeParams m = {};
-  m.q = p.q;
-  m.kv = p.kv;
-  m.tree_parent = tree_parent;
-  m.tree_slot_idx = tree_slot_idx;
-  m.pool_slots = dims->pool_slots;
-  m.pstride = p.pstride;
-  m.nodes = p.nodes;
-  m.heads = p.heads;
-  // two rows a warp once the nodes fill the GPU with one
-  m.heads_per_cta = p.heads >= 16 && int64_t(p.batch) * p.nodes * p.heads > 8 * 4 * int64_t(sms) ? 16 : 8;
+  m.rows = p.pstride;
   m.splits = w.splits;
-  m.scale_log2 = p.scale_log2;
   m.o_part = p.o_part;
   m.lse_part = p.lse_part;
-  m.out = static_cast<uint16_t*>(out);
+  m.out = p.out;
   m.lse = lse;
-  m.status = p.status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // (the union kernel clears the status word)
   if (launch_block_union(p, s) != cudaSuccess || launch_block_attn(p, s) != cudaSuccess ||
-      launch_block_merge(m, p.batch, s) != cudaSuccess)
+      (w.splits > 1 && launch_block_merge(m, p.batch, s) != cudaSuccess))
     return DDT_ERR_LAUNCH;
   return DDT_OK;
 }

@@ -121,9 +121,9 @@ cudaError_t launch_block_topk(const TopkParams& p, int batch, cudaStream_t strea
 constexpr int kBlockRows = 64;  // (node, head) rows of one group
 
 struct alignas(16) BlockEntry {
-  unsigned long long mask;  // rows of the group that list the block
-  int32_t block;
-  int32_t pad;
+  unsigned long long mask;  // rows of the group that read it
+  int32_t index;            // block of the prefix, or pool slot of a tree row
+  int32_t tree;             // 1: a tree row
 };
 
 struct BlockAttnParams {
@@ -133,8 +133,12 @@ struct BlockAttnParams {
   const int32_t* slot_idx;    // [B, slot_stride]
   const int32_t* prefix_len;  // [B]
   const int32_t* block_idx;   // [B, T, topk]
+  const int32_t* tree_parent;    // [B, T]
+  const int32_t* tree_slot_idx;  // [B, T]
   BlockEntry* list;           // [B * groups, list_cap]: union of the group's lists, in block order
+  BlockEntry* tree;           // [B * groups, T]: its nodes' ancestors and themselves, in node order
   int32_t* list_len;          // [B * groups]
+  int32_t* tree_len;          // [B * groups]
   int32_t* list_flags;        // [B * groups] status bits found while making the lists
   int64_t pool_slots;
   int64_t list_cap;
@@ -144,30 +148,24 @@ struct BlockAttnParams {
   int32_t group_nodes;        // nodes of a group (heads <= 64; else a group is 64 heads of one node)
   int32_t splits;
   float scale_log2;
-  float* o_part;              // fp32 [B, splits, pstride, 512], normalised
+  float* o_part;              // fp32 [B, splits, pstride, 512], normalised (splits > 1)
   float* lse_part;            // fp32 [B, splits, pstride], natural log
+  uint16_t* out;              // bf16 [B, T, H, 512] (splits == 1)
+  float* lse;                 // fp32 [B, T, H]
   int32_t* status;
 };
 cudaError_t configure_block_attn();
 cudaError_t launch_block_union(const BlockAttnParams& p, cudaStream_t stream);
 cudaError_t launch_block_attn(const BlockAttnParams& p, cudaStream_t stream);
 
-// The tree part of block attention and the merge of its splits.
+// The merge of block attention's key splits.
 struct BlockMergeParams {
-  const uint16_t* q;
-  const uint16_t* kv;
-  const int32_t* tree_parent;    // [B, T]
-  const int32_t* tree_slot_idx;  // [B, T]
-  int64_t pool_slots;
-  int64_t pstride;
-  int32_t nodes, heads, heads_per_cta;
-  int32_t splits;                // at most 32
-  float scale_log2;
+  int64_t rows;                  // of a request: T * H, also the rows between its splits
+  int32_t splits;                // 2 to 32
   const float* o_part;
   const float* lse_part;
   uint16_t* out;                 // bf16 [B, T, H, 512]
   float* lse;                    // fp32 [B, T, H]
-  int32_t* status;
 };
 cudaError_t launch_block_merge(const BlockMergeParams& p, int batch, cudaStream_t stream);
 

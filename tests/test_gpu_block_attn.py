@@ -180,6 +180,47 @@ def test_a_non_finite_row_reaches_only_the_nodes_that_read_it(value):
     check(d, out, lse, skip={(0, t) for t in readers})
 
 
+def test_a_non_finite_tree_row_reaches_only_its_descendants():
+    d = make([300], 6, 16, 64, 3, seed=12)
+    d["parent"] = torch.tensor([[-1, 0, 0, 1, 2, 3]], dtype=torch.int32, device="cuda")
+    d["kv"][int(d["tree"][0, 1])] = float("nan")
+    out, lse, st = call(d)
+    assert st == 0
+    for t in (1, 3, 5):
+        assert bool(torch.isnan(out[0, t]).all()) and bool(torch.isnan(lse[0, t]).all())
+    check(d, out, lse, skip={(0, 1), (0, 3), (0, 5)})
+
+
+def test_bad_parents_and_tree_slots():
+    d = make([300], 6, 16, 64, 3, seed=13)
+    d["parent"] = torch.tensor([[-1, 0, 1, 5, 3, -2]], dtype=torch.int32, device="cuda")
+    out, lse, st = call(d)
+    assert st == ddtree.STATUS_BAD_PARENT
+    # a bad link ends the walk: node 3 sees itself, node 4 node 3 and itself, node 5 itself
+    d["parent"] = torch.tensor([[-1, 0, 1, -1, 3, -1]], dtype=torch.int32, device="cuda")
+    check(d, out, lse)
+    d["parent"] = torch.tensor([[-1, 0, 1, 2, 3, 4]], dtype=torch.int32, device="cuda")
+    keep = d["tree"].clone()
+    d["tree"][0, 2] = d["kv"].shape[0] + 5
+    out, lse, st = call(d)
+    assert st == ddtree.STATUS_BAD_SLOT
+    d["tree"] = keep
+    check(d, out, lse, skip={(0, t) for t in (2, 3, 4, 5)})
+
+
+@pytest.mark.parametrize("nodes", [1, 2, 65, 128])
+def test_trees_alone(nodes):
+    """No prefix: the tree rows are the only keys; a chain of them, and none at all when its slots are bad."""
+    d = make([0], nodes, 16, 16, 2, seed=14)
+    d["parent"] = torch.arange(-1, nodes - 1, dtype=torch.int32, device="cuda")[None].contiguous()
+    out, lse, st = call(d)
+    assert st == 0
+    check(d, out, lse)
+    d["tree"][:] = -1
+    out, lse, st = call(d)
+    assert st == ddtree.STATUS_BAD_SLOT and not bool(out.any()) and bool((lse == float("-inf")).all())
+
+
 def test_slot_layout_graph_and_stream():
     d = make([900, 300], 9, 16, 64, 6, seed=11)
     out, lse, _ = call(d)
