@@ -265,33 +265,26 @@ class SparseVerifier:
         return read_device_status(self.workspace, stream, library=self.lib)
 
 
-def _need(device, **tensors):
-    """Check tensors given as name=(tensor, dtype, shape): type, shape, contiguity and device."""
+def _need(device, *checks):
+    """Check tensors given as (name, tensor, dtype, shape): type, shape, contiguity and device."""
     index = device.index
-    for name, (t, dtype, shape) in tensors.items():
+    for name, t, dtype, shape in checks:
         if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                              f"{t.dtype} {tuple(t.shape)} on {t.device}"
                              + ("" if t.is_contiguous() else " (not contiguous)"))
 
 
-class _On:
-    """Makes `device` the current one for a call (the library works on the current device)."""
-
-    def __init__(self, device):
-        import torch
-        here = torch.cuda.current_device()
-        self.index, self.back = device.index, None if here == device.index else here
-
-    def __enter__(self):
-        if self.back is not None:
-            import torch
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            import torch
-            torch.cuda.set_device(self.back)
+def _run_on(device, fn, name, *args):
+    """Call the library with `device` current (it works on the current device); raises DDTError."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc != DDT_OK:
+        raise DDTError(rc, name)
 
 
 def _addr(t):
@@ -336,8 +329,9 @@ class KeyWeights:
                               slot_stride if max_prefix_len is None else max_prefix_len)
         self.max_sel = int(nodes if max_sel is None else max_sel)
         self.device = _cuda_device(device)
-        with _On(self.device):
-            n = max(int(self.lib.ddtree_kv_weight_workspace_bytes(ctypes.byref(self.dims), k))
+        self.dims_ref = ctypes.byref(self.dims)
+        with torch.cuda.device(self.device):
+            n = max(int(self.lib.ddtree_kv_weight_workspace_bytes(self.dims_ref, k))
                     for k in range(self.max_sel + 1))
         if n == 0:
             raise DDTError(-2, "ddtree_kv_weight_workspace_bytes")
@@ -352,25 +346,23 @@ class KeyWeights:
             decay = 0.0
         if out is None:
             out = torch.zeros(table, dtype=torch.float32, device=self.device)
-        checks = dict(q=(q, torch.bfloat16, (d.batch, d.num_nodes, d.num_heads, D_QK)),
-                      kv_pool=(kv_pool, torch.bfloat16, (d.pool_slots, D_QK)),
-                      slot_idx=(slot_idx, torch.int32, table), prefix_len=(prefix_len, torch.int32, (d.batch,)),
-                      lse=(lse, torch.float32, (d.batch, d.num_nodes, d.num_heads)), out=(out, torch.float32, table))
+        B, T, H = d.batch, d.num_nodes, d.num_heads
+        _need(self.device, ("q", q, torch.bfloat16, (B, T, H, D_QK)),
+              ("kv_pool", kv_pool, torch.bfloat16, (d.pool_slots, D_QK)), ("slot_idx", slot_idx, torch.int32, table),
+              ("prefix_len", prefix_len, torch.int32, (B,)), ("lse", lse, torch.float32, (B, T, H)),
+              ("out", out, torch.float32, table))
         if weight is not None:
-            checks["weight"] = (weight, torch.float32, table)
+            _need(self.device, ("weight", weight, torch.float32, table))
         sel = 0
         if node_idx is not None:
             if node_idx.dim() != 2 or not 1 <= node_idx.shape[1] <= self.max_sel:
                 raise ValueError(f"node_idx must be [batch, 1..{self.max_sel}], got {tuple(node_idx.shape)}")
             sel = node_idx.shape[1]
-            checks["node_idx"] = (node_idx, torch.int32, (d.batch, sel))
-        _need(self.device, **checks)
-        with _On(self.device):
-            rc = self.lib.ddtree_kv_weight(_addr(q), _addr(kv_pool), _addr(slot_idx), _addr(prefix_len), _addr(lse),
-                                           _addr(node_idx), sel, float(sm_scale), float(decay), _addr(weight),
-                                           _addr(out), ctypes.byref(d), _addr(self.workspace), self.workspace.numel(),
-                                           _stream_of(self.device, stream))
-        _check(rc, "ddtree_kv_weight")
+            _need(self.device, ("node_idx", node_idx, torch.int32, (B, sel)))
+        _run_on(self.device, self.lib.ddtree_kv_weight, "ddtree_kv_weight", q.data_ptr(), kv_pool.data_ptr(),
+                slot_idx.data_ptr(), prefix_len.data_ptr(), lse.data_ptr(), _addr(node_idx), sel, sm_scale, decay,
+                _addr(weight), out.data_ptr(), self.dims_ref, self.workspace.data_ptr(), self.workspace.numel(),
+                _stream_of(self.device, stream))
         return out
 
     def status(self, stream=None) -> int:
@@ -395,19 +387,19 @@ def kv_evict(weight, slot_idx, prefix_len, keep_len, sink=0, recent=0, slot_idx_
     prefix_len_out = torch.empty_like(prefix_len) if prefix_len_out is None else prefix_len_out
     freed = torch.zeros_like(slot_idx) if freed is None else freed
     workspace = torch.empty(256, dtype=torch.uint8, device=device) if workspace is None else workspace
-    _need(device, weight=(weight, torch.float32, (B, stride)), slot_idx=(slot_idx, torch.int32, (B, stride)),
-          prefix_len=(prefix_len, torch.int32, (B,)), keep_len=(keep_len, torch.int32, (B,)),
-          slot_idx_out=(slot_idx_out, torch.int32, (B, stride)), weight_out=(weight_out, torch.float32, (B, stride)),
-          prefix_len_out=(prefix_len_out, torch.int32, (B,)), freed=(freed, torch.int32, (B, stride)),
-          workspace=(workspace, torch.uint8, workspace.shape))
+    table, lens = (B, stride), (B,)
+    _need(device, ("weight", weight, torch.float32, table), ("slot_idx", slot_idx, torch.int32, table),
+          ("prefix_len", prefix_len, torch.int32, lens), ("keep_len", keep_len, torch.int32, lens),
+          ("slot_idx_out", slot_idx_out, torch.int32, table), ("weight_out", weight_out, torch.float32, table),
+          ("prefix_len_out", prefix_len_out, torch.int32, lens), ("freed", freed, torch.int32, table),
+          ("workspace", workspace, torch.uint8, workspace.shape))
     if workspace.numel() < 256:
         raise ValueError("workspace must hold 256 bytes")
     dims = make_dims(B, 1, 1, 1, stride, stride if max_prefix_len is None else max_prefix_len)
-    with _On(device):
-        rc = lib().ddtree_kv_evict(_addr(weight), _addr(slot_idx), _addr(prefix_len), _addr(keep_len), int(sink),
-                                   int(recent), _addr(slot_idx_out), _addr(weight_out), _addr(prefix_len_out),
-                                   _addr(freed), ctypes.byref(dims), _addr(workspace), _stream_of(device, stream))
-    _check(rc, "ddtree_kv_evict")
+    _run_on(device, lib().ddtree_kv_evict, "ddtree_kv_evict", weight.data_ptr(), slot_idx.data_ptr(),
+            prefix_len.data_ptr(), keep_len.data_ptr(), int(sink), int(recent), slot_idx_out.data_ptr(),
+            weight_out.data_ptr(), prefix_len_out.data_ptr(), freed.data_ptr(), ctypes.byref(dims),
+            workspace.data_ptr(), _stream_of(device, stream))
     return slot_idx_out, weight_out, prefix_len_out, freed
 
 
@@ -431,20 +423,17 @@ def block_summary(kv_pool, slot_idx, prefix_len, block, from_len=None, summary=N
     summary = torch.zeros((B, n, D_QK), dtype=torch.bfloat16, device=device) if summary is None else summary
     scale = torch.zeros((B, n), dtype=torch.float32, device=device) if scale is None else scale
     workspace = torch.empty(256, dtype=torch.uint8, device=device) if workspace is None else workspace
-    checks = dict(kv_pool=(kv_pool, torch.bfloat16, (dims.pool_slots, D_QK)),
-                  slot_idx=(slot_idx, torch.int32, (B, stride)), prefix_len=(prefix_len, torch.int32, (B,)),
-                  summary=(summary, torch.bfloat16, (B, n, D_QK)), scale=(scale, torch.float32, (B, n)),
-                  workspace=(workspace, torch.uint8, workspace.shape))
+    _need(device, ("kv_pool", kv_pool, torch.bfloat16, (dims.pool_slots, D_QK)),
+          ("slot_idx", slot_idx, torch.int32, (B, stride)), ("prefix_len", prefix_len, torch.int32, (B,)),
+          ("summary", summary, torch.bfloat16, (B, n, D_QK)), ("scale", scale, torch.float32, (B, n)),
+          ("workspace", workspace, torch.uint8, workspace.shape))
     if from_len is not None:
-        checks["from_len"] = (from_len, torch.int32, (B,))
-    _need(device, **checks)
+        _need(device, ("from_len", from_len, torch.int32, (B,)))
     if workspace.numel() < 256:
         raise ValueError("workspace must hold 256 bytes")
-    with _On(device):
-        rc = lib().ddtree_block_summary(_addr(kv_pool), _addr(slot_idx), _addr(prefix_len), _addr(from_len), int(block),
-                                        _addr(summary), _addr(scale), ctypes.byref(dims), _addr(workspace),
-                                        _stream_of(device, stream))
-    _check(rc, "ddtree_block_summary")
+    _run_on(device, lib().ddtree_block_summary, "ddtree_block_summary", kv_pool.data_ptr(), slot_idx.data_ptr(),
+            prefix_len.data_ptr(), _addr(from_len), int(block), summary.data_ptr(), scale.data_ptr(),
+            ctypes.byref(dims), workspace.data_ptr(), _stream_of(device, stream))
     return summary, scale
 
 
@@ -461,7 +450,8 @@ class BlockSelector:
         self.dims = make_dims(batch, nodes, heads, 1, max_prefix_len, max_prefix_len)
         self.block, self.topk, self.first, self.last = int(block), int(topk), int(first), int(last)
         self.device = _cuda_device(device)
-        n = int(self.lib.ddtree_block_select_workspace_bytes(ctypes.byref(self.dims), self.block))
+        self.dims_ref = ctypes.byref(self.dims)
+        n = int(self.lib.ddtree_block_select_workspace_bytes(self.dims_ref, self.block))
         if n == 0:
             raise DDTError(-2, "ddtree_block_select_workspace_bytes")
         self.blocks = -(-int(max_prefix_len) // self.block)
@@ -472,16 +462,14 @@ class BlockSelector:
         d = self.dims
         if out is None:
             out = torch.empty((d.batch, d.num_nodes, self.topk), dtype=torch.int32, device=self.device)
-        _need(self.device, q=(q, torch.bfloat16, (d.batch, d.num_nodes, d.num_heads, D_QK)),
-              summary=(summary, torch.bfloat16, (d.batch, self.blocks, D_QK)),
-              scale=(scale, torch.float32, (d.batch, self.blocks)), prefix_len=(prefix_len, torch.int32, (d.batch,)),
-              out=(out, torch.int32, (d.batch, d.num_nodes, self.topk)))
-        with _On(self.device):
-            rc = self.lib.ddtree_block_select(_addr(q), _addr(summary), _addr(scale), _addr(prefix_len), self.block,
-                                              self.topk, self.first, self.last, _addr(out), ctypes.byref(d),
-                                              _addr(self.workspace), self.workspace.numel(),
-                                              _stream_of(self.device, stream))
-        _check(rc, "ddtree_block_select")
+        _need(self.device, ("q", q, torch.bfloat16, (d.batch, d.num_nodes, d.num_heads, D_QK)),
+              ("summary", summary, torch.bfloat16, (d.batch, self.blocks, D_QK)),
+              ("scale", scale, torch.float32, (d.batch, self.blocks)),
+              ("prefix_len", prefix_len, torch.int32, (d.batch,)),
+              ("out", out, torch.int32, (d.batch, d.num_nodes, self.topk)))
+        _run_on(self.device, self.lib.ddtree_block_select, "ddtree_block_select", q.data_ptr(), summary.data_ptr(),
+                scale.data_ptr(), prefix_len.data_ptr(), self.block, self.topk, self.first, self.last, out.data_ptr(),
+                self.dims_ref, self.workspace.data_ptr(), self.workspace.numel(), _stream_of(self.device, stream))
         return out
 
     def status(self, stream=None) -> int:
@@ -503,8 +491,9 @@ class BlockVerifier:
                               slot_stride if max_prefix_len is None else max_prefix_len)
         self.block, self.topk = int(block), int(topk)
         self.device = _cuda_device(device)
-        with _On(self.device):
-            n = int(self.lib.ddtree_verify_blocks_workspace_bytes(ctypes.byref(self.dims), self.block, self.topk))
+        self.dims_ref = ctypes.byref(self.dims)
+        with torch.cuda.device(self.device):
+            n = int(self.lib.ddtree_verify_blocks_workspace_bytes(self.dims_ref, self.block, self.topk))
         if n == 0:
             raise DDTError(-2, "ddtree_verify_blocks_workspace_bytes")
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -518,18 +507,17 @@ class BlockVerifier:
             out = torch.empty((B, T, H, D_V), dtype=torch.bfloat16, device=self.device)
         if lse is None:
             lse = torch.empty((B, T, H), dtype=torch.float32, device=self.device)
-        _need(self.device, q=(q, torch.bfloat16, (B, T, H, D_QK)), kv_pool=(kv_pool, torch.bfloat16, (d.pool_slots, D_QK)),
-              slot_idx=(slot_idx, torch.int32, (B, d.slot_stride)), prefix_len=(prefix_len, torch.int32, (B,)),
-              tree_parent=(tree_parent, torch.int32, (B, T)), tree_slot_idx=(tree_slot_idx, torch.int32, (B, T)),
-              block_idx=(block_idx, torch.int32, (B, T, self.topk)), out=(out, torch.bfloat16, (B, T, H, D_V)),
-              lse=(lse, torch.float32, (B, T, H)))
-        with _On(self.device):
-            rc = self.lib.ddtree_verify_attn_blocks(_addr(q), _addr(kv_pool), _addr(slot_idx), _addr(prefix_len),
-                                                    _addr(tree_parent), _addr(tree_slot_idx), _addr(block_idx),
-                                                    self.block, self.topk, float(sm_scale), _addr(out), _addr(lse),
-                                                    ctypes.byref(d), _addr(self.workspace), self.workspace.numel(),
-                                                    _stream_of(self.device, stream))
-        _check(rc, "ddtree_verify_attn_blocks")
+        _need(self.device, ("q", q, torch.bfloat16, (B, T, H, D_QK)),
+              ("kv_pool", kv_pool, torch.bfloat16, (d.pool_slots, D_QK)),
+              ("slot_idx", slot_idx, torch.int32, (B, d.slot_stride)), ("prefix_len", prefix_len, torch.int32, (B,)),
+              ("tree_parent", tree_parent, torch.int32, (B, T)), ("tree_slot_idx", tree_slot_idx, torch.int32, (B, T)),
+              ("block_idx", block_idx, torch.int32, (B, T, self.topk)), ("out", out, torch.bfloat16, (B, T, H, D_V)),
+              ("lse", lse, torch.float32, (B, T, H)))
+        _run_on(self.device, self.lib.ddtree_verify_attn_blocks, "ddtree_verify_attn_blocks", q.data_ptr(),
+                kv_pool.data_ptr(), slot_idx.data_ptr(), prefix_len.data_ptr(), tree_parent.data_ptr(),
+                tree_slot_idx.data_ptr(), block_idx.data_ptr(), self.block, self.topk, sm_scale, out.data_ptr(),
+                lse.data_ptr(), self.dims_ref, self.workspace.data_ptr(), self.workspace.numel(),
+                _stream_of(self.device, stream))
         return out, lse
 
     def status(self, stream=None) -> int:
