@@ -307,7 +307,8 @@ DDT_API int ddtree_verify_attn_static_scratch(const void* q, const void* kv_pool
 
 /*
  * Keeping a long request's cache small: accumulated attention weights of the
- * prefix keys, and eviction of the positions that weigh least.
+ * prefix keys, and eviction of the positions that weigh least.  (These entry
+ * points and the block ones below take max_prefix_len up to 2^30.)
  *
  * ddtree_kv_weight adds up what a verify call's softmax gave each prefix key:
  *   weight_out[b][j] = decay * weight_in[b][j]

@@ -23,6 +23,14 @@ constexpr int kBlockUnitTiles = 4;  // fixed cost of one block-attention unit, i
 
 int round32(int x) { return (x + 31) / 32 * 32; }
 
+// check_dims, and the positions that these kernels count: with steps of a few
+// thousand and block sizes added they stay inside 32 bits.
+int check_cache_dims(const ddt_dims* d) {
+  const int rc = check_dims(d);
+  if (rc != DDT_OK) return rc;
+  return d->max_prefix_len > (1 << 30) ? DDT_ERR_DIMS : DDT_OK;
+}
+
 bool clear_status(void* workspace, cudaStream_t s) {
   return cudaMemsetAsync(workspace, 0, 4 * sizeof(int32_t), s) == cudaSuccess;
 }
@@ -65,7 +73,7 @@ struct WeightLayout {
 };
 // sm_count 0: the sizes only (no grid, no bytes)
 int weight_layout(const ddt_dims* d, int32_t num_sel, int sm_count, WeightLayout* w) {
-  const int rc = check_dims(d);
+  const int rc = check_cache_dims(d);
   if (rc != DDT_OK) return rc;
   if (num_sel < 0 || num_sel > 65535) return DDT_ERR_DIMS;
   const int64_t rows = int64_t(num_sel > 0 ? num_sel : d->num_nodes) * d->num_heads;
@@ -89,7 +97,7 @@ struct SelectLayout {
   size_t q_off, scale_off, score_off, bytes;
 };
 int select_layout(const ddt_dims* d, int32_t block, SelectLayout* w) {
-  const int rc = check_dims(d);
+  const int rc = check_cache_dims(d);
   if (rc != DDT_OK) return rc;
   if (!block_ok(block)) return DDT_ERR_DIMS;
   const size_t nodes = size_t(d->batch) * d->num_nodes, rows = nodes * d->num_heads;
@@ -111,7 +119,7 @@ struct BlocksLayout {
 // minimise waves * (64-key tiles of a unit + kBlockUnitTiles), the tiles being
 // those of lists that do not overlap (how far they do is known on the device only).
 int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, BlocksLayout* w) {
-  const int rc = check_dims(d);
+  const int rc = check_cache_dims(d);
   if (rc != DDT_OK) return rc;
   if (!block_ok(block) || topk < 1 || topk > (1 << 20)) return DDT_ERR_DIMS;
   const int H = d->num_heads, T = d->num_nodes;
@@ -226,7 +234,7 @@ extern "C" int ddtree_kv_evict(const float* weight, const int32_t* slot_idx, con
                                const int32_t* keep_len, int32_t sink, int32_t recent, int32_t* slot_idx_out,
                                float* weight_out, int32_t* prefix_len_out, int32_t* freed_slots, const ddt_dims* dims,
                                void* workspace, ddt_stream_t stream) {
-  int rc = check_dims(dims);
+  int rc = check_cache_dims(dims);
   if (rc != DDT_OK) return rc;
   if (sink < 0 || recent < 0) return DDT_ERR_DIMS;
   if (dims->batch == 0) return DDT_OK;
@@ -271,7 +279,7 @@ extern "C" int ddtree_kv_evict(const float* weight, const int32_t* slot_idx, con
 extern "C" int ddtree_block_summary(const void* kv_pool, const int32_t* slot_idx, const int32_t* prefix_len,
                                     const int32_t* from_len, int32_t block, void* summary, float* scale,
                                     const ddt_dims* dims, void* workspace, ddt_stream_t stream) {
-  int rc = check_dims(dims);
+  int rc = check_cache_dims(dims);
   if (rc != DDT_OK) return rc;
   if (!block_ok(block)) return DDT_ERR_DIMS;
   if (dims->batch == 0) return DDT_OK;

@@ -312,6 +312,13 @@ def _stream_of(device, stream):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
+def _keep(stream, *tensors):
+    """Tell the allocator that `stream` uses tensors which may have been allocated for the current one."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 class KeyWeights:
     """Accumulated attention weight of every prefix key (ddtree_kv_weight), with a workspace for one set of sizes.
 
@@ -363,6 +370,7 @@ class KeyWeights:
                 slot_idx.data_ptr(), prefix_len.data_ptr(), lse.data_ptr(), _addr(node_idx), sel, sm_scale, decay,
                 _addr(weight), out.data_ptr(), self.dims_ref, self.workspace.data_ptr(), self.workspace.numel(),
                 _stream_of(self.device, stream))
+        _keep(stream, out, self.workspace)
         return out
 
     def status(self, stream=None) -> int:
@@ -400,6 +408,7 @@ def kv_evict(weight, slot_idx, prefix_len, keep_len, sink=0, recent=0, slot_idx_
             prefix_len.data_ptr(), keep_len.data_ptr(), int(sink), int(recent), slot_idx_out.data_ptr(),
             weight_out.data_ptr(), prefix_len_out.data_ptr(), freed.data_ptr(), ctypes.byref(dims),
             workspace.data_ptr(), _stream_of(device, stream))
+    _keep(stream, workspace, slot_idx_out, weight_out, prefix_len_out, freed)
     return slot_idx_out, weight_out, prefix_len_out, freed
 
 
@@ -434,6 +443,7 @@ def block_summary(kv_pool, slot_idx, prefix_len, block, from_len=None, summary=N
     _run_on(device, lib().ddtree_block_summary, "ddtree_block_summary", kv_pool.data_ptr(), slot_idx.data_ptr(),
             prefix_len.data_ptr(), _addr(from_len), int(block), summary.data_ptr(), scale.data_ptr(),
             ctypes.byref(dims), workspace.data_ptr(), _stream_of(device, stream))
+    _keep(stream, workspace, summary, scale)
     return summary, scale
 
 
@@ -470,6 +480,7 @@ class BlockSelector:
         _run_on(self.device, self.lib.ddtree_block_select, "ddtree_block_select", q.data_ptr(), summary.data_ptr(),
                 scale.data_ptr(), prefix_len.data_ptr(), self.block, self.topk, self.first, self.last, out.data_ptr(),
                 self.dims_ref, self.workspace.data_ptr(), self.workspace.numel(), _stream_of(self.device, stream))
+        _keep(stream, out, self.workspace)
         return out
 
     def status(self, stream=None) -> int:
@@ -518,6 +529,7 @@ class BlockVerifier:
                 tree_slot_idx.data_ptr(), block_idx.data_ptr(), self.block, self.topk, sm_scale, out.data_ptr(),
                 lse.data_ptr(), self.dims_ref, self.workspace.data_ptr(), self.workspace.numel(),
                 _stream_of(self.device, stream))
+        _keep(stream, out, lse, self.workspace)
         return out, lse
 
     def status(self, stream=None) -> int:

@@ -91,6 +91,12 @@ def test_arguments(lib):
     assert call(lib, "ddtree_block_select", change(SELECT, 7, -1), d) == -2
 
 
+@pytest.mark.parametrize("fn,args", ALL)
+def test_longest_prefix(lib, fn, args):
+    far = dims(batch=1, slot_stride=(1 << 30) + 1, max_prefix_len=(1 << 30) + 1)
+    assert call(lib, fn, args, far) == -2
+
+
 def test_sizes_past_the_counters(lib):
     # 2^31 query rows and more, and more key tiles than the kernels count
     big = dims(batch=65535, nodes=128, heads=1024)

@@ -185,6 +185,57 @@ def test_other_stream_and_graph_replay():
     assert torch.equal(out[0, :120], want[0, :120]) and not bool(out[0, 120:].any()) and torch.equal(out[1], want[1])
 
 
+def test_chosen_nodes_in_a_graph():
+    """The packed rows are made by a kernel of the same graph, which the scores follow as a dependent launch."""
+    d = make(2, [700, 350], 9, 16, seed=9)
+    sel = torch.tensor([[0, 2, 5], [1, -1, -1]], dtype=torch.int32, device="cuda")
+    k = ddtree.KeyWeights(2, 9, 16, d["kv"].shape[0], 700)
+    out = torch.zeros(2, 700, device="cuda")
+    call = lambda: k(d["q"], d["kv"], d["slot"], d["lens"], d["lse"], SCALE, node_idx=sel, out=out)  # noqa: E731
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    sel.copy_(torch.tensor([[8, 3, -1], [4, 4, 0]], dtype=torch.int32, device="cuda"))
+    d["q"].copy_(torch.randn(d["q"].shape, device="cuda").to(torch.bfloat16))
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    check(d, out, sel=sel)
+
+
+def test_slots_behind_four_gigabytes():
+    """Row offsets past 32 bits: the used rows are the last of a pool of 4.2 million."""
+    rows = 4_200_000
+    d = make(1, [500], 3, 16, seed=10)
+    big = torch.zeros(rows, 576, dtype=torch.bfloat16, device="cuda")
+    n = d["kv"].shape[0]
+    big[rows - n:] = d["kv"]
+    d["kv"], d["slot"] = big, (d["slot"] + (rows - n)).contiguous()
+    k = ddtree.KeyWeights(1, 3, 16, rows, 500)
+    out = k(d["q"], d["kv"], d["slot"], d["lens"], d["lse"], SCALE)
+    check(d, out)
+    summary, scale = ddtree.block_summary(d["kv"], d["slot"], d["lens"], 64)
+    small, small_scale = ddtree.block_summary(big[rows - n:].clone(), d["slot"] - (rows - n), d["lens"], 64)
+    assert torch.equal(summary, small) and torch.equal(scale, small_scale)
+    parent = torch.tensor([[-1, 0, 1]], dtype=torch.int32, device="cuda")
+    tree = torch.tensor([[rows - 1, rows - 2, rows - 3]], dtype=torch.int32, device="cuda")
+    idx = torch.arange(8, dtype=torch.int32, device="cuda").expand(1, 3, 8).contiguous()
+    a = ddtree.BlockVerifier(1, 3, 16, rows, 500, 64, 8)(d["q"], big, d["slot"], d["lens"], parent, tree, idx, SCALE)
+    b = ddtree.BlockVerifier(1, 3, 16, n, 500, 64, 8)(d["q"], big[rows - n:].clone(), d["slot"] - (rows - n), d["lens"],
+                                                      parent, tree - (rows - n), idx, SCALE)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_empty_prefixes():
+    d = make(2, [0, 0], 3, 16, seed=11, stride=64)
+    k = ddtree.KeyWeights(2, 3, 16, d["kv"].shape[0], 64)
+    out = torch.full((2, 64), 3.0, device="cuda")
+    k(d["q"], d["kv"], d["slot"], d["lens"], d["lse"], SCALE, out=out)
+    assert k.status() == 0 and bool((out == 3.0).all())
+
+
 def test_refusals():
     d = make(1, [64], 2, 16)
     k = ddtree.KeyWeights(1, 2, 16, d["kv"].shape[0], 64)
