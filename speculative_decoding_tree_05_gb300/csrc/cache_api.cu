@@ -213,7 +213,8 @@ extern "C" int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_
   p.row_aux = packed ? reinterpret_cast<const float*>(ws + w.lse_off) : lse;
   if (!encode_pool_map(&p.tmap_q, qs, q_rows, 64, p.tile_n / 2)) return DDT_ERR_LAUNCH;  // one CTA's half of a tile
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!clear_status(workspace, s)) return DDT_ERR_LAUNCH;
+  // (with packed rows their kernel clears the status word)
+  if (!packed && !clear_status(workspace, s)) return DDT_ERR_LAUNCH;
   if (packed) {
     PackParams k = {};
     k.q = static_cast<const uint16_t*>(q);
@@ -225,6 +226,8 @@ extern "C" int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_
     k.heads = dims->num_heads;
     k.sel = num_sel;
     k.status = p.status;
+    p.node_idx = node_idx;
+    p.sel = num_sel;
     if (launch_pack_nodes(k, dims->batch, s) != cudaSuccess) return DDT_ERR_LAUNCH;
   }
   return launch_scores(p, kScoreWeight, sms, packed, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
@@ -258,7 +261,6 @@ extern "C" int ddtree_kv_evict(const float* weight, const int32_t* slot_idx, con
   int sms = 0;
   if ((rc = current_device(&sms)) != DDT_OK) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!clear_status(workspace, s)) return DDT_ERR_LAUNCH;
   EvictParams p = {};
   p.weight = weight;
   p.slot_idx = slot_idx;

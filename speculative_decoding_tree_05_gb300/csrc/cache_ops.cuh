@@ -42,6 +42,8 @@ struct ScoreParams {
   int64_t part_stride;       // batch * slot_stride
   float scale_log2;          // kScoreWeight: sm_scale * log2(e)
   float decay;
+  const int32_t* node_idx;   // kScoreWeight with packed rows: [B, sel], looked over for the status word; else null
+  int32_t sel;
   const float* row_aux;      // [B, rows]: kScoreWeight natural-log lse, kScoreBlock query scales
   const float* weight_in;    // kScoreWeight: [B, slot_stride] or null
   float* weight_out;         // kScoreWeight: [B, slot_stride]

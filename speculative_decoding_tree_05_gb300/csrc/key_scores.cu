@@ -268,7 +268,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
         if (p.slot_idx != nullptr) {
           const int slot = __ldg(p.slot_idx + static_cast<int64_t>(u.b) * p.slot_stride + j);
           if (slot >= 0 && slot < p.pool_slots) row = slot;
-          if (row < 0) atomicOr(p.status, kStatusBadSlot);
+          if (row < 0) {
+            grid_dep_wait();  // (the kernel before may clear the word)
+            atomicOr(p.status, kStatusBadSlot);
+          }
         } else {
           row = static_cast<int>(u.b * p.key_stride + j);
         }
@@ -452,6 +455,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
       const int L = __ldg(p.prefix_len + b);
       if (L < 0 || L > p.max_prefix_len) atomicOr(p.status, kStatusBadPrefix);
     }
+  if (blockIdx.x == 0 && p.node_idx != nullptr)
+    for (int64_t i = tid; i < static_cast<int64_t>(p.batch) * p.sel; i += kScThreads) {
+      const int t = __ldg(p.node_idx + i);
+      if (t != -1 && (t < 0 || t >= p.nodes)) atomicOr(p.status, kStatusBadNode);
+    }
 }
 
 // Sums of the query shares of a key, in order, and the decayed old weight.
@@ -469,11 +477,12 @@ __global__ void __launch_bounds__(256) weight_sum_kernel(const __grid_constant__
 
 // One CTA copies one selected node's rows (H x 72 pieces of 16 bytes) and lse.
 __global__ void __launch_bounds__(256) pack_nodes_kernel(PackParams p) {
-  grid_dep_launch();
   const int s = blockIdx.x, b = blockIdx.y;
+  // The call's first kernel clears the status word; the score kernel reports a bad entry.
+  if (s == 0 && b == 0 && threadIdx.x == 0) *p.status = 0;
+  grid_dep_launch();
   const int t = __ldg(p.node_idx + static_cast<int64_t>(b) * p.sel + s);
   const bool in = t >= 0 && t < p.nodes;
-  if (!in && t != -1 && threadIdx.x == 0) atomicOr(p.status, kStatusBadNode);
   const int64_t to = (static_cast<int64_t>(b) * p.sel + s) * p.heads;
   const int64_t from = (static_cast<int64_t>(b) * p.nodes + (in ? t : 0)) * p.heads;
   const uint4* src = reinterpret_cast<const uint4*>(p.q + from * kDqk);

@@ -46,9 +46,17 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int
   const int rank = static_cast<int>(cluster_ctarank()), ctas = gridDim.x;  // one cluster spans x
   const int b = blockIdx.y;
   int L = __ldg(p.prefix_len + b);
-  if (L < 0 || L > p.max_prefix_len) {
-    if (rank == 0 && tid == 0) atomicOr(p.status, kStatusBadPrefix);
-    L = L < 0 ? 0 : p.max_prefix_len;
+  L = L < 0 ? 0 : (L > p.max_prefix_len ? p.max_prefix_len : L);
+  if (rank == 0 && b == 0) {
+    // The lengths are all that can be wrong, so one CTA looks at every request's
+    // and writes the status word as a whole: no clear before the launch.
+    bool bad = false;
+    for (int i = tid; i < gridDim.y; i += kEvThreads) {
+      const int n = __ldg(p.prefix_len + i);
+      bad = bad || n < 0 || n > p.max_prefix_len;
+    }
+    bad = __syncthreads_or(bad) != 0;
+    if (tid == 0) *p.status = bad ? kStatusBadPrefix : 0;
   }
   const int keep = min(max(__ldg(p.keep_len + b), 0), L);
   const int lo = min(p.sink, L), hi = max(lo, L - min(p.recent, L));  // [lo, hi): unprotected
