@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
   constexpr int kWarps = kThreads / 32;
   extern __shared__ uint32_t keys_sh[];
   __shared__ int hist[kDigits][kBins];
-  __shared__ int tmp[kWarps + 2];
+  __shared__ int tmp[kWarps + 3];
   __shared__ int warp_gt[32], warp_eq[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.x, b = blockIdx.y;
@@ -99,22 +99,30 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
   const bool in_sh = n <= cached;
   auto load_key = [&](int i) { return i < lo || i >= hi ? 0xffffffffu : order_key_bits(__float_as_uint(__ldcg(score + i))); };
   if (in_sh) {
-#pragma unroll 4
-    for (int i = tid; i < n; i += kThreads) keys_sh[i] = load_key(i);
+    constexpr int kBatch = 8;  // scores in flight per thread
+    for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
+      uint32_t k[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (i0 + u * kThreads < n) k[u] = load_key(i0 + u * kThreads);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (i0 + u * kThreads < n) keys_sh[i0 + u * kThreads] = k[u];
+    }
   }
   if (tid < 32) warp_gt[tid] = warp_eq[tid] = 0;
   __syncthreads();
   auto key_of = [&](int i) { return in_sh ? keys_sh[i] : load_key(i); };
   uint32_t T = 0;
   int want = need;
+  bool found = false;
 #pragma unroll
   for (int pass = 0; pass < kDigits; ++pass) {
+    if (found) break;
 #pragma unroll 4
     for (int i = lo + tid; i < hi; i += kThreads) count_key(hist[pass], key_of(i), T, pass);
     __syncthreads();
-    const int2 r = find_bin<kThreads>(want, [&](int x) { return hist[pass][x]; }, tmp);
-    T |= static_cast<uint32_t>(r.x) << digit_shift(pass);
-    want -= r.y;
+    found = take_digit(find_bin<kThreads>(want, [&](int x) { return hist[pass][x]; }, tmp), pass, &T, &want);
   }
   const int ties = want;
   const WarpRun run = warp_run(0, n, kWarps, warp);

@@ -34,7 +34,7 @@ constexpr int kEvMaxCached = 40960;               // order keys a CTA keeps in s
 struct EvictShared {
   int hist[kBins];            // this CTA's histogram of a digit
   int total[kDigits][kBins];  // the cluster's, in the bins that this CTA owns
-  int tmp[kEvWarps + 2];
+  int tmp[kEvWarps + 3];
   int warp_gt[kEvWarps], warp_eq[kEvWarps];
   int own[2];                 // this CTA's positions kept for sure, at T
 };
@@ -99,8 +99,10 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int
     const int from = max(begin, lo), to = min(end, hi);
     const int log_own = 31 - __clz(kBins / ctas);  // bins per owner
     int want = need;
+    bool found = false;  // the same in every CTA
 #pragma unroll
     for (int pass = 0; pass < kDigits; ++pass) {
+      if (found) break;
       for (int i = tid; i < kBins; i += kEvThreads) sh.hist[i] = 0;
       __syncthreads();
 #pragma unroll 4
@@ -111,11 +113,9 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int
         if (n != 0) red_shared_cluster_add(mapa_shared(smem_u32(&sh.total[pass][i]), i >> log_own), n);
       }
       cluster_sync();  // every CTA's counts have arrived
-      const int2 r = find_bin<kEvThreads>(want, [&](int x) {
+      found = take_digit(find_bin<kEvThreads>(want, [&](int x) {
         return ld_shared_cluster_b32(mapa_shared(smem_u32(&sh.total[pass][x]), x >> log_own));
-      }, sh.tmp);
-      T |= static_cast<uint32_t>(r.x) << digit_shift(pass);
-      want -= r.y;
+      }, sh.tmp), pass, &T, &want);
     }
     ties = want;
   }

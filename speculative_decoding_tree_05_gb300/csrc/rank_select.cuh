@@ -25,10 +25,10 @@ __device__ __forceinline__ void count_key(int* hist, uint32_t key, uint32_t pref
 }
 
 // The bin of the want-th largest key (want >= 1), bins counted from the top, and
-// the keys in higher bins; total(bin) is a bin's count.  Every thread of the block (kThreads, a multiple of
-// 32 that divides kBins) calls it.  tmp: kThreads / 32 + 2 ints of shared memory.
+// the keys in higher bins and in it; total(bin) is a bin's count.  Every thread of the block (kThreads, a multiple of
+// 32 that divides kBins) calls it.  tmp: kThreads / 32 + 3 ints of shared memory.
 template <int kThreads, class TotalFn>
-__device__ __forceinline__ int2 find_bin(int want, TotalFn total, int* tmp) {
+__device__ __forceinline__ int3 find_bin(int want, TotalFn total, int* tmp) {
   constexpr int kPer = kBins / kThreads, kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int top = kBins - 1 - kPer * tid;  // thread t holds bins top, top - 1, ...
@@ -53,11 +53,26 @@ __device__ __forceinline__ int2 find_bin(int want, TotalFn total, int* tmp) {
     if (before < want && want <= before + c[i]) {
       tmp[kWarps] = top - i;
       tmp[kWarps + 1] = before;
+      tmp[kWarps + 2] = c[i];
     }
     before += c[i];
   }
   __syncthreads();
-  return make_int2(tmp[kWarps], tmp[kWarps + 1]);
+  return make_int3(tmp[kWarps], tmp[kWarps + 1], tmp[kWarps + 2]);
+}
+
+// One digit further: T gets the bin's digit, want becomes the rank within it.
+// True when the search is over: after the last digit, or as soon as the whole bin
+// is wanted (for most data after two digits: its keys are then those above T - 1
+// with no ties to choose among).
+__device__ __forceinline__ bool take_digit(int3 r, int pass, uint32_t* T, int* want) {
+  *T |= static_cast<uint32_t>(r.x) << digit_shift(pass);
+  *want -= r.y;
+  if (pass + 1 == kDigits) return true;
+  if (r.z != *want) return false;
+  *T -= 1;  // no key is 0: the lowest, of -inf, is 0x7fffff
+  *want = 0;
+  return true;
 }
 
 // Ordered emission.  A warp owns a run of consecutive positions; a position is
