@@ -58,6 +58,10 @@ __global__ void __launch_bounds__(kQuWarps * 32) quant_rows_kernel(QuantParams p
 }
 
 constexpr int kTkCached = 16384;  // scores kept in shared memory
+// Threads per node: 256 up to 1024 blocks (four scores a thread), 1024 beyond.
+constexpr int kTkSmall = 256, kTkLarge = 1024, kTkSmallBlocks = 1024;
+// a warp's run of scores in shared memory fits its 32 lanes' ballots
+static_assert(kTkCached <= kTkLarge / 32 * 1024 && kTkSmallBlocks <= kTkSmall / 32 * 1024, "");
 
 // One CTA per node: the digit select of rank_select.cuh over its scores, then
 // the chosen blocks in ascending order.
@@ -97,22 +101,21 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
   for (int i = tid; i < kDigits * kBins; i += kThreads) (&hist[0][0])[i] = 0;
   wait_scores();
   const bool in_sh = n <= cached;
-  auto load_key = [&](int i) { return i < lo || i >= hi ? 0xffffffffu : order_key_bits(__float_as_uint(__ldcg(score + i))); };
+  auto key_from = [&](int i, float x) { return i < lo || i >= hi ? 0xffffffffu : order_key_bits(__float_as_uint(x)); };
   if (in_sh) {
-    constexpr int kBatch = 8;  // scores in flight per thread
+    constexpr int kBatch = kThreads == kTkSmall ? kTkSmallBlocks / kTkSmall : 12;  // scores in flight per thread
     for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
-      uint32_t k[kBatch];
+      float x[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) x[u] = __ldcg(score + min(i0 + u * kThreads, n - 1));
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
-        if (i0 + u * kThreads < n) k[u] = load_key(i0 + u * kThreads);
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (i0 + u * kThreads < n) keys_sh[i0 + u * kThreads] = k[u];
+        if (i0 + u * kThreads < n) keys_sh[i0 + u * kThreads] = key_from(i0 + u * kThreads, x[u]);
     }
   }
   if (tid < 32) warp_gt[tid] = warp_eq[tid] = 0;
   __syncthreads();
-  auto key_of = [&](int i) { return in_sh ? keys_sh[i] : load_key(i); };
+  auto key_of = [&](int i) { return in_sh ? keys_sh[i] : key_from(i, __ldcg(score + i)); };
   uint32_t T = 0;
   int want = need;
   bool found = false;
@@ -126,21 +129,57 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
   }
   const int ties = want;
   const WarpRun run = warp_run(0, n, kWarps, warp);
-  const int2 mine = count_run(run, T, key_of);
-  if (lane == 0) {
-    warp_gt[warp] = mine.x;
-    warp_eq[warp] = mine.y;
+  auto before = [&](int2 mine) {  // the run's positions above T and at T -> those of the runs before it
+    if (lane == 0) {
+      warp_gt[warp] = mine.x;
+      warp_eq[warp] = mine.y;
+    }
+    __syncthreads();
+    return make_int2(__reduce_add_sync(0xffffffffu, lane < warp ? warp_gt[lane] : 0),
+                     __reduce_add_sync(0xffffffffu, lane < warp ? warp_eq[lane] : 0));
+  };
+  if (!in_sh) {
+    const int2 at = before(count_run(run, T, key_of));
+    emit_run<int>(run, T, at.x, at.y, ties, key_of, [](int i) { return i; }, [&](int, int v, bool kept, int to) {
+      if (kept) out[to] = v;
+    });
+    return;
   }
-  __syncthreads();
-  const int g = __reduce_add_sync(0xffffffffu, lane < warp ? warp_gt[lane] : 0);
-  const int e = __reduce_add_sync(0xffffffffu, lane < warp ? warp_eq[lane] : 0);
-  emit_run<int>(run, T, g, e, ties, key_of, [](int i) { return i; }, [&](int, int v, bool kept, int at) {
-    if (kept) out[at] = v;
-  });
+  // Few of the blocks are kept, so the count keeps each 32 positions' ballots, in
+  // the lane of that number, and the emission visits set bits alone.
+  uint32_t mg = 0, me = 0;
+#pragma unroll 4
+  for (int j = 0; j < 32; ++j) {
+    const int i = run.begin + 32 * j;
+    if (i >= run.end) break;
+    const uint32_t k = i + lane < run.end ? keys_sh[i + lane] : 0u;  // T > 0
+    const uint32_t bg = __ballot_sync(0xffffffffu, k > T), be = __ballot_sync(0xffffffffu, k == T);
+    if (lane == j) {
+      mg = bg;
+      me = be;
+    }
+  }
+  const int own = __popc(mg) | __popc(me) << 16;  // at most 1024 of each in a run
+  int incl = own;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += v;
+  }
+  const int all = __shfl_sync(0xffffffffu, incl, 31);
+  const int2 at = before(make_int2(all & 0xffff, all >> 16));
+  int g = at.x + ((incl - own) & 0xffff), e = at.y + ((incl - own) >> 16);
+  for (uint32_t m = mg | me; m != 0; m &= m - 1) {
+    const int bit = __ffs(m) - 1, i = run.begin + 32 * lane + bit;
+    if (mg >> bit & 1) {
+      out[g + min(e, ties)] = i;
+      ++g;
+    } else {
+      if (e < ties) out[g + e] = i;
+      ++e;
+    }
+  }
 }
-
-// Threads per node: 256 up to 1024 blocks (four scores a thread), 1024 beyond.
-constexpr int kTkSmall = 256, kTkLarge = 1024, kTkSmallBlocks = 1024;
 
 }  // namespace
 
