@@ -30,6 +30,8 @@ constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBatch = 12;                      // weights in flight per thread
 constexpr int kEvMaxCached = 40960;               // order keys a CTA keeps in shared memory
+constexpr int kEvMaxOrdered = 256;                // requests whose lengths every CTA ranks
+static_assert(kEvMaxOrdered <= kBins, "the lengths lie in the histogram");
 
 struct EvictShared {
   int hist[kBins];            // this CTA's histogram of a digit
@@ -39,15 +41,32 @@ struct EvictShared {
   int own[2];                 // this CTA's positions kept for sure, at T
 };
 
-__global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int cached) {
+__global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictParams p, int cached, bool by_length) {
   extern __shared__ uint32_t keys_sh[];           // [cached] order keys of this CTA's share
   __shared__ EvictShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank()), ctas = gridDim.x;  // one cluster spans x
-  const int b = blockIdx.y;
-  int L = __ldg(p.prefix_len + b);
-  L = L < 0 ? 0 : (L > p.max_prefix_len ? p.max_prefix_len : L);
-  if (rank == 0 && b == 0) {
+  auto length_of = [&](int i) {
+    const int n = __ldg(p.prefix_len + i);
+    return n < 0 ? 0 : (n > p.max_prefix_len ? p.max_prefix_len : n);
+  };
+  int b = blockIdx.y;
+  if (by_length) {  // the y-th longest request, the earlier one of equals
+    const int batch = gridDim.y;
+    for (int i = tid; i < batch; i += kEvThreads) sh.hist[i] = length_of(i);
+    __syncthreads();
+    for (int i = tid; i < batch; i += kEvThreads) {
+      const int mine = sh.hist[i];
+      int before = 0;
+#pragma unroll 8
+      for (int j = 0; j < batch; ++j) before += sh.hist[j] > mine || (sh.hist[j] == mine && j < i);
+      if (before == static_cast<int>(blockIdx.y)) sh.tmp[0] = i;
+    }
+    __syncthreads();
+    b = sh.tmp[0];
+  }
+  const int L = length_of(b);
+  if (rank == 0 && blockIdx.y == 0) {
     // The lengths are all that can be wrong, so one CTA looks at every request's
     // and writes the status word as a whole: no clear before the launch.
     bool bad = false;
@@ -171,9 +190,13 @@ cudaError_t launch_kv_evict(const EvictParams& p, int batch, int sm_count, cudaS
   // One CTA (1024 threads, 64 registers) fills an SM.  The largest cluster, up to
   // 16, with which the batch takes at most two rounds of the SMs: more CTAs a
   // request shorten its steps, further rounds repeat their fixed costs (64
-  // requests of up to 131072: 81 us in clusters of 8, 60 us in clusters of 4).
+  // requests of up to 131072, in the batch's order: 81 us in clusters of 8, 54 us in clusters of 4).
   int ctas = kEvMaxCluster;
   while (ctas > 1 && int64_t(ctas) * batch > 2 * sm_count) ctas /= 2;
+  // Where the clusters take more than one round, the long requests go first, so that
+  // the last to start are short (the same batch: 44 us; in its own order 54 us).
+  // Beyond 256 requests the rounds are many and even out.
+  const bool by_length = int64_t(ctas) * batch > sm_count && batch <= kEvMaxOrdered;
   const int64_t share = (int64_t(p.max_prefix_len) + ctas - 1) / ctas;
   const int cached = share <= kEvMaxCached ? static_cast<int>(share) : 0;
   cudaLaunchConfig_t cfg = {};
@@ -187,7 +210,7 @@ cudaError_t launch_kv_evict(const EvictParams& p, int batch, int sm_count, cudaS
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_evict_kernel, p, cached);
+  return cudaLaunchKernelEx(&cfg, kv_evict_kernel, p, cached, by_length);
 }
 
 }  // namespace ddt

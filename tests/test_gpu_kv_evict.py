@@ -66,6 +66,18 @@ def test_large_batches():
     run(w, lens, [int(n * f) for n, f in zip(lens, rng.random(len(lens)) * 1.1)], 4, 64)
 
 
+@pytest.mark.parametrize("batch", [20, 153, 256, 257, 400])
+def test_batches_whose_requests_take_turns(batch):
+    """More CTAs than SMs: equal, empty, too long and negative lengths in any order."""
+    rng = np.random.default_rng(batch)
+    w = rng.choice(rng.random(50, dtype=np.float32), (batch, 400))
+    lens = [int(x) for x in rng.choice([0, 1, 37, 37, 200, 399, 400], batch)]
+    keep = [int(n * f) for n, f in zip(lens, rng.random(batch) * 1.1)]
+    assert run(w, lens, keep, 2, 5) == 0
+    lens[batch // 2], lens[batch // 3] = -7, 401
+    assert run(w, lens, keep, 2, 5) == ddtree.STATUS_BAD_PREFIX
+
+
 def test_ties_and_special_values():
     rng = np.random.default_rng(1)
     n = 5000
