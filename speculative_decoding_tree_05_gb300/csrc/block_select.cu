@@ -60,8 +60,8 @@ __global__ void __launch_bounds__(kQuWarps * 32) quant_rows_kernel(QuantParams p
 constexpr int kTkCached = 16384;  // scores kept in shared memory
 // Threads per node: 256 up to 1024 blocks (four scores a thread), 1024 beyond.
 constexpr int kTkSmall = 256, kTkLarge = 1024, kTkSmallBlocks = 1024;
-// a warp's run of scores in shared memory fits its 32 lanes' ballots
-static_assert(kTkCached <= kTkLarge / 32 * 1024 && kTkSmallBlocks <= kTkSmall / 32 * 1024, "");
+// a warp's run of scores in shared memory is one span
+static_assert(kTkCached <= kTkLarge / 32 * kSpan && kTkSmallBlocks <= kTkSmall / 32 * kSpan, "");
 
 // One CTA per node: the digit select of rank_select.cuh over its scores, then
 // the chosen blocks in ascending order.
@@ -145,40 +145,14 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
     });
     return;
   }
-  // Few of the blocks are kept, so the count keeps each 32 positions' ballots, in
-  // the lane of that number, and the emission visits set bits alone.
-  uint32_t mg = 0, me = 0;
-#pragma unroll 4
-  for (int j = 0; j < 32; ++j) {
-    const int i = run.begin + 32 * j;
-    if (i >= run.end) break;
-    const uint32_t k = i + lane < run.end ? keys_sh[i + lane] : 0u;  // T > 0
-    const uint32_t bg = __ballot_sync(0xffffffffu, k > T), be = __ballot_sync(0xffffffffu, k == T);
-    if (lane == j) {
-      mg = bg;
-      me = be;
-    }
-  }
-  const int own = __popc(mg) | __popc(me) << 16;  // at most 1024 of each in a run
-  int incl = own;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += v;
-  }
-  const int all = __shfl_sync(0xffffffffu, incl, 31);
-  const int2 at = before(make_int2(all & 0xffff, all >> 16));
-  int g = at.x + ((incl - own) & 0xffff), e = at.y + ((incl - own) >> 16);
-  for (uint32_t m = mg | me; m != 0; m &= m - 1) {
-    const int bit = __ffs(m) - 1, i = run.begin + 32 * lane + bit;
-    if (mg >> bit & 1) {
-      out[g + min(e, ties)] = i;
-      ++g;
-    } else {
-      if (e < ties) out[g + e] = i;
-      ++e;
-    }
-  }
+  // few of the blocks are kept: the emission visits set bits alone
+  const SpanMasks masks = span_masks(run.begin, run.end, T, key_of);
+  int2 all;
+  const int2 in_run = span_before(masks, &all), at = before(all);
+  const int e = at.y + in_run.y;
+  int to = at.x + in_run.x + min(e, ties);
+  for (uint32_t m = masks.gt | lowest_bits(masks.eq, ties - e); m != 0; m &= m - 1)
+    out[to++] = run.begin + 32 * lane + __ffs(m) - 1;
 }
 
 }  // namespace

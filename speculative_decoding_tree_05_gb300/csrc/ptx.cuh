@@ -356,6 +356,9 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
                : "memory");
 }
 
+// Brings the 128-byte line of a global address to L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // True in one lane of a converged warp.  Code under it keeps its operands in
 // uniform registers, which the MMA instructions take (39 cycles an issue
 // instead of 46 behind a lane test).

@@ -100,12 +100,55 @@ __device__ __forceinline__ int2 count_run(WarpRun r, uint32_t T, KeyFn key_of) {
   }
   return make_int2(__reduce_add_sync(0xffffffffu, g), __reduce_add_sync(0xffffffffu, e));
 }
+// Keys in shared memory are counted by ballots that stay: lane j holds those of
+// the 32 positions from begin + 32 j on, for a span of up to 1024 positions.
+constexpr int kSpan = 1024;
+struct SpanMasks {
+  uint32_t gt, eq;  // above T, at T
+};
+template <class KeyFn>
+__device__ __forceinline__ SpanMasks span_masks(int begin, int end, uint32_t T, KeyFn key_of) {
+  const int lane = threadIdx.x & 31;
+  SpanMasks m = {0, 0};
+#pragma unroll 4
+  for (int j = 0; j < 32; ++j) {
+    const int i = begin + 32 * j;
+    if (i >= end) break;
+    const bool in = i + lane < end;
+    const uint32_t k = in ? key_of(i + lane) : 0u;
+    const uint32_t gt = __ballot_sync(0xffffffffu, k > T), eq = __ballot_sync(0xffffffffu, in && k == T);
+    if (lane == j) m = {gt, eq};
+  }
+  return m;
+}
+// Positions above T (x) and at T (y) in the span before the lane's; the span's in all.
+__device__ __forceinline__ int2 span_before(SpanMasks m, int2* all) {
+  const int lane = threadIdx.x & 31;
+  const int own = __popc(m.gt) | __popc(m.eq) << 16;
+  int incl = own;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += v;
+  }
+  const int sum = __shfl_sync(0xffffffffu, incl, 31);
+  *all = make_int2(sum & 0xffff, sum >> 16);
+  return make_int2((incl - own) & 0xffff, (incl - own) >> 16);
+}
+// The lowest n set bits of m.
+__device__ __forceinline__ uint32_t lowest_bits(uint32_t m, int n) {
+  if (n >= __popc(m)) return m;
+  uint32_t left = m;
+  for (int i = 0; i < n; ++i) left &= left - 1;
+  return m ^ left;
+}
+
 // emit(position, value, kept, rank among the kept positions before it) for a run
 // with g positions above T and e at T before it; fetch(position) gives the value,
 // loaded for kEmitBatch positions at a time.
 constexpr int kEmitBatch = 6;
-template <class Value, class KeyFn, class FetchFn, class EmitFn>
-__device__ __forceinline__ void emit_run(WarpRun r, uint32_t T, int g, int e, int ties, KeyFn key_of, FetchFn fetch,
+template <class Value, bool kTies, class KeyFn, class FetchFn, class EmitFn>
+__device__ __forceinline__ void emit_run_of(WarpRun r, uint32_t T, int g, int e, int ties, KeyFn key_of, FetchFn fetch,
                                          EmitFn emit) {
   const int lane = threadIdx.x & 31;
   const uint32_t lt = (1u << lane) - 1u;
@@ -124,13 +167,28 @@ __device__ __forceinline__ void emit_run(WarpRun r, uint32_t T, int g, int e, in
 #pragma unroll
     for (int u = 0; u < kEmitBatch; ++u) {
       const int i = i0 + 32 * u + lane;
-      const uint32_t mg = __ballot_sync(0xffffffffu, k[u] > T), me = __ballot_sync(0xffffffffu, k[u] == T && i < r.end);
-      const int eb = e + __popc(me & lt);
-      if (i < r.end) emit(i, v[u], k[u] > T || (k[u] == T && eb < ties), g + __popc(mg & lt) + min(eb, ties));
+      const uint32_t mg = __ballot_sync(0xffffffffu, k[u] > T);
+      bool kept = k[u] > T;
+      int at = g + __popc(mg & lt);
       g += __popc(mg);
-      e += __popc(me);
+      if (kTies) {
+        const uint32_t me = __ballot_sync(0xffffffffu, k[u] == T && i < r.end);
+        const int eb = e + __popc(me & lt);
+        kept = kept || (k[u] == T && eb < ties);
+        at += min(eb, ties);
+        e += __popc(me);
+      }
+      if (i < r.end) emit(i, v[u], kept, at);
     }
   }
+}
+template <class Value, class KeyFn, class FetchFn, class EmitFn>
+__device__ __forceinline__ void emit_run(WarpRun r, uint32_t T, int g, int e, int ties, KeyFn key_of, FetchFn fetch,
+                                         EmitFn emit) {
+  if (ties > 0)
+    emit_run_of<Value, true>(r, T, g, e, ties, key_of, fetch, emit);
+  else  // the usual case
+    emit_run_of<Value, false>(r, T, g, e, ties, key_of, fetch, emit);
 }
 
 }  // namespace ddt
