@@ -6,6 +6,7 @@
 // The integer product is exact in fp32 and both roundings are fixed by this
 // order, so the ranking is the definition's on every run and tiling.
 #include <cuda_runtime.h>
+#include <type_traits>
 #include <math_constants.h>
 #include "cache_ops.cuh"
 #include "ptx.cuh"
@@ -115,44 +116,49 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
   }
   if (tid < 32) warp_gt[tid] = warp_eq[tid] = 0;
   __syncthreads();
-  auto key_of = [&](int i) { return in_sh ? keys_sh[i] : key_from(i, __ldcg(score + i)); };
-  uint32_t T = 0;
-  int want = need;
-  bool found = false;
+  auto choose = [&](auto key_of, auto in_shared) {
+    uint32_t T = 0;
+    int want = need;
+    bool found = false;
 #pragma unroll
-  for (int pass = 0; pass < kDigits; ++pass) {
-    if (found) break;
+    for (int pass = 0; pass < kDigits; ++pass) {
+      if (found) break;
 #pragma unroll 4
-    for (int i = lo + tid; i < hi; i += kThreads) count_key(hist[pass], key_of(i), T, pass);
-    __syncthreads();
-    found = take_digit(find_bin<kThreads>(want, [&](int x) { return hist[pass][x]; }, tmp), pass, &T, &want);
-  }
-  const int ties = want;
-  const WarpRun run = warp_run(0, n, kWarps, warp);
-  auto before = [&](int2 mine) {  // the run's positions above T and at T -> those of the runs before it
-    if (lane == 0) {
-      warp_gt[warp] = mine.x;
-      warp_eq[warp] = mine.y;
+      for (int i = lo + tid; i < hi; i += kThreads) count_key(hist[pass], key_of(i), T, pass);
+      __syncthreads();
+      found = take_digit(find_bin<kThreads>(want, [&](int x) { return hist[pass][x]; }, tmp), pass, &T, &want);
     }
-    __syncthreads();
-    return make_int2(__reduce_add_sync(0xffffffffu, lane < warp ? warp_gt[lane] : 0),
-                     __reduce_add_sync(0xffffffffu, lane < warp ? warp_eq[lane] : 0));
+    const int ties = want;
+    const WarpRun run = warp_run(0, n, kWarps, warp);
+    auto before = [&](int2 mine) {  // the run's positions above T and at T -> those of the runs before it
+      if (lane == 0) {
+        warp_gt[warp] = mine.x;
+        warp_eq[warp] = mine.y;
+      }
+      __syncthreads();
+      return make_int2(__reduce_add_sync(0xffffffffu, lane < warp ? warp_gt[lane] : 0),
+                       __reduce_add_sync(0xffffffffu, lane < warp ? warp_eq[lane] : 0));
+    };
+    if constexpr (!decltype(in_shared)::value) {
+      const int2 at = before(count_run(run, T, key_of));
+      emit_run<int>(run, T, at.x, at.y, ties, key_of, [](int i) { return i; }, [&](int, int v, bool kept, int to) {
+        if (kept) out[to] = v;
+      });
+    } else {
+      // few of the blocks are kept: the emission visits set bits alone
+      const SpanMasks masks = span_masks(run.begin, run.end, T, key_of);
+      int2 all;
+      const int2 in_run = span_before(masks, &all), at = before(all);
+      const int e = at.y + in_run.y;
+      int to = at.x + in_run.x + min(e, ties);
+      for (uint32_t m = masks.gt | lowest_bits(masks.eq, ties - e); m != 0; m &= m - 1)
+        out[to++] = run.begin + 32 * lane + __ffs(m) - 1;
+    }
   };
-  if (!in_sh) {
-    const int2 at = before(count_run(run, T, key_of));
-    emit_run<int>(run, T, at.x, at.y, ties, key_of, [](int i) { return i; }, [&](int, int v, bool kept, int to) {
-      if (kept) out[to] = v;
-    });
-    return;
-  }
-  // few of the blocks are kept: the emission visits set bits alone
-  const SpanMasks masks = span_masks(run.begin, run.end, T, key_of);
-  int2 all;
-  const int2 in_run = span_before(masks, &all), at = before(all);
-  const int e = at.y + in_run.y;
-  int to = at.x + in_run.x + min(e, ties);
-  for (uint32_t m = masks.gt | lowest_bits(masks.eq, ties - e); m != 0; m &= m - 1)
-    out[to++] = run.begin + 32 * lane + __ffs(m) - 1;
+  if (in_sh)
+    choose([&](int i) { return keys_sh[i]; }, std::true_type());
+  else
+    choose([&](int i) { return key_from(i, __ldcg(score + i)); }, std::false_type());
 }
 
 }  // namespace
