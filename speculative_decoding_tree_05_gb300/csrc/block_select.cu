@@ -59,15 +59,16 @@ __global__ void __launch_bounds__(kQuWarps * 32) quant_rows_kernel(QuantParams p
 }
 
 constexpr int kTkCached = 16384;  // scores kept in shared memory
-// Threads per node: 256 up to 1024 blocks (four scores a thread), 1024 beyond.
-constexpr int kTkSmall = 256, kTkLarge = 1024, kTkSmallBlocks = 1024;
+// Threads per node: 256 up to 1024 blocks (four scores a thread); beyond, 1024,
+// which fill an SM, or 512, three CTAs to an SM, where there are more nodes than SMs.
+constexpr int kTkSmall = 256, kTkMany = 512, kTkLarge = 1024, kTkSmallBlocks = 1024;
 // a warp's run of scores in shared memory is one span
-static_assert(kTkCached <= kTkLarge / 32 * kSpan && kTkSmallBlocks <= kTkSmall / 32 * kSpan, "");
+static_assert(kTkCached <= kTkMany / 32 * kSpan && kTkSmallBlocks <= kTkSmall / 32 * kSpan, "");
 
 // One CTA per node: the digit select of rank_select.cuh over its scores, then
 // the chosen blocks in ascending order.
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int cached) {
+__global__ void __launch_bounds__(kThreads, kThreads == kTkMany ? 3 : 1) block_topk_kernel(TopkParams p, int cached) {
   constexpr int kWarps = kThreads / 32;
   extern __shared__ uint32_t keys_sh[];
   __shared__ int hist[kDigits][kBins];
@@ -164,9 +165,11 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(TopkParams p, int 
 }  // namespace
 
 cudaError_t configure_topk() {
-  cudaError_t e = cudaFuncSetAttribute(block_topk_kernel<kTkSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTkCached * 4);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(block_topk_kernel<kTkLarge>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTkCached * 4);
+  for (auto kernel : {block_topk_kernel<kTkSmall>, block_topk_kernel<kTkMany>, block_topk_kernel<kTkLarge>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTkCached * 4);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_quant_rows(const QuantParams& p, cudaStream_t stream) {
@@ -176,7 +179,7 @@ cudaError_t launch_quant_rows(const QuantParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_block_topk(const TopkParams& p, int batch, cudaStream_t stream) {
+cudaError_t launch_block_topk(const TopkParams& p, int batch, int sm_count, cudaStream_t stream) {
   if (batch == 0) return cudaSuccess;
   const int cached = p.blocks <= kTkCached ? p.blocks : kTkCached;
   // programmatic dependent of the scores: its set-up overlaps their end
@@ -189,9 +192,13 @@ cudaError_t launch_block_topk(const TopkParams& p, int batch, cudaStream_t strea
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.blockDim = dim3(p.blocks <= kTkSmallBlocks ? kTkSmall : kTkLarge);
-  return p.blocks <= kTkSmallBlocks ? cudaLaunchKernelEx(&cfg, block_topk_kernel<kTkSmall>, p, cached)
-                                    : cudaLaunchKernelEx(&cfg, block_topk_kernel<kTkLarge>, p, cached);
+  if (p.blocks <= kTkSmallBlocks) {
+    cfg.blockDim = dim3(kTkSmall);
+    return cudaLaunchKernelEx(&cfg, block_topk_kernel<kTkSmall>, p, cached);
+  }
+  const bool many = int64_t(p.nodes) * batch > sm_count;
+  cfg.blockDim = dim3(many ? kTkMany : kTkLarge);
+  return cudaLaunchKernelEx(&cfg, many ? block_topk_kernel<kTkMany> : block_topk_kernel<kTkLarge>, p, cached);
 }
 
 }  // namespace ddt

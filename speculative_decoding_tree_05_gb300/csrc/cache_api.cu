@@ -380,7 +380,7 @@ extern "C" int ddtree_block_select(const void* q, const void* summary, const flo
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   k.status = p.status;  // cleared there
   if (launch_quant_rows(k, s) != cudaSuccess ||
-      launch_scores(p, kScoreBlock, sms, true, s) != cudaSuccess || launch_block_topk(t, dims->batch, s) != cudaSuccess)
+      launch_scores(p, kScoreBlock, sms, true, s) != cudaSuccess || launch_block_topk(t, dims->batch, sms, s) != cudaSuccess)
     return DDT_ERR_LAUNCH;
   return DDT_OK;
 }

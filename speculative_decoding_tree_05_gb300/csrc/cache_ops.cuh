@@ -117,7 +117,7 @@ struct TopkParams {
   int32_t* status;
 };
 cudaError_t configure_topk();
-cudaError_t launch_block_topk(const TopkParams& p, int batch, cudaStream_t stream);
+cudaError_t launch_block_topk(const TopkParams& p, int batch, int sm_count, cudaStream_t stream);
 
 // ---------------------------------------------------------------- block attention
 constexpr int kBlockRows = 64;  // (node, head) rows of one group
