@@ -39,6 +39,16 @@ __global__ void __launch_bounds__(kQuWarps * 32) quant_rows_kernel(QuantParams p
   m = __reduce_max_sync(0xffffffffu, m);
   const bool finite = m < 0x7f80u;
   const float scale = finite ? __fmul_rn(__uint_as_float(m << 16), 1.f / 127.f) : CUDART_NAN_F;
+  // round(x / scale), half to even: x * (1 / scale) is within 1e-4 of the quotient
+  // (3 roundings of at most 127), so only a value that close to a half, or one that
+  // is not finite, needs the division.  |t| < 2^22, so adding 1.5 * 2^23 rounds it.
+  const float inv = finite && scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+  auto quantized = [&](float x) {
+    const float t = x * inv;
+    float n = __fadd_rn(__fadd_rn(t, 12582912.f), -12582912.f);
+    if (!(fabsf(t - n) < 0.4999f)) n = rintf(__fdiv_rn(x, scale));
+    return fminf(fmaxf(n, -127.f), 127.f);
+  };
   uint4* dst = reinterpret_cast<uint4*>(p.q_int + r * kDqk);
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
@@ -48,8 +58,8 @@ __global__ void __launch_bounds__(kQuWarps * 32) quant_rows_kernel(QuantParams p
     for (int k = 0; k < 4; ++k) {
       float a = 0.f, c = 0.f;
       if (finite && scale > 0.f) {
-        a = fminf(fmaxf(rintf(__fdiv_rn(__uint_as_float(w[k] << 16), scale)), -127.f), 127.f);
-        c = fminf(fmaxf(rintf(__fdiv_rn(__uint_as_float(w[k] & 0xffff0000u), scale)), -127.f), 127.f);
+        a = quantized(__uint_as_float(w[k] << 16));
+        c = quantized(__uint_as_float(w[k] & 0xffff0000u));
       }
       o[k] = (__float_as_uint(a) >> 16) | (__float_as_uint(c) & 0xffff0000u);
     }
