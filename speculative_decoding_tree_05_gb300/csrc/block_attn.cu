@@ -442,12 +442,19 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
         if (lane < 4) scratch[quarter * kBaRows + c0 + 8 * (i >> 1) + (i & 1)] = x;
       }
     };
+    float m[8];  // the running max of this thread's rows, as in mx
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = kBaUnset;
     for (int t = 0; t < n; ++t) {
       const int st = t & 1;
-      // (the masks were released with the stage's first group)
-      if (!mbar_wait_abortable(&sh.s_full[st], (t >> 1) & 1, abort, false, __LINE__) ||
-          !mbar_wait_abortable(&sh.k_full[st][0], (t >> 1) & 1, abort, false, __LINE__))
-        failed = true;
+      // A look at shared memory takes 100 to 300 cycles beside the gathers, so what
+      // can be looked at ahead of the scores is: the last tile's P.V, the key masks
+      // (released with the stage's first group).
+      bool pv_done = t == 0 || mbar_test_wait(&sh.k_empty[(t - 1) & 1][kBaGroups - 1], ((t - 1) >> 1) & 1);
+      if (!mbar_wait_abortable(&sh.k_full[st][0], (t >> 1) & 1, abort, false, __LINE__)) failed = true;
+      const uint64_t m0 = masks[st * kBaKeys + r0], m1 = masks[st * kBaKeys + r0 + 8];
+      const bool part = __any_sync(0xffffffffu, m0 != full || m1 != full);
+      if (!mbar_wait_abortable(&sh.s_full[st], (t >> 1) & 1, abort, false, __LINE__)) failed = true;
       __syncwarp();
       tc_fence_after();
       float s[16];
@@ -455,20 +462,17 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.s_free[st]);
-      const uint64_t m0 = masks[st * kBaKeys + r0], m1 = masks[st * kBaKeys + r0 + 8];
-      const bool part = __any_sync(0xffffffffu, m0 != full || m1 != full);
-      bool bad0 = false, bad1 = false;  // a row of non-finite scores that some rows do not read
+      // A key row that is not finite makes every score of it so, the zero rows' too;
+      // a query row that is not spoils its own scores alone.
+      bool bad0 = false, bad1 = false;
       if (part) {
-        float a0 = 0.f, a1 = 0.f;
+        float a0 = CUDART_INF_F, a1 = CUDART_INF_F;  // the least magnitude, a number if there is one
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          a0 += fabsf(s[4 * i]) + fabsf(s[4 * i + 1]);
-          a1 += fabsf(s[4 * i + 2]) + fabsf(s[4 * i + 3]);
+          a0 = fminf(a0, fminf(fabsf(s[4 * i]), fabsf(s[4 * i + 1])));
+          a1 = fminf(a1, fminf(fabsf(s[4 * i + 2]), fabsf(s[4 * i + 3])));
         }
-        a0 += __shfl_xor_sync(0xffffffffu, a0, 1);
-        a1 += __shfl_xor_sync(0xffffffffu, a1, 1);
-        a0 += __shfl_xor_sync(0xffffffffu, a0, 2);
-        a1 += __shfl_xor_sync(0xffffffffu, a1, 2);
+        // (of this thread's rows; the others' are asked below)
         bad0 = !(a0 < CUDART_INF_F) && m0 != full && m0 != 0;
         bad1 = !(a1 < CUDART_INF_F) && m1 != full && m1 != 0;
         const uint32_t w0 = static_cast<uint32_t>(m0 >> c0), w1 = static_cast<uint32_t>(m1 >> c0);
@@ -487,18 +491,21 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       float over = -CUDART_INF_F;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 m = *reinterpret_cast<const float2*>(mx + c0 + 8 * i);
-        over = fmax3(over, s[4 * i] - m.x, s[4 * i + 1] - m.y);
-        over = fmax3(over, s[4 * i + 2] - m.x, s[4 * i + 3] - m.y);
+        over = fmax3(over, s[4 * i] - m[2 * i], s[4 * i + 1] - m[2 * i + 1]);
+        over = fmax3(over, s[4 * i + 2] - m[2 * i], s[4 * i + 3] - m[2 * i + 1]);
       }
       if (failed) sh.fail[st] = 1;
-      const bool raise = bar_red_or(1, kBaSoftmax, failed || over > kBaThreshold);
+      const bool raise = bar_red_or(1, kBaSoftmax, failed || over > kBaThreshold || bad0 || bad1);
       if (raise && *const_cast<volatile int*>(&sh.fail[st])) {
         ok = false;
         break;
       }
       if (raise) {
-        if (t > 0) wait_pv(t - 1);  // the scratch is the P buffer, and O^T is rescaled
+        if (!pv_done) wait_pv(t - 1);  // the scratch is the P buffer, and O^T is rescaled
+        pv_done = true;
+        uint8_t* bad = smem + kBaOffP + 4 * kBaRows * 4;  // [64 keys][8 threads that hold its scores]
+        bad[r0 * 8 + half * 4 + (lane & 3)] = bad0;
+        bad[(r0 + 8) * 8 + half * 4 + (lane & 3)] = bad1;
         float top8[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -515,9 +522,15 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
           alpha_sh[id] = up ? fast_exp2(m - top) : 1.f;
           mx[id] = up ? top : m;
         }
+        bad0 = reinterpret_cast<const uint64_t*>(bad)[r0] == 0x0101010101010101ull;
+        bad1 = reinterpret_cast<const uint64_t*>(bad)[r0 + 8] == 0x0101010101010101ull;
         bar_sync(1, kBaSoftmax);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) l[i] *= alpha_sh[c0 + 8 * (i >> 1) + (i & 1)];
+        for (int i = 0; i < 8; ++i) {
+          const int row = c0 + 8 * (i >> 1) + (i & 1);
+          l[i] *= alpha_sh[row];
+          m[i] = mx[row];
+        }
         if (t > 0) {
 #pragma unroll 1
           for (int k0 = 0; k0 < 16; ++k0) {  // this warp's half of the columns, 8 at a time
@@ -539,16 +552,15 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       uint32_t pk[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 m = *reinterpret_cast<const float2*>(mx + c0 + 8 * i);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float x = fast_exp2(s[4 * i + 2 * h] - m.x), y = fast_exp2(s[4 * i + 2 * h + 1] - m.y);
+          const float x = fast_exp2(s[4 * i + 2 * h] - m[2 * i]), y = fast_exp2(s[4 * i + 2 * h + 1] - m[2 * i + 1]);
           l[2 * i] += x;
           l[2 * i + 1] += y;
           pk[2 * i + h] = pack_bf16x2(x, y);
         }
       }
-      if (t > 0) wait_pv(t - 1);
+      if (!pv_done) wait_pv(t - 1);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -556,8 +568,7 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       if (part && __any_sync(0xffffffffu, bad0 || bad1)) {
         // A non-finite key row that not every row of the group reads: 0 * inf
         // would spoil the others' O, so its values become zero and the weights
-        // of the rows that do read it NaN.  (Both halves' warps see such a row:
-        // it makes every score non-finite.)
+        // of the rows that do read it NaN.
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t m = static_cast<uint32_t>((h ? m1 : m0) >> c0);

@@ -180,6 +180,29 @@ def test_a_non_finite_row_reaches_only_the_nodes_that_read_it(value):
     check(d, out, lse, skip={(0, t) for t in readers})
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("heads", [1, 16, 64])
+def test_a_non_finite_query_row_spoils_only_itself(value, heads):
+    d = make([640], 8, heads, 64, 4, seed=15, lists="random")
+    d["q"][0, 2, heads // 2, 7] = value
+    d["q"][0, 5] = value
+    out, lse, st = call(d)
+    assert st == 0
+    assert not bool(torch.isfinite(out[0, 5]).any()) and not bool(torch.isfinite(out[0, 2, heads // 2]).any())
+    others = [h for h in range(heads) if h != heads // 2]
+    assert bool(torch.isfinite(out[0, 2, others]).all()) and bool(torch.isfinite(lse[0, 2, others]).all())
+    check(d, out, lse, skip={(0, 2), (0, 5)})
+    # beside a non-finite key row, which still reaches only its readers
+    d["kv"][int(d["slot"][0, 64 * 4 + 11]), 100] = value
+    out, lse, _ = call(d)
+    idx = d["idx"][0].cpu().numpy()
+    readers = [t for t in range(8) if 4 in idx[t]]
+    assert readers and len(readers) < 8
+    for t in readers:
+        assert not bool(torch.isfinite(out[0, t, :, 100]).any())
+    check(d, out, lse, skip={(0, t) for t in readers} | {(0, 2), (0, 5)})
+
+
 def test_a_non_finite_tree_row_reaches_only_its_descendants():
     d = make([300], 6, 16, 64, 3, seed=12)
     d["parent"] = torch.tensor([[-1, 0, 0, 1, 2, 3]], dtype=torch.int32, device="cuda")
