@@ -459,9 +459,6 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       tc_fence_after();
       float s[16];
       tmem_ld_16x32(tmem + lane_off + kBaColS + st * kBaRows + 32 * half, s);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.s_free[st]);
       // A key row that is not finite makes every score of it so, the zero rows' too;
       // a query row that is not spoils its own scores alone.
       bool bad0 = false, bad1 = false;
@@ -475,25 +472,25 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
         // (of this thread's rows; the others' are asked below)
         bad0 = !(a0 < CUDART_INF_F) && m0 != full && m0 != 0;
         bad1 = !(a1 < CUDART_INF_F) && m1 != full && m1 != 0;
+      }
+      auto mask = [&] {
+        if (!part) return;
         const uint32_t w0 = static_cast<uint32_t>(m0 >> c0), w1 = static_cast<uint32_t>(m1 >> c0);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            s[4 * i + e] = (w0 >> (8 * i + e)) & 1u ? s[4 * i + e] * p.scale_log2 : -CUDART_INF_F;
-            s[4 * i + 2 + e] = (w1 >> (8 * i + e)) & 1u ? s[4 * i + 2 + e] * p.scale_log2 : -CUDART_INF_F;
+            if (!((w0 >> (8 * i + e)) & 1u)) s[4 * i + e] = -CUDART_INF_F;
+            if (!((w1 >> (8 * i + e)) & 1u)) s[4 * i + 2 + e] = -CUDART_INF_F;
           }
-      } else {
+      };
+      // s becomes the distance to the row's running max, in log2 units; a score 2^8 above it raises it first
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] *= p.scale_log2;
-      }
-      // s is now in log2 units; a score 2^8 above its row's running max raises the max first
+      for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], p.scale_log2, -m[2 * (i >> 2) + (i & 1)]);
+      mask();
       float over = -CUDART_INF_F;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        over = fmax3(over, s[4 * i] - m[2 * i], s[4 * i + 1] - m[2 * i + 1]);
-        over = fmax3(over, s[4 * i + 2] - m[2 * i], s[4 * i + 3] - m[2 * i + 1]);
-      }
+      for (int i = 0; i < 8; ++i) over = fmax3(over, s[2 * i], s[2 * i + 1]);
       if (failed) sh.fail[st] = 1;
       const bool raise = bar_red_or(1, kBaSoftmax, failed || over > kBaThreshold || bad0 || bad1);
       if (raise && *const_cast<volatile int*>(&sh.fail[st])) {
@@ -506,6 +503,10 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
         uint8_t* bad = smem + kBaOffP + 4 * kBaRows * 4;  // [64 keys][8 threads that hold its scores]
         bad[r0 * 8 + half * 4 + (lane & 3)] = bad0;
         bad[(r0 + 8) * 8 + half * 4 + (lane & 3)] = bad1;
+        tmem_ld_16x32(tmem + lane_off + kBaColS + st * kBaRows + 32 * half, s);  // the scores again
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] *= p.scale_log2;
+        mask();
         float top8[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -531,6 +532,8 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
           l[i] *= alpha_sh[row];
           m[i] = mx[row];
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] -= m[2 * (i >> 2) + (i & 1)];
         if (t > 0) {
 #pragma unroll 1
           for (int k0 = 0; k0 < 16; ++k0) {  // this warp's half of the columns, 8 at a time
@@ -544,6 +547,9 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
         }
         bar_sync(1, kBaSoftmax);  // scratch is read before P is written over it
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_free[st]);
       // P^T, row (key) r of 64 columns, 128-byte swizzle
       uint8_t* pb = smem + kBaOffP;
       auto p_at = [&](int key, int i) {
@@ -554,7 +560,7 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float x = fast_exp2(s[4 * i + 2 * h] - m[2 * i]), y = fast_exp2(s[4 * i + 2 * h + 1] - m[2 * i + 1]);
+          const float x = fast_exp2(s[4 * i + 2 * h]), y = fast_exp2(s[4 * i + 2 * h + 1]);
           l[2 * i] += x;
           l[2 * i + 1] += y;
           pk[2 * i + h] = pack_bf16x2(x, y);
