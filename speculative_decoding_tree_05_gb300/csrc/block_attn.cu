@@ -34,10 +34,12 @@
 // only two of them fit beside the query rows, so a tile takes half a stage's life.
 // The nodes' ancestors and themselves are keys like the others, behind the blocks'
 // keys, each with the rows that see it.  One split writes bf16 and the log-sum-exp
-// at once; with more, a unit writes the normalised O and the log-sum-exp of its
-// share, and the merge kernel joins them.
+// at once; up to eight of a group of few rows are a cluster, whose CTAs join their
+// shares through distributed shared memory; else a unit writes the normalised O and the log-sum-exp of its share, and the
+// merge kernel joins them.
 #include <cuda_runtime.h>
 #include <math_constants.h>
+#include <atomic>
 #include <type_traits>
 #include "cache_ops.cuh"
 #include "ptx.cuh"
@@ -126,6 +128,8 @@ __device__ __forceinline__ Group group_of(const BlockAttnParams& p, int g) {
   return u;
 }
 
+// kClustered: the splits of a group are one cluster, which joins them.
+template <bool kClustered>
 __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_constant__ BlockAttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -193,7 +197,8 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
     const int32_t flags = __ldcg(p.list_flags + g);
     if (flags) atomicOr(p.status, flags);
   }
-  if (n == 0) {  // no key: a partial of weight zero
+  float* mx = reinterpret_cast<float*>(smem + kBaOffMax);
+  if (n == 0 && !kClustered) {  // no key: a partial of weight zero
     uint4* o = p.splits == 1 ? reinterpret_cast<uint4*>(p.out + prow0 * kDv) : reinterpret_cast<uint4*>(p.o_part + prow0 * kDv);
     const int each = p.splits == 1 ? kDv / 8 : kDv / 4;
     for (int i = tid; i < u.rows * each; i += kBaThreads) o[i] = make_uint4(0, 0, 0, 0);
@@ -203,7 +208,9 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
     return;
   }
 
-  if (warp == 0) {
+  if (n == 0) {
+    for (int i = tid; i < kBaRows; i += kBaThreads) mx[i] = -CUDART_INF_F;
+  } else if (warp == 0) {
     if (elect_one()) {
       // scores of all 64 columns (rows of zeros behind the group's): every column read out is defined
       const uint32_t idesc = idesc_bf16_f32(64, kBaRows, false, false);
@@ -418,7 +425,6 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
     const int r0 = quarter * 16 + (lane >> 2);     // keys r0 and r0 + 8 of the tile
     const int c0 = 32 * half + 2 * (lane & 3);     // rows c0 + 8 i + {0, 1}, i < 4
     const int id = half * 128 + quarter * 32 + lane;
-    float* mx = reinterpret_cast<float*>(smem + kBaOffMax);
     float* alpha_sh = reinterpret_cast<float*>(smem + kBaOffAlpha);
     float* scratch = reinterpret_cast<float*>(smem + kBaOffP);  // [4 quarters][64], while no P is in use
     const uint64_t* masks = reinterpret_cast<const uint64_t*>(smem + kBaOffMask);
@@ -608,13 +614,17 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       if (id < kBaRows) {
         const float sum = (scratch[id] + scratch[kBaRows + id]) + (scratch[2 * kBaRows + id] + scratch[3 * kBaRows + id]);
         alpha_sh[id] = sum != 0.f ? 1.f / sum : 0.f;
+        const float log2_sum = sum != 0.f ? mx[id] + log2f(sum) : -CUDART_INF_F;
         float* lse = p.splits == 1 ? p.lse : p.lse_part;
-        if (id < u.rows) lse[prow0 + id] = sum != 0.f ? (mx[id] + log2f(sum)) * kBaLn2 : -CUDART_INF_F;
+        if (kClustered)
+          mx[id] = log2_sum;
+        else if (id < u.rows)
+          lse[prow0 + id] = log2_sum * kBaLn2;
       }
     }
   }
   // the softmax and gather warps write O: quarter of the lanes by warp, four warps a quarter
-  if (warp > 0) {
+  if (n > 0 && warp > 0) {
     if (!bar_red_or(2, kBaThreads - 32, !ok) && warp != 9) {
       tc_fence_after();
       const float* inv_l = reinterpret_cast<const float*>(smem + kBaOffAlpha);
@@ -637,6 +647,10 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
             if (cc + k + (lane & 1) < u.rows)
               *reinterpret_cast<uint32_t*>(dst + k * kDv) = lane & 1 ? pack_bf16x2(got, y) : pack_bf16x2(x, got);
           }
+        } else if (kClustered) {  // the stages are free: rows of 512 fp32
+          float* dst = reinterpret_cast<float*>(smem) + cc * kDv + dim + lane;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k * kDv] = __uint_as_float(o[k]) * inv_l[cc + k];
         } else {
           float* dst = p.o_part + (prow0 + cc) * kDv + dim + lane;
 #pragma unroll
@@ -649,6 +663,46 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
   if (!ok) {
     *abort = 1;
     atomicOr(p.status, kStatusTimeout);
+  }
+  if (kClustered) {
+    // the group's splits are one cluster: each CTA joins a share of the rows from
+    // all of them, out = sum of w_s o_s / sum of w_s with w_s = 2^(log2_sum_s - max)
+    __syncwarp();
+    cluster_sync();
+    const int share = (u.rows + p.splits - 1) / p.splits, first = split * share, rows = min(share, u.rows - first);
+    const int64_t grow = static_cast<int64_t>(u.b) * p.pstride + u.row0 + first;
+    for (int i = tid; i < rows * (kDv / 4); i += kBaThreads) {
+      const int r = i / (kDv / 4), d = (i % (kDv / 4)) * 4;
+      const uint32_t from_lse = smem_u32(mx + first + r), from_o = base + ((first + r) * kDv + d) * 4;
+      float w[kBlockCluster], top = -CUDART_INF_F;
+#pragma unroll
+      for (int k = 0; k < kBlockCluster; ++k) {
+        w[k] = k < p.splits ? __int_as_float(ld_shared_cluster_b32(mapa_shared(from_lse, k))) : -CUDART_INF_F;
+        top = fmaxf(top, w[k]);
+      }
+      float4 o[kBlockCluster];
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kBlockCluster; ++k) {
+        // a NaN (a non-finite key that the row reads) stays one; a share without keys is not read
+        w[k] = w[k] == -CUDART_INF_F ? 0.f : fast_exp2(w[k] - top);
+        o[k] = w[k] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : ld_shared_cluster_f4(mapa_shared(from_o, k));
+        sum += w[k];
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kBlockCluster; ++k) {
+        acc.x = fmaf(w[k], o[k].x, acc.x);
+        acc.y = fmaf(w[k], o[k].y, acc.y);
+        acc.z = fmaf(w[k], o[k].z, acc.z);
+        acc.w = fmaf(w[k], o[k].w, acc.w);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      *reinterpret_cast<uint2*>(p.out + (grow + r) * kDv + d) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (d == 0) p.lse[grow + r] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kBaLn2;
+    }
+    cluster_sync();  // no CTA leaves while its rows are read
   }
   tc_fence_before();
   __syncthreads();
@@ -775,8 +829,44 @@ static_assert(kUnWarps == 32, "the prefix over warps takes one lane each");
 
 }  // namespace
 
+// The launch of `groups` groups in `splits` splits, a cluster each if `clustered`.
+struct BaLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  BaLaunch(int groups, int splits, bool clustered) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = attr[1].val.clusterDim.z = 1;
+    attr[1].val.clusterDim.y = splits;
+    cfg.gridDim = dim3(groups, splits);
+    cfg.blockDim = dim3(kBaThreads);
+    cfg.dynamicSmemBytes = kBaSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = clustered ? 2 : 1;
+  }
+};
+
+std::atomic<int> g_clusters[kBlockCluster + 1];  // of each size, that run at once
+
 cudaError_t configure_block_attn() {
-  return cudaFuncSetAttribute(block_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBaSmem);
+  cudaError_t e = cudaFuncSetAttribute(block_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBaSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(block_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBaSmem);
+  for (int s = 2; e == cudaSuccess && s <= kBlockCluster; ++s) {
+    int n = 0;
+    BaLaunch l(1, s, true);
+    e = cudaOccupancyMaxActiveClusters(&n, block_attn_kernel<true>, &l.cfg);
+    g_clusters[s] = n;
+  }
+  return e;
+}
+
+// A join through distributed shared memory reads at about 25 B/clk, so it suits few
+// rows (16 requests of 16 rows in a graph: 16.8 us, 18.3 with a merge kernel; of 64
+// rows 26.6 and 23.9); clusters that wait for others' SMs suit none.
+bool block_cluster_fits(int64_t groups, int rows, int splits) {
+  return rows <= kBlockRows / 2 && splits > 1 && splits <= kBlockCluster && groups <= g_clusters[splits];
 }
 
 cudaError_t launch_block_union(const BlockAttnParams& p, cudaStream_t stream) {
@@ -785,17 +875,9 @@ cudaError_t launch_block_union(const BlockAttnParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_block_attn(const BlockAttnParams& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(p.batch * p.groups, p.splits);
-  cfg.blockDim = dim3(kBaThreads);
-  cfg.dynamicSmemBytes = kBaSmem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block_attn_kernel, p);
+  BaLaunch l(p.batch * p.groups, p.splits, p.clustered);
+  l.cfg.stream = stream;
+  return cudaLaunchKernelEx(&l.cfg, p.clustered ? block_attn_kernel<true> : block_attn_kernel<false>, p);
 }
 
 }  // namespace ddt

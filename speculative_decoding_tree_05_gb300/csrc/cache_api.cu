@@ -19,7 +19,10 @@ constexpr int kWeightSumTiles = 3;  // the launch that adds the shares' sums, in
 // nine shapes: the weights' mean error is -7e-7 to -5e-7 without it, within 1e-7
 // with it.
 constexpr double kScoreLoss = 2.2e-7;
-constexpr int kBlockUnitTiles = 4;  // fixed cost of one block-attention unit, in 64-key tiles
+// Fixed costs in block attention, in 64-key tiles (1.7 us): of a unit, and of a merge
+// kernel behind it.  (8 requests of 17 nodes x 16 heads in a graph: 3 splits in one
+// wave 67 us, 7 splits in two waves 74 us.)
+constexpr int kBlockUnitTiles = 5, kBlockMergeTiles = 2;
 
 int round32(int x) { return (x + 31) / 32 * 32; }
 
@@ -111,13 +114,15 @@ int select_layout(const ddt_dims* d, int32_t block, SelectLayout* w) {
 
 struct BlocksLayout {
   int groups, group_nodes, splits;
+  bool clustered;
   int64_t list_cap;
   size_t len_off, tree_len_off, flags_off, list_off, tree_off, lse_off, o_off, bytes;
 };
 
 // Groups of up to 64 (node, head) rows, and the key splits of each.  The splits
-// minimise waves * (64-key tiles of a unit + kBlockUnitTiles), the tiles being
-// those of lists that do not overlap (how far they do is known on the device only).
+// minimise waves * (64-key tiles of a unit + kBlockUnitTiles), and kBlockMergeTiles
+// where a merge kernel follows; the tiles are those of lists that do not overlap (how
+// far they do is known on the device only).
 int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, BlocksLayout* w) {
   const int rc = check_cache_dims(d);
   if (rc != DDT_OK) return rc;
@@ -130,16 +135,19 @@ int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, 
   const int64_t blocks = (int64_t(d->max_prefix_len) + block - 1) / block;
   w->list_cap = std::min<int64_t>(int64_t(w->group_nodes) * topk, blocks);
   const int64_t tiles = (w->list_cap * block + std::min(T, 16) + 63) / 64;  // with a path of tree rows
+  const int group_rows = std::min(w->group_nodes * H, kBlockRows);
   int64_t best_cost = -1;
   w->splits = 1;
   for (int s = 1; s <= std::min<int64_t>(tiles, 32); ++s) {
-    const int64_t cost = (all * s + sm_count - 1) / sm_count * ((tiles + s - 1) / s + kBlockUnitTiles);
+    const int64_t cost = (all * s + sm_count - 1) / sm_count * ((tiles + s - 1) / s + kBlockUnitTiles) +
+                         (s == 1 || block_cluster_fits(all, group_rows, s) ? 0 : kBlockMergeTiles);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
       w->splits = s;
     }
   }
-  const size_t part = w->splits > 1 ? size_t(d->batch) * w->splits * T * H : 0;
+  w->clustered = block_cluster_fits(all, group_rows, w->splits);
+  const size_t part = w->splits > 1 && !w->clustered ? size_t(d->batch) * w->splits * T * H : 0;
   w->len_off = kStatusBytes;
   w->tree_len_off = align_up(w->len_off + all * sizeof(int32_t), 256);
   w->flags_off = align_up(w->tree_len_off + all * sizeof(int32_t), 256);
@@ -439,6 +447,7 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
   p.groups = w.groups;
   p.group_nodes = w.group_nodes;
   p.splits = w.splits;
+  p.clustered = w.clustered;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.o_part = reinterpret_cast<float*>(ws + w.o_off);
   p.lse_part = reinterpret_cast<float*>(ws + w.lse_off);
@@ -456,7 +465,7 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // (the union kernel clears the status word)
   if (launch_block_union(p, s) != cudaSuccess || launch_block_attn(p, s) != cudaSuccess ||
-      (w.splits > 1 && launch_block_merge(m, p.batch, s) != cudaSuccess))
+      (w.splits > 1 && !p.clustered && launch_block_merge(m, p.batch, s) != cudaSuccess))
     return DDT_ERR_LAUNCH;
   return DDT_OK;
 }

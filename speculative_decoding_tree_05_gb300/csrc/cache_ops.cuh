@@ -149,14 +149,18 @@ struct BlockAttnParams {
   int32_t groups;             // per request
   int32_t group_nodes;        // nodes of a group (heads <= 64; else a group is 64 heads of one node)
   int32_t splits;
+  bool clustered;             // the splits of a group are one cluster, which joins them
   float scale_log2;
-  float* o_part;              // fp32 [B, splits, pstride, 512], normalised (splits > 1)
+  float* o_part;              // fp32 [B, splits, pstride, 512], normalised (splits > 1, not clustered)
   float* lse_part;            // fp32 [B, splits, pstride], natural log
-  uint16_t* out;              // bf16 [B, T, H, 512] (splits == 1)
+  uint16_t* out;              // bf16 [B, T, H, 512]
   float* lse;                 // fp32 [B, T, H]
   int32_t* status;
 };
+constexpr int kBlockCluster = 8;
 cudaError_t configure_block_attn();
+// Whether groups of `rows` rows in `splits` splits are clusters: they all run at once, and the join is short.
+bool block_cluster_fits(int64_t groups, int rows, int splits);
 cudaError_t launch_block_union(const BlockAttnParams& p, cudaStream_t stream);
 cudaError_t launch_block_attn(const BlockAttnParams& p, cudaStream_t stream);
 

@@ -176,6 +176,14 @@ __device__ __forceinline__ int ld_shared_cluster_b32(uint32_t remote_addr) {
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(remote_addr) : "memory");
   return v;
 }
+__device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t remote_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(remote_addr)
+               : "memory");
+  return v;
+}
 
 // Add to a word of a peer CTA's shared memory (visible to the peer after a cluster barrier).
 __device__ __forceinline__ void red_shared_cluster_add(uint32_t remote_addr, int v) {

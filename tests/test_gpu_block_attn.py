@@ -114,6 +114,22 @@ def test_against_fp64(lens, nodes, heads, block, topk):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("heads", [1, 16, 32, 33, 64])
+@pytest.mark.parametrize("batch,topk,block", [(4, 60, 16), (16, 40, 32), (30, 9, 64), (3, 6, 128)])
+def test_splits_with_and_without_keys(batch, topk, block, heads):
+    """Requests of very different lengths share one choice of key splits: some splits hold no key."""
+    lens = [[2600, 0, 40, 1, 63, 1500][b % 6] for b in range(batch)]
+    d = make(lens, 1, heads, block, topk, seed=heads + topk, lists="all")
+    out, lse, st = call(d)
+    assert st == 0
+    check(d, out, lse)
+    d["kv"][int(d["slot"][0, 2500])] = float("nan")    # in one split of one request
+    out2, lse2, _ = call(d)
+    reads = 2500 // block in d["idx"][0, 0].tolist()
+    assert bool(torch.isnan(out2[0]).all()) == reads and bool(torch.isnan(lse2[0]).all()) == reads
+    assert torch.equal(out2[1:], out[1:]) and torch.equal(lse2[1:], lse[1:])
+
+
 @pytest.mark.parametrize("amp", [4.0, 16.0])
 def test_large_scores_raise_the_running_max(amp):
     d = make([3000], 9, 16, 64, 20, seed=5, amp=amp)
