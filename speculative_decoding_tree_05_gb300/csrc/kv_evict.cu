@@ -4,7 +4,7 @@
 // the last `recent` rank before all others, then the larger weight, then the
 // lower position; what is kept stays in order.  One cluster of CTAs per request,
 // CTA r holding the r-th share of the positions:
-//   1. three digit histograms of the unprotected positions' weights give the
+//   1. two or three digit histograms of the unprotected positions' weights give the
 //      weight of the last position kept (T) and how many of the positions tied at
 //      T are kept.  Each CTA adds the bins that it filled to the totals of their
 //      owner (a share of the bins each) through distributed shared memory and
