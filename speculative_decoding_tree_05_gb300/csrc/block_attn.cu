@@ -827,8 +827,6 @@ __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_co
 }
 static_assert(kUnWarps == 32, "the prefix over warps takes one lane each");
 
-}  // namespace
-
 // The launch of `groups` groups in `splits` splits, a cluster each if `clustered`.
 struct BaLaunch {
   cudaLaunchConfig_t cfg = {};
@@ -849,17 +847,23 @@ struct BaLaunch {
 
 std::atomic<int> g_clusters[kBlockCluster + 1];  // of each size, that run at once
 
+}  // namespace
+
 cudaError_t configure_block_attn() {
   cudaError_t e = cudaFuncSetAttribute(block_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBaSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(block_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBaSmem);
-  for (int s = 2; e == cudaSuccess && s <= kBlockCluster; ++s) {
+  if (e != cudaSuccess) return e;
+  for (int s = 2; s <= kBlockCluster; ++s) {
     int n = 0;
     BaLaunch l(1, s, true);
-    e = cudaOccupancyMaxActiveClusters(&n, block_attn_kernel<true>, &l.cfg);
+    if (cudaOccupancyMaxActiveClusters(&n, block_attn_kernel<true>, &l.cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;  // a merge kernel does it
+    }
     g_clusters[s] = n;
   }
-  return e;
+  return cudaSuccess;
 }
 
 // A join through distributed shared memory reads at about 25 B/clk, so it suits few
