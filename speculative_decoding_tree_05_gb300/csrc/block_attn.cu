@@ -717,6 +717,14 @@ constexpr int kUnThreads = 1024;
 constexpr int kUnWarps = kUnThreads / 32;
 constexpr int kUnBlocks = 4096;
 
+// a |= m in shared memory, by halves (32-bit atomics need no loop)
+__device__ __forceinline__ void or_mask(unsigned long long* a, unsigned long long m) {
+  unsigned* half = reinterpret_cast<unsigned*>(a);
+  const unsigned lo = static_cast<unsigned>(m), hi = static_cast<unsigned>(m >> 32);
+  if (lo) atomicOr(half, lo);
+  if (hi) atomicOr(half + 1, hi);
+}
+
 __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_constant__ BlockAttnParams p) {
   __shared__ unsigned long long mask_sh[kUnBlocks];
   __shared__ unsigned long long tree_sh[kMaxNodes];
@@ -732,6 +740,10 @@ __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_co
     if (g == 0) *p.status = 0;
   }
   const Group u = group_of(p, g);
+  const int t_first = u.row0 / p.heads, t_last = (u.row0 + u.rows - 1) / p.heads;
+  const int32_t* lists = p.block_idx + (static_cast<int64_t>(u.b) * p.nodes + t_first) * p.topk;
+  const int entries = (t_last - t_first + 1) * p.topk;  // at most 64 lists of 2^20
+  const int entry0 = tid < entries ? __ldg(lists + tid) : -1;  // on its way while the rest is set up
   if (tid < p.nodes) {
     par_sh[tid] = __ldg(p.tree_parent + static_cast<int64_t>(u.b) * p.nodes + tid);
     slot_sh[tid] = __ldg(p.tree_slot_idx + static_cast<int64_t>(u.b) * p.nodes + tid);
@@ -744,18 +756,18 @@ __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_co
   __syncthreads();
   grid_dep_launch();
   const int n_blocks = (L + p.block - 1) / p.block;
-  const int t_first = u.row0 / p.heads, t_last = (u.row0 + u.rows - 1) / p.heads;
   auto rows_of = [&](int t) -> unsigned long long {  // of the group's t-th node: its rows [t H, t H + H)
     const int lo = t * p.heads, hi = min(u.rows, lo + p.heads);
     return (hi == 64 ? ~0ull : ((1ull << hi) - 1)) & ~((1ull << lo) - 1);
   };
-  if (tid <= t_last - t_first) {
+  const int walker = kUnThreads - 1 - tid;  // the last warps walk while the first mark the lists
+  if (walker <= t_last - t_first) {
     // a node's walk to the root: a link that is no earlier node ends it, a slot outside the pool is left out
-    int v = t_first + tid, flags = tid == 0 ? bad_len : 0;
+    int v = t_first + walker, flags = walker == 0 ? bad_len : 0;
     for (int guard = 0; v >= 0 && guard < p.nodes; ++guard) {
       const int slot = slot_sh[v], up = par_sh[v];
       if (slot >= 0 && slot < p.pool_slots)
-        atomicOr(&tree_sh[v], rows_of(tid));
+        or_mask(&tree_sh[v], rows_of(walker));
       else
         flags |= kStatusBadSlot;
       if (v == 0 ? up != -1 : (up < 0 || up >= v)) {
@@ -766,8 +778,6 @@ __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_co
     }
     if (flags) atomicOr(&flags_sh, flags);
   }
-  const int32_t* lists = p.block_idx + (static_cast<int64_t>(u.b) * p.nodes + t_first) * p.topk;
-  const int entries = (t_last - t_first + 1) * p.topk;  // at most 64 lists of 2^20
   BlockEntry* out = p.list + static_cast<int64_t>(g) * p.list_cap;
   int base = 0;
   for (int c0 = 0; c0 < n_blocks || c0 == 0; c0 += kUnBlocks) {
@@ -776,12 +786,12 @@ __global__ void __launch_bounds__(kUnThreads) block_union_kernel(const __grid_co
       __syncthreads();
     }
     for (int i = tid; i < entries; i += kUnThreads) {
-      const int x = __ldg(lists + i);
+      const int x = i == tid ? entry0 : __ldg(lists + i);
       if (x < 0 || x >= n_blocks) {
         if (x != -1 && c0 == 0) atomicOr(&flags_sh, kStatusBadBlock);
         continue;
       }
-      if (x >= c0 && x - c0 < kUnBlocks) atomicOr(&mask_sh[x - c0], rows_of(i / p.topk));
+      if (x >= c0 && x - c0 < kUnBlocks) or_mask(&mask_sh[x - c0], rows_of(i / p.topk));
     }
     __syncthreads();
     const int here = min(kUnBlocks, n_blocks - c0);
