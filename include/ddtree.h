@@ -412,9 +412,9 @@ DDT_API int ddtree_block_select(const void* q, const void* summary, const float*
  *   lse        fp32 [B, T, H]
  * The other arguments are ddtree_verify_attn's, and with every block listed it
  * computes the same.  Nodes are processed in groups of up to 64 (node, head)
- * rows over the union of their lists; the softmax weights are rounded to bf16,
- * scores and sums are fp32.  A non-finite key row reaches only the nodes that
- * list its block.  Results are the same bits on every run.
+ * rows over the union of their lists; scores and sums are fp32, softmax weights
+ * keep 16 bits, and out is rounded to bf16 once.  A non-finite key row reaches
+ * only the nodes that list its block.  Results are the same bits on every run.
  * workspace >= ddtree_verify_blocks_workspace_bytes(dims, block, topk), which
  * needs a current CUDA device.
  */

@@ -11,12 +11,15 @@
 // With 64 rows the usual roles waste the tensor core's 128 lanes on O (rows as
 // M), so they are swapped: keys and value dims are the M side, rows the N side.
 //   S^T[64 keys][rows]  = K . Q^T          36 MMAs M64 x N x K16
-//   O^T[512 dims][rows] += V^T . P^T       4 x 4 MMAs M128 x N x K16 (V^T: the same
-//                                          latent blocks read MN-major)
+//   O^T[512 dims][rows] += V^T . P^T       2 x 4 x 4 MMAs M128 x N x K16 (V^T: the
+//                                          same latent blocks read MN-major)
 // O^T takes 256 TMEM columns, so one CTA holds the whole output and nothing is
-// exchanged between SMs; scores and sums stay fp32.  P is rounded to bf16, the
-// operand type, against row sums of the unrounded values: an error of half a
-// bf16 step per weight, averaged over the keys, below the bf16 rounding of out.
+// exchanged between SMs; scores and sums stay fp32.  P is the sum of two bf16
+// parts, what the first leaves of the weight in the second: 16 bits of it count
+// and the only rounding to 8 is that of out.  With one part out was off by
+// 2.05e-3 of its norm beside the 1.65e-3 of its own rounding; the second costs 13 to
+// 18 % (8 requests of 33 nodes x 16 heads: 92.7 -> 105.9 us; both parts as the 128
+// columns of one MMA, where TMEM has room for that, 105.8).
 //
 // Per CTA (576 threads), one unit = (group, split of its key tiles):
 //   warp 0       TMEM; one lane issues S(t), dim group by dim group as stage t lands
@@ -26,10 +29,12 @@
 //   warp 9       one lane issues P.V(t) when P(t) is written
 //   warps 10-17  gather 64 keys per stage, two stages of four dim groups, each
 //                refilled as soon as its part of P.V is done: warps 10-13 the latent
-//                chunks of the first two groups (4 of 9) by 16-byte cp.async, warps
-//                14-17 the others by TMA gather4 (85 cycles an instruction and warp), at the
-//                same time: an SM gathers about 24 B/clk either way and 34 both
-//                ways (L2-resident rows)
+//                chunks of the first two groups (4 of 9) and the rope chunk by
+//                16-byte cp.async, warps 14-17 the other groups by TMA gather4 (85
+//                cycles an instruction and warp), at the same time: an SM gathers
+//                about 24 B/clk either way and 34 both ways (L2-resident rows).  The
+//                rope chunk comes last: P's second part lies there from the softmax to
+//                the end of P.V
 // What bounds it: a stage lives from its load through S, the softmax and P.V, and
 // only two of them fit beside the query rows, so a tile takes half a stage's life.
 // The nodes' ancestors and themselves are keys like the others, behind the blocks'
@@ -51,14 +56,15 @@ constexpr int kBaThreads = 576;
 constexpr int kBaSoftmax = 256;
 constexpr int kBaCopiers = 128;                 // threads that gather the copied groups
 constexpr int kBaCopied = 2;                    // groups gathered by cp.async
-constexpr int kBaGroups = 4;                    // dims {512-575, 0-127}, {128-255}, {256-383}, {384-511}
+constexpr int kBaGroups = 4;                    // dims {0-127}, {128-255}, {256-383}, {384-575}
 constexpr int kBaKeys = 64;
 constexpr int kBaRows = kBlockRows;             // 64
 constexpr int kBaStages = 2;
 constexpr int kBaChunk = kBaKeys * 128;         // 64 dims of 64 keys: 8 KB
 constexpr int kBaStageBytes = 9 * kBaChunk;     // 73728
 constexpr int kBaOffQ = kBaStages * kBaStageBytes;
-constexpr int kBaOffP = kBaOffQ + 9 * kBaChunk;
+constexpr int kBaOffP = kBaOffQ + 9 * kBaChunk;                 // P's first part
+constexpr int kBaOffLow = 8 * kBaChunk;                         // its second one: the rope chunk of the tile's stage, read by then
 constexpr int kBaOffMask = kBaOffP + kBaChunk;                  // [2][64] row masks of the stage's keys
 constexpr int kBaOffMax = kBaOffMask + kBaStages * kBaKeys * 8; // [64] running max
 constexpr int kBaOffAlpha = kBaOffMax + kBaRows * 4;            // [64] rescale factors, later row sums
@@ -147,9 +153,10 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
   if (tid == 0) {
     for (int i = 0; i < kBaStages; ++i)
       for (int x = 0; x < kBaGroups; ++x) {
-        // every thread's cp.async (group 0: and each warp's key masks), or two warps' arrivals with their bytes
-        // (group 0 also: the four gather warps' arrivals with the rope chunk)
-        mbar_init(&sh.k_full[i][x], x == 0 ? kBaCopiers + 4 + 4 : (x < kBaCopied ? kBaCopiers : 2));
+        // every copying thread's cp.async (group 0: and each of its warps' key masks), or two gather warps' arrivals
+        // with their bytes (the last group: both)
+        mbar_init(&sh.k_full[i][x], (x < kBaCopied || x == kBaGroups - 1 ? kBaCopiers : 0) + (x == 0 ? 4 : 0) +
+                                        (x < kBaCopied ? 0 : 2));
         mbar_init(&sh.k_empty[i][x], 1);
       }
     for (int i = 0; i < 2; ++i) {
@@ -230,18 +237,17 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
             ok = false;
             break;
           }
-          if (x < kBaCopied) fence_proxy_async_smem();  // written by cp.async
+          if (x < kBaCopied || x == kBaGroups - 1) fence_proxy_async_smem();  // written by cp.async
           tc_fence_after();
-          if (x == 0) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)  // the rope dims
-              mma_ss(d, desc_advance(k, 8 * kBaChunk + ks * 32), desc_advance(d_q, 8 * kBaChunk + ks * 32), idesc,
-                     ks > 0 ? 1u : 0u);
-          }
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
             mma_ss(d, desc_advance(k, (2 * x + (ks >> 2)) * kBaChunk + (ks & 3) * 32),
-                   desc_advance(d_q, (2 * x + (ks >> 2)) * kBaChunk + (ks & 3) * 32), idesc, 1u);
+                   desc_advance(d_q, (2 * x + (ks >> 2)) * kBaChunk + (ks & 3) * 32), idesc, x + ks > 0 ? 1u : 0u);
+          if (x == kBaGroups - 1) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)  // the rope dims
+              mma_ss(d, desc_advance(k, 8 * kBaChunk + ks * 32), desc_advance(d_q, 8 * kBaChunk + ks * 32), idesc, 1u);
+          }
         }
         if (ok) mma_commit(&sh.s_full[st]);
       }
@@ -253,6 +259,7 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       const uint32_t idesc = idesc_bf16_f32(128, (u.rows + 15) / 16 * 16, true, true);
       const uint64_t d_v = smem_desc(base, kBaChunk, 1024, kSwizzle128B);            // MN-major
       const uint64_t d_p = smem_desc(base + kBaOffP, kBaChunk, 1024, kSwizzle128B);  // MN-major
+      const uint64_t d_low = smem_desc(base + kBaOffLow, kBaChunk, 1024, kSwizzle128B);
       for (int t = 0; t < n; ++t) {
         if (!mbar_wait_abortable(&sh.p_ready, t & 1, abort, false, __LINE__)) {
           ok = false;
@@ -260,14 +267,16 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
         }
         fence_proxy_async_smem();
         tc_fence_after();
-        const uint64_t v = desc_advance(d_v, (t & 1) * kBaStageBytes);
+        const uint64_t v = desc_advance(d_v, (t & 1) * kBaStageBytes), low = desc_advance(d_low, (t & 1) * kBaStageBytes);
         const uint32_t more = t > 0 ? 1u : 0u;
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ss(tmem + mt * kBaRows, desc_advance(v, mt * 2 * kBaChunk + ks * 2048), desc_advance(d_p, ks * 2048),
-                   idesc, ks > 0 ? 1u : more);
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t a = desc_advance(v, mt * 2 * kBaChunk + ks * 2048);
+            mma_ss(tmem + mt * kBaRows, a, desc_advance(d_p, ks * 2048), idesc, ks > 0 ? 1u : more);
+            mma_ss(tmem + mt * kBaRows, a, desc_advance(low, ks * 2048), idesc, 1u);
+          }
           mma_commit(&sh.k_empty[t & 1][mt]);
         }
       }
@@ -364,29 +373,14 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
         }
         copy_rows(sbase, row0, 2, P16(), P16(), slot);
         cp_async_arrive_noinc(&sh.k_full[st][1]);
-      } else {
-        // the rope chunk of 16 of the warp's keys, with group 0
-        const int rope0 = 16 * (gx - kBaCopied);
-        if (!wait_empty(t, 0)) {
+        // the rope chunk, with the last group: P's second part lies there until P.V is done
+        if (!wait_empty(t, kBaGroups - 1)) {
           ok = false;
           break;
         }
-        if (__all_sync(0xffffffffu, slot >= 0 || lane < rope0 || lane >= rope0 + 16)) {
-          if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[st][0], 16 * 128);
-          __syncwarp();
-          const int q = rope0 + 4 * (lane & 3);
-          const int ra = __shfl_sync(0xffffffffu, slot, q), rb = __shfl_sync(0xffffffffu, slot, q + 1);
-          const int rc = __shfl_sync(0xffffffffu, slot, q + 2), rd = __shfl_sync(0xffffffffu, slot, q + 3);
-          if (lane < 4)
-            tma_gather4(sbase + 8 * kBaChunk + (row0 + q) * 128, &p.tmap_kv, 512, ra, rb, rc, rd, &sh.k_full[st][0]);
-        } else {
-          copy_rows(sbase, row0 + rope0, 8, P8(), P16(), __shfl_sync(0xffffffffu, slot, (lane + rope0) & 31));
-          cp_async_commit();
-          cp_async_wait<0>();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.k_full[st][0]);
-        }
+        copy_rows(sbase, row0, 8, P8(), P16(), slot);
+        cp_async_arrive_noinc(&sh.k_full[st][kBaGroups - 1]);
+      } else {
         if (!wait_empty(t, gx)) {
           ok = false;
           break;
@@ -414,10 +408,7 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
     }
     cp_async_wait<0>();
     if (!ok && !copier)  // after a give-up the gathers still in flight land before the CTA exits
-      for (int v = max(0, done - 2); v <= done && v < n; ++v) {
-        mbar_wait(&sh.k_full[v & 1][0], (v >> 1) & 1, 1u << 16);
-        mbar_wait(&sh.k_full[v & 1][gx], (v >> 1) & 1, 1u << 16);
-      }
+      for (int v = max(0, done - 2); v <= done && v < n; ++v) mbar_wait(&sh.k_full[v & 1][gx], (v >> 1) & 1, 1u << 16);
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
     const int quarter = warp & 3, half = (warp - 1) >> 2;
@@ -558,8 +549,9 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       if (lane == 0) mbar_arrive(&sh.s_free[st]);
       // P^T, row (key) r of 64 columns, 128-byte swizzle
       uint8_t* pb = smem + kBaOffP;
-      auto p_at = [&](int key, int i) {
-        return reinterpret_cast<uint32_t*>(pb + key * 128 + (((4 * half + i) ^ (key & 7)) << 4) + (lane & 3) * 4);
+      uint8_t* low = smem + st * kBaStageBytes + kBaOffLow;
+      auto p_at = [&](uint8_t* part, int key, int i) {
+        return reinterpret_cast<uint32_t*>(part + key * 128 + (((4 * half + i) ^ (key & 7)) << 4) + (lane & 3) * 4);
       };
       uint32_t pk[8];
 #pragma unroll
@@ -569,14 +561,17 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
           const float x = fast_exp2(s[4 * i + 2 * h]), y = fast_exp2(s[4 * i + 2 * h + 1]);
           l[2 * i] += x;
           l[2 * i + 1] += y;
-          pk[2 * i + h] = pack_bf16x2(x, y);
+          const uint32_t hi = pack_bf16x2(x, y);
+          pk[2 * i + h] = hi;
+          // (the differences are exact)
+          *p_at(low, r0 + 8 * h, i) = pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
         }
       }
       if (!pv_done) wait_pv(t - 1);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) *p_at(r0 + 8 * h, i) = pk[2 * i + h];
+        for (int h = 0; h < 2; ++h) *p_at(pb, r0 + 8 * h, i) = pk[2 * i + h];
       if (part && __any_sync(0xffffffffu, bad0 || bad1)) {
         // A non-finite key row that not every row of the group reads: 0 * inf
         // would spoil the others' O, so its values become zero and the weights
@@ -592,7 +587,7 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t lo = (m >> (8 * i)) & 1 ? 0x7fc0u : 0u, hi = (m >> (8 * i + 1)) & 1 ? 0x7fc0u : 0u;
-              *p_at(key, i) = lo | (hi << 16);
+              *p_at(pb, key, i) = lo | (hi << 16);
               if (lo) l[2 * i] = CUDART_NAN_F;
               if (hi) l[2 * i + 1] = CUDART_NAN_F;
             }
