@@ -319,6 +319,20 @@ def _keep(stream, *tensors):
             t.record_stream(stream)
 
 
+def _make(stream, fn, *args, **kw):
+    """A tensor that a call makes for itself: allocated, and filled, on the stream that the call runs on.
+
+    On the current stream its fill could run after the kernels on `stream`, and its memory could still be in use there.
+    """
+    import torch
+    if stream is None:
+        return fn(*args, **kw)
+    with torch.cuda.stream(stream):
+        t = fn(*args, **kw)
+    t.record_stream(torch.cuda.current_stream(t.device))   # where the caller is likely to use it
+    return t
+
+
 class KeyWeights:
     """Accumulated attention weight of every prefix key (ddtree_kv_weight), with a workspace for one set of sizes.
 
@@ -352,7 +366,7 @@ class KeyWeights:
         if weight is None:
             decay = 0.0
         if out is None:
-            out = torch.zeros(table, dtype=torch.float32, device=self.device)
+            out = _make(stream, torch.zeros, table, dtype=torch.float32, device=self.device)
         B, T, H = d.batch, d.num_nodes, d.num_heads
         _need(self.device, ("q", q, torch.bfloat16, (B, T, H, D_QK)),
               ("kv_pool", kv_pool, torch.bfloat16, (d.pool_slots, D_QK)), ("slot_idx", slot_idx, torch.int32, table),
@@ -390,11 +404,12 @@ def kv_evict(weight, slot_idx, prefix_len, keep_len, sink=0, recent=0, slot_idx_
     if weight.dim() != 2:
         raise ValueError("weight must be [batch, slot_stride]")
     B, stride = weight.shape
-    slot_idx_out = torch.zeros_like(slot_idx) if slot_idx_out is None else slot_idx_out
-    weight_out = torch.zeros_like(weight) if weight_out is None else weight_out
-    prefix_len_out = torch.empty_like(prefix_len) if prefix_len_out is None else prefix_len_out
-    freed = torch.zeros_like(slot_idx) if freed is None else freed
-    workspace = torch.empty(256, dtype=torch.uint8, device=device) if workspace is None else workspace
+    slot_idx_out = _make(stream, torch.zeros_like, slot_idx) if slot_idx_out is None else slot_idx_out
+    weight_out = _make(stream, torch.zeros_like, weight) if weight_out is None else weight_out
+    prefix_len_out = _make(stream, torch.empty_like, prefix_len) if prefix_len_out is None else prefix_len_out
+    freed = _make(stream, torch.zeros_like, slot_idx) if freed is None else freed
+    if workspace is None:
+        workspace = _make(stream, torch.empty, 256, dtype=torch.uint8, device=device)
     table, lens = (B, stride), (B,)
     _need(device, ("weight", weight, torch.float32, table), ("slot_idx", slot_idx, torch.int32, table),
           ("prefix_len", prefix_len, torch.int32, lens), ("keep_len", keep_len, torch.int32, lens),
@@ -429,9 +444,12 @@ def block_summary(kv_pool, slot_idx, prefix_len, block, from_len=None, summary=N
     n = -(-dims.max_prefix_len // int(block)) if block > 0 else 0
     if from_len is not None and (summary is None or scale is None):
         raise ValueError("from_len updates the summary and scale of an earlier call: pass both")
-    summary = torch.zeros((B, n, D_QK), dtype=torch.bfloat16, device=device) if summary is None else summary
-    scale = torch.zeros((B, n), dtype=torch.float32, device=device) if scale is None else scale
-    workspace = torch.empty(256, dtype=torch.uint8, device=device) if workspace is None else workspace
+    if summary is None:
+        summary = _make(stream, torch.zeros, (B, n, D_QK), dtype=torch.bfloat16, device=device)
+    if scale is None:
+        scale = _make(stream, torch.zeros, (B, n), dtype=torch.float32, device=device)
+    if workspace is None:
+        workspace = _make(stream, torch.empty, 256, dtype=torch.uint8, device=device)
     _need(device, ("kv_pool", kv_pool, torch.bfloat16, (dims.pool_slots, D_QK)),
           ("slot_idx", slot_idx, torch.int32, (B, stride)), ("prefix_len", prefix_len, torch.int32, (B,)),
           ("summary", summary, torch.bfloat16, (B, n, D_QK)), ("scale", scale, torch.float32, (B, n)),
@@ -471,7 +489,7 @@ class BlockSelector:
         import torch
         d = self.dims
         if out is None:
-            out = torch.empty((d.batch, d.num_nodes, self.topk), dtype=torch.int32, device=self.device)
+            out = _make(stream, torch.empty, (d.batch, d.num_nodes, self.topk), dtype=torch.int32, device=self.device)
         _need(self.device, ("q", q, torch.bfloat16, (d.batch, d.num_nodes, d.num_heads, D_QK)),
               ("summary", summary, torch.bfloat16, (d.batch, self.blocks, D_QK)),
               ("scale", scale, torch.float32, (d.batch, self.blocks)),
@@ -515,9 +533,9 @@ class BlockVerifier:
         d = self.dims
         B, T, H = d.batch, d.num_nodes, d.num_heads
         if out is None:
-            out = torch.empty((B, T, H, D_V), dtype=torch.bfloat16, device=self.device)
+            out = _make(stream, torch.empty, (B, T, H, D_V), dtype=torch.bfloat16, device=self.device)
         if lse is None:
-            lse = torch.empty((B, T, H), dtype=torch.float32, device=self.device)
+            lse = _make(stream, torch.empty, (B, T, H), dtype=torch.float32, device=self.device)
         _need(self.device, ("q", q, torch.bfloat16, (B, T, H, D_QK)),
               ("kv_pool", kv_pool, torch.bfloat16, (d.pool_slots, D_QK)),
               ("slot_idx", slot_idx, torch.int32, (B, d.slot_stride)), ("prefix_len", prefix_len, torch.int32, (B,)),
