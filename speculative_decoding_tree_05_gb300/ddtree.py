@@ -166,6 +166,27 @@ def _check(rc, what):
         raise DDTError(rc, what)
 
 
+def _keep(stream, *tensors):
+    """Tell the allocator that `stream` uses tensors which may have been allocated for the current one."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _make(stream, fn, *args, **kw):
+    """A tensor that a call makes for itself: allocated, and filled, on the stream that the call runs on.
+
+    On the current stream its fill could run after the kernels on `stream`, and its memory could still be in use there.
+    """
+    import torch
+    if stream is None:
+        return fn(*args, **kw)
+    with torch.cuda.stream(stream):
+        t = fn(*args, **kw)
+    t.record_stream(torch.cuda.current_stream(t.device))   # where the caller is likely to use it
+    return t
+
+
 class Verifier:
     """Holds a workspace sized for one set of dims and runs verify calls with it.
 
@@ -197,9 +218,9 @@ class Verifier:
         import torch
         B, T, H, D = q.shape
         if out is None:
-            out = torch.empty((B, T, H, D_V), dtype=torch.float32, device=q.device)
+            out = _make(stream, torch.empty, (B, T, H, D_V), dtype=torch.float32, device=q.device)
         if lse is None:
-            lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
+            lse = _make(stream, torch.empty, (B, T, H), dtype=torch.float32, device=q.device)
         if tree_len is not None:
             if phase != "all":
                 raise ValueError("ragged trees run as one call (phase='all')")
@@ -208,6 +229,7 @@ class Verifier:
                                                  float(sm_scale), _ptr(out), _ptr(lse), ctypes.byref(self.dims),
                                                  _ptr(self.workspace), self.workspace.numel(), _stream(stream))
             _check(rc, "ddtree_verify_attn_ragged")
+            _keep(stream, out, lse, self.workspace)
             return out, lse
         fn = {"all": "ddtree_verify_attn", "fused": "ddtree_verify_attn_fused", "prefix": "ddtree_verify_prefix_phase",
               "merge": "ddtree_verify_merge_phase"}[phase]
@@ -216,6 +238,7 @@ class Verifier:
                                 ctypes.byref(self.dims), _ptr(self.workspace), self.workspace.numel(),
                                 _stream(stream))
         _check(rc, fn)
+        _keep(stream, out, lse, self.workspace)
         return out, lse
 
     def status(self, stream=None) -> int:
@@ -225,8 +248,10 @@ class Verifier:
 def verify_attn(q, kv_pool, slot_idx, prefix_len, tree_parent, tree_slot_idx, sm_scale, max_prefix_len=None,
                 out=None, lse=None, stream=None):
     """One-off verify call (allocates its own workspace); returns (out, lse)."""
+    import torch
     B, T, H, _ = q.shape
-    v = Verifier(B, T, H, kv_pool.shape[0], slot_idx.shape[1], max_prefix_len, device=q.device)
+    with torch.cuda.stream(stream):   # (None: the current one) the workspace is that stream's too
+        v = Verifier(B, T, H, kv_pool.shape[0], slot_idx.shape[1], max_prefix_len, device=q.device)
     return v(q, kv_pool, slot_idx, prefix_len, tree_parent, tree_slot_idx, sm_scale, out, lse, stream)
 
 
@@ -252,13 +277,14 @@ class SparseVerifier:
         import torch
         B, T, H, _ = q.shape
         if out is None:
-            out = torch.empty((B, T, H, D_V), dtype=torch.float32, device=q.device)
+            out = _make(stream, torch.empty, (B, T, H, D_V), dtype=torch.float32, device=q.device)
         if lse is None:
-            lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
+            lse = _make(stream, torch.empty, (B, T, H), dtype=torch.float32, device=q.device)
         rc = self.lib.ddtree_verify_attn_sparse(_ptr(q), _ptr(kv_pool), _ptr(indices), float(sm_scale), _ptr(out),
                                                 _ptr(lse), ctypes.byref(self.dims), _ptr(self.workspace),
                                                 self.workspace.numel(), _stream(stream))
         _check(rc, "ddtree_verify_attn_sparse")
+        _keep(stream, out, lse, self.workspace)
         return out, lse
 
     def status(self, stream=None) -> int:
@@ -310,27 +336,6 @@ def _stream_of(device, stream):
     import torch
     # the raw handle: building a Stream object costs as much as a launch
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-
-
-def _keep(stream, *tensors):
-    """Tell the allocator that `stream` uses tensors which may have been allocated for the current one."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
-
-
-def _make(stream, fn, *args, **kw):
-    """A tensor that a call makes for itself: allocated, and filled, on the stream that the call runs on.
-
-    On the current stream its fill could run after the kernels on `stream`, and its memory could still be in use there.
-    """
-    import torch
-    if stream is None:
-        return fn(*args, **kw)
-    with torch.cuda.stream(stream):
-        t = fn(*args, **kw)
-    t.record_stream(torch.cuda.current_stream(t.device))   # where the caller is likely to use it
-    return t
 
 
 class KeyWeights:
@@ -613,13 +618,14 @@ def kv_compact(kv_src, kv_dst, slot_idx, prefix_len, dst_start, slot_idx_out=Non
         if rc != DDT_OK:
             raise DDTError(rc, f"kv_compact_check (slot {bad})")
     if slot_idx_out is None:
-        slot_idx_out = slot_idx.clone()
+        slot_idx_out = _make(stream, slot_idx.clone)
     if workspace is None:
-        workspace = torch.empty(256, dtype=torch.uint8, device=slot_idx.device)
+        workspace = _make(stream, torch.empty, 256, dtype=torch.uint8, device=slot_idx.device)
     dims = make_dims(B, 1, 1, kv_src.shape[0], stride, stride if max_prefix_len is None else max_prefix_len)
     rc = lib().ddtree_kv_compact(_ptr(kv_src), _ptr(kv_dst), _ptr(slot_idx), _ptr(prefix_len), _ptr(dst_start),
                                  _ptr(slot_idx_out), ctypes.byref(dims), _ptr(workspace), _stream(stream))
     _check(rc, "ddtree_kv_compact")
+    _keep(stream, slot_idx_out, workspace)
     return slot_idx_out
 
 
