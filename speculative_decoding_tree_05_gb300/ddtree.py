@@ -630,7 +630,13 @@ def kv_compact(kv_src, kv_dst, slot_idx, prefix_len, dst_start, slot_idx_out=Non
 
 
 def read_device_status(workspace, stream=None, library=None) -> int:
+    """The status word of the last call that used `workspace`, after waiting for `stream`.
+
+    Without a stream it waits for the current one of the workspace's device, where the call ran.
+    """
     st = ctypes.c_int32(0)
-    rc = (lib() if library is None else library).ddtree_read_device_status(_ptr(workspace), ctypes.byref(st), _stream(stream))
-    _check(rc, "ddtree_read_device_status")
+    L = lib() if library is None else library
+    device = workspace.device
+    _run_on(device, L.ddtree_read_device_status, "ddtree_read_device_status", _ptr(workspace), ctypes.byref(st),
+            ctypes.c_void_p(_stream_of(device, stream)))
     return int(st.value)
