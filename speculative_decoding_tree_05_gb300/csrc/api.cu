@@ -20,6 +20,7 @@ constexpr int kMaxDevices = 64;
 
 struct DeviceInfo {
   int sm_count = 0;
+  BlockClusters clusters;
   bool ok = false;      // sm_103 and kernels configured
 };
 
@@ -39,7 +40,7 @@ int device_info(DeviceInfo* out) {
         cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
         major == 10 && minor == 3 && configure_prefix() == cudaSuccess && configure_tail_merge() == cudaSuccess &&
         configure_scores() == cudaSuccess && configure_evict() == cudaSuccess && configure_topk() == cudaSuccess &&
-        configure_block_attn() == cudaSuccess && configure_summary() == cudaSuccess)
+        configure_block_attn(&d.clusters) == cudaSuccess && configure_summary() == cudaSuccess)
       d.ok = true;
     g_dev[dev] = d;
   });
@@ -65,10 +66,11 @@ int check_dims(const ddt_dims* d) {
   return DDT_OK;
 }
 
-int current_device(int* sm_count) {
+int current_device(int* sm_count, BlockClusters* clusters) {
   DeviceInfo dev;
   const int rc = device_info(&dev);
   *sm_count = dev.sm_count;
+  if (clusters) *clusters = dev.clusters;
   return rc;
 }
 

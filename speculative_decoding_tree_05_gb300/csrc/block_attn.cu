@@ -44,7 +44,6 @@
 // merge kernel joins them.
 #include <cuda_runtime.h>
 #include <math_constants.h>
-#include <atomic>
 #include <type_traits>
 #include "cache_ops.cuh"
 #include "ptx.cuh"
@@ -850,11 +849,9 @@ struct BaLaunch {
   }
 };
 
-std::atomic<int> g_clusters[kBlockCluster + 1];  // of each size, that run at once
-
 }  // namespace
 
-cudaError_t configure_block_attn() {
+cudaError_t configure_block_attn(BlockClusters* clusters) {
   cudaError_t e = cudaFuncSetAttribute(block_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBaSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(block_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBaSmem);
@@ -866,7 +863,7 @@ cudaError_t configure_block_attn() {
       cudaGetLastError();
       n = 0;  // a merge kernel does it
     }
-    g_clusters[s] = n;
+    clusters->count[s] = n;
   }
   return cudaSuccess;
 }
@@ -874,8 +871,8 @@ cudaError_t configure_block_attn() {
 // A join through distributed shared memory reads at about 25 B/clk, so it suits few
 // rows (16 requests of 16 rows in a graph: 16.8 us, 18.3 with a merge kernel; of 64
 // rows 26.6 and 23.9); clusters that wait for others' SMs suit none.
-bool block_cluster_fits(int64_t groups, int rows, int splits) {
-  return rows <= kBlockRows / 2 && splits > 1 && splits <= kBlockCluster && groups <= g_clusters[splits];
+bool block_cluster_fits(int64_t groups, int rows, int splits, const BlockClusters& clusters) {
+  return rows <= kBlockRows / 2 && splits > 1 && splits <= kBlockCluster && groups <= clusters.count[splits];
 }
 
 cudaError_t launch_block_union(const BlockAttnParams& p, cudaStream_t stream) {

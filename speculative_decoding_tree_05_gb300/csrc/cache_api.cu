@@ -123,7 +123,8 @@ struct BlocksLayout {
 // minimise waves * (64-key tiles of a unit + kBlockUnitTiles), and kBlockMergeTiles
 // where a merge kernel follows; the tiles are those of lists that do not overlap (how
 // far they do is known on the device only).
-int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, BlocksLayout* w) {
+int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, const BlockClusters& clusters,
+                  BlocksLayout* w) {
   const int rc = check_cache_dims(d);
   if (rc != DDT_OK) return rc;
   if (!block_ok(block) || topk < 1 || topk > (1 << 20)) return DDT_ERR_DIMS;
@@ -140,13 +141,13 @@ int blocks_layout(const ddt_dims* d, int32_t block, int32_t topk, int sm_count, 
   w->splits = 1;
   for (int s = 1; s <= std::min<int64_t>(tiles, 32); ++s) {
     const int64_t cost = (all * s + sm_count - 1) / sm_count * ((tiles + s - 1) / s + kBlockUnitTiles) +
-                         (s == 1 || block_cluster_fits(all, group_rows, s) ? 0 : kBlockMergeTiles);
+                         (s == 1 || block_cluster_fits(all, group_rows, s, clusters) ? 0 : kBlockMergeTiles);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
       w->splits = s;
     }
   }
-  w->clustered = block_cluster_fits(all, group_rows, w->splits);
+  w->clustered = block_cluster_fits(all, group_rows, w->splits, clusters);
   const size_t part = w->splits > 1 && !w->clustered ? size_t(d->batch) * w->splits * T * H : 0;
   w->len_off = kStatusBytes;
   w->tree_len_off = align_up(w->len_off + all * sizeof(int32_t), 256);
@@ -395,8 +396,9 @@ extern "C" int ddtree_block_select(const void* q, const void* summary, const flo
 
 extern "C" size_t ddtree_verify_blocks_workspace_bytes(const ddt_dims* dims, int32_t block, int32_t topk) {
   int sms = 0;
+  BlockClusters clusters;
   BlocksLayout w;
-  if (current_device(&sms) != DDT_OK || blocks_layout(dims, block, topk, sms, &w) != DDT_OK) return 0;
+  if (current_device(&sms, &clusters) != DDT_OK || blocks_layout(dims, block, topk, sms, clusters, &w) != DDT_OK) return 0;
   return w.bytes;
 }
 
@@ -406,7 +408,8 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
                                          int32_t topk, float sm_scale, void* out, float* lse, const ddt_dims* dims,
                                          void* workspace, size_t workspace_bytes, ddt_stream_t stream) {
   BlocksLayout w;
-  int rc = blocks_layout(dims, block, topk, 1, &w);  // the sizes, before any device query
+  BlockClusters clusters;
+  int rc = blocks_layout(dims, block, topk, 1, clusters, &w);  // the sizes, before any device query
   if (rc != DDT_OK) return rc;
   if (dims->batch == 0) return DDT_OK;
   if (!q || !kv_pool || !prefix_len || !tree_parent || !tree_slot_idx || !block_idx || !out || !lse || !workspace ||
@@ -417,8 +420,8 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
       !aligned(block_idx, 4) || !aligned(lse, 4))
     return DDT_ERR_ALIGN;
   int sms = 0;
-  if ((rc = current_device(&sms)) != DDT_OK) return rc;
-  if ((rc = blocks_layout(dims, block, topk, sms, &w)) != DDT_OK) return rc;
+  if ((rc = current_device(&sms, &clusters)) != DDT_OK) return rc;
+  if ((rc = blocks_layout(dims, block, topk, sms, clusters, &w)) != DDT_OK) return rc;
   if (workspace_bytes < w.bytes) return DDT_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   BlockAttnParams p = {};
@@ -467,5 +470,25 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
   if (launch_block_union(p, s) != cudaSuccess || launch_block_attn(p, s) != cudaSuccess ||
       (w.splits > 1 && !p.clustered && launch_block_merge(m, p.batch, s) != cudaSuccess))
     return DDT_ERR_LAUNCH;
+  return DDT_OK;
+}
+
+// Host-side introspection of the schedule (not part of the public header; the CPU
+// tests use it, no device is needed).  Block attention's layout on a device with
+// sm_count SMs that runs clusters[s] clusters of s CTAs at once (s = 2 to 8): out =
+// {groups of a request, key splits, 1 if they are clusters}; *bytes: the workspace.
+extern "C" __attribute__((visibility("default"))) int ddtree_internal_blocks_plan(const ddt_dims* dims, int32_t block,
+                                                                                  int32_t topk, int sm_count,
+                                                                                  const int32_t* clusters, int32_t* out,
+                                                                                  int64_t* bytes) {
+  BlockClusters c;
+  for (int s = 2; s <= kBlockCluster; ++s) c.count[s] = clusters[s];
+  BlocksLayout w;
+  const int rc = blocks_layout(dims, block, topk, sm_count, c, &w);
+  if (rc != DDT_OK) return rc;
+  out[0] = w.groups;
+  out[1] = w.splits;
+  out[2] = w.clustered ? 1 : 0;
+  *bytes = static_cast<int64_t>(w.bytes);
   return DDT_OK;
 }

@@ -158,9 +158,12 @@ struct BlockAttnParams {
   int32_t* status;
 };
 constexpr int kBlockCluster = 8;
-cudaError_t configure_block_attn();
+struct BlockClusters {
+  int count[kBlockCluster + 1] = {};  // clusters of each size that one device runs at once
+};
+cudaError_t configure_block_attn(BlockClusters* clusters);  // on the current device
 // Whether groups of `rows` rows in `splits` splits are clusters: they all run at once, and the join is short.
-bool block_cluster_fits(int64_t groups, int rows, int splits);
+bool block_cluster_fits(int64_t groups, int rows, int splits, const BlockClusters& clusters);
 cudaError_t launch_block_union(const BlockAttnParams& p, cudaStream_t stream);
 cudaError_t launch_block_attn(const BlockAttnParams& p, cudaStream_t stream);
 

@@ -11,8 +11,10 @@ constexpr size_t kStatusBytes = 256;
 
 // Return codes of include/ddtree.h.
 int check_dims(const ddt_dims* d);
-// The current device: DDT_OK and its SM count if it is an sm_103 GPU whose kernels are set up.
-int current_device(int* sm_count);
+struct BlockClusters;  // cache_ops.cuh
+// The current device: DDT_OK and its SM count if it is an sm_103 GPU whose kernels are set up;
+// also how many clusters of block attention it runs at once, if asked.
+int current_device(int* sm_count, BlockClusters* clusters = nullptr);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
