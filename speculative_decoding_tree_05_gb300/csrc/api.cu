@@ -21,8 +21,14 @@ constexpr int kMaxDevices = 64;
 struct DeviceInfo {
   int sm_count = 0;
   BlockClusters clusters;
-  bool ok = false;      // sm_103 and kernels configured
+  bool ok = false;        // sm_103, and the verify kernels are set up
+  bool cache_ok = false;  // and the cache-size and block kernels are
 };
+
+#ifdef DDT_TEST_HOOKS
+// Test builds only: the set-up of the cache-size and block kernels counts as failed.
+int g_test_fail_cache_setup = 0;
+#endif
 
 DeviceInfo g_dev[kMaxDevices];
 std::once_flag g_once[kMaxDevices];
@@ -38,10 +44,16 @@ int device_info(DeviceInfo* out) {
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess &&
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) == cudaSuccess &&
         cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
-        major == 10 && minor == 3 && configure_prefix() == cudaSuccess && configure_tail_merge() == cudaSuccess &&
-        configure_scores() == cudaSuccess && configure_evict() == cudaSuccess && configure_topk() == cudaSuccess &&
-        configure_block_attn(&d.clusters) == cudaSuccess && configure_summary() == cudaSuccess)
-      d.ok = true;
+        major == 10 && minor == 3) {
+      d.ok = configure_prefix() == cudaSuccess && configure_tail_merge() == cudaSuccess;
+      d.cache_ok = configure_scores() == cudaSuccess && configure_evict() == cudaSuccess &&
+                   configure_topk() == cudaSuccess && configure_block_attn(&d.clusters) == cudaSuccess &&
+                   configure_summary() == cudaSuccess;
+#ifdef DDT_TEST_HOOKS
+      if (g_test_fail_cache_setup) d.cache_ok = false;
+#endif
+    }
+    if (!d.ok || !d.cache_ok) cudaGetLastError();  // a failed set-up is reported by the calls that need it, not by a launch
     g_dev[dev] = d;
   });
   *out = g_dev[dev];
@@ -68,10 +80,10 @@ int check_dims(const ddt_dims* d) {
 
 int current_device(int* sm_count, BlockClusters* clusters) {
   DeviceInfo dev;
-  const int rc = device_info(&dev);
+  device_info(&dev);
   *sm_count = dev.sm_count;
   if (clusters) *clusters = dev.clusters;
-  return rc;
+  return dev.cache_ok ? DDT_OK : DDT_ERR_DEVICE;
 }
 
 namespace {
@@ -559,6 +571,10 @@ extern "C" __attribute__((visibility("default"))) int ddtree_internal_group_unit
 int32_t ddt::g_test_drop_step = -1;
 extern "C" __attribute__((visibility("default"))) void ddtree_test_set_drop_step(int32_t step) {
   ddt::g_test_drop_step = step;
+}
+// To be set before the first call on a device.
+extern "C" __attribute__((visibility("default"))) void ddtree_test_fail_cache_setup(int32_t fail) {
+  g_test_fail_cache_setup = fail;
 }
 #endif
 

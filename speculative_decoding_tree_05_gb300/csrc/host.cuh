@@ -12,8 +12,8 @@ constexpr size_t kStatusBytes = 256;
 // Return codes of include/ddtree.h.
 int check_dims(const ddt_dims* d);
 struct BlockClusters;  // cache_ops.cuh
-// The current device: DDT_OK and its SM count if it is an sm_103 GPU whose kernels are set up;
-// also how many clusters of block attention it runs at once, if asked.
+// The current device: DDT_OK and its SM count if it is an sm_103 GPU on which the cache-size and block
+// kernels are set up; also how many clusters of block attention it runs at once, if asked.
 int current_device(int* sm_count, BlockClusters* clusters = nullptr);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
