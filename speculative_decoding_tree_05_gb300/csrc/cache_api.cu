@@ -14,11 +14,6 @@ namespace {
 
 constexpr int kScoreUnitTiles = 4;  // fixed cost of one score unit, in query tiles
 constexpr int kWeightSumTiles = 3;  // the launch that adds the shares' sums, in query tiles
-// What the tensor core's truncating accumulation takes off a score on average,
-// relative to it (two accumulators of 18 steps, key_scores.cu).  Measured over
-// nine shapes: the weights' mean error is -7e-7 to -5e-7 without it, within 1e-7
-// with it.
-constexpr double kScoreLoss = 2.2e-7;
 // Fixed costs in block attention, in 64-key tiles (1.7 us): of a unit, and of a merge
 // kernel behind it.  (8 requests of 17 nodes x 16 heads in a graph: 3 splits in one
 // wave 67 us, 7 splits in two waves 74 us.)
@@ -210,7 +205,7 @@ extern "C" int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_
   p.slot_stride = dims->slot_stride;
   p.heads = dims->num_heads;
   p.nodes = dims->num_nodes;
-  p.scale_log2 = static_cast<float>(sm_scale * 1.4426950408889634 * (1.0 + kScoreLoss));
+  p.scale_log2 = static_cast<float>(sm_scale * 1.4426950408889634);
   p.decay = decay;
   p.weight_in = decay != 0.f ? weight_in : nullptr;
   p.weight_out = weight_out;
