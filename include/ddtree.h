@@ -367,7 +367,9 @@ DDT_API int ddtree_kv_evict(const float* weight, const int32_t* slot_idx, const 
  * prefix's end; N = ceil(max_prefix_len / block) is the block stride.
  *
  * ddtree_block_summary:
- *   mean of the block's rows (the sum is exact, the mean rounded once to fp32),
+ *   mean of the block's rows (their sum is off by at most 2^-34 of the sum of |x|,
+ *   then the mean is rounded once to fp32; where rows cancel to that degree, the
+ *   result can depend on their order),
  *   scale = max |mean| * c, c the fp32 nearest to 1/127, summary = round to nearest
  *   even of mean / scale, at most 127 in size
  *   from_len  int32 [B] device or NULL: only blocks that hold a position at or
@@ -375,8 +377,8 @@ DDT_API int ddtree_kv_evict(const float* weight, const int32_t* slot_idx, const 
  *   summary   bf16 [B, N, 576]: integers in [-127, 127]
  *   scale     fp32 [B, N]
  * Rows whose slot is outside the pool are left out (DDT_STATUS_BAD_SLOT); a
- * block with no row has scale 0, one whose sum is not finite in fp32 has scale
- * NaN and zeros.  Other blocks' entries are not written.  workspace >= 256 bytes.
+ * block with no row has scale 0, one with a row that is not finite has scale NaN
+ * and zeros.  Other blocks' entries are not written.  workspace >= 256 bytes.
  */
 DDT_API int ddtree_block_summary(const void* kv_pool, const int32_t* slot_idx, const int32_t* prefix_len,
                                  const int32_t* from_len, int32_t block, void* summary, float* scale,

@@ -6,8 +6,11 @@
 // The integers are kept as bf16 (exact), the tensor cores' operand type: the
 // dot product of two such rows is an integer below 2^24, so block scores come
 // out exact in fp32 on any tiling.  The sums carry their rounding errors along
-// (two-sum), so the mean is the exact sum's, rounded once, and no integer depends
-// on the order of the rows.
+// (two-sum): off by at most 2^-34 of the sum of |x| over the block's (up to 128)
+// rows, (127 * 2^-24)^2, before the mean is rounded to fp32.  Only where rows
+// cancel to that degree can an integer depend on their order.  They are summed at
+// 2^-7 of their size (exact: bf16 values stay above the least fp32 number), so no
+// partial sum of finite rows overflows.
 //
 // Bound by memory: each row is read once (1152 B).  One CTA per SM: four warps
 // keep up to four stages of 32 rows on their way into shared memory (one bulk
@@ -39,6 +42,8 @@ struct SumShared {
   float amax[kSumTeams][kSumWarps];
   int abort;
 };
+constexpr float kSumDown = 1.f / 128.f;            // of a row's value when it is added
+constexpr float kSumBig = 1.7014118e38f / 128.f;   // 2^127 at that size
 constexpr int kSumOffPart = kSumStages * kSumStageBytes;  // [4 groups][hi, lo][576]
 constexpr int kSumPart = kSumGroups * 2 * kDqk;           // floats of a team
 constexpr int kSumOffShared = kSumOffPart + kSumTeams * kSumPart * 4;
@@ -164,7 +169,8 @@ __global__ void __launch_bounds__(kSumBlockThreads, 1) block_summary_kernel(Summ
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          two_sum(hi[d], lo[d], f32x2(__uint_as_float(w[d] << 16), __uint_as_float(w[d] & 0xffff0000u)));
+          two_sum(hi[d], lo[d],
+                  mul_x2(f32x2(__uint_as_float(w[d] << 16), __uint_as_float(w[d] & 0xffff0000u)), f32x2(kSumDown, kSumDown)));
       };
       for (int ch = 0; ch < chunks; ++ch, ++n) {
         const uint32_t st = n % kSumStages;
@@ -207,16 +213,20 @@ __global__ void __launch_bounds__(kSumBlockThreads, 1) block_summary_kernel(Summ
       float hs[2], ls[2], mean[2];
       f32x2_split(h2, hs[0], hs[1]);
       f32x2_split(l2, ls[0], ls[1]);
-      const float n_rows = static_cast<float>(max(count, 1));
       float am = 0.f;
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
         // (hi + lo) / rows in fp32 pairs: the quotient of hi, and that of what is
         // left of hi and lo (64-bit division is slow here and would cost more than the sums)
+        // a sum beyond fp32 is divided at 2^-7 of its size, by 2^-7 of the rows
+        const float up = fabsf(hs[d]) < kSumBig ? 1.f / kSumDown : 1.f;
+        const float n_rows = static_cast<float>(max(count, 1)) * (up * kSumDown);
+        hs[d] *= up;
+        ls[d] *= up;
         const float q = __fdiv_rn(hs[d], n_rows);
         const float m = __fadd_rn(q, __fdiv_rn(__fadd_rn(__fmaf_rn(-q, n_rows, hs[d]), ls[d]), n_rows));
         mean[d] = count > 0 ? m : 0.f;
-        // an infinite row leaves a NaN in the carried error: any non-finite sum counts as such
+        // (an infinite row leaves a NaN in the carried error)
         am = fabsf(mean[d]) < CUDART_INF_F ? fmaxf(am, fabsf(mean[d])) : CUDART_INF_F;
       }
 #pragma unroll
