@@ -2,7 +2,7 @@
 //
 // out = sum over the splits of w_s o_s / sum of w_s with w_s = exp(lse_s - max),
 // the o_s normalised; lse = max + log of the sum of w_s.  One warp per (node,
-// head) row, all its partials' loads in flight (up to eight splits at a time).
+// head) row, four splits' loads in flight at a time.
 // Bound by reading the partials, which the attention kernel has just written to
 // L2: bytes per row splits * 2052 + 1028.
 #include <cuda_runtime.h>
