@@ -8,8 +8,10 @@ header is newer than them.
 build(variant="testhooks") compiles the same sources with test-only hooks into
 lib/libddtree_testhooks.so: short bounded-wait limits, a switch that makes the
 prefix kernel skip the loads of one pipeline step (so a wait runs out and the
-kernel reports DDT_STATUS_TIMEOUT), and counters of the lazy O rescales and of
-the units rerun with 20-bit score exchange.  Only tests load it.
+kernel reports DDT_STATUS_TIMEOUT), one that makes the kernels of the
+cache-size and block operators keep one buffer back, to the same end, one that
+fails the set-up of those kernels on the host, and counters of the lazy O
+rescales and of the units rerun with 20-bit score exchange.  Only tests load it.
 """
 from __future__ import annotations
 

@@ -572,6 +572,11 @@ int32_t ddt::g_test_drop_step = -1;
 extern "C" __attribute__((visibility("default"))) void ddtree_test_set_drop_step(int32_t step) {
   ddt::g_test_drop_step = step;
 }
+// Test builds only: the kernels of the cache-size and block operators keep this one buffer back (cache_ops.cuh).
+int32_t ddt::g_test_keep_back = -1;
+extern "C" __attribute__((visibility("default"))) void ddtree_test_set_keep_back(int32_t buffer) {
+  ddt::g_test_keep_back = buffer;
+}
 // To be set before the first call on a device.
 extern "C" __attribute__((visibility("default"))) void ddtree_test_fail_cache_setup(int32_t fail) {
   g_test_fail_cache_setup = fail;

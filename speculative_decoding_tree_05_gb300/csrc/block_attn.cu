@@ -545,6 +545,9 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_kernel(const __grid_
       }
       tc_fence_before();
       __syncwarp();
+#ifdef DDT_TEST_HOOKS
+      if (warp != 1 || t != p.test_keep_back)
+#endif
       if (lane == 0) mbar_arrive(&sh.s_free[st]);
       // P^T, row (key) r of 64 columns, 128-byte swizzle
       uint8_t* pb = smem + kBaOffP;

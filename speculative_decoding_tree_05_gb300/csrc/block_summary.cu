@@ -150,7 +150,11 @@ __global__ void __launch_bounds__(kSumBlockThreads, 1) block_summary_kernel(Summ
     };
     auto hand_back = [&](uint32_t i) {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.empty[i % kSumStages]);
+#ifdef DDT_TEST_HOOKS
+      if (warp == 0 && static_cast<int>(i) == p.test_keep_back) return;
+#endif
+      // (not after a give-up: the stage may not have landed, and the copying warps would fill it a second time)
+      if (lane == 0 && !failed) mbar_arrive(&sh.empty[i % kSumStages]);
     };
     int turn = 0;
     for (int64_t j = j0; j < n_blocks; j += step, turn = turn + 1 == kSumTeams ? 0 : turn + 1) {

@@ -188,6 +188,9 @@ extern "C" int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_
   if (workspace_bytes < w.bytes) return DDT_ERR_WORKSPACE;
   const bool packed = num_sel > 0;
   ScoreParams p = {};
+#ifdef DDT_TEST_HOOKS
+  p.test_keep_back = g_test_keep_back;
+#endif
   p.batch = dims->batch;
   p.rows = (packed ? num_sel : dims->num_nodes) * dims->num_heads;
   const int64_t q_rows = int64_t(p.batch) * p.rows;
@@ -299,6 +302,9 @@ extern "C" int ddtree_block_summary(const void* kv_pool, const int32_t* slot_idx
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!clear_status(workspace, s)) return DDT_ERR_LAUNCH;
   SummaryParams p = {};
+#ifdef DDT_TEST_HOOKS
+  p.test_keep_back = g_test_keep_back;
+#endif
   p.kv = static_cast<const uint16_t*>(kv_pool);
   p.slot_idx = slot_idx;
   p.prefix_len = prefix_len;
@@ -337,6 +343,9 @@ extern "C" int ddtree_block_select(const void* q, const void* summary, const flo
   if ((rc = current_device(&sms)) != DDT_OK) return rc;
   const int H = dims->num_heads;
   ScoreParams p = {};
+#ifdef DDT_TEST_HOOKS
+  p.test_keep_back = g_test_keep_back;
+#endif
   p.batch = dims->batch;
   p.rows = dims->num_nodes * H;
   const int64_t q_rows = int64_t(p.batch) * p.rows;
@@ -420,6 +429,9 @@ extern "C" int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, con
   if (workspace_bytes < w.bytes) return DDT_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   BlockAttnParams p = {};
+#ifdef DDT_TEST_HOOKS
+  p.test_keep_back = g_test_keep_back;
+#endif
   p.q = static_cast<const uint16_t*>(q);
   p.kv = static_cast<const uint16_t*>(kv_pool);
   p.slot_idx = slot_idx;

@@ -8,6 +8,10 @@
 
 namespace ddt {
 
+#ifdef DDT_TEST_HOOKS
+extern int32_t g_test_keep_back;  // api.cu
+#endif
+
 constexpr int32_t kStatusBadNode = 32;
 constexpr int32_t kStatusBadBlock = 64;
 
@@ -50,6 +54,9 @@ struct ScoreParams {
   const float* key_scale;    // kScoreBlock: [B, key_stride]
   float* score;              // kScoreBlock: [B, T, key_stride]
   int32_t* status;
+#ifdef DDT_TEST_HOOKS
+  int32_t test_keep_back;    // tile whose score buffer that is not handed back (-1: none), so that the next wait for it runs out
+#endif
 };
 
 cudaError_t configure_scores();
@@ -96,6 +103,9 @@ struct SummaryParams {
   int64_t pool_slots;
   int32_t slot_stride, max_prefix_len, block, blocks;
   int32_t* status;
+#ifdef DDT_TEST_HOOKS
+  int32_t test_keep_back;    // stage that is not handed back (-1: none), so that the next wait for it runs out
+#endif
 };
 cudaError_t configure_summary();
 cudaError_t launch_block_summary(const SummaryParams& p, int batch, int sm_count, cudaStream_t stream);
@@ -156,6 +166,9 @@ struct BlockAttnParams {
   uint16_t* out;              // bf16 [B, T, H, 512]
   float* lse;                 // fp32 [B, T, H]
   int32_t* status;
+#ifdef DDT_TEST_HOOKS
+  int32_t test_keep_back;    // tile whose score buffer that is not handed back (-1: none), so that the next wait for it runs out
+#endif
 };
 constexpr int kBlockCluster = 8;
 struct BlockClusters {

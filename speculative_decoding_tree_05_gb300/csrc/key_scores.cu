@@ -414,6 +414,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
         __syncwarp();
         // relaxed: the scores are in registers, and no store has to be seen (a
         // release at cluster scope took 1900 cycles here, most of a tile)
+#ifdef DDT_TEST_HOOKS
+        if (warp == 4 && static_cast<int>(n_tile) == p.test_keep_back) continue;
+#endif
         if (lane == 0) mbar_arrive_remote_relaxed(buf ? free1 : free0);
       }
       if (bar_red_or(3, 256, !ok)) {
