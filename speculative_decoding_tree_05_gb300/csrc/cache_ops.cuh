@@ -55,7 +55,7 @@ struct ScoreParams {
   float* score;              // kScoreBlock: [B, T, key_stride]
   int32_t* status;
 #ifdef DDT_TEST_HOOKS
-  int32_t test_keep_back;    // tile whose score buffer that is not handed back (-1: none), so that the next wait for it runs out
+  int32_t test_keep_back;    // tile whose score buffer is not handed back (-1: none), so that the next wait for it runs out
 #endif
 };
 
@@ -167,7 +167,7 @@ struct BlockAttnParams {
   float* lse;                 // fp32 [B, T, H]
   int32_t* status;
 #ifdef DDT_TEST_HOOKS
-  int32_t test_keep_back;    // tile whose score buffer that is not handed back (-1: none), so that the next wait for it runs out
+  int32_t test_keep_back;    // tile whose score buffer is not handed back (-1: none), so that the next wait for it runs out
 #endif
 };
 constexpr int kBlockCluster = 8;

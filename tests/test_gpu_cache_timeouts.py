@@ -43,3 +43,56 @@ def test_block_summary(hooks, monkeypatch, block, buffer):
                                            lambda: ddtree.read_device_status(ws))
     assert first & ddtree.STATUS_TIMEOUT and after == 0
     assert torch.equal(got, want) and torch.equal(scale, want_scale)
+
+
+@pytest.mark.parametrize("lens,chosen,buffer", [
+    ([2000], None, 0), ([2000], None, 1), ([9000, 300], None, 0), ([9000, 300], None, 4), ([9000, 300], 40, 1),
+    ([9000, 300], 40, 4)])
+def test_key_weights(hooks, lens, chosen, buffer):
+    """65 x 64 rows are 33 tiles, 20 for 40 chosen nodes; one request of 2000 shares them out, three or four to a unit.
+
+    Tile buffer + 2 waits for what is kept back.
+    """
+    d = weight.make(len(lens), lens, 65, 64, seed=1)
+    sel = None
+    if chosen:
+        sel = torch.arange(chosen, dtype=torch.int32, device="cuda").expand(len(lens), chosen).contiguous()
+    k = ddtree.KeyWeights(len(lens), 65, 64, d["kv"].shape[0], max(lens), library=hooks)
+    first, after, out = status_of(hooks, buffer, lambda: k(d["q"], d["kv"], d["slot"], d["lens"], d["lse"], weight.SCALE,
+                                                           node_idx=sel), k.status)
+    assert first & ddtree.STATUS_TIMEOUT and after == 0
+    weight.check(d, out, sel=sel)
+
+
+@pytest.mark.parametrize("buffer", [0, 1])
+def test_block_selector(hooks, buffer):
+    """8 x 65 x 16 rows against 1250 blocks: 9 tiles of rows a request."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randn(8, 65, 16, 576, generator=g, device="cuda").to(torch.bfloat16)
+    summary = torch.randint(-127, 128, (8, 1250, 576), generator=g, device="cuda").to(torch.bfloat16)
+    scale = torch.rand(8, 1250, generator=g, device="cuda")
+    n = torch.full((8,), 20000, dtype=torch.int32, device="cuda")
+    want = ddtree.BlockSelector(8, 65, 16, 20000, 16, 32)(q, summary, scale, n)
+    s = ddtree.BlockSelector(8, 65, 16, 20000, 16, 32, library=hooks)
+    first, after, got = status_of(hooks, buffer, lambda: s(q, summary, scale, n), s.status)
+    assert first & ddtree.STATUS_TIMEOUT and after == 0
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("buffer", [0, 1])
+@pytest.mark.parametrize("batch,nodes,heads,topk", [
+    (16, 1, 16, 32),        # few rows: the splits are clusters
+    (4, 1, 16, 160),        # more splits than a cluster has, and a merge kernel
+    (2, 8, 16, 100),        # 64 rows
+    (40, 9, 16, 12),        # 120 groups: one split
+    (1, 2, 128, 160)])      # slices of one node's heads
+def test_block_verifier(hooks, buffer, batch, nodes, heads, topk):
+    """A key list long enough that every split has the three tiles that the wait takes."""
+    lens = [topk * 64] * batch
+    d = attn.make(lens, nodes, heads, 64, topk, seed=3, lists="all")
+    v = ddtree.BlockVerifier(batch, nodes, heads, d["kv"].shape[0], max(lens), 64, topk, library=hooks)
+    first, after, (out, lse) = status_of(
+        hooks, buffer, lambda: v(d["q"], d["kv"], d["slot"], d["lens"], d["parent"], d["tree"], d["idx"], attn.SCALE),
+        v.status)
+    assert first & ddtree.STATUS_TIMEOUT and after == 0
+    attn.check(d, out, lse)
