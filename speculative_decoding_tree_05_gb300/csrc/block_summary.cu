@@ -266,11 +266,12 @@ cudaError_t configure_summary() {
 }
 
 cudaError_t launch_block_summary(const SummaryParams& p, int batch, int sm_count, cudaStream_t stream) {
-  if (batch == 0 || p.blocks == 0) return cudaSuccess;
+  if (batch == 0) return cudaSuccess;
   // blocks of a request are dealt to its share of the SMs: how many are touched
   // (from_len) is known on the device only
   const int share = (sm_count + batch - 1) / batch;
-  const unsigned gx = static_cast<unsigned>(p.blocks < share ? p.blocks : share);
+  // (without a block one CTA a request still looks its length over for the status word)
+  const unsigned gx = static_cast<unsigned>(p.blocks < share ? (p.blocks > 0 ? p.blocks : 1) : share);
   block_summary_kernel<<<dim3(gx, batch), kSumBlockThreads, kSumSmem, stream>>>(p);
   return cudaGetLastError();
 }

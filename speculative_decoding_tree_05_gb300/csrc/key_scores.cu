@@ -503,13 +503,13 @@ cudaError_t configure_scores() {
 }
 
 cudaError_t launch_scores(const ScoreParams& p, ScoreMode mode, int sm_count, bool after_kernel, cudaStream_t stream) {
-  if (p.units == 0) return cudaSuccess;
+  // (without a key tile one pair still looks the lengths and nodes over for the status word)
   const int pairs = sm_count >= 4 ? sm_count / 2 : 1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(2 * (p.units < pairs ? p.units : pairs));
+  cfg.gridDim = dim3(2 * (p.units < pairs ? (p.units > 0 ? p.units : 1) : pairs));
   cfg.blockDim = dim3(kScThreads);
   cfg.dynamicSmemBytes = kScSmem;
   cfg.stream = stream;
