@@ -57,7 +57,8 @@ typedef struct CUstream_st* ddt_stream_t;
 #define DDT_ERR_LAUNCH (-5)    /* a kernel launch or CUDA runtime call failed */
 #define DDT_ERR_DEVICE (-6)    /* the current device is not an sm_103 GPU */
 #define DDT_ERR_ALIAS (-7)     /* ddtree_kv_compact_check: destinations overlap or cover a live row;
-                                  ddtree_kv_evict: an output overlaps an input or another output */
+                                  ddtree_kv_evict: an output overlaps an input or another output;
+                                  ddtree_kv_weight: weight_out overlaps weight_in in part */
 
 /* Device status bits (ddtree_read_device_status). */
 #define DDT_STATUS_BAD_SLOT 1      /* a slot index outside [0, pool_slots): key left out */
@@ -323,7 +324,7 @@ DDT_API int ddtree_verify_attn_static_scratch(const void* q, const void* kv_pool
  *              outside [0, T) are left out and set DDT_STATUS_BAD_NODE.  NULL
  *              with num_sel = 0: every node.  num_sel <= 65535.
  *   weight_in  fp32 [B, slot_stride], not read when decay is 0 (it may then be
- *              NULL); may be weight_out
+ *              NULL); may be weight_out, but not overlap it otherwise (DDT_ERR_ALIAS)
  *   weight_out fp32 [B, slot_stride]; entries from prefix_len[b] on are not written
  * A key whose slot is outside the pool gains nothing and sets
  * DDT_STATUS_BAD_SLOT.  Sums are in fp32 in a fixed order: the same bits on

@@ -182,6 +182,9 @@ extern "C" int ddtree_kv_weight(const void* q, const void* kv_pool, const int32_
       !aligned(prefix_len, 4) || !aligned(lse, 4) || !aligned(node_idx, 4) || !aligned(weight_in, 4) ||
       !aligned(weight_out, 4))
     return DDT_ERR_ALIGN;
+  // in place, or apart: an entry is written while others' old weights are still to be read
+  const size_t table = size_t(dims->batch) * dims->slot_stride * 4;
+  if (decay != 0.f && weight_in != weight_out && overlap(weight_in, table, weight_out, table)) return DDT_ERR_ALIAS;
   int sms = 0;
   if ((rc = current_device(&sms)) != DDT_OK) return rc;
   if ((rc = weight_layout(dims, num_sel, sms, &w)) != DDT_OK) return rc;
