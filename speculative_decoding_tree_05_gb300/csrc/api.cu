@@ -592,7 +592,7 @@ extern "C" const char* ddtree_status_string(int code) {
     case DDT_ERR_ALIGN: return "a device pointer is misaligned";
     case DDT_ERR_LAUNCH: return "a kernel launch or CUDA runtime call failed";
     case DDT_ERR_DEVICE: return "the current device is not an sm_103 GPU";
-    case DDT_ERR_ALIAS: return "kv_compact destinations overlap each other or a live source row";
+    case DDT_ERR_ALIAS: return "an output overlaps an input or another output (kv_compact: a destination, another one or a live source row)";
     default: return "unknown status";
   }
 }

@@ -24,3 +24,9 @@ def test_weights_in_place_apart_or_not_read(lib, shift, decay):  # noqa: F811
     if torch.cuda.is_available():
         pytest.skip("a GPU is present: the call would run on these addresses")
     assert weigh(lib, OLD, OLD + shift, decay) == -6
+
+
+def test_the_message_names_no_other_call(lib):  # noqa: F811
+    """The code is eviction's and key weights' too, not kv_compact's alone."""
+    text = ddtree.status_string(-7)
+    assert text.startswith("an output overlaps an input or another output")
