@@ -309,7 +309,8 @@ DDT_API int ddtree_verify_attn_static_scratch(const void* q, const void* kv_pool
 /*
  * Keeping a long request's cache small: accumulated attention weights of the
  * prefix keys, and eviction of the positions that weigh least.  (These entry
- * points and the block ones below take max_prefix_len up to 2^30.)
+ * points and the block ones below take max_prefix_len up to 2^30.  Calls, and
+ * replays of captured ones, that share a workspace must not overlap.)
  *
  * ddtree_kv_weight adds up what a verify call's softmax gave each prefix key:
  *   weight_out[b][j] = decay * weight_in[b][j]
@@ -414,7 +415,7 @@ DDT_API int ddtree_block_select(const void* q, const void* summary, const float*
  *   out        bf16 [B, T, H, 512] (the operand type of the product that follows)
  *   lse        fp32 [B, T, H]
  * The other arguments are ddtree_verify_attn's, and with every block listed it
- * computes the same.  Nodes are processed in groups of up to 64 (node, head)
+ * attends to the same keys (there out is fp32).  Nodes are processed in groups of up to 64 (node, head)
  * rows over the union of their lists; scores and sums are fp32, softmax weights
  * keep 16 bits, and out is rounded to bf16 once.  A non-finite key row reaches
  * only the nodes that list its block.  Results are the same bits on every run.

@@ -368,8 +368,8 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // True in one lane of a converged warp.  Code under it keeps its operands in
-// uniform registers, which the MMA instructions take (39 cycles an issue
-// instead of 46 behind a lane test).
+// uniform registers, which the MMA instructions take; behind a lane test every
+// issue moves them there first.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
