@@ -872,8 +872,8 @@ cudaError_t configure_block_attn(BlockClusters* clusters) {
 }
 
 // A join through distributed shared memory reads at about 25 B/clk, so it suits few
-// rows (16 requests of 16 rows in a graph: 16.8 us, 18.3 with a merge kernel; of 64
-// rows 26.6 and 23.9); clusters that wait for others' SMs suit none.
+// rows (16 requests of 16 rows in a graph: 17.9 us, 19.0 with a merge kernel; of 64
+// rows 29.1 and 25.2); clusters that wait for others' SMs suit none.
 bool block_cluster_fits(int64_t groups, int rows, int splits, const BlockClusters& clusters) {
   return rows <= kBlockRows / 2 && splits > 1 && splits <= kBlockCluster && groups <= clusters.count[splits];
 }

@@ -14,9 +14,9 @@ namespace {
 
 constexpr int kScoreUnitTiles = 4;  // fixed cost of one score unit, in query tiles
 constexpr int kWeightSumTiles = 3;  // the launch that adds the shares' sums, in query tiles
-// Fixed costs in block attention, in 64-key tiles (1.7 us): of a unit, and of a merge
+// Fixed costs in block attention, in 64-key tiles (2.1 us): of a unit, and of a merge
 // kernel behind it.  (8 requests of 17 nodes x 16 heads in a graph: 3 splits in one
-// wave 67 us, 7 splits in two waves 74 us.)
+// wave 76 to 81 us, 11 splits in three waves 94 us.)
 constexpr int kBlockUnitTiles = 5, kBlockMergeTiles = 2;
 
 int round32(int x) { return (x + 31) / 32 * 32; }
