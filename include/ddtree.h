@@ -415,10 +415,11 @@ DDT_API int ddtree_block_select(const void* q, const void* summary, const float*
  *   out        bf16 [B, T, H, 512] (the operand type of the product that follows)
  *   lse        fp32 [B, T, H]
  * The other arguments are ddtree_verify_attn's, and with every block listed it
- * attends to the same keys (there out is fp32).  Nodes are processed in groups of up to 64 (node, head)
- * rows over the union of their lists; scores and sums are fp32, softmax weights
- * keep 16 bits, and out is rounded to bf16 once.  A non-finite key row reaches
- * only the nodes that list its block.  Results are the same bits on every run.
+ * attends to the same keys (there out is fp32).  Nodes are processed in groups of
+ * up to 64 (node, head) rows over the union of their lists; scores and sums are
+ * fp32, softmax weights keep 16 bits, and out is rounded to bf16 once.  A
+ * non-finite key row reaches only the nodes that list its block.  Results are the
+ * same bits on every run.
  * workspace >= ddtree_verify_blocks_workspace_bytes(dims, block, topk), which
  * needs a current CUDA device.
  */
