@@ -57,7 +57,8 @@ typedef struct CUstream_st* ddt_stream_t;
 #define DDT_ERR_LAUNCH (-5)    /* a kernel launch or CUDA runtime call failed */
 #define DDT_ERR_DEVICE (-6)    /* the current device is not an sm_103 GPU */
 #define DDT_ERR_ALIAS (-7)     /* ddtree_kv_compact_check: destinations overlap or cover a live row;
-                                  ddtree_kv_evict: an output overlaps an input or another output;
+                                  ddtree_kv_evict, ddtree_kv8_write, ddtree_kv8_read, ddtree_accept: an
+                                  output overlaps an input or another output;
                                   ddtree_kv_weight: weight_out overlaps weight_in in part */
 
 /* Device status bits (ddtree_read_device_status). */
@@ -68,6 +69,9 @@ typedef struct CUstream_st* ddt_stream_t;
 #define DDT_STATUS_BAD_TREE_LEN 16 /* tree_len[b] outside [0, num_nodes]: clamped */
 #define DDT_STATUS_BAD_NODE 32     /* a node_idx entry outside [0, num_nodes) other than -1: left out */
 #define DDT_STATUS_BAD_BLOCK 64    /* a block_idx entry that is no block of the prefix, other than -1: left out */
+#define DDT_STATUS_BAD_POSITION 128 /* ddtree_kv8_write: a position outside the rotation table: row not written */
+#define DDT_STATUS_BAD_TOKEN 256   /* ddtree_accept: a drafted token outside [0, vocab): the node is left out */
+#define DDT_STATUS_BAD_LOGITS 512  /* ddtree_accept: no logit of the last accepted node is a number: next token -1 */
 
 /*
  * Sizes of one call.  Fixed by the library: D_qk = 576, D_v = 512.
@@ -429,6 +433,122 @@ DDT_API int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, const 
                                       const int32_t* tree_slot_idx, const int32_t* block_idx, int32_t block,
                                       int32_t topk, float sm_scale, void* out, float* lse, const ddt_dims* dims,
                                       void* workspace, size_t workspace_bytes, ddt_stream_t stream);
+
+/*
+ * The latent cache in 8 bits: half the memory and half the bytes of a bf16 pool.
+ *   kv8_pool   [N, 640] bytes: a slot's 512 latent values in e4m3, then its 64 rope
+ *              values in bf16, all divided by the slot's scale
+ *   kv8_scale  fp32 [N]
+ * so that a slot stands for the row scale * (latent, rope).
+ *
+ * ddtree_kv8_write puts rows into their slots.  With (c, r) the 512 latent and 64
+ * rope values of a row, all in fp32 and each value rounded once:
+ *   c' = c / sqrt(mean(c^2) + eps) * norm_weight   if norm_weight is given, else c
+ *   r' = r with its 32 pairs turned by the position's angles, if rotation is given:
+ *        (x, y) -> (x cos - y sin, y cos + x sin), a pair being (2 i, 2 i + 1) where
+ *        interleaved is nonzero, else (i, i + 32)
+ *   scale = the least power of two with max |c'| <= 448 scale, at least 2^-60, and
+ *        large enough for |r'| < 2^121 scale
+ * A row that is not finite gets a scale of NaN and zeros.
+ *   rows        bf16, row i at rows + i * row_stride (elements, a multiple of 8 and
+ *               >= 576): the latent values, then the rope values
+ *   slots       int32 [n] device, -1 = not written; others outside [0, N) are not
+ *               written and set DDT_STATUS_BAD_SLOT.  No slot may be listed twice
+ *               (it would hold a mixture of its rows; the call does not check it).
+ *   norm_weight bf16 [512] or NULL; eps in [1e-12, 1], not looked at without it
+ *   rotation    fp32 [positions, 64] or NULL: the 32 cosines of a position, then its
+ *               32 sines
+ *   position    int32 [n] device (with rotation), each in [0, positions); a row with
+ *               another one is not written and sets DDT_STATUS_BAD_POSITION
+ * Slots that are not listed keep what they hold.  The pool and the scales must not
+ * overlap the rows, the slots or each other (DDT_ERR_ALIAS).  workspace >= 256 bytes.
+ *
+ * ddtree_kv8_read writes the rows that listed slots stand for, rounded to bf16 (exact
+ * for the scales that ddtree_kv8_write makes, above bf16's subnormals), in the order
+ * of the list; any slot may be listed, any number of times:
+ *   rows        bf16, row i at rows + i * row_stride (as above); -1 gives a row of
+ *               zeros, another value outside [0, N) too, and sets DDT_STATUS_BAD_SLOT
+ * n <= 2^31.  A slot that was not finite reads as NaN.
+ */
+DDT_API int ddtree_kv8_write(const void* rows, int64_t row_stride, const int32_t* slots, int64_t n,
+                             const void* norm_weight, float eps, const float* rotation, const int32_t* position,
+                             int32_t positions, int32_t interleaved, void* kv8_pool, float* kv8_scale,
+                             int64_t pool_slots, void* workspace, ddt_stream_t stream);
+DDT_API int ddtree_kv8_read(const void* kv8_pool, const float* kv8_scale, const int32_t* slots, int64_t n, void* rows,
+                            int64_t row_stride, int64_t pool_slots, void* workspace, ddt_stream_t stream);
+
+/*
+ * ddtree_verify_attn_kv8: verify attention over the 8-bit cache, to the same keys as
+ * ddtree_verify_attn (with tree_len, as ddtree_verify_attn_ragged), their rows and the
+ * tree's rows being those that the slots stand for.
+ *   tree_len   int32 [B] device, or NULL: every request has T nodes
+ *   out        bf16 [B, T, H, 512] (the operand type of the product that follows)
+ *   lse        fp32 [B, T, H]
+ * Any positive finite scale will do; a key with another one (NaN) gives NaN to the
+ * nodes that see it, and to no others, as long as the bytes of a slot are finite values
+ * (those that ddtree_kv8_write stores are).  A query row that is not finite gives NaN
+ * to its own output.  Scores and sums are fp32; a query's values enter with bf16's 8
+ * bits down to 2^-11 of the row's largest latent value and in steps of 2^-18 of it below;
+ * a softmax weight enters the second product with 8 bits (as two 8-bit parts), at most 2^-8
+ * off; out is rounded to bf16 once.  Results are the same bits on every run, and do
+ * not depend on the slots' order.
+ * dims as in ddtree_verify_attn, max_prefix_len up to 2^30; prefix_len_sum steers the
+ * division of the work and the workspace's size.
+ * workspace >= ddtree_verify_kv8_workspace_bytes(dims), which needs a current CUDA
+ * device.  Calls, and replays of captured ones, that share a workspace must not overlap.
+ */
+DDT_API size_t ddtree_verify_kv8_workspace_bytes(const ddt_dims* dims);
+DDT_API int ddtree_verify_attn_kv8(const void* q, const void* kv8_pool, const float* kv8_scale, const int32_t* slot_idx,
+                                   const int32_t* prefix_len, const int32_t* tree_parent, const int32_t* tree_slot_idx,
+                                   const int32_t* tree_len, float sm_scale, void* out, float* lse, const ddt_dims* dims,
+                                   void* workspace, size_t workspace_bytes, ddt_stream_t stream);
+
+/*
+ * ddtree_accept: which drafted tokens of a tree stand, and the token after them, so
+ * that what is generated follows the target's probabilities exactly.  Node i holds
+ * the drafted token tokens[b][i] (node 0's, the root's, is not looked at: it stands
+ * already), and logits[b][i] are the target's for the token that follows node i.
+ *   p_i = softmax(logits[b][i] / temperature[b])
+ * From the root on, a node's children are tried in node order.  With w what is left of
+ * the node's p and S its sum (1 at first), child c with token x is accepted if
+ *   uniform[b][c] * S * q(x) < w(x)
+ * and the walk goes on from it; else
+ *   without draft_prob (tokens that were picked, such as the drafter's best): q = 1,
+ *     and w loses x (a token that an earlier sibling had has w = 0);
+ *   with draft_prob (tokens drawn independently from q = draft_prob[b][node]):
+ *     w becomes max(w - S q, 0).
+ * (A refusal that would leave nothing changes nothing.)  At the node where no child
+ * is accepted the next token is the first x with w(0) + .. + w(x) > uniform[b][0] * S.
+ *   logits       [B, T] rows of vocab values, bf16 or (logits_fp32 nonzero) fp32, row
+ *                b * T + i at logits + (b * T + i) * logit_stride (elements, >= vocab,
+ *                no alignment beyond the element's); NaN counts as -inf, +inf as the
+ *                largest finite number
+ *   draft_prob   fp32, rows like the logits' with draft_stride; or NULL
+ *   tokens       int32 [B, T]; a node with a token outside [0, vocab) is left out, with
+ *                all below it, and sets DDT_STATUS_BAD_TOKEN
+ *   tree_parent  int32 [B, T], as in ddtree_verify_attn; a node with a bad parent is
+ *                left out too (DDT_STATUS_BAD_PARENT)
+ *   tree_len     int32 [B] active nodes, or NULL
+ *   uniform      fp32 [B, T] in [0, 1): of each child's trial, and at 0 of the next
+ *                token's draw (values outside are clamped, NaN counts as 0)
+ *   temperature  fp32 [B]; not above 0 (or NaN): greedy, p on the largest logit, the
+ *                lowest token among equals
+ *   path         int32 [B, T]: the root and the accepted nodes in order, then -1
+ *                (ddtree_kv_weight's node_idx)
+ *   path_len     int32 [B]: how many, the root included; 0 for a request without nodes
+ *   next_token   int32 [B]; -1 for a request without nodes, or if no logit of the
+ *                path's last node is a number (DDT_STATUS_BAD_LOGITS)
+ * Weights are whole multiples of 2^-43 of the node's largest, so sums do not depend on
+ * their order.  vocab <= 2^20.  dims gives batch and num_nodes.  Outputs must not
+ * overlap inputs or one another (DDT_ERR_ALIAS).
+ * workspace >= ddtree_accept_workspace_bytes(dims, vocab).
+ */
+DDT_API size_t ddtree_accept_workspace_bytes(const ddt_dims* dims, int32_t vocab);
+DDT_API int ddtree_accept(const void* logits, int32_t logits_fp32, int64_t logit_stride, int32_t vocab,
+                          const float* draft_prob, int64_t draft_stride, const int32_t* tokens,
+                          const int32_t* tree_parent, const int32_t* tree_len, const float* uniform,
+                          const float* temperature, int32_t* path, int32_t* path_len, int32_t* next_token,
+                          const ddt_dims* dims, void* workspace, size_t workspace_bytes, ddt_stream_t stream);
 
 /* Waits for `stream`, then copies the status word of the last call that used
  * `workspace` to *host_status.  Returns DDT_OK or DDT_ERR_*.  The kernels write

@@ -11,6 +11,7 @@
 #include "cache_ops.cuh"
 #include "host.cuh"
 #include "kernels.cuh"
+#include "kv8.cuh"
 #include "schedule.cuh"
 
 namespace ddt {
@@ -48,7 +49,7 @@ int device_info(DeviceInfo* out) {
       d.ok = configure_prefix() == cudaSuccess && configure_tail_merge() == cudaSuccess;
       d.cache_ok = configure_scores() == cudaSuccess && configure_evict() == cudaSuccess &&
                    configure_topk() == cudaSuccess && configure_block_attn(&d.clusters) == cudaSuccess &&
-                   configure_summary() == cudaSuccess;
+                   configure_summary() == cudaSuccess && configure_kv8_attn() == cudaSuccess;
 #ifdef DDT_TEST_HOOKS
       if (g_test_fail_cache_setup) d.cache_ok = false;
 #endif
@@ -206,6 +207,17 @@ bool encode_pool_map(CUtensorMap* m, const void* pool, int64_t rows, uint32_t bo
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides, box, elem_strides,
             CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_kv8_map(CUtensorMap* m, const void* pool, int64_t rows) {
+  const EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {kKv8Row, static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {kKv8Row};
+  const cuuint32_t box[2] = {128, 1}, elem_strides[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides, box, elem_strides,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -26,5 +26,7 @@ inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
 // Rows of 576 bf16 values as a 2-D tensor, box of box_cols columns (64: 128-byte
 // swizzle, 32: 64-byte) x box_rows rows; rows past the tensor read as zero.
 bool encode_pool_map(CUtensorMap* m, const void* pool, int64_t rows, uint32_t box_cols, uint32_t box_rows);
+// Rows of 640 bytes, box of 128 bytes x one row, 128-byte swizzle.
+bool encode_kv8_map(CUtensorMap* m, const void* pool, int64_t rows);
 
 }  // namespace ddt

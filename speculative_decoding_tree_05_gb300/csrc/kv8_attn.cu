@@ -1,0 +1,770 @@
+// kv8_attn.cu -- verify attention over the 8-bit latent cache.
+//
+// A key is 512 latent values k in e4m3 and 64 rope values r in bf16, both to be
+// multiplied by the slot's scale s. The scale leaves both products:
+//   score(i, j) = s_j (q_i . (k_j, r_j)),   o_i = sum over j of (p_ij s_j) k_j / sum of p_ij
+// so the tensor core reads the cache's bytes as they are and nothing is dequantised.
+// Per row i a running reference r_i follows the largest t_ij = log2(p_ij s_j); the
+// weights that enter the second product are 2^(t_ij - r_i), and the sum of p takes
+// them divided by s_j, both in fp32 until they are cut into parts.
+//
+// Operands of 8 bits (fp32 accumulation, which is exact to fp32: 3e-8 of the result):
+//   q   = (hi + lo) 2^e, e4m3 both, e of the row: bf16's 8 bits, for values down to
+//         2^-11 of the row's largest; below that in steps of 2^-18 of it
+//   p s = hi + lo, e4m3 and e5m2: 4 bits, and 3 of what they leave, halves to even: at
+//         most 2^-8 off, as bf16 is, and less on average (e5m2 reaches further down than
+//         e4m3 where the weights of a long cache are small)
+//
+// As in block attention, keys and value dims are the M side and rows the N side:
+//   S^T[64 keys][rows]  = K . Q^T          2 x 16 MMAs M64 x N64 x K32 (8 bit) and 4 of K16 (rope)
+//   O^T[512 dims][rows] += V^T . P^T       2 x 4 x 2 MMAs M128 x N x K32 (V^T: the same bytes
+//                                          read MN-major)
+// O^T takes 256 TMEM columns, so one CTA holds the whole output. By themselves the MMAs of
+// a tile take 1790 cycles with 64 rows, 1400 with 16.
+//
+// Per CTA (576 threads), one unit = (up to 64 (node, head) rows of a request, a share of its tiles):
+//   warp 0       TMEM; one lane issues S(t), dim group by dim group as stage t lands
+//   warps 1-8    softmax: 16 keys x 32 rows each, in the 16x256b shape
+//   warp 9       one lane issues P.V(t) when P(t) is written
+//   warps 10-17  gather 64 keys per stage of 40 KB, three stages of four dim groups, each
+//                refilled as soon as its part of P.V is done: warps 10-13 two dim groups
+//                (two of five 128-byte pieces of a row) by 16-byte cp.async, warps 14-17
+//                the others by TMA gather4, at the same time
+// A request's keys are its prefix and, behind it, all its tree rows, each with the rows
+// that see it. The tiles of the whole batch are cut into equal shares, whatever the
+// lengths; a request has its share of them, in equal units. One unit writes bf16 and the
+// log-sum-exp at once, else each writes its normalised O and the merge kernel joins them.
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <climits>
+#include <type_traits>
+#include "kv8.cuh"
+#include "ptx.cuh"
+
+namespace ddt {
+namespace {
+
+constexpr int kThreads = 576;
+constexpr int kSoftmax = 256;
+constexpr int kCopiers = 128;                       // threads that gather the copied groups
+constexpr int kCopied = 2;                          // dim groups gathered by cp.async
+constexpr int kGroups = 4;                          // dims {0-127}, {128-255}, {256-383}, {384-511 and rope}
+constexpr int kKeys = kKv8Keys;
+constexpr int kRows = kKv8Rows;
+constexpr int kStages = 3;
+constexpr int kChunk = kKeys * 128;                 // 128 bytes of 64 keys: 8 KB
+constexpr int kStageBytes = 5 * kChunk;             // 40960
+constexpr int kOffQ = kStages * kStageBytes;        // hi: 4 chunks, lo: 4, rope: 1
+constexpr int kOffP = kOffQ + 9 * kChunk;           // [2 buffers][2 parts][64 keys][64 rows]
+constexpr int kPart = kKeys * kRows;                // 4096
+constexpr int kOffMask = kOffP + 4 * kPart;         // [stages][64] row masks of the stage's keys
+constexpr int kOffKey = kOffMask + kStages * kKeys * 8;   // [stages][64] (s, log2 s, 1 / s, -)
+constexpr int kOffMax = kOffKey + kStages * kKeys * 16;   // [64] running reference
+constexpr int kOffAlpha = kOffMax + kRows * 4;      // [64] rescale factors, later 1 / row sums
+constexpr int kOffQs = kOffAlpha + kRows * 4;       // [64] the rows' factors of a score
+constexpr int kOffTree = kOffQs + kRows * 4;        // [128] row masks of the tree rows
+constexpr int kOffSlot = kOffTree + kMaxNodes * 8;  // [128] their slots
+constexpr int kOffPar = kOffSlot + kMaxNodes * 4;   // [128] their parents
+constexpr int kOffBar = kOffPar + kMaxNodes * 4;
+constexpr int kSmem = kOffBar + 512 + 1024;
+static_assert(kSmem <= 232448, "one CTA's shared memory");
+constexpr uint32_t kColS = 256;                     // O^T [0, 256), S buffers 2 x 64
+constexpr float kUnset = -1e30f;                    // running reference of a row that has seen no key
+// Weights are 2^(t - r + kLift) and r is raised when one would exceed 2^(kLift + kSlack) = 256
+// (e4m3 ends at 448).
+constexpr float kLift = 4.f, kSlack = 4.f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct Shared {
+  uint64_t k_full[kStages][kGroups];
+  uint64_t k_empty[kStages][kGroups];  // this group's part of the tile's P.V is done (and those before it)
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_ready[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int fail[2];  // softmax: a wait of tile t ran out, by parity of t
+  int flags;
+};
+static_assert(sizeof(Shared) <= 512, "barrier block");
+
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// a |= m in shared memory, by halves (32-bit atomics need no loop)
+__device__ __forceinline__ void or_mask(uint64_t* a, uint64_t m) {
+  unsigned* half = reinterpret_cast<unsigned*>(a);
+  const unsigned lo = static_cast<unsigned>(m), hi = static_cast<unsigned>(m >> 32);
+  if (lo) atomicOr(half, lo);
+  if (hi) atomicOr(half + 1, hi);
+}
+
+__device__ __forceinline__ int tiles_of(const Kv8AttnParams& p, int b) {
+  const int nodes = kv8_nodes(p.tree_len, b, p.nodes);
+  return nodes == 0 ? 0 : (kv8_len(p.prefix_len, b, p.max_prefix_len) + nodes + kKeys - 1) / kKeys;
+}
+
+// Unit u of the batch: which request, which of its units. The requests' tiles make K in
+// all, a share is C = ceil(K / shares) of them, and a request of n tiles has ceil(n / C)
+// units of equal size. Called by whole warps; b < 0: there is no such unit.
+struct Unit {
+  int b, k, count, first;
+};
+__device__ __forceinline__ Unit find_unit(const Kv8AttnParams& p, int u, int lane) {
+  Unit r;
+  if (p.shares == 0) {
+    r.b = kv8_nodes(p.tree_len, u, p.nodes) > 0 ? u : -1;
+    r.k = 0;
+    r.count = 1;
+    r.first = u;
+    return r;
+  }
+  long long sum = 0;
+  for (int i = lane; i < p.batch; i += 32) sum += tiles_of(p, i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int share = static_cast<int>(min((sum + p.shares - 1) / p.shares, 1ll << 30));
+  int base = 0;
+  r.b = -1;
+  for (int i0 = 0; i0 < p.batch; i0 += 32) {
+    const int n = i0 + lane < p.batch ? tiles_of(p, i0 + lane) : 0;
+    const int c = n == 0 ? 0 : (n + share - 1) / share;
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int lo = base + incl - c;
+    const uint32_t vote = __ballot_sync(0xffffffffu, u >= lo && u < lo + c);
+    if (vote != 0) {
+      const int src = __ffs(vote) - 1;
+      r.b = i0 + src;
+      r.first = __shfl_sync(0xffffffffu, lo, src);
+      r.count = __shfl_sync(0xffffffffu, c, src);
+      r.k = u - r.first;
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_constant__ Kv8AttnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Shared& sh = *reinterpret_cast<Shared*>(smem + kOffBar);
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = &sh.abort;
+  const int g = blockIdx.x, unit = blockIdx.y;
+  grid_dep_launch();  // the merge kernel
+  const Unit un = find_unit(p, unit, lane);
+  int32_t* my_flags = p.flags + static_cast<int64_t>(unit) * p.groups + g;
+  const int nodes = un.b < 0 ? 0 : kv8_nodes(p.tree_len, un.b, p.nodes);  // active ones
+  int row0, rows;  // of the group, within the request
+  if (p.heads <= kRows) {
+    row0 = g * p.group_nodes * p.heads;
+    rows = min(p.group_nodes, nodes - g * p.group_nodes) * p.heads;
+  } else {
+    const int slices = (p.heads + kRows - 1) / kRows, t = g / slices, sl = g - t * slices;
+    row0 = t * p.heads + sl * kRows;
+    rows = t < nodes ? min(kRows, p.heads - sl * kRows) : 0;
+  }
+  if (un.b >= 0 && un.k == 0 && g == 0 && tid == 0) {
+    Kv8Piece piece;
+    piece.first = un.first;
+    piece.count = un.count;
+    p.pieces[un.b] = piece;
+  }
+  if (un.b < 0 || rows <= 0) {
+    if (tid == 0) *my_flags = 0;
+    return;
+  }
+  const int L = kv8_len(p.prefix_len, un.b, p.max_prefix_len);
+  const int keys = L + nodes;
+  const int tiles = (keys + kKeys - 1) / kKeys;
+  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * un.k / un.count);
+  const int n = static_cast<int>(static_cast<int64_t>(tiles) * (un.k + 1) / un.count) - t0;  // at least one
+  const int64_t trow0 = static_cast<int64_t>(un.b) * p.nodes * p.heads + row0;  // of q, out and lse
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i)
+      for (int x = 0; x < kGroups; ++x) {
+        // every copying thread's cp.async (group 0: and each of its warps' key factors and masks), or the gather
+        // warps' arrivals with their bytes
+        mbar_init(&sh.k_full[i][x], x < kCopied ? kCopiers + (x == 0 ? 4 : 0) : 4);
+        mbar_init(&sh.k_empty[i][x], 1);
+      }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_free[i], kSoftmax / 32);
+      mbar_init(&sh.p_ready[i], kSoftmax / 32);
+    }
+    mbar_init(&sh.drain, 2);
+    sh.abort = 0;
+    sh.fail[0] = sh.fail[1] = 0;
+    sh.flags = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&sh.tmem_base, 512);
+    tmem_relinquish();
+  }
+  float* mx = reinterpret_cast<float*>(smem + kOffMax);
+  if (tid < kRows) mx[tid] = kUnset;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  bool ok = true;
+
+  if (warp < 10) {
+    // ------------------------------------------------------------------ the group's query rows, in two 8-bit parts
+    const uint16_t* q = p.q + trow0 * kDqk;
+    float* qs = reinterpret_cast<float*>(smem + kOffQs);
+    for (int r0 = warp; r0 < kRows; r0 += 40) {
+      uint4 a[4], b[4];
+      uint32_t c[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // four rows' loads at a time
+        const int r = r0 + 10 * k;
+        const uint16_t* src = q + static_cast<int64_t>(r < rows ? r : 0) * kDqk;
+        a[k] = __ldg(reinterpret_cast<const uint4*>(src) + lane);
+        b[k] = __ldg(reinterpret_cast<const uint4*>(src + 256) + lane);
+        c[k] = __ldg(reinterpret_cast<const uint32_t*>(src + kDv) + lane);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + 10 * k;
+        if (r >= kRows) break;
+        const uint32_t w[9] = {a[k].x, a[k].y, a[k].z, a[k].w, b[k].x, b[k].y, b[k].z, b[k].w, c[k]};
+        uint32_t top = 0, turned = 0;  // the largest magnitudes, latent and rope, as bf16 bits
+        bool fine = true;
+#pragma unroll
+        for (int i = 0; i < 9; ++i) {
+          const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+          fine = fine && lo < 0x7f80u && hi < 0x7f80u;
+          if (i < 8)
+            top = max(top, max(lo, hi));
+          else
+            turned = max(lo, hi);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        turned = __reduce_max_sync(0xffffffffu, turned);
+        fine = __all_sync(0xffffffffu, fine);
+        // the least power of two that brings the row within 448 = 1.75 2^8 (7 bits behind the exponent) and its rope
+        // values below 2^121
+        const int e = max(static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0),
+                          max(static_cast<int>(turned >> 7) - 127 - 120, kKv8MinExp));
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const bool live = r < rows && fine;
+        uint32_t hi4[4], lo4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h2[2], l2[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t v = w[2 * i + j];
+            const float x = __uint_as_float(v << 16) * inv, y = __uint_as_float(v & 0xffff0000u) * inv;
+            h2[j] = pack_e4m3x2(x, y);
+            float hx, hy;
+            unpack_e4m3x2(static_cast<uint16_t>(h2[j]), hx, hy);
+            l2[j] = pack_e4m3x2(x - hx, y - hy);  // (the differences are exact)
+          }
+          hi4[i] = live ? h2[0] | (h2[1] << 16) : 0u;
+          lo4[i] = live ? l2[0] | (l2[1] << 16) : 0u;
+        }
+        // dims 8 lane + {0..7} in chunk lane / 16, dims 256 + 8 lane + {0..7} two chunks further
+        const uint32_t at = (lane >> 4) * kChunk + r * 128 + (((((lane & 15) >> 1) ^ (r & 7)) << 4) | ((lane & 1) << 3));
+        uint8_t* hi = smem + kOffQ + at;
+        *reinterpret_cast<uint2*>(hi) = make_uint2(hi4[0], hi4[1]);
+        *reinterpret_cast<uint2*>(hi + 2 * kChunk) = make_uint2(hi4[2], hi4[3]);
+        *reinterpret_cast<uint2*>(hi + 4 * kChunk) = make_uint2(lo4[0], lo4[1]);
+        *reinterpret_cast<uint2*>(hi + 6 * kChunk) = make_uint2(lo4[2], lo4[3]);
+        const uint32_t rope = live ? pack_bf16x2(__uint_as_float(w[8] << 16) * inv, __uint_as_float(w[8] & 0xffff0000u) * inv) : 0u;
+        *reinterpret_cast<uint32_t*>(smem + kOffQ + 8 * kChunk + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2))) = rope;
+        // a row that is not finite gives NaN to its own scores alone
+        if (lane == 0) qs[r] = r >= rows ? 0.f : fine ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * p.scale_log2 : CUDART_NAN_F;
+      }
+    }
+    fence_proxy_async_smem();
+    bar_sync(3, 320);
+  }
+
+  if (warp == 0) {
+    if (elect_one()) {
+      // scores of all 64 columns (rows of zeros behind the group's): every column read out is defined
+      const uint32_t idesc8 = idesc_f8_f32(64, kRows, kE4m3, kE4m3, false, false), idesc = idesc_bf16_f32(64, kRows, false, false);
+      const uint64_t d_k = smem_desc(base, 16, 1024, kSwizzle128B);
+      const uint64_t d_q = smem_desc(base + kOffQ, 16, 1024, kSwizzle128B);
+      int st = 0, ph = 0;
+      for (int t = 0; ok && t < n; ++t) {
+        if (t >= 2 && !mbar_wait_abortable(&sh.s_free[t & 1], ((t >> 1) - 1) & 1, abort, false, __LINE__)) {
+          ok = false;
+          break;
+        }
+        const uint64_t k = desc_advance(d_k, st * kStageBytes);
+        const uint32_t d = tmem + kColS + (t & 1) * kRows;
+#pragma unroll
+        for (int x = 0; x < kGroups; ++x) {
+          if (!mbar_wait_abortable(&sh.k_full[st][x], ph, abort, false, __LINE__)) {
+            ok = false;
+            break;
+          }
+          if (x < kCopied) fence_proxy_async_smem();  // written by cp.async
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t a = desc_advance(k, x * kChunk + ks * 32);
+            mma_f8_ss(d, a, desc_advance(d_q, x * kChunk + ks * 32), idesc8, x + ks > 0 ? 1u : 0u);
+            mma_f8_ss(d, a, desc_advance(d_q, (4 + x) * kChunk + ks * 32), idesc8, 1u);
+          }
+          if (x == kGroups - 1) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)  // the rope dims
+              mma_ss(d, desc_advance(k, 4 * kChunk + ks * 32), desc_advance(d_q, 8 * kChunk + ks * 32), idesc, 1u);
+          }
+        }
+        if (ok) mma_commit(&sh.s_full[t & 1]);
+        if (++st == kStages) st = 0, ph ^= 1;
+      }
+      mma_commit(&sh.drain);
+      mbar_wait(&sh.drain, 0);
+    }
+  } else if (warp == 9) {
+    if (elect_one()) {
+      const uint32_t cols = (rows + 15) / 16 * 16;
+      const uint32_t idesc_hi = idesc_f8_f32(128, cols, kE4m3, kE4m3, true, true), idesc_lo = idesc_f8_f32(128, cols, kE4m3, kE5m2, true, true);
+      const uint64_t d_v = smem_desc(base, kChunk, 1024, kSwizzle128B);          // MN-major, 128 dims a chunk
+      const uint64_t d_p = smem_desc(base + kOffP, kPart, 512, kSwizzle64B);     // MN-major, 64 rows
+      int st = 0;
+      for (int t = 0; t < n; ++t) {
+        if (!mbar_wait_abortable(&sh.p_ready[t & 1], (t >> 1) & 1, abort, false, __LINE__)) {
+          ok = false;
+          break;
+        }
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t v = desc_advance(d_v, st * kStageBytes), hi = desc_advance(d_p, (t & 1) * 2 * kPart);
+        const uint32_t more = t > 0 ? 1u : 0u;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            const uint64_t a = desc_advance(v, mt * kChunk + ks * 4096);
+            mma_f8_ss(tmem + mt * kRows, a, desc_advance(hi, ks * 2048), idesc_hi, ks > 0 ? 1u : more);
+            mma_f8_ss(tmem + mt * kRows, a, desc_advance(hi, kPart + ks * 2048), idesc_lo, 1u);
+          }
+          mma_commit(&sh.k_empty[st][mt]);
+        }
+        if (++st == kStages) st = 0;
+      }
+      mma_commit(&sh.drain);
+      mbar_wait(&sh.drain, 0);
+    }
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------------ producers
+    const int32_t* slots = p.slot_idx + static_cast<int64_t>(un.b) * p.slot_stride;
+    uint64_t* tree_mask = reinterpret_cast<uint64_t*>(smem + kOffTree);
+    int* tree_slot = reinterpret_cast<int*>(smem + kOffSlot);
+    const uint64_t full = rows == 64 ? ~0ull : ((1ull << rows) - 1);
+    if ((t0 + n) * kKeys > L) {
+      // the tree rows, and which of the group's rows see each: a node's walk to the root sets its rows' bits in
+      // itself and every ancestor; a link that is no earlier node ends it, a slot outside the pool is left out
+      int* par = reinterpret_cast<int*>(smem + kOffPar);
+      const int i = tid - 320;
+      if (i < nodes) {
+        par[i] = __ldg(p.tree_parent + static_cast<int64_t>(un.b) * p.nodes + i);
+        tree_slot[i] = __ldg(p.tree_slot_idx + static_cast<int64_t>(un.b) * p.nodes + i);
+        tree_mask[i] = 0;
+      }
+      bar_sync(4, 256);
+      const int first = row0 / p.heads, last = (row0 + rows - 1) / p.heads;
+      if (i <= last - first) {
+        const int lo = max(0, (first + i) * p.heads - row0), hi = min(rows, (first + i + 1) * p.heads - row0);
+        const uint64_t mine = (hi == 64 ? ~0ull : ((1ull << hi) - 1)) & ~((1ull << lo) - 1);
+        int v = first + i, flags = 0;
+        for (int guard = 0; v >= 0 && guard < nodes; ++guard) {
+          const int slot = tree_slot[v], up = par[v];
+          if (slot >= 0 && slot < p.pool_slots)
+            or_mask(&tree_mask[v], mine);
+          else
+            flags |= kStatusBadSlot;
+          if (v == 0 ? up != -1 : (up < 0 || up >= v)) {
+            flags |= kStatusBadParent;
+            break;
+          }
+          v = up;
+        }
+        if (flags) atomicOr(&sh.flags, flags);
+      }
+      bar_sync(4, 256);
+    }
+    // key i of the request: its slot (-1: none, or no row sees it)
+    auto read_slot = [&](int t, int k) -> int {
+      const int i = (t0 + t) * kKeys + k;
+      if (t >= n || k >= kKeys || i >= keys) return -1;
+      if (i < L) {
+        const int s = __ldg(slots + i);
+        return s < 0 ? INT_MIN : s;  // (a bad slot is told from none)
+      }
+      return tree_mask[i - L] ? tree_slot[i - L] : -1;
+    };
+    auto in_pool = [&](int slot) { return slot >= 0 && slot < p.pool_slots; };
+    auto read_scale = [&](int slot) -> float { return in_pool(slot) ? __ldg(p.scale + slot) : 1.f; };
+    // 16-byte copies of kPieces consecutive pieces (8 a chunk) from chunk c0 on of 16 rows from row0 on; zeros for
+    // rows without a slot
+    auto copy_rows = [&](uint32_t sbase, int r0, int c0, auto pieces, int slot) {
+      constexpr int kPieces = decltype(pieces)::value, kStep = 32 / kPieces;
+      const int y = lane & (kPieces - 1), sub = lane / kPieces;
+      const uint32_t dst = sbase + (c0 + (y >> 3)) * kChunk + (r0 + sub) * 128;
+      const uint8_t* src = p.kv + c0 * 128 + y * 16;
+#pragma unroll
+      for (int i = 0; i < 16 / kStep; ++i) {
+        const int row = __shfl_sync(0xffffffffu, slot, i * kStep + sub);
+        const uint32_t at = ((y & 7) ^ ((i * kStep + sub) & 7)) << 4;
+        cp_async16(dst + i * kStep * 128 + at, row < 0 ? p.kv : src + static_cast<int64_t>(row) * kKv8Row, row < 0 ? 0u : 16u);
+      }
+    };
+    using P16 = std::integral_constant<int, 16>;
+    using P8 = std::integral_constant<int, 8>;
+    const bool copier = warp < 14;
+    const int r0 = 16 * (copier ? warp - 10 : warp - 14);  // the warp's first key of a tile, 16 of them
+    const int k = lane < 16 ? r0 + lane : kKeys;           // the lane's key
+    // A key's row takes two dependent reads, its slot and its scale, each a tile ahead of its use.
+    int slot_now = read_slot(0, k), slot_next = read_slot(1, k);
+    float scale_now = copier ? read_scale(slot_now) : 1.f;
+    int st = 0, ph = 0, done = 0;
+    auto wait_empty = [&](int t, int x) {
+      const bool w = t < kStages || mbar_wait_abortable(&sh.k_empty[st][x], ph ^ 1, abort, false, __LINE__);
+      return __all_sync(0xffffffffu, w) != 0;
+    };
+    for (int t = 0; ok && t < n; ++t) {
+      const bool good = in_pool(slot_now);
+      if (!good && slot_now != -1) atomicOr(&sh.flags, kStatusBadSlot);
+      const int slot = good ? slot_now : -1;
+      const float scale = scale_now;
+      const int i = (t0 + t) * kKeys + k;
+      slot_now = slot_next;
+      if (copier) scale_now = read_scale(slot_now);
+      slot_next = read_slot(t + 2, k);
+      const uint32_t sbase = base + st * kStageBytes;
+      if (copier) {
+        if (!wait_empty(t, 0)) {
+          ok = false;
+          break;
+        }
+        if (lane < 16) {
+          reinterpret_cast<uint64_t*>(smem + kOffMask)[st * kKeys + k] = !good ? 0 : i < L ? full : tree_mask[i - L];
+          // a scale that is not positive and finite: NaN for the rows that see the key
+          const bool fine = scale > 0.f && scale < CUDART_INF_F;
+          reinterpret_cast<float4*>(smem + kOffKey)[st * kKeys + k] =
+              fine ? make_float4(scale, log2f(scale), 1.f / scale, 0.f) : make_float4(CUDART_NAN_F, 0.f, 1.f, 0.f);
+        }
+        copy_rows(sbase, r0, 0, P8(), slot);
+        cp_async_arrive_noinc(&sh.k_full[st][0]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.k_full[st][0]);  // releases the factors and masks
+        if (!wait_empty(t, 1)) {
+          ok = false;
+          break;
+        }
+        copy_rows(sbase, r0, 1, P8(), slot);
+        cp_async_arrive_noinc(&sh.k_full[st][1]);
+      } else {
+        if (!wait_empty(t, 2) || !wait_empty(t, 3)) {
+          ok = false;
+          break;
+        }
+        if (__all_sync(0xffffffffu, slot >= 0 || lane >= 16)) {
+          // lanes 0-11: four of the warp's keys, one of the three chunks
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.k_full[st][2], 16 * 128);
+            mbar_arrive_expect_tx(&sh.k_full[st][3], 16 * 256);
+          }
+          __syncwarp();
+          const int q = 4 * (lane & 3), c = 2 + (lane >> 2);
+          const int ra = __shfl_sync(0xffffffffu, slot, q), rb = __shfl_sync(0xffffffffu, slot, q + 1);
+          const int rc = __shfl_sync(0xffffffffu, slot, q + 2), rd = __shfl_sync(0xffffffffu, slot, q + 3);
+          if (lane < 12)
+            tma_gather4(sbase + c * kChunk + (r0 + q) * 128, &p.tmap, c * 128, ra, rb, rc, rd, &sh.k_full[st][min(c, 3)]);
+        } else {
+          // a key is masked (the end of the keys, a bad slot): zero-filled copies
+          copy_rows(sbase, r0, 2, P16(), slot);
+          copy_rows(sbase, r0, 4, P8(), slot);
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh.k_full[st][2]);
+            mbar_arrive(&sh.k_full[st][3]);
+          }
+        }
+      }
+      done = t + 1;
+      if (++st == kStages) st = 0, ph ^= 1;
+    }
+    cp_async_wait<0>();
+    if (!ok && !copier)  // after a give-up the gathers still in flight land before the CTA exits
+      for (int v = max(0, done - kStages); v < done; ++v) {
+        mbar_wait(&sh.k_full[v % kStages][2], (v / kStages) & 1, 1u << 16);
+        mbar_wait(&sh.k_full[v % kStages][3], (v / kStages) & 1, 1u << 16);
+      }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    const int quarter = warp & 3, half = (warp - 1) >> 2;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int r0 = quarter * 16 + (lane >> 2);     // keys r0 and r0 + 8 of the tile
+    const int c0 = 32 * half + 2 * (lane & 3);     // rows c0 + 8 i + {0, 1}, i < 4
+    const int id = half * 128 + quarter * 32 + lane;
+    float* alpha_sh = reinterpret_cast<float*>(smem + kOffAlpha);
+    const uint64_t* masks = reinterpret_cast<const uint64_t*>(smem + kOffMask);
+    const float4* factors = reinterpret_cast<const float4*>(smem + kOffKey);
+    const uint64_t full = rows == 64 ? ~0ull : ((1ull << rows) - 1);
+    float l[8], qs[8], m[8];  // sums, score factors and (lowered by kLift) references of this thread's rows
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      l[i] = 0.f;
+      qs[i] = reinterpret_cast<const float*>(smem + kOffQs)[c0 + 8 * (i >> 1) + (i & 1)];
+      m[i] = kUnset;
+    }
+    bool failed = false;  // a wait of this thread ran out: the warps leave together at the next barrier
+    auto wait_pv = [&](int t) {  // P.V(t) has read P, and O^T holds every tile up to t
+      if (!mbar_wait_abortable(&sh.k_empty[t % kStages][kGroups - 1], (t / kStages) & 1, abort, false, __LINE__)) failed = true;
+      tc_fence_after();
+    };
+    // column sums or maxima over the 16 keys of the warp, to scratch [4 quarters][64]
+    auto to_scratch = [&](float* scratch, const float (&v)[8], auto op) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float x = v[i];
+        x = op(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = op(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = op(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        if (lane < 4) scratch[quarter * kRows + c0 + 8 * (i >> 1) + (i & 1)] = x;
+      }
+    };
+    int st = 0, ph = 0;
+    for (int t = 0; t < n; ++t) {
+      uint8_t* pb = smem + kOffP + (t & 1) * 2 * kPart;
+      float* scratch = reinterpret_cast<float*>(pb);
+      if (!mbar_wait_abortable(&sh.k_full[st][0], ph, abort, false, __LINE__)) failed = true;
+      const uint64_t m0 = masks[st * kKeys + r0], m1 = masks[st * kKeys + r0 + 8];
+      const float4 f0 = factors[st * kKeys + r0], f1 = factors[st * kKeys + r0 + 8];
+      const bool part = __any_sync(0xffffffffu, m0 != full || m1 != full);
+      if (!mbar_wait_abortable(&sh.s_full[t & 1], (t >> 1) & 1, abort, false, __LINE__)) failed = true;
+      __syncwarp();
+      tc_fence_after();
+      float s[16];
+      // t of each score: log2 of its weight times its key's scale
+      auto scores = [&] {
+        tmem_ld_16x32(tmem + lane_off + kColS + (t & 1) * kRows + 32 * half, s);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int row = 2 * (i >> 2) + (i & 1);
+          s[i] = (i & 2) ? fmaf(s[i] * f1.x, qs[row], f1.y - m[row]) : fmaf(s[i] * f0.x, qs[row], f0.y - m[row]);
+        }
+        if (part) {
+          const uint32_t w0 = static_cast<uint32_t>(m0 >> c0), w1 = static_cast<uint32_t>(m1 >> c0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (!((w0 >> (8 * i + e)) & 1u)) s[4 * i + e] = -CUDART_INF_F;
+              if (!((w1 >> (8 * i + e)) & 1u)) s[4 * i + 2 + e] = -CUDART_INF_F;
+            }
+        }
+      };
+      scores();
+      float over = -CUDART_INF_F;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) over = fmax3(over, s[2 * i], s[2 * i + 1]);
+      if (failed) sh.fail[t & 1] = 1;
+      const bool raise = bar_red_or(1, kSoftmax, failed || over > kLift + kSlack);
+      if (raise && *const_cast<volatile int*>(&sh.fail[t & 1])) {
+        ok = false;
+        break;
+      }
+      if (raise) {
+        if (t > 0) wait_pv(t - 1);  // the scratch is the P buffer, and O^T is rescaled
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = 0.f;
+        scores();  // again, without a reference
+        float top8[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          top8[2 * i] = fmaxf(s[4 * i], s[4 * i + 2]);
+          top8[2 * i + 1] = fmaxf(s[4 * i + 1], s[4 * i + 3]);
+        }
+        to_scratch(scratch, top8, [](float a, float b) { return fmaxf(a, b); });
+        bar_sync(1, kSoftmax);
+        if (id < kRows) {  // one thread per row decides
+          const float old = mx[id];
+          const float top = fmaxf(fmaxf(scratch[id], scratch[kRows + id]), fmaxf(scratch[2 * kRows + id], scratch[3 * kRows + id]));
+          const bool up = top > old + kSlack;
+          alpha_sh[id] = up ? fast_exp2(old - top) : 1.f;
+          mx[id] = up ? top : old;
+        }
+        bar_sync(1, kSoftmax);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = c0 + 8 * (i >> 1) + (i & 1);
+          l[i] *= alpha_sh[row];
+          m[i] = mx[row] - kLift;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] -= m[2 * (i >> 2) + (i & 1)];
+        if (t > 0) {
+#pragma unroll 1
+          for (int k0 = 0; k0 < 16; ++k0) {  // this warp's half of the columns, 8 at a time
+            const int cc = 32 * half + (k0 & 3) * 8;
+            uint32_t o[8];
+            tmem_ld8(tmem + lane_off + (k0 >> 2) * kRows + cc, o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha_sh[cc + k]);
+            tmem_st8(tmem + lane_off + (k0 >> 2) * kRows + cc, o);
+          }
+        }
+        bar_sync(1, kSoftmax);  // scratch is read before P is written over it
+      }
+      tc_fence_before();
+      __syncwarp();
+#ifdef DDT_TEST_HOOKS
+      if (warp != 1 || t != p.test_keep_back)
+#endif
+      if (lane == 0) mbar_arrive(&sh.s_free[t & 1]);
+      uint32_t hi[4], lo[4];  // [i]: rows c0 + 8 i + {0, 1} of keys r0 (low half) and r0 + 8
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t h2[2], l2[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float x = fast_exp2(s[4 * i + 2 * h]), y = fast_exp2(s[4 * i + 2 * h + 1]);
+          const float inv = h ? f1.z : f0.z;
+          l[2 * i] = fmaf(x, inv, l[2 * i]);
+          l[2 * i + 1] = fmaf(y, inv, l[2 * i + 1]);
+          h2[h] = pack_e4m3x2(x, y);
+          float hx, hy;
+          unpack_e4m3x2(static_cast<uint16_t>(h2[h]), hx, hy);
+          l2[h] = pack_e5m2x2(x - hx, y - hy);  // (the differences are exact)
+        }
+        hi[i] = h2[0] | (h2[1] << 16);
+        lo[i] = l2[0] | (l2[1] << 16);
+      }
+      if (!raise && t > 1) wait_pv(t - 2);  // the buffer is free
+      // P^T: row (key) of 64 columns, 64-byte swizzle
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = r0 + 8 * h, col = c0 + 8 * i;
+          uint8_t* at = pb + key * 64 + ((((col >> 4) ^ ((key >> 1) & 3)) << 4) | (col & 15));
+          *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(hi[i] >> (16 * h));
+          *reinterpret_cast<uint16_t*>(at + kPart) = static_cast<uint16_t>(lo[i] >> (16 * h));
+        }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_ready[t & 1]);
+      if (++st == kStages) st = 0, ph ^= 1;
+    }
+    if (ok) {
+      wait_pv(n - 1);  // O^T is complete and the P buffers free
+      if (bar_red_or(1, kSoftmax, failed)) ok = false;
+    }
+    if (ok) {
+      float* scratch = reinterpret_cast<float*>(smem + kOffP);
+      to_scratch(scratch, l, [](float a, float b) { return a + b; });
+      bar_sync(1, kSoftmax);
+      if (id < kRows) {
+        const float sum = (scratch[id] + scratch[kRows + id]) + (scratch[2 * kRows + id] + scratch[3 * kRows + id]);
+        alpha_sh[id] = sum != 0.f ? 1.f / sum : 0.f;
+        const float lse = sum != 0.f ? (mx[id] - kLift + log2f(sum)) * kLn2 : -CUDART_INF_F;
+        if (id < rows) {
+          if (un.count == 1)
+            p.lse[trow0 + id] = lse;
+          else
+            p.lse_part[static_cast<int64_t>(unit) * p.nodes * p.heads + row0 + id] = lse;
+        }
+      }
+    }
+  }
+  // the softmax and gather warps write O: quarter of the lanes by warp, four warps a quarter
+  if (warp > 0) {
+    if (!bar_red_or(2, kThreads - 32, !ok) && warp != 9) {
+      tc_fence_after();
+      const float* inv_l = reinterpret_cast<const float*>(smem + kOffAlpha);
+      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      // lane = value dim: each row's store is 128 contiguous bytes per warp
+#pragma unroll 1
+      for (int k0 = warp < 9 ? (warp - 1) >> 2 : (warp - 2) >> 2; k0 < 32; k0 += 4) {
+        const int mt = k0 >> 3, cc = (k0 & 7) * 8;
+        if (cc >= rows) continue;
+        uint32_t o[8];
+        tmem_ld8(tmem + lane_off + mt * kRows + cc, o);
+        const int dim = mt * 128 + (warp & 3) * 32;
+        if (un.count == 1) {
+          // two rows a store: even lanes hold a pair of dims of the first, odd lanes of the second
+          uint16_t* dst = p.out + (trow0 + cc + (lane & 1)) * kDv + dim + (lane & ~1);
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            const float x = __uint_as_float(o[k]) * inv_l[cc + k], y = __uint_as_float(o[k + 1]) * inv_l[cc + k + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
+            if (cc + k + (lane & 1) < rows)
+              *reinterpret_cast<uint32_t*>(dst + k * kDv) = lane & 1 ? pack_bf16x2(got, y) : pack_bf16x2(x, got);
+          }
+        } else {
+          float* dst = p.o_part + (static_cast<int64_t>(unit) * p.nodes * p.heads + row0 + cc) * kDv + dim + lane;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (cc + k < rows) dst[k * kDv] = __uint_as_float(o[k]) * inv_l[cc + k];
+        }
+      }
+    }
+  }
+  if (!ok) {
+    *abort = 1;
+    atomicOr(&sh.flags, kStatusTimeout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0) *my_flags = sh.flags;
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+cudaError_t configure_kv8_attn() {
+  return cudaFuncSetAttribute(kv8_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+}
+
+cudaError_t launch_kv8_attn(const Kv8AttnParams& p, cudaStream_t stream) {
+  kv8_attn_kernel<<<dim3(p.groups, p.units), kThreads, kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace ddt

@@ -1,0 +1,341 @@
+// step_api.cu -- the extern "C" entry points of the 8-bit latent cache and of the check
+// of drafted tokens: argument checks, workspace layout, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+#include "../../include/ddtree.h"
+#include "accept.cuh"
+#include "host.cuh"
+#include "kv8.cuh"
+
+namespace ddt {
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 31;  // of one call
+
+bool clear_status(void* workspace, cudaStream_t s) {
+  return cudaMemsetAsync(workspace, 0, 4 * sizeof(int32_t), s) == cudaSuccess;
+}
+
+struct Kv8Layout {
+  int groups, group_nodes, shares, units;
+  size_t pieces_off, flags_off, lse_off, o_off, bytes;
+};
+
+// Costs in tiles of 64 keys: of a unit (its prologue, the pipeline's fill, its output),
+// of a merge, and of the partials, this many (unit, group)s a tile.
+constexpr int kUnitTiles = 5, kMergeTiles = 2, kPartialsPerTile = 48;
+
+// Groups of up to 64 (node, head) rows, and the shares of the batch's tiles: as many as
+// minimise waves * (tiles of a share + kUnitTiles) and the merge. Only numbers of shares
+// that just fill a number of waves can be best.
+int kv8_layout(const ddt_dims* d, int sm_count, Kv8Layout* w) {
+  const int rc = check_dims(d);
+  if (rc != DDT_OK) return rc;
+  if (d->max_prefix_len > (1 << 30)) return DDT_ERR_DIMS;
+  const int H = d->num_heads, T = d->num_nodes;
+  w->group_nodes = H <= kKv8Rows ? std::min(T, kKv8Rows / H) : 1;
+  w->groups = H <= kKv8Rows ? (T + w->group_nodes - 1) / w->group_nodes : T * ((H + kKv8Rows - 1) / kKv8Rows);
+  const int64_t B = d->batch, most = (int64_t(d->max_prefix_len) + T + kKv8Keys - 1) / kKv8Keys;
+  int64_t tiles = B * most;
+  if (d->prefix_len_sum > 0) tiles = std::min(tiles, (int64_t(d->prefix_len_sum) + B * T) / kKv8Keys + B);
+  w->shares = 0;
+  int64_t units = B;
+  if (B > 0 && B <= kKv8MaxShared) {
+    int64_t best = -1;
+    auto look = [&](int64_t shares) {
+      shares = std::max<int64_t>(1, std::min(shares, tiles));
+      const int64_t each = (tiles + shares - 1) / shares;
+      // (on average a request adds half a unit to the shares)
+      const int64_t n = std::max(B, std::min(shares + B - 1, shares + B / 2)) * w->groups;
+      const int64_t waves = (n + sm_count - 1) / sm_count;
+      const int64_t cost = waves * (std::min(each, most) + kUnitTiles) + (shares > 1 ? kMergeTiles + n / kPartialsPerTile : 0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        w->shares = static_cast<int>(shares);
+      }
+    };
+    look(1);
+    for (int64_t waves = 1; waves <= 12; ++waves) {
+      const int64_t n = waves * sm_count / w->groups;
+      look(n - (B - 1));
+      look(n - B / 2);
+    }
+    units = w->shares + B - 1;
+  }
+  // the grid's second dimension, and its CTAs in 31 bits
+  if (units > 65535 || units * w->groups > INT32_MAX) return DDT_ERR_DIMS;
+  w->units = static_cast<int>(units);
+  const size_t rows = size_t(T) * H, part = w->shares > 1 ? size_t(units) * rows : 0;
+  w->pieces_off = kStatusBytes;
+  w->flags_off = align_up(w->pieces_off + size_t(B) * sizeof(Kv8Piece), 256);
+  w->lse_off = align_up(w->flags_off + size_t(units) * w->groups * sizeof(int32_t), 256);
+  w->o_off = align_up(w->lse_off + part * sizeof(float), 256);
+  w->bytes = w->o_off + part * kDv * sizeof(float);
+  return DDT_OK;
+}
+
+// The least power of two of warps, up to 16, with which a row's units are read in one go.
+int merge_warps(const Kv8Layout& w, int batch) {
+  int n = 1;
+  const int units = w.units - batch + 1;  // of one request, at most
+  while (n < 16 && n * 4 < units) n *= 2;
+  return n;
+}
+
+struct AcceptLayout {
+  size_t max_off, arg_off, left_off, taken_off, accepted_off, bytes;
+};
+int accept_layout(const ddt_dims* d, int32_t vocab, AcceptLayout* w) {
+  if (!d) return DDT_ERR_NULL;
+  if (d->batch < 0 || d->batch > 65535 || d->num_nodes < 1 || d->num_nodes > kMaxNodes || vocab < 1 || vocab > (1 << 20))
+    return DDT_ERR_DIMS;
+  const size_t n = size_t(d->batch) * d->num_nodes;
+  w->left_off = kStatusBytes;
+  w->taken_off = align_up(w->left_off + n * 8, 256);
+  w->max_off = align_up(w->taken_off + n * 8, 256);
+  w->arg_off = align_up(w->max_off + n * 4, 256);
+  w->accepted_off = align_up(w->arg_off + n * 4, 256);
+  w->bytes = align_up(w->accepted_off + n * 4, 256);
+  return DDT_OK;
+}
+// CTAs of a row: as many as keep the SMs busy and leave each a few thousand values
+int row_cluster(int64_t rows, int vocab, int sm_count) {
+  int n = 8;
+  while (n > 1 && (rows * n > sm_count || vocab < n * 2048)) n /= 2;
+  return n;
+}
+
+}  // namespace
+}  // namespace ddt
+
+using namespace ddt;
+
+extern "C" int ddtree_kv8_write(const void* rows, int64_t row_stride, const int32_t* slots, int64_t n,
+                                const void* norm_weight, float eps, const float* rotation, const int32_t* position,
+                                int32_t positions, int32_t interleaved, void* kv8_pool, float* kv8_scale, int64_t pool_slots,
+                                void* workspace, ddt_stream_t stream) {
+  if (n < 0 || n > kMaxRows || row_stride < kDqk || row_stride % 8 != 0 || pool_slots < 1 || pool_slots > kMaxRows ||
+      (norm_weight && !(eps >= 1e-12f && eps <= 1.f)) || (rotation && positions < 1))
+    return DDT_ERR_DIMS;
+  if (n == 0) return DDT_OK;
+  if (!rows || !slots || !kv8_pool || !kv8_scale || !workspace || (rotation && !position)) return DDT_ERR_NULL;
+  if (!aligned(rows, 16) || !aligned(norm_weight, 16) || !aligned(kv8_pool, 16) || !aligned(workspace, 256) ||
+      !aligned(slots, 4) || !aligned(rotation, 4) || !aligned(position, 4) || !aligned(kv8_scale, 4))
+    return DDT_ERR_ALIGN;
+  const size_t pool = size_t(pool_slots) * kKv8Row, scales = size_t(pool_slots) * 4;
+  const size_t in = (size_t(n - 1) * row_stride + kDqk) * 2;
+  if (overlap(rows, in, kv8_pool, pool) || overlap(rows, in, kv8_scale, scales) || overlap(kv8_pool, pool, kv8_scale, scales) ||
+      overlap(slots, size_t(n) * 4, kv8_pool, pool) || overlap(slots, size_t(n) * 4, kv8_scale, scales))
+    return DDT_ERR_ALIAS;
+  int sms = 0;
+  const int rc = current_device(&sms);
+  if (rc != DDT_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!clear_status(workspace, s)) return DDT_ERR_LAUNCH;
+  Kv8WriteParams p = {};
+  p.rows = static_cast<const uint16_t*>(rows);
+  p.row_stride = row_stride;
+  p.slots = slots;
+  p.norm_weight = static_cast<const uint16_t*>(norm_weight);
+  p.eps = eps;
+  p.rotation = rotation;
+  p.position = position;
+  p.positions = positions;
+  p.pool = static_cast<uint8_t*>(kv8_pool);
+  p.scale = kv8_scale;
+  p.n = n;
+  p.pool_slots = pool_slots;
+  p.status = static_cast<int32_t*>(workspace);
+  return launch_kv8_write(p, interleaved != 0, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
+}
+
+extern "C" int ddtree_kv8_read(const void* kv8_pool, const float* kv8_scale, const int32_t* slots, int64_t n, void* rows,
+                               int64_t row_stride, int64_t pool_slots, void* workspace, ddt_stream_t stream) {
+  if (n < 0 || n > kMaxRows || row_stride < kDqk || row_stride % 8 != 0 || pool_slots < 1 || pool_slots > kMaxRows)
+    return DDT_ERR_DIMS;
+  if (n == 0) return DDT_OK;
+  if (!rows || !slots || !kv8_pool || !kv8_scale || !workspace) return DDT_ERR_NULL;
+  if (!aligned(rows, 16) || !aligned(kv8_pool, 16) || !aligned(workspace, 256) || !aligned(slots, 4) || !aligned(kv8_scale, 4))
+    return DDT_ERR_ALIGN;
+  const size_t out = (size_t(n - 1) * row_stride + kDqk) * 2;
+  if (overlap(rows, out, kv8_pool, size_t(pool_slots) * kKv8Row) || overlap(rows, out, kv8_scale, size_t(pool_slots) * 4) ||
+      overlap(rows, out, slots, size_t(n) * 4))
+    return DDT_ERR_ALIAS;
+  int sms = 0;
+  const int rc = current_device(&sms);
+  if (rc != DDT_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!clear_status(workspace, s)) return DDT_ERR_LAUNCH;
+  Kv8ReadParams p = {};
+  p.pool = static_cast<const uint8_t*>(kv8_pool);
+  p.scale = kv8_scale;
+  p.slots = slots;
+  p.rows = static_cast<uint16_t*>(rows);
+  p.row_stride = row_stride;
+  p.n = n;
+  p.pool_slots = pool_slots;
+  p.status = static_cast<int32_t*>(workspace);
+  return launch_kv8_read(p, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
+}
+
+extern "C" size_t ddtree_verify_kv8_workspace_bytes(const ddt_dims* dims) {
+  int sms = 0;
+  Kv8Layout w;
+  if (current_device(&sms) != DDT_OK || kv8_layout(dims, sms, &w) != DDT_OK) return 0;
+  return w.bytes;
+}
+
+extern "C" int ddtree_verify_attn_kv8(const void* q, const void* kv8_pool, const float* kv8_scale, const int32_t* slot_idx,
+                                      const int32_t* prefix_len, const int32_t* tree_parent, const int32_t* tree_slot_idx,
+                                      const int32_t* tree_len, float sm_scale, void* out, float* lse, const ddt_dims* dims,
+                                      void* workspace, size_t workspace_bytes, ddt_stream_t stream) {
+  Kv8Layout w;
+  int rc = kv8_layout(dims, 1, &w);  // the sizes, before any device query
+  if (rc != DDT_OK) return rc;
+  if (dims->batch == 0) return DDT_OK;
+  if (!q || !kv8_pool || !kv8_scale || !prefix_len || !tree_parent || !tree_slot_idx || !out || !lse || !workspace ||
+      (!slot_idx && dims->max_prefix_len > 0))
+    return DDT_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(kv8_pool, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(kv8_scale, 4) ||
+      !aligned(slot_idx, 4) || !aligned(prefix_len, 4) || !aligned(tree_parent, 4) || !aligned(tree_slot_idx, 4) ||
+      !aligned(tree_len, 4) || !aligned(lse, 4))
+    return DDT_ERR_ALIGN;
+  int sms = 0;
+  if ((rc = current_device(&sms)) != DDT_OK) return rc;
+  if ((rc = kv8_layout(dims, sms, &w)) != DDT_OK) return rc;
+  if (workspace_bytes < w.bytes) return DDT_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  Kv8AttnParams p = {};
+#ifdef DDT_TEST_HOOKS
+  p.test_keep_back = g_test_keep_back;
+#endif
+  if (!encode_kv8_map(&p.tmap, kv8_pool, dims->pool_slots)) return DDT_ERR_LAUNCH;
+  p.q = static_cast<const uint16_t*>(q);
+  p.kv = static_cast<const uint8_t*>(kv8_pool);
+  p.scale = kv8_scale;
+  p.slot_idx = slot_idx;
+  p.prefix_len = prefix_len;
+  p.tree_parent = tree_parent;
+  p.tree_slot_idx = tree_slot_idx;
+  p.tree_len = tree_len;
+  p.pool_slots = dims->pool_slots;
+  p.batch = dims->batch;
+  p.nodes = dims->num_nodes;
+  p.heads = dims->num_heads;
+  p.slot_stride = dims->slot_stride;
+  p.max_prefix_len = dims->max_prefix_len;
+  p.groups = w.groups;
+  p.group_nodes = w.group_nodes;
+  p.shares = w.shares;
+  p.units = w.units;
+  p.scale_log2 = static_cast<float>(sm_scale * 1.4426950408889634);
+  p.o_part = reinterpret_cast<float*>(ws + w.o_off);
+  p.lse_part = reinterpret_cast<float*>(ws + w.lse_off);
+  p.pieces = reinterpret_cast<Kv8Piece*>(ws + w.pieces_off);
+  p.flags = reinterpret_cast<int32_t*>(ws + w.flags_off);
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  Kv8MergeParams m = {};
+  m.o_part = p.o_part;
+  m.lse_part = p.lse_part;
+  m.pieces = p.pieces;
+  m.flags = p.flags;
+  m.prefix_len = prefix_len;
+  m.tree_len = tree_len;
+  m.out = p.out;
+  m.lse = lse;
+  m.batch = p.batch;
+  m.nodes = p.nodes;
+  m.heads = p.heads;
+  m.max_prefix_len = p.max_prefix_len;
+  m.units = w.units;
+  m.groups = w.groups;
+  m.warps = w.shares > 1 ? merge_warps(w, dims->batch) : 1;
+  m.status = reinterpret_cast<int32_t*>(ws);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (launch_kv8_attn(p, s) != cudaSuccess || launch_kv8_merge(m, s) != cudaSuccess) return DDT_ERR_LAUNCH;
+  return DDT_OK;
+}
+
+extern "C" size_t ddtree_accept_workspace_bytes(const ddt_dims* dims, int32_t vocab) {
+  AcceptLayout w;
+  return accept_layout(dims, vocab, &w) == DDT_OK ? w.bytes : 0;
+}
+
+extern "C" int ddtree_accept(const void* logits, int32_t logits_fp32, int64_t logit_stride, int32_t vocab,
+                             const float* draft_prob, int64_t draft_stride, const int32_t* tokens, const int32_t* tree_parent,
+                             const int32_t* tree_len, const float* uniform, const float* temperature, int32_t* path,
+                             int32_t* path_len, int32_t* next_token, const ddt_dims* dims, void* workspace,
+                             size_t workspace_bytes, ddt_stream_t stream) {
+  AcceptLayout w;
+  int rc = accept_layout(dims, vocab, &w);
+  if (rc != DDT_OK) return rc;
+  if (logit_stride < vocab || (draft_prob && draft_stride < vocab)) return DDT_ERR_DIMS;
+  if (dims->batch == 0) return DDT_OK;
+  if (!logits || !tokens || !tree_parent || !uniform || !temperature || !path || !path_len || !next_token || !workspace)
+    return DDT_ERR_NULL;
+  if (!aligned(logits, logits_fp32 ? 4 : 2) || !aligned(draft_prob, 4) || !aligned(tokens, 4) || !aligned(tree_parent, 4) ||
+      !aligned(tree_len, 4) || !aligned(uniform, 4) || !aligned(temperature, 4) || !aligned(path, 4) || !aligned(path_len, 4) ||
+      !aligned(next_token, 4) || !aligned(workspace, 256))
+    return DDT_ERR_ALIGN;
+  if (workspace_bytes < w.bytes) return DDT_ERR_WORKSPACE;
+  const int64_t rows = int64_t(dims->batch) * dims->num_nodes;
+  const size_t nodes = size_t(rows) * 4, reqs = size_t(dims->batch) * 4;
+  const struct { const void* p; size_t n; } in[] = {
+      {logits, (size_t(rows - 1) * logit_stride + vocab) * (logits_fp32 ? 4 : 2)},
+      {draft_prob, draft_prob ? (size_t(rows - 1) * draft_stride + vocab) * 4 : 0},
+      {tokens, nodes}, {tree_parent, nodes}, {tree_len, reqs}, {uniform, nodes}, {temperature, reqs}},
+      out[] = {{path, nodes}, {path_len, reqs}, {next_token, reqs}};
+  for (int i = 0; i < 3; ++i) {
+    for (const auto& x : in)
+      if (overlap(out[i].p, out[i].n, x.p, x.n)) return DDT_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return DDT_ERR_ALIAS;
+  }
+  int sms = 0;
+  if ((rc = current_device(&sms)) != DDT_OK) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  AcceptParams p = {};
+  p.logits = logits;
+  p.logit_stride = logit_stride;
+  p.draft_prob = draft_prob;
+  p.draft_stride = draft_stride;
+  p.tokens = tokens;
+  p.tree_parent = tree_parent;
+  p.tree_len = tree_len;
+  p.uniform = uniform;
+  p.temperature = temperature;
+  p.batch = dims->batch;
+  p.nodes = dims->num_nodes;
+  p.vocab = vocab;
+  p.row_cluster = row_cluster(rows, vocab, sms);
+  p.walk_cluster = row_cluster(dims->batch, vocab, sms);
+  p.row_max = reinterpret_cast<float*>(ws + w.max_off);
+  p.row_arg = reinterpret_cast<int32_t*>(ws + w.arg_off);
+  p.left = reinterpret_cast<unsigned long long*>(ws + w.left_off);
+  p.taken = reinterpret_cast<unsigned long long*>(ws + w.taken_off);
+  p.accepted = reinterpret_cast<int32_t*>(ws + w.accepted_off);
+  p.path = path;
+  p.path_len = path_len;
+  p.next_token = next_token;
+  p.status = reinterpret_cast<int32_t*>(ws);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launch_accept(p, !logits_fp32, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
+}
+
+// Host-side introspection of the schedule (not part of the public header; the CPU tests
+// use it, no device is needed): out = {groups of a request, shares, units}; *bytes: the workspace.
+extern "C" __attribute__((visibility("default"))) int ddtree_internal_kv8_plan(const ddt_dims* dims, int sm_count, int32_t* out,
+                                                                              int64_t* bytes) {
+  Kv8Layout w;
+  const int rc = kv8_layout(dims, sm_count, &w);
+  if (rc != DDT_OK) return rc;
+  out[0] = w.groups;
+  out[1] = w.shares;
+  out[2] = w.units;
+  *bytes = static_cast<int64_t>(w.bytes);
+  return DDT_OK;
+}

@@ -14,6 +14,7 @@ LIB_PATH = os.path.join(HERE, "lib", "libddtree.so")
 
 D_QK = 576
 D_V = 512
+KV8_ROW = 640
 
 DDT_OK = 0
 ERRORS = {-1: "DDT_ERR_NULL", -2: "DDT_ERR_DIMS", -3: "DDT_ERR_WORKSPACE", -4: "DDT_ERR_ALIGN",
@@ -25,6 +26,9 @@ STATUS_TIMEOUT = 8
 STATUS_BAD_TREE_LEN = 16
 STATUS_BAD_NODE = 32
 STATUS_BAD_BLOCK = 64
+STATUS_BAD_POSITION = 128
+STATUS_BAD_TOKEN = 256
+STATUS_BAD_LOGITS = 512
 
 EXPORTS = ("ddtree_verify_workspace_bytes", "ddtree_verify_attn", "ddtree_verify_attn_fused",
            "ddtree_verify_attn_ragged",
@@ -34,6 +38,8 @@ EXPORTS = ("ddtree_verify_workspace_bytes", "ddtree_verify_attn", "ddtree_verify
            "ddtree_kv_weight_workspace_bytes", "ddtree_kv_weight", "ddtree_kv_evict", "ddtree_block_summary",
            "ddtree_block_select_workspace_bytes", "ddtree_block_select",
            "ddtree_verify_blocks_workspace_bytes", "ddtree_verify_attn_blocks",
+           "ddtree_kv8_write", "ddtree_kv8_read", "ddtree_verify_kv8_workspace_bytes", "ddtree_verify_attn_kv8",
+           "ddtree_accept_workspace_bytes", "ddtree_accept",
            "ddtree_read_device_status", "ddtree_status_string")
 
 
@@ -108,6 +114,21 @@ def load(path: str):
         L.ddtree_verify_attn_blocks.restype = ctypes.c_int
         L.ddtree_verify_attn_blocks.argtypes = [vp, vp, i32p, i32p, i32p, i32p, i32p, i32, i32, f32, vp, vp, dims, vp,
                                                 size, vp]
+    if hasattr(L, "ddtree_kv8_write"):
+        i32, i64, f32, size, dims = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(Dims)
+        L.ddtree_kv8_write.restype = ctypes.c_int
+        L.ddtree_kv8_write.argtypes = [vp, i64, i32p, i64, vp, f32, vp, i32p, i32, i32, vp, vp, i64, vp, vp]
+        L.ddtree_kv8_read.restype = ctypes.c_int
+        L.ddtree_kv8_read.argtypes = [vp, vp, i32p, i64, vp, i64, i64, vp, vp]
+        L.ddtree_verify_kv8_workspace_bytes.restype = size
+        L.ddtree_verify_kv8_workspace_bytes.argtypes = [dims]
+        L.ddtree_verify_attn_kv8.restype = ctypes.c_int
+        L.ddtree_verify_attn_kv8.argtypes = [vp, vp, vp, i32p, i32p, i32p, i32p, i32p, f32, vp, vp, dims, vp, size, vp]
+        L.ddtree_accept_workspace_bytes.restype = size
+        L.ddtree_accept_workspace_bytes.argtypes = [dims, i32]
+        L.ddtree_accept.restype = ctypes.c_int
+        L.ddtree_accept.argtypes = [vp, i32, i64, i32, vp, i64, i32p, i32p, i32p, vp, vp, i32p, i32p, i32p, dims, vp, size,
+                                    vp]
     if hasattr(L, "ddtree_internal_plan"):
         L.ddtree_internal_plan.restype = ctypes.c_int
         L.ddtree_internal_plan.argtypes = [ctypes.POINTER(Dims), ctypes.c_int, ctypes.POINTER(ctypes.c_int32)]
@@ -554,6 +575,201 @@ class BlockVerifier:
                 _stream_of(self.device, stream))
         _keep(stream, out, lse, self.workspace)
         return out, lse
+
+    def status(self, stream=None) -> int:
+        return read_device_status(self.workspace, stream, library=self.lib)
+
+
+def kv8_pool(slots, device=None):
+    """An empty 8-bit latent cache: (pool uint8 [slots, 640], scale fp32 [slots]), every slot standing for zeros."""
+    import torch
+    d = _cuda_device(device)
+    return torch.zeros(slots, KV8_ROW, dtype=torch.uint8, device=d), torch.ones(slots, dtype=torch.float32, device=d)
+
+
+def _rows_of(rows, name, device, n):
+    """A row stride, in elements, of bf16 rows that may lie in a wider tensor."""
+    import torch
+    if (rows.dtype is not torch.bfloat16 or rows.dim() != 2 or rows.shape[0] != n or rows.shape[1] != D_QK
+            or rows.device != device or rows.stride(1) != 1 or (n > 1 and rows.stride(0) < D_QK)):
+        raise ValueError(f"{name} must be bfloat16 [{n}, {D_QK}] on {device} with consecutive values in a row, got "
+                         f"{rows.dtype} {tuple(rows.shape)} on {rows.device}, strides {tuple(rows.stride())}")
+    return rows.stride(0) if n > 1 else D_QK
+
+
+def _kv8_checks(pool, scale, slots):
+    import torch
+    device = _on_cuda(pool, "pool")
+    if pool.dim() != 2 or slots.dim() != 1:
+        raise ValueError("pool must be [slots, 640] and slots a list")
+    N, n = pool.shape[0], slots.shape[0]
+    _need(device, ("pool", pool, torch.uint8, (N, KV8_ROW)), ("scale", scale, torch.float32, (N,)),
+          ("slots", slots, torch.int32, (n,)))
+    return device, N, n
+
+
+def _status_words(workspace, device, stream):
+    import torch
+    if workspace is None:
+        return _make(stream, torch.empty, 256, dtype=torch.uint8, device=device)
+    _need(device, ("workspace", workspace, torch.uint8, workspace.shape))
+    if workspace.numel() < 256:
+        raise ValueError("workspace must hold 256 bytes")
+    return workspace
+
+
+def kv8_write(rows, slots, pool, scale, norm_weight=None, eps=1e-6, rotation=None, position=None, interleaved=False,
+              workspace=None, stream=None):
+    """Put bf16 rows [n, 576] into their slots of an 8-bit cache (ddtree_kv8_write); returns (pool, scale).
+
+    slots int32 [n], each slot at most once, -1 = skip the row.  With norm_weight (bf16 [512]) the latent values are
+    normalised first, with rotation (fp32 [positions, 64]: cosines, sines) and position (int32 [n]) the rope values
+    are rotated: pairs (2 i, 2 i + 1) if interleaved, else (i, i + 32).  rows may be a slice of a wider tensor.
+    """
+    import torch
+    device, N, n = _kv8_checks(pool, scale, slots)
+    stride = _rows_of(rows, "rows", device, n)
+    if norm_weight is not None:
+        _need(device, ("norm_weight", norm_weight, torch.bfloat16, (D_V,)))
+    positions = 0
+    if (rotation is None) != (position is None):
+        raise ValueError("rotation and position go together")
+    if rotation is not None:
+        if rotation.dim() != 2:
+            raise ValueError("rotation must be [positions, 64]")
+        positions = rotation.shape[0]
+        _need(device, ("rotation", rotation, torch.float32, (positions, 64)), ("position", position, torch.int32, (n,)))
+    workspace = _status_words(workspace, device, stream)
+    _run_on(device, lib().ddtree_kv8_write, "ddtree_kv8_write", rows.data_ptr(), stride, slots.data_ptr(), n,
+            _addr(norm_weight), eps, _addr(rotation), _addr(position), positions, int(bool(interleaved)), pool.data_ptr(),
+            scale.data_ptr(), N, workspace.data_ptr(), _stream_of(device, stream))
+    _keep(stream, workspace, pool, scale)
+    return pool, scale
+
+
+def kv8_read(pool, scale, slots, out=None, workspace=None, stream=None):
+    """The bf16 rows [n, 576] that listed slots of an 8-bit cache stand for (ddtree_kv8_read); -1 gives zeros."""
+    import torch
+    device, N, n = _kv8_checks(pool, scale, slots)
+    if out is None:
+        out = _make(stream, torch.empty, (n, D_QK), dtype=torch.bfloat16, device=device)
+    stride = _rows_of(out, "out", device, n)
+    workspace = _status_words(workspace, device, stream)
+    _run_on(device, lib().ddtree_kv8_read, "ddtree_kv8_read", pool.data_ptr(), scale.data_ptr(), slots.data_ptr(), n,
+            out.data_ptr(), stride, N, workspace.data_ptr(), _stream_of(device, stream))
+    _keep(stream, workspace, out)
+    return out
+
+
+class Kv8Verifier:
+    """Verify attention over the 8-bit cache (ddtree_verify_attn_kv8), with a workspace for one set of sizes.
+
+    Call with a verify call's tensors, the cache as (pool, scale) in place of kv_pool; tree_len int32 [B] for trees of
+    different sizes.  Returns (out bf16 [B, T, H, 512], lse fp32 [B, T, H]).
+    """
+
+    def __init__(self, batch, nodes, heads, pool_slots, slot_stride, max_prefix_len=None, device=None, prefix_len_sum=0,
+                 library=None):
+        import torch
+        self.lib = lib() if library is None else library
+        self.dims = make_dims(batch, nodes, heads, pool_slots, slot_stride,
+                              slot_stride if max_prefix_len is None else max_prefix_len, prefix_len_sum)
+        self.device = _cuda_device(device)
+        self.dims_ref = ctypes.byref(self.dims)
+        with torch.cuda.device(self.device):
+            n = int(self.lib.ddtree_verify_kv8_workspace_bytes(self.dims_ref))
+        if n == 0:
+            raise DDTError(-2, "ddtree_verify_kv8_workspace_bytes")
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def __call__(self, q, pool, scale, slot_idx, prefix_len, tree_parent, tree_slot_idx, sm_scale, tree_len=None,
+                 out=None, lse=None, stream=None):
+        import torch
+        d = self.dims
+        B, T, H = d.batch, d.num_nodes, d.num_heads
+        if out is None:
+            out = _make(stream, torch.empty, (B, T, H, D_V), dtype=torch.bfloat16, device=self.device)
+        if lse is None:
+            lse = _make(stream, torch.empty, (B, T, H), dtype=torch.float32, device=self.device)
+        _need(self.device, ("q", q, torch.bfloat16, (B, T, H, D_QK)),
+              ("pool", pool, torch.uint8, (d.pool_slots, KV8_ROW)), ("scale", scale, torch.float32, (d.pool_slots,)),
+              ("slot_idx", slot_idx, torch.int32, (B, d.slot_stride)), ("prefix_len", prefix_len, torch.int32, (B,)),
+              ("tree_parent", tree_parent, torch.int32, (B, T)), ("tree_slot_idx", tree_slot_idx, torch.int32, (B, T)),
+              ("out", out, torch.bfloat16, (B, T, H, D_V)), ("lse", lse, torch.float32, (B, T, H)))
+        if tree_len is not None:
+            _need(self.device, ("tree_len", tree_len, torch.int32, (B,)))
+        _run_on(self.device, self.lib.ddtree_verify_attn_kv8, "ddtree_verify_attn_kv8", q.data_ptr(), pool.data_ptr(),
+                scale.data_ptr(), slot_idx.data_ptr(), prefix_len.data_ptr(), tree_parent.data_ptr(),
+                tree_slot_idx.data_ptr(), _addr(tree_len), sm_scale, out.data_ptr(), lse.data_ptr(), self.dims_ref,
+                self.workspace.data_ptr(), self.workspace.numel(), _stream_of(self.device, stream))
+        _keep(stream, out, lse, self.workspace)
+        return out, lse
+
+    def status(self, stream=None) -> int:
+        return read_device_status(self.workspace, stream, library=self.lib)
+
+
+class TreeAcceptor:
+    """Which drafted tokens of a tree stand (ddtree_accept), with a workspace for one set of sizes.
+
+    Call with logits [B, T, vocab] (bf16 or fp32; rows may lie in a wider tensor, one stride for all), tokens and
+    tree_parent int32 [B, T], uniform fp32 [B, T] in [0, 1) and temperature fp32 [B] (0 = greedy); draft_prob fp32
+    [B, T, vocab] where the tokens were drawn from the drafter's distribution, tree_len int32 [B] for trees of
+    different sizes.  Returns (path int32 [B, T]: the root and the accepted nodes, then -1; path_len int32 [B];
+    next_token int32 [B]).
+    """
+
+    def __init__(self, batch, nodes, vocab, device=None, library=None):
+        import torch
+        self.lib = lib() if library is None else library
+        self.dims = make_dims(batch, nodes, 1, 1, 0, 0)
+        self.vocab = int(vocab)
+        self.device = _cuda_device(device)
+        self.dims_ref = ctypes.byref(self.dims)
+        n = int(self.lib.ddtree_accept_workspace_bytes(self.dims_ref, self.vocab))
+        if n == 0:
+            raise DDTError(-2, "ddtree_accept_workspace_bytes")
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def _stride(self, t, name, dtypes):
+        """The distance of consecutive nodes' rows, the same over requests."""
+        B, T = self.dims.batch, self.dims.num_nodes
+        if t.dtype not in dtypes or t.shape != (B, T, self.vocab) or t.device != self.device:
+            raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))} [{B}, {T}, {self.vocab}] on {self.device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        row = t.stride(1) if T > 1 else t.stride(0) if B > 1 else self.vocab
+        if ((self.vocab > 1 and t.stride(2) != 1) or (B > 1 and t.stride(0) != T * row)
+                or (B * T > 1 and row < self.vocab)):
+            raise ValueError(f"{name}'s rows must be consecutive values, at one distance over all nodes: strides "
+                             f"{tuple(t.stride())}")
+        return row
+
+    def __call__(self, logits, tokens, tree_parent, uniform, temperature, draft_prob=None, tree_len=None, path=None,
+                 path_len=None, next_token=None, stream=None):
+        import torch
+        d = self.dims
+        B, T = d.batch, d.num_nodes
+        if path is None:
+            path = _make(stream, torch.empty, (B, T), dtype=torch.int32, device=self.device)
+        if path_len is None:
+            path_len = _make(stream, torch.empty, (B,), dtype=torch.int32, device=self.device)
+        if next_token is None:
+            next_token = _make(stream, torch.empty, (B,), dtype=torch.int32, device=self.device)
+        stride = self._stride(logits, "logits", (torch.bfloat16, torch.float32))
+        draft_stride = 0 if draft_prob is None else self._stride(draft_prob, "draft_prob", (torch.float32,))
+        _need(self.device, ("tokens", tokens, torch.int32, (B, T)), ("tree_parent", tree_parent, torch.int32, (B, T)),
+              ("uniform", uniform, torch.float32, (B, T)), ("temperature", temperature, torch.float32, (B,)),
+              ("path", path, torch.int32, (B, T)), ("path_len", path_len, torch.int32, (B,)),
+              ("next_token", next_token, torch.int32, (B,)))
+        if tree_len is not None:
+            _need(self.device, ("tree_len", tree_len, torch.int32, (B,)))
+        _run_on(self.device, self.lib.ddtree_accept, "ddtree_accept", logits.data_ptr(),
+                int(logits.dtype is torch.float32), stride, self.vocab, _addr(draft_prob), draft_stride, tokens.data_ptr(),
+                tree_parent.data_ptr(), _addr(tree_len), uniform.data_ptr(), temperature.data_ptr(), path.data_ptr(),
+                path_len.data_ptr(), next_token.data_ptr(), self.dims_ref, self.workspace.data_ptr(),
+                self.workspace.numel(), _stream_of(self.device, stream))
+        _keep(stream, path, path_len, next_token, self.workspace)
+        return path, path_len, next_token
 
     def status(self, stream=None) -> int:
         return read_device_status(self.workspace, stream, library=self.lib)
