@@ -539,7 +539,7 @@ DDT_API int ddtree_verify_attn_kv8(const void* q, const void* kv8_pool, const fl
  *   next_token   int32 [B]; -1 for a request without nodes, or if no logit of the
  *                path's last node is a number (DDT_STATUS_BAD_LOGITS)
  * Weights are whole multiples of 2^-43 of the node's largest, so sums do not depend on
- * their order.  vocab <= 2^20.  dims gives batch and num_nodes.  Outputs must not
+ * their order.  vocab <= 2^18.  dims gives batch and num_nodes.  Outputs must not
  * overlap inputs or one another (DDT_ERR_ALIAS).
  * workspace >= ddtree_accept_workspace_bytes(dims, vocab).
  */

@@ -13,13 +13,13 @@
 // same tokens come out on any tiling, and a token on the border between two answers is
 // decided as 64-bit arithmetic decides it, but for one draw in 10^5 or so.
 //
-// Kernel 1, a cluster per node: the row's maximum, the sum of its weights, and for each
-// child whether it would be accepted if the walk came to its parent. Every row is read at
-// once, though the walk will visit few: which ones is known only step by step, and a step
-// (read, reduce, decide) takes longer than all rows together.
-// Kernel 2, a cluster per request: the walk over those answers (a node's children come
-// behind it, so one pass over the nodes), then the draw from what the last node has left:
-// a sum per warp, and the one warp whose range holds the token looks it up.
+// One cluster per request walks down the tree and reads only the rows that it visits,
+// each CTA its share of the vocabulary, which stays in shared memory (logits; with q the
+// weights and q) from the maximum to the draw. Each warp has a range of consecutive tokens
+// and its sum, so a draw is a prefix over CTAs and warps and one warp's look at its range.
+// Bound by the latency of a visit: a row's load, and the two sums over the cluster (its
+// maximum, its weights); a refused token that was drawn is one more. The children's rows are
+// on their way to L2 meanwhile.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <algorithm>
@@ -30,8 +30,9 @@ namespace ddt {
 namespace {
 
 constexpr int kAccThreads = 512, kAccWarps = kAccThreads / 32;
-constexpr int kOne = 43;         // weight 1 is 2^43; up to 2^20 of them fit in 64 bits
+constexpr int kOne = 43;         // weight 1 is 2^43; up to 2^18 of them fit in 64 bits
 constexpr int kUnroll = 8;       // loads in flight of a thread
+constexpr int kPrefetched = 4;   // children whose rows are sent for
 
 // 2^(62 - i / 64), i = 0 to 63
 __constant__ unsigned long long c_pow[64] = {
@@ -81,10 +82,10 @@ struct RowWeight {
     return weight_of(hi, fmaf(d, c_hi, -hi) + fmaf(d, c_lo, e * c_hi), pow_sh);
   }
 };
-__device__ __forceinline__ RowWeight row_weight(float max, int arg, float temperature) {
+__device__ __forceinline__ RowWeight row_weight(float temperature) {
   RowWeight r;
-  r.max = max;
-  r.only = temperature > 0.f ? -1 : arg;
+  r.max = 0.f;
+  r.only = -1;
   const double c = temperature > 0.f ? fmin(1.4426950408889634 / static_cast<double>(temperature), 1e30) : 0.0;
   r.c_hi = static_cast<float>(c);
   r.c_lo = static_cast<float>(c - static_cast<double>(r.c_hi));
@@ -110,6 +111,25 @@ __device__ __forceinline__ float tame(float l) { return l >= -3.4028235e38f ? fm
 // u in [0, 1), NaN as 0
 __device__ __forceinline__ float tame_uniform(float u) { return u > 0.f ? fminf(u, 0.99999994f) : 0.f; }
 
+// The order of logits as whole numbers, the lower index first among equals; and the logit again.
+__device__ __forceinline__ unsigned long long order_of(float l, int x) {
+  const uint32_t u = __float_as_uint(l);
+  const uint32_t key = l == 0.f ? 0x80000000u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return (static_cast<unsigned long long>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(x));
+}
+__device__ __forceinline__ float max_of(unsigned long long order) {
+  const uint32_t key = static_cast<uint32_t>(order >> 32);
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+}
+
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long other = __shfl_xor_sync(0xffffffffu, v, o);
+    v = other > v ? other : v;
+  }
+  return v;
+}
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -121,172 +141,22 @@ __device__ __forceinline__ unsigned long long remote_u64(const unsigned long lon
   return lo | (static_cast<unsigned long long>(hi) << 32);
 }
 
-// This CTA's share [lo, hi) of the vocabulary, of `size` CTAs.
-__device__ __forceinline__ void range_of(int vocab, int rank, int size, int* lo, int* hi) {
-  const int each = ((vocab + size - 1) / size + 31) / 32 * 32;
-  *lo = min(vocab, rank * each);
-  *hi = min(vocab, *lo + each);
-}
+// What the cluster exchanges: a CTA's part of a reduction. Two, used in turn: one is
+// written again when every CTA has passed the next reduction's barrier.
+struct Exchange {
+  unsigned long long slot[2];
+};
 
-// f(index, logit, q) over [lo, hi), by the threads first, first + step, ...
-template <typename T, typename F>
-__device__ __forceinline__ void each(const T* row, const float* q, int lo, int hi, int first, int step, F f) {
-  for (int i0 = lo + first; i0 < hi; i0 += kUnroll * step) {
-    float l[kUnroll], d[kUnroll];
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int i = i0 + k * step;
-      l[k] = i < hi ? logit(row + i) : -CUDART_INF_F;
-      d[k] = q && i < hi ? __ldg(q + i) : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k)
-      if (i0 + k * step < hi) f(i0 + k * step, tame(l[k]), d[k]);
-  }
-}
-
-// The sum over a cluster of one value per thread, to all threads. `slot`: two values of shared memory of its own.
-__device__ __forceinline__ unsigned long long cluster_sum(unsigned long long v, unsigned long long* warps, unsigned long long* slot,
-                                                          int size) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  v = warp_sum(v);
-  if (lane == 0) warps[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    v = warp_sum(lane < kAccWarps ? warps[lane] : 0);
-    if (lane == 0) *slot = v;
-  }
-  cluster_sync();
-  v = warp_sum(lane < size ? remote_u64(slot, lane) : 0);
-  return v;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kAccThreads) accept_rows_kernel(const __grid_constant__ AcceptParams p) {
+template <typename T, bool kDrawn>
+__global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_constant__ AcceptParams p) {
+  extern __shared__ unsigned long long dyn_sh[];  // kDrawn: weights, then q; else logits
   __shared__ unsigned long long pow_sh[64];
-  __shared__ unsigned long long warps_sh[2][kAccWarps];
-  __shared__ unsigned long long slot_sh[kMaxNodes + 2];  // of each pass; read by the cluster
-  __shared__ unsigned long long mult_sh[kMaxNodes];      // S of the steps that were taken
-  __shared__ int child_sh[kMaxNodes], n_child;
+  __shared__ unsigned long long warps_sh[2][kAccWarps], child_w[kMaxNodes];
+  __shared__ Exchange ex;
+  __shared__ float u_sh[kMaxNodes], child_q[kMaxNodes];
+  __shared__ int par_sh[kMaxNodes], tok_sh[kMaxNodes], path_sh[kMaxNodes], child_sh[kMaxNodes], n_child;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int size = p.row_cluster, rank = blockIdx.x % size;
-  const int64_t at = blockIdx.x / size;  // of the node
-  const int b = static_cast<int>(at / p.nodes), v = static_cast<int>(at - static_cast<int64_t>(b) * p.nodes);
-  grid_dep_launch();
-  if (blockIdx.x == 0 && tid == 0) *p.status = 0;  // (the second kernel reports)
-  const int nodes = p.tree_len ? min(max(__ldg(p.tree_len + b), 0), p.nodes) : p.nodes;
-  if (v >= nodes) return;  // the whole cluster
-  const T* row = static_cast<const T*>(p.logits) + at * p.logit_stride;
-  const float* q = p.draft_prob ? p.draft_prob + at * p.draft_stride : nullptr;
-  int lo, hi;
-  range_of(p.vocab, rank, size, &lo, &hi);
-  if (tid < 64) pow_sh[tid] = c_pow[tid];
-  if (warp == 0) {  // v's children that have a token, in node order
-    int n = 0;
-    for (int i0 = v + 1; i0 < nodes; i0 += 32) {
-      const int i = i0 + lane;
-      bool is = false;
-      if (i < nodes && __ldg(p.tree_parent + static_cast<int64_t>(b) * p.nodes + i) == v) {
-        const int x = __ldg(p.tokens + static_cast<int64_t>(b) * p.nodes + i);
-        is = x >= 0 && x < p.vocab;
-      }
-      const uint32_t vote = __ballot_sync(0xffffffffu, is);
-      if (is) child_sh[n + __popc(vote & ((1u << lane) - 1u))] = i;
-      n += __popc(vote);
-    }
-    if (lane == 0) n_child = n;
-  }
-  // the maximum, and where it is first: as one number (the order of the float's bits, then the lower index)
-  unsigned long long best = 0;
-  each(row, nullptr, lo, hi, tid, kAccThreads, [&](int i, float l, float) {
-    const uint32_t u = __float_as_uint(l);
-    const uint32_t key = l == 0.f ? 0x80000000u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    const unsigned long long k = (static_cast<unsigned long long>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(i));
-    best = k > best ? k : best;
-  });
-  auto warp_max = [](unsigned long long k) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long other = __shfl_xor_sync(0xffffffffu, k, o);
-      k = other > k ? other : k;
-    }
-    return k;
-  };
-  best = warp_max(best);
-  if (lane == 0) warps_sh[0][warp] = best;
-  __syncthreads();
-  if (warp == 0) {
-    best = warp_max(lane < kAccWarps ? warps_sh[0][lane] : 0);
-    if (lane == 0) slot_sh[kMaxNodes + 1] = best;
-  }
-  cluster_sync();
-  best = warp_max(lane < size ? remote_u64(&slot_sh[kMaxNodes + 1], lane) : 0);
-  const uint32_t key = static_cast<uint32_t>(best >> 32);
-  const float max = __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
-  const int arg = static_cast<int>(0xffffffffu - static_cast<uint32_t>(best));
-  const bool dead = !(max >= -3.4028235e38f);  // no logit is a number
-  const RowWeight w_of = row_weight(max, arg, __ldg(p.temperature + b));
-  unsigned long long S = 0;
-  if (!dead) each(row, nullptr, lo, hi, tid, kAccThreads, [&](int i, float l, float) { S += w_of(l, i, pow_sh); });
-  S = cluster_sum(S, warps_sh[1], &slot_sh[kMaxNodes], size);
-  const int n = n_child;
-  const int64_t node0 = static_cast<int64_t>(b) * p.nodes;
-  if (tid == 0 && rank == 0) {
-    p.row_max[at] = max;
-    p.row_arg[at] = arg;
-  }
-  for (int c = 0; c < n; ++c) {
-    const int i = child_sh[c], x = __ldg(p.tokens + node0 + i);
-    unsigned long long w = dead ? 0 : w_of(tame(logit(row + x)), x, pow_sh);
-    const double u = tame_uniform(__ldg(p.uniform + node0 + i));
-    unsigned long long taken, left;  // (taken 0: a refusal that would leave nothing changes nothing)
-    bool accepted;
-    if (!q) {
-      for (int j = 0; j < c; ++j)
-        if (__ldg(p.tokens + node0 + child_sh[j]) == x) w = 0;  // refused already
-      accepted = u * static_cast<double>(S) < static_cast<double>(w);
-      left = S - w;
-      taken = w;
-    } else {
-      const float qx = __ldg(q + x);
-      for (int j = 0; j < c; ++j) w = less(w, share_of(mult_sh[j], qx));
-      accepted = u * static_cast<double>(S) * static_cast<double>(fminf(fmaxf(qx, 0.f), 1.f)) < static_cast<double>(w);
-      left = 0;
-      if (!dead) {
-        each(row, q, lo, hi, tid, kAccThreads, [&](int k, float l, float d) {
-          unsigned long long y = w_of(l, k, pow_sh);
-          for (int j = 0; j < c; ++j) y = less(y, share_of(mult_sh[j], d));
-          left += less(y, share_of(S, d));
-        });
-      }
-      left = cluster_sum(left, warps_sh[c & 1], &slot_sh[c], size);
-      taken = S;
-    }
-    if (left == 0) left = S, taken = 0;
-    __syncthreads();
-    if (tid == 0) {
-      mult_sh[c] = taken;
-      if (rank == 0) {
-        p.accepted[node0 + i] = accepted ? 1 : 0;
-        p.taken[node0 + i] = taken;
-      }
-    }
-    S = left;
-    __syncthreads();
-  }
-  if (tid == 0 && rank == 0) p.left[at] = S;
-  cluster_sync();  // no CTA leaves while its slots are read
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kAccThreads) accept_walk_kernel(const __grid_constant__ AcceptParams p) {
-  __shared__ unsigned long long pow_sh[64];
-  __shared__ unsigned long long warps_sh[kAccWarps], total_sh;
-  __shared__ unsigned long long taken_sh[kMaxNodes];
-  __shared__ int par_sh[kMaxNodes], tok_sh[kMaxNodes], acc_sh[kMaxNodes], path_sh[kMaxNodes], child_sh[kMaxNodes];
-  __shared__ int last_sh, len_sh, n_child;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int size = p.walk_cluster, rank = blockIdx.x % size, b = blockIdx.x / size;
+  const int size = p.cluster, rank = blockIdx.x % size, b = blockIdx.x / size;
   const int64_t node0 = static_cast<int64_t>(b) * p.nodes;
   const int given = p.tree_len ? __ldg(p.tree_len + b) : p.nodes, nodes = min(max(given, 0), p.nodes);
   int bits = given != nodes && tid == 0 ? kStatusBadTreeLen : 0;
@@ -297,141 +167,263 @@ __global__ void __launch_bounds__(kAccThreads) accept_walk_kernel(const __grid_c
     if (!named) bits |= kStatusBadToken;
     par_sh[tid] = tid > 0 && linked && named ? up : -1;
     tok_sh[tid] = x;
+    u_sh[tid] = tame_uniform(__ldg(p.uniform + node0 + tid));
   }
   if (tid < 64) pow_sh[tid] = c_pow[tid];
-  const float u0 = nodes > 0 ? tame_uniform(__ldg(p.uniform + node0)) : 0.f;
   const float temperature = __ldg(p.temperature + b);
-  grid_dep_wait();
-  if (tid < nodes && tid > 0) acc_sh[tid] = par_sh[tid] >= 0 ? __ldcg(p.accepted + node0 + tid) : 0;
-  __syncthreads();
-  if (warp == 0) {
-    // the first accepted child of the node, its first accepted child, ...: children come behind their parents
-    int v = 0, len = nodes > 0 ? 1 : 0;
-    if (lane == 0) path_sh[0] = 0;
-    for (int i0 = 0; i0 < nodes; i0 += 32) {
-      uint32_t seen = 0;  // nodes of these 32 that the walk is past
-      for (;;) {
-        const int i = i0 + lane;
-        const uint32_t vote = __ballot_sync(0xffffffffu, i > v && i < nodes && par_sh[i] == v && acc_sh[i] != 0) & ~seen;
-        if (vote == 0) break;
-        const int bit = __ffs(vote) - 1;
-        v = i0 + bit;
-        seen = bit == 31 ? 0xffffffffu : (2u << bit) - 1u;
-        if (lane == 0) path_sh[len] = v;
-        ++len;
-      }
+  const bool greedy = !(temperature > 0.f);
+  RowWeight w_of = row_weight(temperature);
+  // this CTA's share of the vocabulary, this warp's range of it
+  const int lo = min(p.vocab, rank * p.share), hi = min(p.vocab, lo + p.share);
+  const int wlo = min(hi, lo + warp * p.warp_share), whi = min(hi, wlo + p.warp_share);
+  unsigned long long* weight_sh = dyn_sh - (kDrawn ? lo : 0);                     // [x] of token x
+  float* value_sh = reinterpret_cast<float*>(dyn_sh + (kDrawn ? p.share : 0)) - lo;  // kDrawn: q, else logits
+  int step = 0;  // of the reductions
+  // The cluster's sum of one number a thread (`max`: its largest), to all threads; also what comes before this CTA and warp.
+  unsigned long long before_cta, before_warp, my_warp;
+  auto reduce = [&](unsigned long long v, bool max) {
+    auto over = [&](unsigned long long x) { return max ? warp_max(x) : warp_sum(x); };
+    v = over(v);
+    my_warp = v;
+    if (lane == 0) warps_sh[step & 1][warp] = v;
+    __syncthreads();
+    const unsigned long long of_lane = lane < kAccWarps ? warps_sh[step & 1][lane] : 0;
+    v = over(of_lane);
+    if (!max) before_warp = warp_sum(lane < warp ? of_lane : 0);
+    before_cta = 0;
+    if (size > 1) {
+      if (tid == 0) ex.slot[step & 1] = v;
+      cluster_sync();
+      const unsigned long long of_cta = lane < size ? remote_u64(&ex.slot[step & 1], lane) : 0;
+      v = over(of_cta);
+      if (!max) before_cta = warp_sum(lane < rank ? of_cta : 0);
     }
-    int n = 0;
-    for (int i0 = 0; i0 < nodes; i0 += 32) {
-      const bool is = i0 + lane < nodes && i0 + lane > 0 && par_sh[i0 + lane] == v;
-      const uint32_t vote = __ballot_sync(0xffffffffu, is);
-      if (is) child_sh[n + __popc(vote & ((1u << lane) - 1u))] = i0 + lane;
-      n += __popc(vote);
-    }
-    if (lane == 0) {
-      last_sh = v;
-      len_sh = len;
-      n_child = n;
-    }
-  }
-  __syncthreads();
-  const int v = last_sh, n = n_child, len = len_sh;
-  if (rank == 0) {
-    if (tid < p.nodes) p.path[node0 + tid] = tid < len ? path_sh[tid] : -1;
-    if (tid == 0) p.path_len[b] = len;
-  }
-  if (tid < n) taken_sh[tid] = __ldcg(p.taken + node0 + child_sh[tid]);
-  const int64_t at = node0 + v;
-  const float max = nodes > 0 ? __ldcg(p.row_max + at) : -CUDART_INF_F;
-  const bool dead = !(max >= -3.4028235e38f);
-  if (dead) {
-    if (rank == 0 && tid == 0) {
-      p.next_token[b] = -1;
-      if (nodes > 0) bits |= kStatusBadLogits;
-    }
-    if (rank == 0 && bits) atomicOr(p.status, bits);
-    return;  // the whole cluster
-  }
-  const unsigned long long left = __ldcg(p.left + at);
-  const RowWeight w_of = row_weight(max, __ldcg(p.row_arg + at), temperature);
-  const T* row = static_cast<const T*>(p.logits) + at * p.logit_stride;
-  const float* q = p.draft_prob ? p.draft_prob + at * p.draft_stride : nullptr;
-  __syncthreads();
-  auto weight = [&](int i, float l, float d) {
-    unsigned long long w = w_of(l, i, pow_sh);
-    if (q) {
-      for (int j = 0; j < n; ++j) w = less(w, share_of(taken_sh[j], d));
-    } else {
-      for (int j = 0; j < n; ++j)
-        if (taken_sh[j] != 0 && tok_sh[child_sh[j]] == i) w = 0;
-    }
-    return w;
+    ++step;
+    return v;
   };
-  // the first x with the sum up to it above floor(u_0 S)
-  const unsigned long long target = share_of(left, u0);
-  int lo, hi;
-  range_of(p.vocab, rank, size, &lo, &hi);
-  // a warp's part of the CTA's share, in steps of 32
-  const int each_warp = ((hi - lo + kAccWarps - 1) / kAccWarps + 31) / 32 * 32;
-  const int wlo = min(hi, lo + warp * each_warp), whi = min(hi, wlo + each_warp);
-  unsigned long long sum = 0;
-  each(row, q, wlo, whi, lane, 32, [&](int i, float l, float d) { sum += weight(i, l, d); });
-  sum = warp_sum(sum);
-  if (lane == 0) warps_sh[warp] = sum;
   __syncthreads();
-  if (warp == 0) {
-    const unsigned long long s = warp_sum(lane < kAccWarps ? warps_sh[lane] : 0);
-    if (lane == 0) total_sh = s;
-  }
-  cluster_sync();
-  unsigned long long before = warp_sum(lane < rank ? remote_u64(&total_sh, lane) : 0);
-  before += warp_sum(lane < warp ? warps_sh[lane] : 0);
-  if (target >= before && target - before < sum) {  // one warp of the cluster
-    for (int i0 = wlo; i0 < whi; i0 += 32) {
-      const int i = i0 + lane;
-      unsigned long long w = i < whi ? weight(i, tame(logit(row + i)), q ? __ldg(q + i) : 0.f) : 0;
+
+  int v = 0, len = nodes > 0 ? 1 : 0, next = -1;
+  if (tid == 0) path_sh[0] = 0;
+  while (nodes > 0) {
+    const int64_t at = node0 + v;
+    const T* row = static_cast<const T*>(p.logits) + at * p.logit_stride;
+    const float* q = kDrawn ? p.draft_prob + at * p.draft_stride : nullptr;
+    // the row's share, and its largest (greedy: where that is, too, as the order of its bits over the lower index)
+    unsigned long long best = 0;
+    float top = -CUDART_INF_F;
+    for (int x0 = wlo + lane; x0 < whi; x0 += kUnroll * 32) {
+      float l[kUnroll], d[kUnroll];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
+      for (int k = 0; k < kUnroll; ++k) {
+        const int x = x0 + 32 * k;
+        l[k] = x < whi ? logit(row + x) : -CUDART_INF_F;
+        if (kDrawn) d[k] = x < whi ? __ldg(q + x) : 0.f;
       }
-      const uint32_t vote = __ballot_sync(0xffffffffu, before + w > target);
-      if (vote != 0) {
-        if (lane == 0) p.next_token[b] = i0 + __ffs(vote) - 1;
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int x = x0 + 32 * k;
+        if (x >= whi) break;
+        l[k] = tame(l[k]);
+        if (kDrawn) {
+          weight_sh[x] = __float_as_uint(l[k]);
+          value_sh[x] = d[k];
+        } else {
+          value_sh[x] = l[k];
+        }
+        if (greedy) {
+          const unsigned long long key = order_of(l[k], x);
+          best = key > best ? key : best;
+        }
+        top = fmaxf(top, l[k]);
+      }
+    }
+    if (!greedy) best = order_of(top, 0);
+    if (warp == 0) {  // v's children, in node order
+      int n = 0;
+      for (int i0 = v + 1; i0 < nodes; i0 += 32) {
+        const bool is = i0 + lane < nodes && par_sh[i0 + lane] == v;
+        const uint32_t vote = __ballot_sync(0xffffffffu, is);
+        if (is) child_sh[n + __popc(vote & ((1u << lane) - 1u))] = i0 + lane;
+        n += __popc(vote);
+      }
+      if (lane == 0) n_child = n;
+    }
+    best = reduce(best, true);
+    const int n = n_child;
+    for (int c = 0; c < min(n, kPrefetched); ++c) {  // 128-byte lines of this CTA's share
+      const T* next_row = static_cast<const T*>(p.logits) + (node0 + child_sh[c]) * p.logit_stride;
+      constexpr int kLine = 128 / sizeof(T);
+      for (int x = lo + tid * kLine; x < hi; x += kAccThreads * kLine) prefetch_l2(next_row + x);
+      if (kDrawn)
+        for (int x = lo + tid * 32; x < hi; x += kAccThreads * 32)
+          prefetch_l2(p.draft_prob + (node0 + child_sh[c]) * p.draft_stride + x);
+    }
+    const float l_child = tid < n ? tame(logit(row + tok_sh[child_sh[tid]])) : 0.f;
+    const float q_child = kDrawn && tid < n ? __ldg(q + tok_sh[child_sh[tid]]) : 1.f;
+    w_of.max = max_of(best);
+    w_of.only = greedy ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
+    if (!(w_of.max >= -3.4028235e38f)) {  // no logit is a number
+      if (tid == 0) bits |= kStatusBadLogits;
+      break;
+    }
+    unsigned long long sum = 0;
+    for (int x = wlo + lane; x < whi; x += 32) {
+      const unsigned long long w = w_of(kDrawn ? __uint_as_float(static_cast<uint32_t>(weight_sh[x])) : value_sh[x], x, pow_sh);
+      if (kDrawn) weight_sh[x] = w;
+      sum += w;
+    }
+    if (tid < n) {
+      // (a token that an earlier sibling had has been refused by the time it is tried)
+      bool again = false;
+      if (!kDrawn)
+        for (int c = 0; c < tid; ++c) again = again || tok_sh[child_sh[c]] == tok_sh[child_sh[tid]];
+      child_w[tid] = again ? 0 : w_of(l_child, tok_sh[child_sh[tid]], pow_sh);
+      child_q[tid] = fminf(fmaxf(q_child, 0.f), 1.f);
+    }
+    unsigned long long S = reduce(sum, false);
+    unsigned long long due = 0;  // kDrawn: S of the refusal that the weights do not show yet
+    int go = -1;
+    for (int c = 0; c < n; ++c) {
+      const unsigned long long w = child_w[c];
+      const double u = u_sh[child_sh[c]], share = kDrawn ? child_q[c] : 1.0;
+      if (u * static_cast<double>(S) * share < static_cast<double>(w)) {
+        go = child_sh[c];
         break;
       }
-      before += __shfl_sync(0xffffffffu, w, 31);
+      if (!kDrawn) {
+        if (w == 0 || w == S) continue;  // (a refusal that would leave nothing changes nothing)
+        S -= w;
+        const int x = tok_sh[child_sh[c]];
+        if (x < lo) before_cta -= w;
+        if (x >= lo && x < wlo) before_warp -= w;
+        if (x >= wlo && x < whi) {
+          my_warp -= w;
+          value_sh[x] = -CUDART_INF_F;  // (the warp's lanes all write it)
+        }
+      } else {
+        const unsigned long long held_cta = before_cta, held_warp = before_warp, held = my_warp;
+        unsigned long long left = 0;
+        for (int x = wlo + lane; x < whi; x += 32) {
+          const float d = value_sh[x];
+          unsigned long long y = weight_sh[x];
+          if (due != 0) {
+            y = less(y, share_of(due, d));
+            weight_sh[x] = y;
+          }
+          left += less(y, share_of(S, d));
+        }
+        left = reduce(left, false);
+        due = 0;
+        if (left == 0) {
+          before_cta = held_cta, before_warp = held_warp, my_warp = held;
+        } else {
+          __syncthreads();  // child_w has been read
+          if (tid > c && tid < n) child_w[tid] = less(child_w[tid], share_of(S, child_q[tid]));
+          __syncthreads();
+          due = S;
+          S = left;
+        }
+      }
+    }
+    if (go >= 0) {
+      v = go;
+      if (tid == 0) path_sh[len] = v;
+      ++len;
+      __syncthreads();  // the children's lists are read
+      continue;
+    }
+    // the draw: the first x with the sum up to it above floor(u_0 S)
+    const unsigned long long target = share_of(S, u_sh[0]);
+    unsigned long long before = before_cta + before_warp;
+    if (target >= before && target - before < my_warp) {  // one warp of the cluster
+      __syncwarp();
+      // lanes take consecutive tokens, an odd number each (so that they meet in no bank)
+      const int each = ((whi - wlo + 31) / 32) | 1, first = min(whi, wlo + lane * each), last = min(whi, first + each);
+      auto weight = [&](int x) {
+        return kDrawn ? less(weight_sh[x], share_of(due, value_sh[x])) : w_of(value_sh[x], x, pow_sh);
+      };
+      unsigned long long mine = 0;
+      for (int x = first; x < last; ++x) mine += weight(x);
+      unsigned long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      before += incl - mine;
+      if (target >= before && target - before < mine) {
+        int x = first;
+        for (;; ++x) {
+          before += weight(x);
+          if (before > target) break;
+        }
+        p.next_token[b] = x;
+      }
+    }
+    next = 0;  // (written by the warp that found it)
+    break;
+  }
+  __syncthreads();
+  if (rank == 0) {
+    if (tid < p.nodes) p.path[node0 + tid] = tid < len ? path_sh[tid] : -1;
+    if (tid == 0) {
+      p.path_len[b] = len;
+      if (next < 0) p.next_token[b] = -1;
+    }
+    bits = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bits)));
+    if (p.batch > 1) {
+      if (lane == 0 && bits) atomicOr(p.status, bits);
+    } else {  // one request: the word as a whole
+      int* all = reinterpret_cast<int*>(warps_sh);
+      if (lane == 0) all[warp] = bits;
+      __syncthreads();
+      if (tid == 0) {
+        for (int i = 1; i < kAccWarps; ++i) bits |= all[i];
+        *p.status = bits;
+      }
     }
   }
-  if (rank == 0 && bits) atomicOr(p.status, bits);
-  cluster_sync();  // no CTA leaves while its sum is read
+  if (size > 1) cluster_sync();  // no CTA leaves while its slots are read
 }
 
-template <typename K>
-cudaError_t launch(K kernel, const AcceptParams& p, int64_t clusters, int size, bool dependent, cudaStream_t stream) {
+template <typename T, bool kDrawn>
+cudaError_t launch(const AcceptParams& p, size_t bytes, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.x = p.cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * size));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * p.cluster);
   cfg.blockDim = dim3(kAccThreads);
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, accept_kernel<T, kDrawn>, p);
+}
+
+template <typename T, bool kDrawn>
+cudaError_t configure() {
+  cudaError_t e = cudaFuncSetAttribute(accept_kernel<T, kDrawn>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAcceptBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(accept_kernel<T, kDrawn>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e;
 }
 
 }  // namespace
 
-cudaError_t launch_accept(const AcceptParams& p, bool bf16, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.batch) * p.nodes;
-  cudaError_t e = launch(bf16 ? accept_rows_kernel<uint16_t> : accept_rows_kernel<float>, p, rows, p.row_cluster, false, stream);
-  if (e == cudaSuccess)
-    e = launch(bf16 ? accept_walk_kernel<uint16_t> : accept_walk_kernel<float>, p, p.batch, p.walk_cluster, true, stream);
+cudaError_t configure_accept() {
+  cudaError_t e = configure<uint16_t, false>();
+  if (e == cudaSuccess) e = configure<uint16_t, true>();
+  if (e == cudaSuccess) e = configure<float, false>();
+  if (e == cudaSuccess) e = configure<float, true>();
   return e;
+}
+
+cudaError_t launch_accept(const AcceptParams& p, bool bf16, cudaStream_t stream) {
+  const size_t bytes = static_cast<size_t>(p.share) * accept_value_bytes(p.draft_prob != nullptr);
+  if (p.draft_prob) return bf16 ? launch<uint16_t, true>(p, bytes, stream) : launch<float, true>(p, bytes, stream);
+  return bf16 ? launch<uint16_t, false>(p, bytes, stream) : launch<float, false>(p, bytes, stream);
 }
 
 }  // namespace ddt

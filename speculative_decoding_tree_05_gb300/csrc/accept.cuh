@@ -1,5 +1,6 @@
 // accept.cuh -- launch parameters of the check of drafted tokens.
 #pragma once
+#include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
 #include "kernels.cuh"
@@ -8,6 +9,11 @@ namespace ddt {
 
 constexpr int32_t kStatusBadToken = 256;
 constexpr int32_t kStatusBadLogits = 512;
+constexpr int kAcceptVocab = 1 << 18;       // most tokens: a cluster of 16 CTAs holds a row of them in shared memory
+constexpr int kAcceptBytes = 200 * 1024;    // of that, in one CTA
+constexpr int kAcceptCluster = 16;
+// shared memory of a token: its logit, or with draft probabilities its weight and probability
+constexpr int accept_value_bytes(bool drawn) { return drawn ? 12 : 4; }
 
 struct AcceptParams {
   const void* logits;          // bf16 or fp32, node (b, t) at logits + (b * T + t) * logit_stride
@@ -20,19 +26,14 @@ struct AcceptParams {
   const float* uniform;        // [B, T]
   const float* temperature;    // [B]
   int32_t batch, nodes, vocab;
-  int32_t row_cluster, walk_cluster;  // CTAs of a node, of a request: 1, 2, 4 or 8
-  // of each node: its row's maximum, where it is, what its refused children leave of the sum of its weights
-  float* row_max;
-  int32_t* row_arg;
-  unsigned long long* left;
-  // of each node as a child: accepted if its parent is; what its refusal takes, drawn tokens: S, else w (0: nothing)
-  int32_t* accepted;
-  unsigned long long* taken;
+  int32_t cluster;             // CTAs of a request: 1, 2, 4, 8 or 16
+  int32_t share, warp_share;   // tokens of a CTA, and of each of its 16 warps
   int32_t* path;               // [B, T]
   int32_t* path_len;           // [B]
   int32_t* next_token;         // [B]
-  int32_t* status;
+  int32_t* status;             // cleared before the launch, unless there is one request
 };
+cudaError_t configure_accept();
 cudaError_t launch_accept(const AcceptParams& p, bool bf16, cudaStream_t stream);
 
 }  // namespace ddt

@@ -8,6 +8,7 @@
 #include <utility>
 #include <vector>
 #include "../../include/ddtree.h"
+#include "accept.cuh"
 #include "cache_ops.cuh"
 #include "host.cuh"
 #include "kernels.cuh"
@@ -49,7 +50,8 @@ int device_info(DeviceInfo* out) {
       d.ok = configure_prefix() == cudaSuccess && configure_tail_merge() == cudaSuccess;
       d.cache_ok = configure_scores() == cudaSuccess && configure_evict() == cudaSuccess &&
                    configure_topk() == cudaSuccess && configure_block_attn(&d.clusters) == cudaSuccess &&
-                   configure_summary() == cudaSuccess && configure_kv8_attn() == cudaSuccess;
+                   configure_summary() == cudaSuccess && configure_kv8_attn() == cudaSuccess &&
+                   configure_accept() == cudaSuccess;
 #ifdef DDT_TEST_HOOKS
       if (g_test_fail_cache_setup) d.cache_ok = false;
 #endif

@@ -22,13 +22,13 @@
 // O^T takes 256 TMEM columns, so one CTA holds the whole output. By themselves the MMAs of
 // a tile take 1790 cycles with 64 rows, 1400 with 16.
 //
-// Per CTA (576 threads), one unit = (up to 64 (node, head) rows of a request, a share of its tiles):
+// Per CTA (832 threads), one unit = (up to 64 (node, head) rows of a request, a share of its tiles):
 //   warp 0       TMEM; one lane issues S(t), dim group by dim group as stage t lands
-//   warps 1-8    softmax: 16 keys x 32 rows each, in the 16x256b shape
-//   warp 9       one lane issues P.V(t) when P(t) is written
-//   warps 10-17  gather 64 keys per stage of 40 KB, three stages of four dim groups, each
-//                refilled as soon as its part of P.V is done: warps 10-13 two dim groups
-//                (two of five 128-byte pieces of a row) by 16-byte cp.async, warps 14-17
+//   warps 1-16   softmax: 16 keys x 16 rows each, in the 16x256b shape
+//   warp 17      one lane issues P.V(t) when P(t) is written
+//   warps 18-25  gather 64 keys per stage of 40 KB, three stages of four dim groups, each
+//                refilled as soon as its part of P.V is done: warps 18-21 two dim groups
+//                (two of five 128-byte pieces of a row) by 16-byte cp.async, warps 22-25
 //                the others by TMA gather4, at the same time
 // A request's keys are its prefix and, behind it, all its tree rows, each with the rows
 // that see it. The tiles of the whole batch are cut into equal shares, whatever the
@@ -36,7 +36,6 @@
 // log-sum-exp at once, else each writes its normalised O and the merge kernel joins them.
 #include <cuda_runtime.h>
 #include <math_constants.h>
-#include <climits>
 #include <type_traits>
 #include "kv8.cuh"
 #include "ptx.cuh"
@@ -44,8 +43,9 @@
 namespace ddt {
 namespace {
 
-constexpr int kThreads = 576;
-constexpr int kSoftmax = 256;
+constexpr int kThreads = 832;
+constexpr int kSoftmax = 512;
+constexpr int kIssuePv = 17, kFirstCopier = 18, kFirstGather = 22;  // warps
 constexpr int kCopiers = 128;                       // threads that gather the copied groups
 constexpr int kCopied = 2;                          // dim groups gathered by cp.async
 constexpr int kGroups = 4;                          // dims {0-127}, {128-255}, {256-383}, {384-511 and rope}
@@ -78,6 +78,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 struct Shared {
   uint64_t k_full[kStages][kGroups];
   uint64_t k_empty[kStages][kGroups];  // this group's part of the tile's P.V is done (and those before it)
+  uint64_t f_full[kStages];            // the keys' factors and masks
   uint64_t s_full[2], s_free[2];
   uint64_t p_ready[2];
   uint64_t drain;
@@ -88,17 +89,16 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= 512, "barrier block");
 
-__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
+// 16 TMEM lanes x 16 columns over a warp: v[2 i + h] = lane L/4 + 8 h, columns 8 i + 2 (L % 4) + {0, 1}.
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint64_t (&v)[4]) {
+  uint32_t r[8];
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
       : "r"(taddr)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 4; ++i) v[i] = f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
@@ -110,6 +110,23 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+// Two weights in two 8-bit parts, e4m3 and what that leaves in e5m2. Through f16, whose 11 bits lose 2^-12 of a weight
+// and whose differences here are exact: five conversions and a subtraction a pair.
+__device__ __forceinline__ void cut_weights(float x, float y, uint32_t& hi, uint32_t& lo) {
+  uint32_t h, back;
+  uint16_t a, b;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(h));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(a));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(back));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(b) : "r"(h));
+  hi = a;
+  lo = b;
+}
+__device__ __forceinline__ void st_shared_b32(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
 // a |= m in shared memory, by halves (32-bit atomics need no loop)
@@ -210,13 +227,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   const int64_t trow0 = static_cast<int64_t>(un.b) * p.nodes * p.heads + row0;  // of q, out and lse
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i)
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh.f_full[i], 4);
       for (int x = 0; x < kGroups; ++x) {
-        // every copying thread's cp.async (group 0: and each of its warps' key factors and masks), or the gather
-        // warps' arrivals with their bytes
-        mbar_init(&sh.k_full[i][x], x < kCopied ? kCopiers + (x == 0 ? 4 : 0) : 4);
+        // every copying thread's cp.async, or the gather warps' arrivals with their bytes
+        mbar_init(&sh.k_full[i][x], x < kCopied ? kCopiers : 4);
         mbar_init(&sh.k_empty[i][x], 1);
       }
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_free[i], kSoftmax / 32);
@@ -240,16 +258,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   const uint32_t tmem = sh.tmem_base;
   bool ok = true;
 
-  if (warp < 10) {
+  if (warp < kFirstCopier) {
     // ------------------------------------------------------------------ the group's query rows, in two 8-bit parts
     const uint16_t* q = p.q + trow0 * kDqk;
     float* qs = reinterpret_cast<float*>(smem + kOffQs);
-    for (int r0 = warp; r0 < kRows; r0 += 40) {
+    {
       uint4 a[4], b[4];
       uint32_t c[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {  // four rows' loads at a time
-        const int r = r0 + 10 * k;
+      for (int k = 0; k < 4; ++k) {  // all rows' loads at once
+        const int r = warp + kFirstCopier * k;
         const uint16_t* src = q + static_cast<int64_t>(r < rows ? r : 0) * kDqk;
         a[k] = __ldg(reinterpret_cast<const uint4*>(src) + lane);
         b[k] = __ldg(reinterpret_cast<const uint4*>(src + 256) + lane);
@@ -257,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int r = r0 + 10 * k;
+        const int r = warp + kFirstCopier * k;
         if (r >= kRows) break;
         const uint32_t w[9] = {a[k].x, a[k].y, a[k].z, a[k].w, b[k].x, b[k].y, b[k].z, b[k].w, c[k]};
         uint32_t top = 0, turned = 0;  // the largest magnitudes, latent and rope, as bf16 bits
@@ -310,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       }
     }
     fence_proxy_async_smem();
-    bar_sync(3, 320);
+    bar_sync(3, kFirstCopier * 32);
   }
 
   if (warp == 0) {
@@ -353,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       mma_commit(&sh.drain);
       mbar_wait(&sh.drain, 0);
     }
-  } else if (warp == 9) {
+  } else if (warp == kIssuePv) {
     if (elect_one()) {
       const uint32_t cols = (rows + 15) / 16 * 16;
       const uint32_t idesc_hi = idesc_f8_f32(128, cols, kE4m3, kE4m3, true, true), idesc_lo = idesc_f8_f32(128, cols, kE4m3, kE5m2, true, true);
@@ -384,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       mma_commit(&sh.drain);
       mbar_wait(&sh.drain, 0);
     }
-  } else if (warp >= 10) {
+  } else if (warp >= kFirstCopier) {
     // ------------------------------------------------------------------ producers
     const int32_t* slots = p.slot_idx + static_cast<int64_t>(un.b) * p.slot_stride;
     uint64_t* tree_mask = reinterpret_cast<uint64_t*>(smem + kOffTree);
@@ -394,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       // the tree rows, and which of the group's rows see each: a node's walk to the root sets its rows' bits in
       // itself and every ancestor; a link that is no earlier node ends it, a slot outside the pool is left out
       int* par = reinterpret_cast<int*>(smem + kOffPar);
-      const int i = tid - 320;
+      const int i = tid - kFirstCopier * 32;
       if (i < nodes) {
         par[i] = __ldg(p.tree_parent + static_cast<int64_t>(un.b) * p.nodes + i);
         tree_slot[i] = __ldg(p.tree_slot_idx + static_cast<int64_t>(un.b) * p.nodes + i);
@@ -422,18 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       }
       bar_sync(4, 256);
     }
-    // key i of the request: its slot (-1: none, or no row sees it)
+    // Key i of the request: its slot as read. Nothing is computed from a value in the tile that reads it: an
+    // immediate use stalls the warp for the read (800 cycles a tile).
     auto read_slot = [&](int t, int k) -> int {
       const int i = (t0 + t) * kKeys + k;
       if (t >= n || k >= kKeys || i >= keys) return -1;
-      if (i < L) {
-        const int s = __ldg(slots + i);
-        return s < 0 ? INT_MIN : s;  // (a bad slot is told from none)
-      }
-      return tree_mask[i - L] ? tree_slot[i - L] : -1;
+      return i < L ? __ldg(slots + i) : tree_slot[i - L];
     };
     auto in_pool = [&](int slot) { return slot >= 0 && slot < p.pool_slots; };
-    auto read_scale = [&](int slot) -> float { return in_pool(slot) ? __ldg(p.scale + slot) : 1.f; };
     // 16-byte copies of kPieces consecutive pieces (8 a chunk) from chunk c0 on of 16 rows from row0 on; zeros for
     // rows without a slot
     auto copy_rows = [&](uint32_t sbase, int r0, int c0, auto pieces, int slot) {
@@ -450,25 +464,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     };
     using P16 = std::integral_constant<int, 16>;
     using P8 = std::integral_constant<int, 8>;
-    const bool copier = warp < 14;
-    const int r0 = 16 * (copier ? warp - 10 : warp - 14);  // the warp's first key of a tile, 16 of them
+    const bool copier = warp < kFirstGather;
+    const int r0 = 16 * (copier ? warp - kFirstCopier : warp - kFirstGather);  // the warp's first key of a tile, 16 of them
     const int k = lane < 16 ? r0 + lane : kKeys;           // the lane's key
     // A key's row takes two dependent reads, its slot and its scale, each a tile ahead of its use.
     int slot_now = read_slot(0, k), slot_next = read_slot(1, k);
-    float scale_now = copier ? read_scale(slot_now) : 1.f;
+    float scale_now = copier && in_pool(slot_now) ? __ldg(p.scale + slot_now) : 1.f;
     int st = 0, ph = 0, done = 0;
     auto wait_empty = [&](int t, int x) {
       const bool w = t < kStages || mbar_wait_abortable(&sh.k_empty[st][x], ph ^ 1, abort, false, __LINE__);
       return __all_sync(0xffffffffu, w) != 0;
     };
     for (int t = 0; ok && t < n; ++t) {
-      const bool good = in_pool(slot_now);
-      if (!good && slot_now != -1) atomicOr(&sh.flags, kStatusBadSlot);
-      const int slot = good ? slot_now : -1;
-      const float scale = scale_now;
       const int i = (t0 + t) * kKeys + k;
+      uint64_t mask = 0;  // of the rows that see the key
+      if (k < kKeys && i < keys) mask = i < L ? full : tree_mask[i - L];
+      if (mask != 0 && !in_pool(slot_now)) {
+        mask = 0;
+        atomicOr(&sh.flags, kStatusBadSlot);
+      }
+      const int slot = mask != 0 ? slot_now : -1;
+      const float scale = scale_now;
       slot_now = slot_next;
-      if (copier) scale_now = read_scale(slot_now);
+      if (copier) scale_now = in_pool(slot_now) ? __ldg(p.scale + slot_now) : 1.f;
       slot_next = read_slot(t + 2, k);
       const uint32_t sbase = base + st * kStageBytes;
       if (copier) {
@@ -476,23 +494,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
           ok = false;
           break;
         }
-        if (lane < 16) {
-          reinterpret_cast<uint64_t*>(smem + kOffMask)[st * kKeys + k] = !good ? 0 : i < L ? full : tree_mask[i - L];
-          // a scale that is not positive and finite: NaN for the rows that see the key
-          const bool fine = scale > 0.f && scale < CUDART_INF_F;
-          reinterpret_cast<float4*>(smem + kOffKey)[st * kKeys + k] =
-              fine ? make_float4(scale, log2f(scale), 1.f / scale, 0.f) : make_float4(CUDART_NAN_F, 0.f, 1.f, 0.f);
-        }
         copy_rows(sbase, r0, 0, P8(), slot);
         cp_async_arrive_noinc(&sh.k_full[st][0]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.k_full[st][0]);  // releases the factors and masks
         if (!wait_empty(t, 1)) {
           ok = false;
           break;
         }
         copy_rows(sbase, r0, 1, P8(), slot);
         cp_async_arrive_noinc(&sh.k_full[st][1]);
+        if (lane < 16) {
+          reinterpret_cast<uint64_t*>(smem + kOffMask)[st * kKeys + k] = mask;
+          // a scale that is not positive and finite: NaN for the rows that see the key
+          const bool fine = scale > 0.f && scale < CUDART_INF_F;
+          reinterpret_cast<float4*>(smem + kOffKey)[st * kKeys + k] =
+              fine ? make_float4(scale, log2f(scale), 1.f / scale, 0.f) : make_float4(CUDART_NAN_F, 0.f, 1.f, 0.f);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.f_full[st]);  // releases the factors and masks
       } else {
         if (!wait_empty(t, 2) || !wait_empty(t, 3)) {
           ok = false;
@@ -535,21 +553,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       }
   } else {
     // ------------------------------------------------------------------ softmax
-    const int quarter = warp & 3, half = (warp - 1) >> 2;
+    const int quarter = warp & 3, part4 = (warp - 1) >> 2;  // lanes of TMEM, a quarter of the rows
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const int r0 = quarter * 16 + (lane >> 2);     // keys r0 and r0 + 8 of the tile
-    const int c0 = 32 * half + 2 * (lane & 3);     // rows c0 + 8 i + {0, 1}, i < 4
-    const int id = half * 128 + quarter * 32 + lane;
+    const int c0 = 16 * part4 + 2 * (lane & 3);    // rows c0 + 8 i + {0, 1}, i < 2
+    const int id = part4 * 128 + quarter * 32 + lane;
     float* alpha_sh = reinterpret_cast<float*>(smem + kOffAlpha);
     const uint64_t* masks = reinterpret_cast<const uint64_t*>(smem + kOffMask);
     const float4* factors = reinterpret_cast<const float4*>(smem + kOffKey);
     const uint64_t full = rows == 64 ? ~0ull : ((1ull << rows) - 1);
-    float l[8], qs[8], m[8];  // sums, score factors and (lowered by kLift) references of this thread's rows
+    // of this thread's rows, two by two: sums, score factors and (lowered by kLift) references
+    uint64_t l[2], qs[2], m[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      l[i] = 0.f;
-      qs[i] = reinterpret_cast<const float*>(smem + kOffQs)[c0 + 8 * (i >> 1) + (i & 1)];
-      m[i] = kUnset;
+    for (int i = 0; i < 2; ++i) {
+      l[i] = f32x2(0.f, 0.f);
+      qs[i] = *reinterpret_cast<const uint64_t*>(smem + kOffQs + (c0 + 8 * i) * 4);
+      m[i] = f32x2(kUnset, kUnset);
+    }
+    // Where this thread's weights go in a part of P^T (a key's 64 columns, 64-byte swizzle): with its neighbour it
+    // holds four columns of two keys, of which even lanes store the first and odd lanes the second key's.
+    uint32_t p_at[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int key = r0 + 8 * (lane & 1), col = (c0 & ~3) + 8 * i;
+      p_at[i] = base + kOffP + key * 64 + ((((col >> 4) ^ ((key >> 1) & 3)) << 4) | (col & 15));
     }
     bool failed = false;  // a wait of this thread ran out: the warps leave together at the next barrier
     auto wait_pv = [&](int t) {  // P.V(t) has read P, and O^T holds every tile up to t
@@ -557,9 +584,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       tc_fence_after();
     };
     // column sums or maxima over the 16 keys of the warp, to scratch [4 quarters][64]
-    auto to_scratch = [&](float* scratch, const float (&v)[8], auto op) {
+    auto to_scratch = [&](float* scratch, const float (&v)[4], auto op) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         float x = v[i];
         x = op(x, __shfl_xor_sync(0xffffffffu, x, 4));
         x = op(x, __shfl_xor_sync(0xffffffffu, x, 8));
@@ -569,28 +596,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     };
     int st = 0, ph = 0;
     for (int t = 0; t < n; ++t) {
-      uint8_t* pb = smem + kOffP + (t & 1) * 2 * kPart;
-      float* scratch = reinterpret_cast<float*>(pb);
-      if (!mbar_wait_abortable(&sh.k_full[st][0], ph, abort, false, __LINE__)) failed = true;
+      if (!mbar_wait_abortable(&sh.f_full[st], ph, abort, false, __LINE__)) failed = true;
       const uint64_t m0 = masks[st * kKeys + r0], m1 = masks[st * kKeys + r0 + 8];
       const float4 f0 = factors[st * kKeys + r0], f1 = factors[st * kKeys + r0 + 8];
       const bool part = __any_sync(0xffffffffu, m0 != full || m1 != full);
       if (!mbar_wait_abortable(&sh.s_full[t & 1], (t >> 1) & 1, abort, false, __LINE__)) failed = true;
       __syncwarp();
       tc_fence_after();
-      float s[16];
+      float s[8];  // [4 i + 2 h + e]: key r0 + 8 h, row c0 + 8 i + e
       // t of each score: log2 of its weight times its key's scale
       auto scores = [&] {
-        tmem_ld_16x32(tmem + lane_off + kColS + (t & 1) * kRows + 32 * half, s);
+        uint64_t v[4];
+        tmem_ld_16x16(tmem + lane_off + kColS + (t & 1) * kRows + 16 * part4, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int row = 2 * (i >> 2) + (i & 1);
-          s[i] = (i & 2) ? fmaf(s[i] * f1.x, qs[row], f1.y - m[row]) : fmaf(s[i] * f0.x, qs[row], f0.y - m[row]);
+        for (int i = 0; i < 4; ++i) {
+          const float4 f = i & 1 ? f1 : f0;
+          v[i] = fma_x2(mul_x2(v[i], f32x2(f.x, f.x)), qs[i >> 1], sub_x2(f32x2(f.y, f.y), m[i >> 1]));
+          f32x2_split(v[i], s[2 * i], s[2 * i + 1]);
         }
         if (part) {
           const uint32_t w0 = static_cast<uint32_t>(m0 >> c0), w1 = static_cast<uint32_t>(m1 >> c0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               if (!((w0 >> (8 * i + e)) & 1u)) s[4 * i + e] = -CUDART_INF_F;
@@ -599,9 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         }
       };
       scores();
-      float over = -CUDART_INF_F;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) over = fmax3(over, s[2 * i], s[2 * i + 1]);
+      const float over = fmax3(fmax3(s[0], s[1], s[2]), fmax3(s[3], s[4], s[5]), fmaxf(s[6], s[7]));
       if (failed) sh.fail[t & 1] = 1;
       const bool raise = bar_red_or(1, kSoftmax, failed || over > kLift + kSlack);
       if (raise && *const_cast<volatile int*>(&sh.fail[t & 1])) {
@@ -609,43 +634,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         break;
       }
       if (raise) {
+        // Every row's reference becomes its maximum: with 64 rows in step, raising the rows that need it alone
+        // would come to a raise of some row in most tiles.
+        float* scratch = reinterpret_cast<float*>(smem + kOffP + (t & 1) * 2 * kPart);
         if (t > 0) wait_pv(t - 1);  // the scratch is the P buffer, and O^T is rescaled
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] = 0.f;
+        m[0] = m[1] = f32x2(0.f, 0.f);
         scores();  // again, without a reference
-        float top8[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          top8[2 * i] = fmaxf(s[4 * i], s[4 * i + 2]);
-          top8[2 * i + 1] = fmaxf(s[4 * i + 1], s[4 * i + 3]);
-        }
-        to_scratch(scratch, top8, [](float a, float b) { return fmaxf(a, b); });
+        const float top4[4] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3]), fmaxf(s[4], s[6]), fmaxf(s[5], s[7])};
+        to_scratch(scratch, top4, [](float a, float b) { return fmaxf(a, b); });
         bar_sync(1, kSoftmax);
         if (id < kRows) {  // one thread per row decides
           const float old = mx[id];
           const float top = fmaxf(fmaxf(scratch[id], scratch[kRows + id]), fmaxf(scratch[2 * kRows + id], scratch[3 * kRows + id]));
-          const bool up = top > old + kSlack;
-          alpha_sh[id] = up ? fast_exp2(old - top) : 1.f;
-          mx[id] = up ? top : old;
+          alpha_sh[id] = top > old ? fast_exp2(old - top) : 1.f;
+          mx[id] = fmaxf(top, old);
         }
         bar_sync(1, kSoftmax);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = c0 + 8 * (i >> 1) + (i & 1);
-          l[i] *= alpha_sh[row];
-          m[i] = mx[row] - kLift;
+        for (int i = 0; i < 2; ++i) {
+          l[i] = mul_x2(l[i], *reinterpret_cast<const uint64_t*>(alpha_sh + c0 + 8 * i));
+          m[i] = sub_x2(*reinterpret_cast<const uint64_t*>(mx + c0 + 8 * i), f32x2(kLift, kLift));
+          float x, y;
+          f32x2_split(m[i], x, y);
+          s[4 * i] -= x, s[4 * i + 1] -= y, s[4 * i + 2] -= x, s[4 * i + 3] -= y;
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] -= m[2 * (i >> 2) + (i & 1)];
         if (t > 0) {
 #pragma unroll 1
-          for (int k0 = 0; k0 < 16; ++k0) {  // this warp's half of the columns, 8 at a time
-            const int cc = 32 * half + (k0 & 3) * 8;
+          for (int k0 = 0; k0 < 8; ++k0) {  // this warp's quarter of the columns, 8 at a time
+            const int cc = 16 * part4 + (k0 & 1) * 8;
             uint32_t o[8];
-            tmem_ld8(tmem + lane_off + (k0 >> 2) * kRows + cc, o);
+            tmem_ld8(tmem + lane_off + (k0 >> 1) * kRows + cc, o);
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha_sh[cc + k]);
-            tmem_st8(tmem + lane_off + (k0 >> 2) * kRows + cc, o);
+            tmem_st8(tmem + lane_off + (k0 >> 1) * kRows + cc, o);
           }
         }
         bar_sync(1, kSoftmax);  // scratch is read before P is written over it
@@ -656,35 +677,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       if (warp != 1 || t != p.test_keep_back)
 #endif
       if (lane == 0) mbar_arrive(&sh.s_free[t & 1]);
-      uint32_t hi[4], lo[4];  // [i]: rows c0 + 8 i + {0, 1} of keys r0 (low half) and r0 + 8
+      uint32_t hi[2], lo[2];  // [i]: rows c0 + 8 i + {0, 1} of keys r0 (low half) and r0 + 8
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         uint32_t h2[2], l2[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float x = fast_exp2(s[4 * i + 2 * h]), y = fast_exp2(s[4 * i + 2 * h + 1]);
           const float inv = h ? f1.z : f0.z;
-          l[2 * i] = fmaf(x, inv, l[2 * i]);
-          l[2 * i + 1] = fmaf(y, inv, l[2 * i + 1]);
-          h2[h] = pack_e4m3x2(x, y);
-          float hx, hy;
-          unpack_e4m3x2(static_cast<uint16_t>(h2[h]), hx, hy);
-          l2[h] = pack_e5m2x2(x - hx, y - hy);  // (the differences are exact)
+          l[i] = fma_x2(f32x2(x, y), f32x2(inv, inv), l[i]);
+          cut_weights(x, y, h2[h], l2[h]);
         }
         hi[i] = h2[0] | (h2[1] << 16);
         lo[i] = l2[0] | (l2[1] << 16);
       }
       if (!raise && t > 1) wait_pv(t - 2);  // the buffer is free
-      // P^T: row (key) of 64 columns, 64-byte swizzle
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int key = r0 + 8 * h, col = c0 + 8 * i;
-          uint8_t* at = pb + key * 64 + ((((col >> 4) ^ ((key >> 1) & 3)) << 4) | (col & 15));
-          *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(hi[i] >> (16 * h));
-          *reinterpret_cast<uint16_t*>(at + kPart) = static_cast<uint16_t>(lo[i] >> (16 * h));
-        }
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t at = p_at[i] + (t & 1) * 2 * kPart;
+        const uint32_t h = __shfl_xor_sync(0xffffffffu, hi[i], 1), w = __shfl_xor_sync(0xffffffffu, lo[i], 1);
+        st_shared_b32(at, lane & 1 ? __byte_perm(h, hi[i], 0x7632) : __byte_perm(hi[i], h, 0x5410));
+        st_shared_b32(at + kPart, lane & 1 ? __byte_perm(w, lo[i], 0x7632) : __byte_perm(lo[i], w, 0x5410));
+      }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -697,7 +711,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     }
     if (ok) {
       float* scratch = reinterpret_cast<float*>(smem + kOffP);
-      to_scratch(scratch, l, [](float a, float b) { return a + b; });
+      float sums[4];
+      f32x2_split(l[0], sums[0], sums[1]);
+      f32x2_split(l[1], sums[2], sums[3]);
+      to_scratch(scratch, sums, [](float a, float b) { return a + b; });
       bar_sync(1, kSoftmax);
       if (id < kRows) {
         const float sum = (scratch[id] + scratch[kRows + id]) + (scratch[2 * kRows + id] + scratch[3 * kRows + id]);
@@ -712,15 +729,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       }
     }
   }
-  // the softmax and gather warps write O: quarter of the lanes by warp, four warps a quarter
+  // the softmax and gather warps write O: quarter of the lanes by warp, six warps a quarter
   if (warp > 0) {
-    if (!bar_red_or(2, kThreads - 32, !ok) && warp != 9) {
+    if (!bar_red_or(2, kThreads - 32, !ok) && warp != kIssuePv) {
       tc_fence_after();
       const float* inv_l = reinterpret_cast<const float*>(smem + kOffAlpha);
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       // lane = value dim: each row's store is 128 contiguous bytes per warp
 #pragma unroll 1
-      for (int k0 = warp < 9 ? (warp - 1) >> 2 : (warp - 2) >> 2; k0 < 32; k0 += 4) {
+      for (int k0 = warp < kIssuePv ? (warp - 1) >> 2 : (warp - 2) >> 2; k0 < 32; k0 += 6) {
         const int mt = k0 >> 3, cc = (k0 & 7) * 8;
         if (cc >= rows) continue;
         uint32_t o[8];

@@ -85,27 +85,22 @@ int merge_warps(const Kv8Layout& w, int batch) {
   return n;
 }
 
-struct AcceptLayout {
-  size_t max_off, arg_off, left_off, taken_off, accepted_off, bytes;
-};
-int accept_layout(const ddt_dims* d, int32_t vocab, AcceptLayout* w) {
+int check_accept(const ddt_dims* d, int32_t vocab) {
   if (!d) return DDT_ERR_NULL;
-  if (d->batch < 0 || d->batch > 65535 || d->num_nodes < 1 || d->num_nodes > kMaxNodes || vocab < 1 || vocab > (1 << 20))
+  if (d->batch < 0 || d->batch > 65535 || d->num_nodes < 1 || d->num_nodes > kMaxNodes || vocab < 1 || vocab > kAcceptVocab)
     return DDT_ERR_DIMS;
-  const size_t n = size_t(d->batch) * d->num_nodes;
-  w->left_off = kStatusBytes;
-  w->taken_off = align_up(w->left_off + n * 8, 256);
-  w->max_off = align_up(w->taken_off + n * 8, 256);
-  w->arg_off = align_up(w->max_off + n * 4, 256);
-  w->accepted_off = align_up(w->arg_off + n * 4, 256);
-  w->bytes = align_up(w->accepted_off + n * 4, 256);
   return DDT_OK;
 }
-// CTAs of a row: as many as keep the SMs busy and leave each a few thousand values
-int row_cluster(int64_t rows, int vocab, int sm_count) {
-  int n = 8;
-  while (n > 1 && (rows * n > sm_count || vocab < n * 2048)) n /= 2;
-  return n;
+// CTAs of a request: enough to hold a row in shared memory, and more while there are SMs
+// for them and each keeps a thousand tokens.
+void accept_grid(int batch, int vocab, bool drawn, int sm_count, AcceptParams* p) {
+  auto share_of = [&](int n) { return ((vocab + n - 1) / n + 63) / 64 * 64; };
+  int n = 1;
+  while (n < kAcceptCluster && share_of(n) * accept_value_bytes(drawn) > kAcceptBytes) n *= 2;
+  while (n < kAcceptCluster && int64_t(batch) * n * 2 <= sm_count && vocab >= n * 2 * 1024) n *= 2;
+  p->cluster = n;
+  p->share = share_of(n);
+  p->warp_share = ((p->share + 15) / 16 + 31) / 32 * 32;
 }
 
 }  // namespace
@@ -261,8 +256,7 @@ extern "C" int ddtree_verify_attn_kv8(const void* q, const void* kv8_pool, const
 }
 
 extern "C" size_t ddtree_accept_workspace_bytes(const ddt_dims* dims, int32_t vocab) {
-  AcceptLayout w;
-  return accept_layout(dims, vocab, &w) == DDT_OK ? w.bytes : 0;
+  return check_accept(dims, vocab) == DDT_OK ? kStatusBytes : 0;
 }
 
 extern "C" int ddtree_accept(const void* logits, int32_t logits_fp32, int64_t logit_stride, int32_t vocab,
@@ -270,8 +264,7 @@ extern "C" int ddtree_accept(const void* logits, int32_t logits_fp32, int64_t lo
                              const int32_t* tree_len, const float* uniform, const float* temperature, int32_t* path,
                              int32_t* path_len, int32_t* next_token, const ddt_dims* dims, void* workspace,
                              size_t workspace_bytes, ddt_stream_t stream) {
-  AcceptLayout w;
-  int rc = accept_layout(dims, vocab, &w);
+  int rc = check_accept(dims, vocab);
   if (rc != DDT_OK) return rc;
   if (logit_stride < vocab || (draft_prob && draft_stride < vocab)) return DDT_ERR_DIMS;
   if (dims->batch == 0) return DDT_OK;
@@ -281,7 +274,7 @@ extern "C" int ddtree_accept(const void* logits, int32_t logits_fp32, int64_t lo
       !aligned(tree_len, 4) || !aligned(uniform, 4) || !aligned(temperature, 4) || !aligned(path, 4) || !aligned(path_len, 4) ||
       !aligned(next_token, 4) || !aligned(workspace, 256))
     return DDT_ERR_ALIGN;
-  if (workspace_bytes < w.bytes) return DDT_ERR_WORKSPACE;
+  if (workspace_bytes < kStatusBytes) return DDT_ERR_WORKSPACE;
   const int64_t rows = int64_t(dims->batch) * dims->num_nodes;
   const size_t nodes = size_t(rows) * 4, reqs = size_t(dims->batch) * 4;
   const struct { const void* p; size_t n; } in[] = {
@@ -297,7 +290,6 @@ extern "C" int ddtree_accept(const void* logits, int32_t logits_fp32, int64_t lo
   }
   int sms = 0;
   if ((rc = current_device(&sms)) != DDT_OK) return rc;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
   AcceptParams p = {};
   p.logits = logits;
   p.logit_stride = logit_stride;
@@ -311,18 +303,13 @@ extern "C" int ddtree_accept(const void* logits, int32_t logits_fp32, int64_t lo
   p.batch = dims->batch;
   p.nodes = dims->num_nodes;
   p.vocab = vocab;
-  p.row_cluster = row_cluster(rows, vocab, sms);
-  p.walk_cluster = row_cluster(dims->batch, vocab, sms);
-  p.row_max = reinterpret_cast<float*>(ws + w.max_off);
-  p.row_arg = reinterpret_cast<int32_t*>(ws + w.arg_off);
-  p.left = reinterpret_cast<unsigned long long*>(ws + w.left_off);
-  p.taken = reinterpret_cast<unsigned long long*>(ws + w.taken_off);
-  p.accepted = reinterpret_cast<int32_t*>(ws + w.accepted_off);
+  accept_grid(p.batch, vocab, draft_prob != nullptr, sms, &p);
   p.path = path;
   p.path_len = path_len;
   p.next_token = next_token;
-  p.status = reinterpret_cast<int32_t*>(ws);
+  p.status = static_cast<int32_t*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p.batch > 1 && !clear_status(workspace, s)) return DDT_ERR_LAUNCH;
   return launch_accept(p, !logits_fp32, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
 }
 

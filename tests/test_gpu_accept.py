@@ -119,7 +119,8 @@ def check(d, got, requests=None):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("batch,nodes,vocab,tree", [
     (1, 1, 1, "chain"), (1, 9, 2, "chain"), (64, 9, 33, "random"), (7, 33, 1001, "random"), (40, 9, 5003, "chain"),
-    (3, 65, 32768, "random"), (2, 128, 2050, "star"), (1, 5, 131072, "random"), (200, 4, 257, "star")])
+    (3, 65, 32768, "random"), (2, 128, 2050, "star"), (1, 5, 131072, "random"), (200, 4, 257, "star"),
+    (1, 3, 262144, "chain"), (12, 5, 100003, "random")])
 def test_trees(batch, nodes, vocab, tree, dtype, drawn):
     total = judged = 0
     for seed in range(2):

@@ -98,7 +98,7 @@ def test_accept_sizes(lib, bad):
     assert lib.ddtree_accept_workspace_bytes(ctypes.byref(dims(**bad)), 1000) == 0
 
 
-@pytest.mark.parametrize("bad", [dict(vocab=0), dict(vocab=(1 << 20) + 1, stride=1 << 21), dict(stride=999),
+@pytest.mark.parametrize("bad", [dict(vocab=0), dict(vocab=(1 << 18) + 1, stride=1 << 19), dict(stride=999),
                                  dict(draft_stride=999)])
 def test_accept_vocab(lib, bad):
     assert call(lib, "ddtree_accept", ACCEPT, dims(), **bad) == -2
@@ -112,7 +112,7 @@ def test_accept_pointers(lib):
         assert call(lib, "ddtree_accept", ACCEPT, dims(), **{name: None}) == -1, name
         assert call(lib, "ddtree_accept", ACCEPT, dims(), **{name: ACCEPT[name] + 1}) == -4, name
     assert call(lib, "ddtree_accept", ACCEPT, dims(), fp32=1, logits=A(1) + 2) == -4
-    assert call(lib, "ddtree_accept", ACCEPT, dims(), bytes=256) == -3
+    assert call(lib, "ddtree_accept", ACCEPT, dims(), bytes=255) == -3
 
 
 def test_accept_overlaps(lib):
