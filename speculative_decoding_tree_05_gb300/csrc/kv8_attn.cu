@@ -22,14 +22,14 @@
 // O^T takes 256 TMEM columns, so one CTA holds the whole output. By themselves the MMAs of
 // a tile take 1790 cycles with 64 rows, 1400 with 16.
 //
-// Per CTA (832 threads), one unit = (up to 64 (node, head) rows of a request, a share of its tiles):
-//   warp 0       TMEM; one lane issues S(t), dim group by dim group as stage t lands
+// Per CTA (896 threads), one unit = (up to 64 (node, head) rows of a request, a share of its tiles):
+//   warp 0       TMEM; one lane issues S(t) when stage t has landed
 //   warps 1-16   softmax: 16 keys x 16 rows each, in the 16x256b shape
 //   warp 17      one lane issues P.V(t) when P(t) is written
-//   warps 18-25  gather 64 keys per stage of 40 KB, three stages of four dim groups, each
-//                refilled as soon as its part of P.V is done: warps 18-21 two dim groups
-//                (two of five 128-byte pieces of a row) by 16-byte cp.async, warps 22-25
-//                the others by TMA gather4, at the same time
+//   warps 18-25  gather 64 keys per stage of 40 KB, three stages: warps 18-21 two of the five
+//                128-byte pieces of a row by 16-byte cp.async, warps 22-25 the others by TMA
+//                gather4, at the same time (an SM gathers more both ways than either way)
+//   warps 26-27  the keys' scales and row masks
 // A request's keys are its prefix and, behind it, all its tree rows, each with the rows
 // that see it. The tiles of the whole batch are cut into equal shares, whatever the
 // lengths; a request has its share of them, in equal units. One unit writes bf16 and the
@@ -43,12 +43,10 @@
 namespace ddt {
 namespace {
 
-constexpr int kThreads = 832;
+constexpr int kThreads = 896;
 constexpr int kSoftmax = 512;
-constexpr int kIssuePv = 17, kFirstCopier = 18, kFirstGather = 22;  // warps
+constexpr int kIssuePv = 17, kFirstCopier = 18, kFirstGather = 22, kFirstKey = 26;  // warps
 constexpr int kCopiers = 128;                       // threads that gather the copied groups
-constexpr int kCopied = 2;                          // dim groups gathered by cp.async
-constexpr int kGroups = 4;                          // dims {0-127}, {128-255}, {256-383}, {384-511 and rope}
 constexpr int kKeys = kKv8Keys;
 constexpr int kRows = kKv8Rows;
 constexpr int kStages = 3;
@@ -70,14 +68,13 @@ constexpr int kSmem = kOffBar + 512 + 1024;
 static_assert(kSmem <= 232448, "one CTA's shared memory");
 constexpr uint32_t kColS = 256;                     // O^T [0, 256), S buffers 2 x 64
 constexpr float kUnset = -1e30f;                    // running reference of a row that has seen no key
-// Weights are 2^(t - r + kLift) and r is raised when one would exceed 2^(kLift + kSlack) = 256
+// Weights are 2^(t - r + kLift) and r is raised when one would exceed 2^(kLift + kSlack) = 431
 // (e4m3 ends at 448).
-constexpr float kLift = 4.f, kSlack = 4.f;
+constexpr float kLift = 4.f, kSlack = 4.75f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct Shared {
-  uint64_t k_full[kStages][kGroups];
-  uint64_t k_empty[kStages][kGroups];  // this group's part of the tile's P.V is done (and those before it)
+  uint64_t k_full[kStages][2], k_empty[kStages][2];  // [0]: chunks 0 and 1, copied; [1]: the others, gathered
   uint64_t f_full[kStages];            // the keys' factors and masks
   uint64_t s_full[2], s_free[2];
   uint64_t p_ready[2];
@@ -110,6 +107,15 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 
 // Two weights in two 8-bit parts, e4m3 and what that leaves in e5m2. Through f16, whose 11 bits lose 2^-12 of a weight
@@ -228,12 +234,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.f_full[i], 4);
-      for (int x = 0; x < kGroups; ++x) {
-        // every copying thread's cp.async, or the gather warps' arrivals with their bytes
-        mbar_init(&sh.k_full[i][x], x < kCopied ? kCopiers : 4);
-        mbar_init(&sh.k_empty[i][x], 1);
-      }
+      mbar_init(&sh.k_full[i][0], kCopiers);  // every copying thread's cp.async
+      mbar_init(&sh.k_full[i][1], 4);         // four gather warps, with their bytes
+      mbar_init(&sh.k_empty[i][0], 1);        // P.V of the tile is done (and those before it)
+      mbar_init(&sh.k_empty[i][1], 1);        // its first half is, of the gathered chunks
+      mbar_init(&sh.f_full[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       const uint64_t d_k = smem_desc(base, 16, 1024, kSwizzle128B);
       const uint64_t d_q = smem_desc(base + kOffQ, 16, 1024, kSwizzle128B);
       int st = 0, ph = 0;
-      for (int t = 0; ok && t < n; ++t) {
+      for (int t = 0; t < n; ++t) {
         if (t >= 2 && !mbar_wait_abortable(&sh.s_free[t & 1], ((t >> 1) - 1) & 1, abort, false, __LINE__)) {
           ok = false;
           break;
@@ -346,26 +351,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         const uint64_t k = desc_advance(d_k, st * kStageBytes);
         const uint32_t d = tmem + kColS + (t & 1) * kRows;
 #pragma unroll
-        for (int x = 0; x < kGroups; ++x) {
+        for (int x = 0; x < 2; ++x) {  // the copied chunks land first
           if (!mbar_wait_abortable(&sh.k_full[st][x], ph, abort, false, __LINE__)) {
             ok = false;
             break;
           }
-          if (x < kCopied) fence_proxy_async_smem();  // written by cp.async
+          if (x == 0) fence_proxy_async_smem();  // written by cp.async
           tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            const uint64_t a = desc_advance(k, x * kChunk + ks * 32);
-            mma_f8_ss(d, a, desc_advance(d_q, x * kChunk + ks * 32), idesc8, x + ks > 0 ? 1u : 0u);
-            mma_f8_ss(d, a, desc_advance(d_q, (4 + x) * kChunk + ks * 32), idesc8, 1u);
-          }
-          if (x == kGroups - 1) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)  // the rope dims
-              mma_ss(d, desc_advance(k, 4 * kChunk + ks * 32), desc_advance(d_q, 8 * kChunk + ks * 32), idesc, 1u);
+          for (int ks = 8 * x; ks < 8 * x + 8; ++ks) {
+            const uint32_t at = (ks >> 2) * kChunk + (ks & 3) * 32;
+            mma_f8_ss(d, desc_advance(k, at), desc_advance(d_q, at), idesc8, ks > 0 ? 1u : 0u);
+            mma_f8_ss(d, desc_advance(k, at), desc_advance(d_q, 4 * kChunk + at), idesc8, 1u);
           }
         }
-        if (ok) mma_commit(&sh.s_full[t & 1]);
+        if (!ok) break;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)  // the rope dims
+          mma_ss(d, desc_advance(k, 4 * kChunk + ks * 32), desc_advance(d_q, 8 * kChunk + ks * 32), idesc, 1u);
+        mma_commit(&sh.s_full[t & 1]);
         if (++st == kStages) st = 0, ph ^= 1;
       }
       mma_commit(&sh.drain);
@@ -388,14 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         const uint64_t v = desc_advance(d_v, st * kStageBytes), hi = desc_advance(d_p, (t & 1) * 2 * kPart);
         const uint32_t more = t > 0 ? 1u : 0u;
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int y = 0; y < 4; ++y) {
+          const int mt = (y + 2) & 3;  // the gathered chunks first: they take longest to come
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
             const uint64_t a = desc_advance(v, mt * kChunk + ks * 4096);
             mma_f8_ss(tmem + mt * kRows, a, desc_advance(hi, ks * 2048), idesc_hi, ks > 0 ? 1u : more);
             mma_f8_ss(tmem + mt * kRows, a, desc_advance(hi, kPart + ks * 2048), idesc_lo, 1u);
           }
-          mma_commit(&sh.k_empty[st][mt]);
+          if (y & 1) mma_commit(&sh.k_empty[st][y == 1]);
         }
         if (++st == kStages) st = 0;
       }
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         tree_slot[i] = __ldg(p.tree_slot_idx + static_cast<int64_t>(un.b) * p.nodes + i);
         tree_mask[i] = 0;
       }
-      bar_sync(4, 256);
+      bar_sync(4, kThreads - kFirstCopier * 32);
       const int first = row0 / p.heads, last = (row0 + rows - 1) / p.heads;
       if (i <= last - first) {
         const int lo = max(0, (first + i) * p.heads - row0), hi = min(rows, (first + i + 1) * p.heads - row0);
@@ -438,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         }
         if (flags) atomicOr(&sh.flags, flags);
       }
-      bar_sync(4, 256);
+      bar_sync(4, kThreads - kFirstCopier * 32);
     }
     // Key i of the request: its slot as read. Nothing is computed from a value in the tile that reads it: an
     // immediate use stalls the warp for the read (800 cycles a tile).
@@ -464,70 +469,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     };
     using P16 = std::integral_constant<int, 16>;
     using P8 = std::integral_constant<int, 8>;
-    const bool copier = warp < kFirstGather;
-    const int r0 = 16 * (copier ? warp - kFirstCopier : warp - kFirstGather);  // the warp's first key of a tile, 16 of them
-    const int k = lane < 16 ? r0 + lane : kKeys;           // the lane's key
-    // A key's row takes two dependent reads, its slot and its scale, each a tile ahead of its use.
+    const bool copier = warp < kFirstGather, gather = !copier && warp < kFirstKey;
+    // the warp's first key of a tile, 16 of them (a key warp: 32); the lane's key
+    const int r0 = copier ? 16 * (warp - kFirstCopier) : gather ? 16 * (warp - kFirstGather) : 32 * (warp - kFirstKey);
+    const int k = lane < 16 || warp >= kFirstKey ? r0 + lane : kKeys;
     int slot_now = read_slot(0, k), slot_next = read_slot(1, k);
-    float scale_now = copier && in_pool(slot_now) ? __ldg(p.scale + slot_now) : 1.f;
+    float scale_now = 1.f;
+    if (warp >= kFirstKey && in_pool(slot_now)) scale_now = __ldg(p.scale + slot_now);
     int st = 0, ph = 0, done = 0;
-    auto wait_empty = [&](int t, int x) {
-      const bool w = t < kStages || mbar_wait_abortable(&sh.k_empty[st][x], ph ^ 1, abort, false, __LINE__);
-      return __all_sync(0xffffffffu, w) != 0;
-    };
-    for (int t = 0; ok && t < n; ++t) {
+    for (int t = 0; t < n; ++t) {
       const int i = (t0 + t) * kKeys + k;
       uint64_t mask = 0;  // of the rows that see the key
       if (k < kKeys && i < keys) mask = i < L ? full : tree_mask[i - L];
-      if (mask != 0 && !in_pool(slot_now)) {
-        mask = 0;
-        atomicOr(&sh.flags, kStatusBadSlot);
-      }
+      const bool bad = mask != 0 && !in_pool(slot_now);
+      if (bad) mask = 0;
       const int slot = mask != 0 ? slot_now : -1;
       const float scale = scale_now;
+      // A key takes two dependent reads, its slot and its scale, each a tile ahead of its use.
       slot_now = slot_next;
-      if (copier) scale_now = in_pool(slot_now) ? __ldg(p.scale + slot_now) : 1.f;
+      if (warp >= kFirstKey && in_pool(slot_now)) scale_now = __ldg(p.scale + slot_now);
       slot_next = read_slot(t + 2, k);
       const uint32_t sbase = base + st * kStageBytes;
+      const bool empty = t < kStages || mbar_wait_abortable(&sh.k_empty[st][gather], ph ^ 1, abort, false, __LINE__);
+      if (!__all_sync(0xffffffffu, empty)) {
+        ok = false;
+        break;
+      }
       if (copier) {
-        if (!wait_empty(t, 0)) {
-          ok = false;
-          break;
-        }
-        copy_rows(sbase, r0, 0, P8(), slot);
+        copy_rows(sbase, r0, 0, P16(), slot);
         cp_async_arrive_noinc(&sh.k_full[st][0]);
-        if (!wait_empty(t, 1)) {
-          ok = false;
-          break;
-        }
-        copy_rows(sbase, r0, 1, P8(), slot);
-        cp_async_arrive_noinc(&sh.k_full[st][1]);
-        if (lane < 16) {
-          reinterpret_cast<uint64_t*>(smem + kOffMask)[st * kKeys + k] = mask;
-          // a scale that is not positive and finite: NaN for the rows that see the key
-          const bool fine = scale > 0.f && scale < CUDART_INF_F;
-          reinterpret_cast<float4*>(smem + kOffKey)[st * kKeys + k] =
-              fine ? make_float4(scale, log2f(scale), 1.f / scale, 0.f) : make_float4(CUDART_NAN_F, 0.f, 1.f, 0.f);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.f_full[st]);  // releases the factors and masks
-      } else {
-        if (!wait_empty(t, 2) || !wait_empty(t, 3)) {
-          ok = false;
-          break;
-        }
+      } else if (gather) {
         if (__all_sync(0xffffffffu, slot >= 0 || lane >= 16)) {
           // lanes 0-11: four of the warp's keys, one of the three chunks
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&sh.k_full[st][2], 16 * 128);
-            mbar_arrive_expect_tx(&sh.k_full[st][3], 16 * 256);
-          }
+          if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[st][1], 16 * 384);
           __syncwarp();
           const int q = 4 * (lane & 3), c = 2 + (lane >> 2);
           const int ra = __shfl_sync(0xffffffffu, slot, q), rb = __shfl_sync(0xffffffffu, slot, q + 1);
           const int rc = __shfl_sync(0xffffffffu, slot, q + 2), rd = __shfl_sync(0xffffffffu, slot, q + 3);
-          if (lane < 12)
-            tma_gather4(sbase + c * kChunk + (r0 + q) * 128, &p.tmap, c * 128, ra, rb, rc, rd, &sh.k_full[st][min(c, 3)]);
+          if (lane < 12) tma_gather4(sbase + c * kChunk + (r0 + q) * 128, &p.tmap, c * 128, ra, rb, rc, rd, &sh.k_full[st][1]);
         } else {
           // a key is masked (the end of the keys, a bad slot): zero-filled copies
           copy_rows(sbase, r0, 2, P16(), slot);
@@ -536,21 +515,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
           cp_async_wait<0>();
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&sh.k_full[st][2]);
-            mbar_arrive(&sh.k_full[st][3]);
-          }
+          if (lane == 0) mbar_arrive(&sh.k_full[st][1]);
         }
+      } else {
+        if (bad) atomicOr(&sh.flags, kStatusBadSlot);
+        reinterpret_cast<uint64_t*>(smem + kOffMask)[st * kKeys + k] = mask;
+        // a scale that is not positive and finite: NaN for the rows that see the key
+        const bool fine = scale > 0.f && scale < CUDART_INF_F;
+        reinterpret_cast<float4*>(smem + kOffKey)[st * kKeys + k] =
+            fine ? make_float4(scale, log2f(scale), 1.f / scale, 0.f) : make_float4(CUDART_NAN_F, 0.f, 1.f, 0.f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.f_full[st]);
       }
       done = t + 1;
       if (++st == kStages) st = 0, ph ^= 1;
     }
     cp_async_wait<0>();
-    if (!ok && !copier)  // after a give-up the gathers still in flight land before the CTA exits
-      for (int v = max(0, done - kStages); v < done; ++v) {
-        mbar_wait(&sh.k_full[v % kStages][2], (v / kStages) & 1, 1u << 16);
-        mbar_wait(&sh.k_full[v % kStages][3], (v / kStages) & 1, 1u << 16);
-      }
+    if (!ok && gather)  // after a give-up the gathers still in flight land before the CTA exits
+      for (int v = max(0, done - kStages); v < done; ++v) mbar_wait(&sh.k_full[v % kStages][1], (v / kStages) & 1, 1u << 14);
   } else {
     // ------------------------------------------------------------------ softmax
     const int quarter = warp & 3, part4 = (warp - 1) >> 2;  // lanes of TMEM, a quarter of the rows
@@ -580,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     }
     bool failed = false;  // a wait of this thread ran out: the warps leave together at the next barrier
     auto wait_pv = [&](int t) {  // P.V(t) has read P, and O^T holds every tile up to t
-      if (!mbar_wait_abortable(&sh.k_empty[t % kStages][kGroups - 1], (t / kStages) & 1, abort, false, __LINE__)) failed = true;
+      if (!mbar_wait_abortable(&sh.k_empty[t % kStages][0], (t / kStages) & 1, abort, false, __LINE__)) failed = true;
       tc_fence_after();
     };
     // column sums or maxima over the 16 keys of the warp, to scratch [4 quarters][64]
@@ -596,6 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     };
     int st = 0, ph = 0;
     for (int t = 0; t < n; ++t) {
+      // A look at shared memory takes 100 to 300 cycles beside the gathers, so what can be looked at ahead of the
+      // scores is: P.V of the tile before the last, which frees the buffer, and the keys' masks and factors.
+      const bool p_free = t < 2 || mbar_test_wait(&sh.k_empty[(t - 2) % kStages][0], ((t - 2) / kStages) & 1);
       if (!mbar_wait_abortable(&sh.f_full[st], ph, abort, false, __LINE__)) failed = true;
       const uint64_t m0 = masks[st * kKeys + r0], m1 = masks[st * kKeys + r0 + 8];
       const float4 f0 = factors[st * kKeys + r0], f1 = factors[st * kKeys + r0 + 8];
@@ -691,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         hi[i] = h2[0] | (h2[1] << 16);
         lo[i] = l2[0] | (l2[1] << 16);
       }
-      if (!raise && t > 1) wait_pv(t - 2);  // the buffer is free
+      if (!p_free && !raise) wait_pv(t - 2);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t at = p_at[i] + (t & 1) * 2 * kPart;
@@ -731,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   }
   // the softmax and gather warps write O: quarter of the lanes by warp, six warps a quarter
   if (warp > 0) {
-    if (!bar_red_or(2, kThreads - 32, !ok) && warp != kIssuePv) {
+    if (!bar_red_or(2, kThreads - 32, !ok) && warp != kIssuePv && warp < kFirstKey) {
       tc_fence_after();
       const float* inv_l = reinterpret_cast<const float*>(smem + kOffAlpha);
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
