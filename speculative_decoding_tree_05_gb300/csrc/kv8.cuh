@@ -53,13 +53,47 @@ constexpr int kKv8Rows = 64;      // (node, head) rows of one group
 constexpr int kKv8Keys = 64;      // keys of a tile
 constexpr int kKv8MaxShared = 1024;  // requests of a batch whose tiles are shared out
 
+constexpr int kKv8Chunk = kKv8Keys * 128;         // 128 bytes of 64 rows
+constexpr int kKv8Image = 9 * kKv8Chunk + 256;    // a group's query rows: 4 chunks, 4 of the second parts, rope; factors
+
+// Rows of a group, within its request, if `nodes` nodes are active (rows <= 0: none).
+struct Kv8Group {
+  int row0, rows;
+};
+__host__ __device__ inline Kv8Group kv8_group(int heads, int group_nodes, int nodes, int g) {
+  Kv8Group u;
+  if (heads <= kKv8Rows) {
+    u.row0 = g * group_nodes * heads;
+    const int n = nodes - g * group_nodes;
+    u.rows = (n < group_nodes ? n : group_nodes) * heads;
+  } else {
+    const int slices = (heads + kKv8Rows - 1) / kKv8Rows, t = g / slices, sl = g - t * slices, left = heads - sl * kKv8Rows;
+    u.row0 = t * heads + sl * kKv8Rows;
+    u.rows = t < nodes ? (left < kKv8Rows ? left : kKv8Rows) : 0;
+  }
+  return u;
+}
+
+struct Kv8PrepareParams {
+  const uint16_t* q;             // bf16 [B, T, H, 576]
+  const int32_t* prefix_len;
+  const int32_t* tree_len;
+  uint8_t* images;               // [B, groups, kKv8Image]
+  uint16_t* out;                 // rows of inactive nodes are written
+  float* lse;
+  int32_t batch, nodes, heads, max_prefix_len, groups, group_nodes;
+  float scale_log2;              // sm_scale * log2(e)
+  int32_t* status;               // written as a whole; the units add to it
+};
+cudaError_t launch_kv8_prepare(const Kv8PrepareParams& p, cudaStream_t stream);
+
 struct Kv8Piece {                 // a request's units, for the merge
   int32_t first, count;
 };
 
 struct Kv8AttnParams {
   CUtensorMap tmap;              // pool as [N][640] bytes, box 128 bytes x 1 row, 128-byte swizzle
-  const uint16_t* q;             // bf16 [B, T, H, 576]
+  const uint8_t* images;         // [B, groups, kKv8Image], of the kernel before
   const uint8_t* kv;             // [N, 640]
   const float* scale;            // [N]
   const int32_t* slot_idx;       // [B, slot_stride]
@@ -73,13 +107,12 @@ struct Kv8AttnParams {
   int32_t group_nodes;           // nodes of a group (heads <= 64; else a group is 64 heads of one node)
   int32_t shares;                // the batch's tiles in this many equal shares; 0: one unit a request
   int32_t units;                 // bound on the units of a group: shares + batch - 1, or batch
-  float scale_log2;              // sm_scale * log2(e)
   float* o_part;                 // fp32 [units, T * H, 512], normalised
   float* lse_part;               // fp32 [units, T * H], natural log
   Kv8Piece* pieces;              // [B]
-  int32_t* flags;                // [units, groups] status bits of each unit
   uint16_t* out;                 // bf16 [B, T, H, 512]
   float* lse;                    // fp32 [B, T, H]
+  int32_t* status;
 #ifdef DDT_TEST_HOOKS
   int32_t test_keep_back;        // tile whose score buffer is not handed back (-1: none)
 #endif
@@ -91,14 +124,11 @@ struct Kv8MergeParams {
   const float* o_part;
   const float* lse_part;
   const Kv8Piece* pieces;
-  const int32_t* flags;
-  const int32_t* prefix_len;
   const int32_t* tree_len;
   uint16_t* out;
   float* lse;
-  int32_t batch, nodes, heads, max_prefix_len, units, groups;
+  int32_t batch, nodes, heads;
   int32_t warps;                 // warps that share a row: 1, 2, 4, 8 or 16
-  int32_t* status;               // written as a whole
 };
 cudaError_t launch_kv8_merge(const Kv8MergeParams& p, cudaStream_t stream);
 

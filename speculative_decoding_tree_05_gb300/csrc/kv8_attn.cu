@@ -34,6 +34,7 @@
 // that see it. The tiles of the whole batch are cut into equal shares, whatever the
 // lengths; a request has its share of them, in equal units. One unit writes bf16 and the
 // log-sum-exp at once, else each writes its normalised O and the merge kernel joins them.
+// The query rows come cut and laid out from the kernel before (kv8_prepare.cu).
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <type_traits>
@@ -50,17 +51,17 @@ constexpr int kCopiers = 128;                       // threads that gather the c
 constexpr int kKeys = kKv8Keys;
 constexpr int kRows = kKv8Rows;
 constexpr int kStages = 3;
-constexpr int kChunk = kKeys * 128;                 // 128 bytes of 64 keys: 8 KB
+constexpr int kChunk = kKv8Chunk;                   // 128 bytes of 64 keys: 8 KB
 constexpr int kStageBytes = 5 * kChunk;             // 40960
 constexpr int kOffQ = kStages * kStageBytes;        // hi: 4 chunks, lo: 4, rope: 1
-constexpr int kOffP = kOffQ + 9 * kChunk;           // [2 buffers][2 parts][64 keys][64 rows]
+constexpr int kOffQs = kOffQ + 9 * kChunk;          // [64] the rows' factors of a score
+constexpr int kOffP = kOffQs + 1024;                // [2 buffers][2 parts][64 keys][64 rows]
 constexpr int kPart = kKeys * kRows;                // 4096
 constexpr int kOffMask = kOffP + 4 * kPart;         // [stages][64] row masks of the stage's keys
 constexpr int kOffKey = kOffMask + kStages * kKeys * 8;   // [stages][64] (s, log2 s, 1 / s, -)
 constexpr int kOffMax = kOffKey + kStages * kKeys * 16;   // [64] running reference
 constexpr int kOffAlpha = kOffMax + kRows * 4;      // [64] rescale factors, later 1 / row sums
-constexpr int kOffQs = kOffAlpha + kRows * 4;       // [64] the rows' factors of a score
-constexpr int kOffTree = kOffQs + kRows * 4;        // [128] row masks of the tree rows
+constexpr int kOffTree = kOffAlpha + kRows * 4;        // [128] row masks of the tree rows
 constexpr int kOffSlot = kOffTree + kMaxNodes * 8;  // [128] their slots
 constexpr int kOffPar = kOffSlot + kMaxNodes * 4;   // [128] their parents
 constexpr int kOffBar = kOffPar + kMaxNodes * 4;
@@ -78,6 +79,7 @@ struct Shared {
   uint64_t f_full[kStages];            // the keys' factors and masks
   uint64_t s_full[2], s_free[2];
   uint64_t p_ready[2];
+  uint64_t q_full;
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -204,17 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   const int g = blockIdx.x, unit = blockIdx.y;
   grid_dep_launch();  // the merge kernel
   const Unit un = find_unit(p, unit, lane);
-  int32_t* my_flags = p.flags + static_cast<int64_t>(unit) * p.groups + g;
   const int nodes = un.b < 0 ? 0 : kv8_nodes(p.tree_len, un.b, p.nodes);  // active ones
-  int row0, rows;  // of the group, within the request
-  if (p.heads <= kRows) {
-    row0 = g * p.group_nodes * p.heads;
-    rows = min(p.group_nodes, nodes - g * p.group_nodes) * p.heads;
-  } else {
-    const int slices = (p.heads + kRows - 1) / kRows, t = g / slices, sl = g - t * slices;
-    row0 = t * p.heads + sl * kRows;
-    rows = t < nodes ? min(kRows, p.heads - sl * kRows) : 0;
-  }
+  const Kv8Group gr = kv8_group(p.heads, p.group_nodes, nodes, g);
+  const int row0 = gr.row0, rows = gr.rows;
   if (un.b >= 0 && un.k == 0 && g == 0 && tid == 0) {
     Kv8Piece piece;
     piece.first = un.first;
@@ -222,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     p.pieces[un.b] = piece;
   }
   if (un.b < 0 || rows <= 0) {
-    if (tid == 0) *my_flags = 0;
+    grid_dep_wait();  // (this grid is not done before the one that it follows)
     return;
   }
   const int L = kv8_len(p.prefix_len, un.b, p.max_prefix_len);
@@ -230,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   const int tiles = (keys + kKeys - 1) / kKeys;
   const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * un.k / un.count);
   const int n = static_cast<int>(static_cast<int64_t>(tiles) * (un.k + 1) / un.count) - t0;  // at least one
-  const int64_t trow0 = static_cast<int64_t>(un.b) * p.nodes * p.heads + row0;  // of q, out and lse
+  const int64_t trow0 = static_cast<int64_t>(un.b) * p.nodes * p.heads + row0;  // of out and lse
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -246,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       mbar_init(&sh.p_ready[i], kSoftmax / 32);
     }
     mbar_init(&sh.drain, 2);
+    mbar_init(&sh.q_full, 1);
     sh.abort = 0;
     sh.fail[0] = sh.fail[1] = 0;
     sh.flags = 0;
@@ -263,87 +258,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   const uint32_t tmem = sh.tmem_base;
   bool ok = true;
 
-  if (warp < kFirstCopier) {
-    // ------------------------------------------------------------------ the group's query rows, in two 8-bit parts
-    const uint16_t* q = p.q + trow0 * kDqk;
-    float* qs = reinterpret_cast<float*>(smem + kOffQs);
-    {
-      uint4 a[4], b[4];
-      uint32_t c[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {  // all rows' loads at once
-        const int r = warp + kFirstCopier * k;
-        const uint16_t* src = q + static_cast<int64_t>(r < rows ? r : 0) * kDqk;
-        a[k] = __ldg(reinterpret_cast<const uint4*>(src) + lane);
-        b[k] = __ldg(reinterpret_cast<const uint4*>(src + 256) + lane);
-        c[k] = __ldg(reinterpret_cast<const uint32_t*>(src + kDv) + lane);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = warp + kFirstCopier * k;
-        if (r >= kRows) break;
-        const uint32_t w[9] = {a[k].x, a[k].y, a[k].z, a[k].w, b[k].x, b[k].y, b[k].z, b[k].w, c[k]};
-        uint32_t top = 0, turned = 0;  // the largest magnitudes, latent and rope, as bf16 bits
-        bool fine = true;
-#pragma unroll
-        for (int i = 0; i < 9; ++i) {
-          const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-          fine = fine && lo < 0x7f80u && hi < 0x7f80u;
-          if (i < 8)
-            top = max(top, max(lo, hi));
-          else
-            turned = max(lo, hi);
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
-        turned = __reduce_max_sync(0xffffffffu, turned);
-        fine = __all_sync(0xffffffffu, fine);
-        // the least power of two that brings the row within 448 = 1.75 2^8 (7 bits behind the exponent) and its rope
-        // values below 2^121
-        const int e = max(static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0),
-                          max(static_cast<int>(turned >> 7) - 127 - 120, kKv8MinExp));
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        const bool live = r < rows && fine;
-        uint32_t hi4[4], lo4[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t h2[2], l2[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t v = w[2 * i + j];
-            const float x = __uint_as_float(v << 16) * inv, y = __uint_as_float(v & 0xffff0000u) * inv;
-            h2[j] = pack_e4m3x2(x, y);
-            float hx, hy;
-            unpack_e4m3x2(static_cast<uint16_t>(h2[j]), hx, hy);
-            l2[j] = pack_e4m3x2(x - hx, y - hy);  // (the differences are exact)
-          }
-          hi4[i] = live ? h2[0] | (h2[1] << 16) : 0u;
-          lo4[i] = live ? l2[0] | (l2[1] << 16) : 0u;
-        }
-        // dims 8 lane + {0..7} in chunk lane / 16, dims 256 + 8 lane + {0..7} two chunks further
-        const uint32_t at = (lane >> 4) * kChunk + r * 128 + (((((lane & 15) >> 1) ^ (r & 7)) << 4) | ((lane & 1) << 3));
-        uint8_t* hi = smem + kOffQ + at;
-        *reinterpret_cast<uint2*>(hi) = make_uint2(hi4[0], hi4[1]);
-        *reinterpret_cast<uint2*>(hi + 2 * kChunk) = make_uint2(hi4[2], hi4[3]);
-        *reinterpret_cast<uint2*>(hi + 4 * kChunk) = make_uint2(lo4[0], lo4[1]);
-        *reinterpret_cast<uint2*>(hi + 6 * kChunk) = make_uint2(lo4[2], lo4[3]);
-        const uint32_t rope = live ? pack_bf16x2(__uint_as_float(w[8] << 16) * inv, __uint_as_float(w[8] & 0xffff0000u) * inv) : 0u;
-        *reinterpret_cast<uint32_t*>(smem + kOffQ + 8 * kChunk + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2))) = rope;
-        // a row that is not finite gives NaN to its own scores alone
-        if (lane == 0) qs[r] = r >= rows ? 0.f : fine ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * p.scale_log2 : CUDART_NAN_F;
-      }
-    }
-    fence_proxy_async_smem();
-    bar_sync(3, kFirstCopier * 32);
-  }
-
   if (warp == 0) {
     if (elect_one()) {
+      grid_dep_wait();  // the query rows: what comes before overlaps their making
+      mbar_arrive_expect_tx(&sh.q_full, kKv8Image);
+      bulk_load(base + kOffQ, p.images + (static_cast<int64_t>(un.b) * p.groups + g) * kKv8Image, kKv8Image, &sh.q_full);
+      ok = mbar_wait_abortable(&sh.q_full, 0, abort, false, __LINE__);
       // scores of all 64 columns (rows of zeros behind the group's): every column read out is defined
       const uint32_t idesc8 = idesc_f8_f32(64, kRows, kE4m3, kE4m3, false, false), idesc = idesc_bf16_f32(64, kRows, false, false);
       const uint64_t d_k = smem_desc(base, 16, 1024, kSwizzle128B);
       const uint64_t d_q = smem_desc(base + kOffQ, 16, 1024, kSwizzle128B);
       int st = 0, ph = 0;
-      for (int t = 0; t < n; ++t) {
+      for (int t = 0; ok && t < n; ++t) {
         if (t >= 2 && !mbar_wait_abortable(&sh.s_free[t & 1], ((t >> 1) - 1) & 1, abort, false, __LINE__)) {
           ok = false;
           break;
@@ -546,6 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     const uint64_t full = rows == 64 ? ~0ull : ((1ull << rows) - 1);
     // of this thread's rows, two by two: sums, score factors and (lowered by kLift) references
     uint64_t l[2], qs[2], m[2];
+    bool failed = !mbar_wait_abortable(&sh.q_full, 0, abort, false, __LINE__);  // a wait of this thread ran out: the warps leave together at the next barrier
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] = f32x2(0.f, 0.f);
@@ -560,7 +487,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       const int key = r0 + 8 * (lane & 1), col = (c0 & ~3) + 8 * i;
       p_at[i] = base + kOffP + key * 64 + ((((col >> 4) ^ ((key >> 1) & 3)) << 4) | (col & 15));
     }
-    bool failed = false;  // a wait of this thread ran out: the warps leave together at the next barrier
     auto wait_pv = [&](int t) {  // P.V(t) has read P, and O^T holds every tile up to t
       if (!mbar_wait_abortable(&sh.k_empty[t % kStages][0], (t / kStages) & 1, abort, false, __LINE__)) failed = true;
       tc_fence_after();
@@ -714,37 +640,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       }
     }
   }
-  // the softmax and gather warps write O: quarter of the lanes by warp, six warps a quarter
+  // O through the stages, which are free: rows of 512 values, as they lie in memory, stored in bulk. The softmax and
+  // gather warps: quarter of the lanes by warp, six warps a quarter, 16 rows of 32 dims at a time.
   if (warp > 0) {
-    if (!bar_red_or(2, kThreads - 32, !ok) && warp != kIssuePv && warp < kFirstKey) {
+    const bool fine = !bar_red_or(2, kThreads - 32, !ok);
+    if (fine && warp != kIssuePv && warp < kFirstKey) {
       tc_fence_after();
       const float* inv_l = reinterpret_cast<const float*>(smem + kOffAlpha);
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      // lane = value dim: each row's store is 128 contiguous bytes per warp
 #pragma unroll 1
-      for (int k0 = warp < kIssuePv ? (warp - 1) >> 2 : (warp - 2) >> 2; k0 < 32; k0 += 6) {
-        const int mt = k0 >> 3, cc = (k0 & 7) * 8;
+      for (int k0 = warp < kIssuePv ? (warp - 1) >> 2 : (warp - 2) >> 2; k0 < 16; k0 += 6) {
+        const int mt = k0 & 3, cc = (k0 >> 2) * 16;
         if (cc >= rows) continue;
-        uint32_t o[8];
-        tmem_ld8(tmem + lane_off + mt * kRows + cc, o);
-        const int dim = mt * 128 + (warp & 3) * 32;
+        uint32_t o[16];
+        tmem_ld16(tmem + lane_off + mt * kRows + cc, o);
+        const int dim = mt * 128 + (warp & 3) * 32 + lane;  // lane = value dim
         if (un.count == 1) {
           // two rows a store: even lanes hold a pair of dims of the first, odd lanes of the second
-          uint16_t* dst = p.out + (trow0 + cc + (lane & 1)) * kDv + dim + (lane & ~1);
+          uint32_t* dst = reinterpret_cast<uint32_t*>(smem) + ((cc + (lane & 1)) * kDv + (dim & ~1)) / 2;
 #pragma unroll
-          for (int k = 0; k < 8; k += 2) {
+          for (int k = 0; k < 16; k += 2) {
             const float x = __uint_as_float(o[k]) * inv_l[cc + k], y = __uint_as_float(o[k + 1]) * inv_l[cc + k + 1];
             const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
-            if (cc + k + (lane & 1) < rows)
-              *reinterpret_cast<uint32_t*>(dst + k * kDv) = lane & 1 ? pack_bf16x2(got, y) : pack_bf16x2(x, got);
+            dst[k * (kDv / 2)] = lane & 1 ? pack_bf16x2(got, y) : pack_bf16x2(x, got);
           }
         } else {
-          float* dst = p.o_part + (static_cast<int64_t>(unit) * p.nodes * p.heads + row0 + cc) * kDv + dim + lane;
+          float* dst = reinterpret_cast<float*>(smem) + cc * kDv + dim;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (cc + k < rows) dst[k * kDv] = __uint_as_float(o[k]) * inv_l[cc + k];
+          for (int k = 0; k < 16; ++k) dst[k * kDv] = __uint_as_float(o[k]) * inv_l[cc + k];
         }
       }
+      fence_proxy_async_smem();
+    }
+    bar_sync(2, kThreads - 32);
+    if (fine && warp == kIssuePv && elect_one()) {
+      const uint32_t bytes = rows * kDv * (un.count == 1 ? 2 : 4);
+      void* dst = un.count == 1 ? static_cast<void*>(p.out + trow0 * kDv)
+                                : p.o_part + (static_cast<int64_t>(unit) * p.nodes * p.heads + row0) * kDv;
+      bulk_store(dst, base, bytes);
+      bulk_store_wait();
     }
   }
   if (!ok) {
@@ -754,7 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tid == 0) *my_flags = sh.flags;
+  if (tid == 0 && sh.flags != 0) {
+    grid_dep_wait();  // (the status word has been written)
+    atomicOr(p.status, sh.flags);
+  }
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -765,8 +702,17 @@ cudaError_t configure_kv8_attn() {
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnParams& p, cudaStream_t stream) {
-  kv8_attn_kernel<<<dim3(p.groups, p.units), kThreads, kSmem, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(p.groups, p.units);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_attn_kernel, p);
 }
 
 }  // namespace ddt

@@ -1,11 +1,10 @@
-// kv8_merge.cu -- the merge of a request's units of attention over the 8-bit cache, and the call's status word.
+// kv8_merge.cu -- the merge of a request's units of attention over the 8-bit cache.
 //
 // out = sum over the units of w_u o_u / sum of w_u with w_u = exp(lse_u - max), the o_u
 // normalised; lse = max + log of the sum of w_u. A row is shared by 1 to 16 warps, each
 // with every 16th (or so) unit, four units' loads in flight at a time. Bound by reading
 // the partials, which the attention kernel has just written to L2: 2052 bytes a row and unit.
-// Rows of one unit are written by that unit. The last block ORs the units' status bits
-// into one word, which nothing has to clear before the call.
+// Rows of one unit are written by that unit.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include "kv8.cuh"
@@ -23,43 +22,21 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_merge_kernel(const __grid_con
   __shared__ float sum_sh[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_wait();  // the partials
-  if (blockIdx.x == gridDim.x - 1) {
-    int bits = 0;
-    const int64_t all = static_cast<int64_t>(p.units) * p.groups;
-    for (int64_t i = tid; i < all; i += kWarps * 32) bits |= __ldcg(p.flags + i);
-    for (int i = tid; i < p.batch; i += kWarps * 32) {
-      const int L = __ldg(p.prefix_len + i);
-      if (L < 0 || L > p.max_prefix_len) bits |= kStatusBadPrefix;
-      const int n = p.tree_len ? __ldg(p.tree_len + i) : 0;
-      if (n < 0 || n > p.nodes) bits |= kStatusBadTreeLen;
-    }
-    bits = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bits)));
-    int* all_bits = reinterpret_cast<int*>(sum_sh);
-    if (lane == 0) all_bits[warp] = bits;
-    __syncthreads();
-    if (tid == 0) {
-      for (int i = 1; i < kWarps; ++i) bits |= all_bits[i];
-      *p.status = bits;
-    }
-    return;
-  }
   const int per_block = kWarps / p.warps, mine = warp % p.warps;
   const int64_t rows = static_cast<int64_t>(p.nodes) * p.heads, all_rows = rows * p.batch;
   const int64_t grow = static_cast<int64_t>(blockIdx.x) * per_block + warp / p.warps;
   int count = 0, first = 0;
   int64_t r = 0;
-  bool active = false;
   if (grow < all_rows) {
     const int b = static_cast<int>(grow / rows);
     r = grow - b * rows;
-    active = r < static_cast<int64_t>(kv8_nodes(p.tree_len, b, p.nodes)) * p.heads;
-    if (active) {
+    if (r < static_cast<int64_t>(kv8_nodes(p.tree_len, b, p.nodes)) * p.heads) {
       const Kv8Piece* piece = p.pieces + b;
       first = __ldcg(&piece->first);
       count = __ldcg(&piece->count);
     }
   }
-  const bool join = active && count > 1;
+  const bool join = count > 1;
   float4 acc[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);  // dims 4 lane + 128 j + {0..3}
@@ -113,8 +90,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_merge_kernel(const __grid_con
       }
     }
   }
-  if (grow >= all_rows || (active && !join)) return;
-  // (inactive rows: zeros and -inf)
+  if (!join) return;
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
   uint2* dst = reinterpret_cast<uint2*>(p.out + grow * kDv);
 #pragma unroll
@@ -131,7 +107,7 @@ cudaError_t launch_kv8_merge(const Kv8MergeParams& p, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   const int64_t rows = static_cast<int64_t>(p.batch) * p.nodes * p.heads, per_block = kWarps / p.warps;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + per_block - 1) / per_block + 1));
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + per_block - 1) / per_block));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cfg.attrs = attr;

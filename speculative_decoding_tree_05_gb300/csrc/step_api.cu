@@ -21,7 +21,7 @@ bool clear_status(void* workspace, cudaStream_t s) {
 
 struct Kv8Layout {
   int groups, group_nodes, shares, units;
-  size_t pieces_off, flags_off, lse_off, o_off, bytes;
+  size_t pieces_off, images_off, lse_off, o_off, bytes;
 };
 
 // Costs in tiles of 64 keys: of a unit (its prologue, the pipeline's fill, its output),
@@ -70,8 +70,8 @@ int kv8_layout(const ddt_dims* d, int sm_count, Kv8Layout* w) {
   w->units = static_cast<int>(units);
   const size_t rows = size_t(T) * H, part = w->shares > 1 ? size_t(units) * rows : 0;
   w->pieces_off = kStatusBytes;
-  w->flags_off = align_up(w->pieces_off + size_t(B) * sizeof(Kv8Piece), 256);
-  w->lse_off = align_up(w->flags_off + size_t(units) * w->groups * sizeof(int32_t), 256);
+  w->images_off = align_up(w->pieces_off + size_t(B) * sizeof(Kv8Piece), 256);
+  w->lse_off = w->images_off + size_t(B) * w->groups * kKv8Image;
   w->o_off = align_up(w->lse_off + part * sizeof(float), 256);
   w->bytes = w->o_off + part * kDv * sizeof(float);
   return DDT_OK;
@@ -208,7 +208,7 @@ extern "C" int ddtree_verify_attn_kv8(const void* q, const void* kv8_pool, const
   p.test_keep_back = g_test_keep_back;
 #endif
   if (!encode_kv8_map(&p.tmap, kv8_pool, dims->pool_slots)) return DDT_ERR_LAUNCH;
-  p.q = static_cast<const uint16_t*>(q);
+  p.images = ws + w.images_off;
   p.kv = static_cast<const uint8_t*>(kv8_pool);
   p.scale = kv8_scale;
   p.slot_idx = slot_idx;
@@ -226,33 +226,42 @@ extern "C" int ddtree_verify_attn_kv8(const void* q, const void* kv8_pool, const
   p.group_nodes = w.group_nodes;
   p.shares = w.shares;
   p.units = w.units;
-  p.scale_log2 = static_cast<float>(sm_scale * 1.4426950408889634);
   p.o_part = reinterpret_cast<float*>(ws + w.o_off);
   p.lse_part = reinterpret_cast<float*>(ws + w.lse_off);
   p.pieces = reinterpret_cast<Kv8Piece*>(ws + w.pieces_off);
-  p.flags = reinterpret_cast<int32_t*>(ws + w.flags_off);
+  p.status = reinterpret_cast<int32_t*>(ws);
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
+  Kv8PrepareParams k = {};
+  k.q = static_cast<const uint16_t*>(q);
+  k.prefix_len = prefix_len;
+  k.tree_len = tree_len;
+  k.images = ws + w.images_off;
+  k.out = p.out;
+  k.lse = lse;
+  k.batch = p.batch;
+  k.nodes = p.nodes;
+  k.heads = p.heads;
+  k.max_prefix_len = p.max_prefix_len;
+  k.groups = w.groups;
+  k.group_nodes = w.group_nodes;
+  k.scale_log2 = static_cast<float>(sm_scale * 1.4426950408889634);
+  k.status = p.status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (launch_kv8_prepare(k, s) != cudaSuccess || launch_kv8_attn(p, s) != cudaSuccess) return DDT_ERR_LAUNCH;
+  if (w.shares <= 1) return DDT_OK;  // a unit a request
   Kv8MergeParams m = {};
   m.o_part = p.o_part;
   m.lse_part = p.lse_part;
   m.pieces = p.pieces;
-  m.flags = p.flags;
-  m.prefix_len = prefix_len;
   m.tree_len = tree_len;
   m.out = p.out;
   m.lse = lse;
   m.batch = p.batch;
   m.nodes = p.nodes;
   m.heads = p.heads;
-  m.max_prefix_len = p.max_prefix_len;
-  m.units = w.units;
-  m.groups = w.groups;
-  m.warps = w.shares > 1 ? merge_warps(w, dims->batch) : 1;
-  m.status = reinterpret_cast<int32_t*>(ws);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (launch_kv8_attn(p, s) != cudaSuccess || launch_kv8_merge(m, s) != cudaSuccess) return DDT_ERR_LAUNCH;
-  return DDT_OK;
+  m.warps = merge_warps(w, dims->batch);
+  return launch_kv8_merge(m, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
 }
 
 extern "C" size_t ddtree_accept_workspace_bytes(const ddt_dims* dims, int32_t vocab) {
