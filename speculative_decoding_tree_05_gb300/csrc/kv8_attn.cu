@@ -15,18 +15,22 @@
 //         most 2^-8 off, as bf16 is, and less on average (e5m2 reaches further down than
 //         e4m3 where the weights of a long cache are small)
 //
-// As in block attention, keys and value dims are the M side and rows the N side:
-//   S^T[64 keys][rows]  = K . Q^T          2 x 16 MMAs M64 x N64 x K32 (8 bit) and 4 of K16 (rope)
-//   O^T[512 dims][rows] += V^T . P^T       2 x 4 x 2 MMAs M128 x N x K32 (V^T: the same bytes
-//                                          read MN-major)
-// O^T takes 256 TMEM columns, so one CTA holds the whole output. By themselves the MMAs of
-// a tile take 1790 cycles with 64 rows, 1400 with 16.
+// What bounds a tile is the 128 B/clk of shared memory: an MMA reads both its operands
+// there. So the queries are the one operand that stays in tensor memory, both parts of up to 64
+// rows as the 128 lanes of one MMA, which sums them apart; and value dims are the M side
+// of the second product, so that each 8-bit value is read once for 64 rows and part:
+//   S[hi, lo rows][64 keys]      = Q . K^T    16 MMAs M128 x N64 x K32 (8 bit, Q in tensor memory), 4 of K16 (rope)
+//   O^T[512 dims][rows] += V^T . P^T          2 x 4 x 2 MMAs M128 x N x K32 (V^T: the same bytes read MN-major)
+// 56 + 96 KB of operands a tile, and 48 KB written (with both operands of the scores in
+// shared memory it was 144 + 96 KB, and a tile took 2330 cycles). O^T takes 256 TMEM columns,
+// the scores twice 64, the queries 128; one CTA holds the whole output.
 //
 // Per CTA (896 threads), one unit = (up to 64 (node, head) rows of a request, a share of its tiles):
 //   warp 0       TMEM; one lane issues S(t) when stage t has landed
-//   warps 1-16   softmax: 16 keys x 16 rows each, in the 16x256b shape
+//   warps 1-16   softmax: two sets of eight, for even and odd tiles; 16 rows x 32 keys a warp, in the
+//                16x256b shape, the two parts' scores added
 //   warp 17      one lane issues P.V(t) when P(t) is written
-//   warps 18-25  gather 64 keys per stage of 40 KB, three stages: warps 18-21 two of the five
+//   warps 18-25  gather 64 keys per stage of 40 KB, four stages: warps 18-21 two of the five
 //                128-byte pieces of a row by 16-byte cp.async, warps 22-25 the others by TMA
 //                gather4, at the same time (an SM gathers more both ways than either way)
 //   warps 26-27  the keys' scales and row masks
@@ -45,21 +49,21 @@ namespace ddt {
 namespace {
 
 constexpr int kThreads = 896;
-constexpr int kSoftmax = 512;
+constexpr int kSet = 256, kSoftmax = 2 * kSet;       // threads of one softmax set, of both
 constexpr int kIssuePv = 17, kFirstCopier = 18, kFirstGather = 22, kFirstKey = 26;  // warps
 constexpr int kCopiers = 128;                       // threads that gather the copied groups
 constexpr int kKeys = kKv8Keys;
 constexpr int kRows = kKv8Rows;
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 constexpr int kChunk = kKv8Chunk;                   // 128 bytes of 64 keys: 8 KB
 constexpr int kStageBytes = 5 * kChunk;             // 40960
-constexpr int kOffQ = kStages * kStageBytes;        // hi: 4 chunks, lo: 4, rope: 1
-constexpr int kOffQs = kOffQ + 9 * kChunk;          // [64] the rows' factors of a score
-constexpr int kOffP = kOffQs + 1024;                // [2 buffers][2 parts][64 keys][64 rows]
+constexpr int kOffRope = kStages * kStageBytes;     // the queries' rope values, [128 lanes][128 bytes]
+constexpr int kOffQs = kOffRope + 128 * 128;        // [64] the rows' factors of a score
+constexpr int kOffP = kOffQs + 1024;                // [2 buffers][2 parts][64 rows][64 keys]
 constexpr int kPart = kKeys * kRows;                // 4096
 constexpr int kOffMask = kOffP + 4 * kPart;         // [stages][64] row masks of the stage's keys
-constexpr int kOffKey = kOffMask + kStages * kKeys * 8;   // [stages][64] (s, log2 s, 1 / s, -)
-constexpr int kOffMax = kOffKey + kStages * kKeys * 16;   // [64] running reference
+constexpr int kOffKey = kOffMask + kStages * kKeys * 8;   // [stages][3][64] s, log2 s, 1 / s
+constexpr int kOffMax = kOffKey + kStages * kKeys * 12;   // [64] running reference
 constexpr int kOffAlpha = kOffMax + kRows * 4;      // [64] rescale factors, later 1 / row sums
 constexpr int kOffTree = kOffAlpha + kRows * 4;        // [128] row masks of the tree rows
 constexpr int kOffSlot = kOffTree + kMaxNodes * 8;  // [128] their slots
@@ -67,7 +71,7 @@ constexpr int kOffPar = kOffSlot + kMaxNodes * 4;   // [128] their parents
 constexpr int kOffBar = kOffPar + kMaxNodes * 4;
 constexpr int kSmem = kOffBar + 512 + 1024;
 static_assert(kSmem <= 232448, "one CTA's shared memory");
-constexpr uint32_t kColS = 256;                     // O^T [0, 256), S buffers 2 x 64
+constexpr uint32_t kColS = 256, kColQ = 384;        // O^T [0, 256), S buffers 2 x 64, Q
 constexpr float kUnset = -1e30f;                    // running reference of a row that has seen no key
 // Weights are 2^(t - r + kLift) and r is raised when one would exceed 2^(kLift + kSlack) = 431
 // (e4m3 ends at 448).
@@ -79,25 +83,35 @@ struct Shared {
   uint64_t f_full[kStages];            // the keys' factors and masks
   uint64_t s_full[2], s_free[2];
   uint64_t p_ready[2];
-  uint64_t q_full;
+  uint64_t decided[2];                 // the references of this set's tile stand
+  uint64_t q_full;                     // the queries' rope values and factors
+  uint64_t q_ready;                    // the queries in tensor memory
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  int fail[2];  // softmax: a wait of tile t ran out, by parity of t
+  int fail[2];     // softmax: a wait of a thread of the set ran out
+  int raises;      // how often the references have been raised
   int flags;
+  uint16_t seen[kStages][2];  // whether every row of the group sees all of a key warp's keys
 };
 static_assert(sizeof(Shared) <= 512, "barrier block");
 
-// 16 TMEM lanes x 16 columns over a warp: v[2 i + h] = lane L/4 + 8 h, columns 8 i + 2 (L % 4) + {0, 1}.
-__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint64_t (&v)[4]) {
-  uint32_t r[8];
+// 16 TMEM lanes x 16 columns over a warp, from taddr and 16 lanes on, added:
+// v[2 i + h] = lane L/4 + 8 h, columns 8 i + 2 (L % 4) + {0, 1}.
+__device__ __forceinline__ void tmem_ld_sum(uint32_t taddr, uint64_t (&v)[4]) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr), "r"(taddr + (16u << 16))
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+  for (int i = 0; i < 4; ++i)
+    v[i] = add_x2(f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+                  f32x2(__uint_as_float(r[8 + 2 * i]), __uint_as_float(r[9 + 2 * i])));
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
@@ -236,13 +250,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_free[i], kSoftmax / 32);
-      mbar_init(&sh.p_ready[i], kSoftmax / 32);
+      mbar_init(&sh.s_free[i], kSet / 32);
+      mbar_init(&sh.p_ready[i], kSet / 32);
+      mbar_init(&sh.decided[i], 1);
     }
     mbar_init(&sh.drain, 2);
     mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_ready, kSoftmax / 32);
     sh.abort = 0;
-    sh.fail[0] = sh.fail[1] = 0;
+    sh.fail[0] = sh.fail[1] = sh.raises = 0;
     sh.flags = 0;
     fence_mbar_init();
   }
@@ -261,13 +277,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   if (warp == 0) {
     if (elect_one()) {
       grid_dep_wait();  // the query rows: what comes before overlaps their making
-      mbar_arrive_expect_tx(&sh.q_full, kKv8Image);
-      bulk_load(base + kOffQ, p.images + (static_cast<int64_t>(un.b) * p.groups + g) * kKv8Image, kKv8Image, &sh.q_full);
-      ok = mbar_wait_abortable(&sh.q_full, 0, abort, false, __LINE__);
-      // scores of all 64 columns (rows of zeros behind the group's): every column read out is defined
-      const uint32_t idesc8 = idesc_f8_f32(64, kRows, kE4m3, kE4m3, false, false), idesc = idesc_bf16_f32(64, kRows, false, false);
+      mbar_arrive_expect_tx(&sh.q_full, kKv8Image - kKv8ImageRope);
+      bulk_load(base + kOffRope, p.images + (static_cast<int64_t>(un.b) * p.groups + g) * kKv8Image + kKv8ImageRope,
+                kKv8Image - kKv8ImageRope, &sh.q_full);
+      ok = mbar_wait_abortable(&sh.q_full, 0, abort, false, __LINE__) &&
+           mbar_wait_abortable(&sh.q_ready, 0, abort, false, __LINE__);
+      tc_fence_after();
+      const uint32_t idesc8 = idesc_f8_f32(128, kKeys, kE4m3, kE4m3, false, false), idesc = idesc_bf16_f32(128, kKeys, false, false);
       const uint64_t d_k = smem_desc(base, 16, 1024, kSwizzle128B);
-      const uint64_t d_q = smem_desc(base + kOffQ, 16, 1024, kSwizzle128B);
+      const uint64_t d_rope = smem_desc(base + kOffRope, 16, 1024, kSwizzle128B);
       int st = 0, ph = 0;
       for (int t = 0; ok && t < n; ++t) {
         if (t >= 2 && !mbar_wait_abortable(&sh.s_free[t & 1], ((t >> 1) - 1) & 1, abort, false, __LINE__)) {
@@ -275,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
           break;
         }
         const uint64_t k = desc_advance(d_k, st * kStageBytes);
-        const uint32_t d = tmem + kColS + (t & 1) * kRows;
+        const uint32_t d = tmem + kColS + (t & 1) * kKeys;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {  // the copied chunks land first
           if (!mbar_wait_abortable(&sh.k_full[st][x], ph, abort, false, __LINE__)) {
@@ -285,16 +303,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
           if (x == 0) fence_proxy_async_smem();  // written by cp.async
           tc_fence_after();
 #pragma unroll
-          for (int ks = 8 * x; ks < 8 * x + 8; ++ks) {
-            const uint32_t at = (ks >> 2) * kChunk + (ks & 3) * 32;
-            mma_f8_ss(d, desc_advance(k, at), desc_advance(d_q, at), idesc8, ks > 0 ? 1u : 0u);
-            mma_f8_ss(d, desc_advance(k, at), desc_advance(d_q, 4 * kChunk + at), idesc8, 1u);
-          }
+          for (int ks = 8 * x; ks < 8 * x + 8; ++ks)
+            mma_f8_ts(d, tmem + kColQ + ks * 8, desc_advance(k, (ks >> 2) * kChunk + (ks & 3) * 32), idesc8, ks > 0 ? 1u : 0u);
         }
         if (!ok) break;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)  // the rope dims
-          mma_ss(d, desc_advance(k, 4 * kChunk + ks * 32), desc_advance(d_q, 8 * kChunk + ks * 32), idesc, 1u);
+          mma_ss(d, desc_advance(d_rope, ks * 32), desc_advance(k, 4 * kChunk + ks * 32), idesc, 1u);
         mma_commit(&sh.s_full[t & 1]);
         if (++st == kStages) st = 0, ph ^= 1;
       }
@@ -304,9 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   } else if (warp == kIssuePv) {
     if (elect_one()) {
       const uint32_t cols = (rows + 15) / 16 * 16;
-      const uint32_t idesc_hi = idesc_f8_f32(128, cols, kE4m3, kE4m3, true, true), idesc_lo = idesc_f8_f32(128, cols, kE4m3, kE5m2, true, true);
+      const uint32_t idesc_hi = idesc_f8_f32(128, cols, kE4m3, kE4m3, true, false), idesc_lo = idesc_f8_f32(128, cols, kE4m3, kE5m2, true, false);
       const uint64_t d_v = smem_desc(base, kChunk, 1024, kSwizzle128B);          // MN-major, 128 dims a chunk
-      const uint64_t d_p = smem_desc(base + kOffP, kPart, 512, kSwizzle64B);     // MN-major, 64 rows
+      const uint64_t d_p = smem_desc(base + kOffP, 16, 512, kSwizzle64B);        // K-major, 64 keys a row
       int st = 0;
       for (int t = 0; t < n; ++t) {
         if (!mbar_wait_abortable(&sh.p_ready[t & 1], (t >> 1) & 1, abort, false, __LINE__)) {
@@ -323,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
             const uint64_t a = desc_advance(v, mt * kChunk + ks * 4096);
-            mma_f8_ss(tmem + mt * kRows, a, desc_advance(hi, ks * 2048), idesc_hi, ks > 0 ? 1u : more);
-            mma_f8_ss(tmem + mt * kRows, a, desc_advance(hi, kPart + ks * 2048), idesc_lo, 1u);
+            mma_f8_ss(tmem + mt * kRows, a, desc_advance(hi, ks * 32), idesc_hi, ks > 0 ? 1u : more);
+            mma_f8_ss(tmem + mt * kRows, a, desc_advance(hi, kPart + ks * 32), idesc_lo, 1u);
           }
           if (y & 1) mma_commit(&sh.k_empty[st][y == 1]);
         }
@@ -446,10 +461,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       } else {
         if (bad) atomicOr(&sh.flags, kStatusBadSlot);
         reinterpret_cast<uint64_t*>(smem + kOffMask)[st * kKeys + k] = mask;
+        const bool all = __all_sync(0xffffffffu, mask == full);
+        if (lane == 0) sh.seen[st][warp - kFirstKey] = all;
         // a scale that is not positive and finite: NaN for the rows that see the key
         const bool fine = scale > 0.f && scale < CUDART_INF_F;
-        reinterpret_cast<float4*>(smem + kOffKey)[st * kKeys + k] =
-            fine ? make_float4(scale, log2f(scale), 1.f / scale, 0.f) : make_float4(CUDART_NAN_F, 0.f, 1.f, 0.f);
+        float* f = reinterpret_cast<float*>(smem + kOffKey) + st * 3 * kKeys + k;
+        f[0] = fine ? scale : CUDART_NAN_F;
+        f[kKeys] = fine ? log2f(scale) : 0.f;
+        f[2 * kKeys] = fine ? 1.f / scale : 1.f;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.f_full[st]);
       }
@@ -461,142 +480,171 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       for (int v = max(0, done - kStages); v < done; ++v) mbar_wait(&sh.k_full[v % kStages][1], (v / kStages) & 1, 1u << 14);
   } else {
     // ------------------------------------------------------------------ softmax
-    const int quarter = warp & 3, part4 = (warp - 1) >> 2;  // lanes of TMEM, a quarter of the rows
+    // Two sets, for even and odd tiles: a tile's way from its scores to its weights is a chain of waits (3000
+    // cycles, most of them for shared memory beside the gathers), of which two overlap.
+    const int set = (warp - 1) >> 3, quarter = warp & 3, half = ((warp - 1) >> 2) & 1;  // 16 rows, 32 keys of a tile
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const int r0 = quarter * 16 + (lane >> 2);     // keys r0 and r0 + 8 of the tile
-    const int c0 = 16 * part4 + 2 * (lane & 3);    // rows c0 + 8 i + {0, 1}, i < 2
-    const int id = part4 * 128 + quarter * 32 + lane;
+    const int r0 = quarter * 16 + (lane >> 2);     // rows r0 and r0 + 8
+    const int c0 = 32 * half + 2 * (lane & 3);     // keys c0 + 8 i + {0, 1}, i < 4
+    const int id = half * 128 + quarter * 32 + lane;
+    const int bar = 1 + 4 * set;                   // the set's barrier
     float* alpha_sh = reinterpret_cast<float*>(smem + kOffAlpha);
-    const uint64_t* masks = reinterpret_cast<const uint64_t*>(smem + kOffMask);
-    const float4* factors = reinterpret_cast<const float4*>(smem + kOffKey);
-    const uint64_t full = rows == 64 ? ~0ull : ((1ull << rows) - 1);
-    // of this thread's rows, two by two: sums, score factors and (lowered by kLift) references
-    uint64_t l[2], qs[2], m[2];
-    bool failed = !mbar_wait_abortable(&sh.q_full, 0, abort, false, __LINE__);  // a wait of this thread ran out: the warps leave together at the next barrier
+    {  // the queries, a quarter of the lanes' bytes a warp
+      const int part4 = (warp - 1) >> 2;
+      grid_dep_wait();
+      const uint4* src = reinterpret_cast<const uint4*>(p.images + (static_cast<int64_t>(un.b) * p.groups + g) * kKv8Image) +
+                         8 * part4 * 128 + quarter * 32 + lane;
+      uint32_t r[32];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] = f32x2(0.f, 0.f);
-      qs[i] = *reinterpret_cast<const uint64_t*>(smem + kOffQs + (c0 + 8 * i) * 4);
-      m[i] = f32x2(kUnset, kUnset);
+      for (int j = 0; j < 8; ++j) {
+        const uint4 v = __ldcg(src + j * 128);
+        r[4 * j] = v.x, r[4 * j + 1] = v.y, r[4 * j + 2] = v.z, r[4 * j + 3] = v.w;
+      }
+      tmem_st32(tmem + lane_off + kColQ + 32 * part4, r);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_ready);
     }
-    // Where this thread's weights go in a part of P^T (a key's 64 columns, 64-byte swizzle): with its neighbour it
-    // holds four columns of two keys, of which even lanes store the first and odd lanes the second key's.
-    uint32_t p_at[2];
+    bool failed = !mbar_wait_abortable(&sh.q_full, 0, abort, false, __LINE__);  // a wait of this thread ran out: the warps leave together at the next barrier
+    // of this thread's rows: sums (of even and odd keys), score factors and (lowered by kLift) references
+    uint64_t l[2];
+    float qs[2], m[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] = f32x2(0.f, 0.f);
+      qs[h] = reinterpret_cast<const float*>(smem + kOffQs)[r0 + 8 * h];
+      m[h] = kUnset;
+    }
+    // Where this thread's weights go in a part of P^T (a row's 64 keys, 64-byte swizzle): with its neighbour it holds
+    // four keys of two rows, of which even lanes store the first and odd lanes the second row's.
+    uint32_t p_at[2];  // (of i = 0 and 2; 1 and 3 are eight bytes on)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int key = r0 + 8 * (lane & 1), col = (c0 & ~3) + 8 * i;
-      p_at[i] = base + kOffP + key * 64 + ((((col >> 4) ^ ((key >> 1) & 3)) << 4) | (col & 15));
+      const int row = r0 + 8 * (lane & 1), col = (c0 & ~3) + 16 * i;
+      p_at[i] = base + kOffP + set * 2 * kPart + row * 64 + ((((col >> 4) ^ ((row >> 1) & 3)) << 4) | (col & 15));
     }
     auto wait_pv = [&](int t) {  // P.V(t) has read P, and O^T holds every tile up to t
       if (!mbar_wait_abortable(&sh.k_empty[t % kStages][0], (t / kStages) & 1, abort, false, __LINE__)) failed = true;
       tc_fence_after();
     };
-    // column sums or maxima over the 16 keys of the warp, to scratch [4 quarters][64]
-    auto to_scratch = [&](float* scratch, const float (&v)[4], auto op) {
+    // sums or maxima over the warp's 32 keys, to scratch [2 halves of the keys][64 rows]
+    float* scratch = reinterpret_cast<float*>(smem + kOffP + set * 2 * kPart);
+    auto to_scratch = [&](const float (&v)[2], auto op) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x = v[i];
-        x = op(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = op(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = op(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        if (lane < 4) scratch[quarter * kRows + c0 + 8 * (i >> 1) + (i & 1)] = x;
+      for (int h = 0; h < 2; ++h) {
+        float x = op(v[h], __shfl_xor_sync(0xffffffffu, v[h], 1));
+        x = op(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        if ((lane & 3) == 0) scratch[half * kRows + r0 + 8 * h] = x;
       }
     };
-    int st = 0, ph = 0;
-    for (int t = 0; t < n; ++t) {
-      // A look at shared memory takes 100 to 300 cycles beside the gathers, so what can be looked at ahead of the
-      // scores is: P.V of the tile before the last, which frees the buffer, and the keys' masks and factors.
+    int raises = 0;  // that m and l know of
+    for (int t = set; t < n; t += 2) {
+      const int st = t % kStages, ph = (t / kStages) & 1;
       const bool p_free = t < 2 || mbar_test_wait(&sh.k_empty[(t - 2) % kStages][0], ((t - 2) / kStages) & 1);
       if (!mbar_wait_abortable(&sh.f_full[st], ph, abort, false, __LINE__)) failed = true;
-      const uint64_t m0 = masks[st * kKeys + r0], m1 = masks[st * kKeys + r0 + 8];
-      const float4 f0 = factors[st * kKeys + r0], f1 = factors[st * kKeys + r0 + 8];
-      const bool part = __any_sync(0xffffffffu, m0 != full || m1 != full);
-      if (!mbar_wait_abortable(&sh.s_full[t & 1], (t >> 1) & 1, abort, false, __LINE__)) failed = true;
+      const bool part = *reinterpret_cast<const volatile uint32_t*>(sh.seen[st]) != 0x00010001u;
+      const float* factor = reinterpret_cast<const float*>(smem + kOffKey) + st * 3 * kKeys + c0;
+      if (!mbar_wait_abortable(&sh.s_full[set], (t >> 1) & 1, abort, false, __LINE__)) failed = true;
       __syncwarp();
       tc_fence_after();
-      float s[8];  // [4 i + 2 h + e]: key r0 + 8 h, row c0 + 8 i + e
-      // t of each score: log2 of its weight times its key's scale
-      auto scores = [&] {
+      float s[16];  // [4 i + 2 h + e]: row r0 + 8 h, key c0 + 8 i + e: log2 of its weight times its key's scale
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
         uint64_t v[4];
-        tmem_ld_16x16(tmem + lane_off + kColS + (t & 1) * kRows + 16 * part4, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 f = i & 1 ? f1 : f0;
-          v[i] = fma_x2(mul_x2(v[i], f32x2(f.x, f.x)), qs[i >> 1], sub_x2(f32x2(f.y, f.y), m[i >> 1]));
-          f32x2_split(v[i], s[2 * i], s[2 * i + 1]);
-        }
-        if (part) {
-          const uint32_t w0 = static_cast<uint32_t>(m0 >> c0), w1 = static_cast<uint32_t>(m1 >> c0);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              if (!((w0 >> (8 * i + e)) & 1u)) s[4 * i + e] = -CUDART_INF_F;
-              if (!((w1 >> (8 * i + e)) & 1u)) s[4 * i + 2 + e] = -CUDART_INF_F;
-            }
-        }
-      };
-      scores();
-      const float over = fmax3(fmax3(s[0], s[1], s[2]), fmax3(s[3], s[4], s[5]), fmaxf(s[6], s[7]));
-      if (failed) sh.fail[t & 1] = 1;
-      const bool raise = bar_red_or(1, kSoftmax, failed || over > kLift + kSlack);
-      if (raise && *const_cast<volatile int*>(&sh.fail[t & 1])) {
-        ok = false;
-        break;
-      }
-      if (raise) {
-        // Every row's reference becomes its maximum: with 64 rows in step, raising the rows that need it alone
-        // would come to a raise of some row in most tiles.
-        float* scratch = reinterpret_cast<float*>(smem + kOffP + (t & 1) * 2 * kPart);
-        if (t > 0) wait_pv(t - 1);  // the scratch is the P buffer, and O^T is rescaled
-        m[0] = m[1] = f32x2(0.f, 0.f);
-        scores();  // again, without a reference
-        const float top4[4] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3]), fmaxf(s[4], s[6]), fmaxf(s[5], s[7])};
-        to_scratch(scratch, top4, [](float a, float b) { return fmaxf(a, b); });
-        bar_sync(1, kSoftmax);
-        if (id < kRows) {  // one thread per row decides
-          const float old = mx[id];
-          const float top = fmaxf(fmaxf(scratch[id], scratch[kRows + id]), fmaxf(scratch[2 * kRows + id], scratch[3 * kRows + id]));
-          alpha_sh[id] = top > old ? fast_exp2(old - top) : 1.f;
-          mx[id] = fmaxf(top, old);
-        }
-        bar_sync(1, kSoftmax);
+        tmem_ld_sum(tmem + lane_off + kColS + set * kKeys + 32 * half + 16 * j, v);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          l[i] = mul_x2(l[i], *reinterpret_cast<const uint64_t*>(alpha_sh + c0 + 8 * i));
-          m[i] = sub_x2(*reinterpret_cast<const uint64_t*>(mx + c0 + 8 * i), f32x2(kLift, kLift));
-          float x, y;
-          f32x2_split(m[i], x, y);
-          s[4 * i] -= x, s[4 * i + 1] -= y, s[4 * i + 2] -= x, s[4 * i + 3] -= y;
-        }
-        if (t > 0) {
-#pragma unroll 1
-          for (int k0 = 0; k0 < 8; ++k0) {  // this warp's quarter of the columns, 8 at a time
-            const int cc = 16 * part4 + (k0 & 1) * 8;
-            uint32_t o[8];
-            tmem_ld8(tmem + lane_off + (k0 >> 1) * kRows + cc, o);
+          const uint64_t ks = *reinterpret_cast<const uint64_t*>(factor + 16 * j + 8 * i);
+          const uint64_t lg = *reinterpret_cast<const uint64_t*>(factor + kKeys + 16 * j + 8 * i);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha_sh[cc + k]);
-            tmem_st8(tmem + lane_off + (k0 >> 1) * kRows + cc, o);
-          }
+          for (int h = 0; h < 2; ++h)
+            f32x2_split(fma_x2(mul_x2(v[2 * i + h], ks), f32x2(qs[h], qs[h]), lg), s[8 * j + 4 * i + 2 * h],
+                        s[8 * j + 4 * i + 2 * h + 1]);
         }
-        bar_sync(1, kSoftmax);  // scratch is read before P is written over it
       }
       tc_fence_before();
       __syncwarp();
 #ifdef DDT_TEST_HOOKS
-      if (warp != 1 || t != p.test_keep_back)
+      if (warp != 1 + 8 * set || t != p.test_keep_back)
 #endif
-      if (lane == 0) mbar_arrive(&sh.s_free[t & 1]);
-      uint32_t hi[2], lo[2];  // [i]: rows c0 + 8 i + {0, 1} of keys r0 (low half) and r0 + 8
+      if (lane == 0) mbar_arrive(&sh.s_free[set]);
+      if (part) {
+        const uint64_t* masks = reinterpret_cast<const uint64_t*>(smem + kOffMask) + st * kKeys + c0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t seen = static_cast<uint32_t>(masks[8 * i + e] >> r0);
+            if (!(seen & 1u)) s[4 * i + e] = -CUDART_INF_F;
+            if (!(seen & 0x100u)) s[4 * i + 2 + e] = -CUDART_INF_F;
+          }
+      }
+      float top[2];  // of the thread's rows
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        top[h] = fmax3(fmax3(s[2 * h], s[2 * h + 1], s[4 + 2 * h]), fmax3(s[5 + 2 * h], s[8 + 2 * h], s[9 + 2 * h]),
+                       fmaxf(s[12 + 2 * h], s[13 + 2 * h]));
+      // The references, as they are after the tile before, of the other set. They are raised for all rows at once:
+      // with 64 rows in step, raising the rows that need it alone would come to a raise in most tiles.
+      if (t > 0 && !mbar_wait_abortable(&sh.decided[set ^ 1], ((t - 1) >> 1) & 1, abort, false, __LINE__)) failed = true;
+      const int raised = *const_cast<volatile int*>(&sh.raises);
+      if (raised != raises) {
+        raises = raised;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float now = const_cast<volatile float*>(mx)[r0 + 8 * h] - kLift, a = fast_exp2(m[h] - now);
+          l[h] = mul_x2(l[h], f32x2(a, a));
+          m[h] = now;
+        }
+      }
+      if (failed) sh.fail[set] = 1;
+      const bool raise = bar_red_or(bar, kSet, failed || fmaxf(top[0] - m[0], top[1] - m[1]) > kLift + kSlack);
+      if (raise) {
+        if (*const_cast<volatile int*>(&sh.fail[set])) {
+          ok = false;
+          break;
+        }
+        if (t > 0) wait_pv(t - 1);  // O^T is rescaled (and the scratch, the P buffer, is free)
+        to_scratch(top, [](float a, float b) { return fmaxf(a, b); });
+        bar_sync(bar, kSet);
+        if (id < kRows) {  // one thread per row decides
+          const float old = mx[id], now = fmaxf(old, fmaxf(scratch[id], scratch[kRows + id]));
+          alpha_sh[id] = now > old ? fast_exp2(old - now) : 1.f;
+          mx[id] = now;
+        }
+        if (id == 0) sh.raises = raises + 1;
+        ++raises;
+        bar_sync(bar, kSet);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float a = alpha_sh[r0 + 8 * h];
+          l[h] = mul_x2(l[h], f32x2(a, a));
+          m[h] = mx[r0 + 8 * h] - kLift;
+        }
+        if (t > 0) {
+#pragma unroll 1
+          for (int k0 = 0; k0 < 16; ++k0) {  // half of the columns (rows), 8 at a time
+            const int cc = 32 * half + (k0 & 3) * 8;
+            uint32_t o[8];
+            tmem_ld8(tmem + lane_off + (k0 >> 2) * kRows + cc, o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha_sh[cc + k]);
+            tmem_st8(tmem + lane_off + (k0 >> 2) * kRows + cc, o);
+          }
+          tc_fence_before();
+        }
+        bar_sync(bar, kSet);  // scratch is read before P is written over it, and O^T is rescaled
+      }
+      if (id == 0) mbar_arrive(&sh.decided[set]);
+      uint32_t hi[4], lo[4];  // [i]: keys c0 + 8 i + {0, 1} of rows r0 (low half) and r0 + 8
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t inv = *reinterpret_cast<const uint64_t*>(factor + 2 * kKeys + 8 * i);
         uint32_t h2[2], l2[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float x = fast_exp2(s[4 * i + 2 * h]), y = fast_exp2(s[4 * i + 2 * h + 1]);
-          const float inv = h ? f1.z : f0.z;
-          l[i] = fma_x2(f32x2(x, y), f32x2(inv, inv), l[i]);
+          const float x = fast_exp2(s[4 * i + 2 * h] - m[h]), y = fast_exp2(s[4 * i + 2 * h + 1] - m[h]);
+          l[h] = fma_x2(f32x2(x, y), inv, l[h]);
           cut_weights(x, y, h2[h], l2[h]);
         }
         hi[i] = h2[0] | (h2[1] << 16);
@@ -604,8 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       }
       if (!p_free && !raise) wait_pv(t - 2);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t at = p_at[i] + (t & 1) * 2 * kPart;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t at = p_at[i >> 1] + 8 * (i & 1);
         const uint32_t h = __shfl_xor_sync(0xffffffffu, hi[i], 1), w = __shfl_xor_sync(0xffffffffu, lo[i], 1);
         st_shared_b32(at, lane & 1 ? __byte_perm(h, hi[i], 0x7632) : __byte_perm(hi[i], h, 0x5410));
         st_shared_b32(at + kPart, lane & 1 ? __byte_perm(w, lo[i], 0x7632) : __byte_perm(lo[i], w, 0x5410));
@@ -613,22 +661,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_ready[t & 1]);
-      if (++st == kStages) st = 0, ph ^= 1;
+      if (lane == 0) mbar_arrive(&sh.p_ready[set]);
     }
+    if (ok) wait_pv(n - 1);  // O^T is complete and the P buffers free
+    if (bar_red_or(6, kSoftmax, failed || !ok)) ok = false;
     if (ok) {
-      wait_pv(n - 1);  // O^T is complete and the P buffers free
-      if (bar_red_or(1, kSoftmax, failed)) ok = false;
-    }
-    if (ok) {
-      float* scratch = reinterpret_cast<float*>(smem + kOffP);
-      float sums[4];
-      f32x2_split(l[0], sums[0], sums[1]);
-      f32x2_split(l[1], sums[2], sums[3]);
-      to_scratch(scratch, sums, [](float a, float b) { return a + b; });
-      bar_sync(1, kSoftmax);
-      if (id < kRows) {
-        const float sum = (scratch[id] + scratch[kRows + id]) + (scratch[2 * kRows + id] + scratch[3 * kRows + id]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // the last raise may have been the other set's
+        const float a = fast_exp2(m[h] + kLift - mx[r0 + 8 * h]);
+        l[h] = mul_x2(l[h], f32x2(a, a));
+      }
+      float sums[2], x;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f32x2_split(l[h], sums[h], x);
+        sums[h] += x;
+      }
+      to_scratch(sums, [](float a, float b) { return a + b; });
+      bar_sync(6, kSoftmax);
+      if (set == 0 && id < kRows) {
+        const float* other = scratch + 2 * kPart / 4;
+        const float sum = (scratch[id] + scratch[kRows + id]) + (other[id] + other[kRows + id]);
         alpha_sh[id] = sum != 0.f ? 1.f / sum : 0.f;
         const float lse = sum != 0.f ? (mx[id] - kLift + log2f(sum)) * kLn2 : -CUDART_INF_F;
         if (id < rows) {

@@ -2,8 +2,8 @@
 // query rows as the tensor core reads them, cut into two 8-bit parts once instead of once
 // a unit, and the call's first status word.
 //
-// One CTA per (request, group of up to 64 rows) writes the 72 KB that its units copy to
-// shared memory as they are (the layout is kv8_attn.cu's), and a factor per row:
+// One CTA per (request, group of up to 64 rows) writes the 80 KB that its units put into
+// tensor and shared memory as they are, and a factor per row:
 //   q = (hi + lo) 2^e in e4m3, 2^e the least power of two with |latent values| <= 448 2^e;
 //   rope values q 2^-e in bf16.
 // A warp a row; bound by latency (and the conversions, 16 a clock and SM), so a kernel of
@@ -60,8 +60,9 @@ __global__ void __launch_bounds__(kThreads) kv8_prepare_kernel(const __grid_cons
       const int e = max(static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0),
                         max(static_cast<int>(turned >> 7) - 127 - 120, kKv8MinExp));
       const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      // dims 8 lane + {0..7} in chunk lane / 16, dims 256 + 8 lane + {0..7} two chunks further
-      uint8_t* dst = image + (lane >> 4) * kKv8Chunk + r * 128 + (((((lane & 15) >> 1) ^ (r & 7)) << 4) | ((lane & 1) << 3));
+      // A lane has dims 8 lane + {0..7} and 256 + 8 lane + {0..7}; with its neighbour, even lanes take 16 of the
+      // first, odd lanes of the second half.
+      uint32_t cut[2][4];  // [part][8 bytes of the first half, 8 of the second]
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t hi[4], lo[4];
@@ -70,14 +71,24 @@ __global__ void __launch_bounds__(kThreads) kv8_prepare_kernel(const __grid_cons
           const uint32_t v = fine ? w[4 * h + j] : 0u;
           cut_query(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv, hi[j], lo[j]);
         }
-        *reinterpret_cast<uint2*>(dst + 2 * h * kKv8Chunk) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-        *reinterpret_cast<uint2*>(dst + (4 + 2 * h) * kKv8Chunk) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        cut[0][2 * h] = hi[0] | (hi[1] << 16), cut[0][2 * h + 1] = hi[2] | (hi[3] << 16);
+        cut[1][2 * h] = lo[0] | (lo[1] << 16), cut[1][2 * h + 1] = lo[2] | (lo[3] << 16);
       }
+      const bool odd = lane & 1;
       const uint32_t v = fine ? w[8] : 0u;
-      *reinterpret_cast<uint32_t*>(image + 8 * kKv8Chunk + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2))) =
-          pack_bf16x2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv);
+      const uint32_t rope = pack_bf16x2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv);
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const int l = 32 * (r >> 4) + (r & 15) + 16 * part, piece = (lane >> 1) + (odd ? 16 : 0);
+        const uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? cut[part][0] : cut[part][2], 1);
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? cut[part][1] : cut[part][3], 1);
+        *reinterpret_cast<uint4*>(image + (128 * piece + l) * 16) =
+            odd ? make_uint4(x, y, cut[part][2], cut[part][3]) : make_uint4(cut[part][0], cut[part][1], x, y);
+        *reinterpret_cast<uint32_t*>(image + kKv8ImageRope + l * 128 + ((((lane >> 2) ^ (l & 7)) << 4) | ((lane & 3) << 2))) =
+            part == 0 ? rope : 0u;
+      }
       if (lane == 0)
-        reinterpret_cast<float*>(image + 9 * kKv8Chunk)[r] =
+        reinterpret_cast<float*>(image + kKv8ImageFactor)[r] =
             r >= u.rows ? 0.f : fine ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * p.scale_log2 : CUDART_NAN_F;
     }
   }
