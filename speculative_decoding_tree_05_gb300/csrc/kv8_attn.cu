@@ -30,7 +30,7 @@
 //   warps 1-16   softmax: two sets of eight, for even and odd tiles; 16 rows x 32 keys a warp, in the
 //                16x256b shape, the two parts' scores added
 //   warp 17      one lane issues P.V(t) when P(t) is written
-//   warps 18-25  gather 64 keys per stage of 40 KB, four stages: warps 18-21 two of the five
+//   warps 18-25  gather 64 keys per stage of 40 KB, four stages: warps 18-21 three of the five
 //                128-byte pieces of a row by 16-byte cp.async, warps 22-25 the others by TMA
 //                gather4, at the same time (an SM gathers more both ways than either way)
 //   warps 26-27  the keys' scales and row masks
@@ -79,7 +79,7 @@ constexpr float kLift = 4.f, kSlack = 4.75f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct Shared {
-  uint64_t k_full[kStages][2], k_empty[kStages][2];  // [0]: chunks 0 and 1, copied; [1]: the others, gathered
+  uint64_t k_full[kStages][2], k_empty[kStages][2];  // [0]: chunks 0, 1 and 4, copied; [1]: 2 and 3, gathered
   uint64_t f_full[kStages];            // the keys' factors and masks
   uint64_t s_full[2], s_free[2];
   uint64_t p_ready[2];
@@ -438,20 +438,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       }
       if (copier) {
         copy_rows(sbase, r0, 0, P16(), slot);
+        copy_rows(sbase, r0, 4, P8(), slot);
         cp_async_arrive_noinc(&sh.k_full[st][0]);
       } else if (gather) {
         if (__all_sync(0xffffffffu, slot >= 0 || lane >= 16)) {
-          // lanes 0-11: four of the warp's keys, one of the three chunks
-          if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[st][1], 16 * 384);
+          // lanes 0-7: four of the warp's keys, one of the two chunks
+          if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[st][1], 16 * 256);
           __syncwarp();
           const int q = 4 * (lane & 3), c = 2 + (lane >> 2);
           const int ra = __shfl_sync(0xffffffffu, slot, q), rb = __shfl_sync(0xffffffffu, slot, q + 1);
           const int rc = __shfl_sync(0xffffffffu, slot, q + 2), rd = __shfl_sync(0xffffffffu, slot, q + 3);
-          if (lane < 12) tma_gather4(sbase + c * kChunk + (r0 + q) * 128, &p.tmap, c * 128, ra, rb, rc, rd, &sh.k_full[st][1]);
+          if (lane < 8) tma_gather4(sbase + c * kChunk + (r0 + q) * 128, &p.tmap, c * 128, ra, rb, rc, rd, &sh.k_full[st][1]);
         } else {
           // a key is masked (the end of the keys, a bad slot): zero-filled copies
           copy_rows(sbase, r0, 2, P16(), slot);
-          copy_rows(sbase, r0, 4, P8(), slot);
           cp_async_commit();
           cp_async_wait<0>();
           fence_proxy_async_smem();
