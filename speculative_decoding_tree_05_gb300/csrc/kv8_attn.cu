@@ -92,6 +92,11 @@ struct Shared {
   int fail[2];     // softmax: a wait of a thread of the set ran out
   int raises;      // how often the references have been raised
   int flags;
+  // where the unit's results go: bf16 rows of out, or fp32 rows of its partials (in shared memory: registers are
+  // what the loops lack)
+  void* o_dst;
+  float* lse_dst;
+  int last;  // the request's one unit
   uint16_t seen[kStages][2];  // whether every row of the group sees all of a key warp's keys
 };
 static_assert(sizeof(Shared) <= 512, "barrier block");
@@ -124,16 +129,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
 // Two weights in two 8-bit parts, e4m3 and what that leaves in e5m2. Through f16, whose 11 bits lose 2^-12 of a weight
 // and whose differences here are exact: five conversions and a subtraction a pair.
 __device__ __forceinline__ void cut_weights(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -238,7 +233,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   const int tiles = (keys + kKeys - 1) / kKeys;
   const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * un.k / un.count);
   const int n = static_cast<int>(static_cast<int64_t>(tiles) * (un.k + 1) / un.count) - t0;  // at least one
-  const int64_t trow0 = static_cast<int64_t>(un.b) * p.nodes * p.heads + row0;  // of out and lse
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -260,6 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     sh.abort = 0;
     sh.fail[0] = sh.fail[1] = sh.raises = 0;
     sh.flags = 0;
+    const int64_t all = static_cast<int64_t>(p.nodes) * p.heads, at = (un.count == 1 ? un.b : unit) * all + row0;
+    sh.last = un.count == 1;
+    sh.o_dst = un.count == 1 ? static_cast<void*>(p.out + at * kDv) : p.o_part + at * kDv;
+    sh.lse_dst = (un.count == 1 ? p.lse : p.lse_part) + at;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -684,54 +682,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         const float sum = (scratch[id] + scratch[kRows + id]) + (other[id] + other[kRows + id]);
         alpha_sh[id] = sum != 0.f ? 1.f / sum : 0.f;
         const float lse = sum != 0.f ? (mx[id] - kLift + log2f(sum)) * kLn2 : -CUDART_INF_F;
-        if (id < rows) {
-          if (un.count == 1)
-            p.lse[trow0 + id] = lse;
-          else
-            p.lse_part[static_cast<int64_t>(unit) * p.nodes * p.heads + row0 + id] = lse;
-        }
+        if (id < rows) sh.lse_dst[id] = lse;
       }
     }
   }
-  // O through the stages, which are free: rows of 512 values, as they lie in memory, stored in bulk. The softmax and
-  // gather warps: quarter of the lanes by warp, six warps a quarter, 16 rows of 32 dims at a time.
+  // The softmax and gather warps write O: quarter of the lanes by warp, six warps a quarter, 8 rows of 32 dims at a
+  // time; lane = value dim. (Through shared memory and a bulk copy it took 8500 cycles in place of NNNN.)
   if (warp > 0) {
-    const bool fine = !bar_red_or(2, kThreads - 32, !ok);
-    if (fine && warp != kIssuePv && warp < kFirstKey) {
+    if (!bar_red_or(2, kThreads - 32, !ok) && warp != kIssuePv && warp < kFirstKey) {
       tc_fence_after();
-      const float* inv_l = reinterpret_cast<const float*>(smem + kOffAlpha);
+      const float4* inv_l = reinterpret_cast<const float4*>(smem + kOffAlpha);
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
 #pragma unroll 1
-      for (int k0 = warp < kIssuePv ? (warp - 1) >> 2 : (warp - 2) >> 2; k0 < 16; k0 += 6) {
-        const int mt = k0 & 3, cc = (k0 >> 2) * 16;
-        if (cc >= rows) continue;
-        uint32_t o[16];
-        tmem_ld16(tmem + lane_off + mt * kRows + cc, o);
-        const int dim = mt * 128 + (warp & 3) * 32 + lane;  // lane = value dim
-        if (un.count == 1) {
+      for (int k0 = warp < kIssuePv ? (warp - 1) >> 2 : (warp - 2) >> 2; k0 < 32; k0 += 6) {
+        const int mt = k0 & 3, cc = (k0 >> 2) * 8, left = rows - cc;
+        if (left <= 0) break;
+        uint32_t o[8];
+        tmem_ld8(tmem + lane_off + mt * kRows + cc, o);
+        const float4 f0 = inv_l[cc / 4], f1 = inv_l[cc / 4 + 1];
+        const float x[8] = {__uint_as_float(o[0]) * f0.x, __uint_as_float(o[1]) * f0.y, __uint_as_float(o[2]) * f0.z,
+                            __uint_as_float(o[3]) * f0.w, __uint_as_float(o[4]) * f1.x, __uint_as_float(o[5]) * f1.y,
+                            __uint_as_float(o[6]) * f1.z, __uint_as_float(o[7]) * f1.w};
+        const int dim = mt * 128 + (warp & 3) * 32;
+        if (sh.last) {
           // two rows a store: even lanes hold a pair of dims of the first, odd lanes of the second
-          uint32_t* dst = reinterpret_cast<uint32_t*>(smem) + ((cc + (lane & 1)) * kDv + (dim & ~1)) / 2;
+          uint16_t* dst = static_cast<uint16_t*>(sh.o_dst) + (cc + (lane & 1)) * kDv + dim + (lane & ~1);
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            const float x = __uint_as_float(o[k]) * inv_l[cc + k], y = __uint_as_float(o[k + 1]) * inv_l[cc + k + 1];
-            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
-            dst[k * (kDv / 2)] = lane & 1 ? pack_bf16x2(got, y) : pack_bf16x2(x, got);
+          for (int k = 0; k < 8; k += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x[k] : x[k + 1], 1);
+            if (k + (lane & 1) < left)
+              *reinterpret_cast<uint32_t*>(dst + k * kDv) = lane & 1 ? pack_bf16x2(got, x[k + 1]) : pack_bf16x2(x[k], got);
           }
         } else {
-          float* dst = reinterpret_cast<float*>(smem) + cc * kDv + dim;
+          float* dst = static_cast<float*>(sh.o_dst) + cc * kDv + dim + lane;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) dst[k * kDv] = __uint_as_float(o[k]) * inv_l[cc + k];
+          for (int k = 0; k < 8; ++k)
+            if (k < left) dst[k * kDv] = x[k];
         }
       }
-      fence_proxy_async_smem();
-    }
-    bar_sync(2, kThreads - 32);
-    if (fine && warp == kIssuePv && elect_one()) {
-      const uint32_t bytes = rows * kDv * (un.count == 1 ? 2 : 4);
-      void* dst = un.count == 1 ? static_cast<void*>(p.out + trow0 * kDv)
-                                : p.o_part + (static_cast<int64_t>(unit) * p.nodes * p.heads + row0) * kDv;
-      bulk_store(dst, base, bytes);
-      bulk_store_wait();
     }
   }
   if (!ok) {
