@@ -9,9 +9,9 @@
 // the first x with w(0) + ... + w(x) > u_0 S.
 //
 // Weights are whole numbers: w(x) = 2^((l(x) - max l) log2 e / temperature) in steps of
-// 2^-43, their exponent carried in two floats (3e-10 of each weight). So sums are exact in any order, the
-// same tokens come out on any tiling, and a token on the border between two answers is
-// decided as 64-bit arithmetic decides it, but for one draw in 10^5 or so.
+// 2^-43, their exponent carried in two floats (3e-10 of each weight; in one where the weight is below 2^-24, which is
+// off by a step or so). So sums are exact in any order, the same tokens come out on any tiling, and a token on the border
+// between two answers is decided as 64-bit arithmetic decides it, but for one draw in 10^5 or so.
 //
 // One cluster per request walks down the tree and reads only the rows that it visits,
 // each CTA its share of the vocabulary, which stays in shared memory (logits; with q the
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kAccThreads = 512, kAccWarps = kAccThreads / 32;
 constexpr int kOne = 43;         // weight 1 is 2^43; up to 2^18 of them fit in 64 bits
-constexpr int kUnroll = 8;       // loads in flight of a thread
+constexpr int kUnroll = 16;      // loads in flight of a thread
 constexpr int kPrefetched = 4;   // children whose rows are sent for
 
 // 2^(62 - i / 64), i = 0 to 63
@@ -54,9 +54,8 @@ __constant__ unsigned long long c_pow[64] = {
     0x216ab0d9f3121ec5ull, 0x210e8a30eb379012ull, 0x20b361a62b0ae876ull, 0x2059347cef00c1ddull,
 };
 
-// 2^-(hi + lo) in steps of 2^-43, rounded down; hi >= 0, |lo| small. `pow_sh` is c_pow in shared memory.
+// 2^-(hi + lo) in steps of 2^-43, rounded down; 0 <= hi < 24, |lo| small. `pow_sh` is c_pow in shared memory.
 __device__ __forceinline__ unsigned long long weight_of(float hi, float lo, const unsigned long long* pow_sh) {
-  if (!(hi < 44.f)) return 0;
   const float k = rintf(hi * 64.f);
   const float r = fmaf(k, -0.015625f, hi) + lo;  // (the first difference is exact)
   const int ki = static_cast<int>(k);
@@ -75,11 +74,13 @@ struct RowWeight {
   int only;  // greedy: the token; else -1
   __device__ __forceinline__ unsigned long long operator()(float l, int x, const unsigned long long* pow_sh) const {
     if (only >= 0) return x == only ? 1ull << kOne : 0;
+    const float d = max - l, y = d * c_hi;
+    // Most tokens are far below the largest: a plain power in steps of 2^-43, of at most 2^-24, is within a step or so.
+    if (!(y < 24.f)) return y < 44.f ? static_cast<unsigned long long>(__float2uint_rz(fast_exp2(static_cast<float>(kOne) - y))) : 0;
     // max - l = d + e exactly
-    const float d = max - l, b = d - max;
+    const float b = d - max;
     const float e = (max - (d - b)) - (l + b);
-    const float hi = d * c_hi;
-    return weight_of(hi, fmaf(d, c_hi, -hi) + fmaf(d, c_lo, e * c_hi), pow_sh);
+    return weight_of(y, fmaf(d, c_hi, -y) + fmaf(d, c_lo, e * c_hi), pow_sh);
   }
 };
 __device__ __forceinline__ RowWeight row_weight(float temperature) {
@@ -122,85 +123,93 @@ __device__ __forceinline__ float max_of(unsigned long long order) {
   return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 
+// Over a warp, by 16 or 32 bits at a time.
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long other = __shfl_xor_sync(0xffffffffu, v, o);
-    v = other > v ? other : v;
-  }
-  return v;
+  const uint32_t hi = static_cast<uint32_t>(v >> 32), top = __reduce_max_sync(0xffffffffu, hi);
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, hi == top ? static_cast<uint32_t>(v) : 0u);
+  return (static_cast<unsigned long long>(top) << 32) | lo;
 }
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+  unsigned long long sum = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int i = 0; i < 64; i += 16)
+    sum += static_cast<unsigned long long>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> i) & 0xffffu)) << i;
+  return sum;
 }
-__device__ __forceinline__ unsigned long long remote_u64(const unsigned long long* p, uint32_t rank) {
-  const uint32_t at = mapa_shared(smem_u32(p), rank);
-  const uint32_t lo = static_cast<uint32_t>(ld_shared_cluster_b32(at)), hi = static_cast<uint32_t>(ld_shared_cluster_b32(at + 4));
-  return lo | (static_cast<unsigned long long>(hi) << 32);
+__device__ __forceinline__ void store_remote(const unsigned long long* p, uint32_t rank, unsigned long long v) {
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "l"(v) : "memory");
 }
-
-// What the cluster exchanges: a CTA's part of a reduction. Two, used in turn: one is
-// written again when every CTA has passed the next reduction's barrier.
-struct Exchange {
-  unsigned long long slot[2];
-};
 
 template <typename T, bool kDrawn>
 __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_constant__ AcceptParams p) {
   extern __shared__ unsigned long long dyn_sh[];  // kDrawn: weights, then q; else logits
   __shared__ unsigned long long pow_sh[64];
-  __shared__ unsigned long long warps_sh[2][kAccWarps], child_w[kMaxNodes];
-  __shared__ Exchange ex;
+  // every warp's part of a reduction, of the whole cluster; two, used in turn: one is written again when every CTA has
+  // passed the next reduction's barrier
+  __shared__ unsigned long long part_sh[2][kAcceptCluster * kAccWarps];
+  __shared__ unsigned long long child_w[kMaxNodes];  // of the nodes that are children
   __shared__ float u_sh[kMaxNodes], child_q[kMaxNodes];
-  __shared__ int par_sh[kMaxNodes], tok_sh[kMaxNodes], path_sh[kMaxNodes], child_sh[kMaxNodes], n_child;
+  __shared__ int par_sh[kMaxNodes], tok_sh[kMaxNodes], path_sh[kMaxNodes], bits_sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int size = p.cluster, rank = blockIdx.x % size, b = blockIdx.x / size;
+  if (size > 1) cluster_arrive();  // (others write to this CTA's shared memory: it has to be there)
   const int64_t node0 = static_cast<int64_t>(b) * p.nodes;
   const int given = p.tree_len ? __ldg(p.tree_len + b) : p.nodes, nodes = min(max(given, 0), p.nodes);
+  // this CTA's share of the vocabulary, this warp's range of it
+  const int lo = min(p.vocab, rank * p.share), hi = min(p.vocab, lo + p.share);
+  const int wlo = min(hi, lo + warp * p.warp_share), whi = min(hi, wlo + p.warp_share);
+  // sends for this CTA's share of a node's rows, in 128-byte lines
+  auto prefetch = [&](int node) {
+    constexpr int kLine = 128 / sizeof(T);
+    const T* row = static_cast<const T*>(p.logits) + (node0 + node) * p.logit_stride;
+    for (int x = lo + tid * kLine; x < hi; x += kAccThreads * kLine) prefetch_l2(row + x);
+    if (kDrawn)
+      for (int x = lo + tid * 32; x < hi; x += kAccThreads * 32) prefetch_l2(p.draft_prob + (node0 + node) * p.draft_stride + x);
+  };
+  if (nodes > 0) prefetch(0);
   int bits = given != nodes && tid == 0 ? kStatusBadTreeLen : 0;
+  if (tid < kMaxNodes) par_sh[tid] = -1;
   if (tid < nodes) {
     const int up = __ldg(p.tree_parent + node0 + tid), x = __ldg(p.tokens + node0 + tid);
     const bool linked = tid == 0 ? up == -1 : up >= 0 && up < tid, named = tid == 0 || (x >= 0 && x < p.vocab);
     if (!linked) bits |= kStatusBadParent;
     if (!named) bits |= kStatusBadToken;
-    par_sh[tid] = tid > 0 && linked && named ? up : -1;
+    if (tid > 0 && linked && named) par_sh[tid] = up;
     tok_sh[tid] = x;
     u_sh[tid] = tame_uniform(__ldg(p.uniform + node0 + tid));
   }
+  if (tid == 0) bits_sh = 0;
   if (tid < 64) pow_sh[tid] = c_pow[tid];
   const float temperature = __ldg(p.temperature + b);
   const bool greedy = !(temperature > 0.f);
   RowWeight w_of = row_weight(temperature);
-  // this CTA's share of the vocabulary, this warp's range of it
-  const int lo = min(p.vocab, rank * p.share), hi = min(p.vocab, lo + p.share);
-  const int wlo = min(hi, lo + warp * p.warp_share), whi = min(hi, wlo + p.warp_share);
   unsigned long long* weight_sh = dyn_sh - (kDrawn ? lo : 0);                     // [x] of token x
   float* value_sh = reinterpret_cast<float*>(dyn_sh + (kDrawn ? p.share : 0)) - lo;  // kDrawn: q, else logits
   int step = 0;  // of the reductions
-  // The cluster's sum of one number a thread (`max`: its largest), to all threads; also what comes before this CTA and warp.
-  unsigned long long before_cta, before_warp, my_warp;
+  // The cluster's sum of one number a thread (`max`: its largest), to all threads; of a sum also what comes before this
+  // warp's part.
+  unsigned long long before, my_warp;
   auto reduce = [&](unsigned long long v, bool max) {
-    auto over = [&](unsigned long long x) { return max ? warp_max(x) : warp_sum(x); };
-    v = over(v);
+    unsigned long long* part = part_sh[step++ & 1];
+    v = max ? warp_max(v) : warp_sum(v);
     my_warp = v;
-    if (lane == 0) warps_sh[step & 1][warp] = v;
-    __syncthreads();
-    const unsigned long long of_lane = lane < kAccWarps ? warps_sh[step & 1][lane] : 0;
-    v = over(of_lane);
-    if (!max) before_warp = warp_sum(lane < warp ? of_lane : 0);
-    before_cta = 0;
-    if (size > 1) {
-      if (tid == 0) ex.slot[step & 1] = v;
-      cluster_sync();
-      const unsigned long long of_cta = lane < size ? remote_u64(&ex.slot[step & 1], lane) : 0;
-      v = over(of_cta);
-      if (!max) before_cta = warp_sum(lane < rank ? of_cta : 0);
+    if (size == 1) {
+      if (lane == 0) part[warp] = v;
+      __syncthreads();
+    } else {
+      if (lane < size) store_remote(part + rank * kAccWarps + warp, lane, v);
+      cluster_sync();  // (after the last one, nothing is written to another CTA: it may have left)
     }
-    ++step;
-    return v;
+    unsigned long long all = 0, lower = 0;
+    for (int i = lane; i < size * kAccWarps; i += 32) {
+      const unsigned long long x = part[i];
+      all = max ? (x > all ? x : all) : all + x;
+      if (i < rank * kAccWarps + warp) lower += x;
+    }
+    if (!max) before = warp_sum(lower);
+    return max ? warp_max(all) : warp_sum(all);
   };
+  if (size > 1) cluster_wait();
   __syncthreads();
 
   int v = 0, len = nodes > 0 ? 1 : 0, next = -1;
@@ -209,6 +218,13 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
     const int64_t at = node0 + v;
     const T* row = static_cast<const T*>(p.logits) + at * p.logit_stride;
     const float* q = kDrawn ? p.draft_prob + at * p.draft_stride : nullptr;
+    // v's children: bit i of the masks, and a thread for each
+    uint32_t kids[kMaxNodes / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxNodes / 32; ++i) kids[i] = __ballot_sync(0xffffffffu, par_sh[32 * i + lane] == v);
+    const bool child = tid < nodes && par_sh[tid] == v;
+    const float l_child = child ? tame(logit(row + tok_sh[tid])) : 0.f;
+    const float q_child = kDrawn && child ? __ldg(q + tok_sh[tid]) : 1.f;
     // the row's share, and its largest (greedy: where that is, too, as the order of its bits over the lower index)
     unsigned long long best = 0;
     float top = -CUDART_INF_F;
@@ -223,44 +239,27 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         const int x = x0 + 32 * k;
-        if (x >= whi) break;
-        l[k] = tame(l[k]);
-        if (kDrawn) {
-          weight_sh[x] = __float_as_uint(l[k]);
-          value_sh[x] = d[k];
-        } else {
-          value_sh[x] = l[k];
+        if (x < whi) {
+          l[k] = tame(l[k]);
+          if (kDrawn) {
+            weight_sh[x] = __float_as_uint(l[k]);
+            value_sh[x] = d[k];
+          } else {
+            value_sh[x] = l[k];
+          }
+          if (greedy) {
+            const unsigned long long key = order_of(l[k], x);
+            best = key > best ? key : best;
+          }
+          top = fmaxf(top, l[k]);
         }
-        if (greedy) {
-          const unsigned long long key = order_of(l[k], x);
-          best = key > best ? key : best;
-        }
-        top = fmaxf(top, l[k]);
       }
     }
     if (!greedy) best = order_of(top, 0);
-    if (warp == 0) {  // v's children, in node order
-      int n = 0;
-      for (int i0 = v + 1; i0 < nodes; i0 += 32) {
-        const bool is = i0 + lane < nodes && par_sh[i0 + lane] == v;
-        const uint32_t vote = __ballot_sync(0xffffffffu, is);
-        if (is) child_sh[n + __popc(vote & ((1u << lane) - 1u))] = i0 + lane;
-        n += __popc(vote);
-      }
-      if (lane == 0) n_child = n;
-    }
+    // the first children's rows, on their way meanwhile
+    for (int i = 0, sent = 0; i < kMaxNodes / 32 && sent < kPrefetched; ++i)
+      for (uint32_t m = kids[i]; m != 0 && sent < kPrefetched; m &= m - 1, ++sent) prefetch(32 * i + __ffs(m) - 1);
     best = reduce(best, true);
-    const int n = n_child;
-    for (int c = 0; c < min(n, kPrefetched); ++c) {  // 128-byte lines of this CTA's share
-      const T* next_row = static_cast<const T*>(p.logits) + (node0 + child_sh[c]) * p.logit_stride;
-      constexpr int kLine = 128 / sizeof(T);
-      for (int x = lo + tid * kLine; x < hi; x += kAccThreads * kLine) prefetch_l2(next_row + x);
-      if (kDrawn)
-        for (int x = lo + tid * 32; x < hi; x += kAccThreads * 32)
-          prefetch_l2(p.draft_prob + (node0 + child_sh[c]) * p.draft_stride + x);
-    }
-    const float l_child = tid < n ? tame(logit(row + tok_sh[child_sh[tid]])) : 0.f;
-    const float q_child = kDrawn && tid < n ? __ldg(q + tok_sh[child_sh[tid]]) : 1.f;
     w_of.max = max_of(best);
     w_of.only = greedy ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
     if (!(w_of.max >= -3.4028235e38f)) {  // no logit is a number
@@ -273,56 +272,60 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
       if (kDrawn) weight_sh[x] = w;
       sum += w;
     }
-    if (tid < n) {
+    if (child) {
       // (a token that an earlier sibling had has been refused by the time it is tried)
       bool again = false;
       if (!kDrawn)
-        for (int c = 0; c < tid; ++c) again = again || tok_sh[child_sh[c]] == tok_sh[child_sh[tid]];
-      child_w[tid] = again ? 0 : w_of(l_child, tok_sh[child_sh[tid]], pow_sh);
+        for (int c = v + 1; c < tid; ++c) again = again || (par_sh[c] == v && tok_sh[c] == tok_sh[tid]);
+      child_w[tid] = again ? 0 : w_of(l_child, tok_sh[tid], pow_sh);
       child_q[tid] = fminf(fmaxf(q_child, 0.f), 1.f);
     }
     unsigned long long S = reduce(sum, false);
     unsigned long long due = 0;  // kDrawn: S of the refusal that the weights do not show yet
     int go = -1;
-    for (int c = 0; c < n; ++c) {
-      const unsigned long long w = child_w[c];
-      const double u = u_sh[child_sh[c]], share = kDrawn ? child_q[c] : 1.0;
-      if (u * static_cast<double>(S) * share < static_cast<double>(w)) {
-        go = child_sh[c];
-        break;
-      }
-      if (!kDrawn) {
-        if (w == 0 || w == S) continue;  // (a refusal that would leave nothing changes nothing)
-        S -= w;
-        const int x = tok_sh[child_sh[c]];
-        if (x < lo) before_cta -= w;
-        if (x >= lo && x < wlo) before_warp -= w;
-        if (x >= wlo && x < whi) {
-          my_warp -= w;
-          value_sh[x] = -CUDART_INF_F;  // (the warp's lanes all write it)
+#pragma unroll 1
+    for (int i = 0; i < kMaxNodes / 32 && go < 0; ++i) {
+#pragma unroll 1
+      for (uint32_t m = kids[i]; m != 0; m &= m - 1) {
+        const int c = 32 * i + __ffs(m) - 1;
+        const unsigned long long w = child_w[c];
+        const double u = u_sh[c], share = kDrawn ? child_q[c] : 1.0;
+        if (u * static_cast<double>(S) * share < static_cast<double>(w)) {
+          go = c;
+          break;
         }
-      } else {
-        const unsigned long long held_cta = before_cta, held_warp = before_warp, held = my_warp;
-        unsigned long long left = 0;
-        for (int x = wlo + lane; x < whi; x += 32) {
-          const float d = value_sh[x];
-          unsigned long long y = weight_sh[x];
-          if (due != 0) {
-            y = less(y, share_of(due, d));
-            weight_sh[x] = y;
+        if (!kDrawn) {
+          if (w == 0 || w == S) continue;  // (a refusal that would leave nothing changes nothing)
+          S -= w;
+          const int x = tok_sh[c];
+          if (x < wlo) before -= w;
+          if (x >= wlo && x < whi) {
+            my_warp -= w;
+            value_sh[x] = -CUDART_INF_F;  // (the warp's lanes all write it)
           }
-          left += less(y, share_of(S, d));
-        }
-        left = reduce(left, false);
-        due = 0;
-        if (left == 0) {
-          before_cta = held_cta, before_warp = held_warp, my_warp = held;
         } else {
-          __syncthreads();  // child_w has been read
-          if (tid > c && tid < n) child_w[tid] = less(child_w[tid], share_of(S, child_q[tid]));
-          __syncthreads();
-          due = S;
-          S = left;
+          const unsigned long long held_before = before, held = my_warp;
+          unsigned long long left = 0;
+          for (int x = wlo + lane; x < whi; x += 32) {
+            const float d = value_sh[x];
+            unsigned long long y = weight_sh[x];
+            if (due != 0) {
+              y = less(y, share_of(due, d));
+              weight_sh[x] = y;
+            }
+            left += less(y, share_of(S, d));
+          }
+          left = reduce(left, false);
+          due = 0;
+          if (left == 0) {
+            before = held_before, my_warp = held;
+          } else {
+            __syncthreads();  // child_w has been read
+            if (child && tid > c) child_w[tid] = less(child_w[tid], share_of(S, child_q[tid]));
+            __syncthreads();
+            due = S;
+            S = left;
+          }
         }
       }
     }
@@ -330,12 +333,11 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
       v = go;
       if (tid == 0) path_sh[len] = v;
       ++len;
-      __syncthreads();  // the children's lists are read
+      __syncthreads();  // the children's weights are read
       continue;
     }
     // the draw: the first x with the sum up to it above floor(u_0 S)
     const unsigned long long target = share_of(S, u_sh[0]);
-    unsigned long long before = before_cta + before_warp;
     if (target >= before && target - before < my_warp) {  // one warp of the cluster
       __syncwarp();
       // lanes take consecutive tokens, an odd number each (so that they meet in no bank)
@@ -372,19 +374,15 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
       if (next < 0) p.next_token[b] = -1;
     }
     bits = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bits)));
-    if (p.batch > 1) {
-      if (lane == 0 && bits) atomicOr(p.status, bits);
-    } else {  // one request: the word as a whole
-      int* all = reinterpret_cast<int*>(warps_sh);
-      if (lane == 0) all[warp] = bits;
-      __syncthreads();
-      if (tid == 0) {
-        for (int i = 1; i < kAccWarps; ++i) bits |= all[i];
-        *p.status = bits;
-      }
+    if (lane == 0 && bits) atomicOr(&bits_sh, bits);
+    __syncthreads();
+    if (tid == 0) {
+      if (p.batch == 1)
+        *p.status = bits_sh;  // the word as a whole
+      else if (bits_sh)
+        atomicOr(p.status, bits_sh);
     }
   }
-  if (size > 1) cluster_sync();  // no CTA leaves while its slots are read
 }
 
 template <typename T, bool kDrawn>

@@ -36,10 +36,11 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// a + b to a; returns what the rounding left
+__device__ __forceinline__ float add_exact(float& a, float b) {
+  const float s = a + b, part = s - a, rest = (a - (s - part)) + (b - part);
+  a = s;
+  return rest;
 }
 
 // kPairs: the rope values (2 i, 2 i + 1) turn together, else (i, i + 32).
@@ -78,21 +79,44 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv8_write_kernel(const __grid_
 #pragma unroll
     for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[k]));
     const float fit = warp_max(top) > pow2(50) ? pow2(-80) : 1.f;
-    float sum = 0.f;
+    // Sum and root carry what their roundings leave, so that c' is rounded once: a value next to a border between two
+    // 8-bit values goes where the formula puts it. (Squares and products of two bf16 values are exact in fp32.)
+    uint64_t hi = f32x2(0.f, 0.f), lo = hi;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[2 * k] *= fit, x[2 * k + 1] *= fit;
+      const uint64_t v = f32x2(x[2 * k], x[2 * k + 1]), sq = mul_x2(v, v), sum = add_x2(hi, sq), part = sub_x2(sum, hi);
+      lo = add_x2(lo, add_x2(sub_x2(hi, sub_x2(sum, part)), sub_x2(sq, part)));
+      hi = sum;
+    }
+    float h, l, h2, l2;
+    f32x2_split(hi, h, h2);
+    f32x2_split(lo, l, l2);
+    l += l2 + add_exact(h, h2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      h2 = __shfl_xor_sync(0xffffffffu, h, o);
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+      l += add_exact(h, h2);
+    }
+    h *= 1.f / kDv, l *= 1.f / kDv;
+    l += add_exact(h, p.eps * fit * fit);
+    const float y = rsqrtf(h), t = h * y;
+    // one step towards the root's last bits: y (1 + r / 2), r = 1 - (h + l) y^2
+    const float r = fmaf(-l * y, y, fmaf(-fmaf(h, y, -t), y, fmaf(-t, y, 1.f))), more = 0.5f * y * r;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      x[k] *= fit;
-      sum = fmaf(x[k], x[k], sum);
+      const float c = x[k] * w[k];
+      x[k] = fmaf(c, y, c * more);
     }
-    const float inv = 1.f / sqrtf(warp_sum(sum) * (1.f / kDv) + p.eps * fit * fit);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = x[k] * inv * w[k];
   }
   if (p.rotation) {
     const float* turn = p.rotation + static_cast<int64_t>(at) * (2 * kRopePairs) + lane;
     const float c = __ldg(turn), s = __ldg(turn + kRopePairs);
-    const float tx = rx * c - ry * s;
-    ry = ry * c + rx * s;
+    // (each rounded once but for the last sum)
+    const float ys = ry * s, xs = rx * s;
+    const float tx = fmaf(rx, c, -ys) + fmaf(-ry, s, ys);
+    ry = fmaf(ry, c, xs) + fmaf(rx, s, -xs);
     rx = tx;
   }
   float top = 0.f, rope = fmaxf(fabsf(rx), fabsf(ry));
