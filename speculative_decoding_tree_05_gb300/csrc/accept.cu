@@ -87,21 +87,35 @@ __device__ __forceinline__ RowWeight row_weight(float temperature) {
   RowWeight r;
   r.max = 0.f;
   r.only = -1;
-  const double c = temperature > 0.f ? fmin(1.4426950408889634 / static_cast<double>(temperature), 1e30) : 0.0;
-  r.c_hi = static_cast<float>(c);
-  r.c_lo = static_cast<float>(c - static_cast<double>(r.c_hi));
+  // log2 e / temperature in two floats
+  constexpr float kHi = 1.44269502e+00f, kLo = 1.92596303e-08f;
+  r.c_hi = temperature > 0.f ? fminf(kHi / temperature, 1e30f) : 0.f;
+  r.c_lo = r.c_hi > 0.f && r.c_hi < 1e30f ? (fmaf(-r.c_hi, temperature, kHi) + kLo) / temperature : 0.f;
   return r;
 }
 
-// floor(S q) for a probability q (clamped to [0, 1]; NaN: 0)
-__device__ __forceinline__ unsigned long long share_of(unsigned long long S, float q) {
-  if (!(q > 0.f)) return 0;
-  if (q >= 1.f) return S;
-  const uint32_t u = __float_as_uint(q);
-  const int e = static_cast<int>(u >> 23);  // at most 126
-  const unsigned long long mant = e > 0 ? (u & 0x7fffffu) | 0x800000u : 0;
-  return 126 - e > 63 ? 0 : __umul64hi(S, mant << 40) >> (126 - e);
+// floor(S u) for u in [0, 1)
+__device__ __forceinline__ unsigned long long share_of(unsigned long long S, float u) {
+  const uint32_t v = __float_as_uint(u);
+  const int e = static_cast<int>(v >> 23);  // at most 126
+  const unsigned long long mant = e > 0 ? (v & 0x7fffffu) | 0x800000u : 0;
+  return e < 63 ? 0 : __umul64hi(S, mant << 40) >> (126 - e);
 }
+// S q for many probabilities q (in [0, 1]; below that and NaN: 0, above: 1), from the 32 leading bits of S: 2^-32 of it off
+struct Shares {
+  uint32_t top;
+  int shift;  // S is top 2^shift
+  __device__ __forceinline__ explicit Shares(unsigned long long S) {
+    shift = max(0, 32 - __clzll(S));
+    top = static_cast<uint32_t>(S >> shift);
+  }
+  __device__ __forceinline__ unsigned long long operator()(float q) const {
+    const uint32_t v = __float_as_uint(fminf(fmaxf(q, 0.f), 1.f));  // (a NaN becomes 0)
+    const int by = 158 - shift - static_cast<int>(v >> 23);         // q is (2^23 + its last bits) 2^(exponent - 150)
+    const unsigned long long x = static_cast<unsigned long long>(top) * ((v & 0x7fffffu) | 0x800000u) << 8;
+    return by > 63 ? 0 : x >> by;
+  }
+};
 __device__ __forceinline__ unsigned long long less(unsigned long long w, unsigned long long s) { return w > s ? w - s : 0; }
 
 __device__ __forceinline__ float logit(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16); }
@@ -267,6 +281,7 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
       break;
     }
     unsigned long long sum = 0;
+#pragma unroll 4
     for (int x = wlo + lane; x < whi; x += 32) {
       const unsigned long long w = w_of(kDrawn ? __uint_as_float(static_cast<uint32_t>(weight_sh[x])) : value_sh[x], x, pow_sh);
       if (kDrawn) weight_sh[x] = w;
@@ -289,8 +304,8 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
       for (uint32_t m = kids[i]; m != 0; m &= m - 1) {
         const int c = 32 * i + __ffs(m) - 1;
         const unsigned long long w = child_w[c];
-        const double u = u_sh[c], share = kDrawn ? child_q[c] : 1.0;
-        if (u * static_cast<double>(S) * share < static_cast<double>(w)) {
+        // u S q < w of whole numbers: as floor(u floor(S q)) is
+        if (share_of(kDrawn ? Shares(S)(child_q[c]) : S, u_sh[c]) < w) {
           go = c;
           break;
         }
@@ -305,15 +320,17 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
           }
         } else {
           const unsigned long long held_before = before, held = my_warp;
+          const Shares taken(due), next_taken(S);
           unsigned long long left = 0;
+#pragma unroll 4
           for (int x = wlo + lane; x < whi; x += 32) {
             const float d = value_sh[x];
             unsigned long long y = weight_sh[x];
             if (due != 0) {
-              y = less(y, share_of(due, d));
+              y = less(y, taken(d));
               weight_sh[x] = y;
             }
-            left += less(y, share_of(S, d));
+            left += less(y, next_taken(d));
           }
           left = reduce(left, false);
           due = 0;
@@ -321,7 +338,7 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
             before = held_before, my_warp = held;
           } else {
             __syncthreads();  // child_w has been read
-            if (child && tid > c) child_w[tid] = less(child_w[tid], share_of(S, child_q[tid]));
+            if (child && tid > c) child_w[tid] = less(child_w[tid], next_taken(child_q[tid]));
             __syncthreads();
             due = S;
             S = left;
@@ -342,8 +359,9 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
       __syncwarp();
       // lanes take consecutive tokens, an odd number each (so that they meet in no bank)
       const int each = ((whi - wlo + 31) / 32) | 1, first = min(whi, wlo + lane * each), last = min(whi, first + each);
+      const Shares taken(due);
       auto weight = [&](int x) {
-        return kDrawn ? less(weight_sh[x], share_of(due, value_sh[x])) : w_of(value_sh[x], x, pow_sh);
+        return kDrawn ? due != 0 ? less(weight_sh[x], taken(value_sh[x])) : weight_sh[x] : w_of(value_sh[x], x, pow_sh);
       };
       unsigned long long mine = 0;
       for (int x = first; x < last; ++x) mine += weight(x);
