@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kAccThreads = 512, kAccWarps = kAccThreads / 32;
 constexpr int kOne = 43;         // weight 1 is 2^43; up to 2^18 of them fit in 64 bits
+constexpr float kNear = 24.f;    // from 2^-kNear on, plain powers
 constexpr int kUnroll = 16;      // loads in flight of a thread
 constexpr int kPrefetched = 4;   // children whose rows are sent for
 
@@ -72,15 +73,20 @@ __device__ __forceinline__ unsigned long long weight_of(float hi, float lo, cons
 struct RowWeight {
   float max, c_hi, c_lo;
   int only;  // greedy: the token; else -1
+  // of token x, whose distance from the largest logit is y in units of a halving
+  __device__ __forceinline__ float distance(float l) const { return (max - l) * c_hi; }
+  __device__ __forceinline__ unsigned long long exactly(float l, float y, const unsigned long long* pow_sh) const {
+    const float d = max - l, b = d - max, e = (max - (d - b)) - (l + b);  // max - l = d + e exactly
+    return weight_of(y, fmaf(d, c_hi, -y) + fmaf(d, c_lo, e * c_hi), pow_sh);
+  }
+  // Most tokens are far below the largest: a plain power in steps of 2^-43, of at most 2^-24, is within a step or so.
+  static __device__ __forceinline__ unsigned long long plainly(float y) {
+    return __float2uint_rz(fast_exp2(static_cast<float>(kOne) - y));  // (NaN, of an excluded token: 0)
+  }
   __device__ __forceinline__ unsigned long long operator()(float l, int x, const unsigned long long* pow_sh) const {
     if (only >= 0) return x == only ? 1ull << kOne : 0;
-    const float d = max - l, y = d * c_hi;
-    // Most tokens are far below the largest: a plain power in steps of 2^-43, of at most 2^-24, is within a step or so.
-    if (!(y < 24.f)) return y < 44.f ? static_cast<unsigned long long>(__float2uint_rz(fast_exp2(static_cast<float>(kOne) - y))) : 0;
-    // max - l = d + e exactly
-    const float b = d - max;
-    const float e = (max - (d - b)) - (l + b);
-    return weight_of(y, fmaf(d, c_hi, -y) + fmaf(d, c_lo, e * c_hi), pow_sh);
+    const float y = distance(l);
+    return y < kNear ? exactly(l, y, pow_sh) : plainly(y);
   }
 };
 __device__ __forceinline__ RowWeight row_weight(float temperature) {
@@ -101,7 +107,7 @@ __device__ __forceinline__ unsigned long long share_of(unsigned long long S, flo
   const unsigned long long mant = e > 0 ? (v & 0x7fffffu) | 0x800000u : 0;
   return e < 63 ? 0 : __umul64hi(S, mant << 40) >> (126 - e);
 }
-// S q for many probabilities q (in [0, 1]; below that and NaN: 0, above: 1), from the 32 leading bits of S: 2^-32 of it off
+// S q for many probabilities q in [0, 1], from the 32 leading bits of S: 2^-32 of it off
 struct Shares {
   uint32_t top;
   int shift;  // S is top 2^shift
@@ -110,8 +116,8 @@ struct Shares {
     top = static_cast<uint32_t>(S >> shift);
   }
   __device__ __forceinline__ unsigned long long operator()(float q) const {
-    const uint32_t v = __float_as_uint(fminf(fmaxf(q, 0.f), 1.f));  // (a NaN becomes 0)
-    const int by = 158 - shift - static_cast<int>(v >> 23);         // q is (2^23 + its last bits) 2^(exponent - 150)
+    const uint32_t v = __float_as_uint(q);
+    const int by = 158 - shift - static_cast<int>(v >> 23);  // q is (2^23 + its last bits) 2^(exponent - 150)
     const unsigned long long x = static_cast<unsigned long long>(top) * ((v & 0x7fffffu) | 0x800000u) << 8;
     return by > 63 ? 0 : x >> by;
   }
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
           l[k] = tame(l[k]);
           if (kDrawn) {
             weight_sh[x] = __float_as_uint(l[k]);
-            value_sh[x] = d[k];
+            value_sh[x] = fminf(fmaxf(d[k], 0.f), 1.f);  // (a NaN becomes 0)
           } else {
             value_sh[x] = l[k];
           }
@@ -281,11 +287,36 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
       break;
     }
     unsigned long long sum = 0;
-#pragma unroll 4
-    for (int x = wlo + lane; x < whi; x += 32) {
-      const unsigned long long w = w_of(kDrawn ? __uint_as_float(static_cast<uint32_t>(weight_sh[x])) : value_sh[x], x, pow_sh);
-      if (kDrawn) weight_sh[x] = w;
-      sum += w;
+    // four tokens a lane at a time, so that their chains overlap
+    for (int x0 = wlo + lane; x0 - lane < whi; x0 += 128) {
+      float l[4], y[4];
+      unsigned long long w[4];
+      bool near = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = x0 + 32 * k;
+        l[k] = x >= whi ? -CUDART_INF_F : kDrawn ? __uint_as_float(static_cast<uint32_t>(weight_sh[x])) : value_sh[x];
+        y[k] = w_of.distance(l[k]);
+        near = near || y[k] < kNear;
+      }
+      if (greedy) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = x0 + 32 * k < whi && x0 + 32 * k == w_of.only ? 1ull << kOne : 0;
+      } else if (__any_sync(0xffffffffu, near)) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const unsigned long long v = w_of.exactly(l[k], fminf(y[k], kNear), pow_sh);
+          w[k] = y[k] < kNear ? v : RowWeight::plainly(y[k]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = RowWeight::plainly(y[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (kDrawn && x0 + 32 * k < whi) weight_sh[x0 + 32 * k] = w[k];
+        sum += w[k];
+      }
     }
     if (child) {
       // (a token that an earlier sibling had has been refused by the time it is tried)
