@@ -9,7 +9,7 @@
 // the first x with w(0) + ... + w(x) > u_0 S.
 //
 // Weights are whole numbers: w(x) = 2^((l(x) - max l) log2 e / temperature) in steps of
-// 2^-43, their exponent carried in two floats (3e-10 of each weight; in one where the weight is below 2^-24, which is
+// 2^-43, their exponent carried in two floats (10^-9 of each weight; in one where the weight is below 2^-24, which is
 // off by a step or so). So sums are exact in any order, the same tokens come out on any tiling, and a token on the border
 // between two answers is decided as 64-bit arithmetic decides it, but for one draw in 10^5 or so.
 //
@@ -33,7 +33,6 @@ constexpr int kAccThreads = 512, kAccWarps = kAccThreads / 32;
 constexpr int kOne = 43;         // weight 1 is 2^43; up to 2^18 of them fit in 64 bits
 constexpr float kNear = 24.f;    // from 2^-kNear on, plain powers
 constexpr int kUnroll = 16;      // loads in flight of a thread
-constexpr int kPrefetched = 4;   // children whose rows are sent for
 
 // 2^(62 - i / 64), i = 0 to 63
 __constant__ unsigned long long c_pow[64] = {
@@ -55,17 +54,22 @@ __constant__ unsigned long long c_pow[64] = {
     0x216ab0d9f3121ec5ull, 0x210e8a30eb379012ull, 0x20b361a62b0ae876ull, 0x2059347cef00c1ddull,
 };
 
-// 2^-(hi + lo) in steps of 2^-43, rounded down; 0 <= hi < 24, |lo| small. `pow_sh` is c_pow in shared memory.
+// Whole numbers by an addition, where a conversion instruction takes four times as long: x + kWhole is rounded to one
+// (|x| <= 2^22), and its bits count on from kWhole's.
+constexpr float kWhole = 12582912.f;  // 1.5 2^23
+__device__ __forceinline__ int whole_bits(float x_plus) { return __float_as_int(x_plus) - __float_as_int(kWhole); }
+
+// 2^-(hi + lo) in steps of 2^-43, rounded down; 0 <= hi <= 24, |lo| small. `pow_sh` is c_pow in shared memory.
 __device__ __forceinline__ unsigned long long weight_of(float hi, float lo, const unsigned long long* pow_sh) {
-  const float k = rintf(hi * 64.f);
-  const float r = fmaf(k, -0.015625f, hi) + lo;  // (the first difference is exact)
-  const int ki = static_cast<int>(k);
-  // 2^-r - 1, |r| <= 2^-7: its error, 2^-31, is the weight's
+  const float kp = fmaf(hi, 64.f, kWhole);
+  const int ki = whole_bits(kp);
+  const float r = fmaf(kp - kWhole, -0.015625f, hi) + lo;  // (the first difference is exact)
+  // 2^-r - 1, |r| <= 2^-7, to 2^-30: its error is the weight's
   const float z = r * -0.69314718055994531f;
   const float g = fmaf(z * z, fmaf(z, fmaf(z, 1.f / 24, 1.f / 6), 0.5f), z);
-  const int gi = __float2int_rn(g * 274877906944.f);  // 2^38
+  const int gi = whole_bits(fmaf(g, 536870912.f, kWhole));  // g 2^29, below 2^22
   const long long top = static_cast<long long>(pow_sh[ki & 63]);
-  const long long w = top + ((static_cast<long long>(static_cast<int>(top >> 32)) * gi) >> 6);
+  const long long w = top + static_cast<long long>(static_cast<int>(top >> 32)) * gi * 8;
   return static_cast<unsigned long long>(w) >> ((62 - kOne) + (ki >> 6));
 }
 
@@ -74,14 +78,14 @@ struct RowWeight {
   float max, c_hi, c_lo;
   int only;  // greedy: the token; else -1
   // of token x, whose distance from the largest logit is y in units of a halving
-  __device__ __forceinline__ float distance(float l) const { return (max - l) * c_hi; }
+  __device__ __forceinline__ float distance(float l) const { return l > -CUDART_INF_F ? (max - l) * c_hi : CUDART_INF_F; }
   __device__ __forceinline__ unsigned long long exactly(float l, float y, const unsigned long long* pow_sh) const {
     const float d = max - l, b = d - max, e = (max - (d - b)) - (l + b);  // max - l = d + e exactly
     return weight_of(y, fmaf(d, c_hi, -y) + fmaf(d, c_lo, e * c_hi), pow_sh);
   }
   // Most tokens are far below the largest: a plain power in steps of 2^-43, of at most 2^-24, is within a step or so.
   static __device__ __forceinline__ unsigned long long plainly(float y) {
-    return __float2uint_rz(fast_exp2(static_cast<float>(kOne) - y));  // (NaN, of an excluded token: 0)
+    return static_cast<uint32_t>(whole_bits(fast_exp2(fminf(kOne - y, kOne - kNear)) + kWhole));
   }
   __device__ __forceinline__ unsigned long long operator()(float l, int x, const unsigned long long* pow_sh) const {
     if (only >= 0) return x == only ? 1ull << kOne : 0;
@@ -126,6 +130,17 @@ __device__ __forceinline__ unsigned long long less(unsigned long long w, unsigne
 
 __device__ __forceinline__ float logit(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16); }
 __device__ __forceinline__ float logit(const float* p) { return __ldg(p); }
+// The same, issued where it stands (an ordinary load moves down to its use, behind the row).
+__device__ __forceinline__ float logit_now(const uint16_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+__device__ __forceinline__ float logit_now(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
 // NaN counts as -inf, +inf as the largest number
 __device__ __forceinline__ float tame(float l) { return l >= -3.4028235e38f ? fminf(l, 3.4028235e38f) : -CUDART_INF_F; }
 
@@ -179,14 +194,14 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
   const int lo = min(p.vocab, rank * p.share), hi = min(p.vocab, lo + p.share);
   const int wlo = min(hi, lo + warp * p.warp_share), whi = min(hi, wlo + p.warp_share);
   // sends for this CTA's share of a node's rows, in 128-byte lines
-  auto prefetch = [&](int node) {
+  auto prefetch = [&](int node, int first, int step) {  // by threads first, first + 1, .. of step
     constexpr int kLine = 128 / sizeof(T);
     const T* row = static_cast<const T*>(p.logits) + (node0 + node) * p.logit_stride;
-    for (int x = lo + tid * kLine; x < hi; x += kAccThreads * kLine) prefetch_l2(row + x);
+    for (int x = lo + first * kLine; x < hi; x += step * kLine) prefetch_l2(row + x);
     if (kDrawn)
-      for (int x = lo + tid * 32; x < hi; x += kAccThreads * 32) prefetch_l2(p.draft_prob + (node0 + node) * p.draft_stride + x);
+      for (int x = lo + first * 32; x < hi; x += step * 32) prefetch_l2(p.draft_prob + (node0 + node) * p.draft_stride + x);
   };
-  if (nodes > 0) prefetch(0);
+  if (nodes > 0) prefetch(0, tid, kAccThreads);
   int bits = given != nodes && tid == 0 ? kStatusBadTreeLen : 0;
   if (tid < kMaxNodes) par_sh[tid] = -1;
   if (tid < nodes) {
@@ -206,28 +221,46 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
   unsigned long long* weight_sh = dyn_sh - (kDrawn ? lo : 0);                     // [x] of token x
   float* value_sh = reinterpret_cast<float*>(dyn_sh + (kDrawn ? p.share : 0)) - lo;  // kDrawn: q, else logits
   int step = 0;  // of the reductions
-  // The cluster's sum of one number a thread (`max`: its largest), to all threads; of a sum also what comes before this
-  // warp's part.
+  // The cluster's sum of one number a thread (or its largest), to all threads, in two halves with work between them; of
+  // a sum also what comes before this warp's part.
   unsigned long long before, my_warp;
-  auto reduce = [&](unsigned long long v, bool max) {
-    unsigned long long* part = part_sh[step++ & 1];
-    v = max ? warp_max(v) : warp_sum(v);
+  auto send = [&](unsigned long long v) {  // of a warp
+    unsigned long long* part = part_sh[++step & 1];
     my_warp = v;
     if (size == 1) {
       if (lane == 0) part[warp] = v;
-      __syncthreads();
     } else {
       if (lane < size) store_remote(part + rank * kAccWarps + warp, lane, v);
-      cluster_sync();  // (after the last one, nothing is written to another CTA: it may have left)
+      __syncwarp();
+      cluster_arrive();
     }
+  };
+  auto arrived = [&] {
+    __syncwarp();
+    if (size == 1)
+      __syncthreads();
+    else
+      cluster_wait();  // (after the last one, nothing is written to another CTA: it may have left)
+  };
+  auto get_max = [&] {
+    arrived();
+    unsigned long long all = 0;
+    for (int i = lane; i < size * kAccWarps; i += 32) {
+      const unsigned long long x = part_sh[step & 1][i];
+      all = x > all ? x : all;
+    }
+    return warp_max(all);
+  };
+  auto get_sum = [&] {
+    arrived();
     unsigned long long all = 0, lower = 0;
     for (int i = lane; i < size * kAccWarps; i += 32) {
-      const unsigned long long x = part[i];
-      all = max ? (x > all ? x : all) : all + x;
+      const unsigned long long x = part_sh[step & 1][i];
+      all += x;
       if (i < rank * kAccWarps + warp) lower += x;
     }
-    if (!max) before = warp_sum(lower);
-    return max ? warp_max(all) : warp_sum(all);
+    before = warp_sum(lower);
+    return warp_sum(all);
   };
   if (size > 1) cluster_wait();
   __syncthreads();
@@ -243,8 +276,11 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < kMaxNodes / 32; ++i) kids[i] = __ballot_sync(0xffffffffu, par_sh[32 * i + lane] == v);
     const bool child = tid < nodes && par_sh[tid] == v;
-    const float l_child = child ? tame(logit(row + tok_sh[tid])) : 0.f;
-    const float q_child = kDrawn && child ? __ldg(q + tok_sh[tid]) : 1.f;
+    float l_child = 0.f, q_child = 1.f;
+    if (child) {
+      l_child = logit_now(row + tok_sh[tid]);
+      if (kDrawn) q_child = logit_now(q + tok_sh[tid]);
+    }
     // the row's share, and its largest (greedy: where that is, too, as the order of its bits over the lower index)
     unsigned long long best = 0;
     float top = -CUDART_INF_F;
@@ -276,10 +312,18 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
       }
     }
     if (!greedy) best = order_of(top, 0);
-    // the first children's rows, on their way meanwhile
-    for (int i = 0, sent = 0; i < kMaxNodes / 32 && sent < kPrefetched; ++i)
-      for (uint32_t m = kids[i]; m != 0 && sent < kPrefetched; m &= m - 1, ++sent) prefetch(32 * i + __ffs(m) - 1);
-    best = reduce(best, true);
+    send(warp_max(best));
+    {  // the first children's rows, on their way meanwhile: 128 threads for each
+      int c = -1, skip = tid >> 7;
+#pragma unroll
+      for (int i = 0; i < kMaxNodes / 32; ++i) {
+        uint32_t m = kids[i];
+        for (; c < 0 && m != 0; m &= m - 1)
+          if (skip-- == 0) c = 32 * i + __ffs(m) - 1;
+      }
+      if (c >= 0) prefetch(c, tid & 127, 128);
+    }
+    best = get_max();
     w_of.max = max_of(best);
     w_of.only = greedy ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
     if (!(w_of.max >= -3.4028235e38f)) {  // no logit is a number
@@ -318,15 +362,22 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
         sum += w[k];
       }
     }
+    send(warp_sum(sum));
     if (child) {
       // (a token that an earlier sibling had has been refused by the time it is tried)
       bool again = false;
       if (!kDrawn)
-        for (int c = v + 1; c < tid; ++c) again = again || (par_sh[c] == v && tok_sh[c] == tok_sh[tid]);
-      child_w[tid] = again ? 0 : w_of(l_child, tok_sh[tid], pow_sh);
+#pragma unroll
+        for (int i = 0; i < kMaxNodes / 32; ++i)
+          for (uint32_t m = kids[i]; m != 0; m &= m - 1) {
+            const int c = 32 * i + __ffs(m) - 1;
+            again = again || (c < tid && tok_sh[c] == tok_sh[tid]);
+          }
+      child_w[tid] = again ? 0 : w_of(tame(l_child), tok_sh[tid], pow_sh);
       child_q[tid] = fminf(fmaxf(q_child, 0.f), 1.f);
     }
-    unsigned long long S = reduce(sum, false);
+    unsigned long long S = get_sum();
+    __syncthreads();  // the children's weights
     unsigned long long due = 0;  // kDrawn: S of the refusal that the weights do not show yet
     int go = -1;
 #pragma unroll 1
@@ -363,7 +414,8 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
             }
             left += less(y, next_taken(d));
           }
-          left = reduce(left, false);
+          send(warp_sum(left));
+          left = get_sum();
           due = 0;
           if (left == 0) {
             before = held_before, my_warp = held;
