@@ -171,22 +171,25 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
     sum += static_cast<unsigned long long>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> i) & 0xffffu)) << i;
   return sum;
 }
-__device__ __forceinline__ void store_remote(const unsigned long long* p, uint32_t rank, unsigned long long v) {
-  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "l"(v) : "memory");
-}
-
 template <typename T, bool kDrawn>
 __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_constant__ AcceptParams p) {
   extern __shared__ unsigned long long dyn_sh[];  // kDrawn: weights, then q; else logits
   __shared__ unsigned long long pow_sh[64];
-  // every warp's part of a reduction, of the whole cluster; two, used in turn: one is written again when every CTA has
-  // passed the next reduction's barrier
+  // Every warp's part of a reduction, of the whole cluster; two, used in turn: a warp sends its part of the next one when
+  // it has read this one, so a part is written again when all have read it.
   __shared__ unsigned long long part_sh[2][kAcceptCluster * kAccWarps];
+  __shared__ uint64_t part_bar[2];  // their bytes have come
   __shared__ unsigned long long child_w[kMaxNodes];  // of the nodes that are children
   __shared__ float u_sh[kMaxNodes], child_q[kMaxNodes];
   __shared__ int par_sh[kMaxNodes], tok_sh[kMaxNodes], path_sh[kMaxNodes], bits_sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int size = p.cluster, rank = blockIdx.x % size, b = blockIdx.x / size;
+  if (tid == 0) {
+    mbar_init(&part_bar[0], 1);
+    mbar_init(&part_bar[1], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   if (size > 1) cluster_arrive();  // (others write to this CTA's shared memory: it has to be there)
   const int64_t node0 = static_cast<int64_t>(b) * p.nodes;
   const int given = p.tree_len ? __ldg(p.tree_len + b) : p.nodes, nodes = min(max(given, 0), p.nodes);
@@ -224,23 +227,31 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
   // The cluster's sum of one number a thread (or its largest), to all threads, in two halves with work between them; of
   // a sum also what comes before this warp's part.
   unsigned long long before, my_warp;
+  bool lost = false;  // a wait ran out
   auto send = [&](unsigned long long v) {  // of a warp
-    unsigned long long* part = part_sh[++step & 1];
+    ++step;
+    unsigned long long* part = part_sh[step & 1] + rank * kAccWarps + warp;
+    uint64_t* bar = &part_bar[step & 1];
     my_warp = v;
     if (size == 1) {
-      if (lane == 0) part[warp] = v;
+      if (lane == 0) *part = v;
     } else {
-      if (lane < size) store_remote(part + rank * kAccWarps + warp, lane, v);
-      __syncwarp();
-      cluster_arrive();
+      if (tid == 0) mbar_arrive_expect_tx(bar, size * kAccWarps * 8);
+#ifdef DDT_TEST_HOOKS
+      if (rank == 0 && warp == 1 && step == p.test_keep_back) return;
+#endif
+      // (a plain remote store and a barrier of the cluster: 2500 cycles a reduction in place of NNNN)
+      if (lane < size) st_async_b64(mapa_shared(smem_u32(part), lane), v, mapa_shared(smem_u32(bar), lane));
     }
   };
   auto arrived = [&] {
-    __syncwarp();
-    if (size == 1)
+    if (size == 1) {
       __syncthreads();
-    else
-      cluster_wait();  // (after the last one, nothing is written to another CTA: it may have left)
+    } else {
+      bool in = false;
+      for (uint32_t i = 0; !in && i < DDT_WAIT_LIMIT; ++i) in = mbar_try_wait_cluster(&part_bar[step & 1], ((step - 1) >> 1) & 1);
+      lost = __syncthreads_or(!in);
+    }
   };
   auto get_max = [&] {
     arrived();
@@ -324,6 +335,7 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
       if (c >= 0) prefetch(c, tid & 127, 128);
     }
     best = get_max();
+    if (lost) break;
     w_of.max = max_of(best);
     w_of.only = greedy ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
     if (!(w_of.max >= -3.4028235e38f)) {  // no logit is a number
@@ -376,12 +388,12 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
       child_w[tid] = again ? 0 : w_of(tame(l_child), tok_sh[tid], pow_sh);
       child_q[tid] = fminf(fmaxf(q_child, 0.f), 1.f);
     }
-    unsigned long long S = get_sum();
-    __syncthreads();  // the children's weights
+    unsigned long long S = get_sum();  // (and the children's weights)
+    if (lost) break;
     unsigned long long due = 0;  // kDrawn: S of the refusal that the weights do not show yet
     int go = -1;
 #pragma unroll 1
-    for (int i = 0; i < kMaxNodes / 32 && go < 0; ++i) {
+    for (int i = 0; i < kMaxNodes / 32 && go < 0 && !lost; ++i) {
 #pragma unroll 1
       for (uint32_t m = kids[i]; m != 0; m &= m - 1) {
         const int c = 32 * i + __ffs(m) - 1;
@@ -416,6 +428,7 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
           }
           send(warp_sum(left));
           left = get_sum();
+          if (lost) break;
           due = 0;
           if (left == 0) {
             before = held_before, my_warp = held;
@@ -429,6 +442,7 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
         }
       }
     }
+    if (lost) break;
     if (go >= 0) {
       v = go;
       if (tid == 0) path_sh[len] = v;
@@ -467,6 +481,7 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
     next = 0;  // (written by the warp that found it)
     break;
   }
+  if (lost && tid == 0) bits |= kStatusTimeout;
   __syncthreads();
   if (rank == 0) {
     if (tid < p.nodes) p.path[node0 + tid] = tid < len ? path_sh[tid] : -1;
@@ -483,6 +498,11 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
       else if (bits_sh)
         atomicOr(p.status, bits_sh);
     }
+  }
+  if (size > 1) {
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while others may write to it (one whose wait ran out may be behind)
+    if (lost && rank != 0 && tid == 0) atomicOr(p.status, kStatusTimeout);
   }
 }
 

@@ -31,7 +31,10 @@ struct AcceptParams {
   int32_t* path;               // [B, T]
   int32_t* path_len;           // [B]
   int32_t* next_token;         // [B]
-  int32_t* status;             // cleared before the launch, unless there is one request
+  int32_t* status;             // cleared before the launch
+#ifdef DDT_TEST_HOOKS
+  int32_t test_keep_back;      // reduction of which one warp's part is not sent (-1: none)
+#endif
 };
 cudaError_t configure_accept();
 cudaError_t launch_accept(const AcceptParams& p, bool bf16, cudaStream_t stream);

@@ -197,6 +197,12 @@ __device__ __forceinline__ void st_async_b32(uint32_t remote_addr, uint32_t v, u
                : "memory");
 }
 
+__device__ __forceinline__ void st_async_b64(uint32_t remote_addr, uint64_t v, uint32_t remote_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(remote_addr), "l"(v),
+               "r"(remote_bar)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- TMA
 // 2-D tiled load of one box at coordinates (x, y) into shared memory.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint64_t* bar) {

@@ -300,6 +300,9 @@ extern "C" int ddtree_accept(const void* logits, int32_t logits_fp32, int64_t lo
   int sms = 0;
   if ((rc = current_device(&sms)) != DDT_OK) return rc;
   AcceptParams p = {};
+#ifdef DDT_TEST_HOOKS
+  p.test_keep_back = g_test_keep_back;
+#endif
   p.logits = logits;
   p.logit_stride = logit_stride;
   p.draft_prob = draft_prob;

@@ -11,7 +11,7 @@ import pytest
 import torch
 
 from speculative_decoding_tree_05_gb300 import ddtree
-from parity_util import require_cuda
+from parity_util import build_and_load, require_cuda
 
 pytestmark = pytest.mark.gpu
 NEAR = 1e-8
@@ -46,9 +46,9 @@ def make(batch, nodes, vocab, dtype=torch.float32, tree="random", drawn=False, t
                 temperature=torch.full((batch,), temperature, device="cuda"))
 
 
-def call(d, **kw):
+def call(d, library=None, **kw):
     batch, nodes, vocab = d["logits"].shape
-    a = ddtree.TreeAcceptor(batch, nodes, vocab)
+    a = ddtree.TreeAcceptor(batch, nodes, vocab, library=library)
     got = a(d["logits"], d["tokens"], d["parent"], d["uniform"], d["temperature"], draft_prob=d["draft"],
             tree_len=d["tree_len"], **kw)
     return [x.cpu().numpy() for x in got], a.status()
@@ -308,3 +308,20 @@ def test_captured_replayed_and_on_another_stream():
         torch.cuda.synchronize()
         assert a.status() == 0
         check(d, [x.cpu().numpy() for x in out])
+
+
+@pytest.mark.parametrize("batch,step", [(1, 1), (1, 2), (3, 1), (3, 4)])
+def test_a_wait_that_runs_out(batch, step):
+    """A test build does not send a warp's part of one reduction: the status word says so, and the next call is right."""
+    hooks = build_and_load("testhooks")
+    d = make(batch, 9, 40000, torch.bfloat16, "star", drawn=True, seed=17)
+    d["uniform"][:, 1:] = 0.9999            # several refusals, a reduction each
+    want, _ = call(d)
+    hooks.ddtree_test_set_keep_back(step)
+    try:
+        _, st = call(d, library=hooks)
+    finally:
+        hooks.ddtree_test_set_keep_back(-1)
+    assert st & ddtree.STATUS_TIMEOUT
+    got, st = call(d, library=hooks)
+    assert st == 0 and all((x == y).all() for x, y in zip(got, want))
