@@ -461,21 +461,29 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
         return kDrawn ? due != 0 ? less(weight_sh[x], taken(value_sh[x])) : weight_sh[x] : w_of(value_sh[x], x, pow_sh);
       };
       unsigned long long mine = 0;
+#pragma unroll 4
       for (int x = first; x < last; ++x) mine += weight(x);
-      unsigned long long incl = mine;
+      auto up_to = [&](unsigned long long v) {  // the sum over this lane and those below
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      before += incl - mine;
-      if (target >= before && target - before < mine) {
-        int x = first;
-        for (;; ++x) {
-          before += weight(x);
-          if (before > target) break;
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned long long y = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += y;
         }
-        p.next_token[b] = x;
+        return v;
+      };
+      // the lane whose tokens hold the sum, then the token, 32 at a time
+      const unsigned long long above = before + up_to(mine);
+      const int owner = __ffs(__ballot_sync(0xffffffffu, above > target)) - 1;
+      before = __shfl_sync(0xffffffffu, above - mine, owner);
+      const int to = __shfl_sync(0xffffffffu, last, owner);
+      for (int x0 = __shfl_sync(0xffffffffu, first, owner); x0 < to; x0 += 32) {
+        const unsigned long long sum = before + up_to(x0 + lane < to ? weight(x0 + lane) : 0);
+        const uint32_t vote = __ballot_sync(0xffffffffu, sum > target);
+        if (vote != 0) {
+          if (lane == 0) p.next_token[b] = x0 + __ffs(vote) - 1;
+          break;
+        }
+        before = __shfl_sync(0xffffffffu, sum, 31);
       }
     }
     next = 0;  // (written by the warp that found it)
