@@ -172,7 +172,7 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
   return sum;
 }
 template <typename T, bool kDrawn>
-__global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_constant__ AcceptParams p) {
+__global__ void __launch_bounds__(kAccThreads, 2) accept_kernel(const __grid_constant__ AcceptParams p) {
   extern __shared__ unsigned long long dyn_sh[];  // kDrawn: weights, then q; else logits
   __shared__ unsigned long long pow_sh[64];
   // Every warp's part of a reduction, of the whole cluster; two, used in turn: a warp sends its part of the next one when
@@ -514,20 +514,26 @@ __global__ void __launch_bounds__(kAccThreads, 1) accept_kernel(const __grid_con
   }
 }
 
-template <typename T, bool kDrawn>
-cudaError_t launch(const AcceptParams& p, size_t bytes, cudaStream_t stream) {
+struct AccLaunch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * p.cluster);
-  cfg.blockDim = dim3(kAccThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, accept_kernel<T, kDrawn>, p);
+  AccLaunch(int requests, int cluster, size_t bytes) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(requests) * cluster);
+    cfg.blockDim = dim3(kAccThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+
+template <typename T, bool kDrawn>
+cudaError_t launch(const AcceptParams& p, size_t bytes, cudaStream_t stream) {
+  AccLaunch l(p.batch, p.cluster, bytes);
+  l.cfg.stream = stream;
+  return cudaLaunchKernelEx(&l.cfg, accept_kernel<T, kDrawn>, p);
 }
 
 template <typename T, bool kDrawn>
@@ -539,11 +545,16 @@ cudaError_t configure() {
 
 }  // namespace
 
-cudaError_t configure_accept() {
+cudaError_t configure_accept(AcceptClusters* clusters) {
   cudaError_t e = configure<uint16_t, false>();
   if (e == cudaSuccess) e = configure<uint16_t, true>();
   if (e == cudaSuccess) e = configure<float, false>();
   if (e == cudaSuccess) e = configure<float, true>();
+  for (int i = 0; e == cudaSuccess && i < kAcceptSizes; ++i)
+    for (int half = 0; half < 2; ++half) {
+      AccLaunch l(1, 1 << i, half ? kAcceptBytes / 2 : kAcceptBytes);
+      e = cudaOccupancyMaxActiveClusters(&clusters->count[i][half], accept_kernel<float, true>, &l.cfg);
+    }
   return e;
 }
 

@@ -11,7 +11,7 @@ constexpr int32_t kStatusBadToken = 256;
 constexpr int32_t kStatusBadLogits = 512;
 constexpr int kAcceptVocab = 1 << 18;       // most tokens: a cluster of 16 CTAs holds a row of them in shared memory
 constexpr int kAcceptBytes = 200 * 1024;    // of that, in one CTA
-constexpr int kAcceptCluster = 16;
+constexpr int kAcceptCluster = 16, kAcceptSizes = 5;  // most CTAs of a request; 1, 2, 4, 8, 16
 // shared memory of a token: its logit, or with draft probabilities its weight and probability
 constexpr int accept_value_bytes(bool drawn) { return drawn ? 12 : 4; }
 
@@ -36,7 +36,11 @@ struct AcceptParams {
   int32_t test_keep_back;      // reduction of which one warp's part is not sent (-1: none)
 #endif
 };
-cudaError_t configure_accept();
+// How many clusters of 2^i CTAs one device runs at once; [1]: of at most half of kAcceptBytes, two CTAs to an SM
+struct AcceptClusters {
+  int count[kAcceptSizes][2] = {};
+};
+cudaError_t configure_accept(AcceptClusters* clusters);  // on the current device
 cudaError_t launch_accept(const AcceptParams& p, bool bf16, cudaStream_t stream);
 
 }  // namespace ddt

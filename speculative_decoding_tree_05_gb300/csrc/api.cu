@@ -23,6 +23,7 @@ constexpr int kMaxDevices = 64;
 struct DeviceInfo {
   int sm_count = 0;
   BlockClusters clusters;
+  AcceptClusters accept_clusters;
   bool ok = false;        // sm_103, and the verify kernels are set up
   bool cache_ok = false;  // and the cache-size and block kernels are
 };
@@ -51,7 +52,7 @@ int device_info(DeviceInfo* out) {
       d.cache_ok = configure_scores() == cudaSuccess && configure_evict() == cudaSuccess &&
                    configure_topk() == cudaSuccess && configure_block_attn(&d.clusters) == cudaSuccess &&
                    configure_summary() == cudaSuccess && configure_kv8_attn() == cudaSuccess &&
-                   configure_accept() == cudaSuccess;
+                   configure_accept(&d.accept_clusters) == cudaSuccess;
 #ifdef DDT_TEST_HOOKS
       if (g_test_fail_cache_setup) d.cache_ok = false;
 #endif
@@ -87,6 +88,12 @@ int current_device(int* sm_count, BlockClusters* clusters) {
   *sm_count = dev.sm_count;
   if (clusters) *clusters = dev.clusters;
   return dev.cache_ok ? DDT_OK : DDT_ERR_DEVICE;
+}
+
+void current_accept_clusters(AcceptClusters* clusters) {
+  DeviceInfo dev;
+  device_info(&dev);
+  *clusters = dev.accept_clusters;
 }
 
 namespace {

@@ -16,6 +16,9 @@ struct BlockClusters;  // cache_ops.cuh
 // kernels are set up; also how many clusters of block attention it runs at once, if asked.
 int current_device(int* sm_count, BlockClusters* clusters = nullptr);
 
+struct AcceptClusters;  // accept.cuh
+void current_accept_clusters(AcceptClusters* clusters);  // of a device that current_device() has found fit
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {

@@ -91,15 +91,26 @@ int check_accept(const ddt_dims* d, int32_t vocab) {
     return DDT_ERR_DIMS;
   return DDT_OK;
 }
-// CTAs of a request: enough to hold a row in shared memory, and more while there are SMs
-// for them and each keeps a thousand tokens.
-void accept_grid(int batch, int vocab, bool drawn, int sm_count, AcceptParams* p) {
-  auto share_of = [&](int n) { return ((vocab + n - 1) / n + 63) / 64 * 64; };
-  int n = 1;
-  while (n < kAcceptCluster && share_of(n) * accept_value_bytes(drawn) > kAcceptBytes) n *= 2;
-  while (n < kAcceptCluster && int64_t(batch) * n * 2 <= sm_count && vocab >= n * 2 * 1024) n *= 2;
-  p->cluster = n;
-  p->share = share_of(n);
+// CTAs of a request: enough to hold a row in shared memory, and as many as cost least. A
+// visit of a row takes about kVisit cycles and, with draft probabilities, 1.5 for each of a
+// CTA's tokens (else one), twice that where two CTAs meet on an SM; requests in several
+// rounds take as many times as long. (16 requests of 128001 tokens drawn: 8 CTAs each, of
+// which 15 clusters run at once, MMMM us, 16 of half the shared memory NNNN.)
+constexpr int64_t kVisit = 7000;
+void accept_grid(int batch, int vocab, bool drawn, int sm_count, const AcceptClusters& clusters, AcceptParams* p) {
+  int64_t best = -1;
+  for (int i = 0; i < kAcceptSizes; ++i) {
+    const int n = 1 << i, share = ((vocab + n - 1) / n + 63) / 64 * 64, bytes = share * accept_value_bytes(drawn);
+    const int active = bytes <= kAcceptBytes ? clusters.count[i][bytes <= kAcceptBytes / 2] : 0;
+    if (active < 1) continue;
+    const int64_t rounds = (batch + active - 1) / active, on_sm = (int64_t(std::min(batch, active)) * n + sm_count - 1) / sm_count;
+    const int64_t cost = rounds * (kVisit + share * (drawn ? 3 : 2) / 2 * on_sm);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p->cluster = n;
+      p->share = share;
+    }
+  }
   p->warp_share = ((p->share + 15) / 16 + 31) / 32 * 32;
 }
 
@@ -315,7 +326,10 @@ extern "C" int ddtree_accept(const void* logits, int32_t logits_fp32, int64_t lo
   p.batch = dims->batch;
   p.nodes = dims->num_nodes;
   p.vocab = vocab;
-  accept_grid(p.batch, vocab, draft_prob != nullptr, sms, &p);
+  AcceptClusters clusters;
+  current_accept_clusters(&clusters);
+  accept_grid(p.batch, vocab, draft_prob != nullptr, sms, clusters, &p);
+  if (p.cluster == 0) return DDT_ERR_DEVICE;
   p.path = path;
   p.path_len = path_len;
   p.next_token = next_token;
