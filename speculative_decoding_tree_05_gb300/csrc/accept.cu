@@ -4,12 +4,13 @@
 // children are tried in node order: with w the part of p that is left and S its sum, child
 // c with token x is accepted if u_c S q(x) < w(x). Drafted tokens that were picked (the
 // drafter's best) have q = 1, and a refused one leaves w without x; tokens that were drawn
-// from the drafter's distribution q leave max(w - S q, 0). Either way the accepted path
-// and the token after it follow p exactly. Where no child is accepted the next token is
+// from the drafter's distribution q leave max(w - S q, 0), which after several refusals is
+// max(w - T q, 0) of the first w, T the sum of their S. Either way the accepted path and the
+// token after it follow p exactly. Where no child is accepted the next token is
 // the first x with w(0) + ... + w(x) > u_0 S.
 //
 // Weights are whole numbers: w(x) = 2^((l(x) - max l) log2 e / temperature) in steps of
-// 2^-43, their exponent carried in two floats (10^-9 of each weight; in one where the weight is below 2^-24, which is
+// 2^-43, their exponent carried in two floats (2 10^-9 of each weight; in one where the weight is below 2^-24, which is
 // off by a step or so). So sums are exact in any order, the same tokens come out on any tiling, and a token on the border
 // between two answers is decided as 64-bit arithmetic decides it, but for one draw in 10^5 or so.
 //
@@ -34,24 +35,13 @@ constexpr int kOne = 43;         // weight 1 is 2^43; up to 2^18 of them fit in 
 constexpr float kNear = 24.f;    // from 2^-kNear on, plain powers
 constexpr int kUnroll = 16;      // loads in flight of a thread
 
-// 2^(62 - i / 64), i = 0 to 63
-__constant__ unsigned long long c_pow[64] = {
-    0x4000000000000000ull, 0x3f4f83033d21b05dull, 0x3ea0ecb6dc8a80cfull, 0x3df437dcc2b44eeeull,
-    0x3d495f454921b30bull, 0x3ca05dcf167fec4eull, 0x3bf92e66f736bd73ull, 0x3b53cc07b6650ae1ull,
-    0x3ab031b9f7490e4cull, 0x3a0e5a940f12f71aull, 0x396e41b9df20d22aull, 0x38cfe25cafa29694ull,
-    0x383337bb0aa53844ull, 0x37983d209783a449ull, 0x36feede5f6bc8dd5ull, 0x366745709e2bf5edull,
-    0x35d13f32b5a75abdull, 0x353cd6aaf3fb7e88ull, 0x34aa07647c4ab917ull, 0x3418ccf6bbcac965ull,
-    0x3389230547e12039ull, 0x32fb053fbc9c9f17ull, 0x326e6f619b8bc9e9ull, 0x31e35d322aee6c57ull,
-    0x3159ca845541b6b7ull, 0x30d1b3368925d902ull, 0x304b1332999c2516ull, 0x2fc5e66d9e9cc421ull,
-    0x2f4228e7d6030db0ull, 0x2ebfd6ac84cf917full, 0x2e3eebd1d8bee7baull, 0x2dbf6478ca345de4ull,
-    0x2d413cccfe779921ull, 0x2cc47104aa444922ull, 0x2c48fd6074ab0964ull, 0x2bcede2b5a4290ddull,
-    0x2b560fba90a852b2ull, 0x2ade8e6d6a4fb4ceull, 0x2a6856ad3a9f03beull, 0x29f364ed3a594d5aull,
-    0x297fb5aa6c544e3bull, 0x290d456b8279a028ull, 0x289c10c0c3125a06ull, 0x282c1443ee5c53f1ull,
-    0x27bd4c982468446bull, 0x274fb669cb3fedd4ull, 0x26e34e6e7553954eull, 0x26781164c82dfe99ull,
-    0x260dfc14636e2a5cull, 0x25a50b4dc8061680ull, 0x253d3bea3fbdc258ull, 0x24d68acbc4f9ba4bull,
-    0x2470f4dceac470ceull, 0x240c7710c519ac77ull, 0x23a90e62d17354f0ull, 0x2346b7d6df96ea79ull,
-    0x22e57078faa2f5baull, 0x2285355d525bbf67ull, 0x222603a024b6a14aull, 0x21c7d865a7a34404ull,
-    0x216ab0d9f3121ec5ull, 0x210e8a30eb379012ull, 0x20b361a62b0ae876ull, 0x2059347cef00c1ddull,
+// 2^(62 - i / 16), i = 0 to 15: as many as lie in different banks
+constexpr int kPowers = 16;
+__constant__ unsigned long long c_pow[kPowers] = {
+    0x4000000000000000ull, 0x3d495f454921b30bull, 0x3ab031b9f7490e4cull, 0x383337bb0aa53844ull,
+    0x35d13f32b5a75abdull, 0x3389230547e12039ull, 0x3159ca845541b6b7ull, 0x2f4228e7d6030db0ull,
+    0x2d413cccfe779921ull, 0x2b560fba90a852b2ull, 0x297fb5aa6c544e3bull, 0x27bd4c982468446bull,
+    0x260dfc14636e2a5cull, 0x2470f4dceac470ceull, 0x22e57078faa2f5baull, 0x216ab0d9f3121ec5ull,
 };
 
 // Whole numbers by an addition, where a conversion instruction takes four times as long: x + kWhole is rounded to one
@@ -61,16 +51,16 @@ __device__ __forceinline__ int whole_bits(float x_plus) { return __float_as_int(
 
 // 2^-(hi + lo) in steps of 2^-43, rounded down; 0 <= hi <= 24, |lo| small. `pow_sh` is c_pow in shared memory.
 __device__ __forceinline__ unsigned long long weight_of(float hi, float lo, const unsigned long long* pow_sh) {
-  const float kp = fmaf(hi, 64.f, kWhole);
+  const float kp = fmaf(hi, kPowers, kWhole);
   const int ki = whole_bits(kp);
-  const float r = fmaf(kp - kWhole, -0.015625f, hi) + lo;  // (the first difference is exact)
-  // 2^-r - 1, |r| <= 2^-7, to 2^-30: its error is the weight's
+  const float r = fmaf(kp - kWhole, -1.f / kPowers, hi) + lo;  // (the first difference is exact)
+  // 2^-r - 1, |r| <= 2^-5, to 2^-29: its error is the weight's
   const float z = r * -0.69314718055994531f;
   const float g = fmaf(z * z, fmaf(z, fmaf(z, 1.f / 24, 1.f / 6), 0.5f), z);
-  const int gi = whole_bits(fmaf(g, 536870912.f, kWhole));  // g 2^29, below 2^22
-  const long long top = static_cast<long long>(pow_sh[ki & 63]);
-  const long long w = top + static_cast<long long>(static_cast<int>(top >> 32)) * gi * 8;
-  return static_cast<unsigned long long>(w) >> ((62 - kOne) + (ki >> 6));
+  const int gi = __float2int_rn(g * 68719476736.f);  // 2^36
+  const long long top = static_cast<long long>(pow_sh[ki & (kPowers - 1)]);
+  const long long w = top + ((static_cast<long long>(static_cast<int>(top >> 32)) * gi) >> 4);
+  return static_cast<unsigned long long>(w) >> ((62 - kOne) + (ki / kPowers));
 }
 
 // A row's weights: 2^((l - max) c) with c = log2 e / temperature in two floats, or all of it on one token.
@@ -104,26 +94,28 @@ __device__ __forceinline__ RowWeight row_weight(float temperature) {
   return r;
 }
 
-// floor(S u) for u in [0, 1)
+// floor(S u) for u in [0, 1]
 __device__ __forceinline__ unsigned long long share_of(unsigned long long S, float u) {
+  if (u >= 1.f) return S;
   const uint32_t v = __float_as_uint(u);
   const int e = static_cast<int>(v >> 23);  // at most 126
   const unsigned long long mant = e > 0 ? (v & 0x7fffffu) | 0x800000u : 0;
   return e < 63 ? 0 : __umul64hi(S, mant << 40) >> (126 - e);
 }
-// S q for many probabilities q in [0, 1], from the 32 leading bits of S: 2^-32 of it off
+// 16 T q for many probabilities q in [0, 1], from the 32 leading bits of T: 2^-32 of it off
 struct Shares {
   uint32_t top;
-  int shift;  // S is top 2^shift
-  __device__ __forceinline__ explicit Shares(unsigned long long S) {
-    shift = max(0, 32 - __clzll(S));
-    top = static_cast<uint32_t>(S >> shift);
+  int shift;  // 16 T is top 2^shift
+  __device__ __forceinline__ explicit Shares(unsigned long long T) {
+    shift = max(0, 32 - __clzll(T));
+    top = static_cast<uint32_t>(T >> shift);
+    shift += 4;
   }
   __device__ __forceinline__ unsigned long long operator()(float q) const {
     const uint32_t v = __float_as_uint(q);
     const int by = 158 - shift - static_cast<int>(v >> 23);  // q is (2^23 + its last bits) 2^(exponent - 150)
     const unsigned long long x = static_cast<unsigned long long>(top) * ((v & 0x7fffffu) | 0x800000u) << 8;
-    return by > 63 ? 0 : x >> by;
+    return by > 63 ? 0 : by < 0 ? ~0ull : x >> by;
   }
 };
 __device__ __forceinline__ unsigned long long less(unsigned long long w, unsigned long long s) { return w > s ? w - s : 0; }
@@ -174,7 +166,7 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 template <typename T, bool kDrawn>
 __global__ void __launch_bounds__(kAccThreads, 2) accept_kernel(const __grid_constant__ AcceptParams p) {
   extern __shared__ unsigned long long dyn_sh[];  // kDrawn: weights, then q; else logits
-  __shared__ unsigned long long pow_sh[64];
+  __shared__ unsigned long long pow_sh[kPowers];
   // Every warp's part of a reduction, of the whole cluster; two, used in turn: a warp sends its part of the next one when
   // it has read this one, so a part is written again when all have read it.
   __shared__ unsigned long long part_sh[2][kAcceptCluster * kAccWarps];
@@ -217,7 +209,7 @@ __global__ void __launch_bounds__(kAccThreads, 2) accept_kernel(const __grid_con
     u_sh[tid] = tame_uniform(__ldg(p.uniform + node0 + tid));
   }
   if (tid == 0) bits_sh = 0;
-  if (tid < 64) pow_sh[tid] = c_pow[tid];
+  if (tid < kPowers) pow_sh[tid] = c_pow[tid];
   const float temperature = __ldg(p.temperature + b);
   const bool greedy = !(temperature > 0.f);
   RowWeight w_of = row_weight(temperature);
@@ -390,16 +382,16 @@ __global__ void __launch_bounds__(kAccThreads, 2) accept_kernel(const __grid_con
     }
     unsigned long long S = get_sum();  // (and the children's weights)
     if (lost) break;
-    unsigned long long due = 0;  // kDrawn: S of the refusal that the weights do not show yet
+    unsigned long long refused = 0;  // kDrawn: the S of the refusals, in 16s
     int go = -1;
 #pragma unroll 1
     for (int i = 0; i < kMaxNodes / 32 && go < 0 && !lost; ++i) {
 #pragma unroll 1
       for (uint32_t m = kids[i]; m != 0; m &= m - 1) {
         const int c = 32 * i + __ffs(m) - 1;
-        const unsigned long long w = child_w[c];
+        const unsigned long long w = kDrawn ? less(child_w[c], Shares(refused)(child_q[c])) : child_w[c];
         // u S q < w of whole numbers: as floor(u floor(S q)) is
-        if (share_of(kDrawn ? Shares(S)(child_q[c]) : S, u_sh[c]) < w) {
+        if (share_of(kDrawn ? share_of(S, child_q[c]) : S, u_sh[c]) < w) {
           go = c;
           break;
         }
@@ -414,29 +406,17 @@ __global__ void __launch_bounds__(kAccThreads, 2) accept_kernel(const __grid_con
           }
         } else {
           const unsigned long long held_before = before, held = my_warp;
-          const Shares taken(due), next_taken(S);
+          const Shares taken(refused + (S >> 4));
           unsigned long long left = 0;
 #pragma unroll 4
-          for (int x = wlo + lane; x < whi; x += 32) {
-            const float d = value_sh[x];
-            unsigned long long y = weight_sh[x];
-            if (due != 0) {
-              y = less(y, taken(d));
-              weight_sh[x] = y;
-            }
-            left += less(y, next_taken(d));
-          }
+          for (int x = wlo + lane; x < whi; x += 32) left += less(weight_sh[x], taken(value_sh[x]));
           send(warp_sum(left));
           left = get_sum();
           if (lost) break;
-          due = 0;
           if (left == 0) {
             before = held_before, my_warp = held;
           } else {
-            __syncthreads();  // child_w has been read
-            if (child && tid > c) child_w[tid] = less(child_w[tid], next_taken(child_q[tid]));
-            __syncthreads();
-            due = S;
+            refused += S >> 4;
             S = left;
           }
         }
@@ -456,9 +436,9 @@ __global__ void __launch_bounds__(kAccThreads, 2) accept_kernel(const __grid_con
       __syncwarp();
       // lanes take consecutive tokens, an odd number each (so that they meet in no bank)
       const int each = ((whi - wlo + 31) / 32) | 1, first = min(whi, wlo + lane * each), last = min(whi, first + each);
-      const Shares taken(due);
+      const Shares taken(refused);
       auto weight = [&](int x) {
-        return kDrawn ? due != 0 ? less(weight_sh[x], taken(value_sh[x])) : weight_sh[x] : w_of(value_sh[x], x, pow_sh);
+        return kDrawn ? less(weight_sh[x], taken(value_sh[x])) : w_of(value_sh[x], x, pow_sh);
       };
       unsigned long long mine = 0;
 #pragma unroll 4
