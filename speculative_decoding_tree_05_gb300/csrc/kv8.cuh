@@ -35,7 +35,7 @@ struct Kv8WriteParams {
   int64_t n, pool_slots;
   int32_t* status;
 };
-cudaError_t launch_kv8_write(const Kv8WriteParams& p, bool interleaved, cudaStream_t stream);
+cudaError_t launch_kv8_write(const Kv8WriteParams& p, bool interleaved, int sm_count, cudaStream_t stream);
 
 struct Kv8ReadParams {
   const uint8_t* pool;

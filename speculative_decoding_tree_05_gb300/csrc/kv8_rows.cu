@@ -14,28 +14,20 @@
 // bytes a row in, 644 + 1152 out.
 #include <cuda_runtime.h>
 #include <math_constants.h>
+#include <algorithm>
 #include "kv8.cuh"
 #include "ptx.cuh"
 
 namespace ddt {
 namespace {
 
-constexpr int kRowWarps = 8;
+constexpr int kRowWarps = 4;
+constexpr int kWriteBlocks = 7;  // blocks of an SM (72 registers)
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // -126 <= e <= 127
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
-  x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
-  x[4] = bf16_lo(v.z), x[5] = bf16_hi(v.z), x[6] = bf16_lo(v.w), x[7] = bf16_hi(v.w);
-}
-
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
 // a + b to a; returns what the rounding left
 __device__ __forceinline__ float add_exact(float& a, float b) {
   const float s = a + b, part = s - a, rest = (a - (s - part)) + (b - part);
@@ -43,116 +35,153 @@ __device__ __forceinline__ float add_exact(float& a, float b) {
   return rest;
 }
 
+// What a lane has of a row: latent values 8 lane + {0..7} and 256 + 8 lane + {0..7}, two rope values.
+struct RowLane {
+  uint4 a, b;
+  uint32_t rope;
+  int slot, at;
+};
+
 // kPairs: the rope values (2 i, 2 i + 1) turn together, else (i, i + 32).
-template <bool kPairs>
-__global__ void __launch_bounds__(kRowWarps * 32) kv8_write_kernel(const __grid_constant__ Kv8WriteParams p) {
+template <bool kPairs, bool kNorm>
+__global__ void __launch_bounds__(kRowWarps * 32, kWriteBlocks) kv8_write_kernel(const __grid_constant__ Kv8WriteParams p) {
   const int lane = threadIdx.x & 31;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRowWarps;
+  int64_t i = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
   if (i >= p.n) return;
-  const uint16_t* row = p.rows + i * p.row_stride;
-  const int slot = __ldg(p.slots + i);
-  const int at = p.rotation ? __ldg(p.position + i) : 0;
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(row) + lane), b = __ldg(reinterpret_cast<const uint4*>(row + 256) + lane);
-  float rx, ry;
-  if (kPairs) {
-    const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(row + kDv) + lane);
-    rx = bf16_lo(v), ry = bf16_hi(v);
-  } else {
-    rx = bf16_lo(__ldg(row + kDv + lane)), ry = bf16_lo(__ldg(row + kDv + kRopePairs + lane));
+  auto load = [&](int64_t i) {
+    const uint16_t* row = p.rows + i * p.row_stride;
+    RowLane v;
+    v.slot = __ldg(p.slots + i);
+    v.at = p.rotation ? __ldg(p.position + i) : 0;
+    v.a = __ldg(reinterpret_cast<const uint4*>(row) + lane);
+    v.b = __ldg(reinterpret_cast<const uint4*>(row + 256) + lane);
+    if (kPairs)
+      v.rope = __ldg(reinterpret_cast<const uint32_t*>(row + kDv) + lane);
+    else
+      v.rope = __ldg(row + kDv + lane) | (static_cast<uint32_t>(__ldg(row + kDv + kRopePairs + lane)) << 16);
+    return v;
+  };
+  uint32_t w[8];  // the norm's weights of the lane's values, two by two
+  if (kNorm) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.norm_weight) + lane), y = __ldg(reinterpret_cast<const uint4*>(p.norm_weight + 256) + lane);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
   }
-  const bool bad_slot = slot != -1 && (slot < 0 || slot >= p.pool_slots);
-  const bool bad_position = p.rotation && (at < 0 || at >= p.positions);
-  if (slot == -1 || bad_slot || bad_position) {
-    const int32_t bits = slot == -1 ? 0 : (bad_slot ? kStatusBadSlot : 0) | (bad_position ? kStatusBadPosition : 0);
-    if (bits && lane == 0) atomicOr(p.status, bits);
-    return;
-  }
-  float x[16];  // latent values 8 lane + {0..7} and 256 + 8 lane + {0..7}
-  unpack8(a, x);
-  unpack8(b, x + 8);
-  if (p.norm_weight) {
-    float w[16];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(p.norm_weight) + lane), w);
-    unpack8(__ldg(reinterpret_cast<const uint4*>(p.norm_weight + 256) + lane), w + 8);
-    // (rows whose squares would leave fp32 are first made smaller, by a power of two)
-    float top = 0.f;
+  // the angles a row's position has, read when the position has come
+  auto turn_of = [&](int at, float& c, float& s) {
+    if (p.rotation && at >= 0 && at < p.positions) {
+      const float* turn = p.rotation + static_cast<int64_t>(at) * (2 * kRopePairs) + lane;
+      c = __ldg(turn);
+      s = __ldg(turn + kRopePairs);
+    }
+  };
+  RowLane next = load(i);
+  float c = 1.f, s = 0.f;
+  turn_of(next.at, c, s);
+#pragma unroll 1
+  for (; i < p.n; i += step) {
+    const RowLane v = next;
+    if (i + step < p.n) next = load(i + step);
+    float rx = bf16_lo(v.rope), ry = bf16_hi(v.rope);
+    if (p.rotation) {
+      // (each rounded once but for the last sum)
+      const float ys = ry * s, xs = rx * s;
+      const float tx = fmaf(rx, c, -ys) + fmaf(-ry, s, ys);
+      ry = fmaf(ry, c, xs) + fmaf(rx, s, -xs);
+      rx = tx;
+    }
+    const uint32_t in[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+    uint64_t x[8];  // two by two
 #pragma unroll
-    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[k]));
-    const float fit = warp_max(top) > pow2(50) ? pow2(-80) : 1.f;
-    // Sum and root carry what their roundings leave, so that c' is rounded once: a value next to a border between two
-    // 8-bit values goes where the formula puts it. (Squares and products of two bf16 values are exact in fp32.)
-    uint64_t hi = f32x2(0.f, 0.f), lo = hi;
+    for (int k = 0; k < 8; ++k) x[k] = f32x2(bf16_lo(in[k]), bf16_hi(in[k]));
+    if (kNorm) {
+      // The root of the mean square, to its last bits, so that c' is rounded once and a value next to a border between
+      // two 8-bit values goes where the formula puts it: the row is first divided by a power of two, to values below 2
+      // (at least 2^-40: eps is all that counts in smaller rows). Their squares, exact in fp32, are added onto 2^12,
+      // where every sum is a multiple of 2^-11 and so exact over the whole row; what each leaves is added apart.
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = __vmaxu2(m, in[k] & 0x7fff7fffu);
+      m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+      const int e = min(max(static_cast<int>(m >> 7) - 127, -40), 126);  // (a row that is not finite: anything)
+      const float fit = pow2(-e);
+      const uint64_t fit2 = f32x2(fit, fit), origin = f32x2(4096.f, 4096.f);
+      uint64_t hi = origin, lo = f32x2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[k] = mul_x2(x[k], fit2);
+        const uint64_t sq = mul_x2(x[k], x[k]), sum = add_x2(hi, sq);
+        lo = add_x2(lo, sub_x2(sq, sub_x2(sum, hi)));
+        hi = sum;
+      }
+      float h, l, h2, l2;
+      f32x2_split(sub_x2(hi, origin), h, h2);
+      f32x2_split(lo, l, l2);
+      h += h2, l += l2;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        h += __shfl_xor_sync(0xffffffffu, h, o);
+        l += __shfl_xor_sync(0xffffffffu, l, o);
+      }
+      h *= 1.f / kDv, l *= 1.f / kDv;
+      l += add_exact(h, p.eps * fit * fit);
+      l = add_exact(h, l);
+      const float y = rsqrtf(h), t = h * y;
+      // one step towards the root's last bits: y (1 + r / 2), r = 1 - (h + l) y^2
+      const float r = fmaf(-l * y, y, fmaf(-fmaf(h, y, -t), y, fmaf(-t, y, 1.f))), more = 0.5f * y * r;
+      const uint64_t y2 = f32x2(y, y), more2 = f32x2(more, more);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {  // (the product of two bf16 values is exact)
+        const uint64_t c = mul_x2(x[k], f32x2(bf16_lo(w[k]), bf16_hi(w[k])));
+        x[k] = fma_x2(c, y2, mul_x2(c, more2));
+      }
+    }
+    if (i + step < p.n) turn_of(next.at, c, s);
+    float top = 0.f, none = fmaf(rx, 0.f, ry * 0.f);  // none: NaN if a value is not finite
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      x[2 * k] *= fit, x[2 * k + 1] *= fit;
-      const uint64_t v = f32x2(x[2 * k], x[2 * k + 1]), sq = mul_x2(v, v), sum = add_x2(hi, sq), part = sub_x2(sum, hi);
-      lo = add_x2(lo, add_x2(sub_x2(hi, sub_x2(sum, part)), sub_x2(sq, part)));
-      hi = sum;
+      float a, b;
+      f32x2_split(x[k], a, b);
+      top = fmax3(top, fabsf(a), fabsf(b));
+      none = fmaf(a, 0.f, fmaf(b, 0.f, none));
     }
-    float h, l, h2, l2;
-    f32x2_split(hi, h, h2);
-    f32x2_split(lo, l, l2);
-    l += l2 + add_exact(h, h2);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      h2 = __shfl_xor_sync(0xffffffffu, h, o);
-      l += __shfl_xor_sync(0xffffffffu, l, o);
-      l += add_exact(h, h2);
+    const bool fine = __all_sync(0xffffffffu, none == 0.f);
+    const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(top)),
+                   r = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(rx), fabsf(ry))));
+    // 448 = 1.75 * 2^8; rope quotients stay below 2^121
+    int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = max(e, max(static_cast<int>(r >> 23) - 127 - 120, kKv8MinExp));
+    const float inv = fine ? pow2(-e) : 0.f;
+    const uint64_t inv2 = f32x2(inv, inv);
+    const bool bad_slot = v.slot != -1 && (v.slot < 0 || v.slot >= p.pool_slots);
+    const bool bad_position = p.rotation && (v.at < 0 || v.at >= p.positions);
+    if (v.slot == -1 || bad_slot || bad_position) {
+      const int32_t bits = v.slot == -1 ? 0 : (bad_slot ? kStatusBadSlot : 0) | (bad_position ? kStatusBadPosition : 0);
+      if (bits && lane == 0) atomicOr(p.status, bits);
+      continue;
     }
-    h *= 1.f / kDv, l *= 1.f / kDv;
-    l += add_exact(h, p.eps * fit * fit);
-    const float y = rsqrtf(h), t = h * y;
-    // one step towards the root's last bits: y (1 + r / 2), r = 1 - (h + l) y^2
-    const float r = fmaf(-l * y, y, fmaf(-fmaf(h, y, -t), y, fmaf(-t, y, 1.f))), more = 0.5f * y * r;
+    uint8_t* dst = p.pool + static_cast<int64_t>(v.slot) * kKv8Row;
+    // a row that is not finite: a scale of NaN, and zeros (which do not spread to others through a product with 0)
+    uint32_t out[4];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float c = x[k] * w[k];
-      x[k] = fmaf(c, y, c * more);
+    for (int k = 0; k < 4; ++k) {
+      float a, b, c, d;
+      f32x2_split(mul_x2(x[2 * k], inv2), a, b);
+      f32x2_split(mul_x2(x[2 * k + 1], inv2), c, d);
+      out[k] = fine ? pack_e4m3x2(a, b) | (static_cast<uint32_t>(pack_e4m3x2(c, d)) << 16) : 0u;
     }
-  }
-  if (p.rotation) {
-    const float* turn = p.rotation + static_cast<int64_t>(at) * (2 * kRopePairs) + lane;
-    const float c = __ldg(turn), s = __ldg(turn + kRopePairs);
-    // (each rounded once but for the last sum)
-    const float ys = ry * s, xs = rx * s;
-    const float tx = fmaf(rx, c, -ys) + fmaf(-ry, s, ys);
-    ry = fmaf(ry, c, xs) + fmaf(rx, s, -xs);
-    rx = tx;
-  }
-  float top = 0.f, rope = fmaxf(fabsf(rx), fabsf(ry));
-  bool fine = fabsf(rx) <= 3.4028235e38f && fabsf(ry) <= 3.4028235e38f;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    top = fmaxf(top, fabsf(x[k]));
-    fine = fine && fabsf(x[k]) <= 3.4028235e38f;
-  }
-  fine = __all_sync(0xffffffffu, fine);
-  const uint32_t u = __float_as_uint(warp_max(top)), r = __float_as_uint(warp_max(rope));
-  // 448 = 1.75 * 2^8; rope quotients stay below 2^121
-  int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  e = max(e, max(static_cast<int>(r >> 23) - 127 - 120, kKv8MinExp));
-  const float inv = pow2(-e);
-  uint8_t* dst = p.pool + static_cast<int64_t>(slot) * kKv8Row;
-  // a row that is not finite: a scale of NaN, and zeros (which do not spread to others through a product with 0)
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t v[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float* y = x + 8 * h + 4 * k;
-      v[k] = fine ? pack_e4m3x2(y[0] * inv, y[1] * inv) | (static_cast<uint32_t>(pack_e4m3x2(y[2] * inv, y[3] * inv)) << 16) : 0u;
+    *reinterpret_cast<uint2*>(dst + 8 * lane) = make_uint2(out[0], out[1]);
+    *reinterpret_cast<uint2*>(dst + 256 + 8 * lane) = make_uint2(out[2], out[3]);
+    const uint32_t rope2 = fine ? pack_bf16x2(rx * inv, ry * inv) : 0u;
+    uint16_t* rdst = reinterpret_cast<uint16_t*>(dst + kDv);
+    if (kPairs) {
+      reinterpret_cast<uint32_t*>(rdst)[lane] = rope2;
+    } else {
+      rdst[lane] = static_cast<uint16_t>(rope2);
+      rdst[kRopePairs + lane] = static_cast<uint16_t>(rope2 >> 16);
     }
-    *reinterpret_cast<uint2*>(dst + 256 * h + 8 * lane) = make_uint2(v[0], v[1]);
+    if (lane == 0) p.scale[v.slot] = fine ? pow2(e) : CUDART_NAN_F;
   }
-  const uint32_t rope2 = fine ? pack_bf16x2(rx * inv, ry * inv) : 0u;
-  uint16_t* rdst = reinterpret_cast<uint16_t*>(dst + kDv);
-  if (kPairs) {
-    reinterpret_cast<uint32_t*>(rdst)[lane] = rope2;
-  } else {
-    rdst[lane] = static_cast<uint16_t>(rope2);
-    rdst[kRopePairs + lane] = static_cast<uint16_t>(rope2 >> 16);
-  }
-  if (lane == 0) p.scale[slot] = fine ? pow2(e) : CUDART_NAN_F;
 }
 
 __global__ void __launch_bounds__(kRowWarps * 32) kv8_read_kernel(const __grid_constant__ Kv8ReadParams p) {
@@ -190,11 +219,19 @@ unsigned row_blocks(int64_t n) { return static_cast<unsigned>((n + kRowWarps - 1
 
 }  // namespace
 
-cudaError_t launch_kv8_write(const Kv8WriteParams& p, bool interleaved, cudaStream_t stream) {
-  if (interleaved)
-    kv8_write_kernel<true><<<row_blocks(p.n), kRowWarps * 32, 0, stream>>>(p);
-  else
-    kv8_write_kernel<false><<<row_blocks(p.n), kRowWarps * 32, 0, stream>>>(p);
+cudaError_t launch_kv8_write(const Kv8WriteParams& p, bool interleaved, int sm_count, cudaStream_t stream) {
+  // as many blocks as run at once: a warp has its next row on the way while it works at one
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(row_blocks(p.n), int64_t(sm_count) * kWriteBlocks));
+  if (p.norm_weight) {
+    if (interleaved)
+      kv8_write_kernel<true, true><<<blocks, kRowWarps * 32, 0, stream>>>(p);
+    else
+      kv8_write_kernel<false, true><<<blocks, kRowWarps * 32, 0, stream>>>(p);
+  } else if (interleaved) {
+    kv8_write_kernel<true, false><<<blocks, kRowWarps * 32, 0, stream>>>(p);
+  } else {
+    kv8_write_kernel<false, false><<<blocks, kRowWarps * 32, 0, stream>>>(p);
+  }
   return cudaGetLastError();
 }
 

@@ -155,7 +155,7 @@ extern "C" int ddtree_kv8_write(const void* rows, int64_t row_stride, const int3
   p.n = n;
   p.pool_slots = pool_slots;
   p.status = static_cast<int32_t*>(workspace);
-  return launch_kv8_write(p, interleaved != 0, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
+  return launch_kv8_write(p, interleaved != 0, sms, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
 }
 
 extern "C" int ddtree_kv8_read(const void* kv8_pool, const float* kv8_scale, const int32_t* slots, int64_t n, void* rows,
