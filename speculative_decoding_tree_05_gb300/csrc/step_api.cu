@@ -26,7 +26,7 @@ struct Kv8Layout {
 
 // Costs in tiles of 64 keys: of a unit (its prologue, the pipeline's fill, its output),
 // of a merge, and of the partials, this many (unit, group)s a tile.
-constexpr int kUnitTiles = 5, kMergeTiles = 2, kPartialsPerTile = 48;
+constexpr int kUnitTiles = 9, kMergeTiles = 3, kPartialsPerTile = 32;
 
 // Groups of up to 64 (node, head) rows, and the shares of the batch's tiles: as many as
 // minimise waves * (tiles of a share + kUnitTiles) and the merge. Only numbers of shares
@@ -77,11 +77,12 @@ int kv8_layout(const ddt_dims* d, int sm_count, Kv8Layout* w) {
   return DDT_OK;
 }
 
-// The least power of two of warps, up to 16, with which a row's units are read in one go.
-int merge_warps(const Kv8Layout& w, int batch) {
+// Warps that share a row of the merge: the least power of two, up to 16, with which a row's units are read in one go,
+// while there are SMs for so many (64 requests of 144 rows, few units each: 16 warps a row 244 us in all, one BBBB).
+int merge_warps(const Kv8Layout& w, const ddt_dims* d, int sm_count) {
+  const int64_t rows = int64_t(d->batch) * d->num_nodes * d->num_heads, units = w.units - d->batch + 1;  // of one request, at most
   int n = 1;
-  const int units = w.units - batch + 1;  // of one request, at most
-  while (n < 16 && n * 4 < units) n *= 2;
+  while (n < 16 && n * 4 < units && rows * n * 2 <= int64_t(sm_count) * 64) n *= 2;
   return n;
 }
 
@@ -271,7 +272,7 @@ extern "C" int ddtree_verify_attn_kv8(const void* q, const void* kv8_pool, const
   m.batch = p.batch;
   m.nodes = p.nodes;
   m.heads = p.heads;
-  m.warps = merge_warps(w, dims->batch);
+  m.warps = merge_warps(w, dims, sms);
   return launch_kv8_merge(m, s) == cudaSuccess ? DDT_OK : DDT_ERR_LAUNCH;
 }
 
