@@ -461,14 +461,15 @@ DDT_API int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, const 
  *   position    int32 [n] device (with rotation), each in [0, positions); a row with
  *               another one is not written and sets DDT_STATUS_BAD_POSITION
  * Slots that are not listed keep what they hold.  The pool and the scales must not
- * overlap the rows, the slots or each other (DDT_ERR_ALIAS).  workspace >= 256 bytes.
+ * overlap the rows, the slots or each other (DDT_ERR_ALIAS).  workspace: 256 bytes for
+ * the status word, or NULL: then nothing is reported, and the call is one kernel.
  *
  * ddtree_kv8_read writes the rows that listed slots stand for, rounded to bf16 (exact
  * for the scales that ddtree_kv8_write makes, above bf16's subnormals), in the order
  * of the list; any slot may be listed, any number of times:
  *   rows        bf16, row i at rows + i * row_stride (as above); -1 gives a row of
  *               zeros, another value outside [0, N) too, and sets DDT_STATUS_BAD_SLOT
- * n <= 2^31.  A slot that was not finite reads as NaN.
+ * n <= 2^31.  A slot that was not finite reads as NaN.  workspace as above.
  */
 DDT_API int ddtree_kv8_write(const void* rows, int64_t row_stride, const int32_t* slots, int64_t n,
                              const void* norm_weight, float eps, const float* rotation, const int32_t* position,

@@ -33,7 +33,7 @@ struct Kv8WriteParams {
   uint8_t* pool;               // [N, 640]
   float* scale;                // [N]
   int64_t n, pool_slots;
-  int32_t* status;
+  int32_t* status;             // or null
 };
 cudaError_t launch_kv8_write(const Kv8WriteParams& p, bool interleaved, int sm_count, cudaStream_t stream);
 
@@ -44,7 +44,7 @@ struct Kv8ReadParams {
   uint16_t* rows;              // bf16, row i at rows + i * row_stride
   int64_t row_stride;
   int64_t n, pool_slots;
-  int32_t* status;
+  int32_t* status;             // or null
 };
 cudaError_t launch_kv8_read(const Kv8ReadParams& p, cudaStream_t stream);
 

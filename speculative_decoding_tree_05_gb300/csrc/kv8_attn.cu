@@ -625,8 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
             const int cc = 32 * half + (k0 & 3) * 8;
             uint32_t o[8];
             tmem_ld8(tmem + lane_off + (k0 >> 2) * kRows + cc, o);
+            const uint64_t* f = reinterpret_cast<const uint64_t*>(alpha_sh + cc);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha_sh[cc + k]);
+            for (int k = 0; k < 4; ++k) {
+              float x, y;
+              f32x2_split(mul_x2(f32x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), f[k]), x, y);
+              o[2 * k] = __float_as_uint(x), o[2 * k + 1] = __float_as_uint(y);
+            }
             tmem_st8(tmem + lane_off + (k0 >> 2) * kRows + cc, o);
           }
           tc_fence_before();

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kWriteBlocks) kv8_write_kernel
     const bool bad_position = p.rotation && (v.at < 0 || v.at >= p.positions);
     if (v.slot == -1 || bad_slot || bad_position) {
       const int32_t bits = v.slot == -1 ? 0 : (bad_slot ? kStatusBadSlot : 0) | (bad_position ? kStatusBadPosition : 0);
-      if (bits && lane == 0) atomicOr(p.status, bits);
+      if (bits && p.status && lane == 0) atomicOr(p.status, bits);
       continue;
     }
     uint8_t* dst = p.pool + static_cast<int64_t>(v.slot) * kKv8Row;
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv8_read_kernel(const __grid_c
   if (i >= p.n) return;
   const int slot = __ldg(p.slots + i);
   const bool in = slot >= 0 && slot < p.pool_slots;
-  if (!in && slot != -1 && lane == 0) atomicOr(p.status, kStatusBadSlot);
+  if (!in && slot != -1 && p.status && lane == 0) atomicOr(p.status, kStatusBadSlot);
   uint4 a = make_uint4(0, 0, 0, 0);
   uint32_t r = 0;
   float s = 0.f;

@@ -128,7 +128,7 @@ extern "C" int ddtree_kv8_write(const void* rows, int64_t row_stride, const int3
       (norm_weight && !(eps >= 1e-12f && eps <= 1.f)) || (rotation && positions < 1))
     return DDT_ERR_DIMS;
   if (n == 0) return DDT_OK;
-  if (!rows || !slots || !kv8_pool || !kv8_scale || !workspace || (rotation && !position)) return DDT_ERR_NULL;
+  if (!rows || !slots || !kv8_pool || !kv8_scale || (rotation && !position)) return DDT_ERR_NULL;
   if (!aligned(rows, 16) || !aligned(norm_weight, 16) || !aligned(kv8_pool, 16) || !aligned(workspace, 256) ||
       !aligned(slots, 4) || !aligned(rotation, 4) || !aligned(position, 4) || !aligned(kv8_scale, 4))
     return DDT_ERR_ALIGN;
@@ -141,7 +141,7 @@ extern "C" int ddtree_kv8_write(const void* rows, int64_t row_stride, const int3
   const int rc = current_device(&sms);
   if (rc != DDT_OK) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!clear_status(workspace, s)) return DDT_ERR_LAUNCH;
+  if (workspace && !clear_status(workspace, s)) return DDT_ERR_LAUNCH;
   Kv8WriteParams p = {};
   p.rows = static_cast<const uint16_t*>(rows);
   p.row_stride = row_stride;
@@ -164,7 +164,7 @@ extern "C" int ddtree_kv8_read(const void* kv8_pool, const float* kv8_scale, con
   if (n < 0 || n > kMaxRows || row_stride < kDqk || row_stride % 8 != 0 || pool_slots < 1 || pool_slots > kMaxRows)
     return DDT_ERR_DIMS;
   if (n == 0) return DDT_OK;
-  if (!rows || !slots || !kv8_pool || !kv8_scale || !workspace) return DDT_ERR_NULL;
+  if (!rows || !slots || !kv8_pool || !kv8_scale) return DDT_ERR_NULL;
   if (!aligned(rows, 16) || !aligned(kv8_pool, 16) || !aligned(workspace, 256) || !aligned(slots, 4) || !aligned(kv8_scale, 4))
     return DDT_ERR_ALIGN;
   const size_t out = (size_t(n - 1) * row_stride + kDqk) * 2;
@@ -175,7 +175,7 @@ extern "C" int ddtree_kv8_read(const void* kv8_pool, const float* kv8_scale, con
   const int rc = current_device(&sms);
   if (rc != DDT_OK) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!clear_status(workspace, s)) return DDT_ERR_LAUNCH;
+  if (workspace && !clear_status(workspace, s)) return DDT_ERR_LAUNCH;
   Kv8ReadParams p = {};
   p.pool = static_cast<const uint8_t*>(kv8_pool);
   p.scale = kv8_scale;

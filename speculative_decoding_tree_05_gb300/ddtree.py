@@ -590,14 +590,16 @@ def kv8_pool(slots, device=None):
 def _rows_of(rows, name, device, n):
     """A row stride, in elements, of bf16 rows that may lie in a wider tensor."""
     import torch
-    if (rows.dtype is not torch.bfloat16 or rows.dim() != 2 or rows.shape[0] != n or rows.shape[1] != D_QK
-            or rows.device != device or rows.stride(1) != 1 or (n > 1 and rows.stride(0) < D_QK)):
+    stride = rows.stride()
+    if (rows.dtype is not torch.bfloat16 or rows.shape != (n, D_QK) or rows.get_device() != device.index
+            or stride[1] != 1 or (n > 1 and stride[0] < D_QK)):
         raise ValueError(f"{name} must be bfloat16 [{n}, {D_QK}] on {device} with consecutive values in a row, got "
-                         f"{rows.dtype} {tuple(rows.shape)} on {rows.device}, strides {tuple(rows.stride())}")
-    return rows.stride(0) if n > 1 else D_QK
+                         f"{rows.dtype} {tuple(rows.shape)} on {rows.device}, strides {tuple(stride)}")
+    return stride[0] if n > 1 else D_QK
 
 
-def _kv8_checks(pool, scale, slots):
+def _kv8_checks(pool, scale, slots, workspace):
+    """The device, the cache's slots and the listed ones."""
     import torch
     device = _on_cuda(pool, "pool")
     if pool.dim() != 2 or slots.dim() != 1:
@@ -605,17 +607,11 @@ def _kv8_checks(pool, scale, slots):
     N, n = pool.shape[0], slots.shape[0]
     _need(device, ("pool", pool, torch.uint8, (N, KV8_ROW)), ("scale", scale, torch.float32, (N,)),
           ("slots", slots, torch.int32, (n,)))
+    if workspace is not None:
+        _need(device, ("workspace", workspace, torch.uint8, workspace.shape))
+        if workspace.numel() < 256:
+            raise ValueError("workspace must hold 256 bytes")
     return device, N, n
-
-
-def _status_words(workspace, device, stream):
-    import torch
-    if workspace is None:
-        return _make(stream, torch.empty, 256, dtype=torch.uint8, device=device)
-    _need(device, ("workspace", workspace, torch.uint8, workspace.shape))
-    if workspace.numel() < 256:
-        raise ValueError("workspace must hold 256 bytes")
-    return workspace
 
 
 def kv8_write(rows, slots, pool, scale, norm_weight=None, eps=1e-6, rotation=None, position=None, interleaved=False,
@@ -625,9 +621,10 @@ def kv8_write(rows, slots, pool, scale, norm_weight=None, eps=1e-6, rotation=Non
     slots int32 [n], each slot at most once, -1 = skip the row.  With norm_weight (bf16 [512]) the latent values are
     normalised first, with rotation (fp32 [positions, 64]: cosines, sines) and position (int32 [n]) the rope values
     are rotated: pairs (2 i, 2 i + 1) if interleaved, else (i, i + 32).  rows may be a slice of a wider tensor.
+    workspace: 256 bytes for read_device_status; without it bad slots and positions are left out unreported.
     """
     import torch
-    device, N, n = _kv8_checks(pool, scale, slots)
+    device, N, n = _kv8_checks(pool, scale, slots, workspace)
     stride = _rows_of(rows, "rows", device, n)
     if norm_weight is not None:
         _need(device, ("norm_weight", norm_weight, torch.bfloat16, (D_V,)))
@@ -639,25 +636,27 @@ def kv8_write(rows, slots, pool, scale, norm_weight=None, eps=1e-6, rotation=Non
             raise ValueError("rotation must be [positions, 64]")
         positions = rotation.shape[0]
         _need(device, ("rotation", rotation, torch.float32, (positions, 64)), ("position", position, torch.int32, (n,)))
-    workspace = _status_words(workspace, device, stream)
     _run_on(device, lib().ddtree_kv8_write, "ddtree_kv8_write", rows.data_ptr(), stride, slots.data_ptr(), n,
-            _addr(norm_weight), eps, _addr(rotation), _addr(position), positions, int(bool(interleaved)), pool.data_ptr(),
-            scale.data_ptr(), N, workspace.data_ptr(), _stream_of(device, stream))
-    _keep(stream, workspace, pool, scale)
+            _addr(norm_weight), eps, _addr(rotation), _addr(position), positions, interleaved, pool.data_ptr(),
+            scale.data_ptr(), N, _addr(workspace), _stream_of(device, stream))
+    if stream is not None:
+        _keep(stream, pool, scale)
     return pool, scale
 
 
 def kv8_read(pool, scale, slots, out=None, workspace=None, stream=None):
-    """The bf16 rows [n, 576] that listed slots of an 8-bit cache stand for (ddtree_kv8_read); -1 gives zeros."""
+    """The bf16 rows [n, 576] that listed slots of an 8-bit cache stand for (ddtree_kv8_read); -1 gives zeros.
+
+    out may be a slice of a wider tensor; workspace as in kv8_write.
+    """
     import torch
-    device, N, n = _kv8_checks(pool, scale, slots)
+    device, N, n = _kv8_checks(pool, scale, slots, workspace)
     if out is None:
         out = _make(stream, torch.empty, (n, D_QK), dtype=torch.bfloat16, device=device)
     stride = _rows_of(out, "out", device, n)
-    workspace = _status_words(workspace, device, stream)
     _run_on(device, lib().ddtree_kv8_read, "ddtree_kv8_read", pool.data_ptr(), scale.data_ptr(), slots.data_ptr(), n,
-            out.data_ptr(), stride, N, workspace.data_ptr(), _stream_of(device, stream))
-    _keep(stream, workspace, out)
+            out.data_ptr(), stride, N, _addr(workspace), _stream_of(device, stream))
+    _keep(stream, out)
     return out
 
 

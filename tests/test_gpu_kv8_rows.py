@@ -146,6 +146,9 @@ def test_skipped_and_bad_rows_leave_the_cache():
     got = ddtree.kv8_read(pool, scale, bad, workspace=ws)
     assert ddtree.read_device_status(ws) == ddtree.STATUS_BAD_SLOT
     assert not bool(got[[0, 5, 6, 7, 8]].any()) and torch.equal(got[9:], ddtree.kv8_read(pool, scale, where[9:]))
+    quiet_pool, quiet_scale = pool.clone(), scale.clone()      # without a workspace nothing is reported
+    ddtree.kv8_write(rows, bad, quiet_pool, quiet_scale, rotation=table, position=position)
+    assert torch.equal(quiet_pool, pool) and torch.equal(ddtree.kv8_read(quiet_pool, quiet_scale, bad), got)
     none = torch.full((3,), -1, dtype=torch.int32, device="cuda")
     got = ddtree.kv8_read(pool, scale, none, workspace=ws)
     assert ddtree.read_device_status(ws) == 0 and not bool(got.any())

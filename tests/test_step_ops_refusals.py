@@ -56,13 +56,15 @@ def test_no_rows_is_ok(lib):
 
 @pytest.mark.parametrize("name", ["rows", "slots", "position", "pool", "scale", "workspace"])
 def test_write_null_and_misaligned(lib, name):
-    assert call(lib, "ddtree_kv8_write", WRITE, **{name: None}) == -1
+    if name != "workspace":
+        assert call(lib, "ddtree_kv8_write", WRITE, **{name: None}) == -1
     assert call(lib, "ddtree_kv8_write", WRITE, **{name: WRITE[name] + 2}) == -4
 
 
 @pytest.mark.parametrize("name", ["rows", "slots", "pool", "scale", "workspace"])
 def test_read_null_and_misaligned(lib, name):
-    assert call(lib, "ddtree_kv8_read", READ, **{name: None}) == -1
+    if name != "workspace":
+        assert call(lib, "ddtree_kv8_read", READ, **{name: None}) == -1
     assert call(lib, "ddtree_kv8_read", READ, **{name: READ[name] + 2}) == -4
 
 
