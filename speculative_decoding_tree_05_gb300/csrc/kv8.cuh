@@ -57,9 +57,9 @@ constexpr int kKv8Chunk = kKv8Keys * 128;         // 128 bytes of 64 keys
 // A group's query rows as its units take them. Row r has two lanes of the tensor memory, for its two parts:
 // lane 32 (r / 16) + r % 16 and 16 lanes on.
 //   512 bytes of each of the 128 lanes: 16-byte piece u of lane l at (128 u + l) 16
-//   rope values, a 128-byte row a lane (zeros in the second parts' lanes), 128-byte swizzle
+//   rope values, a 128-byte row for each of the 64, 128-byte swizzle
 //   the rows' factors of a score, fp32
-constexpr int kKv8ImageRope = 128 * 512, kKv8ImageFactor = kKv8ImageRope + 128 * 128, kKv8Image = kKv8ImageFactor + 256;
+constexpr int kKv8ImageRope = 128 * 512, kKv8ImageFactor = kKv8ImageRope + kKv8Rows * 128, kKv8Image = kKv8ImageFactor + 256;
 
 // Rows of a group, within its request, if `nodes` nodes are active (rows <= 0: none).
 struct Kv8Group {

@@ -19,9 +19,10 @@
 // there. So the queries are the one operand that stays in tensor memory, both parts of up to 64
 // rows as the 128 lanes of one MMA, which sums them apart; and value dims are the M side
 // of the second product, so that each 8-bit value is read once for 64 rows and part:
-//   S[hi, lo rows][64 keys]      = Q . K^T    16 MMAs M128 x N64 x K32 (8 bit, Q in tensor memory), 4 of K16 (rope)
+//   S[hi, lo rows][64 keys]      = Q . K^T    16 MMAs M128 x N64 x K32 (8 bit, Q in tensor memory)
+//                                             and 4 M64 x N64 x K16 (rope, added to the first parts')
 //   O^T[512 dims][rows] += V^T . P^T          2 x 4 x 2 MMAs M128 x N x K32 (V^T: the same bytes read MN-major)
-// 56 + 96 KB of operands a tile, and 48 KB written (with both operands of the scores in
+// 48 + 96 KB of operands a tile, and 48 KB written (with both operands of the scores in
 // shared memory it was 144 + 96 KB, and a tile took 2330 cycles). O^T takes 256 TMEM columns,
 // the scores twice 64, the queries 128; one CTA holds the whole output.
 //
@@ -57,8 +58,8 @@ constexpr int kRows = kKv8Rows;
 constexpr int kStages = 4;
 constexpr int kChunk = kKv8Chunk;                   // 128 bytes of 64 keys: 8 KB
 constexpr int kStageBytes = 5 * kChunk;             // 40960
-constexpr int kOffRope = kStages * kStageBytes;     // the queries' rope values, [128 lanes][128 bytes]
-constexpr int kOffQs = kOffRope + 128 * 128;        // [64] the rows' factors of a score
+constexpr int kOffRope = kStages * kStageBytes;     // the queries' rope values, [64 rows][128 bytes]
+constexpr int kOffQs = kOffRope + kRows * 128;      // [64] the rows' factors of a score
 constexpr int kOffP = kOffQs + 1024;                // [2 buffers][2 parts][64 rows][64 keys]
 constexpr int kPart = kKeys * kRows;                // 4096
 constexpr int kOffMask = kOffP + 4 * kPart;         // [stages][64] row masks of the stage's keys
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       ok = mbar_wait_abortable(&sh.q_full, 0, abort, false, __LINE__) &&
            mbar_wait_abortable(&sh.q_ready, 0, abort, false, __LINE__);
       tc_fence_after();
-      const uint32_t idesc8 = idesc_f8_f32(128, kKeys, kE4m3, kE4m3, false, false), idesc = idesc_bf16_f32(128, kKeys, false, false);
+      const uint32_t idesc8 = idesc_f8_f32(128, kKeys, kE4m3, kE4m3, false, false), idesc = idesc_bf16_f32(64, kKeys, false, false);  // (M64: the first parts' lanes)
       const uint64_t d_k = smem_desc(base, 16, 1024, kSwizzle128B);
       const uint64_t d_rope = smem_desc(base + kOffRope, 16, 1024, kSwizzle128B);
       int st = 0, ph = 0;
@@ -625,13 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
             const int cc = 32 * half + (k0 & 3) * 8;
             uint32_t o[8];
             tmem_ld8(tmem + lane_off + (k0 >> 2) * kRows + cc, o);
-            const uint64_t* f = reinterpret_cast<const uint64_t*>(alpha_sh + cc);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float x, y;
-              f32x2_split(mul_x2(f32x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), f[k]), x, y);
-              o[2 * k] = __float_as_uint(x), o[2 * k + 1] = __float_as_uint(y);
-            }
+            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha_sh[cc + k]);
             tmem_st8(tmem + lane_off + (k0 >> 2) * kRows + cc, o);
           }
           tc_fence_before();

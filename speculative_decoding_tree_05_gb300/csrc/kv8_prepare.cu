@@ -2,7 +2,7 @@
 // query rows as the tensor core reads them, cut into two 8-bit parts once instead of once
 // a unit, and the call's first status word.
 //
-// One CTA per (request, group of up to 64 rows) writes the 80 KB that its units put into
+// One CTA per (request, group of up to 64 rows) writes the 72 KB that its units put into
 // tensor and shared memory as they are, and a factor per row:
 //   q = (hi + lo) 2^e in e4m3, 2^e the least power of two with |latent values| <= 448 2^e;
 //   rope values q 2^-e in bf16.
@@ -84,9 +84,8 @@ __global__ void __launch_bounds__(kThreads) kv8_prepare_kernel(const __grid_cons
         const uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? cut[part][1] : cut[part][3], 1);
         *reinterpret_cast<uint4*>(image + (128 * piece + l) * 16) =
             odd ? make_uint4(x, y, cut[part][2], cut[part][3]) : make_uint4(cut[part][0], cut[part][1], x, y);
-        *reinterpret_cast<uint32_t*>(image + kKv8ImageRope + l * 128 + ((((lane >> 2) ^ (l & 7)) << 4) | ((lane & 3) << 2))) =
-            part == 0 ? rope : 0u;
       }
+      *reinterpret_cast<uint32_t*>(image + kKv8ImageRope + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2))) = rope;
       if (lane == 0)
         reinterpret_cast<float*>(image + kKv8ImageFactor)[r] =
             r >= u.rows ? 0.f : fine ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * p.scale_log2 : CUDART_NAN_F;
