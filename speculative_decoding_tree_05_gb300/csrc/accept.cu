@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kAccThreads, 2) accept_kernel(const __grid_con
 #ifdef DDT_TEST_HOOKS
       if (rank == 0 && warp == 1 && step == p.test_keep_back) return;
 #endif
-      // (a plain remote store and a barrier of the cluster: 2500 cycles a reduction in place of NNNN)
+      // (a plain remote store and a barrier of the cluster: 2500 cycles a reduction in place of 1700)
       if (lane < size) st_async_b64(mapa_shared(smem_u32(part), lane), v, mapa_shared(smem_u32(bar), lane));
     }
   };

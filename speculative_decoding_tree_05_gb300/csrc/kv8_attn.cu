@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     }
   }
   // The softmax and gather warps write O: quarter of the lanes by warp, six warps a quarter, 8 rows of 32 dims at a
-  // time; lane = value dim. (Through shared memory and a bulk copy it took 8500 cycles in place of NNNN.)
+  // time; lane = value dim. (Through shared memory and a bulk copy it took 8500 cycles in place of 4400.)
   if (warp > 0) {
     if (!bar_red_or(2, kThreads - 32, !ok) && warp != kIssuePv && warp < kFirstKey) {
       tc_fence_after();

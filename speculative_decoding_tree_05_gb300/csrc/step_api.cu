@@ -78,7 +78,7 @@ int kv8_layout(const ddt_dims* d, int sm_count, Kv8Layout* w) {
 }
 
 // Warps that share a row of the merge: the least power of two, up to 16, with which a row's units are read in one go,
-// while there are SMs for so many (64 requests of 144 rows, few units each: 16 warps a row 244 us in all, one BBBB).
+// while there are SMs for so many (64 requests of 144 rows, few units each: 16 warps a row 243 us in all, one 117).
 int merge_warps(const Kv8Layout& w, const ddt_dims* d, int sm_count) {
   const int64_t rows = int64_t(d->batch) * d->num_nodes * d->num_heads, units = w.units - d->batch + 1;  // of one request, at most
   int n = 1;
@@ -94,9 +94,13 @@ int check_accept(const ddt_dims* d, int32_t vocab) {
 }
 // CTAs of a request: enough to hold a row in shared memory, and as many as cost least. A
 // visit of a row takes about kVisit cycles and, with draft probabilities, 1.5 for each of a
-// CTA's tokens (else one), twice that where two CTAs meet on an SM; requests in several
-// rounds take as many times as long. (16 requests of 128001 tokens drawn: 8 CTAs each, of
-// which 15 clusters run at once, MMMM us, 16 of half the shared memory NNNN.)
+// CTA's tokens (else one), half as much again where two CTAs meet on an SM. Requests that
+// find no room wait for others' ends, and as paths differ in length that comes to 0.7 of
+// the whole rounds. Graphs, 9 nodes, CTAs a request 1 / 2 / 4 / 8 / 16 in us (the rule's *):
+//   8 requests of 131072 tokens                   72 / 45 / 35* (4, 8, 16)
+//   64 requests of 32000         90 / 56 / 47* / 48 / 80; drawn - / 70 / 63 / 65* / 113
+//   300 requests of 32000   132 / 107* / 113 / 160 / 320; drawn - / 195 / 175* / 242 / 488
+//   32 requests of 131072  - / - / 64 / 57 / 60*;          drawn - / - / - / 131 / 109*
 constexpr int64_t kVisit = 7000;
 void accept_grid(int batch, int vocab, bool drawn, int sm_count, const AcceptClusters& clusters, AcceptParams* p) {
   int64_t best = -1;
@@ -104,8 +108,9 @@ void accept_grid(int batch, int vocab, bool drawn, int sm_count, const AcceptClu
     const int n = 1 << i, share = ((vocab + n - 1) / n + 63) / 64 * 64, bytes = share * accept_value_bytes(drawn);
     const int active = bytes <= kAcceptBytes ? clusters.count[i][bytes <= kAcceptBytes / 2] : 0;
     if (active < 1) continue;
-    const int64_t rounds = (batch + active - 1) / active, on_sm = (int64_t(std::min(batch, active)) * n + sm_count - 1) / sm_count;
-    const int64_t cost = rounds * (kVisit + share * (drawn ? 3 : 2) / 2 * on_sm);
+    const bool meet = int64_t(std::min(batch, active)) * n > sm_count;
+    const int64_t visit = 4 * kVisit + int64_t(share) * (drawn ? 3 : 2) * (meet ? 3 : 2);  // quarter cycles
+    const int64_t cost = visit * std::max(10 * int64_t(active), 7 * int64_t(batch)) / active;
     if (best < 0 || cost < best) {
       best = cost;
       p->cluster = n;
