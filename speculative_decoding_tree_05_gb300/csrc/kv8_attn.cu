@@ -12,8 +12,9 @@
 //   q   = (hi + lo) 2^e, e4m3 both, e of the row: bf16's 8 bits, for values down to
 //         2^-11 of the row's largest; below that in steps of 2^-18 of it
 //   p s = hi + lo, e4m3 and e5m2: 4 bits, and 3 of what they leave, halves to even: at
-//         most 2^-8 off, as bf16 is, and less on average (e5m2 reaches further down than
-//         e4m3 where the weights of a long cache are small)
+//         most 2^-8 off, as bf16 is, and less on average, down to 2^-8 of the row's largest,
+//         and 2^-16 of that off below (e5m2 reaches further down than e4m3, so the small
+//         weights of a long cache keep 3 bits)
 //
 // What bounds a tile is the 128 B/clk of shared memory: an MMA reads both its operands
 // there. So the queries are the one operand that stays in tensor memory, both parts of up to 64
@@ -75,8 +76,11 @@ static_assert(kSmem <= 232448, "one CTA's shared memory");
 constexpr uint32_t kColS = 256, kColQ = 384;        // O^T [0, 256), S buffers 2 x 64, Q
 constexpr float kUnset = -1e30f;                    // running reference of a row that has seen no key
 // Weights are 2^(t - r + kLift) and r is raised when one would exceed 2^(kLift + kSlack) = 431
-// (e4m3 ends at 448).
-constexpr float kLift = 4.f, kSlack = 4.75f;
+// (e4m3 ends at 448). A raise takes 3000 cycles, as O^T is rescaled, and r follows the largest
+// t, so a row's largest weight is at least 2^kLift: of 14.75 octaves in which a weight has its
+// 8 bits, 8.75 - kLift are for what is to come, kLift + 6 for what is small. 4 in place of 2:
+// 6 raises in a unit of 58 tiles, 92 us in place of 85 (9 nodes of 16 heads, 185000 keys).
+constexpr float kLift = 2.f, kSlack = 6.75f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct Shared {
