@@ -79,6 +79,11 @@ __host__ __device__ inline Kv8Group kv8_group(int heads, int group_nodes, int no
   return u;
 }
 
+// Groups of a request with so many active nodes.
+__host__ __device__ inline int kv8_groups(int heads, int group_nodes, int nodes) {
+  return heads <= kKv8Rows ? (nodes + group_nodes - 1) / group_nodes : nodes * ((heads + kKv8Rows - 1) / kKv8Rows);
+}
+
 struct Kv8PrepareParams {
   const uint16_t* q;             // bf16 [B, T, H, 576]
   const int32_t* prefix_len;
@@ -110,8 +115,9 @@ struct Kv8AttnParams {
   int32_t batch, nodes, heads, slot_stride, max_prefix_len;
   int32_t groups;                // per request
   int32_t group_nodes;           // nodes of a group (heads <= 64; else a group is 64 heads of one node)
-  int32_t shares;                // the batch's tiles in this many equal shares; 0: one unit a request
+  int32_t shares;                // the batch's tiles in this many equal shares, or less; 0: one unit a request
   int32_t units;                 // bound on the units of a group: shares + batch - 1, or batch
+  int32_t sms;
   float* o_part;                 // fp32 [units, T * H, 512], normalised
   float* lse_part;               // fp32 [units, T * H], natural log
   Kv8Piece* pieces;              // [B]

@@ -102,6 +102,7 @@ struct Shared {
   void* o_dst;
   float* lse_dst;
   int last;  // the request's one unit
+  int shares;
   uint16_t seen[kStages][2];  // whether every row of the group sees all of a key warp's keys
 };
 static_assert(sizeof(Shared) <= 512, "barrier block");
@@ -164,15 +165,60 @@ __device__ __forceinline__ int tiles_of(const Kv8AttnParams& p, int b) {
   return nodes == 0 ? 0 : (kv8_len(p.prefix_len, b, p.max_prefix_len) + nodes + kKeys - 1) / kKeys;
 }
 
+// Shares for requests whose trees' lengths the host does not know, at most p.shares (for which the grid and the partials
+// are laid out): those that cost least among 32, one a lane, that would just fill one to eight waves. By one whole warp of
+// every CTA, so it estimates in fp32. In tiles of 64 keys: a unit costs kUnitTiles more than its tiles, a partial
+// kPartialTiles, and the time lies between whole waves of the longest unit and all units' even division among the SMs.
+// (8 requests of 4096 to 131072 keys, trees of 1 to 33 nodes of 16 heads: p.shares made 400 units, 2.6 waves, 507 us,
+// these 463. Other ragged batches: 220 to 167, 129 to 119, 178 to 178, one 152 to 170.)
+constexpr int kMaxPlanned = 32;  // requests
+constexpr float kUnitTiles = 10.f, kPartialTiles = 0.06f;
+__device__ __forceinline__ int plan_shares(const Kv8AttnParams& p, int lane) {
+  const bool mine = lane < p.batch;
+  const float n = mine ? tiles_of(p, lane) : 0;
+  const float g = mine ? kv8_groups(p.heads, p.group_nodes, kv8_nodes(p.tree_len, lane, p.nodes)) : 0;
+  float sum = n, groups = g, work = n * g, most = n;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    groups += __shfl_xor_sync(0xffffffffu, groups, o);
+    work += __shfl_xor_sync(0xffffffffu, work, o);
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+  const float sms = p.sms;
+  // a request adds between none and one unit to its part of the shares
+  const float ctas = (1 + (lane >> 2)) * sms - (lane & 3) * (1.f / 3) * groups;
+  int shares = static_cast<int>(fminf(fmaxf(ctas * sum / fmaxf(work, 1.f), 1.f), static_cast<float>(p.shares)));
+  if (lane >= 30) shares = lane == 30 ? p.shares : 1;
+  const float share = fmaxf(sum / shares, 1.f), per_tile = 1.f / share;
+  float units = 0, partials = 0;
+#pragma unroll 4
+  for (int b = 0; b < p.batch; ++b) {
+    const float c = ceilf(__shfl_sync(0xffffffffu, n, b) * per_tile), u = c * __shfl_sync(0xffffffffu, g, b);
+    units += u;
+    if (c > 1.f) partials += u;
+  }
+  const float longest = fminf(share, most) + kUnitTiles;
+  float cost = 0.5f * ceilf(units / sms) * longest + 0.5f * fmaxf((work + kUnitTiles * units) / sms, longest) + kPartialTiles * partials;
+  int best = lane;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float other = __shfl_xor_sync(0xffffffffu, cost, o);
+    const int at = __shfl_xor_sync(0xffffffffu, best, o);
+    if (other < cost || (other == cost && at < best)) cost = other, best = at;
+  }
+  return __shfl_sync(0xffffffffu, shares, best);
+}
+
 // Unit u of the batch: which request, which of its units. The requests' tiles make K in
 // all, a share is C = ceil(K / shares) of them, and a request of n tiles has ceil(n / C)
 // units of equal size. Called by whole warps; b < 0: there is no such unit.
 struct Unit {
   int b, k, count, first;
 };
-__device__ __forceinline__ Unit find_unit(const Kv8AttnParams& p, int u, int lane) {
+__device__ __forceinline__ Unit find_unit(const Kv8AttnParams& p, int shares, int u, int lane) {
   Unit r;
-  if (p.shares == 0) {
+  if (shares == 0) {
     r.b = kv8_nodes(p.tree_len, u, p.nodes) > 0 ? u : -1;
     r.k = 0;
     r.count = 1;
@@ -183,7 +229,7 @@ __device__ __forceinline__ Unit find_unit(const Kv8AttnParams& p, int u, int lan
   for (int i = lane; i < p.batch; i += 32) sum += tiles_of(p, i);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const int share = static_cast<int>(min((sum + p.shares - 1) / p.shares, 1ll << 30));
+  const int share = static_cast<int>(min((sum + shares - 1) / shares, 1ll << 30));
   int base = 0;
   r.b = -1;
   for (int i0 = 0; i0 < p.batch; i0 += 32) {
@@ -219,7 +265,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   volatile int* abort = &sh.abort;
   const int g = blockIdx.x, unit = blockIdx.y;
   grid_dep_launch();  // the merge kernel
-  const Unit un = find_unit(p, unit, lane);
+  int shares = p.shares;
+  if (shares > 1 && p.tree_len && p.batch <= kMaxPlanned) {
+    if (warp == 0) {
+      const int s = plan_shares(p, lane);
+      if (lane == 0) sh.shares = s;
+    }
+    __syncthreads();
+    shares = sh.shares;
+  }
+  const Unit un = find_unit(p, shares, unit, lane);
   const int nodes = un.b < 0 ? 0 : kv8_nodes(p.tree_len, un.b, p.nodes);  // active ones
   const Kv8Group gr = kv8_group(p.heads, p.group_nodes, nodes, g);
   const int row0 = gr.row0, rows = gr.rows;

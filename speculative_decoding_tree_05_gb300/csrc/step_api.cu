@@ -37,7 +37,7 @@ int kv8_layout(const ddt_dims* d, int sm_count, Kv8Layout* w) {
   if (d->max_prefix_len > (1 << 30)) return DDT_ERR_DIMS;
   const int H = d->num_heads, T = d->num_nodes;
   w->group_nodes = H <= kKv8Rows ? std::min(T, kKv8Rows / H) : 1;
-  w->groups = H <= kKv8Rows ? (T + w->group_nodes - 1) / w->group_nodes : T * ((H + kKv8Rows - 1) / kKv8Rows);
+  w->groups = kv8_groups(H, w->group_nodes, T);
   const int64_t B = d->batch, most = (int64_t(d->max_prefix_len) + T + kKv8Keys - 1) / kKv8Keys;
   int64_t tiles = B * most;
   if (d->prefix_len_sum > 0) tiles = std::min(tiles, (int64_t(d->prefix_len_sum) + B * T) / kKv8Keys + B);
@@ -242,6 +242,7 @@ extern "C" int ddtree_verify_attn_kv8(const void* q, const void* kv8_pool, const
   p.groups = w.groups;
   p.group_nodes = w.group_nodes;
   p.shares = w.shares;
+  p.sms = sms;
   p.units = w.units;
   p.o_part = reinterpret_cast<float*>(ws + w.o_off);
   p.lse_part = reinterpret_cast<float*>(ws + w.lse_off);

@@ -140,6 +140,18 @@ def test_ragged_trees(lens, heads, tree_len):
     check(d, out, lse)
 
 
+@pytest.mark.parametrize("batch", [8, 32, 33])
+def test_ragged_trees_over_long_prefixes(batch):
+    """Trees' lengths that the division into units follows (up to 32 requests), among them trees of no node."""
+    h = np.random.default_rng(batch)
+    d = make([int(x) for x in h.integers(0, 12000 if batch == 8 else 2500, batch)], 33, 16, seed=batch)
+    for tree_len in (h.integers(0, 34, batch), np.where(np.arange(batch) == 5, 33, 0), np.full(batch, 33), np.zeros(batch)):
+        d["tree_len"] = torch.from_numpy(tree_len.astype(np.int32)).cuda()
+        out, lse, st = call(d)
+        assert st == 0
+        check(d, out, lse, requests=[0, 4, 5, batch - 1])
+
+
 @pytest.mark.parametrize("amp,sm", [(8.0, SCALE), (0.01, SCALE), (1.0, -0.2), (1.0, 0.0), (30.0, 0.5)])
 def test_amplitudes_and_scales(amp, sm):
     d = make([900], 9, 16, seed=2, amp=amp)
