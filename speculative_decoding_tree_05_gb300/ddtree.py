@@ -322,6 +322,15 @@ def _need(device, *checks):
                              + ("" if t.is_contiguous() else " (not contiguous)"))
 
 
+def _result(stream, device, name, t, dtype, shape):
+    """A caller's tensor for a result, checked, or one made for it."""
+    import torch
+    if t is None:
+        return _make(stream, torch.empty, shape, dtype=dtype, device=device)
+    _need(device, (name, t, dtype, shape))
+    return t
+
+
 def _run_on(device, fn, name, *args):
     """Call the library with `device` current (it works on the current device); raises DDTError."""
     import torch
@@ -686,17 +695,14 @@ class Kv8Verifier:
         import torch
         d = self.dims
         B, T, H = d.batch, d.num_nodes, d.num_heads
-        if out is None:
-            out = _make(stream, torch.empty, (B, T, H, D_V), dtype=torch.bfloat16, device=self.device)
-        if lse is None:
-            lse = _make(stream, torch.empty, (B, T, H), dtype=torch.float32, device=self.device)
         _need(self.device, ("q", q, torch.bfloat16, (B, T, H, D_QK)),
               ("pool", pool, torch.uint8, (d.pool_slots, KV8_ROW)), ("scale", scale, torch.float32, (d.pool_slots,)),
               ("slot_idx", slot_idx, torch.int32, (B, d.slot_stride)), ("prefix_len", prefix_len, torch.int32, (B,)),
-              ("tree_parent", tree_parent, torch.int32, (B, T)), ("tree_slot_idx", tree_slot_idx, torch.int32, (B, T)),
-              ("out", out, torch.bfloat16, (B, T, H, D_V)), ("lse", lse, torch.float32, (B, T, H)))
+              ("tree_parent", tree_parent, torch.int32, (B, T)), ("tree_slot_idx", tree_slot_idx, torch.int32, (B, T)))
         if tree_len is not None:
             _need(self.device, ("tree_len", tree_len, torch.int32, (B,)))
+        out = _result(stream, self.device, "out", out, torch.bfloat16, (B, T, H, D_V))
+        lse = _result(stream, self.device, "lse", lse, torch.float32, (B, T, H))
         _run_on(self.device, self.lib.ddtree_verify_attn_kv8, "ddtree_verify_attn_kv8", q.data_ptr(), pool.data_ptr(),
                 scale.data_ptr(), slot_idx.data_ptr(), prefix_len.data_ptr(), tree_parent.data_ptr(),
                 tree_slot_idx.data_ptr(), _addr(tree_len), sm_scale, out.data_ptr(), lse.data_ptr(), self.dims_ref,
@@ -733,7 +739,7 @@ class TreeAcceptor:
     def _stride(self, t, name, dtypes):
         """The distance of consecutive nodes' rows, the same over requests."""
         B, T = self.dims.batch, self.dims.num_nodes
-        if t.dtype not in dtypes or t.shape != (B, T, self.vocab) or t.device != self.device:
+        if t.dtype not in dtypes or t.shape != (B, T, self.vocab) or t.get_device() != self.device.index:
             raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))} [{B}, {T}, {self.vocab}] on {self.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
         row = t.stride(1) if T > 1 else t.stride(0) if B > 1 else self.vocab
@@ -748,20 +754,15 @@ class TreeAcceptor:
         import torch
         d = self.dims
         B, T = d.batch, d.num_nodes
-        if path is None:
-            path = _make(stream, torch.empty, (B, T), dtype=torch.int32, device=self.device)
-        if path_len is None:
-            path_len = _make(stream, torch.empty, (B,), dtype=torch.int32, device=self.device)
-        if next_token is None:
-            next_token = _make(stream, torch.empty, (B,), dtype=torch.int32, device=self.device)
         stride = self._stride(logits, "logits", (torch.bfloat16, torch.float32))
         draft_stride = 0 if draft_prob is None else self._stride(draft_prob, "draft_prob", (torch.float32,))
         _need(self.device, ("tokens", tokens, torch.int32, (B, T)), ("tree_parent", tree_parent, torch.int32, (B, T)),
-              ("uniform", uniform, torch.float32, (B, T)), ("temperature", temperature, torch.float32, (B,)),
-              ("path", path, torch.int32, (B, T)), ("path_len", path_len, torch.int32, (B,)),
-              ("next_token", next_token, torch.int32, (B,)))
+              ("uniform", uniform, torch.float32, (B, T)), ("temperature", temperature, torch.float32, (B,)))
         if tree_len is not None:
             _need(self.device, ("tree_len", tree_len, torch.int32, (B,)))
+        path = _result(stream, self.device, "path", path, torch.int32, (B, T))
+        path_len = _result(stream, self.device, "path_len", path_len, torch.int32, (B,))
+        next_token = _result(stream, self.device, "next_token", next_token, torch.int32, (B,))
         _run_on(self.device, self.lib.ddtree_accept, "ddtree_accept", logits.data_ptr(),
                 int(logits.dtype is torch.float32), stride, self.vocab, _addr(draft_prob), draft_stride, tokens.data_ptr(),
                 tree_parent.data_ptr(), _addr(tree_len), uniform.data_ptr(), temperature.data_ptr(), path.data_ptr(),
