@@ -524,7 +524,8 @@ DDT_API int ddtree_verify_attn_kv8(const void* q, const void* kv8_pool, const fl
  *   logits       [B, T] rows of vocab values, bf16 or (logits_fp32 nonzero) fp32, row
  *                b * T + i at logits + (b * T + i) * logit_stride (elements, >= vocab,
  *                no alignment beyond the element's); NaN counts as -inf, +inf as the
- *                largest finite number
+ *                largest finite number, and what is further below the row's largest than
+ *                fp32 reaches as -inf
  *   draft_prob   fp32, rows like the logits' with draft_stride; or NULL
  *   tokens       int32 [B, T]; a node with a token outside [0, vocab) is left out, with
  *                all below it, and sets DDT_STATUS_BAD_TOKEN
@@ -543,7 +544,8 @@ DDT_API int ddtree_verify_attn_kv8(const void* q, const void* kv8_pool, const fl
  * Weights are whole multiples of 2^-43 of the node's largest, so sums do not depend on
  * their order.  vocab <= 2^18.  dims gives batch and num_nodes.  Outputs must not
  * overlap inputs or one another (DDT_ERR_ALIAS).
- * workspace >= ddtree_accept_workspace_bytes(dims, vocab).
+ * workspace >= ddtree_accept_workspace_bytes(dims, vocab).  Calls, and replays of
+ * captured ones, that share a workspace must not overlap.
  */
 DDT_API size_t ddtree_accept_workspace_bytes(const ddt_dims* dims, int32_t vocab);
 DDT_API int ddtree_accept(const void* logits, int32_t logits_fp32, int64_t logit_stride, int32_t vocab,

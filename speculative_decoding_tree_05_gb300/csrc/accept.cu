@@ -69,7 +69,7 @@ struct RowWeight {
   float max, c_hi, c_lo;
   int only;  // greedy: the token; else -1
   // of token x, whose distance from the largest logit is y in units of a halving
-  __device__ __forceinline__ float distance(float l) const { return l > -CUDART_INF_F ? (max - l) * c_hi : CUDART_INF_F; }
+  __device__ __forceinline__ float distance(float l) const { return max - l < CUDART_INF_F ? (max - l) * c_hi : CUDART_INF_F; }
   __device__ __forceinline__ unsigned long long exactly(float l, float y, const unsigned long long* pow_sh) const {
     const float d = max - l, b = d - max, e = (max - (d - b)) - (l + b);  // max - l = d + e exactly
     return weight_of(y, fmaf(d, c_hi, -y) + fmaf(d, c_lo, e * c_hi), pow_sh);

@@ -145,6 +145,22 @@ def test_temperatures_of_their_own(dtype, drawn):
     assert all((x == y).all() for x, y in zip(got, again))
 
 
+@pytest.mark.parametrize("drawn", [False, True])
+def test_logits_whose_difference_is_no_number(drawn):
+    """They count as -inf, at any temperature; differences that are numbers do not."""
+    d = make(12, 3, 300, torch.float32, "star", drawn, seed=17)
+    d["temperature"] = torch.tensor([math.inf, 1e38, 1.0] * 4, device="cuda")
+    d["logits"][:] = 2e38
+    d["logits"][:, :, 100:] = -2e38
+    d["tokens"][:, 1:] = 250
+    e = dict(d, logits=d["logits"].clone())
+    e["logits"][:, :, 100:] = -math.inf
+    got, st = call(d)
+    want, _ = call(e)
+    assert st == 0 and all((x == y).all() for x, y in zip(got, want))
+    assert (got[1] == 1).all() and (got[2] < 100).all() and (got[2] >= 0).all()
+
+
 def test_greedy_takes_the_lowest_of_equal_logits():
     d = make(4, 3, 5000, torch.bfloat16, "chain", temperature=0.0, seed=4)
     d["logits"][:] = 0
