@@ -343,6 +343,16 @@ def _run_on(device, fn, name, *args):
         raise DDTError(rc, name)
 
 
+def _run_at(device, fn, name, *args):
+    """_run_on for tensors that are on `device`, so CUDA is set up: short calls feel a look at the current device."""
+    import torch
+    if torch._C._cuda_getDevice() != device.index:
+        return _run_on(device, fn, name, *args)
+    rc = fn(*args)
+    if rc != DDT_OK:
+        raise DDTError(rc, name)
+
+
 def _addr(t):
     """A tensor's address as ctypes takes it (None: NULL); cheaper than a c_void_p a tensor."""
     return None if t is None else t.data_ptr()
@@ -610,12 +620,17 @@ def _rows_of(rows, name, device, n):
 def _kv8_checks(pool, scale, slots, workspace):
     """The device, the cache's slots and the listed ones."""
     import torch
-    device = _on_cuda(pool, "pool")
-    if pool.dim() != 2 or slots.dim() != 1:
-        raise ValueError("pool must be [slots, 640] and slots a list")
-    N, n = pool.shape[0], slots.shape[0]
-    _need(device, ("pool", pool, torch.uint8, (N, KV8_ROW)), ("scale", scale, torch.float32, (N,)),
-          ("slots", slots, torch.int32, (n,)))
+    at, N, n = pool.get_device(), scale.numel(), slots.numel()
+    # One condition for what _need checks of three tensors: a short call is bound by these lines.
+    if not (at >= 0 and pool.dtype is torch.uint8 and pool.shape == (N, KV8_ROW) and pool.is_contiguous()
+            and scale.dtype is torch.float32 and scale.dim() == 1 and scale.get_device() == at and scale.is_contiguous()
+            and slots.dtype is torch.int32 and slots.dim() == 1 and slots.get_device() == at and slots.is_contiguous()):
+        device = _on_cuda(pool, "pool")
+        if pool.dim() != 2 or slots.dim() != 1:
+            raise ValueError("pool must be [slots, 640] and slots a list")
+        _need(device, ("pool", pool, torch.uint8, (pool.shape[0], KV8_ROW)),
+              ("scale", scale, torch.float32, (pool.shape[0],)), ("slots", slots, torch.int32, (n,)))
+    device = pool.device
     if workspace is not None:
         _need(device, ("workspace", workspace, torch.uint8, workspace.shape))
         if workspace.numel() < 256:
@@ -645,7 +660,7 @@ def kv8_write(rows, slots, pool, scale, norm_weight=None, eps=1e-6, rotation=Non
             raise ValueError("rotation must be [positions, 64]")
         positions = rotation.shape[0]
         _need(device, ("rotation", rotation, torch.float32, (positions, 64)), ("position", position, torch.int32, (n,)))
-    _run_on(device, lib().ddtree_kv8_write, "ddtree_kv8_write", rows.data_ptr(), stride, slots.data_ptr(), n,
+    _run_at(device, lib().ddtree_kv8_write, "ddtree_kv8_write", rows.data_ptr(), stride, slots.data_ptr(), n,
             _addr(norm_weight), eps, _addr(rotation), _addr(position), positions, interleaved, pool.data_ptr(),
             scale.data_ptr(), N, _addr(workspace), _stream_of(device, stream))
     if stream is not None:
@@ -663,7 +678,7 @@ def kv8_read(pool, scale, slots, out=None, workspace=None, stream=None):
     if out is None:
         out = _make(stream, torch.empty, (n, D_QK), dtype=torch.bfloat16, device=device)
     stride = _rows_of(out, "out", device, n)
-    _run_on(device, lib().ddtree_kv8_read, "ddtree_kv8_read", pool.data_ptr(), scale.data_ptr(), slots.data_ptr(), n,
+    _run_at(device, lib().ddtree_kv8_read, "ddtree_kv8_read", pool.data_ptr(), scale.data_ptr(), slots.data_ptr(), n,
             out.data_ptr(), stride, N, _addr(workspace), _stream_of(device, stream))
     _keep(stream, out)
     return out
@@ -703,7 +718,7 @@ class Kv8Verifier:
             _need(self.device, ("tree_len", tree_len, torch.int32, (B,)))
         out = _result(stream, self.device, "out", out, torch.bfloat16, (B, T, H, D_V))
         lse = _result(stream, self.device, "lse", lse, torch.float32, (B, T, H))
-        _run_on(self.device, self.lib.ddtree_verify_attn_kv8, "ddtree_verify_attn_kv8", q.data_ptr(), pool.data_ptr(),
+        _run_at(self.device, self.lib.ddtree_verify_attn_kv8, "ddtree_verify_attn_kv8", q.data_ptr(), pool.data_ptr(),
                 scale.data_ptr(), slot_idx.data_ptr(), prefix_len.data_ptr(), tree_parent.data_ptr(),
                 tree_slot_idx.data_ptr(), _addr(tree_len), sm_scale, out.data_ptr(), lse.data_ptr(), self.dims_ref,
                 self.workspace.data_ptr(), self.workspace.numel(), _stream_of(self.device, stream))
@@ -763,7 +778,7 @@ class TreeAcceptor:
         path = _result(stream, self.device, "path", path, torch.int32, (B, T))
         path_len = _result(stream, self.device, "path_len", path_len, torch.int32, (B,))
         next_token = _result(stream, self.device, "next_token", next_token, torch.int32, (B,))
-        _run_on(self.device, self.lib.ddtree_accept, "ddtree_accept", logits.data_ptr(),
+        _run_at(self.device, self.lib.ddtree_accept, "ddtree_accept", logits.data_ptr(),
                 int(logits.dtype is torch.float32), stride, self.vocab, _addr(draft_prob), draft_stride, tokens.data_ptr(),
                 tree_parent.data_ptr(), _addr(tree_len), uniform.data_ptr(), temperature.data_ptr(), path.data_ptr(),
                 path_len.data_ptr(), next_token.data_ptr(), self.dims_ref, self.workspace.data_ptr(),
