@@ -88,7 +88,7 @@ struct Kv8PrepareParams {
   const uint16_t* q;             // bf16 [B, T, H, 576]
   const int32_t* prefix_len;
   const int32_t* tree_len;
-  uint8_t* images;               // [B, groups, kKv8Image]
+  uint8_t* images;               // [B, groups, kKv8Image], or null: the units cut their rows themselves
   uint16_t* out;                 // rows of inactive nodes are written
   float* lse;
   int32_t batch, nodes, heads, max_prefix_len, groups, group_nodes;
@@ -103,7 +103,9 @@ struct Kv8Piece {                 // a request's units, for the merge
 
 struct Kv8AttnParams {
   CUtensorMap tmap;              // pool as [N][640] bytes, box 128 bytes x 1 row, 128-byte swizzle
-  const uint8_t* images;         // [B, groups, kKv8Image], of the kernel before
+  const uint8_t* images;         // [B, groups, kKv8Image], of the kernel before; or null, then
+  const uint16_t* q;             // bf16 [B, T, H, 576], and
+  float scale_log2;              // sm_scale * log2(e)
   const uint8_t* kv;             // [N, 640]
   const float* scale;            // [N]
   const int32_t* slot_idx;       // [B, slot_stride]

@@ -45,12 +45,12 @@
 // that see it. The tiles of the whole batch are cut into equal shares, whatever the
 // lengths; a request has its share of them, in equal units. One unit writes bf16 and the
 // log-sum-exp at once, else each writes its normalised O and the merge kernel joins them.
-// The query rows come cut and laid out from the kernel before (kv8_prepare.cu).
+// The query rows come cut and laid out from the kernel before (kv8_prepare.cu), or (kCut) a unit
+// cuts its own.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <type_traits>
-#include "kv8.cuh"
-#include "ptx.cuh"
+#include "kv8_cut.cuh"
 
 namespace ddt {
 namespace {
@@ -64,6 +64,9 @@ constexpr int kRows = kKv8Rows;
 constexpr int kStages = 4;
 constexpr int kChunk = kKv8Chunk;                   // 128 bytes of 64 keys: 8 KB
 constexpr int kStageBytes = 5 * kChunk;             // 40960
+constexpr int kOffCut = 2 * kStageBytes;            // while a unit cuts its query rows: [128 lanes][512 + 16 bytes]
+constexpr int kCutRow = 512 + 16;
+static_assert(kOffCut + 128 * kCutRow <= kStages * kStageBytes, "the last two stages");
 constexpr int kOffRope = kStages * kStageBytes;     // the queries' rope values, [64 rows][128 bytes]
 constexpr int kOffQs = kOffRope + kRows * 128;      // [64] the rows' factors of a score
 constexpr int kOffP = kOffQs + 1024;                // [2 buffers][2 parts][64 rows][64 keys]
@@ -261,6 +264,8 @@ __device__ __forceinline__ Unit find_unit(const Kv8AttnParams& p, int shares, in
   return r;
 }
 
+// kCut: the query rows are cut here, beside the first tiles' gathers, not by the kernel before.
+template <bool kCut>
 __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_constant__ Kv8AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -339,12 +344,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
 
   if (warp == 0) {
     if (elect_one()) {
-      grid_dep_wait();  // the query rows: what comes before overlaps their making
-      mbar_arrive_expect_tx(&sh.q_full, kKv8Image - kKv8ImageRope);
-      bulk_load(base + kOffRope, p.images + (static_cast<int64_t>(un.b) * p.groups + g) * kKv8Image + kKv8ImageRope,
-                kKv8Image - kKv8ImageRope, &sh.q_full);
-      ok = mbar_wait_abortable(&sh.q_full, 0, abort, false, __LINE__) &&
-           mbar_wait_abortable(&sh.q_ready, 0, abort, false, __LINE__);
+      if (!kCut) {
+        grid_dep_wait();  // the query rows: what comes before overlaps their making
+        mbar_arrive_expect_tx(&sh.q_full, kKv8Image - kKv8ImageRope);
+        bulk_load(base + kOffRope, p.images + (static_cast<int64_t>(un.b) * p.groups + g) * kKv8Image + kKv8ImageRope,
+                  kKv8Image - kKv8ImageRope, &sh.q_full);
+        ok = mbar_wait_abortable(&sh.q_full, 0, abort, false, __LINE__);
+      }
+      ok = ok && mbar_wait_abortable(&sh.q_ready, 0, abort, false, __LINE__);
       tc_fence_after();
       const uint32_t idesc8 = idesc_f8_f32(128, kKeys, kE4m3, kE4m3, false, false), idesc = idesc_bf16_f32(64, kKeys, false, false);  // (M64: the first parts' lanes)
       const uint64_t d_k = smem_desc(base, 16, 1024, kSwizzle128B);
@@ -494,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       if (warp >= kFirstKey && in_pool(slot_now)) scale_now = __ldg(p.scale + slot_now);
       slot_next = read_slot(t + 2, k);
       const uint32_t sbase = base + st * kStageBytes;
-      const bool empty = t < kStages || mbar_wait_abortable(&sh.k_empty[st][gather], ph ^ 1, abort, false, __LINE__);
+      const bool empty = t < kStages ? !kCut || t < 2 || mbar_wait_abortable(&sh.q_ready, 0, abort, false, __LINE__)
+                                     : mbar_wait_abortable(&sh.k_empty[st][gather], ph ^ 1, abort, false, __LINE__);
       if (!__all_sync(0xffffffffu, empty)) {
         ok = false;
         break;
@@ -552,8 +560,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     const int id = half * 128 + quarter * 32 + lane;
     const int bar = 1 + 4 * set;                   // the set's barrier
     float* alpha_sh = reinterpret_cast<float*>(smem + kOffAlpha);
-    {  // the queries, a quarter of the lanes' bytes a warp
-      const int part4 = (warp - 1) >> 2;
+    const int part4 = (warp - 1) >> 2;  // the queries, a quarter of the lanes' bytes a warp
+    if (kCut) {
+      const uint16_t* q = p.q + (static_cast<int64_t>(un.b) * p.nodes * p.heads + row0) * kDqk;
+      uint32_t w[4][9];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = warp - 1 + 16 * j;
+        load_query(r < rows ? q + static_cast<int64_t>(r) * kDqk : nullptr, lane, w[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = warp - 1 + 16 * j;
+        CutQuery c = {};
+        if (r < rows) c = cut_row(w[j], lane, p.scale_log2);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+          *reinterpret_cast<uint4*>(smem + kOffCut + query_lane(r, part) * kCutRow + query_piece(lane) * 16) = c.part[part];
+        *reinterpret_cast<uint32_t*>(smem + kOffRope + query_rope_at(r, lane)) = c.rope;
+        if (lane == 0) reinterpret_cast<float*>(smem + kOffQs)[r] = c.factor;
+      }
+      bar_sync(6, kSoftmax);
+      uint32_t r[32];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 v = *reinterpret_cast<const uint4*>(smem + kOffCut + (quarter * 32 + lane) * kCutRow + (8 * part4 + j) * 16);
+        r[4 * j] = v.x, r[4 * j + 1] = v.y, r[4 * j + 2] = v.z, r[4 * j + 3] = v.w;
+      }
+      tmem_st32(tmem + lane_off + kColQ + 32 * part4, r);
+      fence_proxy_async_smem();  // the rope values are read, and the last two stages written, by other means
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_ready);
+    } else {
       grid_dep_wait();
       const uint4* src = reinterpret_cast<const uint4*>(p.images + (static_cast<int64_t>(un.b) * p.groups + g) * kKv8Image) +
                          8 * part4 * 128 + quarter * 32 + lane;
@@ -568,7 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_ready);
     }
-    bool failed = !mbar_wait_abortable(&sh.q_full, 0, abort, false, __LINE__);  // a wait of this thread ran out: the warps leave together at the next barrier
+    // a wait of this thread ran out: the warps leave together at the next barrier
+    bool failed = !kCut && !mbar_wait_abortable(&sh.q_full, 0, abort, false, __LINE__);
     // of this thread's rows: sums (of even and odd keys), score factors and (lowered by kLift) references
     uint64_t l[2];
     float qs[2], m[2];
@@ -799,12 +839,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     atomicOr(p.status, sh.flags);
   }
   if (warp == 0) tmem_dealloc(tmem, 512);
+  if (kCut) grid_dep_wait();  // (this grid is not done before the one that it follows)
 }
 
 }  // namespace
 
 cudaError_t configure_kv8_attn() {
-  return cudaFuncSetAttribute(kv8_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(kv8_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnParams& p, cudaStream_t stream) {
@@ -818,7 +860,7 @@ cudaError_t launch_kv8_attn(const Kv8AttnParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_attn_kernel, p);
+  return cudaLaunchKernelEx(&cfg, p.images ? kv8_attn_kernel<false> : kv8_attn_kernel<true>, p);
 }
 
 }  // namespace ddt

@@ -285,6 +285,30 @@ def test_large_batches(batch):
     check(d, out, lse, requests=[0, 1, 2, 3, 40, 63, batch - 1])
 
 
+@pytest.mark.parametrize("batch,most,nodes,heads,ragged", [(40, 20, 9, 64, False), (24, 500, 7, 128, True), (60, 90, 12, 24, True),
+                                                           (170, 300, 1, 16, False), (9, 40, 40, 100, False)])
+def test_many_groups_over_short_prefixes(batch, most, nodes, heads, ragged):
+    """More groups than SMs and no request split: the units cut their query rows themselves."""
+    h = np.random.default_rng(batch)
+    d = make([most] + [int(x) for x in h.integers(0, most + 1, batch - 1)], nodes, heads, seed=batch, tree="chain" if nodes > 20 else "random")
+    if ragged:
+        n = h.integers(0, nodes + 1, batch)
+        n[1] = nodes
+        d["tree_len"] = torch.from_numpy(n.astype(np.int32)).cuda()
+    d["q"][0, 0, heads - 1, 5], d["q"][2, 0, 0, 570] = math.nan, -math.inf
+    d["q"][1, 0, 0] = 0
+    d["q"][1, nodes - 1] *= 2.0 ** -100
+    d["q"][3, 0, 0, 100] = 1000
+    out, lse, st = call(d)
+    assert st == 0
+    active = d["tree_len"] is None or int(d["tree_len"][0]) > 0
+    if active:
+        assert bool(torch.isnan(out[0, 0, heads - 1]).all()) and bool(torch.isfinite(out[0, 0, :heads - 1]).all())
+    check(d, out, lse, skip={(0, 0), (2, 0)}, requests=[0, 1, 2, 3, batch // 2, batch - 1])
+    again, lse2, _ = call(d)
+    assert torch.equal(out.nan_to_num(1.5), again.nan_to_num(1.5)) and torch.equal(lse.nan_to_num(1.5), lse2.nan_to_num(1.5))
+
+
 @pytest.mark.parametrize("hint", [0, 1, 2500, 2 ** 31 - 1])
 def test_length_hints(hint):
     d = make([2000, 500], 9, 16, seed=14, stride=60000)

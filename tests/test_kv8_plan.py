@@ -69,5 +69,9 @@ def test_a_long_request_fills_the_device_and_a_short_one_does_not_split_far(lib)
 def test_no_partials_without_a_split(lib):
     image = 128 * 512 + 64 * 128 + 256            # a group's query rows
     assert plan(lib, slot_stride=40, max_prefix_len=40)[3] == 512 + 3 * image
+    # more groups than SMs: their units cut the query rows themselves
+    assert plan(lib, batch=51, slot_stride=40, max_prefix_len=40)[1] == 1
+    assert plan(lib, batch=50, slot_stride=40, max_prefix_len=40)[3] == 768 + 150 * image
+    assert plan(lib, batch=51, slot_stride=40, max_prefix_len=40)[3] == 768
     groups, shares, units, size = plan(lib, slot_stride=185000, max_prefix_len=185000)
     assert size == 512 + 3 * image + -(-units * 144 * 4 // 256) * 256 + units * 144 * 512 * 4
