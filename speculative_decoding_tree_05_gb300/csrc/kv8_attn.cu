@@ -26,7 +26,7 @@
 // 48 + 96 KB of operands a tile, and 48 KB written (with both operands of the scores in
 // shared memory it was 144 + 96 KB, and a tile took 2330 cycles). O^T takes 256 TMEM columns,
 // the scores twice 64, the queries 128; one CTA holds the whole output.
-// A tile of 64 rows takes 2050 cycles now (65 nodes of 128 heads, 65536 keys: 1036 us, 1.15
+// A tile of 64 rows takes 2030 cycles now (65 nodes of 128 heads, 65536 keys: 1023 us, 1.16
 // PFLOP/s), and no one part bounds it: the tensor core works 1500 of them, shared memory 1560,
 // the schedulers issue in 1550, the gathers run at 19 B/clk and SM (without them it is 8 % less),
 // and the softmax's chain of waits is 2000 long, of which two overlap. With one query row a
@@ -184,7 +184,7 @@ __device__ __forceinline__ int tiles_of(const Kv8AttnParams& p, int b) {
 // every CTA, so it estimates in fp32. In tiles of 64 keys: a unit costs kUnitTiles more than its tiles, a partial
 // kPartialTiles, and the time lies between whole waves of the longest unit and all units' even division among the SMs.
 // (8 requests of 4096 to 131072 keys, trees of 1 to 33 nodes of 16 heads: p.shares made 400 units, 2.6 waves, 507 us,
-// these 463. Other ragged batches: 220 to 167, 129 to 119, 178 to 178, one 152 to 170.)
+// these 463 then. Other ragged batches: 220 to 167, 129 to 119, 178 to 178, one 152 to 170.)
 constexpr int kMaxPlanned = 32;  // requests
 constexpr float kUnitTiles = 10.f, kPartialTiles = 0.06f;
 __device__ __forceinline__ int plan_shares(const Kv8AttnParams& p, int lane) {
