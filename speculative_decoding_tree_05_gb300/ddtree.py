@@ -326,6 +326,8 @@ def _result(stream, device, name, t, dtype, shape):
     """A caller's tensor for a result, checked, or one made for it."""
     import torch
     if t is None:
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
         return _make(stream, torch.empty, shape, dtype=dtype, device=device)
     _need(device, (name, t, dtype, shape))
     return t
