@@ -11,10 +11,8 @@
 // Operands of 8 bits (fp32 accumulation, which is exact to fp32: 3e-8 of the result):
 //   q   = (hi + lo) 2^e, e4m3 both, e of the row: bf16's 8 bits, for values down to
 //         2^-11 of the row's largest; below that in steps of 2^-18 of it
-//   p s = hi + lo, e4m3 and e5m2: 4 bits, and 3 of what they leave, halves to even: at
-//         most 2^-8 off, as bf16 is, and less on average, down to 2^-8 of the row's largest,
-//         and 2^-16 of that off below (e5m2 reaches further down than e4m3, so the small
-//         weights of a long cache keep 3 bits)
+//   p s = three e5m2 parts of 3 bits each, which hold f16's 11 bits of a weight (2^-12 of it
+//         off) down to 2^-13 of the row's largest and lose at most 2^-24 of that below
 //
 // With all operands in shared memory its 128 B/clk bounded a tile, as an MMA reads both there.
 // So the queries are the one operand that stays in tensor memory, both parts of up to 64
@@ -22,15 +20,15 @@
 // of the second product, so that each 8-bit value is read once for 64 rows and part:
 //   S[hi, lo rows][64 keys]      = Q . K^T    16 MMAs M128 x N64 x K32 (8 bit, Q in tensor memory)
 //                                             and 4 M64 x N64 x K16 (rope, added to the first parts')
-//   O^T[512 dims][rows] += V^T . P^T          2 x 4 x 2 MMAs M128 x N x K32 (V^T: the same bytes read MN-major)
-// 48 + 96 KB of operands a tile, and 48 KB written (with both operands of the scores in
-// shared memory it was 144 + 96 KB, and a tile took 2330 cycles). O^T takes 256 TMEM columns,
+//   O^T[512 dims][rows] += V^T . P^T          3 x 4 x 2 MMAs M128 x N x K32 (V^T: the same bytes read MN-major)
+// 48 + 144 KB of operands a tile, and 52 KB written (with both operands of the scores in
+// shared memory it was 96 KB more). O^T takes 256 TMEM columns,
 // the scores twice 64, the queries 128; one CTA holds the whole output.
-// A tile of 64 rows takes 2030 cycles now (65 nodes of 128 heads, 65536 keys: 1023 us, 1.16
-// PFLOP/s), and no one part bounds it: the tensor core works 1500 of them, shared memory 1560,
-// the schedulers issue in 1550, the gathers run at 19 B/clk and SM (without them it is 8 % less),
-// and the softmax's chain of waits is 2000 long, of which two overlap. With one query row a
-// key it is the gathers alone (16 requests of up to 32768 keys: 53 us, 4 TB/s in the kernel).
+// A tile of 64 rows takes 2130 cycles (65 nodes of 128 heads, 65536 keys: 1072 us, 1.11
+// PFLOP/s), of which shared memory works 1900; the gathers run at 18 B/clk and SM, and the
+// softmax's chain of waits is 2000 long, of which two overlap. (In two parts of weights, e4m3 and e5m2,
+// it took 2030.) With one query row a
+// key it is the gathers alone (16 requests of up to 32768 keys: 54 us, 4 TB/s in the kernel).
 //
 // Per CTA (896 threads), one unit = (up to 64 (node, head) rows of a request, a share of its tiles):
 //   warp 0       TMEM; one lane issues S(t) when stage t has landed
@@ -69,9 +67,9 @@ constexpr int kCutRow = 512 + 16;
 static_assert(kOffCut + 128 * kCutRow <= kStages * kStageBytes, "the last two stages");
 constexpr int kOffRope = kStages * kStageBytes;     // the queries' rope values, [64 rows][128 bytes]
 constexpr int kOffQs = kOffRope + kRows * 128;      // [64] the rows' factors of a score
-constexpr int kOffP = kOffQs + 1024;                // [2 buffers][2 parts][64 rows][64 keys]
-constexpr int kPart = kKeys * kRows;                // 4096
-constexpr int kOffMask = kOffP + 4 * kPart;         // [stages][64] row masks of the stage's keys
+constexpr int kOffP = kOffQs + 1024;                // [2 buffers][3 parts][64 rows][64 keys]
+constexpr int kPart = kKeys * kRows, kParts = 3;    // 4096
+constexpr int kOffMask = kOffP + 2 * kParts * kPart;      // [stages][64] row masks of the stage's keys
 constexpr int kOffKey = kOffMask + kStages * kKeys * 8;   // [stages][3][64] s, log2 s, 1 / s
 constexpr int kOffMax = kOffKey + kStages * kKeys * 12;   // [64] running reference
 constexpr int kOffAlpha = kOffMax + kRows * 4;      // [64] rescale factors, later 1 / row sums
@@ -83,12 +81,14 @@ constexpr int kSmem = kOffBar + 512 + 1024;
 static_assert(kSmem <= 232448, "one CTA's shared memory");
 constexpr uint32_t kColS = 256, kColQ = 384;        // O^T [0, 256), S buffers 2 x 64, Q
 constexpr float kUnset = -1e30f;                    // running reference of a row that has seen no key
-// Weights are 2^(t - r + kLift) and r is raised when one would exceed 2^(kLift + kSlack) = 431
-// (e4m3 ends at 448). A raise takes 3000 cycles, as O^T is rescaled, and r follows the largest
-// t, so a row's largest weight is at least 2^kLift: of 14.75 octaves in which a weight has its
-// 8 bits, 8.75 - kLift are for what is to come, kLift + 6 for what is small. 4 in place of 2:
-// 6 raises in a unit of 58 tiles, 92 us in place of 85 (9 nodes of 16 heads, 185000 keys).
-constexpr float kLift = 2.f, kSlack = 6.75f;
+// Weights are 2^(t - r + kLift) and r is raised when one would exceed 2^(kLift + kSlack) = 55109
+// (e5m2 ends at 57344). A raise takes 3000 cycles, as O^T is rescaled, and r follows the largest
+// t, so a row's largest weight is at least 2^kLift. What falls below the parts' last step is at
+// most 2^-17 of a weight, 2^-(17 + kLift) of the largest; but behind one dominant key a tail's
+// errors may all have one sign, so they count times the keys of a unit. 9 nodes of 16 heads, 185000
+// keys: 87 us, with a lift of 6 86, of 8 88; with the weights as e4m3 and e5m2, which end at 448
+// and left the keys out that were 2^-19 of the largest, 83.
+constexpr float kLift = 7.f, kSlack = 8.75f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct Shared {
@@ -143,18 +143,19 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// Two weights in two 8-bit parts, e4m3 and what that leaves in e5m2. Through f16, whose 11 bits lose 2^-12 of a weight
-// and whose differences here are exact: five conversions and a subtraction a pair.
-__device__ __forceinline__ void cut_weights(float x, float y, uint32_t& hi, uint32_t& lo) {
-  uint32_t h, back;
-  uint16_t a, b;
+// Two weights in three e5m2 parts, each the nearest to what those before it leave. A pair goes through f16, whose 11 bits
+// lose 2^-12 of a weight; an e5m2 value is f16's upper byte, so the differences are exact, and with 3 bits a part nothing of
+// f16's 11 is left after the third (but for what is below e5m2's least step, 2^-16).
+__device__ __forceinline__ void cut_weights(float x, float y, uint32_t (&part)[kParts]) {
+  uint32_t h;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(h));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(a));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(back));
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(b) : "r"(h));
-  hi = a;
-  lo = b;
+#pragma unroll
+  for (int k = 0; k < kParts; ++k) {
+    uint16_t a;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(a) : "r"(h));
+    part[k] = a;
+    if (k + 1 < kParts) asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(__byte_perm(part[k], 0, 0x1404)));
+  }
 }
 // A shuffle that stays where it stands among the copies.
 __device__ __forceinline__ int shfl_here(int v, int from) {
@@ -162,10 +163,9 @@ __device__ __forceinline__ int shfl_here(int v, int from) {
   asm volatile("shfl.sync.idx.b32 %0, %1, %2, 0x1f, 0xffffffff;" : "=r"(r) : "r"(v), "r"(from) : "memory");
   return r;
 }
-__device__ __forceinline__ void st_shared_b32(uint32_t at, uint32_t v) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+__device__ __forceinline__ void st_shared_b16(uint32_t at, uint32_t v) {
+  asm volatile("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tst.shared.b16 [%0], l;\n\t}" ::"r"(at), "r"(v) : "memory");
 }
-
 // a |= m in shared memory, by halves (32-bit atomics need no loop)
 __device__ __forceinline__ void or_mask(uint64_t* a, uint64_t m) {
   unsigned* half = reinterpret_cast<unsigned*>(a);
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
   } else if (warp == kIssuePv) {
     if (elect_one()) {
       const uint32_t cols = (rows + 15) / 16 * 16;
-      const uint32_t idesc_hi = idesc_f8_f32(128, cols, kE4m3, kE4m3, true, false), idesc_lo = idesc_f8_f32(128, cols, kE4m3, kE5m2, true, false);
+      const uint32_t idesc = idesc_f8_f32(128, cols, kE4m3, kE5m2, true, false);
       const uint64_t d_v = smem_desc(base, kChunk, 1024, kSwizzle128B);          // MN-major, 128 dims a chunk
       const uint64_t d_p = smem_desc(base + kOffP, 16, 512, kSwizzle64B);        // K-major, 64 keys a row
       int st = 0;
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         }
         fence_proxy_async_smem();
         tc_fence_after();
-        const uint64_t v = desc_advance(d_v, st * kStageBytes), hi = desc_advance(d_p, (t & 1) * 2 * kPart);
+        const uint64_t v = desc_advance(d_v, st * kStageBytes), w = desc_advance(d_p, (t & 1) * kParts * kPart);
         const uint32_t more = t > 0 ? 1u : 0u;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -414,8 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
             const uint64_t a = desc_advance(v, mt * kChunk + ks * 4096);
-            mma_f8_ss(tmem + mt * kRows, a, desc_advance(hi, ks * 32), idesc_hi, ks > 0 ? 1u : more);
-            mma_f8_ss(tmem + mt * kRows, a, desc_advance(hi, kPart + ks * 32), idesc_lo, 1u);
+#pragma unroll
+            for (int part = 0; part < kParts; ++part)
+              mma_f8_ss(tmem + mt * kRows, a, desc_advance(w, part * kPart + ks * 32), idesc, ks + part > 0 ? 1u : more);
           }
           if (y & 1) mma_commit(&sh.k_empty[st][y == 1]);
         }
@@ -632,20 +633,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       qs[h] = reinterpret_cast<const float*>(smem + kOffQs)[r0 + 8 * h];
       m[h] = kUnset;
     }
-    // Where this thread's weights go in a part of P^T (a row's 64 keys, 64-byte swizzle): with its neighbour it holds
-    // four keys of two rows, of which even lanes store the first and odd lanes the second row's.
-    uint32_t p_at[2];  // (of i = 0 and 2; 1 and 3 are eight bytes on)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = r0 + 8 * (lane & 1), col = (c0 & ~3) + 16 * i;
-      p_at[i] = base + kOffP + set * 2 * kPart + row * 64 + ((((col >> 4) ^ ((row >> 1) & 3)) << 4) | (col & 15));
-    }
+    // Where this thread's weights go in a part of P^T (a row's 64 keys, 64-byte swizzle): two keys of row r0, of row
+    // r0 + 8 512 bytes on. (i = 1 is eight bytes on, 2 and 3 the next 16-byte piece.)
+    const uint32_t p_at = base + kOffP + set * kParts * kPart + r0 * 64 + ((((c0 >> 4) ^ ((r0 >> 1) & 3)) << 4) | (c0 & 15));
     auto wait_pv = [&](int t) {  // P.V(t) has read P, and O^T holds every tile up to t
       if (!mbar_wait_abortable(&sh.k_empty[t % kStages][0], (t / kStages) & 1, abort, false, __LINE__)) failed = true;
       tc_fence_after();
     };
     // sums or maxima over the warp's 32 keys, to scratch [2 halves of the keys][64 rows]
-    float* scratch = reinterpret_cast<float*>(smem + kOffP + set * 2 * kPart);
+    float* scratch = reinterpret_cast<float*>(smem + kOffP + set * kParts * kPart);
     auto to_scratch = [&](const float (&v)[2], auto op) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -709,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         raises = raised;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float now = const_cast<volatile float*>(mx)[r0 + 8 * h] - kLift, a = fast_exp2(m[h] - now);
+          const float now = const_cast<volatile float*>(mx)[r0 + 8 * h], a = fast_exp2(m[h] - now);
           l[h] = mul_x2(l[h], f32x2(a, a));
           m[h] = now;
         }
@@ -725,8 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         to_scratch(top, [](float a, float b) { return fmaxf(a, b); });
         bar_sync(bar, kSet);
         if (id < kRows) {  // one thread per row decides
-          const float old = mx[id], now = fmaxf(old, fmaxf(scratch[id], scratch[kRows + id]));
-          alpha_sh[id] = now > old ? fast_exp2(old - now) : 1.f;
+          const float old = mx[id], now = fmaxf(old, fmaxf(scratch[id], scratch[kRows + id]) - kLift);
+          alpha_sh[id] = fast_exp2(old - now);
           mx[id] = now;
         }
         if (id == 0) sh.raises = raises + 1;
@@ -736,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         for (int h = 0; h < 2; ++h) {
           const float a = alpha_sh[r0 + 8 * h];
           l[h] = mul_x2(l[h], f32x2(a, a));
-          m[h] = mx[r0 + 8 * h] - kLift;
+          m[h] = mx[r0 + 8 * h];
         }
         if (t > 0) {
 #pragma unroll 1
@@ -753,27 +749,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         bar_sync(bar, kSet);  // scratch is read before P is written over it, and O^T is rescaled
       }
       if (id == 0) mbar_arrive(&sh.decided[set]);
-      uint32_t hi[4], lo[4];  // [i]: keys c0 + 8 i + {0, 1} of rows r0 (low half) and r0 + 8
+      if (!p_free && !raise) wait_pv(t - 2);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint64_t inv = *reinterpret_cast<const uint64_t*>(factor + 2 * kKeys + 8 * i);
-        uint32_t h2[2], l2[2];
+        uint32_t cut[2][kParts];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float x = fast_exp2(s[4 * i + 2 * h] - m[h]), y = fast_exp2(s[4 * i + 2 * h + 1] - m[h]);
           l[h] = fma_x2(f32x2(x, y), inv, l[h]);
-          cut_weights(x, y, h2[h], l2[h]);
+          cut_weights(x, y, cut[h]);
         }
-        hi[i] = h2[0] | (h2[1] << 16);
-        lo[i] = l2[0] | (l2[1] << 16);
-      }
-      if (!p_free && !raise) wait_pv(t - 2);
+        const uint32_t at = (p_at ^ ((i >> 1) * 16)) + 8 * (i & 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t at = p_at[i >> 1] + 8 * (i & 1);
-        const uint32_t h = __shfl_xor_sync(0xffffffffu, hi[i], 1), w = __shfl_xor_sync(0xffffffffu, lo[i], 1);
-        st_shared_b32(at, lane & 1 ? __byte_perm(h, hi[i], 0x7632) : __byte_perm(hi[i], h, 0x5410));
-        st_shared_b32(at + kPart, lane & 1 ? __byte_perm(w, lo[i], 0x7632) : __byte_perm(lo[i], w, 0x5410));
+        for (int k = 0; k < kParts; ++k) {
+          st_shared_b16(at + k * kPart, cut[0][k]);
+          st_shared_b16(at + k * kPart + 512, cut[1][k]);
+        }
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -785,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     if (ok) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // the last raise may have been the other set's
-        const float a = fast_exp2(m[h] + kLift - mx[r0 + 8 * h]);
+        const float a = fast_exp2(m[h] - mx[r0 + 8 * h]);
         l[h] = mul_x2(l[h], f32x2(a, a));
       }
       float sums[2], x;
@@ -797,10 +789,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       to_scratch(sums, [](float a, float b) { return a + b; });
       bar_sync(6, kSoftmax);
       if (set == 0 && id < kRows) {
-        const float* other = scratch + 2 * kPart / 4;
+        const float* other = scratch + kParts * kPart / 4;
         const float sum = (scratch[id] + scratch[kRows + id]) + (other[id] + other[kRows + id]);
         alpha_sh[id] = sum != 0.f ? 1.f / sum : 0.f;
-        const float lse = sum != 0.f ? (mx[id] - kLift + log2f(sum)) * kLn2 : -CUDART_INF_F;
+        const float lse = sum != 0.f ? (mx[id] + log2f(sum)) * kLn2 : -CUDART_INF_F;
         if (id < rows) sh.lse_dst[id] = lse;
       }
     }
