@@ -51,6 +51,10 @@ cudaError_t launch_kv8_read(const Kv8ReadParams& p, cudaStream_t stream);
 // ---------------------------------------------------------------- verify attention
 constexpr int kKv8Rows = 64;      // (node, head) rows of one group
 constexpr int kKv8Keys = 64;      // keys of a tile
+// Tiles whose products add up in tensor memory; then they join those before in fp32. The tensor core cuts its sums (one unit
+// in the last place of fp32 for 32 keys and part, all towards zero: 1.6e-4 of a sum of one sign after 512 tiles, 2.8e-3 after
+// 7000), and what small weights lose counts times the keys.
+constexpr int kKv8Segment = 512;
 constexpr int kKv8MaxShared = 1024;  // requests of a batch whose tiles are shared out
 
 constexpr int kKv8Chunk = kKv8Keys * 128;         // 128 bytes of 64 keys

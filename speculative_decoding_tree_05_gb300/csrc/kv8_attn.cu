@@ -8,7 +8,7 @@
 // weights that enter the second product are 2^(t_ij - r_i), and the sum of p takes
 // them divided by s_j, both in fp32 until they are cut into parts.
 //
-// Operands of 8 bits (fp32 accumulation, which is exact to fp32: 3e-8 of the result):
+// Operands of 8 bits (fp32 accumulation):
 //   q   = (hi + lo) 2^e, e4m3 both, e of the row: bf16's 8 bits, for values down to
 //         2^-11 of the row's largest; below that in steps of 2^-18 of it
 //   p s = three e5m2 parts of 3 bits each, which hold f16's 11 bits of a weight (2^-12 of it
@@ -43,6 +43,8 @@
 // that see it. The tiles of the whole batch are cut into equal shares, whatever the
 // lengths; a request has its share of them, in equal units. One unit writes bf16 and the
 // log-sum-exp at once, else each writes its normalised O and the merge kernel joins them.
+// A unit of more than kKv8Segment tiles closes a segment there: O^T, its sums and references join those of the segments
+// before, in fp32 in the unit's rows of the partials and in shared memory, and start anew.
 // The query rows come cut and laid out from the kernel before (kv8_prepare.cu), or (kCut) a unit
 // cuts its own.
 #include <cuda_runtime.h>
@@ -76,7 +78,10 @@ constexpr int kOffAlpha = kOffMax + kRows * 4;      // [64] rescale factors, lat
 constexpr int kOffTree = kOffAlpha + kRows * 4;        // [128] row masks of the tree rows
 constexpr int kOffSlot = kOffTree + kMaxNodes * 8;  // [128] their slots
 constexpr int kOffPar = kOffSlot + kMaxNodes * 4;   // [128] their parents
-constexpr int kOffBar = kOffPar + kMaxNodes * 4;
+constexpr int kOffSeg = kOffPar + kMaxNodes * 4;    // of the segments before: [64] references, [64] factors,
+constexpr int kOffSegSum = kOffSeg + 2 * kRows * 4; // [512 softmax threads] sums and references of two rows
+constexpr int kOffBar = kOffSegSum + kSoftmax * 16;
+static_assert(kOffSegSum % 16 == 0 && kKv8Segment % 2 == 0 && (kKv8Segment & (kKv8Segment - 1)) == 0, "read as float4; closed at an even tile");
 constexpr int kSmem = kOffBar + 512 + 1024;
 static_assert(kSmem <= 232448, "one CTA's shared memory");
 constexpr uint32_t kColS = 256, kColQ = 384;        // O^T [0, 256), S buffers 2 x 64, Q
@@ -85,7 +90,8 @@ constexpr float kUnset = -1e30f;                    // running reference of a ro
 // (e5m2 ends at 57344). A raise takes 3000 cycles, as O^T is rescaled, and r follows the largest
 // t, so a row's largest weight is at least 2^kLift. What falls below the parts' last step is at
 // most 2^-17 of a weight, 2^-(17 + kLift) of the largest; but behind one dominant key a tail's
-// errors may all have one sign, so they count times the keys of a unit. 9 nodes of 16 heads, 185000
+// errors may all have one sign, so they count times the keys of a segment, after which references
+// start anew: 2^-9 of the largest. 9 nodes of 16 heads, 185000
 // keys: 87 us, with a lift of 6 86, of 8 88; with the weights as e4m3 and e5m2, which end at 448
 // and left the keys out that were 2^-19 of the largest, 83.
 constexpr float kLift = 7.f, kSlack = 8.75f;
@@ -109,6 +115,7 @@ struct Shared {
   // what the loops lack)
   void* o_dst;
   float* lse_dst;
+  float* o_seg;  // fp32 rows of the segments before
   int last;  // the request's one unit
   int shares;
   uint16_t seen[kStages][2];  // whether every row of the group sees all of a key warp's keys
@@ -334,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     sh.last = un.count == 1;
     sh.o_dst = un.count == 1 ? static_cast<void*>(p.out + at * kDv) : p.o_part + at * kDv;
     sh.lse_dst = (un.count == 1 ? p.lse : p.lse_part) + at;
+    sh.o_seg = p.o_part + (unit * all + row0) * kDv;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -407,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t v = desc_advance(d_v, st * kStageBytes), w = desc_advance(d_p, (t & 1) * kParts * kPart);
-        const uint32_t more = t > 0 ? 1u : 0u;
+        const uint32_t more = (t & (kKv8Segment - 1)) > 0 ? 1u : 0u;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           const int mt = (y + 2) & 3;  // the gathered chunks first: they take longest to come
@@ -650,6 +658,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         if ((lane & 3) == 0) scratch[half * kRows + r0 + 8 * h] = x;
       }
     };
+    // What the segments before have come to, of this thread's rows: sums, times 2^reference. (Thread's own.)
+    float4* seg_sum = reinterpret_cast<float4*>(smem + kOffSegSum) + set * kSet + id;
+    float *seg_ref = reinterpret_cast<float*>(smem + kOffSeg), *seg_factor = seg_ref + kRows;
+    auto close_sums = [&](bool first) {
+      const float4 v = first ? make_float4(0.f, 0.f, kUnset, kUnset) : *seg_sum;
+      const float all[2] = {v.x, v.y}, ref[2] = {v.z, v.w};
+      float sum[2], top[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x, y;
+        f32x2_split(l[h], x, y);
+        top[h] = fmaxf(ref[h], m[h]);
+        sum[h] = fmaf(all[h], fast_exp2(ref[h] - top[h]), (x + y) * fast_exp2(m[h] - top[h]));
+        l[h] = f32x2(0.f, 0.f);
+      }
+      *seg_sum = make_float4(sum[0], sum[1], top[0], top[1]);
+    };
     int raises = 0;  // that m and l know of
     for (int t = set; t < n; t += 2) {
       const int st = t % kStages, ph = (t / kStages) & 1;
@@ -703,15 +728,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
       const int raised = *const_cast<volatile int*>(&sh.raises);
       if (raised != raises) {
         raises = raised;
+        const bool next = t > 1 && (t & (kKv8Segment - 1)) == 1;  // a segment's first of the odd tiles
+        if (next) close_sums(t == kKv8Segment + 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float now = const_cast<volatile float*>(mx)[r0 + 8 * h], a = fast_exp2(m[h] - now);
+          const float now = const_cast<volatile float*>(mx)[r0 + 8 * h], a = next ? 0.f : fast_exp2(m[h] - now);
           l[h] = mul_x2(l[h], f32x2(a, a));
           m[h] = now;
         }
       }
+      const bool close = t > 0 && (t & (kKv8Segment - 1)) == 0;  // the segment before is complete (the even tiles' set)
       if (failed) sh.fail[set] = 1;
-      const bool raise = bar_red_or(bar, kSet, failed || fmaxf(top[0] - m[0], top[1] - m[1]) > kLift + kSlack);
+      const bool raise = bar_red_or(bar, kSet, failed || close || fmaxf(top[0] - m[0], top[1] - m[1]) > kLift + kSlack);
       if (raise) {
         if (*const_cast<volatile int*>(&sh.fail[set])) {
           ok = false;
@@ -721,20 +749,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         to_scratch(top, [](float a, float b) { return fmaxf(a, b); });
         bar_sync(bar, kSet);
         if (id < kRows) {  // one thread per row decides
-          const float old = mx[id], now = fmaxf(old, fmaxf(scratch[id], scratch[kRows + id]) - kLift);
-          alpha_sh[id] = fast_exp2(old - now);
+          const float old = mx[id], now = fmaxf(close ? kUnset : old, fmaxf(scratch[id], scratch[kRows + id]) - kLift);
+          if (close) {
+            const float ref = t == kKv8Segment ? kUnset : seg_ref[id], all = fmaxf(ref, old);
+            seg_factor[id] = fast_exp2(ref - all);
+            alpha_sh[id] = fast_exp2(old - all);
+            seg_ref[id] = all;
+          } else {
+            alpha_sh[id] = fast_exp2(old - now);
+          }
           mx[id] = now;
         }
         if (id == 0) sh.raises = raises + 1;
         ++raises;
         bar_sync(bar, kSet);
+        if (close) close_sums(t == kKv8Segment);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float a = alpha_sh[r0 + 8 * h];
           l[h] = mul_x2(l[h], f32x2(a, a));
           m[h] = mx[r0 + 8 * h];
         }
-        if (t > 0) {
+        if (close) {
+          // O^T joins what the segments before have come to; the next product starts it anew
+#pragma unroll 1
+          for (int k0 = 0; k0 < 16; ++k0) {
+            const int mt = k0 >> 2, cc = 32 * half + (k0 & 3) * 8;
+            if (cc >= rows) continue;
+            uint32_t o[8];
+            tmem_ld8(tmem + lane_off + mt * kRows + cc, o);
+            float* dst = sh.o_seg + cc * kDv + mt * 128 + quarter * 32 + lane;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (cc + k < rows) {
+                const float x = __uint_as_float(o[k]) * alpha_sh[cc + k];
+                dst[k * kDv] = t == kKv8Segment ? x : fmaf(dst[k * kDv], seg_factor[cc + k], x);
+              }
+          }
+          tc_fence_before();
+        } else if (t > 0) {
 #pragma unroll 1
           for (int k0 = 0; k0 < 16; ++k0) {  // half of the columns (rows), 8 at a time
             const int cc = 32 * half + (k0 & 3) * 8;
@@ -775,24 +828,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
     if (ok) wait_pv(n - 1);  // O^T is complete and the P buffers free
     if (bar_red_or(6, kSoftmax, failed || !ok)) ok = false;
     if (ok) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // the last raise may have been the other set's
-        const float a = fast_exp2(m[h] - mx[r0 + 8 * h]);
-        l[h] = mul_x2(l[h], f32x2(a, a));
-      }
-      float sums[2], x;
+      float sums[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        // the last raise may have been the other set's
+        const float now = mx[r0 + 8 * h], all = n > kKv8Segment ? fmaxf(now, seg_ref[r0 + 8 * h]) : now;
+        const float a = fast_exp2(m[h] - all);
+        float x;
         f32x2_split(l[h], sums[h], x);
-        sums[h] += x;
+        sums[h] = (sums[h] + x) * a;
+        if (n > kKv8Segment + set) sums[h] = fmaf(h ? seg_sum->y : seg_sum->x, fast_exp2((h ? seg_sum->w : seg_sum->z) - all), sums[h]);
       }
       to_scratch(sums, [](float a, float b) { return a + b; });
       bar_sync(6, kSoftmax);
       if (set == 0 && id < kRows) {
         const float* other = scratch + kParts * kPart / 4;
         const float sum = (scratch[id] + scratch[kRows + id]) + (other[id] + other[kRows + id]);
-        alpha_sh[id] = sum != 0.f ? 1.f / sum : 0.f;
-        const float lse = sum != 0.f ? (mx[id] + log2f(sum)) * kLn2 : -CUDART_INF_F;
+        const float now = mx[id], inv = sum != 0.f ? 1.f / sum : 0.f;
+        float all = now;
+        if (n > kKv8Segment) {
+          all = fmaxf(now, seg_ref[id]);
+          seg_factor[id] = fast_exp2(seg_ref[id] - all) * inv;
+        }
+        alpha_sh[id] = fast_exp2(now - all) * inv;
+        const float lse = sum != 0.f ? (all + log2f(sum)) * kLn2 : -CUDART_INF_F;
         if (id < rows) sh.lse_dst[id] = lse;
       }
     }
@@ -811,10 +870,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         uint32_t o[8];
         tmem_ld8(tmem + lane_off + mt * kRows + cc, o);
         const float4 f0 = inv_l[cc / 4], f1 = inv_l[cc / 4 + 1];
-        const float x[8] = {__uint_as_float(o[0]) * f0.x, __uint_as_float(o[1]) * f0.y, __uint_as_float(o[2]) * f0.z,
-                            __uint_as_float(o[3]) * f0.w, __uint_as_float(o[4]) * f1.x, __uint_as_float(o[5]) * f1.y,
-                            __uint_as_float(o[6]) * f1.z, __uint_as_float(o[7]) * f1.w};
+        float x[8] = {__uint_as_float(o[0]) * f0.x, __uint_as_float(o[1]) * f0.y, __uint_as_float(o[2]) * f0.z,
+                      __uint_as_float(o[3]) * f0.w, __uint_as_float(o[4]) * f1.x, __uint_as_float(o[5]) * f1.y,
+                      __uint_as_float(o[6]) * f1.z, __uint_as_float(o[7]) * f1.w};
         const int dim = mt * 128 + (warp & 3) * 32;
+        if (n > kKv8Segment) {  // and the segments before
+          const float* seg = sh.o_seg + cc * kDv + dim + lane;
+          const float* factor = reinterpret_cast<const float*>(smem + kOffSeg) + kRows + cc;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < left) x[k] = fmaf(seg[k * kDv], factor[k], x[k]);
+        }
         if (sh.last) {
           // two rows a store: even lanes hold a pair of dims of the first, odd lanes of the second
           uint16_t* dst = static_cast<uint16_t*>(sh.o_dst) + (cc + (lane & 1)) * kDv + dim + (lane & ~1);

@@ -69,7 +69,8 @@ int kv8_layout(const ddt_dims* d, int sm_count, Kv8Layout* w) {
   // the grid's second dimension, and its CTAs in 31 bits
   if (units > 65535 || units * w->groups > INT32_MAX) return DDT_ERR_DIMS;
   w->units = static_cast<int>(units);
-  const size_t rows = size_t(T) * H, part = w->shares > 1 ? size_t(units) * rows : 0;
+  // partials of split requests, and of units of several segments
+  const size_t rows = size_t(T) * H, part = w->shares > 1 || most > kKv8Segment ? size_t(units) * rows : 0;
   w->pieces_off = kStatusBytes;
   w->images_off = align_up(w->pieces_off + size_t(B) * sizeof(Kv8Piece), 256);
   // Query rows are cut once a call where units share them, and where there are fewer groups than SMs, for which four CTAs
