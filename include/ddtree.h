@@ -485,9 +485,10 @@ DDT_API int ddtree_kv8_read(const void* kv8_pool, const float* kv8_scale, const 
  *   tree_len   int32 [B] device, or NULL: every request has T nodes
  *   out        bf16 [B, T, H, 512] (the operand type of the product that follows)
  *   lse        fp32 [B, T, H]
- * Any positive finite scale will do; a key with another one (NaN) gives NaN to the
- * nodes that see it, and to no others, as long as the bytes of a slot are finite values
- * (those that ddtree_kv8_write stores are).  A query row that is not finite gives NaN
+ * Scales from 2^-60 (the least that ddtree_kv8_write stores) to 2^40 (latent values up to
+ * 4.9e14) are used; a key with another one (NaN, zero, a subnormal) gives NaN to the nodes
+ * that see it, and to no others, as long as the bytes of a slot are finite values (those
+ * that ddtree_kv8_write stores are).  A query row that is not finite gives NaN
  * to its own output.  Scores and sums are fp32; a query's values enter with bf16's 8
  * bits down to 2^-11 of the row's largest latent value and in steps of 2^-18 of it below;
  * a softmax weight (times its key's scale) enters the second product with f16's 11 bits (as

@@ -95,6 +95,9 @@ constexpr float kUnset = -1e30f;                    // running reference of a ro
 // keys: 87 us, with a lift of 6 86, of 8 88; with the weights as e4m3 and e5m2, which end at 448
 // and left the keys out that were 2^-19 of the largest, 83.
 constexpr float kLift = 7.f, kSlack = 8.75f;
+// Scales that are used. The sum of p takes weights divided by s, and a weight of less than 2^-126 is zero: with these, less
+// than 2^-33 of a row's sum (2^-126 / 2^-60 beside 2^kLift / 2^40).
+constexpr float kLeastScale = 0x1p-60f, kMostScale = 0x1p40f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct Shared {
@@ -557,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attn_kernel(const __grid_cons
         reinterpret_cast<uint64_t*>(smem + kOffMask)[st * kKeys + k] = mask;
         const bool all = __all_sync(0xffffffffu, mask == full);
         if (lane == 0) sh.seen[st][warp - kFirstKey] = all;
-        // a scale that is not positive and finite: NaN for the rows that see the key
-        const bool fine = scale > 0.f && scale < CUDART_INF_F;
+        // a scale that is not usable: NaN for the rows that see the key
+        const bool fine = scale >= kLeastScale && scale <= kMostScale;
         float* f = reinterpret_cast<float*>(smem + kOffKey) + st * 3 * kKeys + k;
         f[0] = fine ? scale : CUDART_NAN_F;
         f[kKeys] = fine ? log2f(scale) : 0.f;
