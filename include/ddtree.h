@@ -490,11 +490,12 @@ DDT_API int ddtree_kv8_read(const void* kv8_pool, const float* kv8_scale, const 
  * that see it, and to no others, as long as the bytes of a slot are finite values (those
  * that ddtree_kv8_write stores are).  A query row that is not finite gives NaN
  * to its own output.  Scores and sums are fp32; a query's values enter with bf16's 8
- * bits down to 2^-11 of the row's largest latent value and in steps of 2^-18 of it below;
+ * bits down to 2^-11 of the row's largest latent value (or of 2^-39 of its largest rope
+ * value, where that is more) and in steps of 2^-18 of it below;
  * a softmax weight (times its key's scale) enters the second product with f16's 11 bits (as
- * three 8-bit parts), at most 2^-12 off, or 2^-24 of the row's largest where that is more
- * (over all keys together at most 2^-9 of the softmax's sum); that product's sums are cut to
- * fp32, 3e-4 of them at most; out is rounded to bf16 once.  Results are the same bits on every run, and do
+ * three 8-bit parts), at most 2^-12 off, or 2^-24 of the largest among its 32768 keys where
+ * that is more (so over all keys together at most 2^-9 of their sum); that product's sums
+ * are cut to fp32, 2^-11 of them at most; out is rounded to bf16 once.  Results are the same bits on every run, and do
  * not depend on the slots' order.
  * dims as in ddtree_verify_attn, max_prefix_len up to 2^30; prefix_len_sum steers the
  * division of the work and the workspace's size.

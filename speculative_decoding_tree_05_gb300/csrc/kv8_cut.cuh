@@ -53,9 +53,10 @@ __device__ __forceinline__ CutQuery cut_row(const uint32_t (&w)[9], int lane, fl
   turned = __reduce_max_sync(0xffffffffu, max(turned & 0xffffu, turned >> 16));
   // a row that is not finite: zeros, and a factor of NaN for its own scores alone
   const bool fine = max(top, turned) < 0x7f80u;
-  // 448 = 1.75 2^8 (7 bits stand behind the exponent); rope values stay below 2^121
+  // 448 = 1.75 2^8 (7 bits stand behind the exponent); rope values stay below 2^48, as those of a key without latent values
+  // (whose scale is 2^-60) are large: products of up to 2^73 of them stay inside fp32
   const int e = max(static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0),
-                    max(static_cast<int>(turned >> 7) - 127 - 120, kKv8MinExp));
+                    max(static_cast<int>(turned >> 7) - 127 - 47, kKv8MinExp));
   const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
   // With its neighbour, even lanes take 16 dims of the first, odd lanes of the second half.
   uint32_t cut[2][4];  // [part][8 bytes of the first half, 8 of the second]

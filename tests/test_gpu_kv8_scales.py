@@ -2,7 +2,10 @@
 
 Scales from 2^-60 to 2^40 are used; a key with another one gives NaN to the nodes that see it and to no others. The
 comparison allows a weight's 2^-12 and a score's error (below 2^-12) twice, the result's rounding to bf16 (2^-8) and what
-the sums lose: 2^-9 of the weighted size in all.
+the sums lose: 2^-9 of the weighted size in all. A weight times scale below the parts' last step, 2^-16 where the row's
+largest is at least 2^7, is off by up to half of that step, 2^-24 of the largest, whatever its own size: with w s that
+largest and v the stored values, 2^-24 w s times the sum of all |v| of a dim. (It shows where the keys that weigh most have
+a value of next to nothing.)
 """
 import math
 
@@ -57,9 +60,11 @@ def check(d, out, lse, nodes):
         k = row[list(range(keys)) + sorted({keys, keys + t})]
         s = SCALE * (d["q"][0, t].double() @ k.T)
         w = torch.softmax(s, -1)
+        by = d["scale"].double()[list(range(keys)) + sorted({keys, keys + t})]
+        last = 2.0 ** -24 * (w * by).amax(1)[:, None] * (k[:, :512].abs() / by[:, None]).sum(0)
         ref, size = w @ k[:, :512], w @ k[:, :512].abs()
         assert bool(((lse[0, t].double() - torch.logsumexp(s, -1)).abs() <= 2.0 ** -11).all()), t
-        assert bool(((out[0, t].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -9 * size).all()), t
+        assert bool(((out[0, t].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -9 * size + last).all()), t
 
 
 @pytest.mark.parametrize("exponents", [[-60], [40], [-60, -7], [-7, 40], [-60, 40, 0], [-60, -60, -60, -60, -60, -60, 40]])
@@ -81,3 +86,28 @@ def test_a_scale_that_is_not_usable(bad):
     d["scale"][302], d["scale"][17] = 2.0 ** -7, bad
     out, lse = call(d)
     assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+
+
+@pytest.mark.parametrize("exponents,rope", [([-60], 16.0), ([-60], 200.0), ([-60, -7], 30.0), ([-7], 1000.0)])
+def test_rope_values_alone(exponents, rope):
+    """No latent value in the queries, and (where the scale is the least one) none in the keys to speak of."""
+    d = make(500, 5, 16, exponents, seed=7, rope=rope)
+    d["q"][..., 512:] *= 64.0 / rope
+    out, lse = call(d)
+    check(d, out, lse, range(5))
+
+
+def test_rows_without_latent_values():
+    """As ddtree_kv8_write stores them; a query with large rope values beside small latent ones."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    rows = torch.zeros(405, 576, device="cuda")
+    rows[:, 512:] = 20 * torch.randn(405, 64, generator=g, device="cuda")
+    rows[::3, :512] = torch.randn(135, 512, generator=g, device="cuda")
+    d = make(400, 5, 16, [0], seed=8, latent=1.0)
+    ddtree.kv8_write(rows.to(torch.bfloat16), torch.arange(405, dtype=torch.int32, device="cuda"), d["pool"], d["scale"])
+    d["q"][..., 512:] *= 2
+    d["q"][0, 1, :, :512] = 0
+    d["q"][0, 2, :, :512] *= 2.0 ** -30
+    d["q"][0, 3, :, :512] *= 2.0 ** -55
+    out, lse = call(d)
+    check(d, out, lse, range(5))
