@@ -461,7 +461,7 @@ DDT_API int ddtree_verify_attn_blocks(const void* q, const void* kv_pool, const 
  *   position    int32 [n] device (with rotation), each in [0, positions); a row with
  *               another one is not written and sets DDT_STATUS_BAD_POSITION
  * Slots that are not listed keep what they hold.  The pool and the scales must not
- * overlap the rows, the slots or each other (DDT_ERR_ALIAS).  workspace: 256 bytes for
+ * overlap the other inputs or each other (DDT_ERR_ALIAS).  workspace: 256 bytes for
  * the status word, or NULL: then nothing is reported, and the call is one kernel.
  *
  * ddtree_kv8_read writes the rows that listed slots stand for, rounded to bf16 (exact

@@ -148,6 +148,11 @@ extern "C" int ddtree_kv8_write(const void* rows, int64_t row_stride, const int3
   if (overlap(rows, in, kv8_pool, pool) || overlap(rows, in, kv8_scale, scales) || overlap(kv8_pool, pool, kv8_scale, scales) ||
       overlap(slots, size_t(n) * 4, kv8_pool, pool) || overlap(slots, size_t(n) * 4, kv8_scale, scales))
     return DDT_ERR_ALIAS;
+  const struct { const void* p; size_t n; } more[] = {{norm_weight, size_t(kDv) * 2},
+                                                      {rotation, size_t(rotation ? positions : 0) * (2 * kRopePairs) * 4},
+                                                      {rotation ? position : nullptr, size_t(n) * 4}};
+  for (const auto& x : more)
+    if (overlap(x.p, x.n, kv8_pool, pool) || overlap(x.p, x.n, kv8_scale, scales)) return DDT_ERR_ALIAS;
   int sms = 0;
   const int rc = current_device(&sms);
   if (rc != DDT_OK) return rc;
