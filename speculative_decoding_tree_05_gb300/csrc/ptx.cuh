@@ -487,11 +487,6 @@ __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint16_t pack_e5m2x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ void unpack_f16x2(uint32_t v, float& lo, float& hi) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
       : "=f"(lo), "=f"(hi)
@@ -500,11 +495,6 @@ __device__ __forceinline__ void unpack_f16x2(uint32_t v, float& lo, float& hi) {
 __device__ __forceinline__ void unpack_e4m3x2(uint16_t v, float& lo, float& hi) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
-  unpack_f16x2(h, lo, hi);
-}
-__device__ __forceinline__ void unpack_e5m2x2(uint16_t v, float& lo, float& hi) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(v));
   unpack_f16x2(h, lo, hi);
 }
 
