@@ -18,6 +18,13 @@ constexpr int64_t kMaxRows = int64_t(1) << 31;  // of one call
 bool clear_status(void* workspace, cudaStream_t s) {
   return cudaMemsetAsync(workspace, 0, 4 * sizeof(int32_t), s) == cudaSuccess;
 }
+// A call without rows or requests: its status is that nothing was wrong, not what the call before it left.
+int nothing_to_do(void* workspace, size_t bytes, ddt_stream_t stream) {
+  if (!workspace) return DDT_OK;
+  if (!aligned(workspace, 256)) return DDT_ERR_ALIGN;
+  if (bytes < kStatusBytes) return DDT_ERR_WORKSPACE;
+  return clear_status(workspace, reinterpret_cast<cudaStream_t>(stream)) ? DDT_OK : DDT_ERR_LAUNCH;
+}
 
 struct Kv8Layout {
   int groups, group_nodes, shares, units;
@@ -138,7 +145,7 @@ extern "C" int ddtree_kv8_write(const void* rows, int64_t row_stride, const int3
   if (n < 0 || n > kMaxRows || row_stride < kDqk || row_stride % 8 != 0 || pool_slots < 1 || pool_slots > kMaxRows ||
       (norm_weight && !(eps >= 1e-12f && eps <= 1.f)) || (rotation && positions < 1))
     return DDT_ERR_DIMS;
-  if (n == 0) return DDT_OK;
+  if (n == 0) return nothing_to_do(workspace, kStatusBytes, stream);
   if (!rows || !slots || !kv8_pool || !kv8_scale || (rotation && !position)) return DDT_ERR_NULL;
   if (!aligned(rows, 16) || !aligned(norm_weight, 16) || !aligned(kv8_pool, 16) || !aligned(workspace, 256) ||
       !aligned(slots, 4) || !aligned(rotation, 4) || !aligned(position, 4) || !aligned(kv8_scale, 4))
@@ -179,7 +186,7 @@ extern "C" int ddtree_kv8_read(const void* kv8_pool, const float* kv8_scale, con
                                int64_t row_stride, int64_t pool_slots, void* workspace, ddt_stream_t stream) {
   if (n < 0 || n > kMaxRows || row_stride < kDqk || row_stride % 8 != 0 || pool_slots < 1 || pool_slots > kMaxRows)
     return DDT_ERR_DIMS;
-  if (n == 0) return DDT_OK;
+  if (n == 0) return nothing_to_do(workspace, kStatusBytes, stream);
   if (!rows || !slots || !kv8_pool || !kv8_scale) return DDT_ERR_NULL;
   if (!aligned(rows, 16) || !aligned(kv8_pool, 16) || !aligned(workspace, 256) || !aligned(slots, 4) || !aligned(kv8_scale, 4))
     return DDT_ERR_ALIGN;
@@ -218,7 +225,7 @@ extern "C" int ddtree_verify_attn_kv8(const void* q, const void* kv8_pool, const
   Kv8Layout w;
   int rc = kv8_layout(dims, 1, &w);  // the sizes, before any device query
   if (rc != DDT_OK) return rc;
-  if (dims->batch == 0) return DDT_OK;
+  if (dims->batch == 0) return nothing_to_do(workspace, workspace_bytes, stream);
   if (!q || !kv8_pool || !kv8_scale || !prefix_len || !tree_parent || !tree_slot_idx || !out || !lse || !workspace ||
       (!slot_idx && dims->max_prefix_len > 0))
     return DDT_ERR_NULL;
@@ -307,7 +314,7 @@ extern "C" int ddtree_accept(const void* logits, int32_t logits_fp32, int64_t lo
   int rc = check_accept(dims, vocab);
   if (rc != DDT_OK) return rc;
   if (logit_stride < vocab || (draft_prob && draft_stride < vocab)) return DDT_ERR_DIMS;
-  if (dims->batch == 0) return DDT_OK;
+  if (dims->batch == 0) return nothing_to_do(workspace, workspace_bytes, stream);
   if (!logits || !tokens || !tree_parent || !uniform || !temperature || !path || !path_len || !next_token || !workspace)
     return DDT_ERR_NULL;
   if (!aligned(logits, logits_fp32 ? 4 : 2) || !aligned(draft_prob, 4) || !aligned(tokens, 4) || !aligned(tree_parent, 4) ||
