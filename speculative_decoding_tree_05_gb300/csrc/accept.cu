@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kAccThreads, 2) accept_kernel(const __grid_con
       for (uint32_t m = kids[i]; m != 0; m &= m - 1) {
         const int c = 32 * i + __ffs(m) - 1;
         const unsigned long long w = kDrawn ? less(child_w[c], Shares(refused)(child_q[c])) : child_w[c];
-        // u S q < w of whole numbers: as floor(u floor(S q)) is
+        // u S q < w, each product rounded down to a whole number (one step of 2^-43 of the largest weight)
         if (share_of(kDrawn ? share_of(S, child_q[c]) : S, u_sh[c]) < w) {
           go = c;
           break;
