@@ -24,11 +24,11 @@
 // 48 + 144 KB of operands a tile, and 52 KB written (with both operands of the scores in
 // shared memory it was 96 KB more). O^T takes 256 TMEM columns,
 // the scores twice 64, the queries 128; one CTA holds the whole output.
-// A tile of 64 rows takes 2130 cycles (65 nodes of 128 heads, 65536 keys: 1072 us, 1.11
-// PFLOP/s), of which shared memory works 1900; the gathers run at 18 B/clk and SM, and the
-// softmax's chain of waits is 2000 long, of which two overlap. (In two parts of weights, e4m3 and e5m2,
-// it took 2030.) With one query row a
-// key it is the gathers alone (16 requests of up to 32768 keys: 54 us, 4 TB/s in the kernel).
+// A tile of 64 rows takes 2130 cycles (65 nodes of 128 heads, 65536 keys: 1070 us, 1.11
+// PFLOP/s), of which shared memory works 1900, the schedulers issue in 1500 and the tensor core
+// works 1410; the gathers run at 18 B/clk and SM, and the softmax's chain of waits is 2000 long,
+// of which two overlap. (With two parts of weights, e4m3 and e5m2, it took 2030.) With one query
+// row a key it is the gathers alone (16 requests of up to 32768 keys: 54 us, 4 TB/s in the kernel).
 //
 // Per CTA (896 threads), one unit = (up to 64 (node, head) rows of a request, a share of its tiles):
 //   warp 0       TMEM; one lane issues S(t) when stage t has landed

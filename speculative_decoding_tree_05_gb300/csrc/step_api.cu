@@ -82,7 +82,7 @@ int kv8_layout(const ddt_dims* d, int sm_count, Kv8Layout* w) {
   w->images_off = align_up(w->pieces_off + size_t(B) * sizeof(Kv8Piece), 256);
   // Query rows are cut once a call where units share them, and where there are fewer groups than SMs, for which four CTAs
   // a group are quicker (9 nodes of 16 heads over 40 keys: 14.5 us, 16.5 by the units). Many units of their own groups cut
-  // their rows beside their first gathers (1540 groups of 46 keys: 156 us in place of 184, 900 of 16 to 99 98 for 117).
+  // their rows beside their first gathers (1540 groups of 46 keys: 164 us in place of 194, 900 of 16 to 99 103 for 121).
   w->images = w->shares > 1 || B * w->groups <= sm_count;
   w->lse_off = w->images_off + (w->images ? size_t(B) * w->groups * kKv8Image : 0);
   w->o_off = align_up(w->lse_off + part * sizeof(float), 256);
