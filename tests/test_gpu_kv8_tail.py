@@ -3,8 +3,8 @@
 A key far above the others is the ordinary state of a language model; what the many small weights add up to has to reach
 the output. Tolerance, from the arithmetic and the same for any number of keys: a weight enters the second product as the
 nearest f16 (2^-12 of it), a score's error (up to 2^-13 here: 40 partial sums of two units of 2^-24 of sum |q k| < 200,
-and three roundings of 2^-23 of values below 32) counts twice, a sum over 32768 keys is
-cut to fp32 for every 32 of them and each part (2^-23 each, 2^-11.4 in all): together within 2^-9 of the values' weighted size. What falls below the parts' last
+and three roundings of 2^-23 of values below 32) counts twice, a sum over 32768 keys is cut to fp32 for every 32 of them and
+each part (2^-23 each, 2^-11.4 in all): together within 2^-9 of the values' weighted size. What falls below the parts' last
 step is at most 2^-24 of the largest weight a key, 2^-9 of it over 32768 keys of one sign. Rounding out to bf16: 2^-8 of it.
 """
 import ctypes
